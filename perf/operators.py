@@ -188,6 +188,9 @@ def prepare(case, seed):
         s["grads"] = [flat[a:a + n] for a, n in zip(starts, sizes)]
         s["outs"] = [out[a:a + n] for a, n in zip(starts, sizes)]
         s["max_norm"] = 1.0
+        if own:  # the description of its gradients that a training program keeps beside them
+            import diffusion_transformer_elementwise_gb300 as dit
+            s["list"] = dit.TensorList(s["grads"], out=s["outs"])
     return s
 
 
@@ -223,7 +226,7 @@ def _own(s):
     if c["op"] == "embed_grad":
         return [dit.embedding_backward(s["grad"], s["ids"], c["V"], c["scale"],
                                        out=s["grad_table"])]
-    _, norm = dit.clip_grads(s["grads"], s["max_norm"], out=s["outs"])
+    _, norm = dit.clip_grads(s["list"], s["max_norm"])
     return [s["flat_out"], norm]
 
 
