@@ -13,9 +13,18 @@ LTX-2-style video diffusion transformers.
   runtime key (op, dtype, layouts, D) on the GPU
 * :func:`set_statistic` / :func:`statistic` -- the modulation's row
   statistic: "fast" (default) or "exact" (correctly rounded, bit-exact)
+* :func:`rmsnorm`, :func:`add_rmsnorm`, :func:`rmsnorm_fp8`,
+  :func:`add_rmsnorm_fp8` -- the weighted RMSNorm of token transformers, with
+  the residual's addition and an E4M3 output with dynamic scales
+* :func:`rmsnorm_backward` -- its gradients
+* :func:`embedding`, :func:`embedding_backward` -- rows of a table by token
+  id, and the table's gradient by sorted tokens
+* :func:`grad_norm`, :func:`clip_grads`, :class:`TensorList` -- the 2-norm over
+  many tensors, and clipping by it
 
 Each call is one kernel of ``libdit_elementwise.so`` (C ABI in
-``include/dit_elementwise.h``), launched on the current torch stream.  Build
+``include/dit_elementwise.h``), launched on the current torch stream; the
+gradients and the norm over tensors are a few.  Build
 the library with :func:`build`; without it every call raises.
 """
 from ._binding import (  # noqa: F401
@@ -36,5 +45,17 @@ from ._binding import (  # noqa: F401
     set_first_use_check,
     set_statistic,
     statistic,
+)
+from ._token import (  # noqa: F401
+    TensorList,
+    add_rmsnorm,
+    add_rmsnorm_fp8,
+    clip_grads,
+    embedding,
+    embedding_backward,
+    grad_norm,
+    rmsnorm,
+    rmsnorm_backward,
+    rmsnorm_fp8,
 )
 from .build import build  # noqa: F401

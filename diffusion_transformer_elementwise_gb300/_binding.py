@@ -98,6 +98,8 @@ def library() -> ctypes.CDLL:
             lib.dit_set_statistic.restype = ci
             lib.dit_get_statistic.argtypes = []
             lib.dit_get_statistic.restype = ci
+            from . import _token
+            _token.declare(lib)
             _lib = lib
     return _lib
 

@@ -9,6 +9,7 @@
 #include <mutex>
 #include <tuple>
 
+#include "dit_checks.h"
 #include "dit_elementwise.h"
 #include "dit_internal.h"
 
@@ -69,37 +70,17 @@ int resident_ctas(const DeviceInfo& dev, const void* fn, int block, size_t smem)
 
 using dit::DeviceInfo;
 using dit::RowArgs;
+using dit::Span;
+using dit::elem_size;
+using dit::element_count;
+using dit::launch_status;
+using dit::misaligned;
+using dit::overlaps;
+using dit::span;
+using dit::valid_dtype;
+using dit::valid_layout;
 
 namespace {
-
-int elem_size(dit_dtype t) { return t == DIT_FP32 ? 4 : 2; }
-
-bool valid_dtype(int t) { return t == DIT_BF16 || t == DIT_FP16 || t == DIT_FP32; }
-bool valid_layout(int l) { return l == DIT_FULL || l == DIT_ROW_BCAST; }
-
-// N = B * L * D elements; false on a negative size or overflow of the byte
-// count of a tensor.
-bool element_count(int64_t B, int64_t L, int64_t D, int es, int64_t* n) {
-  if (B < 0 || L < 0 || D < 0) return false;
-  int64_t bl, bld, bytes;
-  if (__builtin_mul_overflow(B, L, &bl)) return false;
-  if (__builtin_mul_overflow(bl, D, &bld)) return false;
-  if (__builtin_mul_overflow(bld, (int64_t)es, &bytes)) return false;
-  *n = bld;
-  return true;
-}
-
-struct Span {
-  uintptr_t lo, hi;  // [lo, hi) bytes
-};
-Span span(const void* p, int64_t bytes) {
-  return Span{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes};
-}
-bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
-
-bool misaligned(const void* p, int es) { return ((uintptr_t)p & (uintptr_t)(es - 1)) != 0; }
-
-dit_status launch_status(cudaError_t e) { return e == cudaSuccess ? DIT_OK : DIT_ERR_LAUNCH; }
 
 // The process's row statistic (dit_set_statistic), read when a call is made.
 std::atomic<int> g_statistic{DIT_STATISTIC_FAST};
@@ -142,6 +123,11 @@ const char* dit_status_string(dit_status s) {
       return "DIT_ERR_BAD_OP: op is not a dit_op value, or count is outside [0, DIT_MAX_GROUP]";
     case DIT_ERR_WORKSPACE:
       return "DIT_ERR_WORKSPACE: workspace NULL, too small or not 256-byte aligned";
+    case DIT_ERR_BAD_SCALAR:
+      return "DIT_ERR_BAD_SCALAR: a scale, weight_offset or max_norm is not finite (or negative)";
+    case DIT_ERR_BAD_FORMAT:
+      return "DIT_ERR_BAD_FORMAT: not a dit_id_type value, or group is not 0 or 128";
+    case DIT_ERR_NO_MEMORY: return "DIT_ERR_NO_MEMORY: no host memory for the call's list";
     case DIT_ERR_BAD_STATISTIC:
       return "DIT_ERR_BAD_STATISTIC: not a dit_statistic value";
   }

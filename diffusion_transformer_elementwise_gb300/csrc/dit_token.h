@@ -1,0 +1,94 @@
+// dit_token.h -- host-side interface between the C entry points of the
+// token-transformer operators (dit_token_api.cu) and their kernels.
+#pragma once
+
+#include "dit_internal.h"
+
+namespace dit {
+
+// Weighted RMSNorm over `rows` rows of D elements (k_norm.cu).
+struct NormArgs {
+  void* res;        // hidden + update (NULL: no update)
+  void* out;        // the normed row: the tensors' type, or E4M3
+  float* scales;    // E4M3: [rows, groups]
+  const void* x;    // hidden
+  const void* u;    // update, or NULL
+  const void* w;    // weight [D]
+  int64_t rows;
+  int D;
+  int warps;        // warps per row (set by the launcher)
+  float eps, offset;
+  float d_f, inv_d;
+  int groups;       // E4M3: scales per row
+};
+// wide: every row of every tensor starts on a 16-byte boundary (8 or 4 for
+// the E4M3 output).  q8: 0 none, 1 one scale per row, 2 one per 128 columns.
+cudaError_t launch_norm(const DeviceInfo& dev, int dtype, bool wide, int q8, const NormArgs& a,
+                        cudaStream_t s);
+
+// Its gradient (k_norm_grad.cu).
+struct NormGradArgs {
+  void* gx;
+  float* partial;   // [ctas, D] sums of the weight's gradient, or NULL
+  const void* g;    // gradient of the normed output
+  const void* gres; // gradient arriving on the skip path, or NULL
+  const void* x;    // the norm's input
+  const void* w;
+  int64_t rows;
+  int D;
+  int warps;
+  float eps, offset;
+  float d_f, inv_d;
+};
+// the most CTAs (rows of `partial`) a call takes
+constexpr int64_t kNormGradMaxCtas = 608;
+// gw: the weight's gradient, or NULL
+cudaError_t launch_norm_grad(const DeviceInfo& dev, int dtype, bool wide, const NormGradArgs& a,
+                             void* gw, cudaStream_t s);
+
+// Embedding lookup and its gradient (k_embedding.cu).  ids: int32 or int64
+// (ids64); ids outside [0, V) give zero rows and take no gradient.
+struct EmbedArgs {
+  void* out;
+  const void* ids;
+  const void* table;
+  int64_t tokens, V;
+  int D;
+  bool ids64;
+  float scale;
+};
+cudaError_t launch_embedding(int dtype, bool wide, const EmbedArgs& a, cudaStream_t s);
+
+struct EmbedGradArgs {
+  void* gt;          // gradient of the table [V, D]
+  const void* g;     // gradient of the rows [tokens, D]
+  const void* ids;
+  int64_t tokens, V;
+  int D;
+  bool ids64;
+  float scale;
+  // workspace: two buffers of (key, position) pairs, and the partial rows
+  uint2* pairs[2];
+  float* partial;    // [segments][2][D]
+};
+// sorted tokens per segment, and segments of a call
+constexpr int kEmbedSegment = 32;
+inline int64_t embed_segments(int64_t tokens) { return (tokens + kEmbedSegment - 1) / kEmbedSegment; }
+cudaError_t launch_embedding_grad(int dtype, bool wide, const EmbedGradArgs& a, cudaStream_t s);
+
+// The global norm of many tensors, and their clipping (k_clip.cu).
+struct ClipTensor {
+  const void* g;
+  void* out;  // NULL: the norm alone
+  int64_t n;
+  int dtype;
+};
+// the most tensors of one launch, and partial sums it writes
+constexpr int kClipBatch = 960;
+constexpr int64_t kClipMaxCtas = 1216;
+// partial: kClipMaxCtas doubles per kClipBatch tensors.  norm: the norm.
+// clip: also out = g * min(1, max_norm / (norm + eps)).
+cudaError_t launch_clip(const DeviceInfo& dev, const ClipTensor* t, int64_t count, bool clip,
+                        float max_norm, float eps, double* partial, float* norm, cudaStream_t s);
+
+}  // namespace dit

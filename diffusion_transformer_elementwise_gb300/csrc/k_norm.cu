@@ -1,0 +1,450 @@
+// k_norm.cu -- weighted RMSNorm with the residual's addition, and an E4M3
+// output with dynamic scales.
+//
+//   s = rnd(hidden + update)                  (stored; or s = x alone)
+//   r = 1 / sqrt(mean(s^2) + eps)             (the fast statistic)
+//   y = fl(fl(s r) fl(offset + w))
+//   out = rnd(y), or E4M3:  scale = max|y| / 448,  code = e4m3(y / scale)
+//
+// with the maximum over the row or over each 128 columns of it.
+//
+// The codes need no r: with t = fl(s fl(offset + w)), y / max|y| = t / max|t|,
+// so code = e4m3(fl(t fl(448 / max|t|))) and scale = fl(fl(max|t| r) / 448).
+// The maximum is taken in the same reduction as the sum of squares, and a
+// code carries fewer roundings than y / scale would.  Rows whose sum of
+// squares or maximum leaves [2^-100, 2^100] (overflow, infinities, NaN, all
+// zero) take y itself: the maximum again, of y, and code = e4m3(y 448 /
+// max|y|).  An all-zero row or group has scale 0 and codes 0; a NaN or an
+// infinity makes its maximum NaN, so its scale and codes are NaN.
+//
+// A team of warps holds a row in registers, up to four units of 512 bytes a
+// warp; longer rows are read twice by one CTA each.
+#include "dit_stat.cuh"
+#include "dit_token.h"
+#include "dit_unit.cuh"
+
+namespace dit {
+namespace {
+
+constexpr float kE4M3Max = 448.0f;
+
+__device__ __forceinline__ bool usable(float m) { return m >= 0x1p-100f && m <= 0x1p100f; }
+
+// The factor from values to codes, and the scale, of one row or group.
+struct Quant {
+  float pre, mul, scale;
+};
+// from the maximum of |t| (usable, or zero with a usable sum)
+__device__ __forceinline__ Quant quant_of_t(float m, float r) {
+  Quant q;
+  q.pre = 1.0f;
+  q.mul = m == 0.0f ? 0.0f : __fdiv_rn(kE4M3Max, m);
+  q.scale = __fdiv_rn(__fmul_rn(m, r), kE4M3Max);
+  return q;
+}
+// from the maximum of |y|, whatever it is; a small one is scaled up first, so
+// that 448 / m does not overflow
+__device__ __forceinline__ Quant quant_of_y(float m) {
+  Quant q;
+  q.pre = m < 0x1p-60f ? 0x1p64f : 1.0f;
+  q.mul = m == 0.0f ? 0.0f : __fdiv_rn(kE4M3Max, __fmul_rn(m, q.pre));
+  q.scale = __fdiv_rn(m, kE4M3Max);
+  return q;
+}
+
+template <class T, bool WIDE>
+struct NormRow {
+  using U = Unit<T, WIDE>;
+  static constexpr int P = U::P;
+  // 128-column groups of a unit whose maxima a lane helps to find, and the
+  // lanes that share one
+  static constexpr int NG = !WIDE && sizeof(T) == 2 ? 2 : 1;
+  static constexpr int LANES = WIDE && sizeof(T) == 2 ? 16 : 32;
+
+  // hidden + update, rounded (the first value alone without an update)
+  __device__ __forceinline__ static Raw<16> add(const Raw<16>& h, const Raw<16>& u) {
+    F2 a[P], b[P];
+    Granule<T>::widen(h, a);
+    Granule<T>::widen(u, b);
+#pragma unroll
+    for (int i = 0; i < P; ++i) a[i] = f2_add(a[i], b[i]);
+    return Granule<T>::narrow(a);
+  }
+  __device__ __forceinline__ static void weight(const Raw<16>& w, float offset, F2 (&f)[P]) {
+    Granule<T>::widen(w, f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) f[i] = f2_add(f2(offset, offset), f[i]);
+  }
+  __device__ __forceinline__ static void normed(const Raw<16>& x, const F2 (&w)[P], float r,
+                                                F2 (&y)[P]) {
+    Granule<T>::widen(x, y);
+#pragma unroll
+    for (int i = 0; i < P; ++i) y[i] = f2_mul(f2_mul(y[i], f2(r, r)), w[i]);
+  }
+  // s times the weight, without r
+  __device__ __forceinline__ static void weighted(const Raw<16>& x, const F2 (&w)[P], F2 (&t)[P]) {
+    Granule<T>::widen(x, t);
+#pragma unroll
+    for (int i = 0; i < P; ++i) t[i] = f2_mul(t[i], w[i]);
+  }
+  // columns past the row hold zero; where r is not finite they became NaN
+  __device__ __forceinline__ static void mask(F2 (&y)[P], int c0, int D, int lane) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (U::col(c0, lane, 2 * i) >= D) y[i].x = 0.0f;
+      if (U::col(c0, lane, 2 * i + 1) >= D) y[i].y = 0.0f;
+    }
+  }
+  __device__ __forceinline__ static float max_of(const F2 (&v)[P]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) m = max_nan(m, max_nan(fabsf(f2_lo(v[i])), fabsf(f2_hi(v[i]))));
+    return m;
+  }
+  __device__ __forceinline__ static Raw<U::EPL> codes(const F2 (&v)[P], const Quant (&q)[NG]) {
+    Raw<U::EPL> r;
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) {
+      const Quant& k = q[NG == 2 ? i : 0];
+      uint32_t w = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const F2 p = f2_mul(v[2 * i + j], f2(k.pre, k.pre));
+        w |= e4m3x2(f2_mul(p, f2(k.mul, k.mul))) << (16 * j);
+      }
+      r.w[i] = w;
+    }
+    return r;
+  }
+  // the maxima of the lane's groups of a unit
+  __device__ __forceinline__ static void group_max(const F2 (&v)[P], float (&m)[NG]) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      m[g] = 0.0f;
+#pragma unroll
+      for (int i = g * P / NG; i < (g + 1) * P / NG; ++i)
+        m[g] = max_nan(m[g], max_nan(fabsf(f2_lo(v[i])), fabsf(f2_hi(v[i]))));
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1)
+        m[g] = max_nan(m[g], __shfl_xor_sync(0xFFFFFFFFu, m[g], o));
+    }
+  }
+
+  // one unit of the output, one scale per 128 columns (the whole warp calls)
+  __device__ __forceinline__ static void emit_groups(const NormArgs& a, int64_t row, int c0,
+                                                     int lane, const Raw<16>& x,
+                                                     const Raw<16>& wr, float S, float r) {
+    F2 w[P], v[P];
+    weight(wr, a.offset, w);
+    weighted(x, w, v);
+    float m[NG];
+    group_max(v, m);
+    Quant q[NG];
+    bool slow = !usable(S);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      q[g] = quant_of_t(m[g], r);
+      slow = slow || (m[g] != 0.0f && !usable(m[g]));
+    }
+    if (__any_sync(0xFFFFFFFFu, slow)) {  // rare
+      F2 y[P];
+      normed(x, w, r, y);
+      mask(y, c0, a.D, lane);
+      group_max(y, m);
+      if (slow) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) q[g] = quant_of_y(m[g]);
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = y[i];
+      }
+    }
+    U::store8((char*)a.out + row * a.D, c0, a.D, lane, codes(v, q));
+    const int first = WIDE ? c0 + lane / LANES * 128 : c0;
+    if (lane % LANES == 0) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int k = first / 128 + g;
+        if (k < a.groups) a.scales[row * a.groups + k] = q[g].scale;
+      }
+    }
+  }
+};
+
+// r of a row from its fp32 sum of squares S; a sum outside the usable range
+// is taken again, scaled, by `again(scale)` (uniform over the row's threads).
+template <class Again>
+__device__ __forceinline__ float inverse_rms(float S, const NormArgs& a, Again again) {
+  if (fast_sum_in_range(S)) return fast_inverse_rms(S, a.d_f, a.inv_d, a.eps);
+  const float sc = fast_rescale(S);
+  return fast_inverse_rms_scaled(again(sc), sc, a.d_f, a.inv_d, a.eps);
+}
+
+template <class T, bool WIDE, int NU, bool ADD, int Q8>
+__global__ void __launch_bounds__(kTeamThreads) norm_team_kernel(NormArgs a) {
+  using R = NormRow<T, WIDE>;
+  using U = typename R::U;
+  constexpr int P = U::P;
+  __shared__ float2 slots[2 * kTeamWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int W = a.warps, teams = (blockDim.x >> 5) / W;
+  const int team = warp / W, m = warp - team * W;
+  Team t{slots + team * 2 * W, W, m, 1 + team, 0};
+  const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
+
+  for (int64_t row = (int64_t)blockIdx.x * teams + team; row < a.rows;
+       row += (int64_t)gridDim.x * teams) {
+    Raw<16> x[NU], w[NU];
+    F2 acc[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+    float big = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      const int c0 = (m + j * W) * U::COLS;
+      x[j] = U::load((const char*)a.x + row * pitch, c0, a.D, lane);
+      if constexpr (ADD) {
+        const Raw<16> u = U::load((const char*)a.u + row * pitch, c0, a.D, lane);
+        x[j] = R::add(x[j], u);
+      }
+      w[j] = U::load_weight(a.w, c0, a.D, lane);
+    }
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      const int c0 = (m + j * W) * U::COLS;
+      if constexpr (ADD) U::store((char*)a.res + row * pitch, c0, a.D, lane, x[j]);
+      F2 f[P];
+      Granule<T>::widen(x[j], f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) acc[i & 1] = f2_fma(f[i], f[i], acc[i & 1]);
+      if constexpr (Q8 == 1) {
+        F2 wf[P], v[P];
+        R::weight(w[j], a.offset, wf);
+        R::weighted(x[j], wf, v);
+        big = max_nan(big, R::max_of(v));
+      }
+    }
+    acc[0] = f2_add(acc[0], acc[1]);
+    float2 red = make_float2(warp_sum(__fadd_rn(acc[0].x, acc[0].y)), 0.0f);
+    if constexpr (Q8 == 1) red.y = warp_max(big);
+    red = t.combine<Q8 == 1>(red);
+    const float r = inverse_rms(red.x, a, [&](float sc) {
+      float s2 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NU; ++j) {
+        F2 f[P];
+        Granule<T>::widen(x[j], f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const float u0 = __fmul_rn(f2_lo(f[i]), sc), u1 = __fmul_rn(f2_hi(f[i]), sc);
+          s2 = __fmaf_rn(u1, u1, __fmaf_rn(u0, u0, s2));
+        }
+      }
+      return t.combine<false>(make_float2(warp_sum(s2), 0.0f)).x;
+    });
+
+    if constexpr (Q8 == 0) {
+#pragma unroll
+      for (int j = 0; j < NU; ++j) {
+        F2 wf[P], y[P];
+        R::weight(w[j], a.offset, wf);
+        R::normed(x[j], wf, r, y);
+        U::store((char*)a.out + row * pitch, (m + j * W) * U::COLS, a.D, lane, Granule<T>::narrow(y));
+      }
+    } else if constexpr (Q8 == 2) {
+#pragma unroll
+      for (int j = 0; j < NU; ++j)
+        R::emit_groups(a, row, (m + j * W) * U::COLS, lane, x[j], w[j], red.x, r);
+    } else {
+      // one scale per row
+      const bool slow = !usable(red.x) || (red.y != 0.0f && !usable(red.y));
+      Quant q[R::NG];
+      if (slow) {  // rare, uniform over the row's threads
+        float my = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NU; ++j) {
+          F2 wf[P], y[P];
+          R::weight(w[j], a.offset, wf);
+          R::normed(x[j], wf, r, y);
+          R::mask(y, (m + j * W) * U::COLS, a.D, lane);
+          my = max_nan(my, R::max_of(y));
+        }
+        q[0] = quant_of_y(t.combine<true>(make_float2(0.0f, warp_max(my))).y);
+      } else {
+        q[0] = quant_of_t(red.y, r);
+      }
+#pragma unroll
+      for (int g = 1; g < R::NG; ++g) q[g] = q[0];
+#pragma unroll
+      for (int j = 0; j < NU; ++j) {
+        F2 wf[P], v[P];
+        R::weight(w[j], a.offset, wf);
+        if (slow)
+          R::normed(x[j], wf, r, v);
+        else
+          R::weighted(x[j], wf, v);
+        U::store8((char*)a.out + row * a.D, (m + j * W) * U::COLS, a.D, lane, R::codes(v, q));
+      }
+      if (m == 0 && lane == 0) a.scales[row] = q[0].scale;
+    }
+  }
+}
+
+// Rows longer than a CTA's registers: one CTA per row, the row read again for
+// the output (with an update, each thread its own stores of the residual).
+// The squares of a unit are summed in fp32 and the units in fp64, so that a
+// thread's thousands of units add no error.
+template <class T, bool WIDE, bool ADD, int Q8>
+__global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
+  using R = NormRow<T, WIDE>;
+  using U = typename R::U;
+  constexpr int P = U::P;
+  __shared__ float2 slots[2 * 32];
+  __shared__ double sums[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  Team t{slots, W, warp, 1, 0};
+  const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
+
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const char* src = (const char*)(ADD ? a.res : a.x) + row * pitch;
+    double total = 0.0;
+    float big = 0.0f;
+    for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
+      Raw<16> x = U::load((const char*)a.x + row * pitch, c0, a.D, lane);
+      if constexpr (ADD) {
+        x = R::add(x, U::load((const char*)a.u + row * pitch, c0, a.D, lane));
+        U::store((char*)a.res + row * pitch, c0, a.D, lane, x);
+      }
+      F2 f[P];
+      Granule<T>::widen(x, f);
+      F2 acc = f2_mul(f[0], f[0]);
+#pragma unroll
+      for (int i = 1; i < P; ++i) acc = f2_fma(f[i], f[i], acc);
+      total += (double)__fadd_rn(acc.x, acc.y);
+      if constexpr (Q8 == 1) {
+        F2 wf[P], v[P];
+        R::weight(U::load_weight(a.w, c0, a.D, lane), a.offset, wf);
+        R::weighted(x, wf, v);
+        big = max_nan(big, R::max_of(v));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+    __syncthreads();  // the previous row's sums have been read
+    if (lane == 0) sums[warp] = total;
+    if constexpr (Q8 == 1) big = t.combine<true>(make_float2(0.0f, warp_max(big))).y;
+    __syncthreads();
+    total = 0.0;
+    for (int w = 0; w < W; ++w) total += sums[w];
+    const float S = (float)total;
+    const float r = inverse_rms(S, a, [&](float sc) {
+      double s2 = 0.0;
+      for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
+        F2 f[P];
+        Granule<T>::widen(U::load(src, c0, a.D, lane), f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const double u0 = (double)__fmul_rn(f2_lo(f[i]), sc), u1 = (double)__fmul_rn(f2_hi(f[i]), sc);
+          s2 += u0 * u0 + u1 * u1;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
+      __syncthreads();
+      if (lane == 0) sums[warp] = s2;
+      __syncthreads();
+      s2 = 0.0;
+      for (int w = 0; w < W; ++w) s2 += sums[w];
+      return (float)s2;
+    });
+
+    bool slow = false;
+    Quant q[R::NG];
+    if constexpr (Q8 == 1) {
+      slow = !usable(S) || (big != 0.0f && !usable(big));
+      if (slow) {
+        float my = 0.0f;
+        for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
+          F2 wf[P], y[P];
+          R::weight(U::load_weight(a.w, c0, a.D, lane), a.offset, wf);
+          R::normed(U::load(src, c0, a.D, lane), wf, r, y);
+          R::mask(y, c0, a.D, lane);
+          my = max_nan(my, R::max_of(y));
+        }
+        q[0] = quant_of_y(t.combine<true>(make_float2(0.0f, warp_max(my))).y);
+      } else {
+        q[0] = quant_of_t(big, r);
+      }
+#pragma unroll
+      for (int g = 1; g < R::NG; ++g) q[g] = q[0];
+      if (threadIdx.x == 0) a.scales[row] = q[0].scale;
+    }
+    for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
+      const Raw<16> x = U::load(src, c0, a.D, lane);
+      const Raw<16> w = U::load_weight(a.w, c0, a.D, lane);
+      if constexpr (Q8 == 2) {
+        R::emit_groups(a, row, c0, lane, x, w, S, r);
+      } else {
+        F2 wf[P], v[P];
+        R::weight(w, a.offset, wf);
+        if (Q8 == 0 || slow)
+          R::normed(x, wf, r, v);
+        else
+          R::weighted(x, wf, v);
+        if constexpr (Q8 == 0)
+          U::store((char*)a.out + row * pitch, c0, a.D, lane, Granule<T>::narrow(v));
+        else
+          U::store8((char*)a.out + row * a.D, c0, a.D, lane, R::codes(v, q));
+      }
+    }
+  }
+}
+
+template <class T, bool WIDE, bool ADD, int Q8>
+cudaError_t launch(const DeviceInfo& dev, NormArgs a, cudaStream_t s) {
+  const int64_t units = (a.D + Unit<T, WIDE>::COLS - 1) / Unit<T, WIDE>::COLS;
+  auto team = [&](auto nu) -> cudaError_t {
+    constexpr int NU = decltype(nu)::value;
+    const TeamShape t = team_shape(units, NU);
+    a.warps = t.warps;
+    const int block = t.warps * t.teams * 32;
+    int64_t grid = (a.rows + t.teams - 1) / t.teams;
+    if (grid > (int64_t(1) << 30)) grid = int64_t(1) << 30;
+    norm_team_kernel<T, WIDE, NU, ADD, Q8><<<(unsigned)grid, block, 0, s>>>(a);
+    return cudaGetLastError();
+  };
+  if (units <= 8) return team(std::integral_constant<int, 1>{});
+  if (units <= 2 * kTeamWarps) return team(std::integral_constant<int, 2>{});
+  if (units <= 4 * kTeamWarps) return team(std::integral_constant<int, 4>{});
+  int64_t grid = (int64_t)dev.sm_count * 2;
+  if (grid > a.rows) grid = a.rows;
+  norm_long_kernel<T, WIDE, ADD, Q8><<<(unsigned)grid, 1024, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <class T, bool WIDE>
+cudaError_t launch_form(const DeviceInfo& dev, int q8, const NormArgs& a, cudaStream_t s) {
+  if (a.u)
+    return q8 == 0   ? launch<T, WIDE, true, 0>(dev, a, s)
+           : q8 == 1 ? launch<T, WIDE, true, 1>(dev, a, s)
+                     : launch<T, WIDE, true, 2>(dev, a, s);
+  return q8 == 0   ? launch<T, WIDE, false, 0>(dev, a, s)
+         : q8 == 1 ? launch<T, WIDE, false, 1>(dev, a, s)
+                   : launch<T, WIDE, false, 2>(dev, a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const DeviceInfo& dev, int dtype, bool wide, int q8, const NormArgs& a,
+                        cudaStream_t s) {
+  switch (dtype) {
+    case 0:
+      return wide ? launch_form<__nv_bfloat16, true>(dev, q8, a, s)
+                  : launch_form<__nv_bfloat16, false>(dev, q8, a, s);
+    case 1:
+      return wide ? launch_form<__half, true>(dev, q8, a, s)
+                  : launch_form<__half, false>(dev, q8, a, s);
+    default:
+      return wide ? launch_form<float, true>(dev, q8, a, s)
+                  : launch_form<float, false>(dev, q8, a, s);
+  }
+}
+
+}  // namespace dit

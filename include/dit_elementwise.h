@@ -17,6 +17,17 @@
  *                                  in one launch
  *   dit_selfcheck                  bit-for-bit check of one runtime key
  *
+ * and the same kind of operations for the token transformers beside it (the
+ * language model that reads the prompt), with their gradients:
+ *
+ *   dit_rmsnorm, dit_add_rmsnorm   out = rms_norm(x, eps) * (offset + weight),
+ *                                  x = hidden + update; *_fp8: E4M3 output
+ *                                  with a scale per row or per 128 columns
+ *   dit_rmsnorm_backward           gradients of x and of the weight
+ *   dit_embedding                  rows of a table by token id, times a scale
+ *   dit_embedding_backward         the table's gradient, by sorted tokens
+ *   dit_grad_norm, dit_clip_grads  the 2-norm over many tensors; clipping
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * Tensors.  Every tensor is contiguous, row-major [B, L, D] in device memory
@@ -87,10 +98,14 @@ typedef enum {
   DIT_ERR_NO_DEVICE = 9,    /* no current CUDA device could be queried        */
   DIT_ERR_BAD_OP = 10,      /* op is not a dit_op value, or (dit_grouped) count
                                is outside [0, DIT_MAX_GROUP]                  */
-  DIT_ERR_WORKSPACE = 11,   /* dit_selfcheck: workspace NULL, smaller than
-                               dit_selfcheck_workspace_bytes or not 256-byte
-                               aligned                                        */
-  DIT_ERR_BAD_STATISTIC = 12  /* dit_set_statistic: not a dit_statistic value */
+  DIT_ERR_WORKSPACE = 11,   /* a workspace that is NULL, smaller than the call's
+                               _workspace_bytes or not 256-byte aligned       */
+  DIT_ERR_BAD_STATISTIC = 12, /* dit_set_statistic: not a dit_statistic value */
+  DIT_ERR_BAD_SCALAR = 13,  /* a scale, weight_offset or max_norm is infinite or
+                               NaN (max_norm: or negative)                    */
+  DIT_ERR_BAD_FORMAT = 14,  /* an id type or a scale group that is not one of
+                               the documented values                          */
+  DIT_ERR_NO_MEMORY = 15    /* the host has no memory for the call's own list */
 } dit_status;
 
 /* Version of this interface; bumped on any incompatible change. */
@@ -448,6 +463,146 @@ dit_status dit_selfcheck_static(dit_op op, dit_dtype dtype,
  * device is current or the runtime cannot give the address.
  */
 dit_status dit_selfcheck_static_workspace(void** workspace, int64_t* bytes);
+
+/* ---------------------------------------------------------------------------
+ * Token-transformer operators
+ *
+ * The conventions above hold, with these differences.
+ *   Tensors are contiguous; rows = the product of all sizes but the last, D =
+ *   the last.  A call whose output is empty returns DIT_OK and launches
+ *   nothing (the gradients of weights and tables are written even when there are no
+ *   rows: they are zero).  D is at most 2^24, rows and tokens at most 2^31 - 1.
+ *   The row statistic is the fast one, whatever dit_set_statistic says.
+ *   A call may enqueue several kernels, in order, on `stream`; every sum has
+ *   one order for given sizes and alignment on one GPU model, so the same call gives
+ *   the same bits.
+ * Workspaces.  A call that needs memory of its own takes `workspace` (device,
+ *   256-byte aligned, at least the size its _workspace_bytes function gives;
+ *   that function returns -1 for sizes the call refuses).  It
+ *   holds nothing between calls and needs no initial value; calls that may
+ *   run at the same time, and graphs that may replay at the same time, need
+ *   one each.
+ * None of this has a counterpart in the pages: they are the memory-bound
+ * operations of a language model's step, offered beside the diffusion
+ * transformer's.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Weighted RMSNorm, alone or with the residual's addition:
+ *   s   = rnd(hidden + update)              -> residual_out (dit_add_rmsnorm)
+ *   r   = 1 / sqrt(mean_d(s^2) + eps)       (the fast statistic)
+ *   out = rnd(fl32(fl32(s * r) * fl32(weight_offset + weight[d])))
+ * with s = x for dit_rmsnorm.  weight: [D], weight_offset 0 for a plain weight,
+ * 1 for one stored as its difference from one.  The statistic is taken over
+ * the residual as stored.  residual_out may be hidden; no other overlap of an
+ * output with another tensor is allowed.  Any element-aligned pointer and any D: rows of
+ * 16-byte granules move in 16-byte accesses, others element by element.
+ */
+dit_status dit_rmsnorm(void* out, const void* x, const void* weight, int64_t rows, int64_t D,
+                       float eps, float weight_offset, dit_dtype dtype, dit_stream_t stream);
+
+dit_status dit_add_rmsnorm(void* residual_out, void* out, const void* hidden, const void* update,
+                           const void* weight, int64_t rows, int64_t D, float eps,
+                           float weight_offset, dit_dtype dtype, dit_stream_t stream);
+
+/*
+ * The same with the normed output in E4M3 (as dit_rmsnorm_modulate_fp8) and
+ * dynamic scales: with y the fp32 value of out before its rounding and m the
+ * maximum of |y| over the row (group 0) or over each 128 columns of it (group 128, the
+ * last group holding what is left),
+ *   scale = m / 448,  code = e4m3(y / scale),  y ~ code * scale,
+ * evaluated as code = e4m3(fl32(t * fl32(448 / max|t|))) with t = fl32(s *
+ * fl32(weight_offset + weight)), which leaves r out of the codes, and
+ * scale = fl32(fl32(max|t| * r) / 448); from y itself where a sum of squares
+ * or a maximum leaves [2^-100, 2^100].  m = 0 gives scale 0 and codes 0; a NaN
+ * or an infinity in s makes the scale of its row or group NaN, and the codes NaN.
+ * out: [rows, D] bytes.  scales: fp32 [rows, 1], or [rows, ceil(D / 128)].
+ * Other groups: DIT_ERR_BAD_FORMAT.  out and scales may overlap nothing.
+ */
+dit_status dit_rmsnorm_fp8(void* out, float* scales, const void* x, const void* weight,
+                           int64_t rows, int64_t D, int64_t group, float eps, float weight_offset,
+                           dit_dtype dtype, dit_stream_t stream);
+
+dit_status dit_add_rmsnorm_fp8(void* residual_out, void* out, float* scales, const void* hidden,
+                               const void* update, const void* weight, int64_t rows, int64_t D,
+                               int64_t group, float eps, float weight_offset, dit_dtype dtype,
+                               dit_stream_t stream);
+
+/*
+ * Gradient of the weighted RMSNorm.  With n = x * r, t = grad_out *
+ * (weight_offset + weight) and grad_residual the gradient that reaches x on
+ * the skip path (NULL: none),
+ *   grad_x      = rnd(r * (t - n * mean_d(t * n)) + grad_residual)
+ *   grad_weight = rnd(sum over the rows of grad_out * n)
+ * in fp32.  x is the norm's input: for dit_add_rmsnorm its residual_out, and
+ * grad_x is then the gradient of hidden and of update alike.
+ * grad_weight may be NULL (a frozen weight; the workspace may then be NULL too).
+ * grad_x may be grad_out or grad_residual; no other overlap of an output with
+ * another tensor or with the workspace is allowed.
+ */
+int64_t dit_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t D);
+
+dit_status dit_rmsnorm_backward(void* grad_x, void* grad_weight, const void* grad_out,
+                                const void* grad_residual, const void* x, const void* weight,
+                                int64_t rows, int64_t D, float eps, float weight_offset,
+                                dit_dtype dtype, void* workspace, int64_t workspace_bytes,
+                                dit_stream_t stream);
+
+/*
+ * Embedding lookup:  out[t] = rnd(fl32(table[ids[t]] * scale)),
+ * a row of zeros where ids[t] is outside [0, V) (a padded place).
+ * out: [tokens, D], table: [V, D], V at most 2^31 - 1; ids: [tokens], aligned to their size.
+ */
+typedef enum { DIT_INT32 = 0, DIT_INT64 = 1 } dit_id_type;
+
+dit_status dit_embedding(void* out, const void* ids, const void* table, int64_t tokens, int64_t V,
+                         int64_t D, float scale, dit_dtype dtype, dit_id_type id_type,
+                         dit_stream_t stream);
+
+/*
+ * Its gradient:  grad_table[v] = rnd(fl32(scale * sum of grad_out[t], ids[t] = v)),
+ * every row of [V, D] written, zeros where no token names it; ids outside
+ * [0, V) take no part.  The tokens are sorted by id (stably, so the rows of
+ * an id are added in the order of their positions) and the sums are fp32.
+ * grad_table may overlap neither the inputs nor the workspace.
+ */
+int64_t dit_embedding_backward_workspace_bytes(int64_t tokens, int64_t D);
+
+dit_status dit_embedding_backward(void* grad_table, const void* grad_out, const void* ids,
+                                  int64_t tokens, int64_t V, int64_t D, float scale,
+                                  dit_dtype dtype, dit_id_type id_type, void* workspace,
+                                  int64_t workspace_bytes, dit_stream_t stream);
+
+/*
+ * Global norm of many tensors, and clipping by it:
+ *   norm   = sqrt(sum over all tensors and elements of g^2)
+ *   out[i] = rnd(fl32(g[i] * c)),  c = fl32(min(1, max_norm / (norm + eps)))
+ * The squares are summed in fp32 within a thread's few dozen elements and in
+ * fp64 beyond (in fp64 throughout where such a sum leaves [2^-100, 2^100]).
+ * norm: device, one fp32 (the norm before clipping).  A NaN norm makes
+ * c NaN; an infinite one makes c 0.
+ *
+ * tensors: a HOST array of `count` descriptions, read during the call only;
+ * each tensor has its own size and dtype, and sizes of zero are
+ * allowed.  dit_grad_norm ignores `out`.  out may be g itself; any other overlap
+ * of an out with a g, an out, the norm or the workspace returns DIT_ERR_ALIAS.
+ * Each tensor has at most 2^44 elements.
+ */
+typedef struct {
+  const void* g;
+  void* out;
+  int64_t n;
+  int64_t dtype; /* a dit_dtype value */
+} dit_tensor;
+
+int64_t dit_grad_norm_workspace_bytes(int64_t count);
+
+dit_status dit_grad_norm(float* norm, const dit_tensor* tensors, int64_t count, void* workspace,
+                         int64_t workspace_bytes, dit_stream_t stream);
+
+dit_status dit_clip_grads(float* norm, const dit_tensor* tensors, int64_t count, float max_norm,
+                          float eps, void* workspace, int64_t workspace_bytes,
+                          dit_stream_t stream);
 
 #ifdef __cplusplus
 }
