@@ -6,6 +6,9 @@
 
 namespace dit {
 
+// How the rows of a call's tensors are accessed (dit_unit.cuh).
+enum Layout { WIDE, PHASED, NARROW };
+
 // Weighted RMSNorm over `rows` rows of D elements (k_norm.cu).
 struct NormArgs {
   void* res;        // hidden + update (NULL: no update)
@@ -21,9 +24,11 @@ struct NormArgs {
   float d_f, inv_d;
   int groups;       // E4M3: scales per row
 };
-// wide: every row of every tensor starts on a 16-byte boundary (8 or 4 for
-// the E4M3 output).  q8: 0 none, 1 one scale per row, 2 one per 128 columns.
-cudaError_t launch_norm(const DeviceInfo& dev, int dtype, bool wide, int q8, const NormArgs& a,
+// layout: a Layout of dit_unit.cuh that the tensors allow (the E4M3 output,
+// a byte an element, needs 8-byte rows beside 16-byte granules of a 16-bit
+// type, 4-byte ones beside fp32).  q8: 0 none, 1 one scale per row, 2 one per
+// 128 columns.
+cudaError_t launch_norm(const DeviceInfo& dev, int dtype, int layout, int q8, const NormArgs& a,
                         cudaStream_t s);
 
 // Its gradient (k_norm_grad.cu).
@@ -41,9 +46,9 @@ struct NormGradArgs {
   float d_f, inv_d;
 };
 // the most CTAs (rows of `partial`) a call takes
-constexpr int64_t kNormGradMaxCtas = 608;
+constexpr int64_t kNormGradMaxCtas = 304;
 // gw: the weight's gradient, or NULL
-cudaError_t launch_norm_grad(const DeviceInfo& dev, int dtype, bool wide, const NormGradArgs& a,
+cudaError_t launch_norm_grad(const DeviceInfo& dev, int dtype, int layout, const NormGradArgs& a,
                              void* gw, cudaStream_t s);
 
 // Embedding lookup and its gradient (k_embedding.cu).  ids: int32 or int64

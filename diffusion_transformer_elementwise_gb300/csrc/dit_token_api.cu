@@ -38,6 +38,12 @@ bool row_shape(int64_t rows, int64_t D, int es, int64_t* n) {
 // row_bytes are made of 16-byte granules
 bool wide_rows(uint64_t bits, int64_t row_bytes) { return ((bits | (uint64_t)row_bytes) & 15u) == 0; }
 
+// streamed: the addresses (ORed) of the tensors read or written row by row
+dit::Layout layout_of(uint64_t streamed, const void* weight, int64_t row_bytes) {
+  if (wide_rows(streamed | (uintptr_t)weight, row_bytes)) return dit::WIDE;
+  return (streamed & 15u) == 0 ? dit::PHASED : dit::NARROW;
+}
+
 dit_status workspace_status(const void* w, int64_t have, int64_t need) {
   if (!w || ((uintptr_t)w & (uintptr_t)(kAlign - 1)) != 0 || have < need) return DIT_ERR_WORKSPACE;
   return DIT_OK;
@@ -92,11 +98,11 @@ dit_status norm_impl(bool add, int q8, void* res, void* out, float* scales, cons
   a.d_f = (float)D;
   a.inv_d = 1.0f / (float)D;
   a.groups = (int)groups;
-  uint64_t bits = (uintptr_t)x | (uintptr_t)w;
+  uint64_t bits = (uintptr_t)x;
   if (add) bits |= (uintptr_t)u | (uintptr_t)res;
   // an E4M3 row has 8 (fp32: 4) bytes for each granule of the input's
   bits |= q8 ? (uint64_t)((uintptr_t)out & (uintptr_t)(16 / es - 1)) : (uint64_t)(uintptr_t)out;
-  return launch_status(dit::launch_norm(dev, dtype, wide_rows(bits, D * es), q8, a,
+  return launch_status(dit::launch_norm(dev, dtype, layout_of(bits, w, D * es), q8, a,
                                         (cudaStream_t)stream));
 }
 
@@ -195,10 +201,10 @@ dit_status dit_rmsnorm_backward(void* grad_x, void* grad_weight, const void* gra
   a.offset = weight_offset;
   a.d_f = (float)D;
   a.inv_d = 1.0f / (float)D;
-  const uint64_t bits = (uintptr_t)grad_x | (uintptr_t)grad_out | (uintptr_t)grad_residual |
-                        (uintptr_t)x | (uintptr_t)weight;
-  return launch_status(dit::launch_norm_grad(dev, dtype, wide_rows(bits, D * es), a, grad_weight,
-                                             (cudaStream_t)stream));
+  const uint64_t bits =
+      (uintptr_t)grad_x | (uintptr_t)grad_out | (uintptr_t)grad_residual | (uintptr_t)x;
+  return launch_status(dit::launch_norm_grad(dev, dtype, layout_of(bits, weight, D * es), a,
+                                             grad_weight, (cudaStream_t)stream));
 }
 
 dit_status dit_embedding(void* out, const void* ids, const void* table, int64_t tokens, int64_t V,

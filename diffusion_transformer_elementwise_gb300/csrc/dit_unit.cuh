@@ -2,18 +2,27 @@
 // stores and reductions shared by the weighted-norm kernels.
 //
 // A unit is 512 bytes of a row: 256 columns of a 16-bit type or 128 of fp32,
-// 16 bytes per lane.  In a wide unit lane l holds the 16-byte granule l, so an
-// access of the warp is 512 contiguous bytes.  Rows that are not made of
-// 16-byte granules (an odd width, or a tensor that starts off a 16-byte
-// boundary) take narrow units: lane l's element i is column 32 i + l, one
-// element per access, 64 or 128 contiguous bytes of the warp.  Both keep a
-// lane's elements packed in a Raw<16>, so the arithmetic does not see the
-// difference.  Columns past the row read as zero and are not stored.
+// 16 bytes per lane, kept packed in a Raw<16>.  Three layouts:
+//   WIDE     the rows are made of 16-byte granules.  Lane l holds granule l of
+//            the unit; a warp's access is 512 contiguous bytes.
+//   PHASED   the tensors start on 16-byte boundaries but the rows do not (an odd
+//            width).  Lanes hold the granules of the tensor, not of the row: row
+//            r starts `off` elements into its first granule, so that
+//            granule's first elements, and its last granule's last ones,
+//            belong to the neighbours: they read as zero and are not stored.
+//            Rows whose numbers differ by a multiple of EPL (elements per
+//            granule) have the same `off`, so a team that takes such rows loads
+//            its weights, at that offset, once.
+//   NARROW   a tensor that starts off a 16-byte boundary.  Lane l's element i is
+//            column 32 i + l, one element per access.
+// The arithmetic is the same for all three.  Columns past the row read as
+// zero and are not stored.
 #pragma once
 
 #include "dit_device.cuh"
 #include "dit_internal.h"
 #include "dit_pipe.cuh"
+#include "dit_token.h"
 
 namespace dit {
 
@@ -29,75 +38,129 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-template <class T, bool WIDE>
+template <class T, int LAYOUT>
 struct Unit {
   static constexpr int ES = (int)sizeof(T);
   static constexpr int EPL = 16 / ES;       // elements per lane
   static constexpr int COLS = 32 * EPL;     // columns of a unit
   static constexpr int P = Granule<T>::P;   // fp32 pairs per lane
 
-  // the column of a lane's element i in the unit that starts at column c0
-  __device__ __forceinline__ static int col(int c0, int lane, int i) {
-    return WIDE ? c0 + lane * EPL + i : c0 + i * 32 + lane;
+  int D, lane;
+  int off;    // PHASED: the row's offset from a granule's start, elements
+  bool last;  // PHASED: the tensors' last row: nothing past its end is read
+
+  __device__ __forceinline__ Unit(int D, int lane) : D(D), lane(lane), off(0), last(false) {}
+  __device__ __forceinline__ void at_row(int64_t row, int64_t rows) {
+    if constexpr (LAYOUT == PHASED) {
+      off = (int)(((uint64_t)row * (uint64_t)(D % EPL)) % EPL);
+      last = row == rows - 1;
+    }
+  }
+  // the column of this lane's element i in the unit that starts at column c0
+  // (PHASED: negative in a first granule shared with the row before)
+  __device__ __forceinline__ int col(int c0, int i) const {
+    return LAYOUT == NARROW ? c0 + i * 32 + lane : c0 + lane * EPL + i - off;
+  }
+  // whether all of a lane's columns are the row's
+  __device__ __forceinline__ bool whole(int c) const { return c >= 0 && c + EPL <= D; }
+  __device__ __forceinline__ static void put(Raw<16>& r, int i, const Raw<ES>& e) {
+    if constexpr (ES == 4)
+      r.w[i] = e.w[0];
+    else
+      r.w[i >> 1] |= (uint32_t)e.h << (16 * (i & 1));
+  }
+  __device__ __forceinline__ static Raw<ES> get(const Raw<16>& r, int i) {
+    Raw<ES> e;
+    if constexpr (ES == 4)
+      e.w[0] = r.w[i];
+    else
+      e.h = (uint16_t)(r.w[i >> 1] >> (16 * (i & 1)));
+    return e;
   }
   template <bool STREAM>
-  __device__ __forceinline__ static Raw<16> load_as(const void* row, int c0, int D, int lane) {
+  __device__ __forceinline__ Raw<16> elements(const void* row, int c0) const {
     Raw<16> r = {};
-    if constexpr (WIDE) {
-      if (col(c0, lane, 0) < D) {
-        const char* p = (const char*)row + (int64_t)col(c0, lane, 0) * ES;
-        r = STREAM ? ld_stream<16>(p) : ld_bcast<16>(p);
-      }
-    } else {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int c = col(c0, lane, i);
-        if (c >= D) continue;
-        const char* p = (const char*)row + (int64_t)c * ES;
-        const Raw<ES> e = STREAM ? ld_stream<ES>(p) : ld_bcast<ES>(p);
-        if constexpr (ES == 4)
-          r.w[i] = e.w[0];
-        else
-          r.w[i >> 1] |= (uint32_t)e.h << (16 * (i & 1));
-      }
+    for (int i = 0; i < EPL; ++i) {
+      const int c = col(c0, i);
+      if (c < 0 || c >= D) continue;
+      const char* p = (const char*)row + (int64_t)c * ES;
+      put(r, i, STREAM ? ld_stream<ES>(p) : ld_bcast<ES>(p));
     }
     return r;
   }
+  // PHASED: zero the neighbours' elements of a granule that starts at column c
+  __device__ __forceinline__ void mask(Raw<16>& r, int c) const {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      if (c + i >= 0 && c + i < D) continue;
+      if constexpr (ES == 4)
+        r.w[i] = 0;
+      else
+        r.w[i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+    }
+  }
   // activations, read once
-  __device__ __forceinline__ static Raw<16> load(const void* row, int c0, int D, int lane) {
-    return load_as<true>(row, c0, D, lane);
-  }
-  // weights, re-read by every row
-  __device__ __forceinline__ static Raw<16> load_weight(const void* w, int c0, int D, int lane) {
-    return load_as<false>(w, c0, D, lane);
-  }
-  __device__ __forceinline__ static void store(void* row, int c0, int D, int lane, const Raw<16>& r) {
-    if constexpr (WIDE) {
-      if (col(c0, lane, 0) < D) st_stream<16>((char*)row + (int64_t)col(c0, lane, 0) * ES, r);
+  __device__ __forceinline__ Raw<16> load(const void* row, int c0) const {
+    if constexpr (LAYOUT == NARROW) {
+      return elements<true>(row, c0);
     } else {
+      Raw<16> r = {};
+      const int c = col(c0, 0);
+      if (c < D) {
+        const char* p = (const char*)row + (int64_t)c * ES;
+        if (LAYOUT == WIDE || whole(c)) {
+          r = ld_stream<16>(p);
+        } else if (last && c + EPL > D) {
+          r = elements<true>(row, c0);
+        } else {
+          r = ld_stream<16>(p);
+          mask(r, c);
+        }
+      }
+      return r;
+    }
+  }
+  // weights, read by every row
+  __device__ __forceinline__ Raw<16> load_weight(const void* w, int c0) const {
+    if constexpr (LAYOUT != WIDE) {
+      return elements<false>(w, c0);
+    } else {
+      Raw<16> r = {};
+      if (col(c0, 0) < D) r = ld_bcast<16>((const char*)w + (int64_t)col(c0, 0) * ES);
+      return r;
+    }
+  }
+  __device__ __forceinline__ void store(void* row, int c0, const Raw<16>& r) const {
+    const int c = col(c0, 0);
+    if constexpr (LAYOUT == WIDE) {
+      if (c < D) st_stream<16>((char*)row + (int64_t)c * ES, r);
+    } else {
+      if (LAYOUT == PHASED && whole(c)) {
+        st_stream<16>((char*)row + (int64_t)c * ES, r);
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const int c = col(c0, lane, i);
-        if (c >= D) continue;
-        Raw<ES> e;
-        if constexpr (ES == 4)
-          e.w[0] = r.w[i];
-        else
-          e.h = (uint16_t)(r.w[i >> 1] >> (16 * (i & 1)));
-        st_stream<ES>((char*)row + (int64_t)c * ES, e);
+        const int k = col(c0, i);
+        if (k >= 0 && k < D) st_stream<ES>((char*)row + (int64_t)k * ES, get(r, i));
       }
     }
   }
   // one byte per element, element i in byte i of q
-  __device__ __forceinline__ static void store8(void* row, int c0, int D, int lane,
-                                                const Raw<EPL>& q) {
-    if constexpr (WIDE) {
-      if (col(c0, lane, 0) < D) st_stream<EPL>((char*)row + col(c0, lane, 0), q);
+  __device__ __forceinline__ void store8(void* row, int c0, const Raw<EPL>& q) const {
+    const int c = col(c0, 0);
+    if constexpr (LAYOUT == WIDE) {
+      if (c < D) st_stream<EPL>((char*)row + c, q);
     } else {
+      if (LAYOUT == PHASED && whole(c)) {
+        st_stream<EPL>((char*)row + c, q);
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const int c = col(c0, lane, i);
-        if (c < D) ((uint8_t*)row)[c] = (uint8_t)(q.w[i >> 2] >> (8 * (i & 3)));
+        const int k = col(c0, i);
+        if (k >= 0 && k < D) ((uint8_t*)row)[k] = (uint8_t)(q.w[i >> 2] >> (8 * (i & 3)));
       }
     }
   }
@@ -149,6 +212,12 @@ constexpr int kTeamThreads = 32 * kTeamWarps;
 struct TeamShape {
   int warps, teams;
 };
+// Units of a row of D columns (PHASED: at most, over the rows' offsets).
+template <class T, int LAYOUT>
+int64_t row_units(int64_t D) {
+  using U = Unit<T, LAYOUT>;
+  return (D + (LAYOUT == PHASED ? U::EPL - 1 : 0) + U::COLS - 1) / U::COLS;
+}
 inline TeamShape team_shape(int64_t units, int nu) {
   TeamShape t;
   t.warps = (int)((units + nu - 1) / nu);

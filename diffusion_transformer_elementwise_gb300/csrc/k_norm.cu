@@ -52,14 +52,15 @@ __device__ __forceinline__ Quant quant_of_y(float m) {
   return q;
 }
 
-template <class T, bool WIDE>
+template <class T, int LAYOUT>
 struct NormRow {
-  using U = Unit<T, WIDE>;
+  using U = Unit<T, LAYOUT>;
   static constexpr int P = U::P;
   // 128-column groups of a unit whose maxima a lane helps to find, and the
   // lanes that share one
-  static constexpr int NG = !WIDE && sizeof(T) == 2 ? 2 : 1;
-  static constexpr int LANES = WIDE && sizeof(T) == 2 ? 16 : 32;
+  static constexpr int NG = LAYOUT == NARROW && sizeof(T) == 2 ? 2 : 1;
+  static constexpr int LANES = LAYOUT != NARROW && sizeof(T) == 2 ? 16 : 32;
+  static constexpr int BLOCKS = 32 / LANES * NG;  // groups of a unit
 
   // hidden + update, rounded (the first value alone without an update)
   __device__ __forceinline__ static Raw<16> add(const Raw<16>& h, const Raw<16>& u) {
@@ -87,12 +88,13 @@ struct NormRow {
 #pragma unroll
     for (int i = 0; i < P; ++i) t[i] = f2_mul(t[i], w[i]);
   }
-  // columns past the row hold zero; where r is not finite they became NaN
-  __device__ __forceinline__ static void mask(F2 (&y)[P], int c0, int D, int lane) {
+  // columns outside the row hold zero; where r is not finite they became NaN
+  __device__ __forceinline__ static void mask(F2 (&y)[P], const U& unit, int c0) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      if (U::col(c0, lane, 2 * i) >= D) y[i].x = 0.0f;
-      if (U::col(c0, lane, 2 * i + 1) >= D) y[i].y = 0.0f;
+      const int c = unit.col(c0, 2 * i), d = unit.col(c0, 2 * i + 1);
+      if (c < 0 || c >= unit.D) y[i].x = 0.0f;
+      if (d < 0 || d >= unit.D) y[i].y = 0.0f;
     }
   }
   __device__ __forceinline__ static float max_of(const F2 (&v)[P]) {
@@ -130,10 +132,11 @@ struct NormRow {
     }
   }
 
-  // one unit of the output, one scale per 128 columns (the whole warp calls)
-  __device__ __forceinline__ static void emit_groups(const NormArgs& a, int64_t row, int c0,
-                                                     int lane, const Raw<16>& x,
-                                                     const Raw<16>& wr, float S, float r) {
+  // one unit of the output, one scale per 128 columns (the whole warp calls;
+  // a group lies inside the unit)
+  __device__ __forceinline__ static void emit_groups(const NormArgs& a, const U& unit, int64_t row,
+                                                     int c0, const Raw<16>& x, const Raw<16>& wr,
+                                                     float S, float r) {
     F2 w[P], v[P];
     weight(wr, a.offset, w);
     weighted(x, w, v);
@@ -149,7 +152,7 @@ struct NormRow {
     if (__any_sync(0xFFFFFFFFu, slow)) {  // rare
       F2 y[P];
       normed(x, w, r, y);
-      mask(y, c0, a.D, lane);
+      mask(y, unit, c0);
       group_max(y, m);
       if (slow) {
 #pragma unroll
@@ -158,15 +161,47 @@ struct NormRow {
         for (int i = 0; i < P; ++i) v[i] = y[i];
       }
     }
-    U::store8((char*)a.out + row * a.D, c0, a.D, lane, codes(v, q));
-    const int first = WIDE ? c0 + lane / LANES * 128 : c0;
-    if (lane % LANES == 0) {
+    unit.store8((char*)a.out + row * a.D, c0, codes(v, q));
+    const int first = LAYOUT == NARROW ? c0 : c0 + unit.lane / LANES * 128;
+    if (unit.lane % LANES == 0) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const int k = first / 128 + g;
         if (k < a.groups) a.scales[row * a.groups + k] = q[g].scale;
       }
     }
+  }
+
+  // PHASED rows: a group's first column is element `off` of a granule, so
+  // the granule's first `off` elements belong to the group before it, which
+  // another warp may hold.  The maxima of a lane's own group and of that head (first
+  // lanes of a group; else zero).
+  __device__ __forceinline__ static void split_max(const F2 (&v)[P], const U& unit, float& own,
+                                                   float& head) {
+    const int cut = unit.lane % LANES == 0 ? unit.off : 0;
+    own = head = 0.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const float lo = fabsf(f2_lo(v[i])), hi = fabsf(f2_hi(v[i]));
+      if (2 * i < cut) head = max_nan(head, lo); else own = max_nan(own, lo);
+      if (2 * i + 1 < cut) head = max_nan(head, hi); else own = max_nan(own, hi);
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1)
+      own = max_nan(own, __shfl_xor_sync(0xFFFFFFFFu, own, o));
+  }
+  // codes with the factor `before` for the first `cut` elements
+  __device__ __forceinline__ static Raw<U::EPL> split_codes(const F2 (&v)[P], int cut, Quant before,
+                                                            Quant q) {
+    F2 s[P];
+    Quant one[NG];
+    one[0].pre = one[0].mul = 1.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const Quant a = 2 * i < cut ? before : q, b = 2 * i + 1 < cut ? before : q;
+      s[i] = f2_mul(f2_mul(v[i], f2(a.pre, b.pre)), f2(a.mul, b.mul));
+    }
+    return codes(s, one);
   }
 };
 
@@ -179,52 +214,75 @@ __device__ __forceinline__ float inverse_rms(float S, const NormArgs& a, Again a
   return fast_inverse_rms_scaled(again(sc), sc, a.d_f, a.inv_d, a.eps);
 }
 
-template <class T, bool WIDE, int NU, bool ADD, int Q8>
-__global__ void __launch_bounds__(kTeamThreads) norm_team_kernel(NormArgs a) {
-  using R = NormRow<T, WIDE>;
+// A CTA's teams take rows CTA * teams + team, and on by the grid's rows, a
+// multiple of the rows' period for PHASED rows.
+template <class T, int LAYOUT, int NU, bool ADD, int Q8>
+__global__ void __launch_bounds__(kTeamThreads, NU <= 2 ? 2 : 1) norm_team_kernel(NormArgs a) {
+  using R = NormRow<T, LAYOUT>;
   using U = typename R::U;
   constexpr int P = U::P;
   __shared__ float2 slots[2 * kTeamWarps];
+  // PHASED groups: (own, head) of each group of the CTA's rows, by row parity
+  constexpr bool kSplit = LAYOUT == PHASED && Q8 == 2;
+  constexpr int kBlocks = NU * R::BLOCKS;  // groups of a warp
+  __shared__ float2 groups[kSplit ? 2 : 1][kSplit ? kTeamWarps * kBlocks : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = a.warps, teams = (blockDim.x >> 5) / W;
   const int team = warp / W, m = warp - team * W;
   Team t{slots + team * 2 * W, W, m, 1 + team, 0};
   const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
+  int64_t row = (int64_t)blockIdx.x * teams + team;
+  if (row >= a.rows) return;  // the whole team
 
-  for (int64_t row = (int64_t)blockIdx.x * teams + team; row < a.rows;
-       row += (int64_t)gridDim.x * teams) {
-    Raw<16> x[NU], w[NU];
+  U unit(a.D, lane);
+  unit.at_row(row, a.rows);
+  Raw<16> w[NU];
+#pragma unroll
+  for (int j = 0; j < NU; ++j) w[j] = unit.load_weight(a.w, (m + j * W) * U::COLS);
+  for (; row < a.rows; row += (int64_t)gridDim.x * teams) {
+    unit.at_row(row, a.rows);
+    Raw<16> x[NU];
     F2 acc[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
     float big = 0.0f;
+    Raw<16> u[NU];
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
       const int c0 = (m + j * W) * U::COLS;
-      x[j] = U::load((const char*)a.x + row * pitch, c0, a.D, lane);
-      if constexpr (ADD) {
-        const Raw<16> u = U::load((const char*)a.u + row * pitch, c0, a.D, lane);
-        x[j] = R::add(x[j], u);
-      }
-      w[j] = U::load_weight(a.w, c0, a.D, lane);
+      x[j] = unit.load((const char*)a.x + row * pitch, c0);
+      if constexpr (ADD) u[j] = unit.load((const char*)a.u + row * pitch, c0);
     }
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
       const int c0 = (m + j * W) * U::COLS;
-      if constexpr (ADD) U::store((char*)a.res + row * pitch, c0, a.D, lane, x[j]);
+      if constexpr (ADD) {
+        x[j] = R::add(x[j], u[j]);
+        unit.store((char*)a.res + row * pitch, c0, x[j]);
+      }
       F2 f[P];
       Granule<T>::widen(x[j], f);
 #pragma unroll
       for (int i = 0; i < P; ++i) acc[i & 1] = f2_fma(f[i], f[i], acc[i & 1]);
-      if constexpr (Q8 == 1) {
+      if constexpr (Q8 == 1 || kSplit) {
         F2 wf[P], v[P];
         R::weight(w[j], a.offset, wf);
         R::weighted(x[j], wf, v);
-        big = max_nan(big, R::max_of(v));
+        if constexpr (kSplit) {
+          float own, head;
+          R::split_max(v, unit, own, head);
+          if (lane % R::LANES == 0)
+            groups[t.par][(team * W * NU + m + j * W) * R::BLOCKS + lane / R::LANES] = make_float2(own, head);
+          const bool bad = (own != 0.0f && !usable(own)) || (head != 0.0f && !usable(head));
+          big = bad ? 1.0f : big;
+        } else {
+          big = max_nan(big, R::max_of(v));
+        }
       }
     }
     acc[0] = f2_add(acc[0], acc[1]);
     float2 red = make_float2(warp_sum(__fadd_rn(acc[0].x, acc[0].y)), 0.0f);
-    if constexpr (Q8 == 1) red.y = warp_max(big);
-    red = t.combine<Q8 == 1>(red);
+    if constexpr (Q8 == 1 || kSplit) red.y = warp_max(big);
+    [[maybe_unused]] int par = t.par;
+    red = t.combine<Q8 == 1 || kSplit>(red);
     const float r = inverse_rms(red.x, a, [&](float sc) {
       float s2 = 0.0f;
 #pragma unroll
@@ -246,43 +304,81 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_kernel(NormArgs a) {
         F2 wf[P], y[P];
         R::weight(w[j], a.offset, wf);
         R::normed(x[j], wf, r, y);
-        U::store((char*)a.out + row * pitch, (m + j * W) * U::COLS, a.D, lane, Granule<T>::narrow(y));
+        unit.store((char*)a.out + row * pitch, (m + j * W) * U::COLS, Granule<T>::narrow(y));
       }
-    } else if constexpr (Q8 == 2) {
+    } else if constexpr (Q8 == 2 && !kSplit) {
 #pragma unroll
       for (int j = 0; j < NU; ++j)
-        R::emit_groups(a, row, (m + j * W) * U::COLS, lane, x[j], w[j], red.x, r);
+        R::emit_groups(a, unit, row, (m + j * W) * U::COLS, x[j], w[j], red.x, r);
     } else {
-      // one scale per row
-      const bool slow = !usable(red.x) || (red.y != 0.0f && !usable(red.y));
-      Quant q[R::NG];
-      if (slow) {  // rare, uniform over the row's threads
+      // one scale per row, or groups that cross granules
+      const bool slow = kSplit ? !usable(red.x) || red.y != 0.0f
+                               : !usable(red.x) || (red.y != 0.0f && !usable(red.y));
+      Quant q[R::NG] = {};
+      if (slow) {  // rare, uniform over the row's threads: the maxima of y
         float my = 0.0f;
+        if constexpr (kSplit) {
+          par = t.par;
+          if (W == 1) __syncwarp();  // the pieces below replace those read above
+        }
 #pragma unroll
         for (int j = 0; j < NU; ++j) {
           F2 wf[P], y[P];
           R::weight(w[j], a.offset, wf);
           R::normed(x[j], wf, r, y);
-          R::mask(y, (m + j * W) * U::COLS, a.D, lane);
-          my = max_nan(my, R::max_of(y));
+          R::mask(y, unit, (m + j * W) * U::COLS);
+          if constexpr (kSplit) {
+            float own, head;
+            R::split_max(y, unit, own, head);
+            if (lane % R::LANES == 0)
+              groups[par][(team * W * NU + m + j * W) * R::BLOCKS + lane / R::LANES] = make_float2(own, head);
+          } else {
+            my = max_nan(my, R::max_of(y));
+          }
         }
-        q[0] = quant_of_y(t.combine<true>(make_float2(0.0f, warp_max(my))).y);
-      } else {
+        const float2 again = t.combine<true>(make_float2(0.0f, warp_max(my)));
+        if constexpr (!kSplit) q[0] = quant_of_y(again.y);
+      } else if constexpr (!kSplit) {
         q[0] = quant_of_t(red.y, r);
+      }
+      if constexpr (kSplit) {
+        if (W == 1) __syncwarp();
       }
 #pragma unroll
       for (int g = 1; g < R::NG; ++g) q[g] = q[0];
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
+        const int c0 = (m + j * W) * U::COLS;
         F2 wf[P], v[P];
         R::weight(w[j], a.offset, wf);
         if (slow)
           R::normed(x[j], wf, r, v);
         else
           R::weighted(x[j], wf, v);
-        U::store8((char*)a.out + row * a.D, (m + j * W) * U::COLS, a.D, lane, R::codes(v, q));
+        if constexpr (kSplit) {
+          // group k's maximum: its own part, and the next one's head
+          const float2* g = groups[par] + team * W * kBlocks;
+          const int k = (m + j * W) * R::BLOCKS + lane / R::LANES, n = W * kBlocks;
+          auto quant = [&](int k) {
+            const float big = k + 1 < n ? max_nan(g[k].x, g[k + 1].y) : g[k].x;
+            return slow ? quant_of_y(big) : quant_of_t(big, r);
+          };
+          const int cut = lane % R::LANES == 0 ? unit.off : 0;
+          const Quant mine = quant(k);
+          const Quant before = cut && k > 0 ? quant(k - 1) : mine;
+          unit.store8((char*)a.out + row * a.D, c0, R::split_codes(v, cut, before, mine));
+          if (lane % R::LANES == 0 && k < a.groups) a.scales[row * a.groups + k] = mine.scale;
+        } else {
+          unit.store8((char*)a.out + row * a.D, c0, R::codes(v, q));
+        }
       }
-      if (m == 0 && lane == 0) a.scales[row] = q[0].scale;
+      if (!kSplit && m == 0 && lane == 0) a.scales[row] = q[0].scale;
+      if constexpr (kSplit) {
+        if (W == 1) {
+          t.par ^= 1;  // (a team of one warp has no barrier to alternate them)
+          __syncwarp();
+        }
+      }
     }
   }
 }
@@ -291,9 +387,9 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_kernel(NormArgs a) {
 // the output (with an update, each thread its own stores of the residual).
 // The squares of a unit are summed in fp32 and the units in fp64, so that a
 // thread's thousands of units add no error.
-template <class T, bool WIDE, bool ADD, int Q8>
+template <class T, int LAYOUT, bool ADD, int Q8>
 __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
-  using R = NormRow<T, WIDE>;
+  using R = NormRow<T, LAYOUT>;
   using U = typename R::U;
   constexpr int P = U::P;
   __shared__ float2 slots[2 * 32];
@@ -301,16 +397,17 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   Team t{slots, W, warp, 1, 0};
   const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
+  const U unit(a.D, lane);
 
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const char* src = (const char*)(ADD ? a.res : a.x) + row * pitch;
     double total = 0.0;
     float big = 0.0f;
     for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
-      Raw<16> x = U::load((const char*)a.x + row * pitch, c0, a.D, lane);
+      Raw<16> x = unit.load((const char*)a.x + row * pitch, c0);
       if constexpr (ADD) {
-        x = R::add(x, U::load((const char*)a.u + row * pitch, c0, a.D, lane));
-        U::store((char*)a.res + row * pitch, c0, a.D, lane, x);
+        x = R::add(x, unit.load((const char*)a.u + row * pitch, c0));
+        unit.store((char*)a.res + row * pitch, c0, x);
       }
       F2 f[P];
       Granule<T>::widen(x, f);
@@ -320,7 +417,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
       total += (double)__fadd_rn(acc.x, acc.y);
       if constexpr (Q8 == 1) {
         F2 wf[P], v[P];
-        R::weight(U::load_weight(a.w, c0, a.D, lane), a.offset, wf);
+        R::weight(unit.load_weight(a.w, c0), a.offset, wf);
         R::weighted(x, wf, v);
         big = max_nan(big, R::max_of(v));
       }
@@ -338,7 +435,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
       double s2 = 0.0;
       for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
         F2 f[P];
-        Granule<T>::widen(U::load(src, c0, a.D, lane), f);
+        Granule<T>::widen(unit.load(src, c0), f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const double u0 = (double)__fmul_rn(f2_lo(f[i]), sc), u1 = (double)__fmul_rn(f2_hi(f[i]), sc);
@@ -363,9 +460,9 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
         float my = 0.0f;
         for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
           F2 wf[P], y[P];
-          R::weight(U::load_weight(a.w, c0, a.D, lane), a.offset, wf);
-          R::normed(U::load(src, c0, a.D, lane), wf, r, y);
-          R::mask(y, c0, a.D, lane);
+          R::weight(unit.load_weight(a.w, c0), a.offset, wf);
+          R::normed(unit.load(src, c0), wf, r, y);
+          R::mask(y, unit, c0);
           my = max_nan(my, R::max_of(y));
         }
         q[0] = quant_of_y(t.combine<true>(make_float2(0.0f, warp_max(my))).y);
@@ -377,10 +474,10 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
       if (threadIdx.x == 0) a.scales[row] = q[0].scale;
     }
     for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
-      const Raw<16> x = U::load(src, c0, a.D, lane);
-      const Raw<16> w = U::load_weight(a.w, c0, a.D, lane);
+      const Raw<16> x = unit.load(src, c0);
+      const Raw<16> w = unit.load_weight(a.w, c0);
       if constexpr (Q8 == 2) {
-        R::emit_groups(a, row, c0, lane, x, w, S, r);
+        R::emit_groups(a, unit, row, c0, x, w, S, r);
       } else {
         F2 wf[P], v[P];
         R::weight(w, a.offset, wf);
@@ -389,62 +486,74 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
         else
           R::weighted(x, wf, v);
         if constexpr (Q8 == 0)
-          U::store((char*)a.out + row * pitch, c0, a.D, lane, Granule<T>::narrow(v));
+          unit.store((char*)a.out + row * pitch, c0, Granule<T>::narrow(v));
         else
-          U::store8((char*)a.out + row * a.D, c0, a.D, lane, R::codes(v, q));
+          unit.store8((char*)a.out + row * a.D, c0, R::codes(v, q));
       }
     }
   }
 }
 
-template <class T, bool WIDE, bool ADD, int Q8>
+template <class T, int LAYOUT, bool ADD, int Q8>
 cudaError_t launch(const DeviceInfo& dev, NormArgs a, cudaStream_t s) {
-  const int64_t units = (a.D + Unit<T, WIDE>::COLS - 1) / Unit<T, WIDE>::COLS;
+  const int64_t units = row_units<T, LAYOUT>(a.D);
   auto team = [&](auto nu) -> cudaError_t {
     constexpr int NU = decltype(nu)::value;
+    const auto kern = norm_team_kernel<T, LAYOUT, NU, ADD, Q8>;
     const TeamShape t = team_shape(units, NU);
     a.warps = t.warps;
     const int block = t.warps * t.teams * 32;
     int64_t grid = (a.rows + t.teams - 1) / t.teams;
+    if (LAYOUT == PHASED) {
+      // one wave, whose rows are a multiple of the period: a team's rows
+      // have one offset, at which it loads the weights once
+      const int64_t wave = (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, block);
+      if (grid > wave) grid = wave < 8 ? 8 : wave;
+      grid = (grid + 7) / 8 * 8;
+    }
     if (grid > (int64_t(1) << 30)) grid = int64_t(1) << 30;
-    norm_team_kernel<T, WIDE, NU, ADD, Q8><<<(unsigned)grid, block, 0, s>>>(a);
+    kern<<<(unsigned)grid, block, 0, s>>>(a);
     return cudaGetLastError();
   };
   if (units <= 8) return team(std::integral_constant<int, 1>{});
   if (units <= 2 * kTeamWarps) return team(std::integral_constant<int, 2>{});
   if (units <= 4 * kTeamWarps) return team(std::integral_constant<int, 4>{});
-  int64_t grid = (int64_t)dev.sm_count * 2;
-  if (grid > a.rows) grid = a.rows;
-  norm_long_kernel<T, WIDE, ADD, Q8><<<(unsigned)grid, 1024, 0, s>>>(a);
-  return cudaGetLastError();
+  if constexpr (LAYOUT == PHASED) {
+    return launch<T, NARROW, ADD, Q8>(dev, a, s);
+  } else {
+    int64_t grid = (int64_t)dev.sm_count * 2;
+    if (grid > a.rows) grid = a.rows;
+    norm_long_kernel<T, LAYOUT, ADD, Q8><<<(unsigned)grid, 1024, 0, s>>>(a);
+    return cudaGetLastError();
+  }
 }
 
-template <class T, bool WIDE>
+template <class T, int LAYOUT>
 cudaError_t launch_form(const DeviceInfo& dev, int q8, const NormArgs& a, cudaStream_t s) {
   if (a.u)
-    return q8 == 0   ? launch<T, WIDE, true, 0>(dev, a, s)
-           : q8 == 1 ? launch<T, WIDE, true, 1>(dev, a, s)
-                     : launch<T, WIDE, true, 2>(dev, a, s);
-  return q8 == 0   ? launch<T, WIDE, false, 0>(dev, a, s)
-         : q8 == 1 ? launch<T, WIDE, false, 1>(dev, a, s)
-                   : launch<T, WIDE, false, 2>(dev, a, s);
+    return q8 == 0   ? launch<T, LAYOUT, true, 0>(dev, a, s)
+           : q8 == 1 ? launch<T, LAYOUT, true, 1>(dev, a, s)
+                     : launch<T, LAYOUT, true, 2>(dev, a, s);
+  return q8 == 0   ? launch<T, LAYOUT, false, 0>(dev, a, s)
+         : q8 == 1 ? launch<T, LAYOUT, false, 1>(dev, a, s)
+                   : launch<T, LAYOUT, false, 2>(dev, a, s);
+}
+
+template <class T>
+cudaError_t launch_layout(const DeviceInfo& dev, int layout, int q8, const NormArgs& a,
+                          cudaStream_t s) {
+  return layout == WIDE     ? launch_form<T, WIDE>(dev, q8, a, s)
+         : layout == PHASED ? launch_form<T, PHASED>(dev, q8, a, s)
+                            : launch_form<T, NARROW>(dev, q8, a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_norm(const DeviceInfo& dev, int dtype, bool wide, int q8, const NormArgs& a,
+cudaError_t launch_norm(const DeviceInfo& dev, int dtype, int layout, int q8, const NormArgs& a,
                         cudaStream_t s) {
-  switch (dtype) {
-    case 0:
-      return wide ? launch_form<__nv_bfloat16, true>(dev, q8, a, s)
-                  : launch_form<__nv_bfloat16, false>(dev, q8, a, s);
-    case 1:
-      return wide ? launch_form<__half, true>(dev, q8, a, s)
-                  : launch_form<__half, false>(dev, q8, a, s);
-    default:
-      return wide ? launch_form<float, true>(dev, q8, a, s)
-                  : launch_form<float, false>(dev, q8, a, s);
-  }
+  return dtype == 0   ? launch_layout<__nv_bfloat16>(dev, layout, q8, a, s)
+         : dtype == 1 ? launch_layout<__half>(dev, layout, q8, a, s)
+                      : launch_layout<float>(dev, layout, q8, a, s);
 }
 
 }  // namespace dit

@@ -9,11 +9,17 @@
 // Both sums of a row, x^2 and t x, are one reduction over the row held in
 // registers, and r is formed again from x rather than read.
 //
-// A CTA takes rows c, c + G, c + 2G, ... and adds its part of gw in
-// registers: each thread owns the same columns of every row.  Each CTA writes one
+// One CTA per SM, of as many teams as its registers hold.  A team takes rows
+// a grid's teams apart and adds its part of gw in registers: each thread owns
+// the same columns of every row.  The CTA adds its teams' parts and writes one
 // row of `partial`, and a second kernel adds the rows in order: no atomics, so
 // the same call gives the same bits.
+//
+// Each lane copies the granules it will read itself into its own slots of
+// shared memory (cp.async), kStages rows ahead, so the copies need no barrier
+// and a warp's loads are in flight while it reduces and writes.
 #include <algorithm>
+#include <atomic>
 
 #include "dit_stat.cuh"
 #include "dit_token.h"
@@ -42,9 +48,9 @@ __device__ __forceinline__ RowStat row_stat(float2 sums, const NormGradArgs& a, 
   return o;
 }
 
-template <class T, bool WIDE>
+template <class T, int LAYOUT>
 struct GradRow {
-  using U = Unit<T, WIDE>;
+  using U = Unit<T, LAYOUT>;
   static constexpr int P = U::P;
   // sums of x^2 and of g (offset + w) x over a lane's elements of one unit,
   // x scaled by sc
@@ -89,75 +95,144 @@ struct GradRow {
     return Granule<T>::narrow(o);
   }
   // a lane's elements of one unit of fp32 columns (partial sums)
-  __device__ __forceinline__ static void put(float* row, int c0, int D, int lane, const F2 (&v)[P]) {
+  __device__ __forceinline__ static void put(float* row, const U& unit, int c0, const F2 (&v)[P]) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int c = U::col(c0, lane, 2 * i), d = U::col(c0, lane, 2 * i + 1);
-      if (c < D) row[c] = v[i].x;
-      if (d < D) row[d] = v[i].y;
+      const int c = unit.col(c0, 2 * i), d = unit.col(c0, 2 * i + 1);
+      if (c >= 0 && c < unit.D) row[c] = v[i].x;
+      if (d >= 0 && d < unit.D) row[d] = v[i].y;
     }
   }
 };
 
-template <class T, bool WIDE, int NU>
-__global__ void __launch_bounds__(kTeamThreads) grad_team_kernel(NormGradArgs a) {
-  using R = GradRow<T, WIDE>;
+constexpr int kStages = 2;
+// warps of a CTA, which set the registers of a thread: 80 for one unit a
+// warp, 128 for more
+template <int NU>
+constexpr int kGradWarps = NU == 1 ? 24 : 16;
+
+// SKIP: the gradient of the skip path is added.
+template <class T, int LAYOUT, int NU, bool SKIP>
+__global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGradArgs a) {
+  using R = GradRow<T, LAYOUT>;
   using U = typename R::U;
   constexpr int P = U::P;
-  __shared__ float2 slots[2 * kTeamWarps];
-  extern __shared__ float merged[];  // [teams][warps * NU * U::COLS], more than one team
+  constexpr int NS = SKIP ? 3 : 2;              // streams
+  constexpr bool kStaged = LAYOUT != NARROW;
+  constexpr uint32_t kSlot = 32 * 16;           // a unit of one stream
+  constexpr uint32_t kStage = NS * NU * kSlot;  // a warp's part of a row
+  __shared__ float2 slots[2 * kGradWarps<NU>];
+  extern __shared__ float4 shared[];  // [warps][stages][streams][NU][32], then the teams' parts of gw
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = a.warps, teams = (blockDim.x >> 5) / W;
   const int team = warp / W, m = warp - team * W;
   Team t{slots + team * 2 * W, W, m, 1 + team, 0};
   const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
+  const int64_t step = (int64_t)gridDim.x * teams;
+  const char* const src[3] = {(const char*)a.x, (const char*)a.g, (const char*)a.gres};
+  const uint32_t stage0 = smem_addr(shared) + warp * (kStages * kStage) + lane * 16;
+
+  int64_t row = (int64_t)blockIdx.x * teams + team;
+  U unit(a.D, lane);
+  unit.at_row(row, a.rows);
+  // this warp's part of row r, into stage s (an empty group past the end)
+  auto prefetch = [&](int64_t r, int s) {
+    if constexpr (kStaged) {
+      if (r < a.rows) {
+        const int64_t end = a.rows * pitch;
+#pragma unroll
+        for (int j = 0; j < NU; ++j) {
+          const int c = unit.col((m + j * W) * U::COLS, 0);
+          if (c >= a.D) continue;
+          const int64_t at = r * pitch + (int64_t)c * U::ES;
+          const uint32_t dst = stage0 + s * kStage + j * kSlot;
+#pragma unroll
+          for (int k = 0; k < NS; ++k) {
+            // PHASED: the tensor's last granule may run past its end
+            if (LAYOUT == PHASED && end - at < 16)
+              cp_async16_part(dst + k * NU * kSlot, src[k] + at, (uint32_t)(end - at));
+            else
+              cp_async16(dst + k * NU * kSlot, src[k] + at);
+          }
+        }
+      }
+      cp_async_commit();
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) prefetch(row + s * step, s);
 
   Raw<16> w[NU];
   F2 acc[NU][P];
 #pragma unroll
   for (int j = 0; j < NU; ++j) {
-    w[j] = U::load_weight(a.w, (m + j * W) * U::COLS, a.D, lane);
+    w[j] = unit.load_weight(a.w, (m + j * W) * U::COLS);
 #pragma unroll
     for (int i = 0; i < P; ++i) acc[j][i] = f2(0.0f, 0.0f);
   }
-  for (int64_t row = (int64_t)blockIdx.x * teams + team; row < a.rows;
-       row += (int64_t)gridDim.x * teams) {
+  int s = 0;
+  for (; row < a.rows; row += step) {
+    unit.at_row(row, a.rows);
     Raw<16> x[NU], g[NU], k[NU];
+    if constexpr (kStaged) cp_async_wait<kStages - 1>();  // this lane's copies of the row
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
       const int c0 = (m + j * W) * U::COLS;
-      x[j] = U::load((const char*)a.x + row * pitch, c0, a.D, lane);
-      g[j] = U::load((const char*)a.g + row * pitch, c0, a.D, lane);
-      k[j] = Raw<16>{};
-      if (a.gres) k[j] = U::load((const char*)a.gres + row * pitch, c0, a.D, lane);
+      if constexpr (kStaged) {
+        const int c = unit.col(c0, 0);
+        const uint32_t at = stage0 + s * kStage + j * kSlot;
+        x[j] = g[j] = k[j] = Raw<16>{};
+        if (c < a.D) {
+          x[j] = lds16(at);
+          g[j] = lds16(at + NU * kSlot);
+          if constexpr (SKIP) k[j] = lds16(at + 2 * NU * kSlot);
+          if (LAYOUT == PHASED && !unit.whole(c)) {
+            unit.mask(x[j], c);
+            unit.mask(g[j], c);
+          }
+        }
+      } else {
+        x[j] = unit.load((const char*)a.x + row * pitch, c0);
+        g[j] = unit.load((const char*)a.g + row * pitch, c0);
+        if constexpr (SKIP) k[j] = unit.load((const char*)a.gres + row * pitch, c0);
+      }
     }
-    auto sums = [&](float sc) {
+    F2 sx = f2(0.0f, 0.0f), sq = sx;
+#pragma unroll
+    for (int j = 0; j < NU; ++j) R::sums(x[j], g[j], w[j], a.offset, 1.0f, sx, sq);
+    // the stage has been read
+    prefetch(row + kStages * step, s);
+    s = s + 1 == kStages ? 0 : s + 1;
+    const float2 sums = t.combine<false>(
+        make_float2(warp_sum(__fadd_rn(sx.x, sx.y)), warp_sum(__fadd_rn(sq.x, sq.y))));
+    const RowStat st = row_stat(sums, a, [&](float sc) {
       F2 s = f2(0.0f, 0.0f), q = s;
 #pragma unroll
       for (int j = 0; j < NU; ++j) R::sums(x[j], g[j], w[j], a.offset, sc, s, q);
       return t.combine<false>(
           make_float2(warp_sum(__fadd_rn(s.x, s.y)), warp_sum(__fadd_rn(q.x, q.y))));
-    };
-    const RowStat st = row_stat(sums(1.0f), a, sums);
+    });
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-      const Raw<16> o = R::grad(x[j], g[j], w[j], k[j], a.gres != nullptr, a.offset, st, acc[j]);
-      U::store((char*)a.gx + row * pitch, (m + j * W) * U::COLS, a.D, lane, o);
+      const Raw<16> o = R::grad(x[j], g[j], w[j], k[j], SKIP, a.offset, st, acc[j]);
+      unit.store((char*)a.gx + row * pitch, (m + j * W) * U::COLS, o);
     }
   }
   if (!a.partial) return;
   float* out = a.partial + (int64_t)blockIdx.x * a.D;
   if (teams == 1) {
 #pragma unroll
-    for (int j = 0; j < NU; ++j) R::put(out, (m + j * W) * U::COLS, a.D, lane, acc[j]);
+    for (int j = 0; j < NU; ++j) R::put(out, unit, (m + j * W) * U::COLS, acc[j]);
   } else {
-    const int cols = W * NU * U::COLS;
+    if constexpr (kStaged) cp_async_wait<0>();
+    __syncthreads();  // the stages are no longer read or written
+    float* merged = (float*)shared;  // [teams][D]
 #pragma unroll
-    for (int j = 0; j < NU; ++j) R::put(merged + team * cols, (m + j * W) * U::COLS, a.D, lane, acc[j]);
+    for (int j = 0; j < NU; ++j) R::put(merged + team * a.D, unit, (m + j * W) * U::COLS, acc[j]);
     __syncthreads();
     for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
       float v = merged[c];
-      for (int q = 1; q < teams; ++q) v = __fadd_rn(v, merged[q * cols + c]);
+      for (int q = 1; q < teams; ++q) v = __fadd_rn(v, merged[q * a.D + c]);
       out[c] = v;
     }
   }
@@ -165,14 +240,15 @@ __global__ void __launch_bounds__(kTeamThreads) grad_team_kernel(NormGradArgs a)
 
 // Rows longer than a CTA's registers: read twice, gw added in the CTA's row
 // of `partial` itself (each column by one thread).
-template <class T, bool WIDE>
+template <class T, int LAYOUT>
 __global__ void __launch_bounds__(1024) grad_long_kernel(NormGradArgs a) {
-  using R = GradRow<T, WIDE>;
+  using R = GradRow<T, LAYOUT>;
   using U = typename R::U;
   constexpr int P = U::P;
   __shared__ double2 part[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
+  const U unit(a.D, lane);
   float* out = a.partial ? a.partial + (int64_t)blockIdx.x * a.D : nullptr;
   bool first = true;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, first = false) {
@@ -182,8 +258,8 @@ __global__ void __launch_bounds__(1024) grad_long_kernel(NormGradArgs a) {
       double2 v = make_double2(0.0, 0.0);
       for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
         F2 s = f2(0.0f, 0.0f), q = s;
-        R::sums(U::load(xp, c0, a.D, lane), U::load(gp, c0, a.D, lane),
-                U::load_weight(a.w, c0, a.D, lane), a.offset, sc, s, q);
+        R::sums(unit.load(xp, c0), unit.load(gp, c0),
+                unit.load_weight(a.w, c0), a.offset, sc, s, q);
         v.x += (double)__fadd_rn(s.x, s.y);
         v.y += (double)__fadd_rn(q.x, q.y);
       }
@@ -207,15 +283,15 @@ __global__ void __launch_bounds__(1024) grad_long_kernel(NormGradArgs a) {
       F2 acc[P];
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        const int c = U::col(c0, lane, 2 * i), d = U::col(c0, lane, 2 * i + 1);
+        const int c = unit.col(c0, 2 * i), d = unit.col(c0, 2 * i + 1);
         acc[i] = f2(!first && out && c < a.D ? out[c] : 0.0f, !first && out && d < a.D ? out[d] : 0.0f);
       }
-      const Raw<16> k = a.gres ? U::load((const char*)a.gres + row * pitch, c0, a.D, lane) : Raw<16>{};
-      const Raw<16> o = R::grad(U::load(xp, c0, a.D, lane), U::load(gp, c0, a.D, lane),
-                                U::load_weight(a.w, c0, a.D, lane), k, a.gres != nullptr, a.offset,
+      const Raw<16> k = a.gres ? unit.load((const char*)a.gres + row * pitch, c0) : Raw<16>{};
+      const Raw<16> o = R::grad(unit.load(xp, c0), unit.load(gp, c0),
+                                unit.load_weight(a.w, c0), k, a.gres != nullptr, a.offset,
                                 st, acc);
-      U::store((char*)a.gx + row * pitch, c0, a.D, lane, o);
-      if (out) R::put(out, c0, a.D, lane, acc);
+      unit.store((char*)a.gx + row * pitch, c0, o);
+      if (out) R::put(out, unit, c0, acc);
     }
   }
 }
@@ -240,50 +316,66 @@ __global__ void __launch_bounds__(1024) grad_weight_kernel(const float* partial,
   }
 }
 
-template <class T, bool WIDE>
-cudaError_t launch(const DeviceInfo& dev, NormGradArgs a, void* gw, cudaStream_t s) {
-  using U = Unit<T, WIDE>;
-  const int64_t units = (a.D + U::COLS - 1) / U::COLS;
-  int64_t grid = 0;
-  auto team = [&](auto nu) {
+template <class T, int LAYOUT, bool SKIP>
+cudaError_t launch_rows(const DeviceInfo& dev, NormGradArgs a, int64_t* ctas, cudaStream_t s) {
+  using U = Unit<T, LAYOUT>;
+  const int64_t units = row_units<T, LAYOUT>(a.D);
+  auto team = [&](auto nu) -> cudaError_t {
     constexpr int NU = decltype(nu)::value;
-    const TeamShape t = team_shape(units, NU);
-    a.warps = t.warps;
-    const int block = t.warps * t.teams * 32;
-    const size_t smem = t.teams > 1 ? (size_t)t.teams * t.warps * NU * U::COLS * 4 : 0;
-    const void* fn = (const void*)grad_team_kernel<T, WIDE, NU>;
-    grid = (int64_t)dev.sm_count * resident_ctas(dev, fn, block, smem);
-    grid = std::min(grid, std::min(kNormGradMaxCtas, (a.rows + t.teams - 1) / t.teams));
-    grad_team_kernel<T, WIDE, NU><<<(unsigned)grid, block, smem, s>>>(a);
+    const auto kern = grad_team_kernel<T, LAYOUT, NU, SKIP>;
+    a.warps = (int)((units + NU - 1) / NU);
+    // few rows: a CTA for each before a second team in any
+    const int64_t teams = std::max<int64_t>(
+        1, std::min<int64_t>(kGradWarps<NU> / a.warps, (a.rows + dev.sm_count - 1) / dev.sm_count));
+    int64_t grid = std::min<int64_t>(dev.sm_count, (a.rows + teams - 1) / teams);
+    // PHASED: a team's rows have one offset when they are a multiple of 8 apart
+    if (LAYOUT == PHASED) grid = (grid + 7) / 8 * 8;
+    const int block = (int)teams * a.warps * 32;
+    const size_t stages = LAYOUT == NARROW ? 0 : (size_t)block * kStages * (SKIP ? 3 : 2) * NU * 16;
+    const size_t smem = std::max(stages, teams > 1 ? (size_t)teams * a.D * 4 : 0);
+    static std::atomic<int> opted[kOptinDevices];
+    cudaError_t e = allow_dynamic_smem((const void*)kern, dev, smem, opted);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)grid, block, smem, s>>>(a);
+    *ctas = grid;
+    return cudaGetLastError();
   };
-  if (units <= 8) {
-    team(std::integral_constant<int, 1>{});
-  } else if (units <= 2 * kTeamWarps) {
-    team(std::integral_constant<int, 2>{});
-  } else if (units <= 4 * kTeamWarps) {
-    team(std::integral_constant<int, 4>{});
+  if (units <= 8) return team(std::integral_constant<int, 1>{});
+  if (units <= 2 * kTeamWarps) return team(std::integral_constant<int, 2>{});
+  if (units <= 4 * kTeamWarps) return team(std::integral_constant<int, 4>{});
+  if constexpr (LAYOUT == PHASED) {
+    return launch_rows<T, NARROW, SKIP>(dev, a, ctas, s);
   } else {
-    grid = std::min(std::min<int64_t>(dev.sm_count, a.rows), kNormGradMaxCtas);
-    grad_long_kernel<T, WIDE><<<(unsigned)grid, 1024, 0, s>>>(a);
+    *ctas = std::min<int64_t>(dev.sm_count, a.rows);
+    grad_long_kernel<T, LAYOUT><<<(unsigned)*ctas, 1024, 0, s>>>(a);
+    return cudaGetLastError();
   }
-  const cudaError_t e = cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch(const DeviceInfo& dev, int layout, const NormGradArgs& a, void* gw,
+                   cudaStream_t s) {
+  int64_t ctas = 0;
+  const bool skip = a.gres != nullptr;
+  const cudaError_t e =
+      layout == WIDE     ? (skip ? launch_rows<T, WIDE, true>(dev, a, &ctas, s)
+                                 : launch_rows<T, WIDE, false>(dev, a, &ctas, s))
+      : layout == PHASED ? (skip ? launch_rows<T, PHASED, true>(dev, a, &ctas, s)
+                                 : launch_rows<T, PHASED, false>(dev, a, &ctas, s))
+                         : (skip ? launch_rows<T, NARROW, true>(dev, a, &ctas, s)
+                                 : launch_rows<T, NARROW, false>(dev, a, &ctas, s));
   if (e != cudaSuccess || !gw) return e;
-  grad_weight_kernel<T><<<(unsigned)((a.D + 31) / 32), 1024, 0, s>>>(a.partial, (int)grid, a.D, gw);
+  grad_weight_kernel<T><<<(unsigned)((a.D + 31) / 32), 1024, 0, s>>>(a.partial, (int)ctas, a.D, gw);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_norm_grad(const DeviceInfo& dev, int dtype, bool wide, const NormGradArgs& a,
+cudaError_t launch_norm_grad(const DeviceInfo& dev, int dtype, int layout, const NormGradArgs& a,
                              void* gw, cudaStream_t s) {
-  switch (dtype) {
-    case 0:
-      return wide ? launch<__nv_bfloat16, true>(dev, a, gw, s) : launch<__nv_bfloat16, false>(dev, a, gw, s);
-    case 1:
-      return wide ? launch<__half, true>(dev, a, gw, s) : launch<__half, false>(dev, a, gw, s);
-    default:
-      return wide ? launch<float, true>(dev, a, gw, s) : launch<float, false>(dev, a, gw, s);
-  }
+  return dtype == 0   ? launch<__nv_bfloat16>(dev, layout, a, gw, s)
+         : dtype == 1 ? launch<__half>(dev, layout, a, gw, s)
+                      : launch<float>(dev, layout, a, gw, s);
 }
 
 }  // namespace dit
