@@ -16,7 +16,7 @@ import ctypes
 
 import torch
 
-from ._binding import _FP8, _cuda, _dtype, _launch, _stream, check, library
+from ._binding import _FP8, DTYPE_CODES, _cuda, _dtype, _stream, check, library
 
 ID_CODES = {torch.int32: 0, torch.int64: 1}
 
@@ -72,26 +72,57 @@ def _workspace(given, nbytes, ref, stream):
     return given, given.data_ptr(), given.numel() * given.element_size()
 
 
+_get_device = torch._C._cuda_getDevice
+
+
+def _call(dev, fn, what, *args):
+    """The C entry point with `dev` as the current device; raises on a status."""
+    if _get_device() == dev:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st:
+        check(st, what)
+
+
 def _rows(x, name):
     """(rows, D) of a tensor whose last dimension is the row."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError(f"{name} must be a tensor of at least one dimension")
     D = x.shape[-1]
-    rows = 1
-    for s in x.shape[:-1]:
-        rows *= s
-    return rows, D
+    return (x.numel() // D if D else 0), D
 
 
-def _same_shape(ref, *others):
-    for name, t in others:
-        if t.shape != ref.shape:
-            raise ValueError(f"{name} must have the shape {tuple(ref.shape)}, got {tuple(t.shape)}")
-
-
-def _vector(weight, D):
-    if weight.shape != (D,):
+def _same(x, named, weight=None, D=0):
+    """Checks that the tensors of `named` (name, tensor, ...; x among them) are
+    contiguous, of x's shape and dtype, on its CUDA device, and the weight [D].
+    Returns (device index, dtype code).  The usual case takes one pass; what
+    is wrong is found out in a second."""
+    try:
+        shape, dtype, dev = x.shape, x.dtype, x.get_device()
+        ok = dev >= 0 and dtype in DTYPE_CODES
+        for t in named[1::2]:
+            ok = (ok and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev
+                  and t.shape == shape)
+        if weight is not None:
+            ok = (ok and weight.dtype is dtype and weight.is_contiguous()
+                  and weight.get_device() == dev and weight.dim() == 1 and weight.numel() == D)
+    except AttributeError:
+        ok = False
+    if ok:
+        return dev, DTYPE_CODES[dtype]
+    pairs = list(zip(named[::2], named[1::2]))
+    if weight is not None:
+        pairs.append(("weight", weight))
+    dev = _cuda(*pairs)
+    dt = _dtype(x, *pairs)
+    for name, t in zip(named[::2], named[1::2]):
+        if t.shape != x.shape:
+            raise ValueError(f"{name} must have the shape {tuple(x.shape)}, got {tuple(t.shape)}")
+    if weight is not None and weight.shape != (D,):
         raise ValueError(f"weight must be [{D}], got {tuple(weight.shape)}")
+    return dev, dt
 
 
 def rmsnorm(x, weight, eps=1e-6, weight_offset=0.0, out=None, stream=None):
@@ -101,14 +132,9 @@ def rmsnorm(x, weight, eps=1e-6, weight_offset=0.0, out=None, stream=None):
     rows, D = _rows(x, "x")
     if out is None:
         out = _empty(x.shape, x.dtype, x.device, stream)
-    dev = _cuda(("x", x), ("weight", weight), ("out", out))
-    dt = _dtype(x, ("weight", weight), ("out", out))
-    _vector(weight, D)
-    _same_shape(x, ("out", out))
-    st = _launch(dev, library().dit_rmsnorm, out.data_ptr(), x.data_ptr(), weight.data_ptr(), rows,
-                 D, eps, weight_offset, dt, _stream(dev, stream))
-    if st:
-        check(st, "dit_rmsnorm")
+    dev, dt = _same(x, ("x", x, "out", out), weight, D)
+    _call(dev, library().dit_rmsnorm, "dit_rmsnorm", out.data_ptr(), x.data_ptr(),
+          weight.data_ptr(), rows, D, eps, weight_offset, dt, _stream(dev, stream))
     return out
 
 
@@ -122,17 +148,11 @@ def add_rmsnorm(hidden, update, weight, eps=1e-6, weight_offset=0.0, residual_ou
         residual_out = _empty(hidden.shape, hidden.dtype, hidden.device, stream)
     if out is None:
         out = _empty(hidden.shape, hidden.dtype, hidden.device, stream)
-    dev = _cuda(("hidden", hidden), ("update", update), ("weight", weight),
-                ("residual_out", residual_out), ("out", out))
-    dt = _dtype(hidden, ("update", update), ("weight", weight), ("residual_out", residual_out),
-                ("out", out))
-    _vector(weight, D)
-    _same_shape(hidden, ("update", update), ("residual_out", residual_out), ("out", out))
-    st = _launch(dev, library().dit_add_rmsnorm, residual_out.data_ptr(), out.data_ptr(),
-                 hidden.data_ptr(), update.data_ptr(), weight.data_ptr(), rows, D, eps,
-                 weight_offset, dt, _stream(dev, stream))
-    if st:
-        check(st, "dit_add_rmsnorm")
+    dev, dt = _same(hidden, ("hidden", hidden, "update", update, "residual_out", residual_out,
+                             "out", out), weight, D)
+    _call(dev, library().dit_add_rmsnorm, "dit_add_rmsnorm", residual_out.data_ptr(),
+          out.data_ptr(), hidden.data_ptr(), update.data_ptr(), weight.data_ptr(), rows, D, eps,
+          weight_offset, dt, _stream(dev, stream))
     return residual_out, out
 
 
@@ -149,7 +169,12 @@ def _codes(x, D, group, out, scales, stream):
         scales = _empty(shape, torch.float32, x.device, stream)
     elif scales.dtype is not torch.float32 or scales.shape != shape:
         raise ValueError(f"scales must be float32 {shape}, got {scales.dtype} {tuple(scales.shape)}")
-    _same_shape(x, ("out", out))
+    if out.shape != x.shape:
+        raise ValueError(f"out must have the shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    dev = x.get_device()
+    if (out.get_device() != dev or scales.get_device() != dev or not out.is_contiguous()
+            or not scales.is_contiguous()):
+        _cuda(("x", x), ("out", out), ("scales", scales))
     return out, scales
 
 
@@ -161,13 +186,10 @@ def rmsnorm_fp8(x, weight, eps=1e-6, group=0, weight_offset=0.0, out=None, scale
     (out, scales); out is float8_e4m3fn, or the uint8 tensor given."""
     rows, D = _rows(x, "x")
     out, scales = _codes(x, D, group, out, scales, stream)
-    dev = _cuda(("x", x), ("weight", weight), ("out", out), ("scales", scales))
-    dt = _dtype(x, ("weight", weight))
-    _vector(weight, D)
-    st = _launch(dev, library().dit_rmsnorm_fp8, out.data_ptr(), scales.data_ptr(), x.data_ptr(),
-                 weight.data_ptr(), rows, D, group, eps, weight_offset, dt, _stream(dev, stream))
-    if st:
-        check(st, "dit_rmsnorm_fp8")
+    dev, dt = _same(x, ("x", x), weight, D)
+    _call(dev, library().dit_rmsnorm_fp8, "dit_rmsnorm_fp8", out.data_ptr(), scales.data_ptr(),
+          x.data_ptr(), weight.data_ptr(), rows, D, group, eps, weight_offset, dt,
+          _stream(dev, stream))
     return out, scales
 
 
@@ -180,16 +202,11 @@ def add_rmsnorm_fp8(hidden, update, weight, eps=1e-6, group=0, weight_offset=0.0
     if residual_out is None:
         residual_out = _empty(hidden.shape, hidden.dtype, hidden.device, stream)
     out, scales = _codes(hidden, D, group, out, scales, stream)
-    dev = _cuda(("hidden", hidden), ("update", update), ("weight", weight),
-                ("residual_out", residual_out), ("out", out), ("scales", scales))
-    dt = _dtype(hidden, ("update", update), ("weight", weight), ("residual_out", residual_out))
-    _vector(weight, D)
-    _same_shape(hidden, ("update", update), ("residual_out", residual_out))
-    st = _launch(dev, library().dit_add_rmsnorm_fp8, residual_out.data_ptr(), out.data_ptr(),
-                 scales.data_ptr(), hidden.data_ptr(), update.data_ptr(), weight.data_ptr(), rows,
-                 D, group, eps, weight_offset, dt, _stream(dev, stream))
-    if st:
-        check(st, "dit_add_rmsnorm_fp8")
+    dev, dt = _same(hidden, ("hidden", hidden, "update", update, "residual_out", residual_out),
+                    weight, D)
+    _call(dev, library().dit_add_rmsnorm_fp8, "dit_add_rmsnorm_fp8", residual_out.data_ptr(),
+          out.data_ptr(), scales.data_ptr(), hidden.data_ptr(), update.data_ptr(),
+          weight.data_ptr(), rows, D, group, eps, weight_offset, dt, _stream(dev, stream))
     return residual_out, out, scales
 
 
@@ -209,29 +226,38 @@ def rmsnorm_backward(grad_out, x, weight, eps=1e-6, weight_offset=0.0, grad_resi
         grad_weight = None
     elif grad_weight is None:
         grad_weight = _empty((D,), x.dtype, x.device, stream)
-    named = [("x", x), ("grad_out", grad_out), ("weight", weight), ("grad_x", grad_x)]
-    shaped = [("grad_out", grad_out), ("grad_x", grad_x)]
+    named = ("x", x, "grad_out", grad_out, "grad_x", grad_x)
     if grad_residual is not None:
-        named.append(("grad_residual", grad_residual))
-        shaped.append(named[-1])
-    if grad_weight is not None:
-        named.append(("grad_weight", grad_weight))
-        _vector(grad_weight, D)
-    dev = _cuda(*named)
-    dt = _dtype(x, *named[1:])
-    _vector(weight, D)
-    _same_shape(x, *shaped)
+        named += ("grad_residual", grad_residual)
+    dev, dt = _same(x, named, weight, D)
     lib = library()
-    ws, wp, wn = None, None, 0
+    ws, wp, wn, gw, gr = None, None, 0, None, None
     if grad_weight is not None:
+        if (grad_weight.dtype is not x.dtype or grad_weight.get_device() != dev
+                or grad_weight.shape != (D,) or not grad_weight.is_contiguous()):
+            raise ValueError(f"grad_weight must be a contiguous [{D}] {x.dtype} tensor on cuda:{dev}")
+        gw = grad_weight.data_ptr()
         ws, wp, wn = _workspace(workspace, lib.dit_rmsnorm_backward_workspace_bytes(rows, D), x, stream)
-    st = _launch(dev, lib.dit_rmsnorm_backward, grad_x.data_ptr(),
-                 None if grad_weight is None else grad_weight.data_ptr(), grad_out.data_ptr(),
-                 None if grad_residual is None else grad_residual.data_ptr(), x.data_ptr(),
-                 weight.data_ptr(), rows, D, eps, weight_offset, dt, wp, wn, _stream(dev, stream))
-    if st:
-        check(st, "dit_rmsnorm_backward")
+    if grad_residual is not None:
+        gr = grad_residual.data_ptr()
+    _call(dev, lib.dit_rmsnorm_backward, "dit_rmsnorm_backward", grad_x.data_ptr(), gw,
+          grad_out.data_ptr(), gr, x.data_ptr(), weight.data_ptr(), rows, D, eps, weight_offset, dt,
+          wp, wn, _stream(dev, stream))
     return grad_x, grad_weight
+
+
+def _with_ids(ids, t, named):
+    """Checks ids and the tensors of `named` (name, tensor, ...) against t, one
+    of them; returns (device index, dtype code)."""
+    dev = t.get_device()
+    ok = dev >= 0 and t.dtype in DTYPE_CODES and ids.get_device() == dev and ids.is_contiguous()
+    for o in named[1::2]:
+        ok = ok and o.dtype is t.dtype and o.get_device() == dev and o.is_contiguous()
+    if ok:
+        return dev, DTYPE_CODES[t.dtype]
+    pairs = list(zip(named[::2], named[1::2]))
+    dev = _cuda(*pairs, ("ids", ids))
+    return dev, _dtype(t, *pairs)
 
 
 def _id_type(ids):
@@ -253,12 +279,9 @@ def embedding(ids, table, scale=1.0, out=None, stream=None):
         out = _empty(shape, table.dtype, table.device, stream)
     elif out.shape != shape:
         raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
-    dev = _cuda(("table", table), ("ids", ids), ("out", out))
-    dt = _dtype(table, ("out", out))
-    st = _launch(dev, library().dit_embedding, out.data_ptr(), ids.data_ptr(), table.data_ptr(),
-                 ids.numel(), V, D, scale, dt, it, _stream(dev, stream))
-    if st:
-        check(st, "dit_embedding")
+    dev, dt = _with_ids(ids, table, ("table", table, "out", out))
+    _call(dev, library().dit_embedding, "dit_embedding", out.data_ptr(), ids.data_ptr(),
+          table.data_ptr(), ids.numel(), V, D, scale, dt, it, _stream(dev, stream))
     return out
 
 
@@ -271,7 +294,7 @@ def embedding_backward(grad_out, ids, num_rows, scale=1.0, out=None, workspace=N
     (allocated if None).  Returns out ([num_rows, D])."""
     it = _id_type(ids)
     tokens, D = _rows(grad_out, "grad_out")
-    if tuple(grad_out.shape[:-1]) != tuple(ids.shape):
+    if grad_out.shape[:-1] != ids.shape:
         raise ValueError(f"grad_out must be ids.shape + (D,), got {tuple(grad_out.shape)} for ids "
                          f"{tuple(ids.shape)}")
     V = int(num_rows)
@@ -281,15 +304,13 @@ def embedding_backward(grad_out, ids, num_rows, scale=1.0, out=None, workspace=N
         out = _empty((V, D), grad_out.dtype, grad_out.device, stream)
     elif out.shape != (V, D):
         raise ValueError(f"out must be [{V}, {D}], got {tuple(out.shape)}")
-    dev = _cuda(("grad_out", grad_out), ("ids", ids), ("out", out))
-    dt = _dtype(grad_out, ("out", out))
+    dev, dt = _with_ids(ids, grad_out, ("grad_out", grad_out, "out", out))
     lib = library()
     ws, wp, wn = _workspace(workspace, lib.dit_embedding_backward_workspace_bytes(tokens, D), grad_out,
                             stream)
-    st = _launch(dev, lib.dit_embedding_backward, out.data_ptr(), grad_out.data_ptr(), ids.data_ptr(),
-                 tokens, V, D, scale, dt, it, wp, wn, _stream(dev, stream))
-    if st:
-        check(st, "dit_embedding_backward")
+    _call(dev, lib.dit_embedding_backward, "dit_embedding_backward", out.data_ptr(),
+          grad_out.data_ptr(), ids.data_ptr(), tokens, V, D, scale, dt, it, wp, wn,
+          _stream(dev, stream))
     return out
 
 
@@ -308,6 +329,7 @@ class TensorList:
         if self.out is not None and len(self.out) != len(self.tensors):
             raise ValueError(f"{len(self.tensors)} tensors, but {len(self.out)} outputs")
         self.array = (Tensor * max(1, len(self.tensors)))()
+        self.address = ctypes.addressof(self.array)
         self.device = None
         for i, t in enumerate(self.tensors):
             o = None if self.out is None else self.out[i]
@@ -333,9 +355,10 @@ def _norm_call(lst, norm, workspace, stream):
     ref = lst.tensors[0]
     if norm is None:
         norm = _empty((), torch.float32, ref.device, stream)
-    elif norm.dtype is not torch.float32 or norm.numel() != 1:
-        raise TypeError("norm must be a one-element float32 CUDA tensor")
-    _cuda(("norm", norm), ("tensor 0", ref))
+    else:
+        _cuda(("norm", norm), ("tensor 0", ref))
+        if norm.dtype is not torch.float32 or norm.numel() != 1:
+            raise TypeError("norm must be a one-element float32 CUDA tensor")
     ws, wp, wn = _workspace(workspace, library().dit_grad_norm_workspace_bytes(len(lst)), ref, stream)
     return norm, ws, wp, wn
 
@@ -347,10 +370,8 @@ def grad_norm(tensors, norm=None, workspace=None, stream=None):
     lst = tensors if isinstance(tensors, TensorList) else TensorList(tensors)
     norm, ws, wp, wn = _norm_call(lst, norm, workspace, stream)
     dev = norm.get_device()
-    st = _launch(dev, library().dit_grad_norm, norm.data_ptr(), ctypes.addressof(lst.array),
-                 len(lst), wp, wn, _stream(dev, stream))
-    if st:
-        check(st, "dit_grad_norm")
+    _call(dev, library().dit_grad_norm, "dit_grad_norm", norm.data_ptr(), lst.address, len(lst), wp,
+          wn, _stream(dev, stream))
     return norm
 
 
@@ -371,8 +392,6 @@ def clip_grads(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=None, s
         lst = TensorList(grads, out)
     norm, ws, wp, wn = _norm_call(lst, norm, workspace, stream)
     dev = norm.get_device()
-    st = _launch(dev, library().dit_clip_grads, norm.data_ptr(), ctypes.addressof(lst.array),
-                 len(lst), max_norm, eps, wp, wn, _stream(dev, stream))
-    if st:
-        check(st, "dit_clip_grads")
+    _call(dev, library().dit_clip_grads, "dit_clip_grads", norm.data_ptr(), lst.address, len(lst),
+          max_norm, eps, wp, wn, _stream(dev, stream))
     return lst.out, norm

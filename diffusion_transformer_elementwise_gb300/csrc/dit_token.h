@@ -79,7 +79,8 @@ struct EmbedGradArgs {
 // sorted tokens per segment, and segments of a call
 constexpr int kEmbedSegment = 32;
 inline int64_t embed_segments(int64_t tokens) { return (tokens + kEmbedSegment - 1) / kEmbedSegment; }
-cudaError_t launch_embedding_grad(int dtype, bool wide, const EmbedGradArgs& a, cudaStream_t s);
+cudaError_t launch_embedding_grad(const DeviceInfo& dev, int dtype, bool wide,
+                                  const EmbedGradArgs& a, cudaStream_t s);
 
 // The global norm of many tensors, and their clipping (k_clip.cu).
 struct ClipTensor {

@@ -286,7 +286,7 @@ dit_status dit_embedding_backward(void* grad_table, const void* grad_out, const 
   a.pairs[1] = (uint2*)(w + round_up(tokens * 8));
   a.partial = (float*)(w + 2 * round_up(tokens * 8));
   const bool wide = wide_rows((uintptr_t)grad_table | (uintptr_t)grad_out, D * es);
-  return launch_status(dit::launch_embedding_grad(dtype, wide, a, (cudaStream_t)stream));
+  return launch_status(dit::launch_embedding_grad(dev, dtype, wide, a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

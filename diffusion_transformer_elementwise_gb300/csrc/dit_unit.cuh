@@ -19,6 +19,8 @@
 // zero and are not stored.
 #pragma once
 
+#include <atomic>
+
 #include "dit_device.cuh"
 #include "dit_internal.h"
 #include "dit_pipe.cuh"
@@ -30,6 +32,12 @@ namespace dit {
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// the larger magnitude of a, b and c (NaN if any is)
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ float warp_max(float v) {
@@ -86,6 +94,29 @@ struct Unit {
       if (c < 0 || c >= D) continue;
       const char* p = (const char*)row + (int64_t)c * ES;
       put(r, i, STREAM ? ld_stream<ES>(p) : ld_bcast<ES>(p));
+    }
+    return r;
+  }
+  // copy this lane's granule of row `row` of a tensor to its slot at shared
+  // address dst (cp.async; not NARROW)
+  __device__ __forceinline__ void copy(uint32_t dst, const void* tensor, int64_t row, int64_t rows,
+                                       int c0) const {
+    const int c = col(c0, 0);
+    if (c >= D) return;
+    const int64_t pitch = (int64_t)D * ES, at = row * pitch + (int64_t)c * ES;
+    // PHASED: the tensor's last granule may run past its end
+    if (LAYOUT == PHASED && row == rows - 1 && c + EPL > D)
+      cp_async16_part(dst, (const char*)tensor + at, (uint32_t)((D - c) * ES));
+    else
+      cp_async16(dst, (const char*)tensor + at);
+  }
+  // what copy() left in the slot
+  __device__ __forceinline__ Raw<16> copied(uint32_t src, int c0) const {
+    Raw<16> r = {};
+    const int c = col(c0, 0);
+    if (c < D) {
+      r = lds16(src);
+      if (LAYOUT == PHASED && !whole(c)) mask(r, c);
     }
     return r;
   }
@@ -212,6 +243,24 @@ constexpr int kTeamThreads = 32 * kTeamWarps;
 struct TeamShape {
   int warps, teams;
 };
+// Lets kernel `fn` take all the shared memory its static arrays leave, once per
+// (kernel, device).  `opted`: the kernel's flags.
+inline cudaError_t allow_shared(const void* fn, const DeviceInfo& dev, std::atomic<int>* opted) {
+  const bool cached = dev.device >= 0 && dev.device < kOptinDevices;
+  if (cached && opted[dev.device].load(std::memory_order_acquire)) return cudaSuccess;
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, fn);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             dev.smem_optin - (int)at.sharedSizeBytes);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();  // do not leave it for the next call to report
+    return e;
+  }
+  if (cached) opted[dev.device].store(1, std::memory_order_release);
+  return cudaSuccess;
+}
+
 // Units of a row of D columns (PHASED: at most, over the rows' offsets).
 template <class T, int LAYOUT>
 int64_t row_units(int64_t D) {

@@ -370,18 +370,14 @@ cudaError_t launch_sums(SumArgs a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_sort(SortArgs a, cudaStream_t s) {
+cudaError_t launch_sort(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
   a.ctas = a.tokens > 4096 ? kSortCluster : 1;
   const int64_t warps = (int64_t)a.ctas * kSortWarps;
   a.per_warp = ((a.tokens + warps - 1) / warps + 31) / 32 * 32;
   const size_t smem = (size_t)kSortWarps * (1 << a.bits) * 4;
-  // (set on every call: a host-side flag of the device's function)
-  const cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSortWarps * (4 << kSortBits));
-  if (e != cudaSuccess) {
-    (void)cudaGetLastError();
-    return e;
-  }
+  static std::atomic<int> opted[kOptinDevices];
+  const cudaError_t e = allow_shared((const void*)sort_kernel, dev, opted);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.ctas);
   cfg.blockDim = dim3(kSortWarps * 32);
@@ -414,8 +410,8 @@ cudaError_t launch_embedding(int dtype, bool wide, const EmbedArgs& a, cudaStrea
   });
 }
 
-cudaError_t launch_embedding_grad(int dtype, bool wide, const EmbedGradArgs& a,
-                                  cudaStream_t s) {
+cudaError_t launch_embedding_grad(const DeviceInfo& dev, int dtype, bool wide,
+                                  const EmbedGradArgs& a, cudaStream_t s) {
   SortArgs q = {};
   q.ids = a.ids;
   q.ids64 = a.ids64;
@@ -428,7 +424,7 @@ cudaError_t launch_embedding_grad(int dtype, bool wide, const EmbedGradArgs& a,
   q.passes = (bits + kSortBits - 1) / kSortBits;
   q.bits = (bits + q.passes - 1) / q.passes;
   if (a.tokens > 0) {
-    const cudaError_t e = launch_sort(q, s);
+    const cudaError_t e = launch_sort(dev, q, s);
     if (e != cudaSuccess) return e;
   }
   SumArgs m = {};

@@ -9,9 +9,11 @@
 // with the maximum over the row or over each 128 columns of it.
 //
 // The codes need no r: with t = fl(s fl(offset + w)), y / max|y| = t / max|t|,
-// so code = e4m3(fl(t fl(448 / max|t|))) and scale = fl(fl(max|t| r) / 448).
-// The maximum is taken in the same reduction as the sum of squares, and a
-// code carries fewer roundings than y / scale would.  Rows whose sum of
+// so code = e4m3(fl(t m')) with m' = 448 / max|t| (a hardware reciprocal, one
+// Newton-Raphson step and a product: within 1.5 u) and scale =
+// fl(fl(max|t| r) fl(1 / 448)).  The maximum is taken in the same reduction
+// as the sum of squares, and a code carries fewer roundings than y / scale
+// would.  Rows whose sum of
 // squares or maximum leaves [2^-100, 2^100] (overflow, infinities, NaN, all
 // zero) take y itself: the maximum again, of y, and code = e4m3(y 448 /
 // max|y|).  An all-zero row or group has scale 0 and codes 0; a NaN or an
@@ -32,22 +34,28 @@ __device__ __forceinline__ bool usable(float m) { return m >= 0x1p-100f && m <= 
 
 // The factor from values to codes, and the scale, of one row or group.
 struct Quant {
-  float pre, mul, scale;
+  float mul, scale;
 };
+// 448 / m for a normal m in [2^-100, 2^100]
+__device__ __forceinline__ float codes_per(float m) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(m));
+  y = __fmaf_rn(y, __fmaf_rn(-m, y, 1.0f), y);
+  return __fmul_rn(kE4M3Max, y);
+}
 // from the maximum of |t| (usable, or zero with a usable sum)
 __device__ __forceinline__ Quant quant_of_t(float m, float r) {
   Quant q;
-  q.pre = 1.0f;
-  q.mul = m == 0.0f ? 0.0f : __fdiv_rn(kE4M3Max, m);
-  q.scale = __fdiv_rn(__fmul_rn(m, r), kE4M3Max);
+  q.mul = m == 0.0f ? 0.0f : codes_per(m);
+  q.scale = __fmul_rn(__fmul_rn(m, r), 1.0f / kE4M3Max);
   return q;
 }
-// from the maximum of |y|, whatever it is; a small one is scaled up first, so
-// that 448 / m does not overflow
+// from the maximum of |y|, whatever it is, for values that small_factor
+// scaled up where they are so small that 448 / m would overflow
+__device__ __forceinline__ float small_factor(float m) { return m < 0x1p-60f ? 0x1p64f : 1.0f; }
 __device__ __forceinline__ Quant quant_of_y(float m) {
   Quant q;
-  q.pre = m < 0x1p-60f ? 0x1p64f : 1.0f;
-  q.mul = m == 0.0f ? 0.0f : __fdiv_rn(kE4M3Max, __fmul_rn(m, q.pre));
+  q.mul = m == 0.0f ? 0.0f : __fdiv_rn(kE4M3Max, __fmul_rn(m, small_factor(m)));
   q.scale = __fdiv_rn(m, kE4M3Max);
   return q;
 }
@@ -97,24 +105,22 @@ struct NormRow {
       if (d < 0 || d >= unit.D) y[i].y = 0.0f;
     }
   }
+  __device__ __forceinline__ static void scale_by(F2 (&v)[P], float f) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = f2_mul(v[i], f2(f, f));
+  }
   __device__ __forceinline__ static float max_of(const F2 (&v)[P]) {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < P; ++i) m = max_nan(m, max_nan(fabsf(f2_lo(v[i])), fabsf(f2_hi(v[i]))));
+    for (int i = 0; i < P; ++i) m = max_abs3(m, f2_lo(v[i]), f2_hi(v[i]));
     return m;
   }
   __device__ __forceinline__ static Raw<U::EPL> codes(const F2 (&v)[P], const Quant (&q)[NG]) {
     Raw<U::EPL> r;
 #pragma unroll
     for (int i = 0; i < P / 2; ++i) {
-      const Quant& k = q[NG == 2 ? i : 0];
-      uint32_t w = 0;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const F2 p = f2_mul(v[2 * i + j], f2(k.pre, k.pre));
-        w |= e4m3x2(f2_mul(p, f2(k.mul, k.mul))) << (16 * j);
-      }
-      r.w[i] = w;
+      const float m = q[NG == 2 ? i : 0].mul;
+      r.w[i] = e4m3x2(f2_mul(v[2 * i], f2(m, m))) | e4m3x2(f2_mul(v[2 * i + 1], f2(m, m))) << 16;
     }
     return r;
   }
@@ -125,7 +131,7 @@ struct NormRow {
       m[g] = 0.0f;
 #pragma unroll
       for (int i = g * P / NG; i < (g + 1) * P / NG; ++i)
-        m[g] = max_nan(m[g], max_nan(fabsf(f2_lo(v[i])), fabsf(f2_hi(v[i]))));
+        m[g] = max_abs3(m[g], f2_lo(v[i]), f2_hi(v[i]));
 #pragma unroll
       for (int o = LANES / 2; o > 0; o >>= 1)
         m[g] = max_nan(m[g], __shfl_xor_sync(0xFFFFFFFFu, m[g], o));
@@ -158,7 +164,10 @@ struct NormRow {
 #pragma unroll
         for (int g = 0; g < NG; ++g) q[g] = quant_of_y(m[g]);
 #pragma unroll
-        for (int i = 0; i < P; ++i) v[i] = y[i];
+        for (int i = 0; i < P; ++i) {
+          const float f = small_factor(m[NG == 2 ? i / 2 : 0]);
+          v[i] = f2_mul(y[i], f2(f, f));
+        }
       }
     }
     unit.store8((char*)a.out + row * a.D, c0, codes(v, q));
@@ -178,29 +187,28 @@ struct NormRow {
   // lanes of a group; else zero).
   __device__ __forceinline__ static void split_max(const F2 (&v)[P], const U& unit, float& own,
                                                    float& head) {
-    const int cut = unit.lane % LANES == 0 ? unit.off : 0;
-    own = head = 0.0f;
+    float a = 0.0f, b = 0.0f;  // elements before `off` (one value for the warp), and from it
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const float lo = fabsf(f2_lo(v[i])), hi = fabsf(f2_hi(v[i]));
-      if (2 * i < cut) head = max_nan(head, lo); else own = max_nan(own, lo);
-      if (2 * i + 1 < cut) head = max_nan(head, hi); else own = max_nan(own, hi);
+      if (2 * i < unit.off) a = max_abs3(a, a, f2_lo(v[i])); else b = max_abs3(b, b, f2_lo(v[i]));
+      if (2 * i + 1 < unit.off) a = max_abs3(a, a, f2_hi(v[i])); else b = max_abs3(b, b, f2_hi(v[i]));
     }
+    const bool first = unit.lane % LANES == 0;
+    head = first ? a : 0.0f;
+    own = first ? b : max_nan(a, b);
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1)
       own = max_nan(own, __shfl_xor_sync(0xFFFFFFFFu, own, o));
   }
   // codes with the factor `before` for the first `cut` elements
-  __device__ __forceinline__ static Raw<U::EPL> split_codes(const F2 (&v)[P], int cut, Quant before,
-                                                            Quant q) {
+  __device__ __forceinline__ static Raw<U::EPL> split_codes(const F2 (&v)[P], int cut, float before,
+                                                            float mul) {
     F2 s[P];
     Quant one[NG];
-    one[0].pre = one[0].mul = 1.0f;
+    one[0].mul = 1.0f;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const Quant a = 2 * i < cut ? before : q, b = 2 * i + 1 < cut ? before : q;
-      s[i] = f2_mul(f2_mul(v[i], f2(a.pre, b.pre)), f2(a.mul, b.mul));
-    }
+    for (int i = 0; i < P; ++i)
+      s[i] = f2_mul(v[i], f2(2 * i < cut ? before : mul, 2 * i + 1 < cut ? before : mul));
     return codes(s, one);
   }
 };
@@ -214,43 +222,106 @@ __device__ __forceinline__ float inverse_rms(float S, const NormArgs& a, Again a
   return fast_inverse_rms_scaled(again(sc), sc, a.d_f, a.inv_d, a.eps);
 }
 
+// A row's codes with one factor q; values(x, weights, v) gives what it applies to.
+template <class R, int NU, class U, class Values>
+__device__ __forceinline__ void emit_row(const NormArgs& a, const U& unit, int64_t row, int m, int W,
+                                         const Raw<16> (&x)[NU], const Raw<16> (&w)[NU],
+                                         Values values, Quant q) {
+  Quant all[R::NG];
+#pragma unroll
+  for (int g = 0; g < R::NG; ++g) all[g] = q;
+#pragma unroll
+  for (int j = 0; j < NU; ++j) {
+    F2 wf[U::P], v[U::P];
+    R::weight(w[j], a.offset, wf);
+    values(x[j], wf, v);
+    unit.store8((char*)a.out + row * a.D, (m + j * W) * U::COLS, R::codes(v, all));
+  }
+  if (m == 0 && unit.lane == 0) a.scales[row] = q.scale;
+}
+
+// Threads of a CTA and registers of a thread: up to two units a warp, two
+// CTAs of 16 warps per SM (64 registers); four units, one (128).
+constexpr int kNormStages = 2;
+
 // A CTA's teams take rows CTA * teams + team, and on by the grid's rows, a
-// multiple of the rows' period for PHASED rows.
-template <class T, int LAYOUT, int NU, bool ADD, int Q8>
+// multiple of the rows' period for PHASED rows.  STAGED: one wave of CTAs,
+// each lane copying the granules it will read into its own slots of shared
+// memory (cp.async), kNormStages rows ahead, so the copies need no barrier and are in
+// flight while the team reduces and writes; otherwise a team's rows are few
+// (one, for most sizes) and other CTAs' loads fill the memory's pipe.
+template <class T, int LAYOUT, int NU, bool ADD, int Q8, bool STAGED>
 __global__ void __launch_bounds__(kTeamThreads, NU <= 2 ? 2 : 1) norm_team_kernel(NormArgs a) {
   using R = NormRow<T, LAYOUT>;
   using U = typename R::U;
   constexpr int P = U::P;
+  constexpr int NS = ADD ? 2 : 1;               // streams
+  constexpr uint32_t kSlot = 32 * 16;           // a unit of one stream
+  constexpr uint32_t kStage = NS * NU * kSlot;  // a warp's part of a row
+  static_assert(!STAGED || LAYOUT != NARROW, "cp.async moves granules");
   __shared__ float2 slots[2 * kTeamWarps];
   // PHASED groups: (own, head) of each group of the CTA's rows, by row parity
   constexpr bool kSplit = LAYOUT == PHASED && Q8 == 2;
   constexpr int kBlocks = NU * R::BLOCKS;  // groups of a warp
   __shared__ float2 groups[kSplit ? 2 : 1][kSplit ? kTeamWarps * kBlocks : 1];
+  extern __shared__ float4 shared[];  // STAGED: [warps][stages][streams][NU][32]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = a.warps, teams = (blockDim.x >> 5) / W;
   const int team = warp / W, m = warp - team * W;
   Team t{slots + team * 2 * W, W, m, 1 + team, 0};
   const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
+  const int64_t step = (int64_t)gridDim.x * teams;
   int64_t row = (int64_t)blockIdx.x * teams + team;
   if (row >= a.rows) return;  // the whole team
 
   U unit(a.D, lane);
   unit.at_row(row, a.rows);
-  Raw<16> w[NU];
+  const uint32_t stage0 =
+      STAGED ? smem_addr(shared) + warp * (kNormStages * kStage) + lane * 16 : 0u;
+  auto prefetch = [&](int64_t r, int s) {  // an empty group past the end
+    if (r < a.rows) {
 #pragma unroll
-  for (int j = 0; j < NU; ++j) w[j] = unit.load_weight(a.w, (m + j * W) * U::COLS);
-  for (; row < a.rows; row += (int64_t)gridDim.x * teams) {
+      for (int j = 0; j < NU; ++j) {
+        const int c0 = (m + j * W) * U::COLS;
+        const uint32_t dst = stage0 + s * kStage + j * kSlot;
+        unit.copy(dst, a.x, r, a.rows, c0);
+        if constexpr (ADD) unit.copy(dst + NU * kSlot, a.u, r, a.rows, c0);
+      }
+    }
+    cp_async_commit();
+  };
+  if constexpr (STAGED) {
+#pragma unroll
+    for (int s = 0; s < kNormStages; ++s) prefetch(row + s * step, s);
+  }
+  Raw<16> w[NU];
+  if constexpr (STAGED) {
+#pragma unroll
+    for (int j = 0; j < NU; ++j) w[j] = unit.load_weight(a.w, (m + j * W) * U::COLS);
+  }
+  int s = 0;
+  for (; row < a.rows; row += step) {
     unit.at_row(row, a.rows);
-    Raw<16> x[NU];
-    F2 acc[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
-    float big = 0.0f;
-    Raw<16> u[NU];
+    Raw<16> x[NU], u[NU];
+    if constexpr (STAGED) cp_async_wait<kNormStages - 1>();  // this lane's copies of the row
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
       const int c0 = (m + j * W) * U::COLS;
-      x[j] = unit.load((const char*)a.x + row * pitch, c0);
-      if constexpr (ADD) u[j] = unit.load((const char*)a.u + row * pitch, c0);
+      if constexpr (STAGED) {
+        const uint32_t at = stage0 + s * kStage + j * kSlot;
+        x[j] = unit.copied(at, c0);
+        if constexpr (ADD) u[j] = unit.copied(at + NU * kSlot, c0);
+      } else {
+        x[j] = unit.load((const char*)a.x + row * pitch, c0);
+        if constexpr (ADD) u[j] = unit.load((const char*)a.u + row * pitch, c0);
+      }
     }
+    if constexpr (!STAGED) {
+#pragma unroll
+      for (int j = 0; j < NU; ++j) w[j] = unit.load_weight(a.w, (m + j * W) * U::COLS);
+    }
+    F2 acc[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+    float big = 0.0f;
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
       const int c0 = (m + j * W) * U::COLS;
@@ -270,7 +341,8 @@ __global__ void __launch_bounds__(kTeamThreads, NU <= 2 ? 2 : 1) norm_team_kerne
           float own, head;
           R::split_max(v, unit, own, head);
           if (lane % R::LANES == 0)
-            groups[t.par][(team * W * NU + m + j * W) * R::BLOCKS + lane / R::LANES] = make_float2(own, head);
+            groups[t.par][team * W * kBlocks + (m + j * W) * R::BLOCKS + lane / R::LANES] =
+                make_float2(own, head);
           const bool bad = (own != 0.0f && !usable(own)) || (head != 0.0f && !usable(head));
           big = bad ? 1.0f : big;
         } else {
@@ -278,9 +350,14 @@ __global__ void __launch_bounds__(kTeamThreads, NU <= 2 ? 2 : 1) norm_team_kerne
         }
       }
     }
+    if constexpr (STAGED) {  // the stage has been read
+      prefetch(row + kNormStages * step, s);
+      s = s + 1 == kNormStages ? 0 : s + 1;
+    }
     acc[0] = f2_add(acc[0], acc[1]);
     float2 red = make_float2(warp_sum(__fadd_rn(acc[0].x, acc[0].y)), 0.0f);
-    if constexpr (Q8 == 1 || kSplit) red.y = warp_max(big);
+    if constexpr (Q8 == 1) red.y = warp_max(big);
+    if constexpr (kSplit) red.y = __any_sync(0xFFFFFFFFu, big != 0.0f) ? 1.0f : 0.0f;
     [[maybe_unused]] int par = t.par;
     red = t.combine<Q8 == 1 || kSplit>(red);
     const float r = inverse_rms(red.x, a, [&](float sc) {
@@ -310,74 +387,91 @@ __global__ void __launch_bounds__(kTeamThreads, NU <= 2 ? 2 : 1) norm_team_kerne
 #pragma unroll
       for (int j = 0; j < NU; ++j)
         R::emit_groups(a, unit, row, (m + j * W) * U::COLS, x[j], w[j], red.x, r);
-    } else {
-      // one scale per row, or groups that cross granules
-      const bool slow = kSplit ? !usable(red.x) || red.y != 0.0f
-                               : !usable(red.x) || (red.y != 0.0f && !usable(red.y));
-      Quant q[R::NG] = {};
-      if (slow) {  // rare, uniform over the row's threads: the maxima of y
+    } else if constexpr (!kSplit) {
+      // one scale per row
+      if (usable(red.x) && (red.y == 0.0f || usable(red.y))) {
+        const Quant q = quant_of_t(red.y, r);
+        emit_row<R, NU>(
+            a, unit, row, m, W, x, w,
+            [&](const Raw<16>& x, const F2(&wf)[P], F2(&v)[P]) { R::weighted(x, wf, v); }, q);
+      } else {  // rare, uniform over the row's threads: the maximum of y
         float my = 0.0f;
-        if constexpr (kSplit) {
-          par = t.par;
-          if (W == 1) __syncwarp();  // the pieces below replace those read above
-        }
 #pragma unroll
         for (int j = 0; j < NU; ++j) {
           F2 wf[P], y[P];
           R::weight(w[j], a.offset, wf);
           R::normed(x[j], wf, r, y);
           R::mask(y, unit, (m + j * W) * U::COLS);
-          if constexpr (kSplit) {
-            float own, head;
-            R::split_max(y, unit, own, head);
-            if (lane % R::LANES == 0)
-              groups[par][(team * W * NU + m + j * W) * R::BLOCKS + lane / R::LANES] = make_float2(own, head);
-          } else {
-            my = max_nan(my, R::max_of(y));
-          }
+          my = max_nan(my, R::max_of(y));
         }
-        const float2 again = t.combine<true>(make_float2(0.0f, warp_max(my)));
-        if constexpr (!kSplit) q[0] = quant_of_y(again.y);
-      } else if constexpr (!kSplit) {
-        q[0] = quant_of_t(red.y, r);
+        my = t.combine<true>(make_float2(0.0f, warp_max(my))).y;
+        const float f = small_factor(my);
+        emit_row<R, NU>(
+            a, unit, row, m, W, x, w,
+            [&](const Raw<16>& x, const F2(&wf)[P], F2(&v)[P]) {
+              R::normed(x, wf, r, v);
+              R::scale_by(v, f);
+            },
+            quant_of_y(my));
       }
-      if constexpr (kSplit) {
-        if (W == 1) __syncwarp();
-      }
+    } else {
+      // groups that cross granules, units and warps
+      const bool slow = !usable(red.x) || red.y != 0.0f;
+      auto values = [&](int j, F2(&v)[P]) {
+        F2 wf[P];
+        R::weight(w[j], a.offset, wf);
+        if (slow) {
+          R::normed(x[j], wf, r, v);
+          R::mask(v, unit, (m + j * W) * U::COLS);
+        } else {
+          R::weighted(x[j], wf, v);
+        }
+      };
+      if (slow) {  // rare, uniform over the row's threads: the maxima of y
+        par = t.par;
 #pragma unroll
-      for (int g = 1; g < R::NG; ++g) q[g] = q[0];
+        for (int j = 0; j < NU; ++j) {
+          F2 y[P];
+          values(j, y);
+          float own, head;
+          R::split_max(y, unit, own, head);
+          if (lane % R::LANES == 0)
+            groups[par][team * W * kBlocks + (m + j * W) * R::BLOCKS + lane / R::LANES] =
+                make_float2(own, head);
+        }
+        t.combine<true>(make_float2(0.0f, 0.0f));
+      }
+      if (W == 1) __syncwarp();
+      const float2* g = groups[par] + team * W * kBlocks;
+      const int n = W * kBlocks;
+      // group k's maximum: its own part, and the next one's head
+      auto maximum = [&](int k) { return k + 1 < n ? max_nan(g[k].x, g[k + 1].y) : g[k].x; };
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
-        const int c0 = (m + j * W) * U::COLS;
-        F2 wf[P], v[P];
-        R::weight(w[j], a.offset, wf);
-        if (slow)
-          R::normed(x[j], wf, r, v);
-        else
-          R::weighted(x[j], wf, v);
-        if constexpr (kSplit) {
-          // group k's maximum: its own part, and the next one's head
-          const float2* g = groups[par] + team * W * kBlocks;
-          const int k = (m + j * W) * R::BLOCKS + lane / R::LANES, n = W * kBlocks;
-          auto quant = [&](int k) {
-            const float big = k + 1 < n ? max_nan(g[k].x, g[k + 1].y) : g[k].x;
-            return slow ? quant_of_y(big) : quant_of_t(big, r);
-          };
-          const int cut = lane % R::LANES == 0 ? unit.off : 0;
-          const Quant mine = quant(k);
-          const Quant before = cut && k > 0 ? quant(k - 1) : mine;
-          unit.store8((char*)a.out + row * a.D, c0, R::split_codes(v, cut, before, mine));
-          if (lane % R::LANES == 0 && k < a.groups) a.scales[row * a.groups + k] = mine.scale;
+        F2 v[P];
+        values(j, v);
+        const int k = (m + j * W) * R::BLOCKS + lane / R::LANES;
+        const int cut = lane % R::LANES == 0 ? unit.off : 0;
+        const float big = maximum(k), prev = cut && k > 0 ? maximum(k - 1) : big;
+        Quant mine, before;
+        if (slow) {
+          mine = quant_of_y(big);
+          before = quant_of_y(prev);
+          const float f = small_factor(big), b = small_factor(prev);
+#pragma unroll
+          for (int i = 0; i < P; ++i)
+            v[i] = f2_mul(v[i], f2(2 * i < cut ? b : f, 2 * i + 1 < cut ? b : f));
         } else {
-          unit.store8((char*)a.out + row * a.D, c0, R::codes(v, q));
+          mine = quant_of_t(big, r);
+          before = quant_of_t(prev, r);
         }
+        unit.store8((char*)a.out + row * a.D, (m + j * W) * U::COLS,
+                    R::split_codes(v, cut, before.mul, mine.mul));
+        if (lane % R::LANES == 0 && k < a.groups) a.scales[row * a.groups + k] = mine.scale;
       }
-      if (!kSplit && m == 0 && lane == 0) a.scales[row] = q[0].scale;
-      if constexpr (kSplit) {
-        if (W == 1) {
-          t.par ^= 1;  // (a team of one warp has no barrier to alternate them)
-          __syncwarp();
-        }
+      if (W == 1) {
+        t.par ^= 1;  // (a team of one warp has no barrier to alternate them)
+        __syncwarp();
       }
     }
   }
@@ -453,7 +547,8 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
     });
 
     bool slow = false;
-    Quant q[R::NG];
+    float small = 1.0f;
+    Quant q[R::NG] = {};
     if constexpr (Q8 == 1) {
       slow = !usable(S) || (big != 0.0f && !usable(big));
       if (slow) {
@@ -465,7 +560,9 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
           R::mask(y, unit, c0);
           my = max_nan(my, R::max_of(y));
         }
-        q[0] = quant_of_y(t.combine<true>(make_float2(0.0f, warp_max(my))).y);
+        my = t.combine<true>(make_float2(0.0f, warp_max(my))).y;
+        q[0] = quant_of_y(my);
+        small = small_factor(my);
       } else {
         q[0] = quant_of_t(big, r);
       }
@@ -485,6 +582,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
           R::normed(x, wf, r, v);
         else
           R::weighted(x, wf, v);
+        if (slow) R::scale_by(v, small);
         if constexpr (Q8 == 0)
           unit.store((char*)a.out + row * pitch, c0, Granule<T>::narrow(v));
         else
@@ -494,30 +592,39 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
   }
 }
 
+template <class T, int LAYOUT, int NU, bool ADD, int Q8, bool STAGED>
+cudaError_t launch_team(const DeviceInfo& dev, NormArgs a, int64_t units, cudaStream_t s) {
+  const auto kern = norm_team_kernel<T, LAYOUT, NU, ADD, Q8, STAGED>;
+  TeamShape t = team_shape(units, NU);
+  if (STAGED) t.teams = kTeamWarps / t.warps;
+  a.warps = t.warps;
+  const int block = t.warps * t.teams * 32;
+  int64_t grid = (a.rows + t.teams - 1) / t.teams;
+  size_t smem = 0;
+  if (STAGED) {
+    smem = (size_t)block * 16 * NU * (ADD ? 2 : 1) * kNormStages;
+    static std::atomic<int> opted[kOptinDevices];
+    const cudaError_t e = allow_shared((const void*)kern, dev, opted);
+    if (e != cudaSuccess) return e;
+    const int64_t wave = (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, block, smem);
+    if (grid > wave) grid = wave;
+    // a team's rows are a multiple of the period apart
+    if (LAYOUT == PHASED) grid = (grid + 7) / 8 * 8;
+  }
+  if (grid > (int64_t(1) << 30)) grid = int64_t(1) << 30;
+  kern<<<(unsigned)grid, block, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <class T, int LAYOUT, bool ADD, int Q8>
 cudaError_t launch(const DeviceInfo& dev, NormArgs a, cudaStream_t s) {
   const int64_t units = row_units<T, LAYOUT>(a.D);
-  auto team = [&](auto nu) -> cudaError_t {
-    constexpr int NU = decltype(nu)::value;
-    const auto kern = norm_team_kernel<T, LAYOUT, NU, ADD, Q8>;
-    const TeamShape t = team_shape(units, NU);
-    a.warps = t.warps;
-    const int block = t.warps * t.teams * 32;
-    int64_t grid = (a.rows + t.teams - 1) / t.teams;
-    if (LAYOUT == PHASED) {
-      // one wave, whose rows are a multiple of the period: a team's rows
-      // have one offset, at which it loads the weights once
-      const int64_t wave = (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, block);
-      if (grid > wave) grid = wave < 8 ? 8 : wave;
-      grid = (grid + 7) / 8 * 8;
-    }
-    if (grid > (int64_t(1) << 30)) grid = int64_t(1) << 30;
-    kern<<<(unsigned)grid, block, 0, s>>>(a);
-    return cudaGetLastError();
-  };
-  if (units <= 8) return team(std::integral_constant<int, 1>{});
-  if (units <= 2 * kTeamWarps) return team(std::integral_constant<int, 2>{});
-  if (units <= 4 * kTeamWarps) return team(std::integral_constant<int, 4>{});
+  // rows of one or two units a warp, WIDE: a CTA per row, or a few; others staged
+  if (units <= 8) return launch_team<T, LAYOUT, 1, ADD, Q8, LAYOUT == PHASED>(dev, a, units, s);
+  if (units <= 2 * kTeamWarps)
+    return launch_team<T, LAYOUT, 2, ADD, Q8, LAYOUT == PHASED>(dev, a, units, s);
+  if (units <= 4 * kTeamWarps)
+    return launch_team<T, LAYOUT, 4, ADD, Q8, LAYOUT != NARROW>(dev, a, units, s);
   if constexpr (LAYOUT == PHASED) {
     return launch<T, NARROW, ADD, Q8>(dev, a, s);
   } else {

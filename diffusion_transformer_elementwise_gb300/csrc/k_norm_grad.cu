@@ -19,7 +19,6 @@
 // shared memory (cp.async), kStages rows ahead, so the copies need no barrier
 // and a warp's loads are in flight while it reduces and writes.
 #include <algorithm>
-#include <atomic>
 
 #include "dit_stat.cuh"
 #include "dit_token.h"
@@ -129,7 +128,6 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
   Team t{slots + team * 2 * W, W, m, 1 + team, 0};
   const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
   const int64_t step = (int64_t)gridDim.x * teams;
-  const char* const src[3] = {(const char*)a.x, (const char*)a.g, (const char*)a.gres};
   const uint32_t stage0 = smem_addr(shared) + warp * (kStages * kStage) + lane * 16;
 
   int64_t row = (int64_t)blockIdx.x * teams + team;
@@ -139,21 +137,13 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
   auto prefetch = [&](int64_t r, int s) {
     if constexpr (kStaged) {
       if (r < a.rows) {
-        const int64_t end = a.rows * pitch;
 #pragma unroll
         for (int j = 0; j < NU; ++j) {
-          const int c = unit.col((m + j * W) * U::COLS, 0);
-          if (c >= a.D) continue;
-          const int64_t at = r * pitch + (int64_t)c * U::ES;
+          const int c0 = (m + j * W) * U::COLS;
           const uint32_t dst = stage0 + s * kStage + j * kSlot;
-#pragma unroll
-          for (int k = 0; k < NS; ++k) {
-            // PHASED: the tensor's last granule may run past its end
-            if (LAYOUT == PHASED && end - at < 16)
-              cp_async16_part(dst + k * NU * kSlot, src[k] + at, (uint32_t)(end - at));
-            else
-              cp_async16(dst + k * NU * kSlot, src[k] + at);
-          }
+          unit.copy(dst, a.x, r, a.rows, c0);
+          unit.copy(dst + NU * kSlot, a.g, r, a.rows, c0);
+          if constexpr (SKIP) unit.copy(dst + 2 * NU * kSlot, a.gres, r, a.rows, c0);
         }
       }
       cp_async_commit();
@@ -179,18 +169,10 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
     for (int j = 0; j < NU; ++j) {
       const int c0 = (m + j * W) * U::COLS;
       if constexpr (kStaged) {
-        const int c = unit.col(c0, 0);
         const uint32_t at = stage0 + s * kStage + j * kSlot;
-        x[j] = g[j] = k[j] = Raw<16>{};
-        if (c < a.D) {
-          x[j] = lds16(at);
-          g[j] = lds16(at + NU * kSlot);
-          if constexpr (SKIP) k[j] = lds16(at + 2 * NU * kSlot);
-          if (LAYOUT == PHASED && !unit.whole(c)) {
-            unit.mask(x[j], c);
-            unit.mask(g[j], c);
-          }
-        }
+        x[j] = unit.copied(at, c0);
+        g[j] = unit.copied(at + NU * kSlot, c0);
+        if constexpr (SKIP) k[j] = unit.copied(at + 2 * NU * kSlot, c0);
       } else {
         x[j] = unit.load((const char*)a.x + row * pitch, c0);
         g[j] = unit.load((const char*)a.g + row * pitch, c0);
@@ -334,7 +316,7 @@ cudaError_t launch_rows(const DeviceInfo& dev, NormGradArgs a, int64_t* ctas, cu
     const size_t stages = LAYOUT == NARROW ? 0 : (size_t)block * kStages * (SKIP ? 3 : 2) * NU * 16;
     const size_t smem = std::max(stages, teams > 1 ? (size_t)teams * a.D * 4 : 0);
     static std::atomic<int> opted[kOptinDevices];
-    cudaError_t e = allow_dynamic_smem((const void*)kern, dev, smem, opted);
+    cudaError_t e = allow_shared((const void*)kern, dev, opted);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)grid, block, smem, s>>>(a);
     *ctas = grid;
