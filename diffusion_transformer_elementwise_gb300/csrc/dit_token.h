@@ -19,7 +19,6 @@ struct NormArgs {
   const void* w;    // weight [D]
   int64_t rows;
   int D;
-  int warps;        // warps per row (set by the launcher)
   float eps, offset;
   float d_f, inv_d;
   int groups;       // E4M3: scales per row
@@ -41,7 +40,6 @@ struct NormGradArgs {
   const void* w;
   int64_t rows;
   int D;
-  int warps;
   float eps, offset;
   float d_f, inv_d;
 };

@@ -201,35 +201,44 @@ struct Unit {
 // the warps of one row
 // ---------------------------------------------------------------------------
 
-// A team of `warps` warps holds a row; a CTA holds blockDim.x / 32 / warps
-// teams.  sum2 and max1 combine a value of every warp over the team: through
-// shared memory and one barrier of the team's threads (a named barrier; none
-// for a team of one warp).  The slots alternate, so a slot is rewritten only
-// behind the next call's barrier, which the team's other warps reach after
-// reading it.
+// A team of `warps` warps (at most 16) holds a row; a CTA is blockDim.y teams
+// of blockDim.x threads.  combine adds (MAX: .y takes the larger of) a value of every warp
+// over the team: through shared memory, one barrier of the team's threads (a
+// named barrier; none for a team of one warp) and a butterfly.  The slots
+// alternate, so a slot is rewritten only behind the next call's barrier,
+// which the team's other warps reach after reading it.
 struct Team {
   float2* slots;  // this team's [2][warps]
-  int warps, m, id;
+  int warps, m, lane, id;
   int par;
-  __device__ __forceinline__ void barrier() const {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(warps * 32) : "memory");
-  }
-  // both members of v over the team, in the warps' order: sums (MAX: .y the
-  // maximum)
+  // slots: [2][the CTA's warps]
+  __device__ __forceinline__ explicit Team(float2* slots)
+      : slots(slots + threadIdx.y * 2 * (blockDim.x >> 5)),
+        warps(blockDim.x >> 5),
+        m(threadIdx.x >> 5),
+        lane(threadIdx.x & 31),
+        id(1 + threadIdx.y),
+        par(0) {}
   template <bool MAX>
   __device__ __forceinline__ float2 combine(float2 v) {
     if (warps == 1) return v;
     float2* s = slots + par * warps;
     par ^= 1;
-    if ((threadIdx.x & 31) == 0) s[m] = v;
-    barrier();
-    float2 t = s[0];
-    for (int w = 1; w < warps; ++w) {
-      const float2 o = s[w];
-      t.x = __fadd_rn(t.x, o.x);
-      t.y = MAX ? max_nan(t.y, o.y) : __fadd_rn(t.y, o.y);
-    }
-    return t;
+    if (lane == 0) s[m] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(warps * 32) : "memory");
+    auto join = [&](int o) {
+      const float x = __shfl_xor_sync(0xFFFFFFFFu, v.x, o), y = __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
+      v.x = __fadd_rn(v.x, x);
+      v.y = MAX ? max_nan(v.y, y) : __fadd_rn(v.y, y);
+    };
+    const int k = lane & (warps <= 4 ? 3 : warps <= 8 ? 7 : 15);
+    v = make_float2(0.0f, 0.0f);
+    if (k < warps) v = s[k];
+    join(1);
+    join(2);
+    if (warps > 4) join(4);
+    if (warps > 8) join(8);
+    return v;
   }
 };
 
@@ -238,11 +247,6 @@ struct Team {
 constexpr int kTeamWarps = 16;
 constexpr int kTeamThreads = 32 * kTeamWarps;
 
-// Shape of the teams for rows of `units` units with up to `nu` units a warp:
-// warps per row, and teams per CTA of at least eight warps.
-struct TeamShape {
-  int warps, teams;
-};
 // Lets kernel `fn` take all the shared memory its static arrays leave, once per
 // (kernel, device).  `opted`: the kernel's flags.
 inline cudaError_t allow_shared(const void* fn, const DeviceInfo& dev, std::atomic<int>* opted) {
@@ -267,11 +271,43 @@ int64_t row_units(int64_t D) {
   using U = Unit<T, LAYOUT>;
   return (D + (LAYOUT == PHASED ? U::EPL - 1 : 0) + U::COLS - 1) / U::COLS;
 }
-inline TeamShape team_shape(int64_t units, int nu) {
-  TeamShape t;
-  t.warps = (int)((units + nu - 1) / nu);
-  t.teams = t.warps >= 8 ? 1 : 8 / t.warps;
-  return t;
+
+// The weight, offset added, in shared memory as fp32 for rows at `unit`'s
+// offset: plane q of granule g (of ngr) holds columns 4q .. 4q + 3 of it, so a
+// warp reads 512 contiguous bytes of a plane.  Columns outside the row are zero.
+template <class T, int LAYOUT>
+__device__ __forceinline__ void stage_weight(float4* planes, int ngr, Unit<T, LAYOUT> unit,
+                                             const void* weight, float offset) {
+  using U = Unit<T, LAYOUT>;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+  for (int g = tid; g < ngr; g += blockDim.x * blockDim.y) {
+    // granule g of the row: lane 0's of a unit that starts there
+    unit.lane = 0;
+    const int c0 = g * U::EPL;
+    F2 f[U::P];
+    Granule<T>::widen(unit.load_weight(weight, c0), f);
+#pragma unroll
+    for (int i = 0; i < U::P; ++i) {
+      f[i] = f2_add(f2(offset, offset), f[i]);
+      const int c = unit.col(c0, 2 * i), d = unit.col(c0, 2 * i + 1);
+      if (c < 0 || c >= unit.D) f[i].x = 0.0f;
+      if (d < 0 || d >= unit.D) f[i].y = 0.0f;
+    }
+#pragma unroll
+    for (int q = 0; q < U::P / 2; ++q)
+      planes[q * ngr + g] = make_float4(f[2 * q].x, f[2 * q].y, f[2 * q + 1].x, f[2 * q + 1].y);
+  }
+}
+// granule g's weights
+template <class T>
+__device__ __forceinline__ void staged_weight(const float4* planes, int ngr, int g,
+                                              F2 (&w)[Granule<T>::P]) {
+#pragma unroll
+  for (int q = 0; q < Granule<T>::P / 2; ++q) {
+    const float4 v = planes[q * ngr + g];
+    w[2 * q] = f2(v.x, v.y);
+    w[2 * q + 1] = f2(v.z, v.w);
+  }
 }
 
 }  // namespace dit

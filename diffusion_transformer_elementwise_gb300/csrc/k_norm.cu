@@ -21,10 +21,15 @@
 //
 // A team of warps holds a row in registers, up to four units of 512 bytes a
 // warp; longer rows are read twice by one CTA each.
+#include <algorithm>
+
 #include "dit_stat.cuh"
 #include "dit_token.h"
 #include "dit_unit.cuh"
 
+#ifndef DIT_NORM_STAGED
+#define DIT_NORM_STAGED 64
+#endif
 namespace dit {
 namespace {
 
@@ -141,10 +146,9 @@ struct NormRow {
   // one unit of the output, one scale per 128 columns (the whole warp calls;
   // a group lies inside the unit)
   __device__ __forceinline__ static void emit_groups(const NormArgs& a, const U& unit, int64_t row,
-                                                     int c0, const Raw<16>& x, const Raw<16>& wr,
+                                                     int c0, const Raw<16>& x, const F2 (&w)[P],
                                                      float S, float r) {
-    F2 w[P], v[P];
-    weight(wr, a.offset, w);
+    F2 v[P];
     weighted(x, w, v);
     float m[NG];
     group_max(v, m);
@@ -222,258 +226,270 @@ __device__ __forceinline__ float inverse_rms(float S, const NormArgs& a, Again a
   return fast_inverse_rms_scaled(again(sc), sc, a.d_f, a.inv_d, a.eps);
 }
 
-// A row's codes with one factor q; values(x, weights, v) gives what it applies to.
-template <class R, int NU, class U, class Values>
-__device__ __forceinline__ void emit_row(const NormArgs& a, const U& unit, int64_t row, int m, int W,
-                                         const Raw<16> (&x)[NU], const Raw<16> (&w)[NU],
-                                         Values values, Quant q) {
-  Quant all[R::NG];
-#pragma unroll
-  for (int g = 0; g < R::NG; ++g) all[g] = q;
+// One row held by a team: its statistic, then its output.  x: the lane's
+// granules; weights(j, wf): unit j's weights, offset added; after_read(): called once the sums
+// have been formed (the caller's next copies).  kSplit: PHASED groups of 128, whose
+// pieces go through `pieces`, [2][groups of the team's warps].
+template <class T, int LAYOUT, int NU, int Q8, class Weights, class AfterRead>
+__device__ __forceinline__ void finish_row(const NormArgs& a, const Unit<T, LAYOUT>& unit, Team& t,
+                                           int64_t row, const Raw<16> (&x)[NU], Weights weights,
+                                           AfterRead after_read, float2* pieces) {
+  using R = NormRow<T, LAYOUT>;
+  using U = Unit<T, LAYOUT>;
+  constexpr int P = U::P;
+  constexpr bool kSplit = LAYOUT == PHASED && Q8 == 2;
+  const int m = t.m, W = t.warps, lane = t.lane;
+  const int n = W * NU * R::BLOCKS;  // groups of 128 the team's units reach
+  auto piece = [&](int j) { return (m + j * W) * R::BLOCKS + lane / R::LANES; };
+
+  F2 acc[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+  float big = 0.0f;
 #pragma unroll
   for (int j = 0; j < NU; ++j) {
-    F2 wf[U::P], v[U::P];
-    R::weight(w[j], a.offset, wf);
-    values(x[j], wf, v);
-    unit.store8((char*)a.out + row * a.D, (m + j * W) * U::COLS, R::codes(v, all));
-  }
-  if (m == 0 && unit.lane == 0) a.scales[row] = q.scale;
-}
-
-// Threads of a CTA and registers of a thread: up to two units a warp, two
-// CTAs of 16 warps per SM (64 registers); four units, one (128).
-constexpr int kNormStages = 2;
-
-// A CTA's teams take rows CTA * teams + team, and on by the grid's rows, a
-// multiple of the rows' period for PHASED rows.  STAGED: one wave of CTAs,
-// each lane copying the granules it will read into its own slots of shared
-// memory (cp.async), kNormStages rows ahead, so the copies need no barrier and are in
-// flight while the team reduces and writes; otherwise a team's rows are few
-// (one, for most sizes) and other CTAs' loads fill the memory's pipe.
-template <class T, int LAYOUT, int NU, bool ADD, int Q8, bool STAGED>
-__global__ void __launch_bounds__(kTeamThreads, NU <= 2 ? 2 : 1) norm_team_kernel(NormArgs a) {
-  using R = NormRow<T, LAYOUT>;
-  using U = typename R::U;
-  constexpr int P = U::P;
-  constexpr int NS = ADD ? 2 : 1;               // streams
-  constexpr uint32_t kSlot = 32 * 16;           // a unit of one stream
-  constexpr uint32_t kStage = NS * NU * kSlot;  // a warp's part of a row
-  static_assert(!STAGED || LAYOUT != NARROW, "cp.async moves granules");
-  __shared__ float2 slots[2 * kTeamWarps];
-  // PHASED groups: (own, head) of each group of the CTA's rows, by row parity
-  constexpr bool kSplit = LAYOUT == PHASED && Q8 == 2;
-  constexpr int kBlocks = NU * R::BLOCKS;  // groups of a warp
-  __shared__ float2 groups[kSplit ? 2 : 1][kSplit ? kTeamWarps * kBlocks : 1];
-  extern __shared__ float4 shared[];  // STAGED: [warps][stages][streams][NU][32]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int W = a.warps, teams = (blockDim.x >> 5) / W;
-  const int team = warp / W, m = warp - team * W;
-  Team t{slots + team * 2 * W, W, m, 1 + team, 0};
-  const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
-  const int64_t step = (int64_t)gridDim.x * teams;
-  int64_t row = (int64_t)blockIdx.x * teams + team;
-  if (row >= a.rows) return;  // the whole team
-
-  U unit(a.D, lane);
-  unit.at_row(row, a.rows);
-  const uint32_t stage0 =
-      STAGED ? smem_addr(shared) + warp * (kNormStages * kStage) + lane * 16 : 0u;
-  auto prefetch = [&](int64_t r, int s) {  // an empty group past the end
-    if (r < a.rows) {
+    F2 f[P];
+    Granule<T>::widen(x[j], f);
 #pragma unroll
-      for (int j = 0; j < NU; ++j) {
-        const int c0 = (m + j * W) * U::COLS;
-        const uint32_t dst = stage0 + s * kStage + j * kSlot;
-        unit.copy(dst, a.x, r, a.rows, c0);
-        if constexpr (ADD) unit.copy(dst + NU * kSlot, a.u, r, a.rows, c0);
-      }
-    }
-    cp_async_commit();
-  };
-  if constexpr (STAGED) {
-#pragma unroll
-    for (int s = 0; s < kNormStages; ++s) prefetch(row + s * step, s);
-  }
-  Raw<16> w[NU];
-  if constexpr (STAGED) {
-#pragma unroll
-    for (int j = 0; j < NU; ++j) w[j] = unit.load_weight(a.w, (m + j * W) * U::COLS);
-  }
-  int s = 0;
-  for (; row < a.rows; row += step) {
-    unit.at_row(row, a.rows);
-    Raw<16> x[NU], u[NU];
-    if constexpr (STAGED) cp_async_wait<kNormStages - 1>();  // this lane's copies of the row
-#pragma unroll
-    for (int j = 0; j < NU; ++j) {
-      const int c0 = (m + j * W) * U::COLS;
-      if constexpr (STAGED) {
-        const uint32_t at = stage0 + s * kStage + j * kSlot;
-        x[j] = unit.copied(at, c0);
-        if constexpr (ADD) u[j] = unit.copied(at + NU * kSlot, c0);
+    for (int i = 0; i < P; ++i) acc[i & 1] = f2_fma(f[i], f[i], acc[i & 1]);
+    if constexpr (Q8 == 1 || kSplit) {
+      F2 wf[P], v[P];
+      weights(j, wf);
+      R::weighted(x[j], wf, v);
+      if constexpr (kSplit) {
+        float own, head;
+        R::split_max(v, unit, own, head);
+        if (lane % R::LANES == 0) pieces[t.par * n + piece(j)] = make_float2(own, head);
+        const bool bad = (own != 0.0f && !usable(own)) || (head != 0.0f && !usable(head));
+        big = bad ? 1.0f : big;
       } else {
-        x[j] = unit.load((const char*)a.x + row * pitch, c0);
-        if constexpr (ADD) u[j] = unit.load((const char*)a.u + row * pitch, c0);
+        big = max_nan(big, R::max_of(v));
       }
     }
-    if constexpr (!STAGED) {
-#pragma unroll
-      for (int j = 0; j < NU; ++j) w[j] = unit.load_weight(a.w, (m + j * W) * U::COLS);
-    }
-    F2 acc[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
-    float big = 0.0f;
+  }
+  after_read();
+  acc[0] = f2_add(acc[0], acc[1]);
+  float2 red = make_float2(warp_sum(__fadd_rn(acc[0].x, acc[0].y)), 0.0f);
+  if constexpr (Q8 == 1) red.y = warp_max(big);
+  if constexpr (kSplit) red.y = __any_sync(0xFFFFFFFFu, big != 0.0f) ? 1.0f : 0.0f;
+  [[maybe_unused]] int par = t.par;
+  red = t.combine<Q8 == 1 || kSplit>(red);
+  const float r = inverse_rms(red.x, a, [&](float sc) {
+    float s2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-      const int c0 = (m + j * W) * U::COLS;
-      if constexpr (ADD) {
-        x[j] = R::add(x[j], u[j]);
-        unit.store((char*)a.res + row * pitch, c0, x[j]);
-      }
       F2 f[P];
       Granule<T>::widen(x[j], f);
 #pragma unroll
-      for (int i = 0; i < P; ++i) acc[i & 1] = f2_fma(f[i], f[i], acc[i & 1]);
-      if constexpr (Q8 == 1 || kSplit) {
-        F2 wf[P], v[P];
-        R::weight(w[j], a.offset, wf);
-        R::weighted(x[j], wf, v);
-        if constexpr (kSplit) {
-          float own, head;
-          R::split_max(v, unit, own, head);
-          if (lane % R::LANES == 0)
-            groups[t.par][team * W * kBlocks + (m + j * W) * R::BLOCKS + lane / R::LANES] =
-                make_float2(own, head);
-          const bool bad = (own != 0.0f && !usable(own)) || (head != 0.0f && !usable(head));
-          big = bad ? 1.0f : big;
-        } else {
-          big = max_nan(big, R::max_of(v));
-        }
+      for (int i = 0; i < P; ++i) {
+        const float u0 = __fmul_rn(f2_lo(f[i]), sc), u1 = __fmul_rn(f2_hi(f[i]), sc);
+        s2 = __fmaf_rn(u1, u1, __fmaf_rn(u0, u0, s2));
       }
     }
-    if constexpr (STAGED) {  // the stage has been read
-      prefetch(row + kNormStages * step, s);
-      s = s + 1 == kNormStages ? 0 : s + 1;
+    return t.combine<false>(make_float2(warp_sum(s2), 0.0f)).x;
+  });
+
+  if constexpr (Q8 == 0) {
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      F2 wf[P], y[P];
+      weights(j, wf);
+      R::normed(x[j], wf, r, y);
+      unit.store((char*)a.out + row * ((int64_t)a.D * U::ES), (m + j * W) * U::COLS, Granule<T>::narrow(y));
     }
-    acc[0] = f2_add(acc[0], acc[1]);
-    float2 red = make_float2(warp_sum(__fadd_rn(acc[0].x, acc[0].y)), 0.0f);
-    if constexpr (Q8 == 1) red.y = warp_max(big);
-    if constexpr (kSplit) red.y = __any_sync(0xFFFFFFFFu, big != 0.0f) ? 1.0f : 0.0f;
-    [[maybe_unused]] int par = t.par;
-    red = t.combine<Q8 == 1 || kSplit>(red);
-    const float r = inverse_rms(red.x, a, [&](float sc) {
-      float s2 = 0.0f;
+  } else if constexpr (Q8 == 2 && !kSplit) {
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      F2 wf[P];
+      weights(j, wf);
+      R::emit_groups(a, unit, row, (m + j * W) * U::COLS, x[j], wf, red.x, r);
+    }
+  } else if constexpr (!kSplit) {
+    // one scale per row
+    auto emit = [&](Quant q, auto values) {
+      Quant all[R::NG];
+#pragma unroll
+      for (int g = 0; g < R::NG; ++g) all[g] = q;
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
-        F2 f[P];
-        Granule<T>::widen(x[j], f);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const float u0 = __fmul_rn(f2_lo(f[i]), sc), u1 = __fmul_rn(f2_hi(f[i]), sc);
-          s2 = __fmaf_rn(u1, u1, __fmaf_rn(u0, u0, s2));
-        }
+        F2 wf[P], v[P];
+        weights(j, wf);
+        values(x[j], wf, v);
+        unit.store8((char*)a.out + row * a.D, (m + j * W) * U::COLS, R::codes(v, all));
       }
-      return t.combine<false>(make_float2(warp_sum(s2), 0.0f)).x;
-    });
-
-    if constexpr (Q8 == 0) {
+      if (m == 0 && lane == 0) a.scales[row] = q.scale;
+    };
+    if (usable(red.x) && (red.y == 0.0f || usable(red.y))) {
+      emit(quant_of_t(red.y, r),
+           [&](const Raw<16>& x, const F2(&wf)[P], F2(&v)[P]) { R::weighted(x, wf, v); });
+    } else {  // rare, uniform over the row's threads: the maximum of y
+      float my = 0.0f;
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
         F2 wf[P], y[P];
-        R::weight(w[j], a.offset, wf);
+        weights(j, wf);
         R::normed(x[j], wf, r, y);
-        unit.store((char*)a.out + row * pitch, (m + j * W) * U::COLS, Granule<T>::narrow(y));
+        R::mask(y, unit, (m + j * W) * U::COLS);
+        my = max_nan(my, R::max_of(y));
       }
-    } else if constexpr (Q8 == 2 && !kSplit) {
-#pragma unroll
-      for (int j = 0; j < NU; ++j)
-        R::emit_groups(a, unit, row, (m + j * W) * U::COLS, x[j], w[j], red.x, r);
-    } else if constexpr (!kSplit) {
-      // one scale per row
-      if (usable(red.x) && (red.y == 0.0f || usable(red.y))) {
-        const Quant q = quant_of_t(red.y, r);
-        emit_row<R, NU>(
-            a, unit, row, m, W, x, w,
-            [&](const Raw<16>& x, const F2(&wf)[P], F2(&v)[P]) { R::weighted(x, wf, v); }, q);
-      } else {  // rare, uniform over the row's threads: the maximum of y
-        float my = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NU; ++j) {
-          F2 wf[P], y[P];
-          R::weight(w[j], a.offset, wf);
-          R::normed(x[j], wf, r, y);
-          R::mask(y, unit, (m + j * W) * U::COLS);
-          my = max_nan(my, R::max_of(y));
-        }
-        my = t.combine<true>(make_float2(0.0f, warp_max(my))).y;
-        const float f = small_factor(my);
-        emit_row<R, NU>(
-            a, unit, row, m, W, x, w,
-            [&](const Raw<16>& x, const F2(&wf)[P], F2(&v)[P]) {
-              R::normed(x, wf, r, v);
-              R::scale_by(v, f);
-            },
-            quant_of_y(my));
+      my = t.combine<true>(make_float2(0.0f, warp_max(my))).y;
+      const float f = small_factor(my);
+      emit(quant_of_y(my), [&](const Raw<16>& x, const F2(&wf)[P], F2(&v)[P]) {
+        R::normed(x, wf, r, v);
+        R::scale_by(v, f);
+      });
+    }
+  } else {
+    // groups that cross granules, units and warps
+    const bool slow = !usable(red.x) || red.y != 0.0f;
+    auto values = [&](int j, F2(&v)[P]) {
+      F2 wf[P];
+      weights(j, wf);
+      if (slow) {
+        R::normed(x[j], wf, r, v);
+        R::mask(v, unit, (m + j * W) * U::COLS);
+      } else {
+        R::weighted(x[j], wf, v);
       }
-    } else {
-      // groups that cross granules, units and warps
-      const bool slow = !usable(red.x) || red.y != 0.0f;
-      auto values = [&](int j, F2(&v)[P]) {
-        F2 wf[P];
-        R::weight(w[j], a.offset, wf);
-        if (slow) {
-          R::normed(x[j], wf, r, v);
-          R::mask(v, unit, (m + j * W) * U::COLS);
-        } else {
-          R::weighted(x[j], wf, v);
-        }
-      };
-      if (slow) {  // rare, uniform over the row's threads: the maxima of y
-        par = t.par;
-#pragma unroll
-        for (int j = 0; j < NU; ++j) {
-          F2 y[P];
-          values(j, y);
-          float own, head;
-          R::split_max(y, unit, own, head);
-          if (lane % R::LANES == 0)
-            groups[par][team * W * kBlocks + (m + j * W) * R::BLOCKS + lane / R::LANES] =
-                make_float2(own, head);
-        }
-        t.combine<true>(make_float2(0.0f, 0.0f));
-      }
-      if (W == 1) __syncwarp();
-      const float2* g = groups[par] + team * W * kBlocks;
-      const int n = W * kBlocks;
-      // group k's maximum: its own part, and the next one's head
-      auto maximum = [&](int k) { return k + 1 < n ? max_nan(g[k].x, g[k + 1].y) : g[k].x; };
+    };
+    if (slow) {  // rare, uniform over the row's threads: the maxima of y
+      par = t.par;
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
-        F2 v[P];
-        values(j, v);
-        const int k = (m + j * W) * R::BLOCKS + lane / R::LANES;
-        const int cut = lane % R::LANES == 0 ? unit.off : 0;
-        const float big = maximum(k), prev = cut && k > 0 ? maximum(k - 1) : big;
-        Quant mine, before;
-        if (slow) {
-          mine = quant_of_y(big);
-          before = quant_of_y(prev);
-          const float f = small_factor(big), b = small_factor(prev);
-#pragma unroll
-          for (int i = 0; i < P; ++i)
-            v[i] = f2_mul(v[i], f2(2 * i < cut ? b : f, 2 * i + 1 < cut ? b : f));
-        } else {
-          mine = quant_of_t(big, r);
-          before = quant_of_t(prev, r);
-        }
-        unit.store8((char*)a.out + row * a.D, (m + j * W) * U::COLS,
-                    R::split_codes(v, cut, before.mul, mine.mul));
-        if (lane % R::LANES == 0 && k < a.groups) a.scales[row * a.groups + k] = mine.scale;
+        F2 y[P];
+        values(j, y);
+        float own, head;
+        R::split_max(y, unit, own, head);
+        if (lane % R::LANES == 0) pieces[par * n + piece(j)] = make_float2(own, head);
       }
-      if (W == 1) {
-        t.par ^= 1;  // (a team of one warp has no barrier to alternate them)
-        __syncwarp();
+      t.combine<true>(make_float2(0.0f, 0.0f));
+    }
+    if (W == 1) __syncwarp();
+    const float2* g = pieces + par * n;
+    // group k's maximum: its own part, and the next one's head
+    auto maximum = [&](int k) { return k + 1 < n ? max_nan(g[k].x, g[k + 1].y) : g[k].x; };
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      F2 v[P];
+      values(j, v);
+      const int k = piece(j);
+      const int cut = lane % R::LANES == 0 ? unit.off : 0;
+      const float big = maximum(k), prev = cut && k > 0 ? maximum(k - 1) : big;
+      Quant mine, before;
+      if (slow) {
+        mine = quant_of_y(big);
+        before = quant_of_y(prev);
+        const float f = small_factor(big), b = small_factor(prev);
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          v[i] = f2_mul(v[i], f2(2 * i < cut ? b : f, 2 * i + 1 < cut ? b : f));
+      } else {
+        mine = quant_of_t(big, r);
+        before = quant_of_t(prev, r);
+      }
+      unit.store8((char*)a.out + row * a.D, (m + j * W) * U::COLS,
+                  R::split_codes(v, cut, before.mul, mine.mul));
+      if (lane % R::LANES == 0 && k < a.groups) a.scales[row * a.groups + k] = mine.scale;
+    }
+    if (W == 1) {
+      t.par ^= 1;  // (a team of one warp has no barrier to alternate them)
+      __syncwarp();
+    }
+  }
+}
+
+// A row or a few per team, straight from global memory (WIDE, NARROW): other
+// CTAs' loads fill the memory's pipe.
+template <class T, int LAYOUT, int NU, bool ADD, int Q8>
+__global__ void __launch_bounds__(kTeamThreads, 2) norm_direct_kernel(NormArgs a) {
+  using R = NormRow<T, LAYOUT>;
+  using U = typename R::U;
+  __shared__ float2 slots[2 * kTeamWarps];
+  Team t(slots);
+  const U unit(a.D, t.lane);
+  const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
+  for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < a.rows;
+       row += (int64_t)gridDim.x * blockDim.y) {
+    Raw<16> x[NU], u[NU], w[NU];
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      const int c0 = (t.m + j * t.warps) * U::COLS;
+      x[j] = unit.load((const char*)a.x + row * pitch, c0);
+      if constexpr (ADD) u[j] = unit.load((const char*)a.u + row * pitch, c0);
+    }
+#pragma unroll
+    for (int j = 0; j < NU; ++j) w[j] = unit.load_weight(a.w, (t.m + j * t.warps) * U::COLS);
+    if constexpr (ADD) {
+#pragma unroll
+      for (int j = 0; j < NU; ++j) {
+        x[j] = R::add(x[j], u[j]);
+        unit.store((char*)a.res + row * pitch, (t.m + j * t.warps) * U::COLS, x[j]);
       }
     }
+    finish_row<T, LAYOUT, NU, Q8>(
+        a, unit, t, row, x, [&](int j, F2(&wf)[U::P]) { R::weight(w[j], a.offset, wf); }, [] {},
+        nullptr);
+  }
+}
+
+// One wave of CTAs over many rows (WIDE, PHASED).  The weights lie in shared
+// memory as fp32, and each lane copies the granules of its team's next row into its
+// own slots of shared memory (cp.async) as soon as it has read the current one out of
+// them: the copies need no barrier, and are in flight while the team reduces
+// and writes.  A CTA's rows are a multiple of gridDim.x apart, which for
+// PHASED rows is a multiple of 8: all at one offset from a granule.
+template <class T, int LAYOUT, int NU, bool ADD, int Q8>
+__global__ void __launch_bounds__(kTeamThreads, 2) norm_staged_kernel(NormArgs a) {
+  using R = NormRow<T, LAYOUT>;
+  using U = typename R::U;
+  constexpr int NS = ADD ? 2 : 1;      // streams
+  constexpr uint32_t kSlot = 32 * 16;  // a unit of one stream
+  constexpr bool kSplit = LAYOUT == PHASED && Q8 == 2;
+  static_assert(LAYOUT != NARROW, "cp.async moves granules");
+  __shared__ float2 slots[2 * kTeamWarps];
+  __shared__ float2 pieces[kSplit ? 2 * kTeamWarps * NU * R::BLOCKS : 1];
+  extern __shared__ float4 shared[];  // weights, then [warps][streams][NU][32]
+  Team t(slots);
+  const int W = t.warps, m = t.m;
+  U unit(a.D, t.lane);
+  unit.at_row(blockIdx.x, a.rows);
+  const int ngr = W * NU * 32;  // granules of a row, padded
+  const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t row = blockIdx.x + (int64_t)gridDim.x * threadIdx.y;
+  const uint32_t stage = smem_addr(shared + ngr * (U::P / 2)) +
+                         (threadIdx.y * W + m) * (NS * NU * kSlot) + t.lane * 16;
+  auto prefetch = [&](int64_t r) {
+    if (r >= a.rows) return;
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      const int c0 = (m + j * W) * U::COLS;
+      unit.copy(stage + j * kSlot, a.x, r, a.rows, c0);
+      if constexpr (ADD) unit.copy(stage + (NU + j) * kSlot, a.u, r, a.rows, c0);
+    }
+  };
+  prefetch(row);
+  cp_async_commit();
+  stage_weight<T, LAYOUT>(shared, ngr, unit, a.w, a.offset);
+  __syncthreads();
+  for (; row < a.rows; row += step) {
+    cp_async_wait<0>();  // this lane's copies of the row
+    Raw<16> x[NU];
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      const int c0 = (m + j * W) * U::COLS;
+      x[j] = unit.copied(stage + j * kSlot, c0);
+      if constexpr (ADD) {
+        x[j] = R::add(x[j], unit.copied(stage + (NU + j) * kSlot, c0));
+        unit.store((char*)a.res + row * pitch, c0, x[j]);
+      }
+    }
+    finish_row<T, LAYOUT, NU, Q8>(
+        a, unit, t, row, x,
+        [&](int j, F2(&wf)[U::P]) { staged_weight<T>(shared, ngr, (m + j * W) * 32 + t.lane, wf); },
+        [&] {
+          prefetch(row + step);
+          cp_async_commit();
+        },
+        pieces + threadIdx.y * (2 * W * NU * R::BLOCKS));
   }
 }
 
@@ -482,14 +498,14 @@ __global__ void __launch_bounds__(kTeamThreads, NU <= 2 ? 2 : 1) norm_team_kerne
 // The squares of a unit are summed in fp32 and the units in fp64, so that a
 // thread's thousands of units add no error.
 template <class T, int LAYOUT, bool ADD, int Q8>
-__global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
+__global__ void __launch_bounds__(kTeamThreads) norm_long_kernel(NormArgs a) {
   using R = NormRow<T, LAYOUT>;
   using U = typename R::U;
   constexpr int P = U::P;
-  __shared__ float2 slots[2 * 32];
-  __shared__ double sums[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
-  Team t{slots, W, warp, 1, 0};
+  __shared__ float2 slots[2 * kTeamWarps];
+  __shared__ double sums[kTeamWarps];
+  Team t(slots);
+  const int lane = t.lane, warp = t.m, W = t.warps;
   const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
   const U unit(a.D, lane);
 
@@ -572,12 +588,11 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
     }
     for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
       const Raw<16> x = unit.load(src, c0);
-      const Raw<16> w = unit.load_weight(a.w, c0);
+      F2 wf[P], v[P];
+      R::weight(unit.load_weight(a.w, c0), a.offset, wf);
       if constexpr (Q8 == 2) {
-        R::emit_groups(a, unit, row, c0, x, w, S, r);
+        R::emit_groups(a, unit, row, c0, x, wf, S, r);
       } else {
-        F2 wf[P], v[P];
-        R::weight(w, a.offset, wf);
         if (Q8 == 0 || slow)
           R::normed(x, wf, r, v);
         else
@@ -592,46 +607,55 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
   }
 }
 
-template <class T, int LAYOUT, int NU, bool ADD, int Q8, bool STAGED>
-cudaError_t launch_team(const DeviceInfo& dev, NormArgs a, int64_t units, cudaStream_t s) {
-  const auto kern = norm_team_kernel<T, LAYOUT, NU, ADD, Q8, STAGED>;
-  TeamShape t = team_shape(units, NU);
-  if (STAGED) t.teams = kTeamWarps / t.warps;
-  a.warps = t.warps;
-  const int block = t.warps * t.teams * 32;
-  int64_t grid = (a.rows + t.teams - 1) / t.teams;
-  size_t smem = 0;
-  if (STAGED) {
-    smem = (size_t)block * 16 * NU * (ADD ? 2 : 1) * kNormStages;
-    static std::atomic<int> opted[kOptinDevices];
-    const cudaError_t e = allow_shared((const void*)kern, dev, opted);
-    if (e != cudaSuccess) return e;
-    const int64_t wave = (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, block, smem);
-    if (grid > wave) grid = wave;
-    // a team's rows are a multiple of the period apart
-    if (LAYOUT == PHASED) grid = (grid + 7) / 8 * 8;
-  }
-  if (grid > (int64_t(1) << 30)) grid = int64_t(1) << 30;
-  kern<<<(unsigned)grid, block, smem, s>>>(a);
+template <class T, int LAYOUT, int NU, bool ADD, int Q8>
+cudaError_t launch_direct(const NormArgs& a, int64_t units, cudaStream_t s) {
+  const int warps = (int)((units + NU - 1) / NU), teams = warps >= 8 ? 1 : 8 / warps;
+  const int64_t grid = std::min<int64_t>((a.rows + teams - 1) / teams, int64_t(1) << 30);
+  norm_direct_kernel<T, LAYOUT, NU, ADD, Q8><<<(unsigned)grid, dim3(warps * 32, teams), 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <class T, int LAYOUT, int NU, bool ADD, int Q8>
+cudaError_t launch_staged(const DeviceInfo& dev, const NormArgs& a, int64_t units, cudaStream_t s) {
+  const auto kern = norm_staged_kernel<T, LAYOUT, NU, ADD, Q8>;
+  const int warps = (int)((units + NU - 1) / NU);
+  // few rows: a CTA for each before a second team in any
+  const int teams = (int)std::max<int64_t>(
+      1, std::min<int64_t>(kTeamWarps / warps, (a.rows + dev.sm_count - 1) / dev.sm_count));
+  const size_t smem = (size_t)warps * NU * 512 * (sizeof(T) == 2 ? 2 : 1) +
+                      (size_t)warps * teams * NU * 512 * (ADD ? 2 : 1);
+  static std::atomic<int> opted[kOptinDevices];
+  const cudaError_t e = allow_shared((const void*)kern, dev, opted);
+  if (e != cudaSuccess) return e;
+  const int64_t wave =
+      (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, warps * teams * 32, smem);
+  int64_t grid = std::min<int64_t>(wave, (a.rows + teams - 1) / teams);
+  if (LAYOUT == PHASED) grid = (grid + 7) / 8 * 8;
+  kern<<<(unsigned)grid, dim3(warps * 32, teams), smem, s>>>(a);
   return cudaGetLastError();
 }
 
 template <class T, int LAYOUT, bool ADD, int Q8>
-cudaError_t launch(const DeviceInfo& dev, NormArgs a, cudaStream_t s) {
+cudaError_t launch(const DeviceInfo& dev, const NormArgs& a, cudaStream_t s) {
   const int64_t units = row_units<T, LAYOUT>(a.D);
-  // rows of one or two units a warp, WIDE: a CTA per row, or a few; others staged
-  if (units <= 8) return launch_team<T, LAYOUT, 1, ADD, Q8, LAYOUT == PHASED>(dev, a, units, s);
-  if (units <= 2 * kTeamWarps)
-    return launch_team<T, LAYOUT, 2, ADD, Q8, LAYOUT == PHASED>(dev, a, units, s);
-  if (units <= 4 * kTeamWarps)
-    return launch_team<T, LAYOUT, 4, ADD, Q8, LAYOUT != NARROW>(dev, a, units, s);
-  if constexpr (LAYOUT == PHASED) {
-    return launch<T, NARROW, ADD, Q8>(dev, a, s);
-  } else {
-    int64_t grid = (int64_t)dev.sm_count * 2;
-    if (grid > a.rows) grid = a.rows;
-    norm_long_kernel<T, LAYOUT, ADD, Q8><<<(unsigned)grid, 1024, 0, s>>>(a);
+  if constexpr (LAYOUT != NARROW) {
+    // PHASED rows, and WIDE ones of more than a few for each SM
+    const bool staged = LAYOUT == PHASED || a.rows * units > DIT_NORM_STAGED * (int64_t)dev.sm_count ||
+                        units > 2 * kTeamWarps;
+    if (staged && units <= 4 * kTeamWarps) {
+      if (units == 1) return launch_staged<T, LAYOUT, 1, ADD, Q8>(dev, a, units, s);
+      if (units == 2) return launch_staged<T, LAYOUT, 2, ADD, Q8>(dev, a, units, s);
+      return launch_staged<T, LAYOUT, 4, ADD, Q8>(dev, a, units, s);
+    }
+  }
+  if constexpr (LAYOUT != PHASED) {
+    if (units <= 8) return launch_direct<T, LAYOUT, 1, ADD, Q8>(a, units, s);
+    if (units <= 2 * kTeamWarps) return launch_direct<T, LAYOUT, 2, ADD, Q8>(a, units, s);
+    const int64_t grid = std::min<int64_t>((int64_t)dev.sm_count * 4, a.rows);
+    norm_long_kernel<T, LAYOUT, ADD, Q8><<<(unsigned)grid, kTeamThreads, 0, s>>>(a);
     return cudaGetLastError();
+  } else {
+    return launch<T, NARROW, ADD, Q8>(dev, a, s);
   }
 }
 

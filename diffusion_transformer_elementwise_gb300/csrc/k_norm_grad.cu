@@ -16,7 +16,7 @@
 // the same call gives the same bits.
 //
 // Each lane copies the granules it will read itself into its own slots of
-// shared memory (cp.async), kStages rows ahead, so the copies need no barrier
+// shared memory (cp.async), a row or two ahead, so the copies need no barrier
 // and a warp's loads are in flight while it reduces and writes.
 #include <algorithm>
 
@@ -51,37 +51,40 @@ template <class T, int LAYOUT>
 struct GradRow {
   using U = Unit<T, LAYOUT>;
   static constexpr int P = U::P;
-  // sums of x^2 and of g (offset + w) x over a lane's elements of one unit,
-  // x scaled by sc
+  // a unit's weights from global memory, offset added
+  __device__ __forceinline__ static void weight(const U& unit, const NormGradArgs& a, int c0,
+                                                F2 (&w)[P]) {
+    Granule<T>::widen(unit.load_weight(a.w, c0), w);
+#pragma unroll
+    for (int i = 0; i < P; ++i) w[i] = f2_add(f2(a.offset, a.offset), w[i]);
+  }
+  // sums of x^2 and of g w x over a lane's elements of one unit (w: offset +
+  // weight), x scaled by sc
   __device__ __forceinline__ static void sums(const Raw<16>& xr, const Raw<16>& gr,
-                                              const Raw<16>& wr, float offset, float sc, F2& s,
-                                              F2& q) {
-    F2 x[P], g[P], w[P];
+                                              const F2 (&w)[P], float sc, F2& s, F2& q) {
+    F2 x[P], g[P];
     Granule<T>::widen(xr, x);
     Granule<T>::widen(gr, g);
-    Granule<T>::widen(wr, w);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       x[i] = f2_mul(x[i], f2(sc, sc));
-      const F2 t = f2_mul(g[i], f2_add(f2(offset, offset), w[i]));
+      const F2 t = f2_mul(g[i], w[i]);
       s = f2_fma(x[i], x[i], s);
       q = f2_fma(t, x[i], q);
     }
   }
   // gx of one unit, and g n added to acc
   __device__ __forceinline__ static Raw<16> grad(const Raw<16>& xr, const Raw<16>& gr,
-                                                 const Raw<16>& wr, const Raw<16>& skip,
-                                                 bool has_skip, float offset, RowStat st,
-                                                 F2 (&acc)[P]) {
-    F2 x[P], g[P], w[P], o[P];
+                                                 const F2 (&w)[P], const Raw<16>& skip,
+                                                 bool has_skip, RowStat st, F2 (&acc)[P]) {
+    F2 x[P], g[P], o[P];
     Granule<T>::widen(xr, x);
     Granule<T>::widen(gr, g);
-    Granule<T>::widen(wr, w);
     const F2 r = f2(st.r, st.r), nk = f2(-st.k, -st.k);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const F2 n = f2_mul(x[i], r);
-      const F2 t = f2_mul(g[i], f2_add(f2(offset, offset), w[i]));
+      const F2 t = f2_mul(g[i], w[i]);
       acc[i] = f2_fma(g[i], n, acc[i]);
       o[i] = f2_mul(f2_fma(n, nk, t), r);
     }
@@ -104,11 +107,13 @@ struct GradRow {
   }
 };
 
-constexpr int kStages = 2;
-// warps of a CTA, which set the registers of a thread: 80 for one unit a
-// warp, 128 for more
+// rows staged ahead (shared memory holds one of the widest rows)
 template <int NU>
-constexpr int kGradWarps = NU == 1 ? 24 : 16;
+constexpr int kStagesOf = NU == 4 ? 1 : 2;
+// most warps of a CTA, which set the registers of a thread: 80 for one unit a
+// warp, 96 for two, 128 for four
+template <int NU>
+constexpr int kGradWarps = NU == 1 ? 24 : NU == 2 ? 20 : 16;
 
 // SKIP: the gradient of the skip path is added.
 template <class T, int LAYOUT, int NU, bool SKIP>
@@ -117,22 +122,24 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
   using U = typename R::U;
   constexpr int P = U::P;
   constexpr int NS = SKIP ? 3 : 2;              // streams
+  constexpr int kStages = kStagesOf<NU>;
   constexpr bool kStaged = LAYOUT != NARROW;
   constexpr uint32_t kSlot = 32 * 16;           // a unit of one stream
   constexpr uint32_t kStage = NS * NU * kSlot;  // a warp's part of a row
   __shared__ float2 slots[2 * kGradWarps<NU>];
-  extern __shared__ float4 shared[];  // [warps][stages][streams][NU][32], then the teams' parts of gw
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int W = a.warps, teams = (blockDim.x >> 5) / W;
-  const int team = warp / W, m = warp - team * W;
-  Team t{slots + team * 2 * W, W, m, 1 + team, 0};
+  // weights (not NARROW), [warps][stages][streams][NU][32]; in the end the teams' parts of gw
+  extern __shared__ float4 shared[];
+  Team t(slots);
+  const int lane = t.lane, W = t.warps, m = t.m, team = threadIdx.y, teams = blockDim.y;
+  const int ngr = W * NU * 32;  // granules of a row, padded
   const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
   const int64_t step = (int64_t)gridDim.x * teams;
-  const uint32_t stage0 = smem_addr(shared) + warp * (kStages * kStage) + lane * 16;
+  const uint32_t stage0 =
+      smem_addr(shared + ngr * (P / 2)) + (team * W + m) * (kStages * kStage) + lane * 16;
 
-  int64_t row = (int64_t)blockIdx.x * teams + team;
+  int64_t row = blockIdx.x + (int64_t)gridDim.x * team;
   U unit(a.D, lane);
-  unit.at_row(row, a.rows);
+  unit.at_row(blockIdx.x, a.rows);
   // this warp's part of row r, into stage s (an empty group past the end)
   auto prefetch = [&](int64_t r, int s) {
     if constexpr (kStaged) {
@@ -152,17 +159,23 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
 #pragma unroll
   for (int s = 0; s < kStages; ++s) prefetch(row + s * step, s);
 
-  Raw<16> w[NU];
+  auto weights = [&](int j, F2(&w)[P]) {
+    if constexpr (kStaged)
+      staged_weight<T>(shared, ngr, (m + j * W) * 32 + lane, w);
+    else
+      R::weight(unit, a, (m + j * W) * U::COLS, w);
+  };
   F2 acc[NU][P];
 #pragma unroll
-  for (int j = 0; j < NU; ++j) {
-    w[j] = unit.load_weight(a.w, (m + j * W) * U::COLS);
+  for (int j = 0; j < NU; ++j)
 #pragma unroll
     for (int i = 0; i < P; ++i) acc[j][i] = f2(0.0f, 0.0f);
+  if constexpr (kStaged) {
+    stage_weight<T, LAYOUT>(shared, ngr, unit, a.w, a.offset);
+    __syncthreads();
   }
   int s = 0;
   for (; row < a.rows; row += step) {
-    unit.at_row(row, a.rows);
     Raw<16> x[NU], g[NU], k[NU];
     if constexpr (kStaged) cp_async_wait<kStages - 1>();  // this lane's copies of the row
 #pragma unroll
@@ -179,24 +192,29 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
         if constexpr (SKIP) k[j] = unit.load((const char*)a.gres + row * pitch, c0);
       }
     }
-    F2 sx = f2(0.0f, 0.0f), sq = sx;
+    auto row_sums = [&](float sc) {
+      F2 s = f2(0.0f, 0.0f), q = s;
 #pragma unroll
-    for (int j = 0; j < NU; ++j) R::sums(x[j], g[j], w[j], a.offset, 1.0f, sx, sq);
+      for (int j = 0; j < NU; ++j) {
+        F2 w[P];
+        weights(j, w);
+        R::sums(x[j], g[j], w, sc, s, q);
+      }
+      return make_float2(__fadd_rn(s.x, s.y), __fadd_rn(q.x, q.y));
+    };
+    const float2 mine = row_sums(1.0f);
     // the stage has been read
     prefetch(row + kStages * step, s);
     s = s + 1 == kStages ? 0 : s + 1;
-    const float2 sums = t.combine<false>(
-        make_float2(warp_sum(__fadd_rn(sx.x, sx.y)), warp_sum(__fadd_rn(sq.x, sq.y))));
-    const RowStat st = row_stat(sums, a, [&](float sc) {
-      F2 s = f2(0.0f, 0.0f), q = s;
-#pragma unroll
-      for (int j = 0; j < NU; ++j) R::sums(x[j], g[j], w[j], a.offset, sc, s, q);
-      return t.combine<false>(
-          make_float2(warp_sum(__fadd_rn(s.x, s.y)), warp_sum(__fadd_rn(q.x, q.y))));
-    });
+    auto over_team = [&](float2 v) {
+      return t.combine<false>(make_float2(warp_sum(v.x), warp_sum(v.y)));
+    };
+    const RowStat st = row_stat(over_team(mine), a, [&](float sc) { return over_team(row_sums(sc)); });
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-      const Raw<16> o = R::grad(x[j], g[j], w[j], k[j], SKIP, a.offset, st, acc[j]);
+      F2 w[P];
+      weights(j, w);
+      const Raw<16> o = R::grad(x[j], g[j], w, k[j], SKIP, st, acc[j]);
       unit.store((char*)a.gx + row * pitch, (m + j * W) * U::COLS, o);
     }
   }
@@ -212,7 +230,7 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
 #pragma unroll
     for (int j = 0; j < NU; ++j) R::put(merged + team * a.D, unit, (m + j * W) * U::COLS, acc[j]);
     __syncthreads();
-    for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+    for (int c = team * blockDim.x + threadIdx.x; c < a.D; c += blockDim.x * teams) {
       float v = merged[c];
       for (int q = 1; q < teams; ++q) v = __fadd_rn(v, merged[q * a.D + c]);
       out[c] = v;
@@ -240,8 +258,9 @@ __global__ void __launch_bounds__(1024) grad_long_kernel(NormGradArgs a) {
       double2 v = make_double2(0.0, 0.0);
       for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
         F2 s = f2(0.0f, 0.0f), q = s;
-        R::sums(unit.load(xp, c0), unit.load(gp, c0),
-                unit.load_weight(a.w, c0), a.offset, sc, s, q);
+        F2 w[P];
+        R::weight(unit, a, c0, w);
+        R::sums(unit.load(xp, c0), unit.load(gp, c0), w, sc, s, q);
         v.x += (double)__fadd_rn(s.x, s.y);
         v.y += (double)__fadd_rn(q.x, q.y);
       }
@@ -269,9 +288,9 @@ __global__ void __launch_bounds__(1024) grad_long_kernel(NormGradArgs a) {
         acc[i] = f2(!first && out && c < a.D ? out[c] : 0.0f, !first && out && d < a.D ? out[d] : 0.0f);
       }
       const Raw<16> k = a.gres ? unit.load((const char*)a.gres + row * pitch, c0) : Raw<16>{};
-      const Raw<16> o = R::grad(unit.load(xp, c0), unit.load(gp, c0),
-                                unit.load_weight(a.w, c0), k, a.gres != nullptr, a.offset,
-                                st, acc);
+      F2 w[P];
+      R::weight(unit, a, c0, w);
+      const Raw<16> o = R::grad(unit.load(xp, c0), unit.load(gp, c0), w, k, a.gres != nullptr, st, acc);
       unit.store((char*)a.gx + row * pitch, c0, o);
       if (out) R::put(out, unit, c0, acc);
     }
@@ -305,20 +324,22 @@ cudaError_t launch_rows(const DeviceInfo& dev, NormGradArgs a, int64_t* ctas, cu
   auto team = [&](auto nu) -> cudaError_t {
     constexpr int NU = decltype(nu)::value;
     const auto kern = grad_team_kernel<T, LAYOUT, NU, SKIP>;
-    a.warps = (int)((units + NU - 1) / NU);
+    const int64_t warps = (units + NU - 1) / NU;
     // few rows: a CTA for each before a second team in any
     const int64_t teams = std::max<int64_t>(
-        1, std::min<int64_t>(kGradWarps<NU> / a.warps, (a.rows + dev.sm_count - 1) / dev.sm_count));
+        1, std::min<int64_t>(kGradWarps<NU> / warps, (a.rows + dev.sm_count - 1) / dev.sm_count));
     int64_t grid = std::min<int64_t>(dev.sm_count, (a.rows + teams - 1) / teams);
-    // PHASED: a team's rows have one offset when they are a multiple of 8 apart
+    // PHASED: a CTA's rows have one offset when they are a multiple of 8 apart
     if (LAYOUT == PHASED) grid = (grid + 7) / 8 * 8;
-    const int block = (int)teams * a.warps * 32;
-    const size_t stages = LAYOUT == NARROW ? 0 : (size_t)block * kStages * (SKIP ? 3 : 2) * NU * 16;
-    const size_t smem = std::max(stages, teams > 1 ? (size_t)teams * a.D * 4 : 0);
+    size_t smem = 0;
+    if (LAYOUT != NARROW)
+      smem = (size_t)warps * NU * 512 * (sizeof(T) == 2 ? 2 : 1) +
+             (size_t)warps * teams * NU * 512 * kStagesOf<NU> * (SKIP ? 3 : 2);
+    if (teams > 1) smem = std::max(smem, (size_t)teams * a.D * 4);
     static std::atomic<int> opted[kOptinDevices];
     cudaError_t e = allow_shared((const void*)kern, dev, opted);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)grid, block, smem, s>>>(a);
+    kern<<<(unsigned)grid, dim3((unsigned)warps * 32, (unsigned)teams), smem, s>>>(a);
     *ctas = grid;
     return cudaGetLastError();
   };
