@@ -2,7 +2,8 @@
 // stores and reductions shared by the weighted-norm kernels.
 //
 // A unit is 512 bytes of a row: 256 columns of a 16-bit type or 128 of fp32,
-// 16 bytes per lane, kept packed in a Raw<16>.  Three layouts:
+// 16 bytes per lane, kept packed in a Raw<16>.  A warp holds consecutive units
+// of a row.  Three layouts:
 //   WIDE     the rows are made of 16-byte granules.  Lane l holds granule l of
 //            the unit; a warp's access is 512 contiguous bytes.
 //   PHASED   the tensors start on 16-byte boundaries but the rows do not (an odd
@@ -11,8 +12,7 @@
 //            granule's first elements, and its last granule's last ones,
 //            belong to the neighbours: they read as zero and are not stored.
 //            Rows whose numbers differ by a multiple of EPL (elements per
-//            granule) have the same `off`, so a team that takes such rows loads
-//            its weights, at that offset, once.
+//            granule) have the same `off`.
 //   NARROW   a tensor that starts off a 16-byte boundary.  Lane l's element i is
 //            column 32 i + l, one element per access.
 // The arithmetic is the same for all three.  Columns past the row read as
@@ -46,6 +46,9 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// The units of one warp: `units` of them from unit `first` of the row.  j
+// counts them; e is the tensor's element index of the lane's first column
+// (at()), so that an access is one base address and a constant offset.
 template <class T, int LAYOUT>
 struct Unit {
   static constexpr int ES = (int)sizeof(T);
@@ -54,28 +57,32 @@ struct Unit {
   static constexpr int P = Granule<T>::P;   // fp32 pairs per lane
 
   int D, lane;
-  int off;    // PHASED: the row's offset from a granule's start, elements
-  bool last;  // PHASED: the tensors' last row: nothing past its end is read
+  int off;     // PHASED: the row's offset from a granule's start, elements
+  int c;       // the lane's first column (PHASED: negative in a granule shared with the row before)
+  bool edges;  // PHASED: the warp holds a granule shared with a neighbouring row
 
-  __device__ __forceinline__ Unit(int D, int lane) : D(D), lane(lane), off(0), last(false) {}
-  __device__ __forceinline__ void at_row(int64_t row, int64_t rows) {
+  // rows row, row + 8 k, ...
+  __device__ __forceinline__ Unit(int D, int lane, int first, int units, int64_t row)
+      : D(D), lane(lane), off(0), edges(false) {
+    if constexpr (LAYOUT == PHASED) off = (int)(((uint64_t)row * (uint64_t)(D % EPL)) % EPL);
+    c = first * COLS + (LAYOUT == NARROW ? lane : lane * EPL - off);
     if constexpr (LAYOUT == PHASED) {
-      off = (int)(((uint64_t)row * (uint64_t)(D % EPL)) % EPL);
-      last = row == rows - 1;
+      bool mine = false;
+      for (int j = 0; j < units; ++j) mine = mine || (valid(j) && !whole(j));
+      edges = __any_sync(0xFFFFFFFFu, mine);
     }
   }
-  // the column of this lane's element i in the unit that starts at column c0
-  // (PHASED: negative in a first granule shared with the row before)
-  __device__ __forceinline__ int col(int c0, int i) const {
-    return LAYOUT == NARROW ? c0 + i * 32 + lane : c0 + lane * EPL + i - off;
+  __device__ __forceinline__ int64_t at(int64_t row) const { return row * D + c; }
+  // the column of element i of unit j
+  __device__ __forceinline__ int col(int j, int i) const {
+    return c + j * COLS + (LAYOUT == NARROW ? i * 32 : i);
   }
-  // whether all of a lane's columns are the row's
-  __device__ __forceinline__ bool whole(int c) const { return c >= 0 && c + EPL <= D; }
-  __device__ __forceinline__ static void put(Raw<16>& r, int i, const Raw<ES>& e) {
-    if constexpr (ES == 4)
-      r.w[i] = e.w[0];
-    else
-      r.w[i >> 1] |= (uint32_t)e.h << (16 * (i & 1));
+  __device__ __forceinline__ bool valid(int j) const { return col(j, 0) < D; }
+  __device__ __forceinline__ bool whole(int j) const {
+    return LAYOUT == WIDE ? valid(j) : col(j, 0) >= 0 && col(j, 0) + EPL <= D;
+  }
+  __device__ __forceinline__ static const char* ptr(const void* tensor, int64_t e, int j) {
+    return (const char*)tensor + e * ES + j * (COLS * ES);
   }
   __device__ __forceinline__ static Raw<ES> get(const Raw<16>& r, int i) {
     Raw<ES> e;
@@ -86,114 +93,87 @@ struct Unit {
     return e;
   }
   template <bool STREAM>
-  __device__ __forceinline__ Raw<16> elements(const void* row, int c0) const {
+  __device__ __forceinline__ Raw<16> elements(const char* p, int j) const {
+    constexpr int S = LAYOUT == NARROW ? 32 * ES : ES;
     Raw<16> r = {};
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int c = col(c0, i);
-      if (c < 0 || c >= D) continue;
-      const char* p = (const char*)row + (int64_t)c * ES;
-      put(r, i, STREAM ? ld_stream<ES>(p) : ld_bcast<ES>(p));
-    }
-    return r;
-  }
-  // copy this lane's granule of row `row` of a tensor to its slot at shared
-  // address dst (cp.async; not NARROW)
-  __device__ __forceinline__ void copy(uint32_t dst, const void* tensor, int64_t row, int64_t rows,
-                                       int c0) const {
-    const int c = col(c0, 0);
-    if (c >= D) return;
-    const int64_t pitch = (int64_t)D * ES, at = row * pitch + (int64_t)c * ES;
-    // PHASED: the tensor's last granule may run past its end
-    if (LAYOUT == PHASED && row == rows - 1 && c + EPL > D)
-      cp_async16_part(dst, (const char*)tensor + at, (uint32_t)((D - c) * ES));
-    else
-      cp_async16(dst, (const char*)tensor + at);
-  }
-  // what copy() left in the slot
-  __device__ __forceinline__ Raw<16> copied(uint32_t src, int c0) const {
-    Raw<16> r = {};
-    const int c = col(c0, 0);
-    if (c < D) {
-      r = lds16(src);
-      if (LAYOUT == PHASED && !whole(c)) mask(r, c);
-    }
-    return r;
-  }
-  // PHASED: zero the neighbours' elements of a granule that starts at column c
-  __device__ __forceinline__ void mask(Raw<16>& r, int c) const {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      if (c + i >= 0 && c + i < D) continue;
+      if (col(j, i) < 0 || col(j, i) >= D) continue;
+      const Raw<ES> e = STREAM ? ld_stream<ES>(p + i * S) : ld_bcast<ES>(p + i * S);
       if constexpr (ES == 4)
-        r.w[i] = 0;
+        r.w[i] = e.w[0];
       else
-        r.w[i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+        r.w[i >> 1] |= (uint32_t)e.h << (16 * (i & 1));
     }
+    return r;
   }
-  // activations, read once
-  __device__ __forceinline__ Raw<16> load(const void* row, int c0) const {
+  // activations, read once (WIDE, NARROW)
+  __device__ __forceinline__ Raw<16> load(const void* tensor, int64_t e, int j) const {
+    static_assert(LAYOUT != PHASED, "PHASED rows are copied");
     if constexpr (LAYOUT == NARROW) {
-      return elements<true>(row, c0);
+      return elements<true>(ptr(tensor, e, j), j);
     } else {
       Raw<16> r = {};
-      const int c = col(c0, 0);
-      if (c < D) {
-        const char* p = (const char*)row + (int64_t)c * ES;
-        if (LAYOUT == WIDE || whole(c)) {
-          r = ld_stream<16>(p);
-        } else if (last && c + EPL > D) {
-          r = elements<true>(row, c0);
-        } else {
-          r = ld_stream<16>(p);
-          mask(r, c);
-        }
-      }
+      if (valid(j)) r = ld_stream<16>(ptr(tensor, e, j));
       return r;
     }
   }
   // weights, read by every row
-  __device__ __forceinline__ Raw<16> load_weight(const void* w, int c0) const {
+  __device__ __forceinline__ Raw<16> load_weight(const void* w, int j) const {
     if constexpr (LAYOUT != WIDE) {
-      return elements<false>(w, c0);
+      return elements<false>(ptr(w, c, j), j);
     } else {
       Raw<16> r = {};
-      if (col(c0, 0) < D) r = ld_bcast<16>((const char*)w + (int64_t)col(c0, 0) * ES);
+      if (valid(j)) r = ld_bcast<16>(ptr(w, c, j));
       return r;
     }
   }
-  __device__ __forceinline__ void store(void* row, int c0, const Raw<16>& r) const {
-    const int c = col(c0, 0);
-    if constexpr (LAYOUT == WIDE) {
-      if (c < D) st_stream<16>((char*)row + (int64_t)c * ES, r);
-    } else {
-      if (LAYOUT == PHASED && whole(c)) {
-        st_stream<16>((char*)row + (int64_t)c * ES, r);
-        return;
-      }
+  // Copy the lane's granule of unit j to its slot at shared address dst
+  // (cp.async; WIDE, PHASED): the row's bytes from the granule's start on, zeros after
+  // them, nothing past the row's end is read.
+  __device__ __forceinline__ void copy(uint32_t dst, const void* tensor, int64_t e, int j) const {
+    const int left = (D - col(j, 0)) * ES;
+    cp_async16_part(dst, ptr(tensor, e, j), (uint32_t)(left < 0 ? 0 : left > 16 ? 16 : left));
+  }
+  // what copy() left in the slot, without the row before
+  __device__ __forceinline__ Raw<16> copied(uint32_t src, int j) const {
+    Raw<16> r = lds16(src);
+    if (LAYOUT == PHASED && j == 0 && c < 0) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int k = col(c0, i);
-        if (k >= 0 && k < D) st_stream<ES>((char*)row + (int64_t)k * ES, get(r, i));
+      for (int i = 0; i < EPL - 1; ++i) {
+        if (i >= off) continue;
+        if constexpr (ES == 4)
+          r.w[i] = 0;
+        else
+          r.w[i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
       }
     }
+    return r;
+  }
+  __device__ __forceinline__ void store(void* tensor, int64_t e, int j, const Raw<16>& r) const {
+    char* p = (char*)ptr(tensor, e, j);
+    if constexpr (LAYOUT != NARROW) {
+      if (whole(j)) st_stream<16>(p, r);
+      if (LAYOUT == WIDE || !edges) return;
+    }
+    if (LAYOUT == PHASED && (whole(j) || !valid(j))) return;
+    constexpr int S = LAYOUT == NARROW ? 32 * ES : ES;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (col(j, i) >= 0 && col(j, i) < D) st_stream<ES>(p + i * S, get(r, i));
   }
   // one byte per element, element i in byte i of q
-  __device__ __forceinline__ void store8(void* row, int c0, const Raw<EPL>& q) const {
-    const int c = col(c0, 0);
-    if constexpr (LAYOUT == WIDE) {
-      if (c < D) st_stream<EPL>((char*)row + c, q);
-    } else {
-      if (LAYOUT == PHASED && whole(c)) {
-        st_stream<EPL>((char*)row + c, q);
-        return;
-      }
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int k = col(c0, i);
-        if (k >= 0 && k < D) ((uint8_t*)row)[k] = (uint8_t)(q.w[i >> 2] >> (8 * (i & 3)));
-      }
+  __device__ __forceinline__ void store8(void* tensor, int64_t e, int j, const Raw<EPL>& q) const {
+    char* p = (char*)tensor + e + j * COLS;
+    if constexpr (LAYOUT != NARROW) {
+      if (whole(j)) st_stream<EPL>(p, q);
+      if (LAYOUT == WIDE || !edges) return;
     }
+    if (LAYOUT == PHASED && (whole(j) || !valid(j))) return;
+    constexpr int S = LAYOUT == NARROW ? 32 : 1;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (col(j, i) >= 0 && col(j, i) < D) p[i * S] = (char)(q.w[i >> 2] >> (8 * (i & 3)));
   }
 };
 
@@ -272,26 +252,27 @@ int64_t row_units(int64_t D) {
   return (D + (LAYOUT == PHASED ? U::EPL - 1 : 0) + U::COLS - 1) / U::COLS;
 }
 
-// The weight, offset added, in shared memory as fp32 for rows at `unit`'s
-// offset: plane q of granule g (of ngr) holds columns 4q .. 4q + 3 of it, so a
-// warp reads 512 contiguous bytes of a plane.  Columns outside the row are zero.
+// The weight, offset added, in shared memory as fp32 for rows at offset `off`
+// from a granule: plane q of granule g (of ngr) holds columns 4q .. 4q + 3 of
+// it, so a warp reads 512 contiguous bytes of a plane.  Columns outside the
+// row are zero.
 template <class T, int LAYOUT>
-__device__ __forceinline__ void stage_weight(float4* planes, int ngr, Unit<T, LAYOUT> unit,
+__device__ __forceinline__ void stage_weight(float4* planes, int ngr, int D, int64_t row,
                                              const void* weight, float offset) {
   using U = Unit<T, LAYOUT>;
   const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+  const U start(D, 0, 0, 0, row);
   for (int g = tid; g < ngr; g += blockDim.x * blockDim.y) {
-    // granule g of the row: lane 0's of a unit that starts there
-    unit.lane = 0;
-    const int c0 = g * U::EPL;
+    U unit = start;
+    unit.c += g * U::EPL;
     F2 f[U::P];
-    Granule<T>::widen(unit.load_weight(weight, c0), f);
+    Granule<T>::widen(unit.load_weight(weight, 0), f);
 #pragma unroll
     for (int i = 0; i < U::P; ++i) {
       f[i] = f2_add(f2(offset, offset), f[i]);
-      const int c = unit.col(c0, 2 * i), d = unit.col(c0, 2 * i + 1);
-      if (c < 0 || c >= unit.D) f[i].x = 0.0f;
-      if (d < 0 || d >= unit.D) f[i].y = 0.0f;
+      const int c = unit.col(0, 2 * i), d = unit.col(0, 2 * i + 1);
+      if (c < 0 || c >= D) f[i].x = 0.0f;
+      if (d < 0 || d >= D) f[i].y = 0.0f;
     }
 #pragma unroll
     for (int q = 0; q < U::P / 2; ++q)

@@ -102,10 +102,10 @@ struct NormRow {
     for (int i = 0; i < P; ++i) t[i] = f2_mul(t[i], w[i]);
   }
   // columns outside the row hold zero; where r is not finite they became NaN
-  __device__ __forceinline__ static void mask(F2 (&y)[P], const U& unit, int c0) {
+  __device__ __forceinline__ static void mask(F2 (&y)[P], const U& unit, int j) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int c = unit.col(c0, 2 * i), d = unit.col(c0, 2 * i + 1);
+      const int c = unit.col(j, 2 * i), d = unit.col(j, 2 * i + 1);
       if (c < 0 || c >= unit.D) y[i].x = 0.0f;
       if (d < 0 || d >= unit.D) y[i].y = 0.0f;
     }
@@ -143,11 +143,11 @@ struct NormRow {
     }
   }
 
-  // one unit of the output, one scale per 128 columns (the whole warp calls;
-  // a group lies inside the unit)
+  // unit j of the output, one scale per 128 columns (the whole warp calls;
+  // k: the group of this lane's first column; its groups lie inside the unit)
   __device__ __forceinline__ static void emit_groups(const NormArgs& a, const U& unit, int64_t row,
-                                                     int c0, const Raw<16>& x, const F2 (&w)[P],
-                                                     float S, float r) {
+                                                     int64_t e, int j, int k, const Raw<16>& x,
+                                                     const F2 (&w)[P], float S, float r) {
     F2 v[P];
     weighted(x, w, v);
     float m[NG];
@@ -162,7 +162,7 @@ struct NormRow {
     if (__any_sync(0xFFFFFFFFu, slow)) {  // rare
       F2 y[P];
       normed(x, w, r, y);
-      mask(y, unit, c0);
+      mask(y, unit, j);
       group_max(y, m);
       if (slow) {
 #pragma unroll
@@ -174,14 +174,11 @@ struct NormRow {
         }
       }
     }
-    unit.store8((char*)a.out + row * a.D, c0, codes(v, q));
-    const int first = LAYOUT == NARROW ? c0 : c0 + unit.lane / LANES * 128;
+    unit.store8(a.out, e, j, codes(v, q));
     if (unit.lane % LANES == 0) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const int k = first / 128 + g;
-        if (k < a.groups) a.scales[row * a.groups + k] = q[g].scale;
-      }
+      for (int g = 0; g < NG; ++g)
+        if (k + g < a.groups) a.scales[row * a.groups + k + g] = q[g].scale;
     }
   }
 
@@ -226,13 +223,13 @@ __device__ __forceinline__ float inverse_rms(float S, const NormArgs& a, Again a
   return fast_inverse_rms_scaled(again(sc), sc, a.d_f, a.inv_d, a.eps);
 }
 
-// One row held by a team: its statistic, then its output.  x: the lane's
-// granules; weights(j, wf): unit j's weights, offset added; after_read(): called once the sums
+// One row held by a team: its statistic, then its output.  e: unit.at(row);
+// x: the lane's granules; weights(j, wf): unit j's weights, offset added; after_read(): called once the sums
 // have been formed (the caller's next copies).  kSplit: PHASED groups of 128, whose
 // pieces go through `pieces`, [2][groups of the team's warps].
 template <class T, int LAYOUT, int NU, int Q8, class Weights, class AfterRead>
 __device__ __forceinline__ void finish_row(const NormArgs& a, const Unit<T, LAYOUT>& unit, Team& t,
-                                           int64_t row, const Raw<16> (&x)[NU], Weights weights,
+                                           int64_t row, int64_t e, const Raw<16> (&x)[NU], Weights weights,
                                            AfterRead after_read, float2* pieces) {
   using R = NormRow<T, LAYOUT>;
   using U = Unit<T, LAYOUT>;
@@ -240,7 +237,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Unit<T, LAYO
   constexpr bool kSplit = LAYOUT == PHASED && Q8 == 2;
   const int m = t.m, W = t.warps, lane = t.lane;
   const int n = W * NU * R::BLOCKS;  // groups of 128 the team's units reach
-  auto piece = [&](int j) { return (m + j * W) * R::BLOCKS + lane / R::LANES; };
+  auto piece = [&](int j) { return (m * NU + j) * R::BLOCKS + lane / R::LANES; };
 
   F2 acc[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
   float big = 0.0f;
@@ -293,14 +290,14 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Unit<T, LAYO
       F2 wf[P], y[P];
       weights(j, wf);
       R::normed(x[j], wf, r, y);
-      unit.store((char*)a.out + row * ((int64_t)a.D * U::ES), (m + j * W) * U::COLS, Granule<T>::narrow(y));
+      unit.store(a.out, e, j, Granule<T>::narrow(y));
     }
   } else if constexpr (Q8 == 2 && !kSplit) {
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
       F2 wf[P];
       weights(j, wf);
-      R::emit_groups(a, unit, row, (m + j * W) * U::COLS, x[j], wf, red.x, r);
+      R::emit_groups(a, unit, row, e, j, piece(j), x[j], wf, red.x, r);
     }
   } else if constexpr (!kSplit) {
     // one scale per row
@@ -313,7 +310,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Unit<T, LAYO
         F2 wf[P], v[P];
         weights(j, wf);
         values(x[j], wf, v);
-        unit.store8((char*)a.out + row * a.D, (m + j * W) * U::COLS, R::codes(v, all));
+        unit.store8(a.out, e, j, R::codes(v, all));
       }
       if (m == 0 && lane == 0) a.scales[row] = q.scale;
     };
@@ -327,7 +324,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Unit<T, LAYO
         F2 wf[P], y[P];
         weights(j, wf);
         R::normed(x[j], wf, r, y);
-        R::mask(y, unit, (m + j * W) * U::COLS);
+        R::mask(y, unit, j);
         my = max_nan(my, R::max_of(y));
       }
       my = t.combine<true>(make_float2(0.0f, warp_max(my))).y;
@@ -345,7 +342,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Unit<T, LAYO
       weights(j, wf);
       if (slow) {
         R::normed(x[j], wf, r, v);
-        R::mask(v, unit, (m + j * W) * U::COLS);
+        R::mask(v, unit, j);
       } else {
         R::weighted(x[j], wf, v);
       }
@@ -385,8 +382,7 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Unit<T, LAYO
         mine = quant_of_t(big, r);
         before = quant_of_t(prev, r);
       }
-      unit.store8((char*)a.out + row * a.D, (m + j * W) * U::COLS,
-                  R::split_codes(v, cut, before.mul, mine.mul));
+      unit.store8(a.out, e, j, R::split_codes(v, cut, before.mul, mine.mul));
       if (lane % R::LANES == 0 && k < a.groups) a.scales[row * a.groups + k] = mine.scale;
     }
     if (W == 1) {
@@ -404,28 +400,27 @@ __global__ void __launch_bounds__(kTeamThreads, 2) norm_direct_kernel(NormArgs a
   using U = typename R::U;
   __shared__ float2 slots[2 * kTeamWarps];
   Team t(slots);
-  const U unit(a.D, t.lane);
-  const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
+  const U unit(a.D, t.lane, t.m * NU, NU, 0);
   for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < a.rows;
        row += (int64_t)gridDim.x * blockDim.y) {
+    const int64_t e = unit.at(row);
     Raw<16> x[NU], u[NU], w[NU];
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-      const int c0 = (t.m + j * t.warps) * U::COLS;
-      x[j] = unit.load((const char*)a.x + row * pitch, c0);
-      if constexpr (ADD) u[j] = unit.load((const char*)a.u + row * pitch, c0);
+      x[j] = unit.load(a.x, e, j);
+      if constexpr (ADD) u[j] = unit.load(a.u, e, j);
     }
 #pragma unroll
-    for (int j = 0; j < NU; ++j) w[j] = unit.load_weight(a.w, (t.m + j * t.warps) * U::COLS);
+    for (int j = 0; j < NU; ++j) w[j] = unit.load_weight(a.w, j);
     if constexpr (ADD) {
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
         x[j] = R::add(x[j], u[j]);
-        unit.store((char*)a.res + row * pitch, (t.m + j * t.warps) * U::COLS, x[j]);
+        unit.store(a.res, e, j, x[j]);
       }
     }
     finish_row<T, LAYOUT, NU, Q8>(
-        a, unit, t, row, x, [&](int j, F2(&wf)[U::P]) { R::weight(w[j], a.offset, wf); }, [] {},
+        a, unit, t, row, e, x, [&](int j, F2(&wf)[U::P]) { R::weight(w[j], a.offset, wf); }, [] {},
         nullptr);
   }
 }
@@ -449,47 +444,42 @@ __global__ void __launch_bounds__(kTeamThreads, 2) norm_staged_kernel(NormArgs a
   extern __shared__ float4 shared[];  // weights, then [warps][streams][NU][32]
   Team t(slots);
   const int W = t.warps, m = t.m;
-  U unit(a.D, t.lane);
-  unit.at_row(blockIdx.x, a.rows);
+  const U unit(a.D, t.lane, m * NU, NU, blockIdx.x);
   const int ngr = W * NU * 32;  // granules of a row, padded
-  const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   int64_t row = blockIdx.x + (int64_t)gridDim.x * threadIdx.y;
   const uint32_t stage = smem_addr(shared + ngr * (U::P / 2)) +
                          (threadIdx.y * W + m) * (NS * NU * kSlot) + t.lane * 16;
   auto prefetch = [&](int64_t r) {
-    if (r >= a.rows) return;
+    if (r < a.rows) {
+      const int64_t e = unit.at(r);
 #pragma unroll
-    for (int j = 0; j < NU; ++j) {
-      const int c0 = (m + j * W) * U::COLS;
-      unit.copy(stage + j * kSlot, a.x, r, a.rows, c0);
-      if constexpr (ADD) unit.copy(stage + (NU + j) * kSlot, a.u, r, a.rows, c0);
+      for (int j = 0; j < NU; ++j) {
+        unit.copy(stage + j * kSlot, a.x, e, j);
+        if constexpr (ADD) unit.copy(stage + (NU + j) * kSlot, a.u, e, j);
+      }
     }
+    cp_async_commit();
   };
   prefetch(row);
-  cp_async_commit();
-  stage_weight<T, LAYOUT>(shared, ngr, unit, a.w, a.offset);
+  stage_weight<T, LAYOUT>(shared, ngr, a.D, blockIdx.x, a.w, a.offset);
   __syncthreads();
   for (; row < a.rows; row += step) {
+    const int64_t e = unit.at(row);
     cp_async_wait<0>();  // this lane's copies of the row
     Raw<16> x[NU];
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-      const int c0 = (m + j * W) * U::COLS;
-      x[j] = unit.copied(stage + j * kSlot, c0);
+      x[j] = unit.copied(stage + j * kSlot, j);
       if constexpr (ADD) {
-        x[j] = R::add(x[j], unit.copied(stage + (NU + j) * kSlot, c0));
-        unit.store((char*)a.res + row * pitch, c0, x[j]);
+        x[j] = R::add(x[j], unit.copied(stage + (NU + j) * kSlot, j));
+        unit.store(a.res, e, j, x[j]);
       }
     }
     finish_row<T, LAYOUT, NU, Q8>(
-        a, unit, t, row, x,
-        [&](int j, F2(&wf)[U::P]) { staged_weight<T>(shared, ngr, (m + j * W) * 32 + t.lane, wf); },
-        [&] {
-          prefetch(row + step);
-          cp_async_commit();
-        },
-        pieces + threadIdx.y * (2 * W * NU * R::BLOCKS));
+        a, unit, t, row, e, x,
+        [&](int j, F2(&wf)[U::P]) { staged_weight<T>(shared, ngr, (m * NU + j) * 32 + t.lane, wf); },
+        [&] { prefetch(row + step); }, pieces + threadIdx.y * (2 * W * NU * R::BLOCKS));
   }
 }
 
@@ -506,18 +496,19 @@ __global__ void __launch_bounds__(kTeamThreads) norm_long_kernel(NormArgs a) {
   __shared__ double sums[kTeamWarps];
   Team t(slots);
   const int lane = t.lane, warp = t.m, W = t.warps;
-  const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
-  const U unit(a.D, lane);
+  const U unit(a.D, lane, warp, 1, 0);  // units warp, warp + W, ...
+  const int units = (a.D + U::COLS - 1) / U::COLS - warp;  // from this warp's first
 
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const char* src = (const char*)(ADD ? a.res : a.x) + row * pitch;
+    const void* src = ADD ? a.res : a.x;
+    const int64_t e = unit.at(row);
     double total = 0.0;
     float big = 0.0f;
-    for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
-      Raw<16> x = unit.load((const char*)a.x + row * pitch, c0);
+    for (int j = 0; j < units; j += W) {
+      Raw<16> x = unit.load(a.x, e, j);
       if constexpr (ADD) {
-        x = R::add(x, unit.load((const char*)a.u + row * pitch, c0));
-        unit.store((char*)a.res + row * pitch, c0, x);
+        x = R::add(x, unit.load(a.u, e, j));
+        unit.store(a.res, e, j, x);
       }
       F2 f[P];
       Granule<T>::widen(x, f);
@@ -527,7 +518,7 @@ __global__ void __launch_bounds__(kTeamThreads) norm_long_kernel(NormArgs a) {
       total += (double)__fadd_rn(acc.x, acc.y);
       if constexpr (Q8 == 1) {
         F2 wf[P], v[P];
-        R::weight(unit.load_weight(a.w, c0), a.offset, wf);
+        R::weight(unit.load_weight(a.w, j), a.offset, wf);
         R::weighted(x, wf, v);
         big = max_nan(big, R::max_of(v));
       }
@@ -543,9 +534,9 @@ __global__ void __launch_bounds__(kTeamThreads) norm_long_kernel(NormArgs a) {
     const float S = (float)total;
     const float r = inverse_rms(S, a, [&](float sc) {
       double s2 = 0.0;
-      for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
+      for (int j = 0; j < units; j += W) {
         F2 f[P];
-        Granule<T>::widen(unit.load(src, c0), f);
+        Granule<T>::widen(unit.load(src, e, j), f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const double u0 = (double)__fmul_rn(f2_lo(f[i]), sc), u1 = (double)__fmul_rn(f2_hi(f[i]), sc);
@@ -569,11 +560,11 @@ __global__ void __launch_bounds__(kTeamThreads) norm_long_kernel(NormArgs a) {
       slow = !usable(S) || (big != 0.0f && !usable(big));
       if (slow) {
         float my = 0.0f;
-        for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
+        for (int j = 0; j < units; j += W) {
           F2 wf[P], y[P];
-          R::weight(unit.load_weight(a.w, c0), a.offset, wf);
-          R::normed(unit.load(src, c0), wf, r, y);
-          R::mask(y, unit, c0);
+          R::weight(unit.load_weight(a.w, j), a.offset, wf);
+          R::normed(unit.load(src, e, j), wf, r, y);
+          R::mask(y, unit, j);
           my = max_nan(my, R::max_of(y));
         }
         my = t.combine<true>(make_float2(0.0f, warp_max(my))).y;
@@ -586,12 +577,12 @@ __global__ void __launch_bounds__(kTeamThreads) norm_long_kernel(NormArgs a) {
       for (int g = 1; g < R::NG; ++g) q[g] = q[0];
       if (threadIdx.x == 0) a.scales[row] = q[0].scale;
     }
-    for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
-      const Raw<16> x = unit.load(src, c0);
+    for (int j = 0; j < units; j += W) {
+      const Raw<16> x = unit.load(src, e, j);
       F2 wf[P], v[P];
-      R::weight(unit.load_weight(a.w, c0), a.offset, wf);
+      R::weight(unit.load_weight(a.w, j), a.offset, wf);
       if constexpr (Q8 == 2) {
-        R::emit_groups(a, unit, row, c0, x, wf, S, r);
+        R::emit_groups(a, unit, row, e, j, (warp + j) * R::BLOCKS + lane / R::LANES, x, wf, S, r);
       } else {
         if (Q8 == 0 || slow)
           R::normed(x, wf, r, v);
@@ -599,9 +590,9 @@ __global__ void __launch_bounds__(kTeamThreads) norm_long_kernel(NormArgs a) {
           R::weighted(x, wf, v);
         if (slow) R::scale_by(v, small);
         if constexpr (Q8 == 0)
-          unit.store((char*)a.out + row * pitch, c0, Granule<T>::narrow(v));
+          unit.store(a.out, e, j, Granule<T>::narrow(v));
         else
-          unit.store8((char*)a.out + row * a.D, c0, R::codes(v, q));
+          unit.store8(a.out, e, j, R::codes(v, q));
       }
     }
   }

@@ -52,9 +52,9 @@ struct GradRow {
   using U = Unit<T, LAYOUT>;
   static constexpr int P = U::P;
   // a unit's weights from global memory, offset added
-  __device__ __forceinline__ static void weight(const U& unit, const NormGradArgs& a, int c0,
+  __device__ __forceinline__ static void weight(const U& unit, const NormGradArgs& a, int j,
                                                 F2 (&w)[P]) {
-    Granule<T>::widen(unit.load_weight(a.w, c0), w);
+    Granule<T>::widen(unit.load_weight(a.w, j), w);
 #pragma unroll
     for (int i = 0; i < P; ++i) w[i] = f2_add(f2(a.offset, a.offset), w[i]);
   }
@@ -97,10 +97,10 @@ struct GradRow {
     return Granule<T>::narrow(o);
   }
   // a lane's elements of one unit of fp32 columns (partial sums)
-  __device__ __forceinline__ static void put(float* row, const U& unit, int c0, const F2 (&v)[P]) {
+  __device__ __forceinline__ static void put(float* row, const U& unit, int j, const F2 (&v)[P]) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int c = unit.col(c0, 2 * i), d = unit.col(c0, 2 * i + 1);
+      const int c = unit.col(j, 2 * i), d = unit.col(j, 2 * i + 1);
       if (c >= 0 && c < unit.D) row[c] = v[i].x;
       if (d >= 0 && d < unit.D) row[d] = v[i].y;
     }
@@ -132,25 +132,23 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
   Team t(slots);
   const int lane = t.lane, W = t.warps, m = t.m, team = threadIdx.y, teams = blockDim.y;
   const int ngr = W * NU * 32;  // granules of a row, padded
-  const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
   const int64_t step = (int64_t)gridDim.x * teams;
   const uint32_t stage0 =
       smem_addr(shared + ngr * (P / 2)) + (team * W + m) * (kStages * kStage) + lane * 16;
 
   int64_t row = blockIdx.x + (int64_t)gridDim.x * team;
-  U unit(a.D, lane);
-  unit.at_row(blockIdx.x, a.rows);
+  const U unit(a.D, lane, m * NU, NU, blockIdx.x);
   // this warp's part of row r, into stage s (an empty group past the end)
   auto prefetch = [&](int64_t r, int s) {
     if constexpr (kStaged) {
       if (r < a.rows) {
+        const int64_t e = unit.at(r);
 #pragma unroll
         for (int j = 0; j < NU; ++j) {
-          const int c0 = (m + j * W) * U::COLS;
           const uint32_t dst = stage0 + s * kStage + j * kSlot;
-          unit.copy(dst, a.x, r, a.rows, c0);
-          unit.copy(dst + NU * kSlot, a.g, r, a.rows, c0);
-          if constexpr (SKIP) unit.copy(dst + 2 * NU * kSlot, a.gres, r, a.rows, c0);
+          unit.copy(dst, a.x, e, j);
+          unit.copy(dst + NU * kSlot, a.g, e, j);
+          if constexpr (SKIP) unit.copy(dst + 2 * NU * kSlot, a.gres, e, j);
         }
       }
       cp_async_commit();
@@ -161,9 +159,9 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
 
   auto weights = [&](int j, F2(&w)[P]) {
     if constexpr (kStaged)
-      staged_weight<T>(shared, ngr, (m + j * W) * 32 + lane, w);
+      staged_weight<T>(shared, ngr, (m * NU + j) * 32 + lane, w);
     else
-      R::weight(unit, a, (m + j * W) * U::COLS, w);
+      R::weight(unit, a, j, w);
   };
   F2 acc[NU][P];
 #pragma unroll
@@ -171,25 +169,25 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
 #pragma unroll
     for (int i = 0; i < P; ++i) acc[j][i] = f2(0.0f, 0.0f);
   if constexpr (kStaged) {
-    stage_weight<T, LAYOUT>(shared, ngr, unit, a.w, a.offset);
+    stage_weight<T, LAYOUT>(shared, ngr, a.D, blockIdx.x, a.w, a.offset);
     __syncthreads();
   }
   int s = 0;
   for (; row < a.rows; row += step) {
+    const int64_t e = unit.at(row);
     Raw<16> x[NU], g[NU], k[NU];
     if constexpr (kStaged) cp_async_wait<kStages - 1>();  // this lane's copies of the row
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-      const int c0 = (m + j * W) * U::COLS;
       if constexpr (kStaged) {
         const uint32_t at = stage0 + s * kStage + j * kSlot;
-        x[j] = unit.copied(at, c0);
-        g[j] = unit.copied(at + NU * kSlot, c0);
-        if constexpr (SKIP) k[j] = unit.copied(at + 2 * NU * kSlot, c0);
+        x[j] = unit.copied(at, j);
+        g[j] = unit.copied(at + NU * kSlot, j);
+        if constexpr (SKIP) k[j] = unit.copied(at + 2 * NU * kSlot, j);
       } else {
-        x[j] = unit.load((const char*)a.x + row * pitch, c0);
-        g[j] = unit.load((const char*)a.g + row * pitch, c0);
-        if constexpr (SKIP) k[j] = unit.load((const char*)a.gres + row * pitch, c0);
+        x[j] = unit.load(a.x, e, j);
+        g[j] = unit.load(a.g, e, j);
+        if constexpr (SKIP) k[j] = unit.load(a.gres, e, j);
       }
     }
     auto row_sums = [&](float sc) {
@@ -215,20 +213,20 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
       F2 w[P];
       weights(j, w);
       const Raw<16> o = R::grad(x[j], g[j], w, k[j], SKIP, st, acc[j]);
-      unit.store((char*)a.gx + row * pitch, (m + j * W) * U::COLS, o);
+      unit.store(a.gx, e, j, o);
     }
   }
   if (!a.partial) return;
   float* out = a.partial + (int64_t)blockIdx.x * a.D;
   if (teams == 1) {
 #pragma unroll
-    for (int j = 0; j < NU; ++j) R::put(out, unit, (m + j * W) * U::COLS, acc[j]);
+    for (int j = 0; j < NU; ++j) R::put(out, unit, j, acc[j]);
   } else {
     if constexpr (kStaged) cp_async_wait<0>();
     __syncthreads();  // the stages are no longer read or written
     float* merged = (float*)shared;  // [teams][D]
 #pragma unroll
-    for (int j = 0; j < NU; ++j) R::put(merged + team * a.D, unit, (m + j * W) * U::COLS, acc[j]);
+    for (int j = 0; j < NU; ++j) R::put(merged + team * a.D, unit, j, acc[j]);
     __syncthreads();
     for (int c = team * blockDim.x + threadIdx.x; c < a.D; c += blockDim.x * teams) {
       float v = merged[c];
@@ -247,20 +245,19 @@ __global__ void __launch_bounds__(1024) grad_long_kernel(NormGradArgs a) {
   constexpr int P = U::P;
   __shared__ double2 part[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
-  const int64_t pitch = (int64_t)a.D * (int)sizeof(T);
-  const U unit(a.D, lane);
+  const U unit(a.D, lane, warp, 1, 0);  // units warp, warp + W, ...
+  const int units = (a.D + U::COLS - 1) / U::COLS - warp;  // from this warp's first
   float* out = a.partial ? a.partial + (int64_t)blockIdx.x * a.D : nullptr;
   bool first = true;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, first = false) {
-    const char* xp = (const char*)a.x + row * pitch;
-    const char* gp = (const char*)a.g + row * pitch;
+    const int64_t e = unit.at(row);
     auto sums = [&](float sc) {
       double2 v = make_double2(0.0, 0.0);
-      for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
+      for (int j = 0; j < units; j += W) {
         F2 s = f2(0.0f, 0.0f), q = s;
         F2 w[P];
-        R::weight(unit, a, c0, w);
-        R::sums(unit.load(xp, c0), unit.load(gp, c0), w, sc, s, q);
+        R::weight(unit, a, j, w);
+        R::sums(unit.load(a.x, e, j), unit.load(a.g, e, j), w, sc, s, q);
         v.x += (double)__fadd_rn(s.x, s.y);
         v.y += (double)__fadd_rn(q.x, q.y);
       }
@@ -280,19 +277,19 @@ __global__ void __launch_bounds__(1024) grad_long_kernel(NormGradArgs a) {
       return make_float2((float)v.x, (float)v.y);
     };
     const RowStat st = row_stat(sums(1.0f), a, sums);
-    for (int c0 = warp * U::COLS; c0 < a.D; c0 += W * U::COLS) {
+    for (int j = 0; j < units; j += W) {
       F2 acc[P];
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        const int c = unit.col(c0, 2 * i), d = unit.col(c0, 2 * i + 1);
+        const int c = unit.col(j, 2 * i), d = unit.col(j, 2 * i + 1);
         acc[i] = f2(!first && out && c < a.D ? out[c] : 0.0f, !first && out && d < a.D ? out[d] : 0.0f);
       }
-      const Raw<16> k = a.gres ? unit.load((const char*)a.gres + row * pitch, c0) : Raw<16>{};
+      const Raw<16> k = a.gres ? unit.load(a.gres, e, j) : Raw<16>{};
       F2 w[P];
-      R::weight(unit, a, c0, w);
-      const Raw<16> o = R::grad(unit.load(xp, c0), unit.load(gp, c0), w, k, a.gres != nullptr, st, acc);
-      unit.store((char*)a.gx + row * pitch, c0, o);
-      if (out) R::put(out, unit, c0, acc);
+      R::weight(unit, a, j, w);
+      const Raw<16> o = R::grad(unit.load(a.x, e, j), unit.load(a.g, e, j), w, k, a.gres != nullptr, st, acc);
+      unit.store(a.gx, e, j, o);
+      if (out) R::put(out, unit, j, acc);
     }
   }
 }
