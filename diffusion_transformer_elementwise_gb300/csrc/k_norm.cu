@@ -27,9 +27,6 @@
 #include "dit_token.h"
 #include "dit_unit.cuh"
 
-#ifndef DIT_NORM_STAGED
-#define DIT_NORM_STAGED 64
-#endif
 namespace dit {
 namespace {
 
@@ -630,9 +627,14 @@ template <class T, int LAYOUT, bool ADD, int Q8>
 cudaError_t launch(const DeviceInfo& dev, const NormArgs& a, cudaStream_t s) {
   const int64_t units = row_units<T, LAYOUT>(a.D);
   if constexpr (LAYOUT != NARROW) {
-    // PHASED rows, and WIDE ones of more than a few for each SM
-    const bool staged = LAYOUT == PHASED || a.rows * units > DIT_NORM_STAGED * (int64_t)dev.sm_count ||
-                        units > 2 * kTeamWarps;
+    // PHASED rows; WIDE ones beyond 64 units per SM (bf16, L2-resident below:
+    // [1216,2048] 3.6 us direct, 3.3 staged; [608,2048] 2.4 and 2.6;
+    // [32768,1024] 37.9 and 19.6), but not the plain output with an update on rows of
+    // more than 4 KB ([8192,4096] 41.2 us direct, 45.8 staged; [16384,2048]
+    // 51.1 and 44.9); rows that direct CTAs do not hold
+    const bool many = a.rows * units > 64 * (int64_t)dev.sm_count;
+    const bool staged = LAYOUT == PHASED || units > 2 * kTeamWarps ||
+                        (many && !(ADD && Q8 == 0 && units > 8));
     if (staged && units <= 4 * kTeamWarps) {
       if (units == 1) return launch_staged<T, LAYOUT, 1, ADD, Q8>(dev, a, units, s);
       if (units == 2) return launch_staged<T, LAYOUT, 2, ADD, Q8>(dev, a, units, s);
