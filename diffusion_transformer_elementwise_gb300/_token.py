@@ -65,6 +65,8 @@ def _workspace(given, nbytes, ref, stream):
     """(tensor, address, size) of the caller's workspace, or of a new one."""
     if nbytes < 0:
         raise ValueError("sizes out of range")
+    if nbytes == 0:
+        return None, None, 0
     if given is None:
         given = _empty((nbytes,), torch.uint8, ref.device, stream)
     else:

@@ -70,10 +70,14 @@ struct EmbedGradArgs {
   int D;
   bool ids64;
   float scale;
-  // workspace: two buffers of (key, position) pairs, and the partial rows
+  // workspace (more than kFewTokens tokens): two buffers of (key, position)
+  // pairs, the list of runs that cross segments, and the partial rows
   uint2* pairs[2];
+  uint32_t* runs;    // a count, then at most `segments` entries
   float* partial;    // [segments][2][D]
 };
+// up to this many tokens the gradient takes one launch and no workspace
+constexpr int kFewTokens = 256;
 // sorted tokens per segment, and segments of a call
 constexpr int kEmbedSegment = 32;
 inline int64_t embed_segments(int64_t tokens) { return (tokens + kEmbedSegment - 1) / kEmbedSegment; }

@@ -240,9 +240,12 @@ dit_status dit_embedding(void* out, const void* ids, const void* table, int64_t 
 int64_t dit_embedding_backward_workspace_bytes(int64_t tokens, int64_t D) {
   int64_t n, m;
   if (!row_shape(tokens, D, 4, &n)) return -1;
-  // two buffers of (key, position) pairs, two partial rows per segment
-  if (__builtin_mul_overflow(dit::embed_segments(tokens) * 2, D * 4, &m)) return -1;
-  return 2 * round_up(tokens * 8) + round_up(m);
+  if (tokens <= dit::kFewTokens) return 0;
+  // two buffers of (key, position) pairs, the list of runs that cross
+  // segments, two partial rows per segment
+  const int64_t segments = dit::embed_segments(tokens);
+  if (__builtin_mul_overflow(segments * 2, D * 4, &m)) return -1;
+  return 2 * round_up(tokens * 8) + round_up((segments + 1) * 4) + round_up(m);
 }
 
 dit_status dit_embedding_backward(void* grad_table, const void* grad_out, const void* ids,
@@ -261,11 +264,11 @@ dit_status dit_embedding_backward(void* grad_table, const void* grad_out, const 
     return DIT_ERR_MISALIGNED;
   const int64_t need = dit_embedding_backward_workspace_bytes(tokens, D);
   if (need < 0) return DIT_ERR_BAD_SHAPE;
-  if (tokens > 0) {
+  if (need > 0) {
     const dit_status st = workspace_status(workspace, workspace_bytes, need);
     if (st != DIT_OK) return st;
   }
-  const Span so = span(grad_table, nt * es), ws = span(workspace, tokens > 0 ? need : 0);
+  const Span so = span(grad_table, nt * es), ws = span(workspace, need);
   const Span sg = span(grad_out, n * es), si = span(ids, tokens * is);
   if (overlaps(so, ws) || overlaps(so, sg) || overlaps(so, si) || overlaps(ws, sg) ||
       overlaps(ws, si))
@@ -281,10 +284,13 @@ dit_status dit_embedding_backward(void* grad_table, const void* grad_out, const 
   a.D = (int)D;
   a.ids64 = id_type == DIT_INT64;
   a.scale = scale;
-  char* w = (char*)workspace;
-  a.pairs[0] = (uint2*)w;
-  a.pairs[1] = (uint2*)(w + round_up(tokens * 8));
-  a.partial = (float*)(w + 2 * round_up(tokens * 8));
+  if (need > 0) {
+    char* w = (char*)workspace;
+    a.pairs[0] = (uint2*)w;
+    a.pairs[1] = (uint2*)(w += round_up(tokens * 8));
+    a.runs = (uint32_t*)(w += round_up(tokens * 8));
+    a.partial = (float*)(w + round_up((dit::embed_segments(tokens) + 1) * 4));
+  }
   const bool wide = wide_rows((uintptr_t)grad_table | (uintptr_t)grad_out, D * es);
   return launch_status(dit::launch_embedding_grad(dev, dtype, wide, a, (cudaStream_t)stream));
 }

@@ -8,15 +8,17 @@
 //
 // The gradient sorts the tokens first: a stable radix sort of (id, position),
 // so the rows of one id stand together in the order of their positions, and
-// every sum has one order -- no atomics, the same bits from every call.  The
-// sorted tokens are cut into segments of 32, one team of threads each,
-// whatever the ids' distribution.  A run of one id inside a segment is summed
-// and written once.  A run that crosses segments leaves one fp32 row per
-// segment in the workspace, and a last kernel adds those in order.  The rows
-// of the table that no token names are found in the sorted ids and filled
-// with zeros by further CTAs of the same launch, so each row of the gradient
-// is written once.
+// every sum has one order -- no atomics on values, the same bits from every
+// call.  The sorted tokens are cut into segments of 32, one team of threads
+// each, whatever the ids' distribution.  A run of one id inside a segment is
+// summed and written once.  A run that crosses segments leaves one fp32 row
+// per segment in the workspace, and a last kernel adds those.  The rows of
+// the table that no token names are found in the sorted ids and filled with
+// zeros by further CTAs of the same launch, so each row of the gradient is
+// written once.  Up to kFewTokens tokens need no sort: every CTA reads all ids, the
+// first token of each id adds its rows, and one launch does it all.
 #include <algorithm>
+#include <type_traits>
 
 #include "dit_stat.cuh"
 #include "dit_token.h"
@@ -31,40 +33,102 @@ __device__ __forceinline__ uint32_t key_at(const void* ids, bool ids64, int64_t 
   return id >= 0 && id < V ? (uint32_t)id : (uint32_t)V;
 }
 
-// VB bytes of T times a scale, rounded once
-template <class T, int VB>
-__device__ __forceinline__ Raw<VB> scaled(const Raw<VB>& r, float scale) {
-  using V = Vec<T, VB>;
-  float f[V::N];
-  V::widen(r, f);
+// Rows cut into tiles, a few columns per thread: a 16-byte granule of rows
+// that are made of such (WIDE), else four single elements blockDim.x columns
+// apart.
+template <class T, bool WIDE>
+struct Tile {
+  static constexpr int ES = (int)sizeof(T);
+  static constexpr int N = WIDE ? 16 / ES : 4;
+  static constexpr int VB = N * ES;
+  using R = Raw<VB>;
+  int D, c;  // c: the thread's first column
+  __device__ __forceinline__ Tile(int D, int tile)
+      : D(D), c(tile * (int)blockDim.x * N + (WIDE ? threadIdx.x * N : threadIdx.x)) {}
+  __device__ __forceinline__ int col(int i) const { return WIDE ? c + i : c + i * (int)blockDim.x; }
+  __device__ __forceinline__ bool valid() const { return c < D; }
+  __device__ __forceinline__ R load(const void* row) const {
+    if constexpr (WIDE) {
+      return ld_stream<16>((const char*)row + (int64_t)c * ES);
+    } else {
+      R r = {};
 #pragma unroll
-  for (int i = 0; i < V::N; ++i) f[i] = __fmul_rn(f[i], scale);
-  return V::narrow(f);
-}
+      for (int i = 0; i < N; ++i) {
+        if (col(i) >= D) continue;
+        const Raw<ES> e = ld_stream<ES>((const char*)row + (int64_t)col(i) * ES);
+        if constexpr (ES == 4)
+          r.w[i] = e.w[0];
+        else
+          r.w[i >> 1] |= (uint32_t)e.h << (16 * (i & 1));
+      }
+      return r;
+    }
+  }
+  __device__ __forceinline__ static void widen(const R& r, float (&f)[N]) {
+    Vec<T, VB>::widen(r, f);
+  }
+  // f * scale, rounded once
+  __device__ __forceinline__ void store(void* row, const float (&f)[N], float scale) const {
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __fmul_rn(f[i], scale);
+    const R r = Vec<T, VB>::narrow(v);
+    if constexpr (WIDE) {
+      st_stream<16>((char*)row + (int64_t)c * ES, r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (col(i) >= D) continue;
+        Raw<ES> e;
+        if constexpr (ES == 4)
+          e.w[0] = r.w[i];
+        else
+          e.h = (uint16_t)(r.w[i >> 1] >> (16 * (i & 1)));
+        st_stream<ES>((char*)row + (int64_t)col(i) * ES, e);
+      }
+    }
+  }
+};
 
-// threads of a CTA over the vectors of a row (a power of two, at most 256)
-int row_threads(int64_t nvec) {
-  int t = 1;
-  while (t < 256 && t < nvec) t *= 2;
+// columns a thread takes, threads of a CTA over a row (a power of two, 32 to
+// 256), and the row's tiles
+inline int tile_columns(int es, bool wide) { return wide ? 16 / es : 4; }
+int row_threads(int64_t D, int n) {
+  int t = 32;
+  while (t < 256 && (int64_t)t * n < D) t *= 2;
   return t;
+}
+int64_t row_tiles(int64_t D, int n) {
+  const int64_t tile = (int64_t)n * row_threads(D, n);
+  return (D + tile - 1) / tile;
 }
 
 // blockDim = (threads of a row, tokens of a CTA)
-template <class T, int VB>
-__global__ void __launch_bounds__(256) embedding_kernel(EmbedArgs a) {
-  constexpr int ES = (int)sizeof(T);
-  const int64_t pitch = (int64_t)a.D * ES;
-  const int nvec = (int)(pitch / VB);
+template <class T, bool WIDE>
+__global__ void __launch_bounds__(256) embedding_kernel(EmbedArgs a, int tiles) {
+  using L = Tile<T, WIDE>;
+  const int64_t pitch = (int64_t)a.D * L::ES;
   for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.tokens;
        t += (int64_t)gridDim.x * blockDim.y) {
     const uint32_t key = key_at(a.ids, a.ids64, t, a.V);
     const char* src = (const char*)a.table + (int64_t)key * pitch;
-    char* dst = (char*)a.out + t * pitch;
     const bool seen = key < a.V;
-    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-      Raw<VB> r = {};
-      if (seen) r = scaled<T, VB>(ld_stream<VB>(src + (int64_t)v * VB), a.scale);
-      st_stream<VB>(dst + (int64_t)v * VB, r);
+    constexpr int AHEAD = WIDE ? 2 : 4;  // tiles in flight
+    for (int k = 0; k < tiles; k += AHEAD) {
+      typename L::R r[AHEAD];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        const L tile(a.D, k + j);
+        r[j] = typename L::R{};
+        if (seen && tile.valid()) r[j] = tile.load(src);
+      }
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        const L tile(a.D, k + j);
+        float f[L::N];
+        L::widen(r[j], f);
+        if (tile.valid()) tile.store((char*)a.out + t * pitch, f, seen ? a.scale : 0.0f);
+      }
     }
   }
 }
@@ -91,6 +155,7 @@ constexpr int kSortCluster = 8;
 struct SortArgs {
   const void* ids;
   uint2* pairs[2];
+  uint32_t* runs;    // the count of runs that cross segments: set to zero here
   int64_t tokens, V;
   int64_t per_warp;  // consecutive tokens of a warp, a multiple of 32
   int ctas;          // CTAs of the cluster
@@ -102,35 +167,55 @@ struct SortArgs {
 // owns the tokens [(32 c + w) per_warp, ...) of every pass, and counts them
 // per digit; a digit's place is the count of smaller digits, then of earlier
 // CTAs, then of earlier warps, then of earlier tokens of the warp.  Pass p
-// writes pairs[p & 1].
+// writes pairs[p & 1].  Tokens are read 32 * kRounds at a time, once a pass
+// where a warp has no more than that.
 __global__ void __launch_bounds__(kSortWarps * 32) sort_kernel(SortArgs a) {
+  constexpr int kRounds = 8;
   extern __shared__ uint32_t count[];  // [warps][digits]
   __shared__ uint32_t total[1 << kSortBits];
+  __shared__ uint32_t start[1 << kSortBits];
   __shared__ uint32_t scan[kSortWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int digits = 1 << a.bits;
   const uint32_t cta = a.ctas > 1 ? blockIdx.x : 0;
   const int64_t first = ((int64_t)cta * kSortWarps + warp) * a.per_warp;
   const int64_t last = first + a.per_warp < a.tokens ? first + a.per_warp : a.tokens;
+  const bool once = a.per_warp <= 32 * kRounds;
   uint32_t* mine = count + warp * digits;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.runs = 0;
 
   for (int p = 0; p < a.passes; ++p) {
     const uint2* src = a.pairs[(p & 1) ^ 1];
-    auto load = [&](int64_t i) {
-      return p == 0 ? make_uint2(key_at(a.ids, a.ids64, i, a.V), (uint32_t)i) : __ldcg(src + i);
+    uint2 v[kRounds];
+    auto load = [&](int64_t i0) {
+#pragma unroll
+      for (int k = 0; k < kRounds; ++k) {
+        const int64_t i = i0 + 32 * k + lane;
+        v[k] = make_uint2(0u, 0u);
+        if (i < last)
+          v[k] = p == 0 ? make_uint2(key_at(a.ids, a.ids64, i, a.V), (uint32_t)i) : __ldcg(src + i);
+      }
     };
     auto digit = [&](uint32_t key) { return (int)((key >> (p * a.bits)) & (uint32_t)(digits - 1)); };
     for (int i = lane; i < digits; i += 32) mine[i] = 0;
     __syncwarp();
-    for (int64_t i = first + lane; i < last; i += 32) atomicAdd(&mine[digit(load(i).x)], 1u);
+    for (int64_t i0 = first; i0 < last; i0 += 32 * kRounds) {
+      load(i0);
+#pragma unroll
+      for (int k = 0; k < kRounds; ++k)
+        if (i0 + 32 * k + lane < last) atomicAdd(&mine[digit(v[k].x)], 1u);
+    }
     __syncthreads();
     // counters of a digit -> counts of earlier warps; the CTA's total
     uint32_t sum = 0;
     if ((int)threadIdx.x < digits) {
+      uint32_t n[kSortWarps];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) n[w] = count[w * digits + threadIdx.x];
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t n = count[w * digits + threadIdx.x];
         count[w * digits + threadIdx.x] = sum;
-        sum += n;
+        sum += n[w];
       }
       total[threadIdx.x] = sum;
     }
@@ -141,7 +226,8 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_kernel(SortArgs a) {
       if ((int)threadIdx.x < digits) {
         all = 0;
         const uint32_t addr = smem_addr(&total[threadIdx.x]);
-        for (int c = 0; c < a.ctas; ++c) {
+#pragma unroll
+        for (int c = 0; c < kSortCluster; ++c) {
           const uint32_t n = ld_cluster(addr, c);
           before += (uint32_t)c < cta ? n : 0u;
           all += n;
@@ -156,32 +242,34 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_kernel(SortArgs a) {
       const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, inc, o);
       if (lane >= o) inc += n;
     }
-    __syncthreads();  // (a CTA alone: total and scan of the previous pass have been read)
     if (lane == 31) scan[warp] = inc;
     __syncthreads();
-    uint32_t place = before + inc - all;
-    for (int w = 0; w < warp; ++w) place += scan[w];
-    if ((int)threadIdx.x < digits)
-      for (int w = 0; w < kSortWarps; ++w) count[w * digits + threadIdx.x] += place;
+    const uint32_t part = lane < warp ? scan[lane] : 0u;  // the warps before this one
+    uint32_t place = before + inc - all + __reduce_add_sync(0xFFFFFFFFu, part);
+    if ((int)threadIdx.x < digits) start[threadIdx.x] = place;
     __syncthreads();
     // place the warp's tokens, 32 at a time in their order
     uint2* dst = a.pairs[p & 1];
-    for (int64_t i0 = first; i0 < last; i0 += 32) {
-      const bool has = i0 + lane < last;
-      const uint2 v = has ? load(i0 + lane) : make_uint2(0u, 0u);
-      const int d = digit(v.x);
-      uint32_t same = __ballot_sync(0xFFFFFFFFu, has);
-      for (int b = 0; b < a.bits; ++b) {
-        const uint32_t set = __ballot_sync(0xFFFFFFFFu, (d >> b) & 1);
-        same &= (d >> b) & 1 ? set : ~set;
+    for (int64_t i0 = first; i0 < last; i0 += 32 * kRounds) {
+      if (!once) load(i0);
+#pragma unroll
+      for (int k = 0; k < kRounds; ++k) {
+        if (i0 + 32 * k >= last) break;  // the whole warp
+        const bool has = i0 + 32 * k + lane < last;
+        const int d = digit(v[k].x);
+        uint32_t same = __ballot_sync(0xFFFFFFFFu, has);
+        for (int b = 0; b < a.bits; ++b) {
+          const uint32_t set = __ballot_sync(0xFFFFFFFFu, (d >> b) & 1);
+          same &= (d >> b) & 1 ? set : ~set;
+        }
+        const uint32_t base = has ? mine[d] : 0u;
+        __syncwarp();
+        if (has) {
+          dst[start[d] + base + __popc(same & ((1u << lane) - 1u))] = v[k];
+          if (lane == __ffs(same) - 1) mine[d] = base + __popc(same);
+        }
+        __syncwarp();
       }
-      const uint32_t base = has ? mine[d] : 0u;
-      __syncwarp();
-      if (has) {
-        dst[base + __popc(same & ((1u << lane) - 1u))] = v;
-        if (lane == __ffs(same) - 1) mine[d] = base + __popc(same);
-      }
-      __syncwarp();
     }
     if (a.ctas > 1)
       cluster_barrier();  // the next pass reads what the other CTAs placed
@@ -197,13 +285,16 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_kernel(SortArgs a) {
 struct SumArgs {
   void* gt;
   const void* g;
+  const void* ids;      // few tokens: unsorted
   const uint2* sorted;
   float* partial;
+  uint32_t* runs;       // [0] the count of, [1...] the first segments of runs that cross segments
   int64_t tokens, V;
   int64_t segments;
-  int64_t seg_ctas;   // CTAs of the segments; the others fill rows with zeros
-  int D;
-  int zero_rows;      // rows of the table per CTA that fills zeros
+  int64_t seg_ctas;     // CTAs of the segments; the others fill rows with zeros
+  int D, tiles;
+  int zero_rows;        // rows of the table per CTA that fills zeros
+  bool ids64;
   float scale;
 };
 
@@ -237,16 +328,26 @@ __device__ __forceinline__ void fill_zero(char* p, int64_t bytes, int lane) {
   for (int64_t i = head + body * 16 + lane * ES; i < bytes; i += 32 * ES) st_stream<ES>(p + i, Raw<ES>{});
 }
 
-// blockDim = (threads of a row, segments of a CTA); gridDim.y column tiles of
-// blockDim.x * 16 bytes (elements, for rows that are not made of granules).
-template <class T, int VB>
-__global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
-  using V = Vec<T, VB>;
-  constexpr int N = V::N, ES = (int)sizeof(T);
+// Rows [v0, v1) of the table that `named` (a bit each, shared) does not mark,
+// filled with zeros by the CTA's warps.
+template <int ES>
+__device__ __forceinline__ void fill_rows(const SumArgs& a, const uint32_t* named, int64_t v0,
+                                          int64_t v1, int tid, int nthr) {
   const int64_t pitch = (int64_t)a.D * ES;
+  for (int64_t v = v0 + (tid >> 5); v < v1; v += nthr >> 5) {
+    const int k = (int)(v - v0);
+    if (!((named[k >> 5] >> (k & 31)) & 1u)) fill_zero<ES>((char*)a.gt + v * pitch, pitch, tid & 31);
+  }
+}
+
+// blockDim = (threads of a row, segments of a CTA); segment CTAs come in
+// groups of `tiles`, one column tile each.
+template <class T, bool WIDE>
+__global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
+  using L = Tile<T, WIDE>;
+  constexpr int N = L::N;
+  const int64_t pitch = (int64_t)a.D * L::ES;
   if ((int64_t)blockIdx.x >= a.seg_ctas) {
-    if (blockIdx.y > 0) return;
-    // rows that no token names
     __shared__ uint32_t named[kMaxZeroRows / 32];
     const int tid = threadIdx.y * blockDim.x + threadIdx.x;
     const int nthr = blockDim.x * blockDim.y;
@@ -261,66 +362,69 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
       atomicOr(&named[k >> 5], 1u << (k & 31));
     }
     __syncthreads();
-    for (int64_t v = v0 + (tid >> 5); v < v1; v += nthr >> 5) {
-      const int k = (int)(v - v0);
-      if (!((named[k >> 5] >> (k & 31)) & 1u)) 
-        fill_zero<ES>((char*)a.gt + v * pitch, pitch, tid & 31);
-    }
+    fill_rows<L::ES>(a, named, v0, v1, tid, nthr);
     return;
   }
-  const int64_t seg = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int vec = blockIdx.y * blockDim.x + threadIdx.x;
-  if (seg >= a.segments || vec >= (int)(pitch / VB)) return;
+  const int tile = (int)(blockIdx.x % a.tiles);
+  const int64_t seg = (int64_t)(blockIdx.x / a.tiles) * blockDim.y + threadIdx.y;
+  const L t(a.D, tile);
+  if (seg >= a.segments) return;  // the whole team
   const int64_t i0 = seg * kEmbedSegment;
-  const int64_t i1 = i0 + kEmbedSegment < a.tokens ? i0 + kEmbedSegment : a.tokens;
-  const char* src = (const char*)a.g + (int64_t)vec * VB;
-  uint32_t key = __ldg(&a.sorted[i0].x);
-  bool head = i0 > 0 && __ldg(&a.sorted[i0 - 1].x) == key;
-  const uint32_t after = i1 < a.tokens ? __ldg(&a.sorted[i1].x) : (uint32_t)a.V;
+  const int n = (int)min((int64_t)kEmbedSegment, a.tokens - i0);
+  // the segment's tokens, one per lane of each warp
+  const int lane = threadIdx.x & 31;
+  const uint2 mine = lane < n ? __ldg(a.sorted + i0 + lane) : make_uint2((uint32_t)a.V, 0u);
+  const uint32_t before = i0 > 0 ? __ldg(&a.sorted[i0 - 1].x) : (uint32_t)a.V;
+  const uint32_t after = i0 + n < a.tokens ? __ldg(&a.sorted[i0 + n].x) : (uint32_t)a.V;
+  uint32_t key = __shfl_sync(0xFFFFFFFFu, mine.x, 0);
+  bool head = i0 > 0 && before == key;
   float acc[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) acc[e] = 0.0f;
   // the run of `key` ends here (open: it goes on in the next segment)
   auto flush = [&](bool open) {
-    if (key < a.V) {
+    if (key < a.V && t.valid()) {
       if (head || open) {
-        float* p = a.partial + (seg * 2 + (head ? 0 : 1)) * a.D + (int64_t)vec * N;
+        float* p = a.partial + (seg * 2 + (head ? 0 : 1)) * a.D;
+        if constexpr (WIDE) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) p[e] = acc[e];
+          for (int e = 0; e < N; e += 4)
+            *(float4*)(p + t.c + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (t.col(e) < a.D) p[t.col(e)] = acc[e];
+        }
+        if (!head && tile == 0 && threadIdx.x == 0) a.runs[1 + atomicAdd(a.runs, 1u)] = (uint32_t)seg;
       } else {
-        float f[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) f[e] = __fmul_rn(acc[e], a.scale);
-        st_stream<VB>((char*)a.gt + (int64_t)key * pitch + (int64_t)vec * VB, V::narrow(f));
+        t.store((char*)a.gt + (int64_t)key * pitch, acc, a.scale);
       }
     }
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[e] = 0.0f;
   };
   constexpr int AHEAD = 8;  // rows in flight
-  for (int64_t i = i0; i < i1; i += AHEAD) {
-    Raw<VB> r[AHEAD];
-    uint32_t k[AHEAD];
+  for (int i = 0; i < n; i += AHEAD) {
+    typename L::R r[AHEAD];
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
-      k[j] = (uint32_t)a.V;
-      if (i + j < i1) {
-        const uint2 s = __ldg(a.sorted + i + j);
-        k[j] = s.x;
-        if (s.x < a.V) r[j] = ld_stream<VB>(src + (int64_t)s.y * pitch);
-      }
+      // (lanes past the segment's end hold an id outside the table)
+      const uint32_t k = __shfl_sync(0xFFFFFFFFu, mine.x, i + j);
+      const uint32_t at = __shfl_sync(0xFFFFFFFFu, mine.y, i + j);
+      if (k < a.V && t.valid()) r[j] = t.load((const char*)a.g + (int64_t)at * pitch);
     }
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
-      if (i + j >= i1) break;
-      if (k[j] != key) {
+      if (i + j >= n) break;
+      const uint32_t k = __shfl_sync(0xFFFFFFFFu, mine.x, i + j);
+      if (k != key) {
         flush(false);
-        key = k[j];
+        key = k;
         head = false;
       }
-      if (key < a.V) {
+      if (key < a.V && t.valid()) {
         float f[N];
-        V::widen(r[j], f);
+        L::widen(r[j], f);
 #pragma unroll
         for (int e = 0; e < N; ++e) acc[e] = __fadd_rn(acc[e], f[e]);
       }
@@ -329,44 +433,158 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
   flush(after == key);
 }
 
-// A run that starts in segment s and goes on: its parts added in order.
-template <class T>
+// The parts of each run that crosses segments, added: 32 * N columns by 8
+// groups of parts per CTA, group q taking parts q, q + 8, ... (the run's first
+// segment is part 0), then the groups in order.  N: 4 where that divides D.
+template <class T, int N>
 __global__ void __launch_bounds__(256) embedding_join_kernel(SumArgs a) {
-  const int64_t seg = (int64_t)blockIdx.x;
-  const int64_t i1 = (seg + 1) * kEmbedSegment;
-  if (i1 >= a.tokens) return;
-  const uint32_t key = __ldg(&a.sorted[i1 - 1].x);
-  if (key >= a.V || __ldg(&a.sorted[i1].x) != key) return;  // ends here
-  const int64_t i0 = seg * kEmbedSegment;
-  if (i0 > 0 && __ldg(&a.sorted[i0].x) == key && __ldg(&a.sorted[i0 - 1].x) == key) return;  // began before
-  int64_t n = 1;  // further segments of the run
-  while (i1 + n * kEmbedSegment < a.tokens && __ldg(&a.sorted[i1 + n * kEmbedSegment].x) == key) ++n;
-  const float* p = a.partial + (seg * 2 + 1) * a.D;
-  for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < a.D; c += gridDim.y * blockDim.x) {
-    float v = p[c];
-    for (int64_t j = 0; j < n; ++j) v = __fadd_rn(v, p[(1 + 2 * j) * a.D + c]);
-    float f[1] = {__fmul_rn(v, a.scale)};
-    st_stream<sizeof(T)>((char*)a.gt + ((int64_t)key * a.D + c) * (int)sizeof(T),
-                         Vec<T, (int)sizeof(T)>::narrow(f));
+  __shared__ float part[8][N][33];
+  const int lane = threadIdx.x, q = threadIdx.y;
+  const int64_t tiles = (a.D + 32 * N - 1) / (32 * N), items = (int64_t)a.runs[0] * tiles;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t seg = a.runs[1 + it / tiles];
+    const int c = ((int)(it % tiles) * 32 + lane) * N;
+    const int64_t i1 = (seg + 1) * kEmbedSegment;
+    const uint32_t key = a.sorted[i1 - 1].x;
+    // the parts behind the first: segments that start with the key, 32 at a time
+    int64_t n = 0;
+    for (;;) {
+      const int64_t i = i1 + (n + lane) * kEmbedSegment;
+      const uint32_t on = __ballot_sync(0xFFFFFFFFu, i < a.tokens && a.sorted[i].x == key);
+      n += on == 0xFFFFFFFFu ? 32 : __ffs(~on) - 1;
+      if (on != 0xFFFFFFFFu) break;
+    }
+    const float* p = a.partial + (seg * 2 + 1) * a.D + c;
+    float v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = 0.0f;
+    if (c < a.D) {
+#pragma unroll 4
+      for (int64_t j = q; j <= n; j += 8) {
+        const float* at = p + (j ? 2 * j - 1 : 0) * a.D;
+        if constexpr (N == 4) {
+          const float4 f = *(const float4*)at;
+          v[0] = __fadd_rn(v[0], f.x);
+          v[1] = __fadd_rn(v[1], f.y);
+          v[2] = __fadd_rn(v[2], f.z);
+          v[3] = __fadd_rn(v[3], f.w);
+        } else {
+          v[0] = __fadd_rn(v[0], *at);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) part[q][k][lane] = v[k];
+    __syncthreads();
+    // group q < N finishes column c + q of the lanes
+    if (q < N && c < a.D) {
+      float f[1] = {part[0][q][lane]};
+#pragma unroll
+      for (int k = 1; k < 8; ++k) f[0] = __fadd_rn(f[0], part[k][q][lane]);
+      f[0] = __fmul_rn(f[0], a.scale);
+      st_stream<sizeof(T)>((char*)a.gt + ((int64_t)key * a.D + c + q) * (int)sizeof(T),
+                           Vec<T, (int)sizeof(T)>::narrow(f));
+    }
+    __syncthreads();  // read before the next item's
   }
 }
 
-template <class T, int VB>
-cudaError_t launch_sums(SumArgs a, cudaStream_t s) {
-  const int64_t nvec = (int64_t)a.D * (int)sizeof(T) / VB;
-  const int tx = row_threads(nvec), ty = 256 / tx;
-  a.seg_ctas = (a.segments + ty - 1) / ty;
+// Few tokens, unsorted, in one launch: CTA (token, tile) adds the rows of its
+// token's id if no earlier token has it; the others fill rows with zeros.
+template <class T, bool WIDE>
+__global__ void __launch_bounds__(256) embedding_few_kernel(SumArgs a) {
+  using L = Tile<T, WIDE>;
+  constexpr int N = L::N;
+  __shared__ uint32_t named[kMaxZeroRows / 32];  // (zero rows) a bit per row of the table
+  __shared__ uint32_t match[kFewTokens / 32];    // (tokens) a bit per token with this id
+  const int64_t pitch = (int64_t)a.D * L::ES;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
+  const int n = (int)a.tokens;
+  if ((int64_t)blockIdx.x >= a.seg_ctas) {
+    const int64_t v0 = ((int64_t)blockIdx.x - a.seg_ctas) * a.zero_rows;
+    const int64_t v1 = v0 + a.zero_rows < a.V ? v0 + a.zero_rows : a.V;
+    if (tid < kMaxZeroRows / 32) named[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += nthr) {
+      const int64_t k = (int64_t)key_at(a.ids, a.ids64, i, a.V) - v0;
+      if (k >= 0 && k < v1 - v0) atomicOr(&named[k >> 5], 1u << (k & 31));
+    }
+    __syncthreads();
+    fill_rows<L::ES>(a, named, v0, v1, tid, nthr);
+    return;
+  }
+  const int me = (int)(blockIdx.x / a.tiles);
+  const uint32_t key = key_at(a.ids, a.ids64, me, a.V);
+  if (key >= a.V) return;
+  for (int i0 = tid & ~31; i0 < kFewTokens; i0 += nthr) {
+    const int i = i0 + (tid & 31);
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, i < n && key_at(a.ids, a.ids64, i, a.V) == key);
+    if ((tid & 31) == 0) match[i0 >> 5] = m;
+  }
+  __syncthreads();
+  for (int w = 0; w <= me >> 5; ++w) {
+    const uint32_t earlier = w < me >> 5 ? 0xFFFFFFFFu : (1u << (me & 31)) - 1u;
+    if (match[w] & earlier) return;  // an earlier token adds them
+  }
+  const L t(a.D, (int)(blockIdx.x % a.tiles));
+  if (threadIdx.y > 0 || !t.valid()) return;
+  float acc[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+  for (int w = me >> 5; w < kFewTokens / 32; ++w) {
+    uint32_t m = match[w];
+    while (m) {
+      constexpr int AHEAD = 4;  // rows in flight
+      typename L::R r[AHEAD];
+      int got = 0;
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        if (!m) continue;
+        const int i = w * 32 + __ffs(m) - 1;
+        m &= m - 1;
+        r[j] = t.load((const char*)a.g + (int64_t)i * pitch);
+        got = j + 1;
+      }
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        if (j >= got) continue;
+        float f[N];
+        L::widen(r[j], f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = __fadd_rn(acc[e], f[e]);
+      }
+    }
+  }
+  t.store((char*)a.gt + (int64_t)key * pitch, acc, a.scale);
+}
+
+template <class T, bool WIDE>
+cudaError_t launch_sums(const DeviceInfo& dev, SumArgs a, cudaStream_t s) {
+  const int64_t row_bytes = (int64_t)a.D * (int)sizeof(T);
+  const int n = tile_columns((int)sizeof(T), WIDE);
+  const int tx = row_threads(a.D, n), ty = 256 / tx;
+  a.tiles = (int)row_tiles(a.D, n);
   // about 128 KB of zeros per CTA
-  a.zero_rows = (int)std::min<int64_t>(kMaxZeroRows, std::max<int64_t>(1, (128 << 10) / ((int64_t)a.D * (int)sizeof(T))));
+  a.zero_rows = (int)std::min<int64_t>(kMaxZeroRows, std::max<int64_t>(1, (128 << 10) / row_bytes));
   const int64_t zero_ctas = (a.V + a.zero_rows - 1) / a.zero_rows;
-  const int64_t tiles = (nvec + tx - 1) / tx;
-  if (a.seg_ctas + zero_ctas > 0x7FFFFFFF || tiles > 65535) return cudaErrorInvalidConfiguration;
-  embedding_sum_kernel<T, VB><<<dim3((unsigned)(a.seg_ctas + zero_ctas), (unsigned)tiles),
-                                dim3(tx, ty), 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.segments < 2) return e;
-  const unsigned cols = (unsigned)std::min<int64_t>(64, ((int64_t)a.D + 255) / 256);
-  embedding_join_kernel<T><<<dim3((unsigned)(a.segments - 1), cols), 256, 0, s>>>(a);
+  const bool few = a.tokens <= kFewTokens;
+  a.seg_ctas = (few ? a.tokens : (a.segments + ty - 1) / ty) * a.tiles;
+  if (a.seg_ctas + zero_ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)(a.seg_ctas + zero_ctas);
+  if (few) {
+    embedding_few_kernel<T, WIDE><<<grid, dim3(tx, ty), 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  embedding_sum_kernel<T, WIDE><<<grid, dim3(tx, ty), 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const bool four = a.D % 4 == 0;
+  const int64_t most = (a.segments - 1) * ((a.D + (four ? 127 : 31)) / (four ? 128 : 32));
+  const unsigned join = (unsigned)std::min<int64_t>(most, 8 * dev.sm_count);
+  if (four)
+    embedding_join_kernel<T, 4><<<join, dim3(32, 8), 0, s>>>(a);
+  else
+    embedding_join_kernel<T, 1><<<join, dim3(32, 8), 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -392,59 +610,62 @@ cudaError_t launch_sort(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, sort_kernel, a);
 }
 
+template <class Fn>
+cudaError_t with_tile(int dtype, bool wide, Fn&& fn) {
+  using Yes = std::true_type;
+  using No = std::false_type;
+  if (dtype == 0) return wide ? fn(TypeTag<__nv_bfloat16>{}, Yes{}) : fn(TypeTag<__nv_bfloat16>{}, No{});
+  if (dtype == 1) return wide ? fn(TypeTag<__half>{}, Yes{}) : fn(TypeTag<__half>{}, No{});
+  return wide ? fn(TypeTag<float>{}, Yes{}) : fn(TypeTag<float>{}, No{});
+}
+
 }  // namespace
 
 cudaError_t launch_embedding(int dtype, bool wide, const EmbedArgs& a, cudaStream_t s) {
-  const int es = dtype == 2 ? 4 : 2;
-  return dispatch_dtype_width(dtype, wide ? 16 : es, [&](auto tt, auto w) -> cudaError_t {
+  return with_tile(dtype, wide, [&](auto tt, auto w) -> cudaError_t {
     using T = typename decltype(tt)::type;
-    constexpr int VB = decltype(w)::value;
-    if constexpr (VB == 16 || VB == (int)sizeof(T)) {
-      const int tx = row_threads((int64_t)a.D * es / VB), ty = 256 / tx;
-      const int64_t grid = std::min<int64_t>((a.tokens + ty - 1) / ty, int64_t(1) << 30);
-      embedding_kernel<T, VB><<<(unsigned)grid, dim3(tx, ty), 0, s>>>(a);
-      return cudaGetLastError();
-    } else {
-      return cudaErrorInvalidValue;
-    }
+    const int n = tile_columns((int)sizeof(T), wide);
+    const int tx = row_threads(a.D, n), ty = 256 / tx;
+    const int64_t grid = std::min<int64_t>((a.tokens + ty - 1) / ty, int64_t(1) << 30);
+    embedding_kernel<T, decltype(w)::value>
+        <<<(unsigned)grid, dim3(tx, ty), 0, s>>>(a, (int)row_tiles(a.D, n));
+    return cudaGetLastError();
   });
 }
 
 cudaError_t launch_embedding_grad(const DeviceInfo& dev, int dtype, bool wide,
                                   const EmbedGradArgs& a, cudaStream_t s) {
-  SortArgs q = {};
-  q.ids = a.ids;
-  q.ids64 = a.ids64;
-  q.tokens = a.tokens;
-  q.V = a.V;
-  q.pairs[0] = a.pairs[0];
-  q.pairs[1] = a.pairs[1];
-  int bits = 1;  // of the keys 0 .. V
-  while (bits < 32 && (a.V >> bits) != 0) ++bits;
-  q.passes = (bits + kSortBits - 1) / kSortBits;
-  q.bits = (bits + q.passes - 1) / q.passes;
-  if (a.tokens > 0) {
-    const cudaError_t e = launch_sort(dev, q, s);
-    if (e != cudaSuccess) return e;
-  }
   SumArgs m = {};
   m.gt = a.gt;
   m.g = a.g;
-  m.sorted = a.pairs[(q.passes - 1) & 1];
+  m.ids = a.ids;
+  m.ids64 = a.ids64;
   m.partial = a.partial;
+  m.runs = a.runs;
   m.tokens = a.tokens;
   m.V = a.V;
   m.segments = embed_segments(a.tokens);
   m.D = a.D;
   m.scale = a.scale;
-  const int es = dtype == 2 ? 4 : 2;
-  return dispatch_dtype_width(dtype, wide ? 16 : es, [&](auto tt, auto w) -> cudaError_t {
-    using T = typename decltype(tt)::type;
-    constexpr int VB = decltype(w)::value;
-    if constexpr (VB == 16 || VB == (int)sizeof(T))
-      return launch_sums<T, VB>(m, s);
-    else
-      return cudaErrorInvalidValue;
+  if (a.tokens > kFewTokens) {
+    SortArgs q = {};
+    q.ids = a.ids;
+    q.ids64 = a.ids64;
+    q.tokens = a.tokens;
+    q.V = a.V;
+    q.pairs[0] = a.pairs[0];
+    q.pairs[1] = a.pairs[1];
+    q.runs = a.runs;
+    int bits = 1;  // of the keys 0 .. V
+    while (bits < 32 && (a.V >> bits) != 0) ++bits;
+    q.passes = (bits + kSortBits - 1) / kSortBits;
+    q.bits = (bits + q.passes - 1) / q.passes;
+    const cudaError_t e = launch_sort(dev, q, s);
+    if (e != cudaSuccess) return e;
+    m.sorted = a.pairs[(q.passes - 1) & 1];
+  }
+  return with_tile(dtype, wide, [&](auto tt, auto w) -> cudaError_t {
+    return launch_sums<typename decltype(tt)::type, decltype(w)::value>(dev, m, s);
   });
 }
 

@@ -564,7 +564,8 @@ dit_status dit_embedding(void* out, const void* ids, const void* table, int64_t 
  * every row of [V, D] written, zeros where no token names it; ids outside
  * [0, V) take no part.  The tokens are sorted by id (stably, so the rows of
  * an id are added in the order of their positions) and the sums are fp32.
- * grad_table may overlap neither the inputs nor the workspace.
+ * grad_table may overlap neither the inputs nor the workspace.  Up to 256
+ * tokens need no workspace (its size is 0, the pointer may be NULL).
  */
 int64_t dit_embedding_backward_workspace_bytes(int64_t tokens, int64_t D);
 

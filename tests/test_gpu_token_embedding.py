@@ -87,7 +87,8 @@ def test_lookup_shapes_offsets_and_values(dtype):
 
 @pytest.mark.parametrize("kind", ["text", "same", "distinct", "padded"])
 @pytest.mark.parametrize("n,V,D", [(1, 1, 8), (1, 1000, 64), (31, 40, 7), (32, 40, 8), (33, 3, 129),
-                                   (126, 3000, 256), (1000, 50, 1), (4096, 700, 24),
+                                   (126, 3000, 256), (255, 30, 4100), (256, 500, 33),
+                                   (257, 500, 33), (1000, 50, 1), (4096, 700, 24),
                                    (4097, 5000, 72), (6000, 130000, 8), (9000, 17, 40),
                                    (300, 300, 4100)])
 @dtypes
@@ -156,7 +157,9 @@ def test_refusals():
     with pytest.raises(dit.DitError):
         dit.embedding_backward(g, ids, 4, out=g)
     with pytest.raises(dit.DitError):
-        dit.embedding_backward(g, ids, 5, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        dit.embedding_backward(torch.ones((300, 16), device="cuda"),
+                               torch.zeros(300, dtype=torch.int64, device="cuda"), 5,
+                               workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
 
 
 def test_streams_and_graphs():

@@ -128,7 +128,8 @@ def test_embedding(lib):
 
 def test_embedding_backward(lib):
     wb = lib.dit_embedding_backward_workspace_bytes
-    assert wb(100, 64) == 2 * 1024 + 2 * 4 * 64 * 4 and wb(0, 64) == 0
+    # pairs twice, the list of runs (a count and 32 entries), 2 * 32 partial rows
+    assert wb(1000, 64) == 2 * 8192 + 256 + 2 * 32 * 64 * 4 and wb(256, 64) == wb(0, 64) == 0
     assert wb(-1, 64) == -1 and wb(1, 1 << 25) == -1
 
     def f(gt=O, g=G, ids=IDS, n=4, V=10, D=8, scale=1.0, dt=BF16, it=1, ws=WS, b=None):
@@ -140,9 +141,13 @@ def test_embedding_backward(lib):
     assert f(it=-1) == FORMAT and f(dt=9) == DTYPE and f(scale=NAN) == SCALAR
     assert f(n=-1, b=0) == SHAPE and f(V=-2) == SHAPE
     assert f(gt=None) == NULLP and f(g=None) == NULLP and f(ids=None) == NULLP
-    assert f(ws=None) == WORKSPACE and f(b=wb(4, 8) - 1) == WORKSPACE and f(ws=WS + 8) == WORKSPACE
+    assert f(ws=None) == NODEV                # few tokens need none
+    assert f(n=1000) == NODEV
+    assert f(n=1000, ws=None) == WORKSPACE and f(n=1000, ws=WS + 8) == WORKSPACE
+    assert f(n=1000, b=wb(1000, 8) - 1) == WORKSPACE
     assert f(ids=IDS + 4) == MISALIGNED
-    assert f(gt=G) == ALIAS and f(gt=IDS) == ALIAS and f(gt=WS) == ALIAS and f(ws=G) == ALIAS
+    assert f(gt=G) == ALIAS and f(gt=IDS) == ALIAS
+    assert f(n=1000, gt=WS) == ALIAS and f(n=1000, ws=G) == ALIAS and f(n=1000, ws=IDS) == ALIAS
 
 
 def descs(*d):
