@@ -6,7 +6,8 @@
 
 namespace dit {
 
-// How the rows of a call's tensors are accessed (dit_unit.cuh).
+// How the rows of a call's tensors are accessed (Unit of dit_unit.cuh, Tile of
+// k_embedding.cu).
 enum Layout { WIDE, PHASED, NARROW };
 
 // Weighted RMSNorm over `rows` rows of D elements (k_norm.cu).
@@ -60,7 +61,7 @@ struct EmbedArgs {
   bool ids64;
   float scale;
 };
-cudaError_t launch_embedding(int dtype, bool wide, const EmbedArgs& a, cudaStream_t s);
+cudaError_t launch_embedding(int dtype, int layout, const EmbedArgs& a, cudaStream_t s);
 
 struct EmbedGradArgs {
   void* gt;          // gradient of the table [V, D]
@@ -81,7 +82,7 @@ constexpr int kFewTokens = 256;
 // sorted tokens per segment, and segments of a call
 constexpr int kEmbedSegment = 32;
 inline int64_t embed_segments(int64_t tokens) { return (tokens + kEmbedSegment - 1) / kEmbedSegment; }
-cudaError_t launch_embedding_grad(const DeviceInfo& dev, int dtype, bool wide,
+cudaError_t launch_embedding_grad(const DeviceInfo& dev, int dtype, int layout,
                                   const EmbedGradArgs& a, cudaStream_t s);
 
 // The global norm of many tensors, and their clipping (k_clip.cu).

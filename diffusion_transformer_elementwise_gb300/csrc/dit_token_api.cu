@@ -233,8 +233,8 @@ dit_status dit_embedding(void* out, const void* ids, const void* table, int64_t 
   a.D = (int)D;
   a.ids64 = id_type == DIT_INT64;
   a.scale = scale;
-  const bool wide = wide_rows((uintptr_t)out | (uintptr_t)table, D * es);
-  return launch_status(dit::launch_embedding(dtype, wide, a, (cudaStream_t)stream));
+  const dit::Layout layout = layout_of((uintptr_t)out | (uintptr_t)table, nullptr, D * es);
+  return launch_status(dit::launch_embedding(dtype, layout, a, (cudaStream_t)stream));
 }
 
 int64_t dit_embedding_backward_workspace_bytes(int64_t tokens, int64_t D) {
@@ -291,8 +291,9 @@ dit_status dit_embedding_backward(void* grad_table, const void* grad_out, const 
     a.runs = (uint32_t*)(w += round_up(tokens * 8));
     a.partial = (float*)(w + round_up((dit::embed_segments(tokens) + 1) * 4));
   }
-  const bool wide = wide_rows((uintptr_t)grad_table | (uintptr_t)grad_out, D * es);
-  return launch_status(dit::launch_embedding_grad(dev, dtype, wide, a, (cudaStream_t)stream));
+  const dit::Layout layout =
+      layout_of((uintptr_t)grad_table | (uintptr_t)grad_out, nullptr, D * es);
+  return launch_status(dit::launch_embedding_grad(dev, dtype, layout, a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

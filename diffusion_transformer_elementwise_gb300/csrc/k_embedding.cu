@@ -33,66 +33,156 @@ __device__ __forceinline__ uint32_t key_at(const void* ids, bool ids64, int64_t 
   return id >= 0 && id < V ? (uint32_t)id : (uint32_t)V;
 }
 
-// Rows cut into tiles, a few columns per thread: a 16-byte granule of rows
-// that are made of such (WIDE), else four single elements blockDim.x columns
-// apart.
-template <class T, bool WIDE>
+// The 16 bytes that start s elements (0 < s < 16 / ES) into the 32 bytes lo,
+// hi.  s is the same for the whole warp.
+template <int ES>
+__device__ __forceinline__ Raw<16> shifted(const Raw<16>& lo, const Raw<16>& hi, int s) {
+  const int q = s * ES / 4;  // whole words
+  uint32_t a[6], b[5];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    const uint32_t x = i < 4 ? lo.w[i] : hi.w[i - 4];
+    const uint32_t y = i + 2 < 4 ? lo.w[i + 2] : hi.w[i - 2];
+    a[i] = q & 2 ? y : x;
+  }
+#pragma unroll
+  for (int i = 0; i < 5; ++i) b[i] = q & 1 ? a[i + 1] : a[i];
+  const uint32_t bits = ES == 2 && (s & 1) ? 16u : 0u;
+  Raw<16> r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.w[i] = __funnelshift_r(b[i], b[i + 1], bits);
+  return r;
+}
+
+// The 16 bytes that start at element e (>= 0) of a tensor of `total` elements
+// whose first byte is 16-byte aligned: two granules and a shift, which is the
+// same for every lane (their e are alike modulo a granule).  Elements past
+// the tensor's end read as zero.
+template <class T>
+__device__ __forceinline__ Raw<16> load_shifted(const void* tensor, int64_t e, int64_t total) {
+  constexpr int ES = (int)sizeof(T), EPG = 16 / ES;
+  const int s = (int)(e & (EPG - 1));
+  const int64_t g = e - s;
+  if (g + (s ? 2 : 1) * EPG <= total) {
+    const Raw<16> lo = ld_stream<16>((const char*)tensor + g * ES);
+    if (s == 0) return lo;
+    return shifted<ES>(lo, ld_stream<16>((const char*)tensor + (g + EPG) * ES), s);
+  }
+  Raw<16> r = {};
+#pragma unroll
+  for (int i = 0; i < EPG; ++i) {
+    if (e + i >= total) continue;
+    const Raw<ES> v = ld_stream<ES>((const char*)tensor + (e + i) * ES);
+    if constexpr (ES == 4)
+      r.w[i] = v.w[0];
+    else
+      r.w[i >> 1] |= (uint32_t)v.h << (16 * (i & 1));
+  }
+  return r;
+}
+
+// Rows cut into tiles, a few columns per thread.  WIDE: a granule of rows that
+// are made of 16-byte granules.  PHASED: the same columns of rows that are
+// not, in tensors that start on 16-byte boundaries (load_shifted).  NARROW: four
+// single elements blockDim.x columns apart.
+template <class T, int LAYOUT>
 struct Tile {
   static constexpr int ES = (int)sizeof(T);
-  static constexpr int N = WIDE ? 16 / ES : 4;
+  static constexpr int N = LAYOUT == NARROW ? 4 : 16 / ES;
   static constexpr int VB = N * ES;
   using R = Raw<VB>;
   int D, c;  // c: the thread's first column
   __device__ __forceinline__ Tile(int D, int tile)
-      : D(D), c(tile * (int)blockDim.x * N + (WIDE ? threadIdx.x * N : threadIdx.x)) {}
-  __device__ __forceinline__ int col(int i) const { return WIDE ? c + i : c + i * (int)blockDim.x; }
+      : D(D), c(tile * (int)blockDim.x * N + (LAYOUT == NARROW ? threadIdx.x : threadIdx.x * N)) {}
+  __device__ __forceinline__ int col(int i) const {
+    return LAYOUT == NARROW ? c + i * (int)blockDim.x : c + i;
+  }
   __device__ __forceinline__ bool valid() const { return c < D; }
-  __device__ __forceinline__ R load(const void* row) const {
-    if constexpr (WIDE) {
-      return ld_stream<16>((const char*)row + (int64_t)c * ES);
+  __device__ __forceinline__ static void put(R& r, int i, const void* p) {
+    const Raw<ES> e = ld_stream<ES>(p);
+    if constexpr (ES == 4)
+      r.w[i] = e.w[0];
+    else
+      r.w[i >> 1] |= (uint32_t)e.h << (16 * (i & 1));
+  }
+  // the thread's columns of row `row` of `rows` (PHASED: past the row's end,
+  // what follows it)
+  __device__ __forceinline__ R load(const void* tensor, int64_t row, int64_t rows) const {
+    const int64_t e = row * D + c;
+    if constexpr (LAYOUT == WIDE) {
+      return ld_stream<16>((const char*)tensor + e * ES);
     } else {
-      R r = {};
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (col(i) >= D) continue;
-        const Raw<ES> e = ld_stream<ES>((const char*)row + (int64_t)col(i) * ES);
-        if constexpr (ES == 4)
-          r.w[i] = e.w[0];
-        else
-          r.w[i >> 1] |= (uint32_t)e.h << (16 * (i & 1));
+      if (LAYOUT == PHASED && c >= 0) {
+        if constexpr (LAYOUT == PHASED) return load_shifted<T>(tensor, e, rows * D);
       }
+      R r = {};
+      constexpr int S = LAYOUT == NARROW ? 0 : 1;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (col(i) >= 0 && col(i) < D)
+          put(r, i, (const char*)tensor + (e + (S ? i : i * (int)blockDim.x)) * ES);
       return r;
     }
   }
   __device__ __forceinline__ static void widen(const R& r, float (&f)[N]) {
     Vec<T, VB>::widen(r, f);
   }
-  // f * scale, rounded once
-  __device__ __forceinline__ void store(void* row, const float (&f)[N], float scale) const {
+  // elements [lo, hi) of r, whose first is element e of the tensor
+  __device__ __forceinline__ static void scatter(void* tensor, int64_t e, const R& r, int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i < lo || i >= hi) continue;
+      Raw<ES> v;
+      if constexpr (ES == 4)
+        v.w[0] = r.w[i];
+      else
+        v.h = (uint16_t)(r.w[i >> 1] >> (16 * (i & 1)));
+      st_stream<ES>((char*)tensor + (e + i * (LAYOUT == NARROW ? (int)blockDim.x : 1)) * ES, v);
+    }
+  }
+  // f * scale, rounded once, to row `row`.  granules: element c of the row is
+  // the first of a granule; PHASED rows without are stored by the whole warp.
+  __device__ __forceinline__ void store(void* tensor, int64_t row, const float (&f)[N], float scale,
+                                        bool granules = false) const {
     float v[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = __fmul_rn(f[i], scale);
     const R r = Vec<T, VB>::narrow(v);
-    if constexpr (WIDE) {
-      st_stream<16>((char*)row + (int64_t)c * ES, r);
+    const int64_t e = row * D + c;
+    if constexpr (LAYOUT == WIDE) {
+      if (valid()) st_stream<16>((char*)tensor + e * ES, r);
+    } else if constexpr (LAYOUT == NARROW) {
+      // columns c, c + blockDim.x, ... below D
+      const int left = D - c, w = (int)blockDim.x;
+      scatter(tensor, e, r, 0, left <= 0 ? 0 : (left + w - 1) / w);
     } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (col(i) >= D) continue;
-        Raw<ES> e;
-        if constexpr (ES == 4)
-          e.w[0] = r.w[i];
+      const int s = granules ? 0 : (int)(e & (N - 1)), lane = threadIdx.x & 31;
+      if (s == 0) {
+        if (c >= 0 && c + N <= D)
+          st_stream<16>((char*)tensor + e * ES, r);
         else
-          e.h = (uint16_t)(r.w[i >> 1] >> (16 * (i & 1)));
-        st_stream<ES>((char*)row + (int64_t)col(i) * ES, e);
+          scatter(tensor, e, r, -c, D - c);
+        return;
       }
+      // the granule that starts s elements before column c: the previous
+      // lane's last s elements and this lane's first ones
+      R before;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) before.w[i] = __shfl_up_sync(0xFFFFFFFFu, r.w[i], 1);
+      const R g = shifted<ES>(before, r, N - s);
+      const int first = lane ? 0 : s;  // (lane 0 has no previous lane)
+      if (first == 0 && c - s + N <= D)
+        st_stream<16>((char*)tensor + (e - s) * ES, g);
+      else
+        scatter(tensor, e - s, g, first, D - (c - s));
+      if (lane == 31) scatter(tensor, e, r, N - s, D - c);
     }
   }
 };
 
 // columns a thread takes, threads of a CTA over a row (a power of two, 32 to
 // 256), and the row's tiles
-inline int tile_columns(int es, bool wide) { return wide ? 16 / es : 4; }
+int tile_columns(int es, int layout) { return layout == NARROW ? 4 : 16 / es; }
 int row_threads(int64_t D, int n) {
   int t = 32;
   while (t < 256 && (int64_t)t * n < D) t *= 2;
@@ -103,31 +193,33 @@ int64_t row_tiles(int64_t D, int n) {
   return (D + tile - 1) / tile;
 }
 
-// blockDim = (threads of a row, tokens of a CTA)
-template <class T, bool WIDE>
+// blockDim = (threads of a row, tokens of a CTA).  PHASED: the threads' columns
+// are the output's granules, so only the loads are shifted.
+template <class T, int LAYOUT>
 __global__ void __launch_bounds__(256) embedding_kernel(EmbedArgs a, int tiles) {
-  using L = Tile<T, WIDE>;
-  const int64_t pitch = (int64_t)a.D * L::ES;
+  using L = Tile<T, LAYOUT>;
   for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.tokens;
        t += (int64_t)gridDim.x * blockDim.y) {
     const uint32_t key = key_at(a.ids, a.ids64, t, a.V);
-    const char* src = (const char*)a.table + (int64_t)key * pitch;
     const bool seen = key < a.V;
-    constexpr int AHEAD = WIDE ? 2 : 4;  // tiles in flight
+    const int off = LAYOUT == PHASED ? (int)((t * (a.D % L::N)) % L::N) : 0;
+    constexpr int AHEAD = LAYOUT == NARROW ? 4 : 2;  // tiles in flight
     for (int k = 0; k < tiles; k += AHEAD) {
       typename L::R r[AHEAD];
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
-        const L tile(a.D, k + j);
+        L tile(a.D, k + j);
+        tile.c -= off;
         r[j] = typename L::R{};
-        if (seen && tile.valid()) r[j] = tile.load(src);
+        if (seen && tile.valid()) r[j] = tile.load(a.table, key, a.V);
       }
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
-        const L tile(a.D, k + j);
+        L tile(a.D, k + j);
+        tile.c -= off;
         float f[L::N];
         L::widen(r[j], f);
-        if (tile.valid()) tile.store((char*)a.out + t * pitch, f, seen ? a.scale : 0.0f);
+        if (tile.valid()) tile.store(a.out, t, f, seen ? a.scale : 0.0f, true);
       }
     }
   }
@@ -150,7 +242,7 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
 
 constexpr int kSortWarps = 32;
 constexpr int kSortBits = 9;  // at most, per pass: 32 counters per digit in shared memory
-constexpr int kSortCluster = 8;
+constexpr int kSortCluster = 16;  // (the opt-in size; 60000 tokens: 8 took 20.8 us, 16 take 16.7)
 
 struct SortArgs {
   const void* ids;
@@ -291,7 +383,7 @@ struct SumArgs {
   uint32_t* runs;       // [0] the count of, [1...] the first segments of runs that cross segments
   int64_t tokens, V;
   int64_t segments;
-  int64_t seg_ctas;     // CTAs of the segments; the others fill rows with zeros
+  int64_t seg_ctas;     // the first CTAs, of the segments (or tokens); the others fill rows with zeros
   int D, tiles;
   int zero_rows;        // rows of the table per CTA that fills zeros
   bool ids64;
@@ -342,16 +434,16 @@ __device__ __forceinline__ void fill_rows(const SumArgs& a, const uint32_t* name
 
 // blockDim = (threads of a row, segments of a CTA); segment CTAs come in
 // groups of `tiles`, one column tile each.
-template <class T, bool WIDE>
+template <class T, int LAYOUT>
 __global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
-  using L = Tile<T, WIDE>;
+  using L = Tile<T, LAYOUT>;
   constexpr int N = L::N;
-  const int64_t pitch = (int64_t)a.D * L::ES;
-  if ((int64_t)blockIdx.x >= a.seg_ctas) {
+  const int64_t role = (int64_t)blockIdx.x;
+  if (role >= a.seg_ctas) {
     __shared__ uint32_t named[kMaxZeroRows / 32];
     const int tid = threadIdx.y * blockDim.x + threadIdx.x;
     const int nthr = blockDim.x * blockDim.y;
-    const int64_t v0 = ((int64_t)blockIdx.x - a.seg_ctas) * a.zero_rows;
+    const int64_t v0 = (role - a.seg_ctas) * a.zero_rows;
     const int64_t v1 = v0 + a.zero_rows < a.V ? v0 + a.zero_rows : a.V;
     if (tid < kMaxZeroRows / 32) named[tid] = 0;
     __syncthreads();
@@ -365,8 +457,8 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
     fill_rows<L::ES>(a, named, v0, v1, tid, nthr);
     return;
   }
-  const int tile = (int)(blockIdx.x % a.tiles);
-  const int64_t seg = (int64_t)(blockIdx.x / a.tiles) * blockDim.y + threadIdx.y;
+  const int tile = (int)(role % a.tiles);
+  const int64_t seg = role / a.tiles * blockDim.y + threadIdx.y;
   const L t(a.D, tile);
   if (seg >= a.segments) return;  // the whole team
   const int64_t i0 = seg * kEmbedSegment;
@@ -383,10 +475,10 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
   for (int e = 0; e < N; ++e) acc[e] = 0.0f;
   // the run of `key` ends here (open: it goes on in the next segment)
   auto flush = [&](bool open) {
-    if (key < a.V && t.valid()) {
-      if (head || open) {
+    if (key < a.V) {
+      if ((head || open) && t.valid()) {
         float* p = a.partial + (seg * 2 + (head ? 0 : 1)) * a.D;
-        if constexpr (WIDE) {
+        if constexpr (LAYOUT == WIDE) {
 #pragma unroll
           for (int e = 0; e < N; e += 4)
             *(float4*)(p + t.c + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
@@ -396,8 +488,8 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
             if (t.col(e) < a.D) p[t.col(e)] = acc[e];
         }
         if (!head && tile == 0 && threadIdx.x == 0) a.runs[1 + atomicAdd(a.runs, 1u)] = (uint32_t)seg;
-      } else {
-        t.store((char*)a.gt + (int64_t)key * pitch, acc, a.scale);
+      } else if (!head && !open) {
+        t.store(a.gt, key, acc, a.scale);
       }
     }
 #pragma unroll
@@ -411,7 +503,7 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
       // (lanes past the segment's end hold an id outside the table)
       const uint32_t k = __shfl_sync(0xFFFFFFFFu, mine.x, i + j);
       const uint32_t at = __shfl_sync(0xFFFFFFFFu, mine.y, i + j);
-      if (k < a.V && t.valid()) r[j] = t.load((const char*)a.g + (int64_t)at * pitch);
+      if (k < a.V && t.valid()) r[j] = t.load(a.g, at, a.tokens);
     }
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
@@ -433,17 +525,18 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
   flush(after == key);
 }
 
-// The parts of each run that crosses segments, added: 32 * N columns by 8
-// groups of parts per CTA, group q taking parts q, q + 8, ... (the run's first
-// segment is part 0), then the groups in order.  N: 4 where that divides D.
-template <class T, int N>
+// The parts of each run that crosses segments, added: 128 columns by 8 groups
+// of parts per CTA, group q taking parts q, q + 8, ... (the run's first
+// segment is part 0), then the groups in order.  A lane takes columns 32 apart.
+template <class T>
 __global__ void __launch_bounds__(256) embedding_join_kernel(SumArgs a) {
+  constexpr int N = 4;
   __shared__ float part[8][N][33];
   const int lane = threadIdx.x, q = threadIdx.y;
   const int64_t tiles = (a.D + 32 * N - 1) / (32 * N), items = (int64_t)a.runs[0] * tiles;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int64_t seg = a.runs[1 + it / tiles];
-    const int c = ((int)(it % tiles) * 32 + lane) * N;
+    const int c = (int)(it % tiles) * (32 * N) + lane;
     const int64_t i1 = (seg + 1) * kEmbedSegment;
     const uint32_t key = a.sorted[i1 - 1].x;
     // the parts behind the first: segments that start with the key, 32 at a time
@@ -458,31 +551,23 @@ __global__ void __launch_bounds__(256) embedding_join_kernel(SumArgs a) {
     float v[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = 0.0f;
-    if (c < a.D) {
-#pragma unroll 4
-      for (int64_t j = q; j <= n; j += 8) {
-        const float* at = p + (j ? 2 * j - 1 : 0) * a.D;
-        if constexpr (N == 4) {
-          const float4 f = *(const float4*)at;
-          v[0] = __fadd_rn(v[0], f.x);
-          v[1] = __fadd_rn(v[1], f.y);
-          v[2] = __fadd_rn(v[2], f.z);
-          v[3] = __fadd_rn(v[3], f.w);
-        } else {
-          v[0] = __fadd_rn(v[0], *at);
-        }
-      }
+#pragma unroll 2
+    for (int64_t j = q; j <= n; j += 8) {
+      const float* at = p + (j ? 2 * j - 1 : 0) * a.D;
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (c + 32 * k < a.D) v[k] = __fadd_rn(v[k], at[32 * k]);
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) part[q][k][lane] = v[k];
     __syncthreads();
-    // group q < N finishes column c + q of the lanes
-    if (q < N && c < a.D) {
+    // group q < N finishes the lanes' column q
+    if (q < N && c + 32 * q < a.D) {
       float f[1] = {part[0][q][lane]};
 #pragma unroll
       for (int k = 1; k < 8; ++k) f[0] = __fadd_rn(f[0], part[k][q][lane]);
       f[0] = __fmul_rn(f[0], a.scale);
-      st_stream<sizeof(T)>((char*)a.gt + ((int64_t)key * a.D + c + q) * (int)sizeof(T),
+      st_stream<sizeof(T)>((char*)a.gt + ((int64_t)key * a.D + c + 32 * q) * (int)sizeof(T),
                            Vec<T, (int)sizeof(T)>::narrow(f));
     }
     __syncthreads();  // read before the next item's
@@ -491,17 +576,17 @@ __global__ void __launch_bounds__(256) embedding_join_kernel(SumArgs a) {
 
 // Few tokens, unsorted, in one launch: CTA (token, tile) adds the rows of its
 // token's id if no earlier token has it; the others fill rows with zeros.
-template <class T, bool WIDE>
+template <class T, int LAYOUT>
 __global__ void __launch_bounds__(256) embedding_few_kernel(SumArgs a) {
-  using L = Tile<T, WIDE>;
+  using L = Tile<T, LAYOUT>;
   constexpr int N = L::N;
   __shared__ uint32_t named[kMaxZeroRows / 32];  // (zero rows) a bit per row of the table
   __shared__ uint32_t match[kFewTokens / 32];    // (tokens) a bit per token with this id
-  const int64_t pitch = (int64_t)a.D * L::ES;
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
   const int n = (int)a.tokens;
-  if ((int64_t)blockIdx.x >= a.seg_ctas) {
-    const int64_t v0 = ((int64_t)blockIdx.x - a.seg_ctas) * a.zero_rows;
+  const int64_t role = (int64_t)blockIdx.x;
+  if (role >= a.seg_ctas) {
+    const int64_t v0 = (role - a.seg_ctas) * a.zero_rows;
     const int64_t v1 = v0 + a.zero_rows < a.V ? v0 + a.zero_rows : a.V;
     if (tid < kMaxZeroRows / 32) named[tid] = 0;
     __syncthreads();
@@ -513,7 +598,7 @@ __global__ void __launch_bounds__(256) embedding_few_kernel(SumArgs a) {
     fill_rows<L::ES>(a, named, v0, v1, tid, nthr);
     return;
   }
-  const int me = (int)(blockIdx.x / a.tiles);
+  const int me = (int)(role / a.tiles);
   const uint32_t key = key_at(a.ids, a.ids64, me, a.V);
   if (key >= a.V) return;
   for (int i0 = tid & ~31; i0 < kFewTokens; i0 += nthr) {
@@ -526,8 +611,8 @@ __global__ void __launch_bounds__(256) embedding_few_kernel(SumArgs a) {
     const uint32_t earlier = w < me >> 5 ? 0xFFFFFFFFu : (1u << (me & 31)) - 1u;
     if (match[w] & earlier) return;  // an earlier token adds them
   }
-  const L t(a.D, (int)(blockIdx.x % a.tiles));
-  if (threadIdx.y > 0 || !t.valid()) return;
+  const L t(a.D, (int)(role % a.tiles));
+  if (threadIdx.y > 0) return;  // whole warps
   float acc[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) acc[e] = 0.0f;
@@ -542,12 +627,12 @@ __global__ void __launch_bounds__(256) embedding_few_kernel(SumArgs a) {
         if (!m) continue;
         const int i = w * 32 + __ffs(m) - 1;
         m &= m - 1;
-        r[j] = t.load((const char*)a.g + (int64_t)i * pitch);
+        if (t.valid()) r[j] = t.load(a.g, i, a.tokens);
         got = j + 1;
       }
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
-        if (j >= got) continue;
+        if (j >= got || !t.valid()) continue;
         float f[N];
         L::widen(r[j], f);
 #pragma unroll
@@ -555,13 +640,13 @@ __global__ void __launch_bounds__(256) embedding_few_kernel(SumArgs a) {
       }
     }
   }
-  t.store((char*)a.gt + (int64_t)key * pitch, acc, a.scale);
+  t.store(a.gt, key, acc, a.scale);
 }
 
-template <class T, bool WIDE>
+template <class T, int LAYOUT>
 cudaError_t launch_sums(const DeviceInfo& dev, SumArgs a, cudaStream_t s) {
   const int64_t row_bytes = (int64_t)a.D * (int)sizeof(T);
-  const int n = tile_columns((int)sizeof(T), WIDE);
+  const int n = tile_columns((int)sizeof(T), LAYOUT);
   const int tx = row_threads(a.D, n), ty = 256 / tx;
   a.tiles = (int)row_tiles(a.D, n);
   // about 128 KB of zeros per CTA
@@ -572,19 +657,14 @@ cudaError_t launch_sums(const DeviceInfo& dev, SumArgs a, cudaStream_t s) {
   if (a.seg_ctas + zero_ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(a.seg_ctas + zero_ctas);
   if (few) {
-    embedding_few_kernel<T, WIDE><<<grid, dim3(tx, ty), 0, s>>>(a);
+    embedding_few_kernel<T, LAYOUT><<<grid, dim3(tx, ty), 0, s>>>(a);
     return cudaGetLastError();
   }
-  embedding_sum_kernel<T, WIDE><<<grid, dim3(tx, ty), 0, s>>>(a);
+  embedding_sum_kernel<T, LAYOUT><<<grid, dim3(tx, ty), 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const bool four = a.D % 4 == 0;
-  const int64_t most = (a.segments - 1) * ((a.D + (four ? 127 : 31)) / (four ? 128 : 32));
-  const unsigned join = (unsigned)std::min<int64_t>(most, 8 * dev.sm_count);
-  if (four)
-    embedding_join_kernel<T, 4><<<join, dim3(32, 8), 0, s>>>(a);
-  else
-    embedding_join_kernel<T, 1><<<join, dim3(32, 8), 0, s>>>(a);
+  const int64_t most = (a.segments - 1) * ((a.D + 127) / 128);
+  embedding_join_kernel<T><<<(unsigned)std::min<int64_t>(most, 8 * dev.sm_count), dim3(32, 8), 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -594,8 +674,13 @@ cudaError_t launch_sort(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
   a.per_warp = ((a.tokens + warps - 1) / warps + 31) / 32 * 32;
   const size_t smem = (size_t)kSortWarps * (1 << a.bits) * 4;
   static std::atomic<int> opted[kOptinDevices];
-  const cudaError_t e = allow_shared((const void*)sort_kernel, dev, opted);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = allow_shared((const void*)sort_kernel, dev, opted);
+  if (e == cudaSuccess && a.ctas > 8)
+    e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.ctas);
   cfg.blockDim = dim3(kSortWarps * 32);
@@ -610,30 +695,36 @@ cudaError_t launch_sort(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, sort_kernel, a);
 }
 
+template <class T, class Fn>
+cudaError_t with_layout(int layout, Fn&& fn) {
+  return layout == WIDE     ? fn(TypeTag<T>{}, std::integral_constant<int, WIDE>{})
+         : layout == PHASED ? fn(TypeTag<T>{}, std::integral_constant<int, PHASED>{})
+                            : fn(TypeTag<T>{}, std::integral_constant<int, NARROW>{});
+}
 template <class Fn>
-cudaError_t with_tile(int dtype, bool wide, Fn&& fn) {
-  using Yes = std::true_type;
-  using No = std::false_type;
-  if (dtype == 0) return wide ? fn(TypeTag<__nv_bfloat16>{}, Yes{}) : fn(TypeTag<__nv_bfloat16>{}, No{});
-  if (dtype == 1) return wide ? fn(TypeTag<__half>{}, Yes{}) : fn(TypeTag<__half>{}, No{});
-  return wide ? fn(TypeTag<float>{}, Yes{}) : fn(TypeTag<float>{}, No{});
+cudaError_t with_tile(int dtype, int layout, Fn&& fn) {
+  return dtype == 0   ? with_layout<__nv_bfloat16>(layout, fn)
+         : dtype == 1 ? with_layout<__half>(layout, fn)
+                      : with_layout<float>(layout, fn);
 }
 
 }  // namespace
 
-cudaError_t launch_embedding(int dtype, bool wide, const EmbedArgs& a, cudaStream_t s) {
-  return with_tile(dtype, wide, [&](auto tt, auto w) -> cudaError_t {
+cudaError_t launch_embedding(int dtype, int layout, const EmbedArgs& a, cudaStream_t s) {
+  return with_tile(dtype, layout, [&](auto tt, auto w) -> cudaError_t {
     using T = typename decltype(tt)::type;
-    const int n = tile_columns((int)sizeof(T), wide);
+    constexpr int LAYOUT = decltype(w)::value;
+    const int n = tile_columns((int)sizeof(T), LAYOUT);
     const int tx = row_threads(a.D, n), ty = 256 / tx;
     const int64_t grid = std::min<int64_t>((a.tokens + ty - 1) / ty, int64_t(1) << 30);
-    embedding_kernel<T, decltype(w)::value>
-        <<<(unsigned)grid, dim3(tx, ty), 0, s>>>(a, (int)row_tiles(a.D, n));
+    // PHASED: a row reaches into one granule more
+    const int tiles = (int)((a.D + (LAYOUT == PHASED ? n - 1 : 0) + tx * n - 1) / (tx * n));
+    embedding_kernel<T, LAYOUT><<<(unsigned)grid, dim3(tx, ty), 0, s>>>(a, tiles);
     return cudaGetLastError();
   });
 }
 
-cudaError_t launch_embedding_grad(const DeviceInfo& dev, int dtype, bool wide,
+cudaError_t launch_embedding_grad(const DeviceInfo& dev, int dtype, int layout,
                                   const EmbedGradArgs& a, cudaStream_t s) {
   SumArgs m = {};
   m.gt = a.gt;
@@ -664,7 +755,7 @@ cudaError_t launch_embedding_grad(const DeviceInfo& dev, int dtype, bool wide,
     if (e != cudaSuccess) return e;
     m.sorted = a.pairs[(q.passes - 1) & 1];
   }
-  return with_tile(dtype, wide, [&](auto tt, auto w) -> cudaError_t {
+  return with_tile(dtype, layout, [&](auto tt, auto w) -> cudaError_t {
     return launch_sums<typename decltype(tt)::type, decltype(w)::value>(dev, m, s);
   });
 }
