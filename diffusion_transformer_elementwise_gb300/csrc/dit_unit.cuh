@@ -245,6 +245,30 @@ inline cudaError_t allow_shared(const void* fn, const DeviceInfo& dev, std::atom
   return cudaSuccess;
 }
 
+// A kernel launched by launch_after starts while the one before it in the
+// stream ends: it waits for that one's results (after_previous, before it
+// touches memory), which says early that the next may come (let_next).
+// griddepcontrol waits in hardware.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class Args>
+cudaError_t launch_after(void (*kern)(Args), unsigned grid, dim3 block, size_t smem, cudaStream_t s,
+                         const Args& args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args);
+}
+
 // Units of a row of D columns (PHASED: at most, over the rows' offsets).
 template <class T, int LAYOUT>
 int64_t row_units(int64_t D) {

@@ -5,13 +5,16 @@
 //
 // One launch covers up to kClipBatch tensors: their descriptions travel in the
 // kernel's parameters, so nothing is copied to the device and a captured
-// graph carries them.  A tensor is cut into chunks of 16384 elements, and CTA c of
-// G takes chunks c, c + G, ... over all tensors; each thread sums its elements of a
-// chunk in fp32 (two packed accumulators) and the chunks in fp64.  A chunk's sum that
-// leaves [2^-100, 2^100] (a square that overflowed or went below fp32's
-// normal range) is taken again by its thread in fp64.  Each CTA writes one fp64 partial sum, and every
-// CTA of the second kernel adds them in the same order: the same call gives the same
-// bits.
+// graph carries them.  A tensor is cut into chunks of 16 to 64 KB
+// (smaller for fewer bytes in all, so that every SM has some), and CTA c of G
+// takes chunks c, c + G, ... over all tensors; each thread sums its elements of a
+// chunk in fp32 (two packed accumulators) and the chunks as (high, low) pairs
+// of fp32 (dit_stat.cuh), which cost a tenth of this GPU's fp64.  A chunk's
+// sum that leaves [2^-100, 2^100] (a square that overflowed or went below
+// fp32's normal range) is taken again by its thread in fp64 and kept apart.
+// Each CTA writes one fp64 partial sum, and every CTA of the second kernel
+// adds them in the same order: the same call gives the same bits.  The second kernel takes the chunks
+// from the last, which the L2 still holds, to the first.
 #include <math.h>
 
 #include <algorithm>
@@ -23,8 +26,9 @@
 namespace dit {
 namespace {
 
-constexpr int kChunk = 16384;
-constexpr int kThreads = 256;
+constexpr int kMaxChunk = 64 << 10, kMinChunk = 16 << 10;
+constexpr int kThreads = 512;
+constexpr int kAhead = 4;  // granules of a thread in flight
 
 template <int K>
 struct Batch {
@@ -33,7 +37,7 @@ struct Batch {
   int64_t n[K];
   int32_t first[K + 1];  // the tensors' first chunks
   uint8_t dtype[K];
-  int count;
+  int count, chunk;  // tensors; bytes of a chunk
 };
 
 template <int K>
@@ -87,24 +91,25 @@ __device__ __forceinline__ float element(const void* p, int i) {
   return f[0];
 }
 
-// this thread's sum of the squares of a chunk
+// this thread's sum of the squares of a chunk, added to `sum`, or to `far`
+// when it is out of fp32's range
 template <class T>
-__device__ __forceinline__ double chunk_sum(const char* p, int n) {
+__device__ __forceinline__ void chunk_sum(const char* p, int n, SumPair& sum, double& far) {
   constexpr int ES = (int)sizeof(T), EPG = 16 / ES, P = Granule<T>::P;
   const Span16 s = cut<T>(p, n);
   const char* body = p + s.head * ES;
   const int tid = threadIdx.x;
   F2 acc[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
   uint32_t any = 0;  // a bit of any element but its sign
-  for (int i0 = tid; i0 < s.body; i0 += 4 * kThreads) {
-    Raw<16> r[4];
+  for (int i0 = tid; i0 < s.body; i0 += kAhead * kThreads) {
+    Raw<16> r[kAhead];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kAhead; ++j) {
       r[j] = Raw<16>{};
       if (i0 + j * kThreads < s.body) r[j] = ld_stream<16>(body + (int64_t)(i0 + j * kThreads) * 16);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kAhead; ++j) {
       F2 f[P];
       Granule<T>::widen(r[j], f);
       any |= r[j].w[0] | r[j].w[1] | r[j].w[2] | r[j].w[3];
@@ -119,7 +124,10 @@ __device__ __forceinline__ double chunk_sum(const char* p, int n) {
   acc[0] = f2_add(acc[0], acc[1]);
   const float S = __fmaf_rn(e, e, __fadd_rn(acc[0].x, acc[0].y));
   constexpr uint32_t kBits = ES == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
-  if (fast_sum_in_range(S) || (S == 0.0f && (any & kBits) == 0 && e == 0.0f)) return (double)S;
+  if ((S >= 0x1p-100f && S <= 0x1p100f) || (S == 0.0f && (any & kBits) == 0 && e == 0.0f)) {
+    sum = merge(sum, SumPair{S, 0.0f});
+    return;
+  }
   double d = (double)e * (double)e;
   for (int i = tid; i < s.body; i += kThreads) {
     F2 f[P];
@@ -128,7 +136,7 @@ __device__ __forceinline__ double chunk_sum(const char* p, int n) {
     for (int k = 0; k < P; ++k)
       d += (double)f[k].x * (double)f[k].x + (double)f[k].y * (double)f[k].y;
   }
-  return d;
+  far += d;
 }
 
 template <class F>
@@ -141,45 +149,70 @@ __device__ __forceinline__ void with_type(int dtype, F&& f) {
     f(TypeTag<float>{});
 }
 
-// a value of every thread summed over the CTA, in one order
-__device__ __forceinline__ double cta_sum(double v) {
-  __shared__ double part[kThreads / 32];
+__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double t = 0.0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) t += part[w];
-  return t;
+  return v;
 }
 
 template <int K>
 __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ NormSum<K> a) {
-  double total = 0.0;
+  let_next();
+  __shared__ SumPair pairs[32];
+  __shared__ double fars[kThreads / 32];
+  SumPair sum{0.0f, 0.0f};
+  double far = 0.0;
   const int chunks = a.b.first[a.b.count];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int t = tensor_of(a.b, c);
-    const int64_t at = (int64_t)(c - a.b.first[t]) * kChunk;
-    const int n = (int)min((int64_t)kChunk, a.b.n[t] - at);
     with_type(a.b.dtype[t], [&](auto tag) {
       using T = typename decltype(tag)::type;
-      total += chunk_sum<T>((const char*)a.b.g[t] + at * (int)sizeof(T), n);
+      const int most = a.b.chunk / (int)sizeof(T);
+      const int64_t at = (int64_t)(c - a.b.first[t]) * most;
+      const int n = (int)min((int64_t)most, a.b.n[t] - at);
+      chunk_sum<T>((const char*)a.b.g[t] + at * (int)sizeof(T), n, sum, far);
     });
   }
-  total = cta_sum(total);
-  if (threadIdx.x == 0) a.partial[blockIdx.x] = total;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  sum = warp_merge(sum);
+  if (threadIdx.x < 32) pairs[lane] = SumPair{0.0f, 0.0f};
+  const bool any_far = __syncthreads_or(far != 0.0) != 0;  // (NaN != 0)
+  if (lane == 0) pairs[warp] = sum;
+  if (any_far) {
+    far = warp_sum(far);
+    if (lane == 0) fars[warp] = far;
+  }
+  __syncthreads();
+  if (warp > 0) return;
+  sum = warp_merge(pairs[lane]);
+  if (lane == 0) {
+    double total = (double)sum.h + (double)sum.l;
+    if (any_far)
+      for (int w = 0; w < kThreads / 32; ++w) total += fars[w];
+    a.partial[blockIdx.x] = total;
+  }
 }
 
+// The sum of the partial sums, in one order: by one warp.
 __device__ __forceinline__ double total_of(const double* partial, int64_t n) {
   double v = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += kThreads) v += partial[i];
-  return cta_sum(v);
+#pragma unroll 8
+  for (int64_t i = threadIdx.x & 31; i < n; i += 32) v += partial[i];
+  return warp_sum(v);
+}
+__device__ __forceinline__ float norm_of(double total) {
+  return total >= 0x1p-100 && total <= 0x1p100 ? __fsqrt_rn((float)total) : (float)sqrt(total);
 }
 
-__global__ void __launch_bounds__(kThreads) norm_kernel(const double* partial, int64_t n, float* norm) {
-  const double t = total_of(partial, n);
-  if (threadIdx.x == 0) *norm = (float)sqrt(t);
+struct Norm {
+  const double* partial;
+  int64_t npartial;
+  float* norm;
+};
+__global__ void __launch_bounds__(32) norm_kernel(Norm a) {
+  after_previous();
+  const float n = norm_of(total_of(a.partial, a.npartial));
+  if (threadIdx.x == 0) *a.norm = n;
 }
 
 // granules when g and out are alike modulo 16 bytes, else single elements
@@ -198,13 +231,13 @@ __device__ __forceinline__ void scale_chunk(const char* g, char* out, int n, flo
   const Span16 s = cut<T>(g, n);
   const char* gb = g + s.head * ES;
   char* ob = out + s.head * ES;
-  for (int i0 = tid; i0 < s.body; i0 += 4 * kThreads) {
-    Raw<16> r[4];
+  for (int i0 = tid; i0 < s.body; i0 += kAhead * kThreads) {
+    Raw<16> r[kAhead];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < kAhead; ++j)
       if (i0 + j * kThreads < s.body) r[j] = ld_stream<16>(gb + (int64_t)(i0 + j * kThreads) * 16);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kAhead; ++j) {
       if (i0 + j * kThreads >= s.body) continue;
       F2 f[P];
       Granule<T>::widen(r[j], f);
@@ -218,35 +251,47 @@ __device__ __forceinline__ void scale_chunk(const char* g, char* out, int n, flo
 
 template <int K>
 __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Clip<K> a) {
-  const double norm = sqrt(total_of(a.partial, a.npartial));
-  const double q = (double)a.max_norm / (norm + (double)a.eps);
-  const float c = q > 1.0 ? 1.0f : (float)q;  // NaN stays NaN
-  if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
+  __shared__ float factor;
+  after_previous();
+  if (threadIdx.x < 32) {
+    const float norm = norm_of(total_of(a.partial, a.npartial));
+    const float q = __fdiv_rn(a.max_norm, __fadd_rn(norm, a.eps));
+    if (threadIdx.x == 0) {
+      factor = q > 1.0f ? 1.0f : q;  // NaN stays NaN
+      if (a.norm && blockIdx.x == 0) *a.norm = norm;
+    }
+  }
+  __syncthreads();
+  const float c = factor;
   const int chunks = a.b.first[a.b.count];
-  for (int i = blockIdx.x; i < chunks; i += gridDim.x) {
+  for (int i = chunks - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x) {
     const int t = tensor_of(a.b, i);
-    const int64_t at = (int64_t)(i - a.b.first[t]) * kChunk;
-    const int n = (int)min((int64_t)kChunk, a.b.n[t] - at);
     with_type(a.b.dtype[t], [&](auto tag) {
       using T = typename decltype(tag)::type;
+      const int most = a.b.chunk / (int)sizeof(T);
+      const int64_t at = (int64_t)(i - a.b.first[t]) * most;
+      const int n = (int)min((int64_t)most, a.b.n[t] - at);
       scale_chunk<T>((const char*)a.b.g[t] + at * (int)sizeof(T),
                      (char*)a.b.out[t] + at * (int)sizeof(T), n, c);
     });
   }
 }
 
-// the descriptions of tensors [at, at + K); false when the chunks overflow
+// the descriptions of tensors [at, at + K) in chunks of `chunk` bytes; -1 when there
+// are too many chunks
 template <int K>
-int fill(Batch<K>& b, const ClipTensor* t, int64_t count) {
+int fill(Batch<K>& b, const ClipTensor* t, int64_t count, int chunk) {
   int64_t chunks = 0;
   b.count = (int)std::min<int64_t>(K, count);
+  b.chunk = chunk;
   for (int i = 0; i < b.count; ++i) {
     b.g[i] = t[i].g;
     b.out[i] = t[i].out;
     b.n[i] = t[i].n;
     b.dtype[i] = (uint8_t)t[i].dtype;
     b.first[i] = (int32_t)chunks;
-    chunks += (t[i].n + kChunk - 1) / kChunk;
+    const int most = chunk / (t[i].dtype == 2 ? 4 : 2);
+    chunks += (t[i].n + most - 1) / most;
     if (chunks > 0x7FFFFFFF - kClipMaxCtas) return -1;
   }
   b.first[b.count] = (int32_t)chunks;
@@ -256,40 +301,49 @@ int fill(Batch<K>& b, const ClipTensor* t, int64_t count) {
 template <int K>
 cudaError_t launch(const DeviceInfo& dev, const ClipTensor* t, int64_t count, bool clip,
                    float max_norm, float eps, double* partial, float* norm, cudaStream_t s) {
+  // the smallest chunk that leaves at most 2 chunks per SM
+  double bytes = 0.0;
+  for (int64_t i = 0; i < count; ++i) bytes += (double)t[i].n * (t[i].dtype == 2 ? 4 : 2);
+  int chunk = kMinChunk;
+  while (chunk < kMaxChunk && bytes > 2.0 * dev.sm_count * chunk) chunk *= 2;
   int64_t npartial = 0;
-  auto ctas = [&](int chunks) {
-    return (int)std::min<int64_t>({(int64_t)chunks, kClipMaxCtas, (int64_t)dev.sm_count * 8});
+  auto ctas = [&](const void* fn, int chunks) {
+    const int64_t wave = (int64_t)dev.sm_count * resident_ctas(dev, fn, kThreads);
+    return (unsigned)std::min<int64_t>({(int64_t)chunks, kClipMaxCtas, wave});
   };
   for (int64_t at = 0; at < count; at += K) {
     NormSum<K> a;
-    const int chunks = fill(a.b, t + at, count - at);
+    const int chunks = fill(a.b, t + at, count - at, chunk);
     if (chunks < 0) return cudaErrorInvalidValue;
     if (chunks == 0) continue;
     a.partial = partial + npartial;
-    const int grid = ctas(chunks);
+    const unsigned grid = ctas((const void*)sum_kernel<K>, chunks);
     sum_kernel<K><<<grid, kThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     npartial += grid;
   }
-  if (!clip || npartial == 0) {
-    norm_kernel<<<1, kThreads, 0, s>>>(partial, npartial, norm);
-    return cudaGetLastError();
-  }
+  if (!clip || npartial == 0) return launch_after(norm_kernel, 1, 32, 0, s, Norm{partial, npartial, norm});
   bool first = true;
   for (int64_t at = 0; at < count; at += K) {
     Clip<K> a;
-    const int chunks = fill(a.b, t + at, count - at);
+    const int chunks = fill(a.b, t + at, count - at, chunk);
     if (chunks <= 0) continue;
     a.partial = partial;
     a.npartial = npartial;
     a.max_norm = max_norm;
     a.eps = eps;
     a.norm = first ? norm : nullptr;
-    first = false;
-    clip_kernel<K><<<ctas(chunks), kThreads, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const unsigned grid = ctas((const void*)clip_kernel<K>, chunks);
+    cudaError_t e;
+    if (first) {
+      e = launch_after(clip_kernel<K>, grid, kThreads, 0, s, a);
+    } else {
+      clip_kernel<K><<<grid, kThreads, 0, s>>>(a);
+      e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return e;
+    first = false;
   }
   return cudaSuccess;
 }

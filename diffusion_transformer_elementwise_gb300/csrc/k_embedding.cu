@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_kernel(SortArgs a) {
   const bool once = a.per_warp <= 32 * kRounds;
   uint32_t* mine = count + warp * digits;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.runs = 0;
+  let_next();
 
   for (int p = 0; p < a.passes; ++p) {
     const uint2* src = a.pairs[(p & 1) ^ 1];
@@ -399,7 +400,7 @@ __device__ __forceinline__ int64_t lower_bound(const uint2* sorted, int64_t n, u
   while (hi > lo) {
     const int64_t step = (hi - lo + 31) / 32;
     const int64_t at = lo + step * lane + step - 1;  // the last of this lane's part
-    const bool below = at < hi && __ldg(&sorted[at].x) < key;
+    const bool below = at < hi && sorted[at].x < key;
     const int parts = __popc(__ballot_sync(0xFFFFFFFFu, below));
     lo += step * parts;
     if (lo > hi) lo = hi;
@@ -436,6 +437,8 @@ __device__ __forceinline__ void fill_rows(const SumArgs& a, const uint32_t* name
 // groups of `tiles`, one column tile each.
 template <class T, int LAYOUT>
 __global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
+  let_next();
+  after_previous();
   using L = Tile<T, LAYOUT>;
   constexpr int N = L::N;
   const int64_t role = (int64_t)blockIdx.x;
@@ -465,9 +468,9 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
   const int n = (int)min((int64_t)kEmbedSegment, a.tokens - i0);
   // the segment's tokens, one per lane of each warp
   const int lane = threadIdx.x & 31;
-  const uint2 mine = lane < n ? __ldg(a.sorted + i0 + lane) : make_uint2((uint32_t)a.V, 0u);
-  const uint32_t before = i0 > 0 ? __ldg(&a.sorted[i0 - 1].x) : (uint32_t)a.V;
-  const uint32_t after = i0 + n < a.tokens ? __ldg(&a.sorted[i0 + n].x) : (uint32_t)a.V;
+  const uint2 mine = lane < n ? a.sorted[i0 + lane] : make_uint2((uint32_t)a.V, 0u);
+  const uint32_t before = i0 > 0 ? a.sorted[i0 - 1].x : (uint32_t)a.V;
+  const uint32_t after = i0 + n < a.tokens ? a.sorted[i0 + n].x : (uint32_t)a.V;
   uint32_t key = __shfl_sync(0xFFFFFFFFu, mine.x, 0);
   bool head = i0 > 0 && before == key;
   float acc[N];
@@ -532,6 +535,7 @@ template <class T>
 __global__ void __launch_bounds__(256) embedding_join_kernel(SumArgs a) {
   constexpr int N = 4;
   __shared__ float part[8][N][33];
+  after_previous();
   const int lane = threadIdx.x, q = threadIdx.y;
   const int64_t tiles = (a.D + 32 * N - 1) / (32 * N), items = (int64_t)a.runs[0] * tiles;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
@@ -660,12 +664,11 @@ cudaError_t launch_sums(const DeviceInfo& dev, SumArgs a, cudaStream_t s) {
     embedding_few_kernel<T, LAYOUT><<<grid, dim3(tx, ty), 0, s>>>(a);
     return cudaGetLastError();
   }
-  embedding_sum_kernel<T, LAYOUT><<<grid, dim3(tx, ty), 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(embedding_sum_kernel<T, LAYOUT>, grid, dim3(tx, ty), 0, s, a);
   if (e != cudaSuccess) return e;
   const int64_t most = (a.segments - 1) * ((a.D + 127) / 128);
-  embedding_join_kernel<T><<<(unsigned)std::min<int64_t>(most, 8 * dev.sm_count), dim3(32, 8), 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_after(embedding_join_kernel<T>, (unsigned)std::min<int64_t>(most, 8 * dev.sm_count),
+                      dim3(32, 8), 0, s, a);
 }
 
 cudaError_t launch_sort(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {

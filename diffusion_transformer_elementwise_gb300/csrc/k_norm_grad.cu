@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
   // weights (not NARROW), [warps][stages][streams][NU][32]; in the end the teams' parts of gw
   extern __shared__ float4 shared[];
   Team t(slots);
+  let_next();
   const int lane = t.lane, W = t.warps, m = t.m, team = threadIdx.y, teams = blockDim.y;
   const int ngr = W * NU * 32;  // granules of a row, padded
   const int64_t step = (int64_t)gridDim.x * teams;
@@ -296,21 +297,29 @@ __global__ void __launch_bounds__(1024) grad_long_kernel(NormGradArgs a) {
 
 // gw[c] = the sum of `partial`'s column c over its `n` rows: a CTA takes 32
 // columns, its 32 warps the rows w, w + 32, ..., then their sums in order.
+struct GradWeight {
+  const float* partial;
+  int n, D;
+  void* gw;
+};
 template <class T>
-__global__ void __launch_bounds__(1024) grad_weight_kernel(const float* partial, int n, int D, void* gw) {
+__global__ void __launch_bounds__(1024) grad_weight_kernel(GradWeight a) {
   __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.0f;
-  if (c < D)
-    for (int i = warp; i < n; i += 32) v = __fadd_rn(v, partial[(int64_t)i * D + c]);
+  after_previous();
+  if (c < a.D) {
+#pragma unroll 4
+    for (int i = warp; i < a.n; i += 32) v = __fadd_rn(v, a.partial[(int64_t)i * a.D + c]);
+  }
   part[warp][lane] = v;
   __syncthreads();
   v = warp_sum(part[lane][warp]);  // warp w now holds column w
   const int k = blockIdx.x * 32 + warp;
-  if (lane == 0 && k < D) {
+  if (lane == 0 && k < a.D) {
     float f[1] = {v};
-    st_stream<sizeof(T)>((char*)gw + (int64_t)k * sizeof(T), Vec<T, (int)sizeof(T)>::narrow(f));
+    st_stream<sizeof(T)>((char*)a.gw + (int64_t)k * sizeof(T), Vec<T, (int)sizeof(T)>::narrow(f));
   }
 }
 
@@ -365,8 +374,8 @@ cudaError_t launch(const DeviceInfo& dev, int layout, const NormGradArgs& a, voi
                          : (skip ? launch_rows<T, NARROW, true>(dev, a, &ctas, s)
                                  : launch_rows<T, NARROW, false>(dev, a, &ctas, s));
   if (e != cudaSuccess || !gw) return e;
-  grad_weight_kernel<T><<<(unsigned)((a.D + 31) / 32), 1024, 0, s>>>(a.partial, (int)ctas, a.D, gw);
-  return cudaGetLastError();
+  return launch_after(grad_weight_kernel<T>, (unsigned)((a.D + 31) / 32), 1024, 0, s,
+                      GradWeight{a.partial, (int)ctas, a.D, gw});
 }
 
 }  // namespace

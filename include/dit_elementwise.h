@@ -579,7 +579,8 @@ dit_status dit_embedding_backward(void* grad_table, const void* grad_out, const 
  *   norm   = sqrt(sum over all tensors and elements of g^2)
  *   out[i] = rnd(fl32(g[i] * c)),  c = fl32(min(1, max_norm / (norm + eps)))
  * The squares are summed in fp32 within a thread's few dozen elements and in
- * fp64 beyond (in fp64 throughout where such a sum leaves [2^-100, 2^100]).
+ * pairs of fp32 or in fp64 beyond (in fp64 throughout where such a sum leaves
+ * [2^-100, 2^100]).
  * norm: device, one fp32 (the norm before clipping).  A NaN norm makes
  * c NaN; an infinite one makes c 0.
  *
