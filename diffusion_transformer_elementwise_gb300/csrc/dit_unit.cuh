@@ -222,6 +222,26 @@ struct Team {
   }
 };
 
+// A thread's sum of up to some thousand fp32 terms in three levels, 16 and
+// 256 at a time: at most 16 + 16 + n / 256 roundings on a term's way.
+// Infinities and NaN pass through.
+struct LongSum {
+  float a = 0.0f, b = 0.0f, c = 0.0f;
+  int k = 0;
+  __device__ __forceinline__ void add(float v) {
+    a = __fadd_rn(a, v);
+    if ((++k & 15) == 0) {
+      b = __fadd_rn(b, a);
+      a = 0.0f;
+      if ((k & 255) == 0) {
+        c = __fadd_rn(c, b);
+        b = 0.0f;
+      }
+    }
+  }
+  __device__ __forceinline__ float total() const { return __fadd_rn(__fadd_rn(a, b), c); }
+};
+
 // The most warps of a team's CTA: a row of up to 4 units a warp (64 units,
 // 32 KB) stays in registers at up to 128 of them a thread.
 constexpr int kTeamWarps = 16;

@@ -5,8 +5,8 @@
 //
 // One launch covers up to kClipBatch tensors: their descriptions travel in the
 // kernel's parameters, so nothing is copied to the device and a captured
-// graph carries them.  A tensor is cut into chunks of 16 to 64 KB
-// (smaller for fewer bytes in all, so that every SM has some), and CTA c of G
+// graph carries them.  A tensor is cut into chunks of 16 or 32 KB
+// (the smaller for few bytes in all, so that every SM has some), and CTA c of G
 // takes chunks c, c + G, ... over all tensors; each thread sums its elements of a
 // chunk in fp32 (two packed accumulators) and the chunks as (high, low) pairs
 // of fp32 (dit_stat.cuh), which cost a tenth of this GPU's fp64.  A chunk's
@@ -14,7 +14,7 @@
 // fp32's normal range) is taken again by its thread in fp64 and kept apart.
 // Each CTA writes one fp64 partial sum, and every CTA of the second kernel
 // adds them in the same order: the same call gives the same bits.  The second kernel takes the chunks
-// from the last, which the L2 still holds, to the first.
+// from the last, which the L2 may still hold, to the first.
 #include <math.h>
 
 #include <algorithm>
@@ -26,7 +26,7 @@
 namespace dit {
 namespace {
 
-constexpr int kMaxChunk = 64 << 10, kMinChunk = 16 << 10;
+constexpr int kMaxChunk = 32 << 10, kMinChunk = 16 << 10;
 constexpr int kThreads = 512;
 constexpr int kAhead = 4;  // granules of a thread in flight
 

@@ -482,15 +482,13 @@ __global__ void __launch_bounds__(kTeamThreads, 2) norm_staged_kernel(NormArgs a
 
 // Rows longer than a CTA's registers: one CTA per row, the row read again for
 // the output (with an update, each thread its own stores of the residual).
-// The squares of a unit are summed in fp32 and the units in fp64, so that a
-// thread's thousands of units add no error.
+// A thread's units, thousands of them, are added in levels (LongSum).
 template <class T, int LAYOUT, bool ADD, int Q8>
 __global__ void __launch_bounds__(kTeamThreads) norm_long_kernel(NormArgs a) {
   using R = NormRow<T, LAYOUT>;
   using U = typename R::U;
   constexpr int P = U::P;
   __shared__ float2 slots[2 * kTeamWarps];
-  __shared__ double sums[kTeamWarps];
   Team t(slots);
   const int lane = t.lane, warp = t.m, W = t.warps;
   const U unit(a.D, lane, warp, 1, 0);  // units warp, warp + W, ...
@@ -499,7 +497,7 @@ __global__ void __launch_bounds__(kTeamThreads) norm_long_kernel(NormArgs a) {
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const void* src = ADD ? a.res : a.x;
     const int64_t e = unit.at(row);
-    double total = 0.0;
+    LongSum sum;
     float big = 0.0f;
     for (int j = 0; j < units; j += W) {
       Raw<16> x = unit.load(a.x, e, j);
@@ -512,7 +510,7 @@ __global__ void __launch_bounds__(kTeamThreads) norm_long_kernel(NormArgs a) {
       F2 acc = f2_mul(f[0], f[0]);
 #pragma unroll
       for (int i = 1; i < P; ++i) acc = f2_fma(f[i], f[i], acc);
-      total += (double)__fadd_rn(acc.x, acc.y);
+      sum.add(__fadd_rn(acc.x, acc.y));
       if constexpr (Q8 == 1) {
         F2 wf[P], v[P];
         R::weight(unit.load_weight(a.w, j), a.offset, wf);
@@ -520,34 +518,25 @@ __global__ void __launch_bounds__(kTeamThreads) norm_long_kernel(NormArgs a) {
         big = max_nan(big, R::max_of(v));
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    __syncthreads();  // the previous row's sums have been read
-    if (lane == 0) sums[warp] = total;
-    if constexpr (Q8 == 1) big = t.combine<true>(make_float2(0.0f, warp_max(big))).y;
-    __syncthreads();
-    total = 0.0;
-    for (int w = 0; w < W; ++w) total += sums[w];
-    const float S = (float)total;
+    float2 red = make_float2(warp_sum(sum.total()), 0.0f);
+    if constexpr (Q8 == 1) red.y = warp_max(big);
+    red = t.combine<Q8 == 1>(red);
+    const float S = red.x;
+    big = red.y;
     const float r = inverse_rms(S, a, [&](float sc) {
-      double s2 = 0.0;
+      LongSum again;
       for (int j = 0; j < units; j += W) {
         F2 f[P];
         Granule<T>::widen(unit.load(src, e, j), f);
+        float s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          const double u0 = (double)__fmul_rn(f2_lo(f[i]), sc), u1 = (double)__fmul_rn(f2_hi(f[i]), sc);
-          s2 += u0 * u0 + u1 * u1;
+          const float u0 = __fmul_rn(f2_lo(f[i]), sc), u1 = __fmul_rn(f2_hi(f[i]), sc);
+          s2 = __fmaf_rn(u1, u1, __fmaf_rn(u0, u0, s2));
         }
+        again.add(s2);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
-      __syncthreads();
-      if (lane == 0) sums[warp] = s2;
-      __syncthreads();
-      s2 = 0.0;
-      for (int w = 0; w < W; ++w) s2 += sums[w];
-      return (float)s2;
+      return t.combine<false>(make_float2(warp_sum(again.total()), 0.0f)).x;
     });
 
     bool slow = false;

@@ -129,8 +129,9 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
   __shared__ float2 slots[2 * kGradWarps<NU>];
   // weights (not NARROW), [warps][stages][streams][NU][32]; in the end the teams' parts of gw
   extern __shared__ float4 shared[];
-  Team t(slots);
   let_next();
+  if (blockIdx.x >= a.rows) return;  // (the grid is rounded up for PHASED rows)
+  Team t(slots);
   const int lane = t.lane, W = t.warps, m = t.m, team = threadIdx.y, teams = blockDim.y;
   const int ngr = W * NU * 32;  // granules of a row, padded
   const int64_t step = (int64_t)gridDim.x * teams;
@@ -240,12 +241,13 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
 // Rows longer than a CTA's registers: read twice, gw added in the CTA's row
 // of `partial` itself (each column by one thread).
 template <class T, int LAYOUT>
-__global__ void __launch_bounds__(1024) grad_long_kernel(NormGradArgs a) {
+__global__ void __launch_bounds__(kTeamThreads) grad_long_kernel(NormGradArgs a) {
   using R = GradRow<T, LAYOUT>;
   using U = typename R::U;
   constexpr int P = U::P;
-  __shared__ double2 part[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  __shared__ float2 slots[2 * kTeamWarps];
+  Team t(slots);
+  const int lane = t.lane, warp = t.m, W = t.warps;
   const U unit(a.D, lane, warp, 1, 0);  // units warp, warp + W, ...
   const int units = (a.D + U::COLS - 1) / U::COLS - warp;  // from this warp's first
   float* out = a.partial ? a.partial + (int64_t)blockIdx.x * a.D : nullptr;
@@ -253,29 +255,16 @@ __global__ void __launch_bounds__(1024) grad_long_kernel(NormGradArgs a) {
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, first = false) {
     const int64_t e = unit.at(row);
     auto sums = [&](float sc) {
-      double2 v = make_double2(0.0, 0.0);
+      LongSum xx, tx;
       for (int j = 0; j < units; j += W) {
         F2 s = f2(0.0f, 0.0f), q = s;
         F2 w[P];
         R::weight(unit, a, j, w);
         R::sums(unit.load(a.x, e, j), unit.load(a.g, e, j), w, sc, s, q);
-        v.x += (double)__fadd_rn(s.x, s.y);
-        v.y += (double)__fadd_rn(q.x, q.y);
+        xx.add(__fadd_rn(s.x, s.y));
+        tx.add(__fadd_rn(q.x, q.y));
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
-        v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
-      }
-      __syncthreads();  // the previous sums have been read
-      if (lane == 0) part[warp] = v;
-      __syncthreads();
-      v = make_double2(0.0, 0.0);
-      for (int k = 0; k < W; ++k) {
-        v.x += part[k].x;
-        v.y += part[k].y;
-      }
-      return make_float2((float)v.x, (float)v.y);
+      return t.combine<false>(make_float2(warp_sum(xx.total()), warp_sum(tx.total())));
     };
     const RowStat st = row_stat(sums(1.0f), a, sums);
     for (int j = 0; j < units; j += W) {
@@ -346,7 +335,7 @@ cudaError_t launch_rows(const DeviceInfo& dev, NormGradArgs a, int64_t* ctas, cu
     cudaError_t e = allow_shared((const void*)kern, dev, opted);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)grid, dim3((unsigned)warps * 32, (unsigned)teams), smem, s>>>(a);
-    *ctas = grid;
+    *ctas = std::min(grid, a.rows);
     return cudaGetLastError();
   };
   if (units <= 8) return team(std::integral_constant<int, 1>{});
@@ -355,8 +344,8 @@ cudaError_t launch_rows(const DeviceInfo& dev, NormGradArgs a, int64_t* ctas, cu
   if constexpr (LAYOUT == PHASED) {
     return launch_rows<T, NARROW, SKIP>(dev, a, ctas, s);
   } else {
-    *ctas = std::min<int64_t>(dev.sm_count, a.rows);
-    grad_long_kernel<T, LAYOUT><<<(unsigned)*ctas, 1024, 0, s>>>(a);
+    *ctas = std::min(std::min<int64_t>(2 * dev.sm_count, a.rows), kNormGradMaxCtas);
+    grad_long_kernel<T, LAYOUT><<<(unsigned)*ctas, kTeamThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
 }
