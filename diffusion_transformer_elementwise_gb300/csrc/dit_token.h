@@ -8,7 +8,7 @@ namespace dit {
 
 // How the rows of a call's tensors are accessed (Unit of dit_unit.cuh, Tile of
 // k_embedding.cu).
-enum Layout { WIDE, PHASED, NARROW };
+enum Layout { WIDE, PHASED, NARROW, SHIFTED };
 
 // Weighted RMSNorm over `rows` rows of D elements (k_norm.cu).
 struct NormArgs {
@@ -34,6 +34,7 @@ cudaError_t launch_norm(const DeviceInfo& dev, int dtype, int layout, int q8, co
 // Its gradient (k_norm_grad.cu).
 struct NormGradArgs {
   void* gx;
+  void* gw;         // the weight's gradient, where the launcher has it written at once
   float* partial;   // [ctas, D] sums of the weight's gradient, or NULL
   const void* g;    // gradient of the normed output
   const void* gres; // gradient arriving on the skip path, or NULL
@@ -46,6 +47,9 @@ struct NormGradArgs {
 };
 // the most CTAs (rows of `partial`) a call takes
 constexpr int64_t kNormGradMaxCtas = 304;
+// Up to this many rows that stay in registers take one launch; up to this
+// width they do in every type and layout, and the call needs no workspace.
+constexpr int64_t kFewRows = 128, kFewRowsD = 8189;
 // gw: the weight's gradient, or NULL
 cudaError_t launch_norm_grad(const DeviceInfo& dev, int dtype, int layout, const NormGradArgs& a,
                              void* gw, cudaStream_t s);

@@ -145,6 +145,7 @@ dit_status dit_add_rmsnorm_fp8(void* residual_out, void* out, float* scales, con
 int64_t dit_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t D) {
   int64_t n;
   if (!row_shape(rows, D, 4, &n)) return -1;
+  if (rows <= dit::kFewRows && D <= dit::kFewRowsD) return 0;
   return round_up(std::min(rows, dit::kNormGradMaxCtas) * D * 4);
 }
 
@@ -165,7 +166,7 @@ dit_status dit_rmsnorm_backward(void* grad_x, void* grad_weight, const void* gra
       misaligned(grad_residual, es) || misaligned(x, es) || misaligned(weight, es))
     return DIT_ERR_MISALIGNED;
   const int64_t need = dit_rmsnorm_backward_workspace_bytes(rows, D);
-  const bool use_ws = grad_weight && n > 0;
+  const bool use_ws = grad_weight && n > 0 && need > 0;
   if (use_ws) {
     const dit_status st = workspace_status(workspace, workspace_bytes, need);
     if (st != DIT_OK) return st;
@@ -190,7 +191,7 @@ dit_status dit_rmsnorm_backward(void* grad_x, void* grad_weight, const void* gra
   }
   dit::NormGradArgs a = {};
   a.gx = grad_x;
-  a.partial = grad_weight ? (float*)workspace : nullptr;
+  a.partial = use_ws ? (float*)workspace : nullptr;
   a.g = grad_out;
   a.gres = grad_residual;
   a.x = x;

@@ -13,9 +13,13 @@
 //            belong to the neighbours: they read as zero and are not stored.
 //            Rows whose numbers differ by a multiple of EPL (elements per
 //            granule) have the same `off`.
+//   SHIFTED  the same rows, for work on fixed blocks of columns: the granules
+//            are copied as they lie (and one more for the warp), and each lane takes its
+//            16 bytes from column c0 + EPL l on out of two of them; stores
+//            pass the elements on to the lane that has the rest of a granule.
 //   NARROW   a tensor that starts off a 16-byte boundary.  Lane l's element i is
 //            column 32 i + l, one element per access.
-// The arithmetic is the same for all three.  Columns past the row read as
+// The arithmetic is the same for all.  Columns past the row read as
 // zero and are not stored.
 #pragma once
 
@@ -46,6 +50,27 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// The 16 bytes that start s elements (0 < s < 16 / ES) into the 32 bytes lo,
+// hi.  s is the same for the whole warp.
+template <int ES>
+__device__ __forceinline__ Raw<16> shifted(const Raw<16>& lo, const Raw<16>& hi, int s) {
+  const int q = s * ES / 4;  // whole words
+  uint32_t a[6], b[5];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    const uint32_t x = i < 4 ? lo.w[i] : hi.w[i - 4];
+    const uint32_t y = i + 2 < 4 ? lo.w[i + 2] : hi.w[i - 2];
+    a[i] = q & 2 ? y : x;
+  }
+#pragma unroll
+  for (int i = 0; i < 5; ++i) b[i] = q & 1 ? a[i + 1] : a[i];
+  const uint32_t bits = ES == 2 && (s & 1) ? 16u : 0u;
+  Raw<16> r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.w[i] = __funnelshift_r(b[i], b[i + 1], bits);
+  return r;
+}
+
 // The units of one warp: `units` of them from unit `first` of the row.  j
 // counts them; e is the tensor's element index of the lane's first column
 // (at()), so that an access is one base address and a constant offset.
@@ -56,16 +81,20 @@ struct Unit {
   static constexpr int COLS = 32 * EPL;     // columns of a unit
   static constexpr int P = Granule<T>::P;   // fp32 pairs per lane
 
-  int D, lane;
-  int off;     // PHASED: the row's offset from a granule's start, elements
+  static constexpr bool OFFSET = LAYOUT == PHASED || LAYOUT == SHIFTED;
+  int D, lane, units;
+  int off;     // OFFSET: the row's offset from a granule's start, elements
   int c;       // the lane's first column (PHASED: negative in a granule shared with the row before)
   bool edges;  // PHASED: the warp holds a granule shared with a neighbouring row
+  // SHIFTED: what lane 31 held of the unit before
+  Raw<16> last;
+  uint64_t last8;
 
   // rows row, row + 8 k, ...
   __device__ __forceinline__ Unit(int D, int lane, int first, int units, int64_t row)
-      : D(D), lane(lane), off(0), edges(false) {
-    if constexpr (LAYOUT == PHASED) off = (int)(((uint64_t)row * (uint64_t)(D % EPL)) % EPL);
-    c = first * COLS + (LAYOUT == NARROW ? lane : lane * EPL - off);
+      : D(D), lane(lane), units(units), off(0), edges(false), last{}, last8(0) {
+    if constexpr (OFFSET) off = (int)(((uint64_t)row * (uint64_t)(D % EPL)) % EPL);
+    c = first * COLS + (LAYOUT == NARROW ? lane : LAYOUT == PHASED ? lane * EPL - off : lane * EPL);
     if constexpr (LAYOUT == PHASED) {
       bool mine = false;
       for (int j = 0; j < units; ++j) mine = mine || (valid(j) && !whole(j));
@@ -109,7 +138,7 @@ struct Unit {
   }
   // activations, read once (WIDE, NARROW)
   __device__ __forceinline__ Raw<16> load(const void* tensor, int64_t e, int j) const {
-    static_assert(LAYOUT != PHASED, "PHASED rows are copied");
+    static_assert(!OFFSET, "rows at an offset are copied");
     if constexpr (LAYOUT == NARROW) {
       return elements<true>(ptr(tensor, e, j), j);
     } else {
@@ -120,7 +149,7 @@ struct Unit {
   }
   // weights, read by every row
   __device__ __forceinline__ Raw<16> load_weight(const void* w, int j) const {
-    if constexpr (LAYOUT != WIDE) {
+    if constexpr (LAYOUT != WIDE) {  // (any alignment)
       return elements<false>(ptr(w, c, j), j);
     } else {
       Raw<16> r = {};
@@ -129,15 +158,20 @@ struct Unit {
     }
   }
   // Copy the lane's granule of unit j to its slot at shared address dst
-  // (cp.async; WIDE, PHASED): the row's bytes from the granule's start on, zeros after
+  // (cp.async; not NARROW): the row's bytes from the granule's start on, zeros after
   // them, nothing past the row's end is read.
   __device__ __forceinline__ void copy(uint32_t dst, const void* tensor, int64_t e, int j) const {
-    const int left = (D - col(j, 0)) * ES;
-    cp_async16_part(dst, ptr(tensor, e, j), (uint32_t)(left < 0 ? 0 : left > 16 ? 16 : left));
+    const int back = LAYOUT == SHIFTED ? off : 0;
+    const int left = (D - col(j, 0) + back) * ES;
+    cp_async16_part(dst, ptr(tensor, e - back, j), (uint32_t)(left < 0 ? 0 : left > 16 ? 16 : left));
   }
-  // what copy() left in the slot, without the row before
+  // what copy() left in the slot, without the row before (SHIFTED: the lane's
+  // elements of it and the next slot, after a __syncwarp)
   __device__ __forceinline__ Raw<16> copied(uint32_t src, int j) const {
     Raw<16> r = lds16(src);
+    if constexpr (LAYOUT == SHIFTED) {
+      if (off) r = shifted<ES>(r, lds16(src + 16), off);
+    }
     if (LAYOUT == PHASED && j == 0 && c < 0) {
 #pragma unroll
       for (int i = 0; i < EPL - 1; ++i) {
@@ -150,30 +184,90 @@ struct Unit {
     }
     return r;
   }
-  __device__ __forceinline__ void store(void* tensor, int64_t e, int j, const Raw<16>& r) const {
+  // SHIFTED: the granule of unit j that starts `off` elements before the
+  // lane's first; elements [from, ...) of it are the warp's
+  __device__ __forceinline__ int from(int j) const { return lane == 0 && j == 0 ? off : 0; }
+  // (SHIFTED: the whole warp, units in order)
+  __device__ __forceinline__ void store(void* tensor, int64_t e, int j, const Raw<16>& r) {
     char* p = (char*)ptr(tensor, e, j);
-    if constexpr (LAYOUT != NARROW) {
-      if (whole(j)) st_stream<16>(p, r);
-      if (LAYOUT == WIDE || !edges) return;
-    }
-    if (LAYOUT == PHASED && (whole(j) || !valid(j))) return;
-    constexpr int S = LAYOUT == NARROW ? 32 * ES : ES;
+    if constexpr (LAYOUT == SHIFTED) {
+      Raw<16> g = r;
+      if (off) {
+        Raw<16> before;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (col(j, i) >= 0 && col(j, i) < D) st_stream<ES>(p + i * S, get(r, i));
+        for (int i = 0; i < 4; ++i) {
+          before.w[i] = __shfl_up_sync(0xFFFFFFFFu, r.w[i], 1);
+          if (lane == 0) before.w[i] = last.w[i];
+          last.w[i] = __shfl_sync(0xFFFFFFFFu, r.w[i], 31);
+        }
+        g = shifted<ES>(before, r, EPL - off);
+      }
+      const int c0 = col(j, 0) - off, lo = from(j);
+      if (lo == 0 && c0 + EPL <= D) {
+        st_stream<16>(p - off * ES, g);
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (i >= lo && c0 + i < D) st_stream<ES>(p + (i - off) * ES, get(g, i));
+      }
+      if (j == units - 1 && lane == 31) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (i >= EPL - off && col(j, i) < D) st_stream<ES>(p + i * ES, get(r, i));
+      }
+    } else {
+      if constexpr (LAYOUT != NARROW) {
+        if (whole(j)) st_stream<16>(p, r);
+        if (LAYOUT == WIDE || !edges) return;
+      }
+      if (LAYOUT == PHASED && (whole(j) || !valid(j))) return;
+      constexpr int S = LAYOUT == NARROW ? 32 * ES : ES;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (col(j, i) >= 0 && col(j, i) < D) st_stream<ES>(p + i * S, get(r, i));
+    }
   }
-  // one byte per element, element i in byte i of q
-  __device__ __forceinline__ void store8(void* tensor, int64_t e, int j, const Raw<EPL>& q) const {
+  // one byte per element, element i in byte i of q (SHIFTED: the whole warp,
+  // units in order)
+  __device__ __forceinline__ void store8(void* tensor, int64_t e, int j, const Raw<EPL>& q) {
     char* p = (char*)tensor + e + j * COLS;
-    if constexpr (LAYOUT != NARROW) {
-      if (whole(j)) st_stream<EPL>(p, q);
-      if (LAYOUT == WIDE || !edges) return;
-    }
-    if (LAYOUT == PHASED && (whole(j) || !valid(j))) return;
-    constexpr int S = LAYOUT == NARROW ? 32 : 1;
+    if constexpr (LAYOUT == SHIFTED) {
+      uint64_t own = q.w[0];
+      if constexpr (EPL == 8) own |= (uint64_t)q.w[EPL / 4 - 1] << 32;
+      uint64_t g = own;
+      if (off) {
+        uint64_t before = __shfl_up_sync(0xFFFFFFFFu, own, 1);
+        if (lane == 0) before = last8;
+        last8 = __shfl_sync(0xFFFFFFFFu, own, 31);
+        g = (before >> (8 * (EPL - off))) | (own << (8 * off));
+      }
+      const int c0 = col(j, 0) - off, lo = from(j);
+      if (lo == 0 && c0 + EPL <= D) {
+        Raw<EPL> v;
+        v.w[0] = (uint32_t)g;
+        if constexpr (EPL == 8) v.w[EPL / 4 - 1] = (uint32_t)(g >> 32);
+        st_stream<EPL>(p - off, v);
+      } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (col(j, i) >= 0 && col(j, i) < D) p[i * S] = (char)(q.w[i >> 2] >> (8 * (i & 3)));
+        for (int i = 0; i < EPL; ++i)
+          if (i >= lo && c0 + i < D) p[i - off] = (char)(g >> (8 * i));
+      }
+      if (j == units - 1 && lane == 31) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (i >= EPL - off && col(j, i) < D) p[i] = (char)(own >> (8 * i));
+      }
+    } else {
+      if constexpr (LAYOUT != NARROW) {
+        if (whole(j)) st_stream<EPL>(p, q);
+        if (LAYOUT == WIDE || !edges) return;
+      }
+      if (LAYOUT == PHASED && (whole(j) || !valid(j))) return;
+      constexpr int S = LAYOUT == NARROW ? 32 : 1;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (col(j, i) >= 0 && col(j, i) < D) p[i * S] = (char)(q.w[i >> 2] >> (8 * (i & 3)));
+    }
   }
 };
 
@@ -265,6 +359,19 @@ inline cudaError_t allow_shared(const void* fn, const DeviceInfo& dev, std::atom
   return cudaSuccess;
 }
 
+// A barrier of the cluster's CTAs (a hardware wait), which orders their shared
+// and global accesses; a word of the shared memory of its CTA `rank`.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t remote, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  return v;
+}
+
 // A kernel launched by launch_after starts while the one before it in the
 // stream ends: it waits for that one's results (after_previous, before it
 // touches memory), which says early that the next may come (let_next).
@@ -284,6 +391,32 @@ cudaError_t launch_after(void (*kern)(Args), unsigned grid, dim3 block, size_t s
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args);
+}
+
+// A launch of one cluster of `grid` CTAs (16: the size that a kernel opts in to).
+template <class Args>
+cudaError_t launch_cluster(void (*kern)(Args), unsigned grid, dim3 block, size_t smem, cudaStream_t s,
+                           const Args& args) {
+  if (grid > 8) {
+    const cudaError_t e =
+        cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) {
+      (void)cudaGetLastError();
+      return e;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = grid;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args);

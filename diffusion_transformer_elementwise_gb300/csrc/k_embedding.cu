@@ -33,27 +33,6 @@ __device__ __forceinline__ uint32_t key_at(const void* ids, bool ids64, int64_t 
   return id >= 0 && id < V ? (uint32_t)id : (uint32_t)V;
 }
 
-// The 16 bytes that start s elements (0 < s < 16 / ES) into the 32 bytes lo,
-// hi.  s is the same for the whole warp.
-template <int ES>
-__device__ __forceinline__ Raw<16> shifted(const Raw<16>& lo, const Raw<16>& hi, int s) {
-  const int q = s * ES / 4;  // whole words
-  uint32_t a[6], b[5];
-#pragma unroll
-  for (int i = 0; i < 6; ++i) {
-    const uint32_t x = i < 4 ? lo.w[i] : hi.w[i - 4];
-    const uint32_t y = i + 2 < 4 ? lo.w[i + 2] : hi.w[i - 2];
-    a[i] = q & 2 ? y : x;
-  }
-#pragma unroll
-  for (int i = 0; i < 5; ++i) b[i] = q & 1 ? a[i + 1] : a[i];
-  const uint32_t bits = ES == 2 && (s & 1) ? 16u : 0u;
-  Raw<16> r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.w[i] = __funnelshift_r(b[i], b[i + 1], bits);
-  return r;
-}
-
 // The 16 bytes that start at element e (>= 0) of a tensor of `total` elements
 // whose first byte is 16-byte aligned: two granules and a shift, which is the
 // same for every lane (their e are alike modulo a granule).  Elements past
@@ -228,17 +207,6 @@ __global__ void __launch_bounds__(256) embedding_kernel(EmbedArgs a, int tiles) 
 // ---------------------------------------------------------------------------
 // the sort
 // ---------------------------------------------------------------------------
-
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
-  uint32_t remote, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-  return v;
-}
 
 constexpr int kSortWarps = 32;
 constexpr int kSortBits = 9;  // at most, per pass: 32 counters per digit in shared memory
@@ -677,25 +645,9 @@ cudaError_t launch_sort(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
   a.per_warp = ((a.tokens + warps - 1) / warps + 31) / 32 * 32;
   const size_t smem = (size_t)kSortWarps * (1 << a.bits) * 4;
   static std::atomic<int> opted[kOptinDevices];
-  cudaError_t e = allow_shared((const void*)sort_kernel, dev, opted);
-  if (e == cudaSuccess && a.ctas > 8)
-    e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) {
-    (void)cudaGetLastError();
-    return e;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.ctas);
-  cfg.blockDim = dim3(kSortWarps * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = a.ctas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sort_kernel, a);
+  const cudaError_t e = allow_shared((const void*)sort_kernel, dev, opted);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(sort_kernel, (unsigned)a.ctas, kSortWarps * 32, smem, s, a);
 }
 
 template <class T, class Fn>

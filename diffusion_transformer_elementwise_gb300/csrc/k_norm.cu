@@ -69,8 +69,8 @@ struct NormRow {
   // 128-column groups of a unit whose maxima a lane helps to find, and the
   // lanes that share one
   static constexpr int NG = LAYOUT == NARROW && sizeof(T) == 2 ? 2 : 1;
-  static constexpr int LANES = LAYOUT != NARROW && sizeof(T) == 2 ? 16 : 32;
-  static constexpr int BLOCKS = 32 / LANES * NG;  // groups of a unit
+  [[maybe_unused]] static constexpr int LANES = LAYOUT != NARROW && sizeof(T) == 2 ? 16 : 32;
+  [[maybe_unused]] static constexpr int BLOCKS = 32 / LANES * NG;  // groups of a unit
 
   // hidden + update, rounded (the first value alone without an update)
   __device__ __forceinline__ static Raw<16> add(const Raw<16>& h, const Raw<16>& u) {
@@ -142,7 +142,7 @@ struct NormRow {
 
   // unit j of the output, one scale per 128 columns (the whole warp calls;
   // k: the group of this lane's first column; its groups lie inside the unit)
-  __device__ __forceinline__ static void emit_groups(const NormArgs& a, const U& unit, int64_t row,
+  __device__ __forceinline__ static void emit_groups(const NormArgs& a, U& unit, int64_t row,
                                                      int64_t e, int j, int k, const Raw<16>& x,
                                                      const F2 (&w)[P], float S, float r) {
     F2 v[P];
@@ -178,37 +178,6 @@ struct NormRow {
         if (k + g < a.groups) a.scales[row * a.groups + k + g] = q[g].scale;
     }
   }
-
-  // PHASED rows: a group's first column is element `off` of a granule, so
-  // the granule's first `off` elements belong to the group before it, which
-  // another warp may hold.  The maxima of a lane's own group and of that head (first
-  // lanes of a group; else zero).
-  __device__ __forceinline__ static void split_max(const F2 (&v)[P], const U& unit, float& own,
-                                                   float& head) {
-    float a = 0.0f, b = 0.0f;  // elements before `off` (one value for the warp), and from it
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      if (2 * i < unit.off) a = max_abs3(a, a, f2_lo(v[i])); else b = max_abs3(b, b, f2_lo(v[i]));
-      if (2 * i + 1 < unit.off) a = max_abs3(a, a, f2_hi(v[i])); else b = max_abs3(b, b, f2_hi(v[i]));
-    }
-    const bool first = unit.lane % LANES == 0;
-    head = first ? a : 0.0f;
-    own = first ? b : max_nan(a, b);
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1)
-      own = max_nan(own, __shfl_xor_sync(0xFFFFFFFFu, own, o));
-  }
-  // codes with the factor `before` for the first `cut` elements
-  __device__ __forceinline__ static Raw<U::EPL> split_codes(const F2 (&v)[P], int cut, float before,
-                                                            float mul) {
-    F2 s[P];
-    Quant one[NG];
-    one[0].mul = 1.0f;
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-      s[i] = f2_mul(v[i], f2(2 * i < cut ? before : mul, 2 * i + 1 < cut ? before : mul));
-    return codes(s, one);
-  }
 };
 
 // r of a row from its fp32 sum of squares S; a sum outside the usable range
@@ -221,20 +190,18 @@ __device__ __forceinline__ float inverse_rms(float S, const NormArgs& a, Again a
 }
 
 // One row held by a team: its statistic, then its output.  e: unit.at(row);
-// x: the lane's granules; weights(j, wf): unit j's weights, offset added; after_read(): called once the sums
-// have been formed (the caller's next copies).  kSplit: PHASED groups of 128, whose
-// pieces go through `pieces`, [2][groups of the team's warps].
+// x: the lane's granules; weights(j, wf): unit j's weights, offset added;
+// after_read(): called once the sums have been formed (the caller's next
+// copies).
 template <class T, int LAYOUT, int NU, int Q8, class Weights, class AfterRead>
-__device__ __forceinline__ void finish_row(const NormArgs& a, const Unit<T, LAYOUT>& unit, Team& t,
+__device__ __forceinline__ void finish_row(const NormArgs& a, Unit<T, LAYOUT>& unit, Team& t,
                                            int64_t row, int64_t e, const Raw<16> (&x)[NU], Weights weights,
-                                           AfterRead after_read, float2* pieces) {
+                                           AfterRead after_read) {
   using R = NormRow<T, LAYOUT>;
   using U = Unit<T, LAYOUT>;
   constexpr int P = U::P;
-  constexpr bool kSplit = LAYOUT == PHASED && Q8 == 2;
-  const int m = t.m, W = t.warps, lane = t.lane;
-  const int n = W * NU * R::BLOCKS;  // groups of 128 the team's units reach
-  auto piece = [&](int j) { return (m * NU + j) * R::BLOCKS + lane / R::LANES; };
+  static_assert(!(LAYOUT == PHASED && Q8 == 2), "groups of columns: SHIFTED");
+  const int m = t.m, lane = t.lane;
 
   F2 acc[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
   float big = 0.0f;
@@ -244,28 +211,18 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Unit<T, LAYO
     Granule<T>::widen(x[j], f);
 #pragma unroll
     for (int i = 0; i < P; ++i) acc[i & 1] = f2_fma(f[i], f[i], acc[i & 1]);
-    if constexpr (Q8 == 1 || kSplit) {
+    if constexpr (Q8 == 1) {
       F2 wf[P], v[P];
       weights(j, wf);
       R::weighted(x[j], wf, v);
-      if constexpr (kSplit) {
-        float own, head;
-        R::split_max(v, unit, own, head);
-        if (lane % R::LANES == 0) pieces[t.par * n + piece(j)] = make_float2(own, head);
-        const bool bad = (own != 0.0f && !usable(own)) || (head != 0.0f && !usable(head));
-        big = bad ? 1.0f : big;
-      } else {
-        big = max_nan(big, R::max_of(v));
-      }
+      big = max_nan(big, R::max_of(v));
     }
   }
   after_read();
   acc[0] = f2_add(acc[0], acc[1]);
   float2 red = make_float2(warp_sum(__fadd_rn(acc[0].x, acc[0].y)), 0.0f);
   if constexpr (Q8 == 1) red.y = warp_max(big);
-  if constexpr (kSplit) red.y = __any_sync(0xFFFFFFFFu, big != 0.0f) ? 1.0f : 0.0f;
-  [[maybe_unused]] int par = t.par;
-  red = t.combine<Q8 == 1 || kSplit>(red);
+  red = t.combine<Q8 == 1>(red);
   const float r = inverse_rms(red.x, a, [&](float sc) {
     float s2 = 0.0f;
 #pragma unroll
@@ -289,14 +246,15 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Unit<T, LAYO
       R::normed(x[j], wf, r, y);
       unit.store(a.out, e, j, Granule<T>::narrow(y));
     }
-  } else if constexpr (Q8 == 2 && !kSplit) {
+  } else if constexpr (Q8 == 2) {
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
       F2 wf[P];
       weights(j, wf);
-      R::emit_groups(a, unit, row, e, j, piece(j), x[j], wf, red.x, r);
+      const int k = (m * NU + j) * R::BLOCKS + lane / R::LANES;  // this lane's group
+      R::emit_groups(a, unit, row, e, j, k, x[j], wf, red.x, r);
     }
-  } else if constexpr (!kSplit) {
+  } else {
     // one scale per row
     auto emit = [&](Quant q, auto values) {
       Quant all[R::NG];
@@ -331,61 +289,6 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Unit<T, LAYO
         R::scale_by(v, f);
       });
     }
-  } else {
-    // groups that cross granules, units and warps
-    const bool slow = !usable(red.x) || red.y != 0.0f;
-    auto values = [&](int j, F2(&v)[P]) {
-      F2 wf[P];
-      weights(j, wf);
-      if (slow) {
-        R::normed(x[j], wf, r, v);
-        R::mask(v, unit, j);
-      } else {
-        R::weighted(x[j], wf, v);
-      }
-    };
-    if (slow) {  // rare, uniform over the row's threads: the maxima of y
-      par = t.par;
-#pragma unroll
-      for (int j = 0; j < NU; ++j) {
-        F2 y[P];
-        values(j, y);
-        float own, head;
-        R::split_max(y, unit, own, head);
-        if (lane % R::LANES == 0) pieces[par * n + piece(j)] = make_float2(own, head);
-      }
-      t.combine<true>(make_float2(0.0f, 0.0f));
-    }
-    if (W == 1) __syncwarp();
-    const float2* g = pieces + par * n;
-    // group k's maximum: its own part, and the next one's head
-    auto maximum = [&](int k) { return k + 1 < n ? max_nan(g[k].x, g[k + 1].y) : g[k].x; };
-#pragma unroll
-    for (int j = 0; j < NU; ++j) {
-      F2 v[P];
-      values(j, v);
-      const int k = piece(j);
-      const int cut = lane % R::LANES == 0 ? unit.off : 0;
-      const float big = maximum(k), prev = cut && k > 0 ? maximum(k - 1) : big;
-      Quant mine, before;
-      if (slow) {
-        mine = quant_of_y(big);
-        before = quant_of_y(prev);
-        const float f = small_factor(big), b = small_factor(prev);
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-          v[i] = f2_mul(v[i], f2(2 * i < cut ? b : f, 2 * i + 1 < cut ? b : f));
-      } else {
-        mine = quant_of_t(big, r);
-        before = quant_of_t(prev, r);
-      }
-      unit.store8(a.out, e, j, R::split_codes(v, cut, before.mul, mine.mul));
-      if (lane % R::LANES == 0 && k < a.groups) a.scales[row * a.groups + k] = mine.scale;
-    }
-    if (W == 1) {
-      t.par ^= 1;  // (a team of one warp has no barrier to alternate them)
-      __syncwarp();
-    }
   }
 }
 
@@ -397,7 +300,7 @@ __global__ void __launch_bounds__(kTeamThreads, 2) norm_direct_kernel(NormArgs a
   using U = typename R::U;
   __shared__ float2 slots[2 * kTeamWarps];
   Team t(slots);
-  const U unit(a.D, t.lane, t.m * NU, NU, 0);
+  U unit(a.D, t.lane, t.m * NU, NU, 0);
   for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < a.rows;
        row += (int64_t)gridDim.x * blockDim.y) {
     const int64_t e = unit.at(row);
@@ -417,66 +320,73 @@ __global__ void __launch_bounds__(kTeamThreads, 2) norm_direct_kernel(NormArgs a
       }
     }
     finish_row<T, LAYOUT, NU, Q8>(
-        a, unit, t, row, e, x, [&](int j, F2(&wf)[U::P]) { R::weight(w[j], a.offset, wf); }, [] {},
-        nullptr);
+        a, unit, t, row, e, x, [&](int j, F2(&wf)[U::P]) { R::weight(w[j], a.offset, wf); }, [] {});
   }
 }
 
-// One wave of CTAs over many rows (WIDE, PHASED).  The weights lie in shared
+// One wave of CTAs over many rows (not NARROW).  The weights lie in shared
 // memory as fp32, and each lane copies the granules of its team's next row into its
 // own slots of shared memory (cp.async) as soon as it has read the current one out of
-// them: the copies need no barrier, and are in flight while the team reduces
-// and writes.  A CTA's rows are a multiple of gridDim.x apart, which for
-// PHASED rows is a multiple of 8: all at one offset from a granule.
+// them: the copies need no barrier (SHIFTED: a warp's), and are in flight while
+// the team reduces and writes.  A CTA's rows are a multiple of gridDim.x apart, which for
+// rows at an offset is a multiple of 8: all at one offset from a granule.
 template <class T, int LAYOUT, int NU, bool ADD, int Q8>
 __global__ void __launch_bounds__(kTeamThreads, 2) norm_staged_kernel(NormArgs a) {
   using R = NormRow<T, LAYOUT>;
   using U = typename R::U;
-  constexpr int NS = ADD ? 2 : 1;      // streams
-  constexpr uint32_t kSlot = 32 * 16;  // a unit of one stream
-  constexpr bool kSplit = LAYOUT == PHASED && Q8 == 2;
+  constexpr int NS = ADD ? 2 : 1;  // streams
+  // a warp's units of one stream (SHIFTED: and one granule)
+  constexpr uint32_t kSlots = NU * 32 * 16 + (LAYOUT == SHIFTED ? 16 : 0);
   static_assert(LAYOUT != NARROW, "cp.async moves granules");
   __shared__ float2 slots[2 * kTeamWarps];
-  __shared__ float2 pieces[kSplit ? 2 * kTeamWarps * NU * R::BLOCKS : 1];
-  extern __shared__ float4 shared[];  // weights, then [warps][streams][NU][32]
+  extern __shared__ float4 shared[];  // weights, then [warps][streams][kSlots bytes]
   Team t(slots);
   const int W = t.warps, m = t.m;
-  const U unit(a.D, t.lane, m * NU, NU, blockIdx.x);
+  U unit(a.D, t.lane, m * NU, NU, blockIdx.x);
   const int ngr = W * NU * 32;  // granules of a row, padded
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   int64_t row = blockIdx.x + (int64_t)gridDim.x * threadIdx.y;
   const uint32_t stage = smem_addr(shared + ngr * (U::P / 2)) +
-                         (threadIdx.y * W + m) * (NS * NU * kSlot) + t.lane * 16;
+                         (threadIdx.y * W + m) * (NS * kSlots) + t.lane * 16;
   auto prefetch = [&](int64_t r) {
     if (r < a.rows) {
       const int64_t e = unit.at(r);
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
-        unit.copy(stage + j * kSlot, a.x, e, j);
-        if constexpr (ADD) unit.copy(stage + (NU + j) * kSlot, a.u, e, j);
+        unit.copy(stage + j * 512, a.x, e, j);
+        if constexpr (ADD) unit.copy(stage + kSlots + j * 512, a.u, e, j);
+      }
+      if (LAYOUT == SHIFTED && t.lane == 0) {
+        unit.copy(stage + NU * 512, a.x, e, NU);
+        if constexpr (ADD) unit.copy(stage + kSlots + NU * 512, a.u, e, NU);
       }
     }
     cp_async_commit();
   };
   prefetch(row);
-  stage_weight<T, LAYOUT>(shared, ngr, a.D, blockIdx.x, a.w, a.offset);
+  // (SHIFTED: the weights of the columns themselves, as row 0's)
+  stage_weight<T, LAYOUT>(shared, ngr, a.D, LAYOUT == SHIFTED ? 0 : blockIdx.x, a.w, a.offset);
   __syncthreads();
   for (; row < a.rows; row += step) {
     const int64_t e = unit.at(row);
     cp_async_wait<0>();  // this lane's copies of the row
+    if (LAYOUT == SHIFTED) __syncwarp();  // ... and the other lanes'
     Raw<16> x[NU];
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-      x[j] = unit.copied(stage + j * kSlot, j);
+      x[j] = unit.copied(stage + j * 512, j);
       if constexpr (ADD) {
-        x[j] = R::add(x[j], unit.copied(stage + (NU + j) * kSlot, j));
+        x[j] = R::add(x[j], unit.copied(stage + kSlots + j * 512, j));
         unit.store(a.res, e, j, x[j]);
       }
     }
     finish_row<T, LAYOUT, NU, Q8>(
         a, unit, t, row, e, x,
         [&](int j, F2(&wf)[U::P]) { staged_weight<T>(shared, ngr, (m * NU + j) * 32 + t.lane, wf); },
-        [&] { prefetch(row + step); }, pieces + threadIdx.y * (2 * W * NU * R::BLOCKS));
+        [&] {
+          if (LAYOUT == SHIFTED) __syncwarp();  // every lane has read the slots
+          prefetch(row + step);
+        });
   }
 }
 
@@ -491,7 +401,7 @@ __global__ void __launch_bounds__(kTeamThreads) norm_long_kernel(NormArgs a) {
   __shared__ float2 slots[2 * kTeamWarps];
   Team t(slots);
   const int lane = t.lane, warp = t.m, W = t.warps;
-  const U unit(a.D, lane, warp, 1, 0);  // units warp, warp + W, ...
+  U unit(a.D, lane, warp, 1, 0);  // units warp, warp + W, ...
   const int units = (a.D + U::COLS - 1) / U::COLS - warp;  // from this warp's first
 
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -600,14 +510,14 @@ cudaError_t launch_staged(const DeviceInfo& dev, const NormArgs& a, int64_t unit
   const int teams = (int)std::max<int64_t>(
       1, std::min<int64_t>(kTeamWarps / warps, (a.rows + dev.sm_count - 1) / dev.sm_count));
   const size_t smem = (size_t)warps * NU * 512 * (sizeof(T) == 2 ? 2 : 1) +
-                      (size_t)warps * teams * NU * 512 * (ADD ? 2 : 1);
+                      (size_t)warps * teams * (NU * 512 + (LAYOUT == SHIFTED ? 16 : 0)) * (ADD ? 2 : 1);
   static std::atomic<int> opted[kOptinDevices];
   const cudaError_t e = allow_shared((const void*)kern, dev, opted);
   if (e != cudaSuccess) return e;
   const int64_t wave =
       (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, warps * teams * 32, smem);
   int64_t grid = std::min<int64_t>(wave, (a.rows + teams - 1) / teams);
-  if (LAYOUT == PHASED) grid = (grid + 7) / 8 * 8;
+  if (LAYOUT != WIDE) grid = (grid + 7) / 8 * 8;
   kern<<<(unsigned)grid, dim3(warps * 32, teams), smem, s>>>(a);
   return cudaGetLastError();
 }
@@ -625,9 +535,11 @@ cudaError_t launch(const DeviceInfo& dev, const NormArgs& a, cudaStream_t s) {
     const bool staged = LAYOUT == PHASED || units > 2 * kTeamWarps ||
                         (many && !(ADD && Q8 == 0 && units > 8));
     if (staged && units <= 4 * kTeamWarps) {
-      if (units == 1) return launch_staged<T, LAYOUT, 1, ADD, Q8>(dev, a, units, s);
-      if (units == 2) return launch_staged<T, LAYOUT, 2, ADD, Q8>(dev, a, units, s);
-      return launch_staged<T, LAYOUT, 4, ADD, Q8>(dev, a, units, s);
+      // (groups of 128 columns of rows at an offset)
+      constexpr int L = LAYOUT == PHASED && Q8 == 2 ? SHIFTED : LAYOUT;
+      if (units == 1) return launch_staged<T, L, 1, ADD, Q8>(dev, a, units, s);
+      if (units == 2) return launch_staged<T, L, 2, ADD, Q8>(dev, a, units, s);
+      return launch_staged<T, L, 4, ADD, Q8>(dev, a, units, s);
     }
   }
   if constexpr (LAYOUT != PHASED) {

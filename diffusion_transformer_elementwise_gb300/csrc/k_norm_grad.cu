@@ -15,6 +15,10 @@
 // row of `partial`, and a second kernel adds the rows in order: no atomics, so
 // the same call gives the same bits.
 //
+// Few rows (kFewRows) take one launch and no workspace: the CTAs are one cluster,
+// and each adds a slice of gw's columns out of the others' shared memory.  (126 rows
+// of 2048 fp32 take 5 us instead of 4, but one launch of host time instead of two.)
+//
 // Each lane copies the granules it will read itself into its own slots of
 // shared memory (cp.async), a row or two ahead, so the copies need no barrier
 // and a warp's loads are in flight while it reduces and writes.
@@ -115,7 +119,8 @@ constexpr int kStagesOf = NU == 4 ? 1 : 2;
 template <int NU>
 constexpr int kGradWarps = NU == 1 ? 24 : NU == 2 ? 20 : 16;
 
-// SKIP: the gradient of the skip path is added.
+// SKIP: the gradient of the skip path is added.  a.gw (few rows): the grid is
+// one cluster, and gw is written here.
 template <class T, int LAYOUT, int NU, bool SKIP>
 __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGradArgs a) {
   using R = GradRow<T, LAYOUT>;
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
   // weights (not NARROW), [warps][stages][streams][NU][32]; in the end the teams' parts of gw
   extern __shared__ float4 shared[];
   let_next();
-  if (blockIdx.x >= a.rows) return;  // (the grid is rounded up for PHASED rows)
+  if (blockIdx.x >= a.rows && !a.gw) return;  // (the grid is rounded up for PHASED rows)
   Team t(slots);
   const int lane = t.lane, W = t.warps, m = t.m, team = threadIdx.y, teams = blockDim.y;
   const int ngr = W * NU * 32;  // granules of a row, padded
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
       smem_addr(shared + ngr * (P / 2)) + (team * W + m) * (kStages * kStage) + lane * 16;
 
   int64_t row = blockIdx.x + (int64_t)gridDim.x * team;
-  const U unit(a.D, lane, m * NU, NU, blockIdx.x);
+  U unit(a.D, lane, m * NU, NU, blockIdx.x);
   // this warp's part of row r, into stage s (an empty group past the end)
   auto prefetch = [&](int64_t r, int s) {
     if constexpr (kStaged) {
@@ -218,24 +223,40 @@ __global__ void __launch_bounds__(kGradWarps<NU> * 32) grad_team_kernel(NormGrad
       unit.store(a.gx, e, j, o);
     }
   }
-  if (!a.partial) return;
+  if (!a.partial && !a.gw) return;
   float* out = a.partial + (int64_t)blockIdx.x * a.D;
-  if (teams == 1) {
+  if (teams == 1 && !a.gw) {
 #pragma unroll
     for (int j = 0; j < NU; ++j) R::put(out, unit, j, acc[j]);
-  } else {
-    if constexpr (kStaged) cp_async_wait<0>();
-    __syncthreads();  // the stages are no longer read or written
-    float* merged = (float*)shared;  // [teams][D]
-#pragma unroll
-    for (int j = 0; j < NU; ++j) R::put(merged + team * a.D, unit, j, acc[j]);
-    __syncthreads();
-    for (int c = team * blockDim.x + threadIdx.x; c < a.D; c += blockDim.x * teams) {
-      float v = merged[c];
-      for (int q = 1; q < teams; ++q) v = __fadd_rn(v, merged[q * a.D + c]);
-      out[c] = v;
-    }
+    return;
   }
+  if constexpr (kStaged) cp_async_wait<0>();
+  __syncthreads();  // the stages are no longer read or written
+  float* merged = (float*)shared;  // [teams][D]
+#pragma unroll
+  for (int j = 0; j < NU; ++j) R::put(merged + team * a.D, unit, j, acc[j]);
+  __syncthreads();
+  const int tid = team * blockDim.x + threadIdx.x, nthr = blockDim.x * teams;
+  for (int c = tid; c < a.D; c += nthr) {
+    float v = merged[c];
+    for (int q = 1; q < teams; ++q) v = __fadd_rn(v, merged[q * a.D + c]);
+    if (a.gw)
+      merged[c] = v;
+    else
+      out[c] = v;
+  }
+  if (!a.gw) return;
+  cluster_barrier();
+  // columns rank, rank + ctas, ... in runs of 32
+  for (int c0 = (tid / 32 * gridDim.x + blockIdx.x) * 32; c0 < a.D; c0 += nthr * gridDim.x) {
+    const int c = c0 + lane;
+    if (c >= a.D) continue;
+    float v[1] = {0.0f};
+    for (unsigned r = 0; r < gridDim.x; ++r)
+      v[0] = __fadd_rn(v[0], __uint_as_float(ld_cluster(smem_addr(merged + c), r)));
+    st_stream<sizeof(T)>((char*)a.gw + (int64_t)c * sizeof(T), Vec<T, (int)sizeof(T)>::narrow(v));
+  }
+  cluster_barrier();  // the others have read this CTA's part
 }
 
 // Rows longer than a CTA's registers: read twice, gw added in the CTA's row
@@ -248,7 +269,7 @@ __global__ void __launch_bounds__(kTeamThreads) grad_long_kernel(NormGradArgs a)
   __shared__ float2 slots[2 * kTeamWarps];
   Team t(slots);
   const int lane = t.lane, warp = t.m, W = t.warps;
-  const U unit(a.D, lane, warp, 1, 0);  // units warp, warp + W, ...
+  U unit(a.D, lane, warp, 1, 0);  // units warp, warp + W, ...
   const int units = (a.D + U::COLS - 1) / U::COLS - warp;  // from this warp's first
   float* out = a.partial ? a.partial + (int64_t)blockIdx.x * a.D : nullptr;
   bool first = true;
@@ -312,6 +333,7 @@ __global__ void __launch_bounds__(1024) grad_weight_kernel(GradWeight a) {
   }
 }
 
+// *ctas: the rows of a.partial written; 0 where gw is written already
 template <class T, int LAYOUT, bool SKIP>
 cudaError_t launch_rows(const DeviceInfo& dev, NormGradArgs a, int64_t* ctas, cudaStream_t s) {
   using U = Unit<T, LAYOUT>;
@@ -321,20 +343,27 @@ cudaError_t launch_rows(const DeviceInfo& dev, NormGradArgs a, int64_t* ctas, cu
     const auto kern = grad_team_kernel<T, LAYOUT, NU, SKIP>;
     const int64_t warps = (units + NU - 1) / NU;
     // few rows: a CTA for each before a second team in any
-    const int64_t teams = std::max<int64_t>(
+    int64_t teams = std::max<int64_t>(
         1, std::min<int64_t>(kGradWarps<NU> / warps, (a.rows + dev.sm_count - 1) / dev.sm_count));
     int64_t grid = std::min<int64_t>(dev.sm_count, (a.rows + teams - 1) / teams);
+    if (a.gw) {
+      // one cluster: 8 CTAs, 16 for more rows than those hold at once
+      teams = kGradWarps<NU> / warps;
+      grid = a.rows <= 8 * teams ? 8 : 16;
+    }
     // PHASED: a CTA's rows have one offset when they are a multiple of 8 apart
     if (LAYOUT == PHASED) grid = (grid + 7) / 8 * 8;
     size_t smem = 0;
     if (LAYOUT != NARROW)
       smem = (size_t)warps * NU * 512 * (sizeof(T) == 2 ? 2 : 1) +
              (size_t)warps * teams * NU * 512 * kStagesOf<NU> * (SKIP ? 3 : 2);
-    if (teams > 1) smem = std::max(smem, (size_t)teams * a.D * 4);
+    if (teams > 1 || a.gw) smem = std::max(smem, (size_t)teams * a.D * 4);
     static std::atomic<int> opted[kOptinDevices];
     cudaError_t e = allow_shared((const void*)kern, dev, opted);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)grid, dim3((unsigned)warps * 32, (unsigned)teams), smem, s>>>(a);
+    const dim3 block((unsigned)warps * 32, (unsigned)teams);
+    if (a.gw) return launch_cluster(kern, (unsigned)grid, block, smem, s, a);
+    kern<<<(unsigned)grid, block, smem, s>>>(a);
     *ctas = std::min(grid, a.rows);
     return cudaGetLastError();
   };
@@ -344,6 +373,7 @@ cudaError_t launch_rows(const DeviceInfo& dev, NormGradArgs a, int64_t* ctas, cu
   if constexpr (LAYOUT == PHASED) {
     return launch_rows<T, NARROW, SKIP>(dev, a, ctas, s);
   } else {
+    a.gw = nullptr;
     *ctas = std::min(std::min<int64_t>(2 * dev.sm_count, a.rows), kNormGradMaxCtas);
     grad_long_kernel<T, LAYOUT><<<(unsigned)*ctas, kTeamThreads, 0, s>>>(a);
     return cudaGetLastError();
@@ -351,9 +381,9 @@ cudaError_t launch_rows(const DeviceInfo& dev, NormGradArgs a, int64_t* ctas, cu
 }
 
 template <class T>
-cudaError_t launch(const DeviceInfo& dev, int layout, const NormGradArgs& a, void* gw,
-                   cudaStream_t s) {
+cudaError_t launch(const DeviceInfo& dev, int layout, NormGradArgs a, void* gw, cudaStream_t s) {
   int64_t ctas = 0;
+  a.gw = a.rows <= kFewRows ? gw : nullptr;
   const bool skip = a.gres != nullptr;
   const cudaError_t e =
       layout == WIDE     ? (skip ? launch_rows<T, WIDE, true>(dev, a, &ctas, s)
@@ -362,7 +392,7 @@ cudaError_t launch(const DeviceInfo& dev, int layout, const NormGradArgs& a, voi
                                  : launch_rows<T, PHASED, false>(dev, a, &ctas, s))
                          : (skip ? launch_rows<T, NARROW, true>(dev, a, &ctas, s)
                                  : launch_rows<T, NARROW, false>(dev, a, &ctas, s));
-  if (e != cudaSuccess || !gw) return e;
+  if (e != cudaSuccess || !gw || ctas == 0) return e;
   return launch_after(grad_weight_kernel<T>, (unsigned)((a.D + 31) / 32), 1024, 0, s,
                       GradWeight{a.partial, (int)ctas, a.D, gw});
 }

@@ -537,6 +537,7 @@ dit_status dit_add_rmsnorm_fp8(void* residual_out, void* out, float* scales, con
  * in fp32.  x is the norm's input: for dit_add_rmsnorm its residual_out, and
  * grad_x is then the gradient of hidden and of update alike.
  * grad_weight may be NULL (a frozen weight; the workspace may then be NULL too).
+ * Up to 128 rows of at most 8189 columns need no workspace (its size is 0).
  * grad_x may be grad_out or grad_residual; no other overlap of an output with
  * another tensor or with the workspace is allowed.
  */

@@ -101,7 +101,8 @@ def test_backward(dtype, D, skip):
     ref.check_norm_grad(gx, gw, g, x, w, EPS, 1.0, k if skip else None)
 
 
-@pytest.mark.parametrize("rows,D", [(1, 4096), (2, 64), (126, 2048), (3000, 200), (1300, 1000),
+@pytest.mark.parametrize("rows,D", [(1, 4096), (2, 64), (126, 2048), (128, 3077), (129, 3077),
+                                    (100, 8192), (3, 16384), (64, 100), (3000, 200), (1300, 1000),
                                     (700, 4096), (5000, 33), (40, 20000)])
 @dtypes
 def test_backward_many_rows(dtype, rows, D):
@@ -271,7 +272,8 @@ def test_refusals():
     with pytest.raises(dit.DitError):
         dit.rmsnorm(x, w, out=x)
     with pytest.raises(dit.DitError):
-        dit.rmsnorm_backward(x, x, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        many = torch.zeros((200, 64), device="cuda")
+        dit.rmsnorm_backward(many, many, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
 
 
 def test_streams_and_graphs():

@@ -93,7 +93,8 @@ def back(lib, gx=O, gw=S, g=G, k=K, x=X, w=W, rows=4, D=8, eps=1e-6, off=0.0, dt
 
 def test_norm_backward(lib):
     wb = lib.dit_rmsnorm_backward_workspace_bytes
-    assert wb(4, 8) == 256 and wb(10_000, 4096) == 304 * 4096 * 4 and wb(0, 8) == 0
+    assert wb(10_000, 4096) == 304 * 4096 * 4 and wb(129, 8) == 4352
+    assert wb(128, 8189) == wb(0, 8) == 0 and wb(1, 8190) == 32768  # few rows need none
     assert wb(-1, 8) == -1 and wb(1, 1 << 25) == -1 and wb(1 << 31, 8) == -1
     assert back(lib) == NODEV and back(lib, k=None) == NODEV
     assert back(lib, gw=None, ws=None, n=0) == NODEV      # a frozen weight
@@ -101,15 +102,16 @@ def test_norm_backward(lib):
     assert back(lib, rows=0, gx=None, g=None, k=None, x=None, w=None) == NODEV  # gw is still written
     for name in ("gx", "g", "x", "w"):
         assert back(lib, **{name: None}) == NULLP
-    assert back(lib, ws=None) == WORKSPACE and back(lib, ws=WS + 16) == WORKSPACE
-    assert back(lib, n=255) == WORKSPACE
+    assert back(lib, ws=None) == NODEV
+    assert back(lib, rows=200, ws=None) == WORKSPACE and back(lib, rows=200, ws=WS + 16) == WORKSPACE
+    assert back(lib, rows=200, n=wb(200, 8) - 1) == WORKSPACE
     assert back(lib, dt=4) == DTYPE and back(lib, rows=-1, n=0) == SHAPE
     assert back(lib, eps=-1.0) == EPS and back(lib, off=NAN) == SCALAR
     assert back(lib, g=G + 1) == MISALIGNED and back(lib, gw=S + 1) == MISALIGNED
     assert back(lib, gx=G) == NODEV and back(lib, gx=K) == NODEV
     assert back(lib, gx=G + 16) == ALIAS and back(lib, gx=X) == ALIAS and back(lib, gx=W) == ALIAS
     assert back(lib, gw=W) == ALIAS and back(lib, gw=O) == ALIAS and back(lib, gw=G) == ALIAS
-    assert back(lib, ws=X) == ALIAS and back(lib, ws=O) == ALIAS
+    assert back(lib, rows=200, ws=X) == ALIAS and back(lib, rows=200, ws=O) == ALIAS
 
 
 def test_embedding(lib):
