@@ -9,11 +9,11 @@
 // with the maximum over the row or over each 128 columns of it.
 //
 // The codes need no r: with t = fl(s fl(offset + w)), y / max|y| = t / max|t|,
-// so code = e4m3(fl(t m')) with m' = 448 / max|t| (a hardware reciprocal, one
-// Newton-Raphson step and a product: within 1.5 u) and scale =
-// fl(fl(max|t| r) fl(1 / 448)).  The maximum is taken in the same reduction
-// as the sum of squares, and a code carries fewer roundings than y / scale
-// would.  Rows whose sum of
+// so code = e4m3(fl(t m')) with m' = 448 / max|t| as a sum of two fp32 numbers
+// (a hardware reciprocal y, 448 y, and the rest of it: about 2^-44 of m' is
+// lost) and scale = fl(fl(max|t| r) fl(1 / 448)).  The maximum is taken in the same
+// reduction as the sum of squares, and beside t's own roundings a code has the one of
+// its product, so few codes round otherwise than those of exact arithmetic.  Rows whose sum of
 // squares or maximum leaves [2^-100, 2^100] (overflow, infinities, NaN, all
 // zero) take y itself: the maximum again, of y, and code = e4m3(y 448 /
 // max|y|).  An all-zero row or group has scale 0 and codes 0; a NaN or an
@@ -36,19 +36,15 @@ __device__ __forceinline__ bool usable(float m) { return m >= 0x1p-100f && m <= 
 
 // The factor from values to codes, and the scale, of one row or group.
 struct Quant {
-  float mul, scale;
+  float mul, low, scale;  // codes of t: t (mul + low)
 };
-// 448 / m for a normal m in [2^-100, 2^100]
-__device__ __forceinline__ float codes_per(float m) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(m));
-  y = __fmaf_rn(y, __fmaf_rn(-m, y, 1.0f), y);
-  return __fmul_rn(kE4M3Max, y);
-}
 // from the maximum of |t| (usable, or zero with a usable sum)
 __device__ __forceinline__ Quant quant_of_t(float m, float r) {
   Quant q;
-  q.mul = m == 0.0f ? 0.0f : codes_per(m);
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(m == 0.0f ? 1.0f : m));
+  q.mul = m == 0.0f ? 0.0f : __fmul_rn(kE4M3Max, y);
+  q.low = m == 0.0f ? 0.0f : __fmul_rn(__fmaf_rn(-q.mul, m, kE4M3Max), y);
   q.scale = __fmul_rn(__fmul_rn(m, r), 1.0f / kE4M3Max);
   return q;
 }
@@ -58,6 +54,7 @@ __device__ __forceinline__ float small_factor(float m) { return m < 0x1p-60f ? 0
 __device__ __forceinline__ Quant quant_of_y(float m) {
   Quant q;
   q.mul = m == 0.0f ? 0.0f : __fdiv_rn(kE4M3Max, __fmul_rn(m, small_factor(m)));
+  q.low = 0.0f;
   q.scale = __fdiv_rn(m, kE4M3Max);
   return q;
 }
@@ -69,8 +66,9 @@ struct NormRow {
   // 128-column groups of a unit whose maxima a lane helps to find, and the
   // lanes that share one
   static constexpr int NG = LAYOUT == NARROW && sizeof(T) == 2 ? 2 : 1;
-  [[maybe_unused]] static constexpr int LANES = LAYOUT != NARROW && sizeof(T) == 2 ? 16 : 32;
-  [[maybe_unused]] static constexpr int BLOCKS = 32 / LANES * NG;  // groups of a unit
+  static constexpr int LANES = LAYOUT != NARROW && sizeof(T) == 2 ? 16 : 32;
+  static constexpr int BLOCKS = 32 / LANES * NG;  // groups of a unit
+  static_assert(LANES * BLOCKS == 32 * NG, "every lane helps with NG groups");
 
   // hidden + update, rounded (the first value alone without an update)
   __device__ __forceinline__ static Raw<16> add(const Raw<16>& h, const Raw<16>& u) {
@@ -121,8 +119,10 @@ struct NormRow {
     Raw<U::EPL> r;
 #pragma unroll
     for (int i = 0; i < P / 2; ++i) {
-      const float m = q[NG == 2 ? i : 0].mul;
-      r.w[i] = e4m3x2(f2_mul(v[2 * i], f2(m, m))) | e4m3x2(f2_mul(v[2 * i + 1], f2(m, m))) << 16;
+      const Quant& k = q[NG == 2 ? i : 0];
+      const F2 m = f2(k.mul, k.mul), l = f2(k.low, k.low);
+      r.w[i] = e4m3x2(f2_fma(v[2 * i], m, f2_mul(v[2 * i], l))) |
+               e4m3x2(f2_fma(v[2 * i + 1], m, f2_mul(v[2 * i + 1], l))) << 16;
     }
     return r;
   }

@@ -511,9 +511,10 @@ dit_status dit_add_rmsnorm(void* residual_out, void* out, const void* hidden, co
  * maximum of |y| over the row (group 0) or over each 128 columns of it (group 128, the
  * last group holding what is left),
  *   scale = m / 448,  code = e4m3(y / scale),  y ~ code * scale,
- * evaluated as code = e4m3(fl32(t * fl32(448 / max|t|))) with t = fl32(s *
- * fl32(weight_offset + weight)), which leaves r out of the codes, and
- * scale = fl32(fl32(max|t| * r) / 448); from y itself where a sum of squares
+ * evaluated as code = e4m3(fl32(t * (448 / max|t|))) with t = fl32(s *
+ * fl32(weight_offset + weight)), which leaves r out of the codes, and the
+ * quotient carried in two fp32 numbers; scale = fl32(fl32(max|t| * r) *
+ * fl32(1 / 448)).  They are taken from y itself where a sum of squares
  * or a maximum leaves [2^-100, 2^100].  m = 0 gives scale 0 and codes 0; a NaN
  * or an infinity in s makes the scale of its row or group NaN, and the codes NaN.
  * out: [rows, D] bytes.  scales: fp32 [rows, 1], or [rows, ceil(D / 128)].
