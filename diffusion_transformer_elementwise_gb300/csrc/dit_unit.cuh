@@ -362,6 +362,7 @@ inline cudaError_t allow_shared(const void* fn, const DeviceInfo& dev, std::atom
 // A barrier of the cluster's CTAs (a hardware wait), which orders their shared
 // and global accesses; a word of the shared memory of its CTA `rank`.
 __device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();  // (.aligned: the whole warp at once)
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }

@@ -17,7 +17,8 @@
 //
 // Few rows (kFewRows) take one launch and no workspace: the CTAs are one cluster,
 // and each adds a slice of gw's columns out of the others' shared memory.  (126 rows
-// of 2048 fp32 take 5 us instead of 4, but one launch of host time instead of two.)
+// of 2048 fp32 take 8.1 us on the GPU instead of 4.2, but a call 8.3 us of host time
+// instead of 18; a graph of such calls would rather have the two launches.)
 //
 // Each lane copies the granules it will read itself into its own slots of
 // shared memory (cp.async), a row or two ahead, so the copies need no barrier
@@ -345,7 +346,8 @@ cudaError_t launch_rows(const DeviceInfo& dev, NormGradArgs a, int64_t* ctas, cu
     // few rows: a CTA for each before a second team in any
     int64_t teams = std::max<int64_t>(
         1, std::min<int64_t>(kGradWarps<NU> / warps, (a.rows + dev.sm_count - 1) / dev.sm_count));
-    int64_t grid = std::min<int64_t>(dev.sm_count, (a.rows + teams - 1) / teams);
+    int64_t grid = std::min(std::min<int64_t>(dev.sm_count, kNormGradMaxCtas - 8),
+                            (a.rows + teams - 1) / teams);
     if (a.gw) {
       // one cluster: 8 CTAs, 16 for more rows than those hold at once
       teams = kGradWarps<NU> / warps;
@@ -367,7 +369,7 @@ cudaError_t launch_rows(const DeviceInfo& dev, NormGradArgs a, int64_t* ctas, cu
     *ctas = std::min(grid, a.rows);
     return cudaGetLastError();
   };
-  if (units <= 8) return team(std::integral_constant<int, 1>{});
+  if (units == 1) return team(std::integral_constant<int, 1>{});
   if (units <= 2 * kTeamWarps) return team(std::integral_constant<int, 2>{});
   if (units <= 4 * kTeamWarps) return team(std::integral_constant<int, 4>{});
   if constexpr (LAYOUT == PHASED) {

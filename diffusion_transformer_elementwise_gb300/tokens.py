@@ -21,7 +21,7 @@ and back, from the gradient gy of the last y:
     gtable = embedding_backward(gx, ids, V, scale)
     clip_grads([gtable, gw_0, ..., gw_last], max_norm)
 
-``forward`` and ``backward`` run it; ``decode`` is the forward pass of single
+``forward`` and ``backward`` run it, on the current stream; ``decode`` is the forward pass of single
 tokens with the last norm's output in E4M3.  ``capture_step`` records a whole
 step in one CUDA graph.
 """
@@ -61,43 +61,42 @@ def make_inputs(tokens, V, D, blocks=2, dtype="bf16", device="cuda", seed_tag="t
     return ids, table, weights, stand_ins
 
 
-def forward(ids, table, weights, stand_ins, scale=1.0, eps=1e-6, keep=None, stream=None):
+def forward(ids, table, weights, stand_ins, scale=1.0, eps=1e-6, keep=None):
     """The forward pass; returns (x, y) after the last site.  keep: a list that
     receives every norm's input (what backward needs), in order."""
-    x = embedding(ids, table, scale, stream=stream)
-    y = rmsnorm(x, weights[0], eps, stream=stream)
+    x = embedding(ids, table, scale)
+    y = rmsnorm(x, weights[0], eps)
     for a, w in zip(stand_ins, weights[1:]):
         if keep is not None:
             keep.append(x)
         # the residual in place, unless backward needs the old one
-        x, y = add_rmsnorm(x, y * a, w, eps, residual_out=None if keep is not None else x,
-                           stream=stream)
+        x, y = add_rmsnorm(x, y * a, w, eps, residual_out=None if keep is not None else x)
     if keep is not None:
         keep.append(x)
     return x, y
 
 
-def backward(grad_y, ids, num_rows, weights, stand_ins, kept, scale=1.0, eps=1e-6, stream=None):
+def backward(grad_y, ids, num_rows, weights, stand_ins, kept, scale=1.0, eps=1e-6):
     """Gradients of the table and of every weight from the gradient of the
     last y; kept: what forward kept.  Returns (grad_table, grad_weights)."""
     grads = [None] * len(weights)
-    gx, grads[-1] = rmsnorm_backward(grad_y, kept[-1], weights[-1], eps, stream=stream)
+    gx, grads[-1] = rmsnorm_backward(grad_y, kept[-1], weights[-1], eps)
     for k in range(len(stand_ins) - 1, -1, -1):
         gx, grads[k] = rmsnorm_backward(gx * stand_ins[k], kept[k], weights[k], eps,
-                                        grad_residual=gx, stream=stream)
-    return embedding_backward(gx, ids, num_rows, scale, stream=stream), grads
+                                        grad_residual=gx)
+    return embedding_backward(gx, ids, num_rows, scale), grads
 
 
-def decode(ids, table, weights, stand_ins, scale=1.0, eps=1e-6, group=128, stream=None):
+def decode(ids, table, weights, stand_ins, scale=1.0, eps=1e-6, group=128):
     """The forward pass of single tokens, the last norm in E4M3: returns
     (x, codes, scales)."""
-    x = embedding(ids, table, scale, stream=stream)
-    y = rmsnorm(x, weights[0], eps, stream=stream)
+    x = embedding(ids, table, scale)
+    y = rmsnorm(x, weights[0], eps)
     last = len(stand_ins) - 1
     for k, (a, w) in enumerate(zip(stand_ins, weights[1:])):
         if k == last:
-            return add_rmsnorm_fp8(x, y * a, w, eps, group=group, residual_out=x, stream=stream)
-        x, y = add_rmsnorm(x, y * a, w, eps, residual_out=x, stream=stream)
+            return add_rmsnorm_fp8(x, y * a, w, eps, group=group, residual_out=x)
+        x, y = add_rmsnorm(x, y * a, w, eps, residual_out=x)
     raise ValueError("no sites")
 
 

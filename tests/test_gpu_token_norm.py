@@ -153,6 +153,48 @@ def test_tensors_off_a_16_byte_boundary(dtype, off, D):
     ref.check_norm_grad(gx, gw, u, h, w, EPS, 0.0)
 
 
+@pytest.mark.parametrize("D", [64, 4096, 8192])
+@dtypes
+def test_weight_alone_off_a_16_byte_boundary(dtype, D):
+    rows = 6
+    h, u, w = inputs(rows, D, dtype, "woff")
+    hd, ud, wd = h.cuda(), u.cuda(), offset_copy(w, 3)
+    res, out = dit.add_rmsnorm(hd, ud, wd, EPS)
+    gx, gw = dit.rmsnorm_backward(ud, hd, wd, EPS)
+    torch.cuda.synchronize()
+    ref.check_norm(out, res, w, EPS, 0.0)
+    ref.check_norm_grad(gx, gw, u, h, w, EPS, 0.0)
+    for group in (0, 128):
+        q, s = dit.rmsnorm_fp8(hd, wd, EPS, group)
+        ref.check_fp8(q, s, h, w, EPS, 0.0, group)
+
+
+@pytest.mark.parametrize("rows,D", [(200, 3077), (150, 129), (1300, 1001), (90, 16389)])
+@dtypes
+def test_in_place_of_odd_widths(dtype, rows, D):
+    """Outputs over their inputs where rows share 16-byte granules, in every
+    form that allows it, equal the results in other memory."""
+    h, u, w = (t.cuda() for t in inputs(rows, D, dtype, "oddplace"))
+    g = make((rows, D), dtype, "oddplace", "g", rows, D).cuda()
+    res, out = dit.add_rmsnorm(h, u, w, EPS)
+    gx, gw = dit.rmsnorm_backward(g, h, w, EPS, grad_residual=u)
+    for _ in range(3):
+        x = h.clone()
+        r, o = dit.add_rmsnorm(x, u, w, EPS, residual_out=x)
+        assert torch.equal(bits(r), bits(res)) and torch.equal(bits(o), bits(out))
+        for group in (0, 128):
+            q, s = dit.rmsnorm_fp8(res, w, EPS, group)
+            x = h.clone()
+            _, q2, s2 = dit.add_rmsnorm_fp8(x, u, w, EPS, group, residual_out=x)
+            assert torch.equal(bits(x), bits(res)) and torch.equal(bits(q), bits(q2))
+            assert torch.equal(bits(s), bits(s2))
+        g2, u2 = g.clone(), u.clone()
+        a = dit.rmsnorm_backward(g2, h, w, EPS, grad_residual=u, grad_x=g2)
+        b = dit.rmsnorm_backward(g, h, w, EPS, grad_residual=u2, grad_x=u2)
+        for t in (a, b):
+            assert torch.equal(bits(t[0]), bits(gx)) and torch.equal(bits(t[1]), bits(gw))
+
+
 @pytest.mark.parametrize("D", [200, 3077, 4096, 20000])
 @dtypes
 def test_rows_of_extreme_values(dtype, D):
