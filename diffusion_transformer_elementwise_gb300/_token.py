@@ -13,6 +13,7 @@ functions of their own.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -93,7 +94,7 @@ def _rows(x, name):
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError(f"{name} must be a tensor of at least one dimension")
     D = x.shape[-1]
-    return (x.numel() // D if D else 0), D
+    return (x.numel() // D if D else math.prod(x.shape[:-1])), D
 
 
 def _same(x, named, weight=None, D=0):

@@ -59,7 +59,15 @@ dit_status norm_impl(bool add, int q8, void* res, void* out, float* scales, cons
   if (!row_shape(rows, D, es, &n)) return DIT_ERR_BAD_SHAPE;
   if (!(eps >= 0.0f) || isinf(eps)) return DIT_ERR_BAD_EPS;
   if (!finite(offset)) return DIT_ERR_BAD_SCALAR;
-  if (n == 0) return DIT_OK;
+  if (n == 0 && (q8 != 1 || rows == 0 || !scales)) return DIT_OK;
+  if (n == 0) {  // rows of no columns: their scales are zero
+    if (misaligned(scales, 4)) return DIT_ERR_MISALIGNED;
+    DeviceInfo dev;
+    if (dit::current_device(&dev) != cudaSuccess) return DIT_ERR_NO_DEVICE;
+    const cudaError_t e = cudaMemsetAsync(scales, 0, (size_t)rows * 4, (cudaStream_t)stream);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return launch_status(e);
+  }
   if (!out || !x || !w || (add && (!res || !u)) || (q8 && !scales)) return DIT_ERR_NULL_PTR;
   if (misaligned(x, es) || misaligned(w, es) || (!q8 && misaligned(out, es)) ||
       (add && (misaligned(res, es) || misaligned(u, es))) || (q8 && misaligned(scales, 4)))

@@ -495,8 +495,10 @@ dit_status dit_selfcheck_static_workspace(void** workspace, int64_t* bytes);
  * with s = x for dit_rmsnorm.  weight: [D], weight_offset 0 for a plain weight,
  * 1 for one stored as its difference from one.  The statistic is taken over
  * the residual as stored.  residual_out may be hidden; no other overlap of an
- * output with another tensor is allowed.  Any element-aligned pointer and any D: rows of
- * 16-byte granules move in 16-byte accesses, others element by element.
+ * output with another tensor is allowed.  Any element-aligned pointer and any
+ * D: tensors that start on 16-byte boundaries move in 16-byte accesses whatever D
+ * (rows too long for registers only where D is a multiple of them), others
+ * element by element.
  */
 dit_status dit_rmsnorm(void* out, const void* x, const void* weight, int64_t rows, int64_t D,
                        float eps, float weight_offset, dit_dtype dtype, dit_stream_t stream);
@@ -518,7 +520,8 @@ dit_status dit_add_rmsnorm(void* residual_out, void* out, const void* hidden, co
  * or a maximum leaves [2^-100, 2^100].  m = 0 gives scale 0 and codes 0; a NaN
  * or an infinity in s makes the scale of its row or group NaN, and the codes NaN.
  * out: [rows, D] bytes.  scales: fp32 [rows, 1], or [rows, ceil(D / 128)].
- * Other groups: DIT_ERR_BAD_FORMAT.  out and scales may overlap nothing.
+ * Other groups: DIT_ERR_BAD_FORMAT.  out and scales may overlap nothing.  Rows
+ * of no columns (D = 0, group 0) have scale 0, written where scales is not NULL.
  */
 dit_status dit_rmsnorm_fp8(void* out, float* scales, const void* x, const void* weight,
                            int64_t rows, int64_t D, int64_t group, float eps, float weight_offset,

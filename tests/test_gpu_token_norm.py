@@ -290,6 +290,19 @@ def test_empty():
     assert dit.rmsnorm(z, torch.empty(0, device="cuda")).shape == (4, 0)
 
 
+@dtypes
+def test_rows_of_no_columns_have_scale_zero(dtype):
+    z, w = torch.empty((5, 0), dtype=dtype, device="cuda"), torch.empty(0, dtype=dtype, device="cuda")
+    scales, fresh = guarded((5, 1), torch.float32, "cuda")
+    q, s = dit.rmsnorm_fp8(z, w, scales=scales)
+    r, q2, s2 = dit.add_rmsnorm_fp8(z, z, w, residual_out=torch.empty_like(z),
+                                    scales=torch.full((5, 1), 3.0, device="cuda"))
+    torch.cuda.synchronize()
+    assert q.shape == (5, 0) and s is scales and not s.any() and not s2.any()
+    assert fresh()
+    assert dit.rmsnorm_fp8(z, w, group=128)[1].shape == (5, 0)
+
+
 def test_refusals():
     x = torch.zeros((4, 64), device="cuda")
     w = torch.ones(64, device="cuda")
