@@ -11,12 +11,20 @@
 // every sum has one order -- no atomics on values, the same bits from every
 // call.  The sorted tokens are cut into segments of 32, one team of threads
 // each, whatever the ids' distribution.  A run of one id inside a segment is
-// summed and written once.  A run that crosses segments leaves one fp32 row
-// per segment in the workspace, and a last kernel adds those.  The rows of
+// summed and written once; one that ends in the next segment too, by its first
+// segment's team, each segment's part for itself.  A longer run leaves one fp32
+// row per segment in the workspace, and a last kernel adds those.  The rows of
 // the table that no token names are found in the sorted ids and filled with
 // zeros by further CTAs of the same launch, so each row of the gradient is
 // written once.  Up to kFewTokens tokens need no sort: every CTA reads all ids, the
 // first token of each id adds its rows, and one launch does it all.
+//
+// Lookup of 32640 bf16 rows of 4096: 77 us, 6.9 TB/s, bound by memory (odd
+// width, 16000 of 3077: 45 us).  Gradient of 32640 tokens for [128000, 2048]
+// bf16: 119 us, of which the sort 17 (one cluster: bound by latency) and the
+// join 8 to 13; the sums and the zeros are bound by memory, for odd widths by
+// the instructions that shift and store them (16000 x 3077: 84 us).  126
+// tokens for [32000, 2048] fp32: 40 us, 6.6 TB/s, nearly all of it zeros.
 #include <algorithm>
 #include <type_traits>
 
@@ -402,9 +410,15 @@ __device__ __forceinline__ void fill_rows(const SumArgs& a, const uint32_t* name
 }
 
 // blockDim = (threads of a row, segments of a CTA); segment CTAs come in
-// groups of `tiles`, one column tile each.
+// groups of `tiles`, one column tile each.  The rows of a segment come through
+// a ring in shared memory (cp.async), eight in flight for every thread: loaded
+// into registers, eight at a time, they left room for three CTAs an SM and waited
+// on memory for most of the time (60000 tokens of 1024 for 1000 ids: 65 us,
+// the ring 51).
+constexpr int kSumAhead = 8;  // rows in flight (a power of two)
+
 template <class T, int LAYOUT>
-__global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
+__global__ void __launch_bounds__(256, LAYOUT == NARROW ? 3 : 4) embedding_sum_kernel(SumArgs a) {
   let_next();
   after_previous();
   using L = Tile<T, LAYOUT>;
@@ -432,68 +446,164 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(SumArgs a) {
   const int64_t seg = role / a.tiles * blockDim.y + threadIdx.y;
   const L t(a.D, tile);
   if (seg >= a.segments) return;  // the whole team
+  // warps without columns
+  if (t.c - (int)(threadIdx.x & 31) * (LAYOUT == NARROW ? 1 : N) >= a.D) return;
   const int64_t i0 = seg * kEmbedSegment;
-  const int n = (int)min((int64_t)kEmbedSegment, a.tokens - i0);
-  // the segment's tokens, one per lane of each warp
+  // the segment's ids and the next one's, one per lane of each warp
   const int lane = threadIdx.x & 31;
-  const uint2 mine = lane < n ? a.sorted[i0 + lane] : make_uint2((uint32_t)a.V, 0u);
-  const uint32_t before = i0 > 0 ? a.sorted[i0 - 1].x : (uint32_t)a.V;
-  const uint32_t after = i0 + n < a.tokens ? a.sorted[i0 + n].x : (uint32_t)a.V;
-  uint32_t key = __shfl_sync(0xFFFFFFFFu, mine.x, 0);
+  const uint32_t none = (uint32_t)a.V;
+  const uint2* sorted = a.sorted + i0;
+  auto key_of = [&](int i) { return i0 + i >= 0 && i0 + i < a.tokens ? sorted[i].x : none; };
+  const uint32_t mine = key_of(lane), next = key_of(kEmbedSegment + lane);
+  const uint32_t before = key_of(-1), start = key_of(-1 - kEmbedSegment);
+  const uint32_t end = key_of(2 * kEmbedSegment);
+  const uint32_t after = __shfl_sync(0xFFFFFFFFu, next, 0);
+  uint32_t key = __shfl_sync(0xFFFFFFFFu, mine, 0);
   bool head = i0 > 0 && before == key;
-  float acc[N];
+  // tokens [i, m) are this team's: those with an id in the table, without the
+  // end of a run of two segments (which the first segment's team adds), and with
+  // that of the last run here if it is one
+  int i = 0, m = __popc(__ballot_sync(0xFFFFFFFFu, mine < none));
+  if (head && start != key && after != key) {
+    i = __popc(__ballot_sync(0xFFFFFFFFu, mine == key));
+    key = __shfl_sync(0xFFFFFFFFu, mine, i & 31);
+    head = false;
+  }
+  if (i >= m) return;
+  const uint32_t last = __shfl_sync(0xFFFFFFFFu, mine, m - 1);
+  const bool open = after == last && (end == last || (head && last == key));
+  // bit k: a sum ends before token k (at a new run, the next segment, the end)
+  const uint32_t previous = __shfl_up_sync(0xFFFFFFFFu, mine, 1);
+  uint64_t ends = __ballot_sync(0xFFFFFFFFu, mine != previous);
+  if (after == last && !open) {
+    m += __popc(__ballot_sync(0xFFFFFFFFu, next == last));
+    ends |= uint64_t(1) << kEmbedSegment;
+  }
+  auto end_of = [&](int k) {  // of the sum that token k is in
+    const uint64_t e = ends >> k >> 1;
+    return e ? min(m, k + __ffsll((long long)e)) : m;
+  };
+  F2 acc[N / 2], first[N / 2];
 #pragma unroll
-  for (int e = 0; e < N; ++e) acc[e] = 0.0f;
-  // the run of `key` ends here (open: it goes on in the next segment)
-  auto flush = [&](bool open) {
-    if (key < a.V) {
-      if ((head || open) && t.valid()) {
-        float* p = a.partial + (seg * 2 + (head ? 0 : 1)) * a.D;
-        if constexpr (LAYOUT == WIDE) {
+  for (int e = 0; e < N / 2; ++e) acc[e] = first[e] = f2(0.0f, 0.0f);
+  // the run of `key` ends here (goes_on: but not in the tokens)
+  auto flush = [&](bool goes_on) {
+    float f[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = e & 1 ? f2_hi(acc[e / 2]) : f2_lo(acc[e / 2]);
+    if (head || goes_on) {
+      float* p = a.partial + (seg * 2 + (head ? 0 : 1)) * a.D;
+      if constexpr (LAYOUT == WIDE) {
+        if (t.valid()) {
 #pragma unroll
           for (int e = 0; e < N; e += 4)
-            *(float4*)(p + t.c + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < N; ++e)
-            if (t.col(e) < a.D) p[t.col(e)] = acc[e];
+            *(float4*)(p + t.c + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
         }
-        if (!head && tile == 0 && threadIdx.x == 0) a.runs[1 + atomicAdd(a.runs, 1u)] = (uint32_t)seg;
-      } else if (!head && !open) {
-        t.store(a.gt, key, acc, a.scale);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (t.col(e) < a.D) p[t.col(e)] = f[e];
       }
+      if (!head && tile == 0 && threadIdx.x == 0) a.runs[1 + atomicAdd(a.runs, 1u)] = (uint32_t)seg;
+    } else {
+      t.store(a.gt, key, f, a.scale);
     }
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+    for (int e = 0; e < N / 2; ++e) acc[e] = f2(0.0f, 0.0f);
   };
-  constexpr int AHEAD = 8;  // rows in flight
-  for (int i = 0; i < n; i += AHEAD) {
-    typename L::R r[AHEAD];
+  auto add = [&](const typename L::R& r) {
+    float f[N];
+    L::widen(r, f);
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j) {
-      // (lanes past the segment's end hold an id outside the table)
-      const uint32_t k = __shfl_sync(0xFFFFFFFFu, mine.x, i + j);
-      const uint32_t at = __shfl_sync(0xFFFFFFFFu, mine.y, i + j);
-      if (k < a.V && t.valid()) r[j] = t.load(a.g, at, a.tokens);
-    }
+    for (int e = 0; e < N / 2; ++e) acc[e] = f2_add(acc[e], f2(f[2 * e], f[2 * e + 1]));
+  };
+  // before token k, which is not the team's first
+  auto turn = [&](int k) {
+    if (k == kEmbedSegment) {  // the next segment's part, added on its own
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j) {
-      if (i + j >= n) break;
-      const uint32_t k = __shfl_sync(0xFFFFFFFFu, mine.x, i + j);
-      if (k != key) {
-        flush(false);
-        key = k;
-        head = false;
+      for (int e = 0; e < N / 2; ++e) {
+        first[e] = acc[e];
+        acc[e] = f2(0.0f, 0.0f);
       }
-      if (key < a.V && t.valid()) {
-        float f[N];
-        L::widen(r[j], f);
+    } else {
+      flush(false);
+      key = sorted[k].x;
+      head = false;
+    }
+  };
+  if constexpr (LAYOUT == NARROW) {
+    constexpr int AHEAD = 8;  // rows in flight
+    int stop = end_of(i);
+    for (; i < m; i += AHEAD) {
+      typename L::R r[AHEAD];
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = __fadd_rn(acc[e], f[e]);
+      for (int j = 0; j < AHEAD; ++j)
+        if (i + j < m && t.valid()) r[j] = t.load(a.g, sorted[i + j].y, a.tokens);
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        if (i + j >= m) break;
+        if (i + j == stop) {
+          turn(stop);
+          stop = end_of(stop);
+        }
+        add(r[j]);
       }
     }
+  } else {
+    // a ring of rows in shared memory, each warp's own columns: 32 granules,
+    // and for rows at an offset the one behind them
+    __shared__ __align__(16) char ring[kSumAhead][8][33 * 16];
+    const int warp = threadIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const uint32_t base = smem_addr(&ring[0][warp][0]) + lane * 16;
+    auto slot = [&](int k) { return base + ((uint32_t)k % kSumAhead) * (uint32_t)sizeof(ring[0]); };
+    const char* column = (const char*)a.g + (int64_t)t.c * L::ES;
+    const uint32_t pitch = (uint32_t)a.D * L::ES;
+    // elements of row y before its first granule's end (PHASED)
+    auto offset = [&](uint32_t y) { return (int)((y & (N - 1)) * (a.D & (N - 1)) & (N - 1)); };
+    auto fetch = [&](int k) {
+      if (k < m) {
+        const uint32_t y = sorted[k].y;
+        const char* p = column + (uint64_t)y * pitch;
+        if constexpr (LAYOUT == WIDE) {
+          if (t.valid()) cp_async16(slot(k), p);
+        } else {
+          // granules that hold columns of the row (nothing past the tensor)
+          const int s = offset(y);
+          auto copy = [&](int g) {
+            const int c = t.c - s + g * N;
+            const int64_t left = (a.tokens - 1 - (int64_t)y) * a.D + (a.D - c);
+            if (c < a.D)
+              cp_async16_part(slot(k) + g * 16, p + (g * N - s) * L::ES,
+                              (uint32_t)(left < N ? left : N) * L::ES);
+          };
+          copy(0);
+          if (s && lane == 31) copy(1);
+        }
+      }
+      cp_async_commit();
+    };
+    for (int k = 0; k < kSumAhead - 1; ++k) fetch(i + k);
+    for (;;) {
+      const int stop = end_of(i);
+      for (; i < stop; ++i) {
+        cp_async_wait<kSumAhead - 2>();
+        __syncwarp();  // the warp's copies of row i are there, row i - 1 has been read
+        fetch(i + kSumAhead - 1);
+        typename L::R r = lds16(slot(i));
+        if constexpr (LAYOUT == PHASED) {
+          const int s = offset(sorted[i].y);
+          if (s) r = shifted<L::ES>(r, lds16(slot(i) + 16), s);
+        }
+        add(r);
+      }
+      if (i >= m) break;
+      turn(i);
+    }
+    cp_async_wait<0>();
   }
-  flush(after == key);
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) acc[e] = f2_add(first[e], acc[e]);
+  flush(open);
 }
 
 // The parts of each run that crosses segments, added: 128 columns by 8 groups
@@ -511,19 +621,18 @@ __global__ void __launch_bounds__(256) embedding_join_kernel(SumArgs a) {
     const int c = (int)(it % tiles) * (32 * N) + lane;
     const int64_t i1 = (seg + 1) * kEmbedSegment;
     const uint32_t key = a.sorted[i1 - 1].x;
-    // the parts behind the first: segments that start with the key, 32 at a time
+    // the parts behind the first: segments that start with the key, 256 at a
+    // time (they are the first ones, so a count is enough)
     int64_t n = 0;
-    for (;;) {
-      const int64_t i = i1 + (n + lane) * kEmbedSegment;
-      const uint32_t on = __ballot_sync(0xFFFFFFFFu, i < a.tokens && a.sorted[i].x == key);
-      n += on == 0xFFFFFFFFu ? 32 : __ffs(~on) - 1;
-      if (on != 0xFFFFFFFFu) break;
+    for (int more = 256; more == 256; n += more) {
+      const int64_t i = i1 + (n + q * 32 + lane) * kEmbedSegment;
+      more = __syncthreads_count(i < a.tokens && a.sorted[i].x == key);
     }
     const float* p = a.partial + (seg * 2 + 1) * a.D + c;
     float v[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = 0.0f;
-#pragma unroll 2
+#pragma unroll 4
     for (int64_t j = q; j <= n; j += 8) {
       const float* at = p + (j ? 2 * j - 1 : 0) * a.D;
 #pragma unroll

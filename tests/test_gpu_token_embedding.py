@@ -103,6 +103,28 @@ def test_gradient(dtype, n, V, D, kind):
     assert torch.equal(bits(out), bits(again))
 
 
+@pytest.mark.parametrize("lengths", [
+    [32, 32, 64, 32, 96, 32], [31, 33, 32, 65, 63, 64, 1, 97, 95, 128], [1, 64, 31, 64, 64, 200],
+    [20, 44, 64, 20, 45, 63], [30, 500], [300, 1, 31, 2], list(range(1, 70)),
+    list(range(69, 0, -1))], ids=lambda v: "-".join(map(str, v[:6])))
+@pytest.mark.parametrize("D", [8, 77, 512])
+@dtypes
+def test_gradient_of_runs(dtype, D, lengths):
+    """Ids that stand a given number of times: runs that start, end and fill
+    blocks of 32 sorted tokens in every way."""
+    V, out_of_range = 2 * len(lengths) + 1, 37
+    ids = torch.cat([torch.full((n,), 2 * k + 1) for k, n in enumerate(lengths)]
+                    + [torch.full((out_of_range,), -1)])
+    ids = torch.cat([ids, torch.full((max(0, 257 - ids.numel()),), V)])
+    order = np.random.default_rng(seed_for("runs", *lengths)).permutation(ids.numel())
+    ids, g = ids[torch.from_numpy(order)].contiguous(), make((ids.numel(), D), dtype, "runs", D)
+    out, fresh = guarded((V, D), dtype, "cuda")
+    dit.embedding_backward(g.cuda(), ids.cuda(), V, 0.7, out=out)
+    torch.cuda.synchronize()
+    assert fresh()
+    ref.check_embedding_grad(out, g, ids, V, 0.7)
+
+
 @pytest.mark.parametrize("n", [70_000, 300_000])
 def test_gradient_of_many_tokens(n):
     """Several rounds of every warp of the sort, long runs, int32 ids, an id
