@@ -276,10 +276,10 @@ struct Unit {
 // ---------------------------------------------------------------------------
 
 // A team of `warps` warps (at most 16) holds a row; a CTA is blockDim.y teams
-// of blockDim.x threads.  combine adds (MAX: .y takes the larger of) a value of every warp
-// over the team: through shared memory, one barrier of the team's threads (a
-// named barrier; none for a team of one warp) and a butterfly.  The slots
-// alternate, so a slot is rewritten only behind the next call's barrier,
+// of blockDim.x threads.  combine adds (MAX: .y takes the larger of) a value of
+// every warp over the team: through shared memory, one barrier of the team's
+// threads (a named barrier; none for a team of one warp) and a butterfly.  The
+// slots alternate, so a slot is rewritten only behind the next call's barrier,
 // which the team's other warps reach after reading it.
 struct Team {
   float2* slots;  // this team's [2][warps]

@@ -13,8 +13,15 @@
 // sum that leaves [2^-100, 2^100] (a square that overflowed or went below
 // fp32's normal range) is taken again by its thread in fp64 and kept apart.
 // Each CTA writes one fp64 partial sum, and every CTA of the second kernel
-// adds them in the same order: the same call gives the same bits.  The second kernel takes the chunks
-// from the last, which the L2 may still hold, to the first.
+// adds them in the same order: the same call gives the same bits.  The second
+// kernel takes the chunks from the last, which the L2 may still hold, to the
+// first.
+//
+// Memory bounds large calls: 400 M bf16 elements in 291 tensors take 128 us for
+// the norm (6.3 TB/s) and 255 us for the clipping (6.3 TB/s read and written);
+// the norm has to be known before the first output, so the gradients are read
+// twice.  60 fp32 tensors of 2 M elements take 7.4 us, two launches; with sums in
+// fp64 they took 13.4.
 #include <math.h>
 
 #include <algorithm>

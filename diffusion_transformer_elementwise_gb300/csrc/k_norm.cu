@@ -13,14 +13,21 @@
 // (a hardware reciprocal y, 448 y, and the rest of it: about 2^-44 of m' is
 // lost) and scale = fl(fl(max|t| r) fl(1 / 448)).  The maximum is taken in the same
 // reduction as the sum of squares, and beside t's own roundings a code has the one of
-// its product, so few codes round otherwise than those of exact arithmetic.  Rows whose sum of
-// squares or maximum leaves [2^-100, 2^100] (overflow, infinities, NaN, all
+// its product, so few codes round otherwise than those of exact arithmetic.
+// Rows whose sum of squares or maximum leaves [2^-100, 2^100] (overflow, infinities, NaN, all
 // zero) take y itself: the maximum again, of y, and code = e4m3(y 448 /
 // max|y|).  An all-zero row or group has scale 0 and codes 0; a NaN or an
 // infinity makes its maximum NaN, so its scale and codes are NaN.
 //
 // A team of warps holds a row in registers, up to four units of 512 bytes a
-// warp; longer rows are read twice by one CTA each.
+// warp, so that each input is read once; longer rows are read twice by one CTA
+// each.  What bounds it: memory for the norm in the tensors' type (add, [32640,
+// 4096] bf16: 156 us, 6.87 TB/s; odd widths, [8193, 4099]: 49 us); the
+// instructions for E4M3 (per unit about 155 of a warp: [8192, 4096] bf16 in
+// groups of 128, 25.6 us, 3.9 TB/s; [4097, 3077] fp16, 24 us); the launch for
+// few rows (1.7 us).  Shared by both: fp32 weights in shared memory, so that a row
+// spends no instructions on widening them (fp8 groups 39.5 -> 30.7 us), and
+// consecutive units per warp, one base address each (30.7 -> 25.9 us).
 #include <algorithm>
 
 #include "dit_stat.cuh"
@@ -195,8 +202,8 @@ __device__ __forceinline__ float inverse_rms(float S, const NormArgs& a, Again a
 // copies).
 template <class T, int LAYOUT, int NU, int Q8, class Weights, class AfterRead>
 __device__ __forceinline__ void finish_row(const NormArgs& a, Unit<T, LAYOUT>& unit, Team& t,
-                                           int64_t row, int64_t e, const Raw<16> (&x)[NU], Weights weights,
-                                           AfterRead after_read) {
+                                           int64_t row, int64_t e, const Raw<16> (&x)[NU],
+                                           Weights weights, AfterRead after_read) {
   using R = NormRow<T, LAYOUT>;
   using U = Unit<T, LAYOUT>;
   constexpr int P = U::P;
@@ -382,7 +389,9 @@ __global__ void __launch_bounds__(kTeamThreads, 2) norm_staged_kernel(NormArgs a
     }
     finish_row<T, LAYOUT, NU, Q8>(
         a, unit, t, row, e, x,
-        [&](int j, F2(&wf)[U::P]) { staged_weight<T>(shared, ngr, (m * NU + j) * 32 + t.lane, wf); },
+        [&](int j, F2(&wf)[U::P]) {
+          staged_weight<T>(shared, ngr, (m * NU + j) * 32 + t.lane, wf);
+        },
         [&] {
           if (LAYOUT == SHIFTED) __syncwarp();  // every lane has read the slots
           prefetch(row + step);
