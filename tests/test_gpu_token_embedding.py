@@ -223,3 +223,18 @@ def test_offsets_past_32_bits():
     dit.embedding_backward(out, ids, V, out=table.fill_(1.0))
     torch.cuda.synchronize()
     assert torch.equal(table[-2:].cpu(), tail) and not table[:-2].any()
+
+
+@pytest.mark.parametrize("D", [8_000_000, 8_000_003])
+def test_gradient_of_rows_past_32_bits(D):
+    """Tokens whose rows lie past 2^32 bytes, through the sort, runs of two
+    and of more segments: rows of zeros and ones, whose sums are exact."""
+    n, V = 300, 4
+    t = torch.arange(n)
+    ids = torch.where(t % 3 > 0, 0, torch.where(t % 2 > 0, 2, 3))
+    value = (t * 7 % 5 < 2).to(torch.bfloat16)
+    g = value.cuda()[:, None].expand(n, D).contiguous()
+    out = dit.embedding_backward(g, ids.cuda(), V)
+    want = torch.zeros(V).index_add_(0, ids, value.float())
+    assert want.max() <= 256
+    assert bool((out == want.to(torch.bfloat16).cuda()[:, None]).all())
