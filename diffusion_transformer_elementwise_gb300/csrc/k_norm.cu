@@ -22,7 +22,7 @@
 // A team of warps holds a row in registers, up to four units of 512 bytes a
 // warp, so that each input is read once; longer rows are read twice by one CTA
 // each.  What bounds it: memory for the norm in the tensors' type (add, [32640,
-// 4096] bf16: 156 us, 6.87 TB/s; odd widths, [8193, 4099]: 49 us); the
+// 4096] bf16: 156 us, 6.87 TB/s; odd widths, [8193, 4099]: 44 us); the
 // instructions for E4M3 (per unit about 155 of a warp: [8192, 4096] bf16 in
 // groups of 128, 25.6 us, 3.9 TB/s; [4097, 3077] fp16, 24 us); the launch for
 // few rows (1.7 us).  Shared by both: fp32 weights in shared memory, so that a row
@@ -547,7 +547,15 @@ cudaError_t launch(const DeviceInfo& dev, const NormArgs& a, cudaStream_t s) {
       // (groups of 128 columns of rows at an offset)
       constexpr int L = LAYOUT == PHASED && Q8 == 2 ? SHIFTED : LAYOUT;
       if (units == 1) return launch_staged<T, L, 1, ADD, Q8>(dev, a, units, s);
-      if (units == 2) return launch_staged<T, L, 2, ADD, Q8>(dev, a, units, s);
+      // With an update, two units a warp and twice the warps, which hide more
+      // of the memory's latency (E4M3 in groups, [8192,4096]: 39.7 us, with
+      // four units 43.7; odd rows [8193,4099]: 44.0 and 48.5; [1,4099]: 3.0 and
+      // 4.0), but not for so few units ([30000,768] E4M3: 29.9 and 29.2) nor
+      // for E4M3 of odd rows, which gain 2 % ([8192,3001]: 59.7 and 60.8) and
+      // keep the bits of the two calls that the fused one stands for.  Without, the instructions bound it, and those of a row's reduction are
+      // fewer with four (E4M3, odd [8192,4099]: 29.7 us, with two 32.3).
+      if (units == 2 || (ADD && (L == WIDE || Q8 == 0) && units > 4 && units <= 2 * kTeamWarps))
+        return launch_staged<T, L, 2, ADD, Q8>(dev, a, units, s);
       return launch_staged<T, L, 4, ADD, Q8>(dev, a, units, s);
     }
   }
