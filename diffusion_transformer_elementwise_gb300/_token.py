@@ -75,7 +75,8 @@ def _workspace(given, nbytes, ref, stream):
     return given, given.data_ptr(), given.numel() * given.element_size()
 
 
-_get_device = torch._C._cuda_getDevice
+# (a torch without the private name still imports the package)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(dev, fn, what, *args):
