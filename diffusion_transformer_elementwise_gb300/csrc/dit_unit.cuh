@@ -373,6 +373,15 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, uint32_t rank) {
   return v;
 }
 
+// The launch of launch_after and launch_cluster.  An error is returned and not
+// left for the next launch's cudaGetLastError, which would report it again.
+template <class Args>
+cudaError_t launch_config(const cudaLaunchConfig_t& cfg, void (*kern)(Args), const Args& args) {
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
+}
+
 // A kernel launched by launch_after starts while the one before it in the
 // stream ends: it waits for that one's results (after_previous, before it
 // touches memory), which says early that the next may come (let_next).
@@ -394,7 +403,7 @@ cudaError_t launch_after(void (*kern)(Args), unsigned grid, dim3 block, size_t s
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args);
+  return launch_config(cfg, kern, args);
 }
 
 // A launch of one cluster of `grid` CTAs (16: the size that a kernel opts in to).
@@ -420,7 +429,7 @@ cudaError_t launch_cluster(void (*kern)(Args), unsigned grid, dim3 block, size_t
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args);
+  return launch_config(cfg, kern, args);
 }
 
 // Units of a row of D columns (PHASED: at most, over the rows' offsets).
