@@ -494,7 +494,10 @@ dit_status dit_selfcheck_static_workspace(void** workspace, int64_t* bytes);
  *   out = rnd(fl32(fl32(s * r) * fl32(weight_offset + weight[d])))
  * with s = x for dit_rmsnorm.  weight: [D], weight_offset 0 for a plain weight,
  * 1 for one stored as its difference from one.  The statistic is taken over
- * the residual as stored.  residual_out may be hidden; no other overlap of an
+ * the residual as stored.  With eps = 0 a row whose mean square rounds to zero
+ * in fp32 (below 2^-150) has r = +inf: infinities, and NaN where s is zero (E4M3: scales
+ * that are not finite).
+ * residual_out may be hidden; no other overlap of an
  * output with another tensor is allowed.  Any element-aligned pointer and any
  * D: tensors that start on 16-byte boundaries move in 16-byte accesses whatever D
  * (rows too long for registers only where D is a multiple of them), others
