@@ -47,9 +47,23 @@ struct NormGradArgs {
 };
 // the most CTAs (rows of `partial`) a call takes
 constexpr int64_t kNormGradMaxCtas = 304;
-// Up to this many rows that stay in registers take one launch; up to this
-// width they do in every type and layout, and the call needs no workspace.
-constexpr int64_t kFewRows = 128, kFewRowsD = 8189;
+// Up to this many rows that stay in registers take one launch of one cluster;
+// up to this width they do in every type and layout, and the call needs no
+// workspace.  Wider ones (16-bit types) bring a workspace, whose size is not
+// told the type, and take the cluster only up to this many elements.
+// Measured, one cluster against two launches over all SMs, with the skip path:
+// GPU us, and in brackets us a call among calls (host time included).
+//   fp32 128 x 64     3.3  (7.9) |  3.2 (10.6)   bf16 16 x 8184    8.1 (10.4) |  9.2 (11.8)
+//   fp32 128 x 2048   8.2 (10.4) |  3.8 (10.9)   bf16  1 x 16384  11.0 (13.5) | 14.7 (16.6)
+//   fp32  64 x 4096   8.6 (10.7) |  5.0 (10.8)   bf16 16 x 16384  11.8 (14.5) | 15.2 (17.8)
+//   fp32 128 x 4096  12.7 (14.8) |  5.1 (11.0)   bf16 64 x 16384  20.4 (22.7) | 16.5 (18.6)
+//   fp32 128 x 8184  20.9 (22.9) |  7.9 (10.7)   bf16 128 x 16384 31.6 (34.1) | 17.2 (19.7)
+// A call is the shorter in one cluster up to 2^18 elements; more of at most
+// kFewRowsD columns stay there because callers bring no workspace for them.
+constexpr int64_t kFewRows = 128, kFewRowsD = 8189, kFewElements = int64_t(1) << 18;
+inline bool few_rows(int64_t rows, int64_t D) {
+  return rows <= kFewRows && (D <= kFewRowsD || rows * D <= kFewElements);
+}
 // gw: the weight's gradient, or NULL
 cudaError_t launch_norm_grad(const DeviceInfo& dev, int dtype, int layout, const NormGradArgs& a,
                              void* gw, cudaStream_t s);

@@ -15,10 +15,11 @@
 // row of `partial`, and a second kernel adds the rows in order: no atomics, so
 // the same call gives the same bits.
 //
-// Few rows (kFewRows) take one launch and no workspace: the CTAs are one cluster,
-// and each adds a slice of gw's columns out of the others' shared memory.  (126 rows
-// of 2048 fp32 take 8.1 us on the GPU instead of 4.2, but a call 8.3 us of host time
-// instead of 18; a graph of such calls would rather have the two launches.)
+// Few rows (few_rows, with its measurements) take one launch and, up to
+// kFewRowsD columns, no workspace: the CTAs are one cluster, and each adds a
+// slice of gw's columns out of the others' shared memory.  That saves the host a
+// launch and a workspace, and costs the GPU up to 4 us (2^18 elements), which a graph
+// of such calls would rather not pay.
 //
 // Each lane copies the granules it will read itself into its own slots of
 // shared memory (cp.async), a row or two ahead, so the copies need no barrier
@@ -388,7 +389,7 @@ cudaError_t launch_rows(const DeviceInfo& dev, NormGradArgs a, int64_t* ctas, cu
 template <class T>
 cudaError_t launch(const DeviceInfo& dev, int layout, NormGradArgs a, void* gw, cudaStream_t s) {
   int64_t ctas = 0;
-  a.gw = a.rows <= kFewRows ? gw : nullptr;
+  a.gw = few_rows(a.rows, a.D) ? gw : nullptr;
   const bool skip = a.gres != nullptr;
   const cudaError_t e =
       layout == WIDE     ? (skip ? launch_rows<T, WIDE, true>(dev, a, &ctas, s)
