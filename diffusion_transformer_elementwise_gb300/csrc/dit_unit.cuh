@@ -3,7 +3,7 @@
 //
 // A unit is 512 bytes of a row: 256 columns of a 16-bit type or 128 of fp32,
 // 16 bytes per lane, kept packed in a Raw<16>.  A warp holds consecutive units
-// of a row.  Three layouts:
+// of a row.  Four layouts:
 //   WIDE     the rows are made of 16-byte granules.  Lane l holds granule l of
 //            the unit; a warp's access is 512 contiguous bytes.
 //   PHASED   the tensors start on 16-byte boundaries but the rows do not (an odd

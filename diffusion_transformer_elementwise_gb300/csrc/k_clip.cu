@@ -357,7 +357,10 @@ cudaError_t launch(const DeviceInfo& dev, const ClipTensor* t, int64_t count, bo
 
 }  // namespace
 
-// Few tensors take a launch with small parameters.
+// Few tensors take a launch with small parameters (1.9 KB, the others 28 KB).
+// Host us a call with its workspace, small tensors: 60 in the small form 10.4, in the
+// large one 12.3; 65 in batches of the small form 16.0, in the large one 12.3; 300
+// 37.5 and 18.6.
 cudaError_t launch_clip(const DeviceInfo& dev, const ClipTensor* t, int64_t count, bool clip,
                         float max_norm, float eps, double* partial, float* norm, cudaStream_t s) {
   return count <= 64 ? launch<64>(dev, t, count, clip, max_norm, eps, partial, norm, s)

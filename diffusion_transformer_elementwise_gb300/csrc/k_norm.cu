@@ -22,12 +22,15 @@
 // A team of warps holds a row in registers, up to four units of 512 bytes a
 // warp, so that each input is read once; longer rows are read twice by one CTA
 // each.  What bounds it: memory for the norm in the tensors' type (add, [32640,
-// 4096] bf16: 156 us, 6.87 TB/s; odd widths, [8193, 4099]: 44 us); the
-// instructions for E4M3 (per unit about 155 of a warp: [8192, 4096] bf16 in
-// groups of 128, 25.6 us, 3.9 TB/s; [4097, 3077] fp16, 24 us); the launch for
-// few rows (1.7 us).  Shared by both: fp32 weights in shared memory, so that a row
-// spends no instructions on widening them (fp8 groups 39.5 -> 30.7 us), and
-// consecutive units per warp, one base address each (30.7 -> 25.9 us).
+// 4096] bf16: 156 us, 6.87 TB/s; odd widths, [8193, 4099]: 45 us); the
+// instructions for E4M3 (162 of a warp per unit: [8192, 4096] bf16 in groups of
+// 128, 26.6 us, 3.8 TB/s; [4097, 3077] fp16, 24.2 us) and for the plain norm of odd
+// widths without an update (131: [8193, 4099] 24.4 us, 5.5 TB/s); the launch for
+// few rows (1.75 us).  Some E4M3 entries of 16-bit types spill (4 to 200 bytes).
+// Shared by both: fp32 weights in shared memory, so that a row spends no
+// instructions on widening them (they took E4M3 groups, [8192, 4096], from 39.5
+// to 30.7 us when it was added), and consecutive units per warp, one base address
+// each (then to 25.9).
 #include <algorithm>
 
 #include "dit_stat.cuh"
