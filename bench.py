@@ -159,7 +159,9 @@ def _code_only(text):
 # sources that the benchmarked kernels do not use: the token-transformer
 # operators
 OTHER_SOURCES = {"dit_token.h", "dit_token_api.cu", "dit_unit.cuh", "k_norm.cu", "k_norm_grad.cu",
-                 "k_embedding.cu", "k_clip.cu"}
+                 "k_embedding.cu", "k_clip.cu", "dit_attend.h", "dit_attend_api.cu",
+                 "dit_attend.cuh", "dit_heads.cuh", "k_rope.cu", "k_rope_grad.cu", "k_cache.cu",
+                 "k_attend.cu"}
 
 
 def kernel_source_hash():

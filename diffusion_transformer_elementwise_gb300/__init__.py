@@ -21,12 +21,32 @@ LTX-2-style video diffusion transformers.
   id, and the table's gradient by sorted tokens
 * :func:`grad_norm`, :func:`clip_grads`, :class:`TensorList` -- the 2-norm over
   many tensors, and clipping by it
+* :func:`rotary_frequencies`, :func:`rotary_table` -- cos and sin of the
+  angles of positions, over one or several axes
+* :func:`rope`, :func:`rmsnorm_rope`, :func:`rmsnorm_rope_backward` -- queries
+  and keys turned by them, with the norm of each head in the same pass, and
+  the gradients
+* :class:`KVCache`, :func:`cache_write`, :func:`cache_read`,
+  :func:`paged_attention` -- a paged cache of keys and values (E4M3 with a
+  scale per row, or in the dtype), and the attention of one new token per
+  sequence over it
 
 Each call is one kernel of ``libdit_elementwise.so`` (C ABI in
 ``include/dit_elementwise.h``), launched on the current torch stream; the
-gradients and the norm over tensors are a few.  Build
+gradients, the norm over tensors and the paged attention are a few.  Build
 the library with :func:`build`; without it every call raises.
 """
+from ._attend import (  # noqa: F401
+    KVCache,
+    cache_read,
+    cache_write,
+    paged_attention,
+    rmsnorm_rope,
+    rmsnorm_rope_backward,
+    rope,
+    rotary_frequencies,
+    rotary_table,
+)
 from ._binding import (  # noqa: F401
     DitError,
     ensure_checked,

@@ -98,8 +98,9 @@ def library() -> ctypes.CDLL:
             lib.dit_set_statistic.restype = ci
             lib.dit_get_statistic.argtypes = []
             lib.dit_get_statistic.restype = ci
-            from . import _token
+            from . import _attend, _token
             _token.declare(lib)
+            _attend.declare(lib)
             _lib = lib
     return _lib
 

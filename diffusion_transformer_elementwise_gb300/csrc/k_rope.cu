@@ -1,0 +1,171 @@
+// k_rope.cu -- rotary angles, and the rotation of queries and keys with or
+// without the norm of each head (sm_103a).
+//
+//   angle[t, j] = position * freq,   cos and sin in fp32
+//   y = x r (offset + w),  r = 1 / sqrt(mean(x^2) + eps)      (norm)
+//   a' = a cos - b sin,  b' = b cos + a sin                     per pair (a, b)
+#include <math_constants.h>
+
+#include "dit_attend.h"
+#include "dit_heads.cuh"
+
+namespace dit {
+namespace {
+
+// ---------------------------------------------------------------------------
+// the table
+// ---------------------------------------------------------------------------
+
+constexpr int kTableThreads = 256;
+
+// A frequency in turns per unit: for integer positions |f| modulo one turn as a
+// 64-bit fraction (a position times it, modulo 2^64, is the angle whatever the position),
+// for fp32 ones as the sum of three fp32 numbers.
+struct Turns {
+  uint64_t fraction;
+  float part[3];
+  bool negative, usable;
+};
+__device__ __forceinline__ Turns turns_of(double freq) {
+  Turns t;
+  const double f = freq * 0.15915494309189535;  // 1 / (2 pi)
+  t.usable = isfinite(freq);
+  t.negative = f < 0.0;
+  const double m = fabs(f);
+  t.fraction = t.usable ? __double2ull_rn((m - floor(m)) * 18446744073709551616.0) : 0;
+  t.part[0] = (float)f;
+  t.part[1] = (float)(f - (double)t.part[0]);
+  t.part[2] = (float)(f - (double)t.part[0] - (double)t.part[1]);
+  return t;
+}
+// a part of a turn in [-1/2, 1/2] or a little beyond
+__device__ __forceinline__ float turn_part(const Turns& f, int64_t position) {
+  int64_t x = (int64_t)((uint64_t)position * f.fraction);
+  if (f.negative) x = (int64_t)(0 - (uint64_t)x);
+  return (float)x * 0x1p-64f;
+}
+__device__ __forceinline__ float turn_part(const Turns& f, float p) {
+  // p f as high parts and their errors, each without its whole turns
+  float sum = __fmul_rn(p, f.part[2]);
+  sum = __fadd_rn(sum, -rintf(sum));
+#pragma unroll
+  for (int i = 1; i >= 0; --i) {
+    const float high = __fmul_rn(p, f.part[i]);
+    const float low = __fmaf_rn(p, f.part[i], -high);
+    sum = __fadd_rn(sum, __fadd_rn(low, -rintf(low)));
+    sum = __fadd_rn(sum, __fadd_rn(high, -rintf(high)));
+  }
+  return __fadd_rn(sum, -rintf(sum));
+}
+
+// A thread has a column and every gridDim.y-th token.
+template <class P>
+__global__ void __launch_bounds__(kTableThreads) table_kernel(const __grid_constant__ TableArgs a) {
+  const int columns = min(a.R, kTableThreads);
+  const int rows = kTableThreads / columns;
+  const int row = threadIdx.x / columns;
+  if (row >= rows) return;
+  for (int j = threadIdx.x % columns; j < a.R; j += columns) {
+    const Turns f = turns_of(a.freqs[j]);
+    int axis = 0;
+    while (axis < a.axes - 1 && j >= a.end[axis]) ++axis;
+    const P* positions = (const P*)a.positions + (int64_t)axis * a.tokens;
+    for (int64_t t = (int64_t)blockIdx.x * rows + row; t < a.tokens; t += (int64_t)gridDim.x * rows) {
+      float s, c;
+      if constexpr (sizeof(P) == 4 && P(0.5) != P(0)) {
+        const float p = positions[t];
+        sincospif(2.0f * turn_part(f, p), &s, &c);
+        if (!isfinite(p)) s = c = CUDART_NAN_F;
+      } else {
+        sincospif(2.0f * turn_part(f, (int64_t)positions[t]), &s, &c);
+      }
+      if (!f.usable) s = c = CUDART_NAN_F;
+      a.cos[t * a.R + j] = c;
+      a.sin[t * a.R + j] = s;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the rotation
+// ---------------------------------------------------------------------------
+
+constexpr int kRowThreads = 256;
+
+// Any view: a warp has a head, an element per access.
+template <class T, bool NORM>
+__global__ void __launch_bounds__(kRowThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int heads = a.t[0].H + a.t[1].H;
+  const int64_t rows = a.tokens * heads;
+  const int64_t stride = (int64_t)gridDim.x * (kRowThreads / 32);
+  for (int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); i < rows; i += stride) {
+    const HeadRow row(a, i, heads);
+    const RopeTensor& t = a.t[row.tensor];
+    const T* x = (const T*)t.x.p + row.at(t.x);
+    T* out = (T*)t.out.p + row.at(t.out);
+    float r = 1.0f;
+    if constexpr (NORM) {
+      float sum = 0.0f;
+      for (int c = lane; c < a.D; c += 32) {
+        const float v = to_float(x[c]);
+        sum = __fmaf_rn(v, v, sum);
+      }
+      r = inverse_rms(lanes_sum<32>(sum), a.D, a.eps);
+    }
+    auto value = [&](int c) {
+      const float v = to_float(x[c]);
+      if constexpr (!NORM) return v;
+      return __fmul_rn(__fmul_rn(v, r), __fadd_rn(a.offset, to_float(((const T*)t.w)[c])));
+    };
+    const float* cs = a.cos + row.table * a.R;
+    const float* sn = a.sin + row.table * a.R;
+    for (int j = lane; j < a.R; j += 32) {
+      const int c = a.interleaved ? 2 * j : j, d = a.interleaved ? c + 1 : c + a.R;
+      const float2 y = turned(value(c), value(d), cs[j], a.inverse ? -sn[j] : sn[j]);
+      out[c] = from_float<T>(y.x);
+      out[d] = from_float<T>(y.y);
+    }
+    for (int c = 2 * a.R + lane; c < a.D; c += 32) {
+      if constexpr (NORM)
+        out[c] = from_float<T>(value(c));
+      else
+        out[c] = x[c];
+    }
+  }
+}
+
+template <class T>
+cudaError_t launch(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {
+  const int64_t rows = a.tokens * (a.t[0].H + a.t[1].H);
+  const bool norm = a.t[0].w || a.t[1].w;
+  const auto kern = norm ? rope_kernel<T, true> : rope_kernel<T, false>;
+  const int64_t warps = kRowThreads / 32;
+  const int64_t most = (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kRowThreads) * 8;
+  kern<<<(unsigned)std::min(most, (rows + warps - 1) / warps), kRowThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_table(const DeviceInfo& dev, int position_type, const TableArgs& a,
+                         cudaStream_t s) {
+  const int64_t rows = kTableThreads / std::min(a.R, kTableThreads);
+  const int64_t most = (int64_t)dev.sm_count * 8;
+  const unsigned grid = (unsigned)std::min(most, (a.tokens + rows - 1) / rows);
+  if (position_type == DIT_POS_INT32)
+    table_kernel<int32_t><<<grid, kTableThreads, 0, s>>>(a);
+  else if (position_type == DIT_POS_INT64)
+    table_kernel<int64_t><<<grid, kTableThreads, 0, s>>>(a);
+  else
+    table_kernel<float><<<grid, kTableThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rope(const DeviceInfo& dev, int dtype, const RopeArgs& a, cudaStream_t s) {
+  return dtype == 0   ? launch<__nv_bfloat16>(dev, a, s)
+         : dtype == 1 ? launch<__half>(dev, a, s)
+                      : launch<float>(dev, a, s);
+}
+
+}  // namespace dit

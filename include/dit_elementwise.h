@@ -28,6 +28,17 @@
  *   dit_embedding_backward         the table's gradient, by sorted tokens
  *   dit_grad_norm, dit_clip_grads  the 2-norm over many tensors; clipping
  *
+ * and around attention, for both:
+ *
+ *   dit_rotary_table               cos and sin of the positions' angles, over
+ *                                  one or several axes
+ *   dit_rope, dit_rmsnorm_rope     queries and keys turned by them, with the
+ *                                  norm of each head in the same pass
+ *   dit_rmsnorm_rope_backward      its gradients
+ *   dit_cache_write, dit_cache_read  a paged cache of keys and values, E4M3
+ *                                  with a scale per row or in the dtype
+ *   dit_paged_attention            one new token per sequence over that cache
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * Tensors.  Every tensor is contiguous, row-major [B, L, D] in device memory
@@ -613,6 +624,167 @@ dit_status dit_grad_norm(float* norm, const dit_tensor* tensors, int64_t count, 
 dit_status dit_clip_grads(float* norm, const dit_tensor* tensors, int64_t count, float max_norm,
                           float eps, void* workspace, int64_t workspace_bytes,
                           dit_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators around attention
+ *
+ * What a transformer does between the projection of queries, keys and values and the
+ * projection of attention's output, as far as it is bound by memory: the
+ * rotation of queries and keys by their positions, with the norm of each head
+ * in the same pass, its gradient, a paged cache of keys and values, and the attention
+ * of one new token per sequence over it.  The conventions of the token-transformer
+ * operators hold (workspaces, one order for every sum, several kernels a
+ * call), with these differences.
+ *   Tensors of heads may be views with any strides but the last: dit_heads.
+ *   Strides are in elements and not negative; a stride of 0 repeats an input.
+ *   An output's elements must lie apart from each other and from every other
+ *   tensor of the call (DIT_ERR_ALIAS), which views that interleave without
+ *   touching, such as the queries and keys of one packed projection, do; where an
+ *   output may be an input, it is exactly that view.
+ * ------------------------------------------------------------------------- */
+
+/* Element (b, l, h, d) of a tensor [B, L, H, D] is p[b batch + l token + h head + d].
+ * Operators over tokens alone ([tokens, H, D]) do not read `batch`. */
+typedef struct {
+  void* p; /* inputs are not written */
+  int64_t batch, token, head;
+} dit_heads;
+
+/*
+ * Rotary angles:  angle[t, j] = positions[axis(j), t] * freqs[j],
+ *   cos[t, j] = rnd(cos(angle)),  sin[t, j] = rnd(sin(angle))
+ * positions: [axes, tokens]; the first sections[0] columns belong to axis 0,
+ * the next sections[1] to axis 1, and so on (one axis for text; time, height and width
+ * for images and video).  sections: a HOST array of `axes` (1 to
+ * DIT_MAX_AXES) counts, read during the call only; R is their sum, at most 512.  freqs:
+ * [R], fp64, the angle per unit of position.  cos, sin: fp32 [tokens, R].
+ * The frequency is taken in turns, in fp64 (within 2^-52 of it), and the angle reduced to a part of
+ * a turn before it is rounded: for integer positions as a 64-bit fraction of a
+ * turn (exact but for the frequency's 64-bit fraction, 2^-64 |position| turns), for fp32 ones as a sum of
+ * fp32 products and their errors.  The part of a turn, its sine and its cosine are fp32.  A
+ * position or frequency that is not finite, or an fp32 product that overflows, gives NaN.
+ */
+#define DIT_MAX_AXES 8
+typedef enum { DIT_POS_INT32 = 0, DIT_POS_INT64 = 1, DIT_POS_FP32 = 2 } dit_position_type;
+
+dit_status dit_rotary_table(float* cos, float* sin, const void* positions, const double* freqs,
+                            int64_t tokens, const int64_t* sections, int64_t axes,
+                            dit_position_type position_type, dit_stream_t stream);
+
+/*
+ * Rotation of queries and keys: with the pair (a, b) of columns (j, j + R), or
+ * (2j, 2j + 1) where `interleaved`, for j < R, and the token's row of the table,
+ *   a' = rnd(a cos - b sin),  b' = rnd(b cos + a sin)
+ * (inverse: with -sin, which is the gradient); columns from 2R on are copied.
+ * Each tensor is [B, L, H, D]: Hq heads of queries, Hk of keys, 2R <= D <= 1024,
+ * H at most 65535.
+ * cos, sin: fp32 [table_rows, R] with table_rows = B * L, or L (one table for
+ * all batches).  k and k_out may be NULL (Hk = 0).  An output may be its input.
+ */
+dit_status dit_rope(const dit_heads* q_out, const dit_heads* k_out, const dit_heads* q,
+                    const dit_heads* k, const float* cos, const float* sin, int64_t B, int64_t L,
+                    int64_t Hq, int64_t Hk, int64_t D, int64_t R, int64_t table_rows,
+                    int interleaved, int inverse, dit_dtype dtype, dit_stream_t stream);
+
+/*
+ * The same after a weighted RMSNorm of each head (its D columns), in one pass and
+ * rounded once:  y = x * r * (weight_offset + weight),  r = 1 / sqrt(mean(x^2) + eps).
+ * weight_q, weight_k: [D], shared by the heads.  The statistic is a
+ * fp32 sum, a correctly rounded quotient, root and reciprocal.  R may be 0 (the norm alone; cos and
+ * sin may then be NULL).
+ */
+dit_status dit_rmsnorm_rope(const dit_heads* q_out, const dit_heads* k_out, const dit_heads* q,
+                            const dit_heads* k, const void* weight_q, const void* weight_k,
+                            const float* cos, const float* sin, int64_t B, int64_t L, int64_t Hq,
+                            int64_t Hk, int64_t D, int64_t R, int64_t table_rows, float eps,
+                            float weight_offset, int interleaved, dit_dtype dtype,
+                            dit_stream_t stream);
+
+/*
+ * Its gradient.  With u the gradient of the output turned back, n = x * r and
+ * t = u * (weight_offset + weight),
+ *   grad_x      = rnd(r * (t - n * mean(t * n)))        (grad_q, grad_k)
+ *   grad_weight = rnd(sum over tokens and heads of u * n)
+ * in fp32.  grad_weight_q and grad_weight_k may each be NULL (a frozen weight).  q_grad
+ * and k_grad, the outputs, may be the gradients they come from (q_out_grad,
+ * k_out_grad).
+ */
+int64_t dit_rmsnorm_rope_backward_workspace_bytes(int64_t D);
+
+dit_status dit_rmsnorm_rope_backward(const dit_heads* q_grad, const dit_heads* k_grad,
+                                     void* grad_weight_q, void* grad_weight_k,
+                                     const dit_heads* q_out_grad, const dit_heads* k_out_grad,
+                                     const dit_heads* q, const dit_heads* k, const void* weight_q,
+                                     const void* weight_k, const float* cos, const float* sin,
+                                     int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t D,
+                                     int64_t R, int64_t table_rows, float eps, float weight_offset,
+                                     int interleaved, dit_dtype dtype, void* workspace,
+                                     int64_t workspace_bytes, dit_stream_t stream);
+
+/*
+ * A paged cache of keys and values.  Each of k and v is [pages, heads, page_size,
+ * D], page p starting at p * page_stride elements (at least heads * page_size * D, so that
+ * both may be halves of one allocation) and the rest contiguous.  format: a dit_dtype value, or
+ * DIT_E4M3: codes with one scale per row of D, scales [pages, heads,
+ * page_size] fp32, page p at p * scale_stride.  The value is code * scale.
+ * pages * page_size is at most 2^31 - 1, D at most 1024, page_stride at most 2^40.
+ * A place ("slot") is page * page_size + the token's place in the page.
+ */
+#define DIT_E4M3 3
+typedef struct {
+  void *k, *v;
+  float *k_scales, *v_scales; /* DIT_E4M3 only */
+  int64_t pages, heads, page_size, D;
+  int64_t page_stride, scale_stride;
+  int64_t format;
+} dit_cache;
+
+/*
+ * Write the keys and values [tokens, heads, D] of dtype `dtype` (the cache's, where it is one) to
+ * slots[t]; a token whose slot is outside [0, pages * page_size) is not
+ * written.  The slots within that range must differ from each other: a slot that is named twice
+ * gets some of the rows of both.  In E4M3, with m the maximum of |x| over the row,
+ *   scale = fl32(m / 448),  code = e4m3(fl32(x * 448 / m)),
+ * the quotient carried in two fp32 numbers.  m = 0 gives scale 0 and codes 0; a NaN or an
+ * infinity makes the row's scale and codes NaN.  Nothing else of the cache changes.
+ */
+dit_status dit_cache_write(const dit_cache* cache, const dit_heads* k, const dit_heads* v,
+                           int64_t tokens, const void* slots, dit_id_type id_type,
+                           dit_dtype dtype, dit_stream_t stream);
+
+/* The reverse:  k[t] = the row of slots[t], in E4M3 rnd(code * scale), a row of zeros where
+ * the slot is outside the cache. */
+dit_status dit_cache_read(const dit_cache* cache, const dit_heads* k, const dit_heads* v,
+                          int64_t tokens, const void* slots, dit_id_type id_type, dit_dtype dtype,
+                          dit_stream_t stream);
+
+/*
+ * Attention of one new token per sequence: for sequence b of n = lengths[b] tokens, query head
+ * h and its key head h / (Hq / heads), over the tokens t from
+ * max(0, n - window) (window 0: from 0) to n,
+ *   s[t] = scale * sum_d q[b, h, d] k[t, d],  w[t] = exp(s[t] - max s),
+ *   out[b, h] = rnd(sum w[t] v[t] / sum w[t]),  lse[b, h] = log(sum exp(s[t])).
+ * Token t is at place t % page_size of page pages[b, t / page_size].  The new token's own
+ * key and value are in the cache (write them first).
+ *   q, out: [B, Hq, D] (dit_heads without `batch`); Hq a multiple of the cache's heads; D <= 512.
+ *   pages: int32 [B, width], row b at b * pages_stride.  lengths: [B], int32 or
+ *   int64.  A length is cut to [0, width * page_size] (at most 2^31 - 4096).  A token whose page
+ *   is outside the cache is left out.  A sequence with no token has out 0
+ *   and lse -infinity.  What lies in the cache's pages behind a sequence does not matter, NaN included.
+ *   lse: fp32 [B, Hq], or NULL.
+ * Keys, values and weights of 16-bit types are multiplied on the tensor cores: the weights
+ * are rounded to that type there (E4M3: to fp16, after the value's scale is
+ * taken in), products and sums are fp32.  For fp32 queries everything is fp32.
+ * The length is split over the GPU and the parts joined by a second kernel, in one order for
+ * given lengths.
+ */
+int64_t dit_paged_attention_workspace_bytes(int64_t Hq, int64_t heads, int64_t D);
+
+dit_status dit_paged_attention(const dit_heads* out, float* lse, const dit_heads* q,
+                               const dit_cache* cache, const int32_t* pages, int64_t pages_stride,
+                               int64_t width, const void* lengths, int64_t B, int64_t Hq,
+                               float scale, int64_t window, dit_id_type id_type, dit_dtype dtype,
+                               void* workspace, int64_t workspace_bytes, dit_stream_t stream);
 
 #ifdef __cplusplus
 }
