@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
   const int segments = (int)a.c.heads * blocks;
   Part part = part_of<kThreads>(a, segments, 8, numbers);
   if (tid < 2) a.owner[2 * blockIdx.x + tid] = -1;
+  let_next();
   const int slot_rows = min(a.group, kAttendRows);
   Segment g;
   while (next_segment(a, part, segments, g)) {
@@ -186,32 +187,36 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 }
 
 template <class T, class K>
-cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, cudaStream_t s) {
+cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cudaStream_t s) {
   const auto kern = attend_kernel<T, K>;
   const size_t smem = (size_t)2 * kAttendRows * a.c.D * 4;
   static std::atomic<int> opted[kOptinDevices];
-  cudaError_t e = allow_shared((const void*)kern, dev, opted);
+  const cudaError_t e = allow_shared((const void*)kern, dev, opted);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = std::min(
-      kAttendMaxCtas, (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kThreads, smem));
-  kern<<<(unsigned)ctas, kThreads, smem, s>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_after(join_kernel<T>, (unsigned)ctas, kThreads, 0, s, JoinArgs{a, (int)ctas});
+  *ctas = std::min(kAttendMaxCtas,
+                   (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kThreads, smem));
+  kern<<<(unsigned)*ctas, kThreads, smem, s>>>(a);
+  return cudaGetLastError();
 }
 
 template <class T>
-cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, cudaStream_t s) {
-  return a.c.format == DIT_E4M3 ? launch<T, uint8_t>(dev, a, s) : launch<T, T>(dev, a, s);
+cudaError_t launch(const DeviceInfo& dev, bool mma, const AttendArgs& a, cudaStream_t s) {
+  int64_t ctas = 0;
+  const cudaError_t e = mma                        ? launch_attend_mma(dev, std::is_same<T, __half>::value, a, &ctas, s)
+                        : a.c.format == DIT_E4M3 ? launch<T, uint8_t>(dev, a, &ctas, s)
+                                                 : launch<T, T>(dev, a, &ctas, s);
+  if (e != cudaSuccess) return e;
+  return launch_after(join_kernel<T>, (unsigned)ctas, kThreads, 0, s, JoinArgs{a, (int)ctas});
 }
 
 }  // namespace
 
 cudaError_t launch_attend(const DeviceInfo& dev, int dtype, bool granules, const AttendArgs& a,
                           cudaStream_t s) {
-  return dtype == 0   ? launch<__nv_bfloat16>(dev, a, s)
-         : dtype == 1 ? launch<__half>(dev, a, s)
-                      : launch<float>(dev, a, s);
+  const bool mma = dtype != 2 && granules && a.c.D <= 256;
+  return dtype == 0   ? launch<__nv_bfloat16>(dev, mma, a, s)
+         : dtype == 1 ? launch<__half>(dev, mma, a, s)
+                      : launch<float>(dev, false, a, s);
 }
 
 }  // namespace dit
