@@ -31,14 +31,7 @@ struct Sequence {
   }
 };
 
-// A CTA's part of the line, and a walk over its segments.
-struct Part {
-  int64_t begin, end;   // tiles of the line
-  int64_t at;           // where the walk is
-  int b;                // its sequence
-  int64_t start;        // where that sequence starts on the line
-};
-
+// The sum of `v` over the CTA's threads.  shared: THREADS / 32 numbers.
 template <int THREADS>
 __device__ __forceinline__ int64_t cta_sum(int64_t v, int64_t* shared) {
 #pragma unroll
@@ -52,84 +45,129 @@ __device__ __forceinline__ int64_t cta_sum(int64_t v, int64_t* shared) {
   return v;
 }
 
-// segments: of a sequence.  least: tiles that a CTA takes at least.
-// shared: THREADS / 32 + 2 numbers.
-template <int THREADS>
-__device__ __forceinline__ Part part_of(const AttendArgs& a, int segments, int least, int64_t* shared) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t mine = 0;
-  for (int b = tid; b < a.B; b += THREADS) mine += Sequence(a, b).tiles;
-  const int64_t total = cta_sum<THREADS>(mine, shared) * segments;
-  const int64_t per = max((int64_t)least, (total + gridDim.x - 1) / gridDim.x);
-  Part p;
-  p.begin = min((int64_t)blockIdx.x * per, total);
-  p.end = min(p.begin + per, total);
-  p.at = p.begin;
-  p.b = 0;
-  p.start = 0;
-  if (p.begin >= p.end) return p;
-  // the sequence that holds `begin`
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-    const int b = b0 + tid;
-    const int64_t n = b < a.B ? (int64_t)Sequence(a, b).tiles * segments : 0;
-    int64_t sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    if (lane == 31) shared[warp] = sum;
-    __syncthreads();
-    int64_t upto = before + sum;
-    int64_t all = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < warp) upto += shared[w];
-      all += shared[w];
-    }
-    if (p.begin < upto && p.begin >= upto - n) {
-      shared[THREADS / 32] = b;
-      shared[THREADS / 32 + 1] = upto - n;
-    }
-    __syncthreads();
-    before += all;
-    if (p.begin < before) break;
-  }
-  p.b = (int)shared[THREADS / 32];
-  p.start = shared[THREADS / 32 + 1];
-  return p;
-}
+// A place of the line: a sequence, and where on the line it starts.
+struct Mark {
+  int b;
+  int64_t start;
+};
 
-// The next segment of a part: which, its tiles within the part, and where
-// its result goes.
+// The line: each of a sequence's `segments` segments takes its tiles and `extra` units more, which stand for
+// the time that a segment takes whatever its length.
+struct Line {
+  int segments, extra;
+  __device__ __forceinline__ int64_t length(const Sequence& q) const {
+    return (int64_t)(q.tiles + extra) * segments;
+  }
+  template <int THREADS>
+  __device__ __forceinline__ int64_t total(const AttendArgs& a, int64_t* shared) const {
+    int64_t mine = 0;
+    for (int b = threadIdx.x; b < a.B; b += THREADS) mine += length(Sequence(a, b));
+    return cta_sum<THREADS>(mine, shared);
+  }
+  // the sequence that holds unit `at` of the line, for the whole CTA; shared: THREADS / 32 + 2 numbers
+  template <int THREADS>
+  __device__ __forceinline__ Mark find(const AttendArgs& a, int64_t at, int64_t* shared) const {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+      const int b = b0 + tid;
+      const int64_t n = b < a.B ? length(Sequence(a, b)) : 0;
+      int64_t upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      if (lane == 31) shared[warp] = upto;
+      __syncthreads();
+      upto += before;
+#pragma unroll
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) upto += shared[w];
+        before += shared[w];
+      }
+      if (at < upto && at >= upto - n) {
+        shared[THREADS / 32] = b;
+        shared[THREADS / 32 + 1] = upto - n;
+      }
+      __syncthreads();
+      if (at < before) break;
+    }
+    const Mark m{(int)shared[THREADS / 32], shared[THREADS / 32 + 1]};
+    __syncthreads();
+    return m;
+  }
+  // the same for one warp, from a mark at or before it
+  __device__ __forceinline__ Mark find_from(const AttendArgs& a, int64_t at, Mark m) const {
+    const int lane = threadIdx.x & 31;
+    for (;;) {
+      const int b = m.b + lane;
+      const int64_t n = b < a.B ? length(Sequence(a, b)) : 0;
+      int64_t upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      upto += m.start;
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, at < upto);
+      if (past) {
+        const int first = __ffs(past) - 1;
+        return Mark{m.b + first, __shfl_sync(0xFFFFFFFFu, upto - n, first)};
+      }
+      m.start = __shfl_sync(0xFFFFFFFFu, upto, 31);
+      m.b += 32;
+    }
+  }
+};
+
+// A segment's tiles within a part of the line.
 struct Segment {
   int b, s;             // sequence, and number within it
-  int64_t id;           // b * segments + s
   int lo, hi;           // tokens of the sequence
   int first, last;      // tiles here, of the sequence's
-  bool head, tail;      // shared with the CTAs before, or only with those after
+  bool open, head, tail;  // goes on in the next part; begun in an earlier one; begun here and open
 };
-__device__ __forceinline__ bool next_segment(const AttendArgs& a, Part& p, int segments, Segment& g) {
-  if (p.at >= p.end) return false;
-  Sequence q(a, p.b);
-  if (p.at >= p.start + (int64_t)q.tiles * segments) {
-    p.start += (int64_t)q.tiles * segments;
-    q = Sequence(a, ++p.b);
+
+// A walk over the segments of the part [at, end) of the line.
+struct Walk {
+  int64_t at, end, start;  // start: of the segment at hand
+  int b, s;
+  Sequence q;
+  // mark: the sequence that holds `at`, if the part is not empty
+  __device__ __forceinline__ Walk(const AttendArgs& a, const Line& line, int64_t at, int64_t end, Mark mark)
+      : at(at), end(end), start(mark.start), b(mark.b), s(0), q(a, mark.b) {
+    if (at >= end) return;
+    const int64_t n = q.tiles + line.extra;
+    s = (int)((at - start) / n);
+    start += s * n;
   }
-  g.b = p.b;
-  g.s = (int)((p.at - p.start) / q.tiles);
-  g.id = (int64_t)p.b * segments + g.s;
-  const int64_t start = p.start + (int64_t)g.s * q.tiles, end = start + q.tiles;
-  g.lo = q.lo;
-  g.hi = q.hi;
-  g.first = q.first + (int)(p.at - start);
-  g.last = q.first + (int)(min(end, p.end) - start);
-  g.head = start < p.begin;
-  g.tail = !g.head && end > p.end;
-  p.at = min(end, p.end);
-  return true;
-}
+  __device__ __forceinline__ bool next(const AttendArgs& a, const Line& line, Segment& g) {
+    while (at < end) {
+      const int64_t n = q.tiles + line.extra, stop = min(end - start, n);
+      const int first = max(0, (int)(at - start) - line.extra), last = max(0, (int)stop - line.extra);
+      g.b = b;
+      g.s = s;
+      g.lo = q.lo;
+      g.hi = q.hi;
+      g.first = q.first + first;
+      g.last = q.first + last;
+      g.head = first > 0;
+      g.open = last < q.tiles;
+      g.tail = g.open && !g.head;
+      at = start + stop;
+      if (stop == n) {
+        start = at;
+        if (++s == line.segments) {
+          s = 0;
+          if (++b < a.B) q = Sequence(a, b);
+        }
+      }
+      if (last > first) return true;  // (no tile where the part ends within `extra`)
+    }
+    return false;
+  }
+};
 
 // Where token t's rows lie: its row's element and scale number, or -1.
 struct Place {

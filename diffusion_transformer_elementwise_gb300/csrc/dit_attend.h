@@ -77,9 +77,13 @@ constexpr int64_t kAttendMaxCtas = 608;
 cudaError_t launch_attend(const DeviceInfo& dev, int dtype, bool granules, const AttendArgs& a,
                           cudaStream_t s);
 
-// the tensor cores' form of its first kernel, for 16-bit queries (half: fp16) of
-// at most 256 columns in 16-byte granules (k_attend_mma.cu)
-cudaError_t launch_attend_mma(const DeviceInfo& dev, bool half, const AttendArgs& a, int64_t* ctas,
+// The tensor cores' form of its first kernel (k_attend_mma.cu): for 16-bit queries of at most 256
+// columns in 16-byte granules.  Its CTAs and their warps have parts of their own behind
+// `partial`: [ctas][warps][2][rows][D + 2].
+constexpr int64_t kAttendMmaCtas = 160;
+constexpr int kAttendWarps = 16;
+bool attend_mma_takes(int dtype, bool granules, const AttendArgs& a);
+cudaError_t launch_attend_mma(const DeviceInfo& dev, int dtype, const AttendArgs& a, int64_t* ctas,
                               cudaStream_t s);
 
 }  // namespace dit

@@ -456,8 +456,8 @@ int64_t dit_paged_attention_workspace_bytes(int64_t Hq, int64_t heads, int64_t D
       D > kMaxAttendDim)
     return -1;
   const int64_t rows = std::min<int64_t>(Hq / heads, dit::kAttendRows);
-  return round_up(dit::kAttendMaxCtas * 2 * 8) +
-         round_up(dit::kAttendMaxCtas * 2 * rows * (D + 2) * 4);
+  const int64_t parts = std::max(dit::kAttendMaxCtas, dit::kAttendMmaCtas * (1 + dit::kAttendWarps));
+  return round_up(dit::kAttendMaxCtas * 2 * 8) + round_up(parts * 2 * rows * (D + 2) * 4);
 }
 
 dit_status dit_paged_attention(const dit_heads* out, float* lse, const dit_heads* q,

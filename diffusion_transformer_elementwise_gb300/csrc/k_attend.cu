@@ -12,6 +12,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = 64;  // at a time
 constexpr int kMaxD = 512;
+constexpr int kExtra = 4, kLeast = 8;  // units of a segment beside its tiles; the smallest part
 
 template <class K>
 __device__ __forceinline__ float cached(const void* p, int64_t i) {
@@ -36,13 +37,17 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
   float* o = space + kAttendRows * D;  // [rows][D]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int blocks = (a.group + kAttendRows - 1) / kAttendRows;
-  const int segments = (int)a.c.heads * blocks;
-  Part part = part_of<kThreads>(a, segments, 8, numbers);
+  const Line line{(int)a.c.heads * blocks, kExtra};
+  const int64_t total = line.total<kThreads>(a, numbers);
+  const int64_t per = max((int64_t)kLeast, (total + gridDim.x - 1) / gridDim.x);
+  const int64_t begin = min(blockIdx.x * per, total), end = min(begin + per, total);
   if (tid < 2) a.owner[2 * blockIdx.x + tid] = -1;
   let_next();
+  if (begin >= end) return;
   const int slot_rows = min(a.group, kAttendRows);
+  Walk walk(a, line, begin, end, line.find<kThreads>(a, begin, numbers));
   Segment g;
-  while (next_segment(a, part, segments, g)) {
+  while (walk.next(a, line, g)) {
     const int head = g.s / blocks, row0 = (g.s - head * blocks) * kAttendRows;
     const int rows = min(kAttendRows, a.group - row0);
     const int h0 = head * a.group + row0;
@@ -127,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
     if (g.head || g.tail) {
       const int slot = g.head ? 0 : 1;
       float* out = a.partial + ((int64_t)blockIdx.x * 2 + slot) * slot_rows * (D + 2);
-      if (tid == 0) a.owner[2 * blockIdx.x + slot] = g.id;
+      if (tid == 0) a.owner[2 * blockIdx.x + slot] = (int64_t)g.b * line.segments + g.s;
       for (int i = tid; i < rows * D; i += kThreads) out[2 * slot_rows + i] = o[i];
       if (tid < rows) {
         out[tid] = m[tid];
@@ -202,7 +207,7 @@ cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cu
 template <class T>
 cudaError_t launch(const DeviceInfo& dev, bool mma, const AttendArgs& a, cudaStream_t s) {
   int64_t ctas = 0;
-  const cudaError_t e = mma                        ? launch_attend_mma(dev, std::is_same<T, __half>::value, a, &ctas, s)
+  const cudaError_t e = mma                        ? launch_attend_mma(dev, std::is_same<T, __half>::value ? 1 : 0, a, &ctas, s)
                         : a.c.format == DIT_E4M3 ? launch<T, uint8_t>(dev, a, &ctas, s)
                                                  : launch<T, T>(dev, a, &ctas, s);
   if (e != cudaSuccess) return e;
@@ -213,7 +218,7 @@ cudaError_t launch(const DeviceInfo& dev, bool mma, const AttendArgs& a, cudaStr
 
 cudaError_t launch_attend(const DeviceInfo& dev, int dtype, bool granules, const AttendArgs& a,
                           cudaStream_t s) {
-  const bool mma = dtype != 2 && granules && a.c.D <= 256;
+  const bool mma = attend_mma_takes(dtype, granules, a);
   return dtype == 0   ? launch<__nv_bfloat16>(dev, mma, a, s)
          : dtype == 1 ? launch<__half>(dev, mma, a, s)
                       : launch<float>(dev, false, a, s);

@@ -5,29 +5,28 @@
 // in one pass over the tokens, with s in powers of two (scale times log2 e).
 //
 // What bounds it is memory: each key and value is read once for all query heads
-// of its key head, 16 bit for 4 * group operations.  A warp takes tiles of 16 tokens.  Both
-// products are mma.sync of 16 x 8 x 16: S (heads x tokens) = Q K^T, then O
-// (heads x columns) += P V, P in the registers that S came in.  The tensor cores' 5th
-// generation instructions want 64 or 128 rows, of which a group of heads fills
-// 1 to 16; these here take 2 of 22 cycles that an SM needs to load a token's head at
-// the memory's rate (D = 128, bf16).
+// of its key head.  A warp takes tiles of 16 tokens, each a product of 16 x 8 x 16
+// steps (mma.sync): S (tokens x heads) = K Q^T, then O (columns x heads) += V^T P,
+// so that up to eight heads of a key head fill a product, and sixteen two.  The
+// 5th generation's instructions want 64 or 128 rows and their operands in shared
+// memory in a layout of their own; here the tensor cores' share of the
+// time is small whichever is used.
 //
 // The contraction index of a product may be permuted if both operands agree, and so may
-// the columns of O.  So every lane's operands are 16 contiguous bytes of a row: of keys,
+// the rows of O.  So every lane's operands are 16 contiguous bytes of a row: of keys,
 // lane (g, c) = (lane / 4, lane % 4) has bytes 16 c of each 64 of tokens g and g + 8; of
 // values, bytes 16 g of each 128 of the tokens 2c, 2c + 1, 2c + 8, 2c + 9.  Each lane
 // copies the bytes that it will read itself to its own places in shared memory
-// (cp.async), S stages ahead: no bank conflicts, no barriers between warps,
-// and no shuffles.
+// (cp.async), some stages ahead: no bank conflicts, no barriers, no transposition
+// but of P (two movmatrix).
+//
+// Every warp has a part of the line of tiles (dit_attend.cuh) and finishes its
+// segments alone; what it shares with others it leaves in the workspace, where the CTA's warps
+// join what the CTA holds all of, and the second kernel the rest.
 #include "dit_attend.cuh"
 
 namespace dit {
 namespace {
-
-template <int N>
-struct Words {
-  uint32_t w[N];
-};
 
 __device__ __forceinline__ void cp_async8_part(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -41,483 +40,542 @@ __device__ __forceinline__ float exp2_fast(float x) {  // within 2^-22
   return y;
 }
 
-// d += a b: a 16 x 16 (rows of heads), b 16 x 8, of M.  HALF: rows 8 to 15 are zero, and their sums are not kept.
-template <class M, bool HALF>
-__device__ __forceinline__ void mma(float (&d)[HALF ? 2 : 4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                    uint32_t b0, uint32_t b1) {
-  float e2 = 0.0f, e3 = 0.0f;
-  float& d2 = *(HALF ? &e2 : &d[HALF ? 0 : 2]);
-  float& d3 = *(HALF ? &e3 : &d[HALF ? 1 : 3]);
+// d += a b: a 16 x 16, b 16 x 8, of M.
+template <class M>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
   if constexpr (std::is_same<M, __nv_bfloat16>::value)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d2), "+f"(d3)
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d2), "+f"(d3)
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
+// an 8 x 8 matrix of 16-bit numbers, a row's pairs over four lanes, transposed
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t codes) {  // the low two codes
   uint32_t h;
   asm("{ .reg .b16 c, d; mov.b32 {c, d}, %1; cvt.rn.f16x2.e4m3x2 %0, c; }" : "=r"(h) : "r"(codes));
   return h;
 }
+__device__ __forceinline__ Raw<8> lds8(uint32_t at) {
+  Raw<8> r;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(at));
+  return r;
+}
+// the sum or maximum over the lanes of one c
+__device__ __forceinline__ float column_sum(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+__device__ __forceinline__ float column_max(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
 
-// T: the queries' type; FP8: an E4M3 cache; DP: columns, D rounded up (the rest is zero); HALF: at most 8 heads a
-// key head.
-template <class T, bool FP8_, int DP_, bool HALF_>
+// T: the queries' type; FP8: an E4M3 cache; DP: columns, D rounded up (the rest is zero); NB: blocks of
+// eight heads.
+template <class T, bool FP8_, int DP_, int NB_>
 struct Shape {
-  static constexpr bool FP8 = FP8_, HALF = HALF_;
-  static constexpr int DP = DP_;
+  static constexpr bool FP8 = FP8_;
+  static constexpr int DP = DP_, NB = NB_;
   using M = typename std::conditional<FP8, __half, T>::type;  // of the products
   static constexpr int ES = FP8 ? 1 : 2;
   static constexpr int ROW = DP * ES;                 // bytes
-  static constexpr int WARPS = ROW <= 256 ? 8 : 4;
-  static constexpr int THREADS = 32 * WARPS;
   static constexpr int KP = ROW / 64;                 // 16-byte pieces of a key that a lane has
   static constexpr int VB = ROW / 8 < 16 ? ROW / 8 : 16;  // bytes of a piece of a value
   static constexpr int VP = ROW / 8 / VB;             // pieces of a value that a lane has
   static constexpr int CE = VB / ES;                  // columns of such a piece
+  static constexpr int PER = 16 / ES;                 // columns of a key's piece
   static constexpr int STEPS = DP / 16;               // products of 16 columns
-  static constexpr int QW = HALF ? 2 : 4;             // words of a lane's queries for each
-  static constexpr int NC = HALF ? 2 : 4;             // sums of a lane for each 8 columns
   static constexpr int STAGE = 32 * ROW;              // bytes of a warp's stage: 16 keys and values
   // behind them: the scales of 16 keys and values (E4M3), and which tokens count
   static constexpr int EXTRA = FP8 ? 144 : 16;
-  static constexpr int ROWS = HALF ? 8 : 16;
-  static constexpr int PAD = DP + 4;                  // floats of a row of sums in shared memory
-  static constexpr int SLOTS = WARPS / 2;
-  static constexpr int JOIN = SLOTS * ROWS * PAD * 4 + 2 * WARPS * ROWS * 4;
-  static constexpr int ROOM = 227 * 1024 - 1024 - JOIN;
-  static constexpr int FIT = ROOM / (WARPS * (STAGE + EXTRA));
-  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
-  static constexpr int SMEM = STAGES * WARPS * (STAGE + EXTRA) + JOIN;
+  static constexpr int WARPS = ROW <= 128 ? 16 : ROW <= 256 ? 8 : 4;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int FIT = (226 * 1024) / (WARPS * (STAGE + EXTRA));
+  static constexpr int STAGES = FIT > 6 ? 6 : FIT;
+  static constexpr int SMEM = STAGES * WARPS * (STAGE + EXTRA);
   static_assert(STAGES >= 2, "a stage in flight and one in use");
+  static_assert(WARPS <= kAttendWarps, "the workspace has room for their parts");
 };
 
-// A warp's walk over its tiles.
-struct Cursor {
-  Part part;
-  Segment g;
-  int tile;
-  bool live;
+constexpr int kExtra = 2;  // units of a segment beside its tiles
+constexpr int kLeast = 2;  // the smallest part of a warp
+
+// q = t / d for 0 <= t < 2^31: t m / 2^(31 + s) with 2^(s - 1) < d <= 2^s, m = ceil(2^(31 + s) / d): m d exceeds
+// 2^(31 + s) by less than 2^s, which moves the quotient by less than 1 / d.
+struct Divisor {
+  uint32_t d, m, s;
+};
+__device__ __forceinline__ uint32_t quotient(uint32_t t, const Divisor& v) {
+  return (uint32_t)(((uint64_t)t * v.m) >> (31 + v.s));
+}
+
+struct MmaArgs {
+  AttendArgs a;
+  Divisor page;         // page_size
+  int page_rows;        // rows of D from page to page
+  float* warp_partial;  // [ctas][warps][2][rows][D + 2]: the parts of segments that warps share
+};
+
+// a part of a segment in the workspace: maxima, sums, and the unscaled output
+struct Piece {
+  float *m, *l, *o;
+  __device__ __forceinline__ Piece(float* base, int64_t i, int rows, int D)
+      : m(base + i * rows * (D + 2)), l(m + rows), o(l + rows) {}
 };
 
 template <class T, class S>
-__global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_constant__ MmaArgs args) {
   using M = typename S::M;
-  constexpr bool FP8 = S::FP8, HALF = S::HALF;
-  constexpr int NC = S::NC;
+  constexpr bool FP8 = S::FP8;
+  constexpr int NB = S::NB, NCE = S::CE / 2;
   __shared__ int64_t numbers[S::WARPS + 2];
+  __shared__ int64_t owner[S::WARPS][2];  // the warps' shared segments, or -1
+  __shared__ bool open[S::WARPS];         // whether the first goes on in the next warp's part
   extern __shared__ __align__(128) unsigned char space[];
+  const AttendArgs& a = args.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gl = lane >> 2, cl = lane & 3;
   const int D = (int)a.c.D;
-  const int blocks = (a.group + S::ROWS - 1) / S::ROWS;
-  const int segments = (int)a.c.heads * blocks;
+  const int blocks = (a.group + 8 * NB - 1) / (8 * NB);
+  const Line line{(int)a.c.heads * blocks, kExtra};
   const int slot_rows = min(a.group, kAttendRows);
-
-  float* joined = (float*)space;                              // [SLOTS][ROWS][PAD]
-  float* warp_m = joined + S::SLOTS * S::ROWS * S::PAD;       // [WARPS][ROWS]
-  float* warp_l = warp_m + S::WARPS * S::ROWS;                // [WARPS][ROWS]
-  unsigned char* stages = space + S::JOIN + warp * S::STAGES * (S::STAGE + S::EXTRA);
+  unsigned char* stages = space + warp * S::STAGES * (S::STAGE + S::EXTRA);
   const uint32_t stages_at = smem_addr(stages);
 
-  Part part = part_of<S::THREADS>(a, segments, S::WARPS, numbers);
+  const int64_t total = line.total<S::THREADS>(a, numbers);
+  const int64_t warps = (int64_t)gridDim.x * S::WARPS;
+  const int64_t per = max((int64_t)kLeast, (total + warps - 1) / warps);
+  const int64_t begin = min((blockIdx.x * (int64_t)S::WARPS + warp) * per, total), end = min(begin + per, total);
+  const int64_t cta_begin = min(blockIdx.x * (int64_t)S::WARPS * per, total);
   if (tid < 2) a.owner[2 * blockIdx.x + tid] = -1;
   let_next();
-  if (part.begin >= part.end) return;
+  if (cta_begin >= total) return;
+  const Mark mark = line.find<S::THREADS>(a, cta_begin, numbers);
+  const int64_t slot = (blockIdx.x * (int64_t)S::WARPS + warp) * 2;
+  if (lane < 2) owner[warp][lane] = -1;
 
-  // ----- copies -----
-  // (of a token that does not count nothing is read, from any address, and zeros are written)
-  const char* zeros = (const char*)a.q.p;
-  Cursor ahead;
-  ahead.part = part;
-  ahead.live = next_segment(a, ahead.part, segments, ahead.g);
-  ahead.tile = ahead.g.first + warp;
-  int page = -1;  // of token lane % 16 of the tile ahead
-  auto find = [&]() {
-    while (ahead.live && ahead.tile >= ahead.g.last) {
-      ahead.live = next_segment(a, ahead.part, segments, ahead.g);
-      if (ahead.live) ahead.tile = ahead.g.first + warp;
-    }
-    page = -1;
-    if (ahead.live) {
-      const int t = ahead.tile * kTile + (lane & 15);
-      if (t >= ahead.g.lo && t < ahead.g.hi)
-        page = __ldg(a.pages + (int64_t)ahead.g.b * a.pages_stride + t / (int)a.c.page_size);
-    }
-  };
-  auto issue = [&](int stage) {
-    if (ahead.live) {
-      const uint32_t to = stages_at + stage * (S::STAGE + S::EXTRA);
-      const int head = ahead.g.s / blocks;
-      const int t = ahead.tile * kTile + (lane & 15);
-      const bool there = page >= 0 && page < a.c.pages;
-      const int64_t row = (int64_t)head * a.c.page_size + t % (int)a.c.page_size;
-      const int64_t at = there ? (page * a.c.page_stride + row * D) * S::ES : -1;
-      const uint32_t count = __ballot_sync(0xFFFFFFFFu, there);
-      const int bytes = D * S::ES;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int64_t from = __shfl_sync(0xFFFFFFFFu, at, gl + 8 * b);
-#pragma unroll
-        for (int p = 0; p < S::KP; ++p) {
-          const int c = (p * 4 + cl) * 16;
-          const bool any = from >= 0 && c < bytes;
-          cp_async16_part(to + ((b * S::KP + p) * 32 + lane) * 16, any ? (const char*)a.c.k + from + c : zeros,
-                          any ? 16 : 0);
+  if (begin < end) {
+    const Mark mine = line.find_from(a, begin, mark);
+
+    // ----- copies, some tiles ahead -----
+    Walk ahead(a, line, begin, end, mine);
+    Segment ag = {};
+    bool more = ahead.next(a, line, ag);
+    int tile = ag.first, head = more ? ag.s / blocks : 0;
+    int page = -1, place = 0;  // of token lane % 16 of that tile
+    auto look = [&]() {
+      if (more && tile >= ag.last) {
+        more = ahead.next(a, line, ag);
+        tile = ag.first;
+        head = ag.s / blocks;
+      }
+      page = -1;
+      if (more) {
+        const int t = tile * kTile + (lane & 15);
+        if (t >= ag.lo && t < ag.hi) {
+          const int n = (int)quotient(t, args.page);
+          place = t - n * (int)args.page.d;
+          page = __ldg(a.pages + ag.b * a.pages_stride + n);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t from = __shfl_sync(0xFFFFFFFFu, at, 2 * cl + (i & 1) + 8 * (i >> 1));
-#pragma unroll
-        for (int p = 0; p < S::VP; ++p) {
-          const int c = (p * 8 + gl) * S::VB;
-          const bool any = from >= 0 && c < bytes;
-          const uint32_t dst = to + S::STAGE / 2 + ((i * S::VP + p) * 32 + lane) * S::VB;
-          const char* src = any ? (const char*)a.c.v + from + c : zeros;
-          if constexpr (S::VB == 16)
-            cp_async16_part(dst, src, any ? 16 : 0);
-          else
-            cp_async8_part(dst, src, any ? 8 : 0);
-        }
-      }
-      if constexpr (FP8) {
-        const float* scales = lane < 16 ? a.c.k_scales : a.c.v_scales;
-        cp_async4_part(to + S::STAGE + lane * 4,
-                       there ? (const void*)(scales + page * a.c.scale_stride + row) : zeros, there ? 4 : 0);
-      }
-      if (lane == 0) *(uint32_t*)(stages + stage * (S::STAGE + S::EXTRA) + S::STAGE + S::EXTRA - 16) = count & 0xFFFFu;
-      ahead.tile += S::WARPS;
-      find();
-    }
-    cp_async_commit();
-  };
-  find();
-#pragma unroll
-  for (int s = 0; s < S::STAGES - 1; ++s) issue(s);
-
-  // ----- products -----
-  int stage = 0;
-  Segment g;
-  while (next_segment(a, part, segments, g)) {
-    const int head = g.s / blocks, row0 = (g.s - head * blocks) * S::ROWS;
-    const int rows = min(S::ROWS, a.group - row0);
-    const int h0 = head * a.group + row0;
-
-    // queries, in the order of the keys' bytes, and what a product of theirs is multiplied by
-    uint32_t q[S::STEPS][S::QW];
-    float factor[HALF ? 1 : 2];
-#pragma unroll
-    for (int r = 0; r < (HALF ? 1 : 2); ++r) {
-      const bool real = gl + 8 * r < rows;
-      const T* from = (const T*)a.q.p + g.b * a.q.token + (int64_t)(h0 + gl + 8 * r) * a.q.head;
-      constexpr int PER = 16 / S::ES;  // columns of a key's piece
-      factor[r] = __fmul_rn(a.scale, 1.4426950408889634f);
-      Raw<16> raw[S::KP * PER / 8];
-#pragma unroll
-      for (int i = 0; i < S::KP * PER / 8; ++i) {
-        const int p = i / (PER / 8), c = (p * 4 + cl) * PER + (i % (PER / 8)) * 8;
-        raw[i] = Raw<16>{};
-        if (real && c < D) raw[i] = ld_bcast<16>(from + c);
-      }
-      if constexpr (FP8 && std::is_same<T, __nv_bfloat16>::value) {
-        // to fp16 by a power of two that brings the largest below 2^14
-        float most = 0.0f;
-#pragma unroll
-        for (int i = 0; i < S::KP * PER / 8; ++i) {
-          float f[8];
-          Vec<T, 16>::widen(raw[i], f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) most = max_nan(most, fabsf(f[k]));
-        }
-        most = max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-        most = max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-        int e = (int)(__float_as_uint(most) >> 23) - 127;  // its exponent
-        e = most == 0.0f || !isfinite(most) ? 0 : max(e, -100);
-        const float up = __uint_as_float((uint32_t)(min(13 - e, 127) + 127) << 23);
-        factor[r] = __fmul_rn(factor[r], __uint_as_float((uint32_t)(max(e - 13, -126) + 127) << 23));
-#pragma unroll
-        for (int i = 0; i < S::KP * PER / 8; ++i) {
-          float f[8];
-          Vec<T, 16>::widen(raw[i], f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(f[k], up);
-          raw[i] = Vec<__half, 16>::narrow(f);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < S::KP * PER / 8; ++i) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          q[2 * i + k][HALF ? 0 : r] = raw[i].w[2 * k];
-          q[2 * i + k][HALF ? 1 : 2 + r] = raw[i].w[2 * k + 1];
-        }
-      }
-    }
-
-    float o[S::VP][S::CE][NC] = {};
-    float m[HALF ? 1 : 2], l[HALF ? 1 : 2];
-#pragma unroll
-    for (int r = 0; r < (HALF ? 1 : 2); ++r) m[r] = -INFINITY, l[r] = 0.0f;
-    float vref = 0x1p-126f;  // E4M3: o is in units of this power of two
-
-    for (int tile = g.first + warp; tile < g.last; tile += S::WARPS) {
-      cp_async_wait<S::STAGES - 2>();
-      __syncwarp();
-      issue(stage == 0 ? S::STAGES - 1 : stage - 1);
-      const uint32_t from = stages_at + stage * (S::STAGE + S::EXTRA);
-      const unsigned char* extra = stages + stage * (S::STAGE + S::EXTRA) + S::STAGE;
-      const uint32_t count = *(const uint32_t*)(extra + S::EXTRA - 16);
-
-      float s[2][NC] = {};
-#pragma unroll
-      for (int p = 0; p < S::KP; ++p) {
+    };
+    auto issue = [&](int stage) {
+      if (more) {
+        const uint32_t to = stages_at + stage * (S::STAGE + S::EXTRA);
+        const bool there = page >= 0 && page < a.c.pages;
+        const int in_page = head * (int)args.page.d + place;
+        // (of a token that does not count nothing is read, and zeros are written)
+        const int row = there ? page * args.page_rows + in_page : -1;
+        const uint32_t count = __ballot_sync(0xFFFFFFFFu, there);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const Raw<16> k = lds16(from + ((b * S::KP + p) * 32 + lane) * 16);
+          const int r = __shfl_sync(0xFFFFFFFFu, row, gl + 8 * b);
+          const char* src = (const char*)a.c.k + (int64_t)max(r, 0) * (D * S::ES) + cl * 16;
+          const int bytes = r < 0 ? 0 : D * S::ES - cl * 16;
+#pragma unroll
+          for (int p = 0; p < S::KP; ++p) {
+            const bool any = bytes > p * 64;
+            cp_async16_part(to + ((b * S::KP + p) * 32 + lane) * 16, any ? src + p * 64 : src, any ? 16 : 0);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = __shfl_sync(0xFFFFFFFFu, row, 2 * cl + (i & 1) + 8 * (i >> 1));
+          const char* src = (const char*)a.c.v + (int64_t)max(r, 0) * (D * S::ES) + gl * S::VB;
+          const int bytes = r < 0 ? 0 : D * S::ES - gl * S::VB;
+#pragma unroll
+          for (int p = 0; p < S::VP; ++p) {
+            const bool any = bytes > p * 8 * S::VB;
+            const uint32_t dst = to + S::STAGE / 2 + ((i * S::VP + p) * 32 + lane) * S::VB;
+            const char* from = any ? src + p * 8 * S::VB : (const char*)a.c.v;
+            if constexpr (S::VB == 16)
+              cp_async16_part(dst, from, any ? 16 : 0);
+            else
+              cp_async8_part(dst, from, any ? 8 : 0);
+          }
+        }
+        if constexpr (FP8) {
+          const float* scales = lane < 16 ? a.c.k_scales : a.c.v_scales;
+          cp_async4_part(to + S::STAGE + lane * 4, scales + (there ? page * a.c.scale_stride + in_page : 0),
+                         there ? 4 : 0);
+        }
+        if (lane == 0)
+          *(uint32_t*)(stages + stage * (S::STAGE + S::EXTRA) + S::STAGE + S::EXTRA - 16) = count & 0xFFFFu;
+        ++tile;
+        look();
+      }
+      cp_async_commit();
+    };
+    look();
+#pragma unroll
+    for (int s = 0; s < S::STAGES - 1; ++s) issue(s);
+
+    // ----- products -----
+    int stage = 0;
+    Walk walk(a, line, begin, end, mine);
+    Segment g;
+    while (walk.next(a, line, g)) {
+      const int key_head = g.s / blocks, row0 = (g.s - key_head * blocks) * 8 * NB;
+      const int rows = min(8 * NB, a.group - row0);
+      const int h0 = key_head * a.group + row0;
+
+      // queries of head 8 nb + g, in the order of the keys' bytes, and what the products of heads 8 nb + 2c and
+      // the next are multiplied by
+      uint32_t q[NB][S::STEPS][2];
+      float factor[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        constexpr int N = S::KP * S::PER / 8;
+        const bool real = gl + 8 * nb < rows;
+        const T* from = (const T*)a.q.p + g.b * a.q.token + (int64_t)(h0 + gl + 8 * nb) * a.q.head;
+        float by = __fmul_rn(a.scale, 1.4426950408889634f);
+        Raw<16> raw[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int c = (i / (S::PER / 8) * 4 + cl) * S::PER + (i % (S::PER / 8)) * 8;
+          raw[i] = Raw<16>{};
+          if (real && c < D) raw[i] = ld_bcast<16>(from + c);
+        }
+        if constexpr (FP8 && std::is_same<T, __nv_bfloat16>::value) {
+          // to fp16, by a power of two that brings the head's largest below 2^14
+          float most = 0.0f;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            float f[8];
+            Vec<T, 16>::widen(raw[i], f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) most = max_nan(most, fabsf(f[k]));
+          }
+          most = max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+          most = max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+          int e = (int)(__float_as_uint(most) >> 23) - 127;
+          e = most == 0.0f || !isfinite(most) ? 13 : max(e, -100);
+          const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+          by = __fmul_rn(by, __uint_as_float((uint32_t)(e - 13 + 127) << 23));
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            float f[8];
+            Vec<T, 16>::widen(raw[i], f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(f[k], up);
+            raw[i] = Vec<__half, 16>::narrow(f);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) factor[nb][j] = __shfl_sync(0xFFFFFFFFu, by, 4 * (2 * cl + j));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            q[nb][2 * i + k][0] = raw[i].w[2 * k];
+            q[nb][2 * i + k][1] = raw[i].w[2 * k + 1];
+          }
+        }
+      }
+
+      // o[nb][p][i]: columns (8 p + g) CE + 2 i (twice) and the next, heads 8 nb + 2c and the next
+      float o[NB][S::VP][NCE][4] = {};
+      float m[NB][2], l[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) m[nb][j] = -INFINITY, l[nb][j] = 0.0f;
+      float vref = 0x1p-126f;  // E4M3: o is in units of this power of two
+
+      for (int n = g.last - g.first; n > 0; --n) {
+        cp_async_wait<S::STAGES - 2>();
+        __syncwarp();
+        issue(stage == 0 ? S::STAGES - 1 : stage - 1);
+        const uint32_t from = stages_at + stage * (S::STAGE + S::EXTRA);
+        const unsigned char* extra = stages + stage * (S::STAGE + S::EXTRA) + S::STAGE;
+        const uint32_t count = *(const uint32_t*)(extra + S::EXTRA - 16) >> gl;  // bits 0 and 8: tokens g and g + 8
+        const float* scales = (const float*)extra;
+
+        float s[NB][4] = {};
+#pragma unroll
+        for (int p = 0; p < S::KP; ++p) {
+          const Raw<16> x = lds16(from + (p * 32 + lane) * 16), y = lds16(from + ((S::KP + p) * 32 + lane) * 16);
           constexpr int N = FP8 ? 4 : 2;  // products of a piece
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const uint32_t b0 = FP8 ? e4m3x2_to_half2(k.w[i]) : k.w[2 * i];
-            const uint32_t b1 = FP8 ? e4m3x2_to_half2(k.w[i] >> 16) : k.w[2 * i + 1];
-            const uint32_t(&w)[S::QW] = q[p * N + i];
-            mma<M, HALF>(s[b], w[0], HALF ? 0 : w[1], w[HALF ? 1 : 2], HALF ? 0 : w[HALF ? 1 : 3], b0, b1);
+            const uint32_t a0 = FP8 ? e4m3x2_to_half2(x.w[i]) : x.w[2 * i];
+            const uint32_t a1 = FP8 ? e4m3x2_to_half2(y.w[i]) : y.w[2 * i];
+            const uint32_t a2 = FP8 ? e4m3x2_to_half2(x.w[i] >> 16) : x.w[2 * i + 1];
+            const uint32_t a3 = FP8 ? e4m3x2_to_half2(y.w[i] >> 16) : y.w[2 * i + 1];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma<M>(s[nb], a0, a1, a2, a3, q[nb][p * N + i][0], q[nb][p * N + i][1]);
           }
         }
-      }
-      float ks[2][2], vs[2][2];
-      if constexpr (FP8) {
-        const float* scales = (const float*)extra;
+        const float k0 = FP8 ? scales[gl] : 1.0f, k1 = FP8 ? scales[gl + 8] : 1.0f;
+        float f[NB][2];
+        bool moved = false;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            ks[b][i] = scales[8 * b + 2 * cl + i];
-            vs[b][i] = scales[16 + 8 * b + 2 * cl + i];
-          }
-      }
-      float f[HALF ? 1 : 2];
-      bool moved = false;
-#pragma unroll
-      for (int r = 0; r < (HALF ? 1 : 2); ++r) {
-        float most = m[r];
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float& x = s[b][2 * r + i];
-            x = __fmul_rn(x, FP8 ? __fmul_rn(factor[r], ks[b][i]) : factor[r]);
-            if (!(count >> (8 * b + 2 * cl + i) & 1)) x = -INFINITY;
-            most = fmaxf(most, x);
-          }
-        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-        const float base = most == -INFINITY ? 0.0f : most;
-        f[r] = exp2_fast(__fadd_rn(m[r], -base));
-        moved = moved || most != m[r];
-        m[r] = most;
-        float sum = 0.0f;
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float& x = s[b][2 * r + i];
-            x = exp2_fast(__fadd_rn(x, -base));
-            sum = __fadd_rn(sum, x);
-          }
-        l[r] = __fmaf_rn(l[r], f[r], sum);
-      }
-      float of[HALF ? 1 : 2];
-#pragma unroll
-      for (int r = 0; r < (HALF ? 1 : 2); ++r) of[r] = f[r];
-      if constexpr (FP8) {
-        // weights times the values' scales, in units of a power of two above all of them so far, fit fp16
-        const uint32_t mine = __float_as_uint(((const float*)extra)[16 + (lane & 15)]);
-        const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, mine);
-        if (most >= __float_as_uint(vref)) {
-          const uint32_t e = min((most >> 23) + 1, 254u);
-          const float now = most > 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(e << 23);
-          const float down = __fdiv_rn(vref, now);
-          vref = now;
-          moved = true;
-#pragma unroll
-          for (int r = 0; r < (HALF ? 1 : 2); ++r) of[r] = __fmul_rn(of[r], down);
-        }
-        const float unit = __fdiv_rn(1.0f, vref);
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float w = __fmul_rn(vs[b][i], unit);
-#pragma unroll
-            for (int r = 0; r < (HALF ? 1 : 2); ++r) s[b][2 * r + i] = __fmul_rn(s[b][2 * r + i], w);
-          }
-      }
-      if (__any_sync(0xFFFFFFFFu, moved)) {
-#pragma unroll
-        for (int p = 0; p < S::VP; ++p)
-#pragma unroll
-          for (int i = 0; i < S::CE; ++i)
-#pragma unroll
-            for (int k = 0; k < NC; ++k) o[p][i][k] = __fmul_rn(o[p][i][k], of[k >> 1]);
-      }
-      uint32_t w[2][HALF ? 1 : 2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int r = 0; r < (HALF ? 1 : 2); ++r) w[b][r] = Pair<M>::narrow(f2(s[b][2 * r], s[b][2 * r + 1]));
-      const uint32_t values = from + S::STAGE / 2;
-#pragma unroll
-      for (int p = 0; p < S::VP; ++p) {
-        constexpr int N = S::VB / 4;
-        Words<N> v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t at = values + ((i * S::VP + p) * 32 + lane) * S::VB;
-          if constexpr (N == 4) {
-            const Raw<16> x = lds16(at);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[i].w[k] = x.w[k];
-          } else {
-            asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v[i].w[0]), "=r"(v[i].w[1]) : "r"(at));
+          for (int j = 0; j < 2; ++j) {
+            float x = s[nb][j], y = s[nb][2 + j];
+            if constexpr (FP8) x = __fmul_rn(x, k0), y = __fmul_rn(y, k1);
+            x = count & 1 ? __fmul_rn(x, factor[nb][j]) : -INFINITY;
+            y = count & 256 ? __fmul_rn(y, factor[nb][j]) : -INFINITY;
+            const float most = column_max(fmaxf(m[nb][j], fmaxf(x, y)));
+            const float base = most == -INFINITY ? 0.0f : most;
+            f[nb][j] = exp2_fast(__fadd_rn(m[nb][j], -base));
+            moved = moved || most != m[nb][j];
+            m[nb][j] = most;
+            s[nb][j] = exp2_fast(__fadd_rn(x, -base));
+            s[nb][2 + j] = exp2_fast(__fadd_rn(y, -base));
+            l[nb][j] = __fmaf_rn(l[nb][j], f[nb][j], __fadd_rn(s[nb][j], s[nb][2 + j]));
           }
         }
+        if constexpr (FP8) {
+          // weights times the values' scales, in units of a power of two above all of them so far, fit fp16
+          const float v0 = scales[16 + gl], v1 = scales[24 + gl];
+          const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(__float_as_uint(v0), __float_as_uint(v1)));
+          if (most >= __float_as_uint(vref)) {
+            const uint32_t e = min((most >> 23) + 1, 253u);
+            const float now = most > 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(e << 23);
+            const float down = __fdiv_rn(vref, now);
+            vref = now;
+            moved = true;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          if constexpr (FP8) {
-            // the codes of two tokens side by side, column by column
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t sel = h ? 0x7362 : 0x5140;
-              const uint32_t x = __byte_perm(v[0].w[k], v[1].w[k], sel), y = __byte_perm(v[2].w[k], v[3].w[k], sel);
+              for (int j = 0; j < 2; ++j) f[nb][j] = __fmul_rn(f[nb][j], down);
+          }
+          // (1 / vref: its exponent reflected; NaN stays NaN)
+          const float unit = vref != vref ? vref : __uint_as_float(0x7F000000u - __float_as_uint(vref));
+          const float w0 = __fmul_rn(v0, unit), w1 = __fmul_rn(v1, unit);
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-                mma<M, HALF>(o[p][4 * k + 2 * h + j], w[0][0], HALF ? 0 : w[0][HALF ? 0 : 1], w[1][0],
-                             HALF ? 0 : w[1][HALF ? 0 : 1], e4m3x2_to_half2(j ? x >> 16 : x),
-                             e4m3x2_to_half2(j ? y >> 16 : y));
-            }
-          } else {
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t sel = j ? 0x7632 : 0x5410;
-              mma<M, HALF>(o[p][2 * k + j], w[0][0], HALF ? 0 : w[0][HALF ? 0 : 1], w[1][0],
-                           HALF ? 0 : w[1][HALF ? 0 : 1], __byte_perm(v[0].w[k], v[1].w[k], sel),
-                           __byte_perm(v[2].w[k], v[3].w[k], sel));
+              s[nb][j] = __fmul_rn(s[nb][j], w0);
+              s[nb][2 + j] = __fmul_rn(s[nb][2 + j], w1);
+            }
+        }
+        if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int p = 0; p < S::VP; ++p)
+#pragma unroll
+              for (int i = 0; i < NCE; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[nb][p][i][k] = __fmul_rn(o[nb][p][i][k], f[nb][k & 1]);
+        }
+        uint32_t w[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) w[nb][k] = transposed(Pair<M>::narrow(f2(s[nb][2 * k], s[nb][2 * k + 1])));
+        const uint32_t values = from + S::STAGE / 2;
+#pragma unroll
+        for (int p = 0; p < S::VP; ++p) {
+          Raw<S::VB> v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t at = values + ((i * S::VP + p) * 32 + lane) * S::VB;
+            if constexpr (S::VB == 16)
+              v[i] = lds16(at);
+            else
+              v[i] = lds8(at);
+          }
+#pragma unroll
+          for (int k = 0; k < S::VB / 4; ++k) {
+            if constexpr (FP8) {
+              // the codes of two tokens side by side, column by column
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t sel = h ? 0x7362 : 0x5140;
+                const uint32_t x = __byte_perm(v[0].w[k], v[1].w[k], sel), y = __byte_perm(v[2].w[k], v[3].w[k], sel);
+                const uint32_t a0 = e4m3x2_to_half2(x), a1 = e4m3x2_to_half2(x >> 16);
+                const uint32_t a2 = e4m3x2_to_half2(y), a3 = e4m3x2_to_half2(y >> 16);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][2 * k + h], a0, a1, a2, a3, w[nb][0], w[nb][1]);
+              }
+            } else {
+              const uint32_t a0 = __byte_perm(v[0].w[k], v[1].w[k], 0x5410);
+              const uint32_t a1 = __byte_perm(v[0].w[k], v[1].w[k], 0x7632);
+              const uint32_t a2 = __byte_perm(v[2].w[k], v[3].w[k], 0x5410);
+              const uint32_t a3 = __byte_perm(v[2].w[k], v[3].w[k], 0x7632);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][k], a0, a1, a2, a3, w[nb][0], w[nb][1]);
             }
           }
         }
+        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
       }
-      stage = stage + 1 == S::STAGES ? 0 : stage + 1;
-    }
 
-    // ----- the warps' parts together -----
-#pragma unroll
-    for (int r = 0; r < (HALF ? 1 : 2); ++r) {
-      l[r] = __fadd_rn(l[r], __shfl_xor_sync(0xFFFFFFFFu, l[r], 1));
-      l[r] = __fadd_rn(l[r], __shfl_xor_sync(0xFFFFFFFFu, l[r], 2));
-      if (cl == 0) {
-        warp_m[warp * S::ROWS + gl + 8 * r] = m[r];
-        warp_l[warp * S::ROWS + gl + 8 * r] = l[r];
+      // ----- the segment's result, or its piece -----
+      const bool piece = g.head || g.tail;
+      const Piece to(args.warp_partial, slot + (g.head ? 0 : 1), slot_rows, D);
+      if (piece && lane == 0) {
+        owner[warp][g.head ? 0 : 1] = (int64_t)g.b * line.segments + g.s;
+        if (g.head) open[warp] = g.open;
       }
-    }
-    __syncthreads();
-    float top[HALF ? 1 : 2];
 #pragma unroll
-    for (int r = 0; r < (HALF ? 1 : 2); ++r) {
-      top[r] = -INFINITY;
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int k = 0; k < S::WARPS; ++k) top[r] = fmaxf(top[r], warp_m[k * S::ROWS + gl + 8 * r]);
-      float by = exp2_fast(__fadd_rn(m[r], -(top[r] == -INFINITY ? 0.0f : top[r])));
-      if constexpr (FP8) by = __fmul_rn(by, vref);
+        for (int j = 0; j < 2; ++j) {
+          const float sum = column_sum(l[nb][j]);
+          const int r = 8 * nb + 2 * cl + j;
+          if (r >= rows) continue;
+          float by = piece ? 1.0f : sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+          if constexpr (FP8) by = __fmul_rn(by, vref);
 #pragma unroll
-      for (int p = 0; p < S::VP; ++p)
+          for (int p = 0; p < S::VP; ++p) {
+            float out[S::CE];
 #pragma unroll
-        for (int i = 0; i < S::CE; ++i)
+            for (int i = 0; i < NCE; ++i) {
+              out[2 * i] = __fmul_rn(o[nb][p][i][j], by);
+              out[2 * i + 1] = __fmul_rn(o[nb][p][i][2 + j], by);
+            }
+            const int c = (8 * p + gl) * S::CE;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) o[p][i][2 * r + k] = __fmul_rn(o[p][i][2 * r + k], by);
-    }
-    // the column of o[p][i][2 r + k]
-    auto column = [&](int p, int i, int k) { return (p * 8 + 2 * cl + k) * S::CE + i; };
-    auto each = [&](int slot, auto&& body) {
-      float* base = joined + slot * S::ROWS * S::PAD;
+            for (int i = 0; i < S::CE; i += 8) {
+              if (c + i >= D) continue;
+              const float(&x)[8] = *(const float(*)[8])(out + i);
+              if (piece) {
+                float2* dst = (float2*)(to.o + r * D + c + i);
 #pragma unroll
-      for (int p = 0; p < S::VP; ++p)
-#pragma unroll
-        for (int k = 0; k < NC; ++k)
-#pragma unroll
-          for (int i = 0; i < S::CE; i += 4)
-            body(*(float4*)(base + (gl + 8 * (k >> 1)) * S::PAD + column(p, i, k & 1)), o[p][i][k], o[p][i + 1][k],
-                 o[p][i + 2][k], o[p][i + 3][k]);
-    };
-    if (warp >= S::SLOTS)
-      each(warp - S::SLOTS, [](float4& x, float& p, float& q, float& r, float& s) { x = make_float4(p, q, r, s); });
-    __syncthreads();
-    if (warp < S::SLOTS)
-      each(warp, [](float4& x, float& p, float& q, float& r, float& s) {
-        x = make_float4(__fadd_rn(p, x.x), __fadd_rn(q, x.y), __fadd_rn(r, x.z), __fadd_rn(s, x.w));
-      });
-    __syncthreads();
-    const bool shared_out = g.head || g.tail;
-    const int place = g.head ? 0 : 1;
-    float* parts = a.partial + ((int64_t)blockIdx.x * 2 + place) * slot_rows * (D + 2);
-    if (shared_out && tid == 0) a.owner[2 * blockIdx.x + place] = g.id;
-    for (int i = tid; i < rows * (S::DP / 8); i += S::THREADS) {
-      const int r = i / (S::DP / 8), c = (i - r * (S::DP / 8)) * 8;
-      if (c >= D) continue;
-      float most = -INFINITY, total = 0.0f;
-#pragma unroll
-      for (int k = 0; k < S::WARPS; ++k) most = fmaxf(most, warp_m[k * S::ROWS + r]);
-#pragma unroll
-      for (int k = 0; k < S::WARPS; ++k)
-        total = __fmaf_rn(warp_l[k * S::ROWS + r],
-                          exp2_fast(__fadd_rn(warp_m[k * S::ROWS + r], -(most == -INFINITY ? 0.0f : most))), total);
-      float sum[8] = {};
-#pragma unroll
-      for (int k = 0; k < S::SLOTS; ++k) {
-        const float* x = joined + (k * S::ROWS + r) * S::PAD + c;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = __fadd_rn(sum[j], x[j]);
-      }
-      if (shared_out) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) parts[2 * slot_rows + r * D + c + j] = sum[j];
-        if (c == 0) {
-          parts[r] = most;
-          parts[slot_rows + r] = total;
+                for (int k = 0; k < 4; ++k) dst[k] = make_float2(x[2 * k], x[2 * k + 1]);
+              } else {
+                st_stream<16>((T*)a.out.p + g.b * a.out.token + (int64_t)(h0 + r) * a.out.head + c + i,
+                              Vec<T, 16>::narrow(x));
+              }
+            }
+          }
+          if (gl != 0) continue;
+          if (piece) {
+            to.m[r] = m[nb][j];
+            to.l[r] = sum;
+          } else if (a.lse) {
+            a.lse[(int64_t)g.b * a.Hq + h0 + r] = lse_of(m[nb][j], sum);
+          }
         }
-      } else {
-        const float by = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+    }
+    cp_async_wait<0>();  // no copy may outlive the CTA's shared memory
+  }
+
+  // ----- pieces of the same segment in this CTA, together: a warp takes a head of one -----
+  __syncthreads();
+  const int64_t first = blockIdx.x * (int64_t)S::WARPS * 2;
+  for (int task = warp; task < (S::WARPS + 1) * slot_rows; task += S::WARPS) {
+    // chain 0 begins before this CTA, chain i + 1 with the second piece of warp i
+    const int chain = task / slot_rows, r = task - chain * slot_rows;
+    const int64_t id = chain == 0 ? owner[0][0] : owner[chain - 1][1];
+    if (id < 0) continue;
+    const int b = (int)(id / line.segments), s = (int)(id - (int64_t)b * line.segments);
+    const int key_head = s / blocks, row0 = (s - key_head * blocks) * 8 * NB;
+    if (r >= min(8 * NB, a.group - row0)) continue;
+    const int h = key_head * a.group + row0 + r;
+    int last = chain;  // the warps [chain, last) go on with it
+    while (last < S::WARPS && owner[last][0] == id) ++last;
+    const bool begun = chain > 0, done = begun && last > chain && !open[last - 1];
+    const int pieces = last - chain + begun;
+    auto at = [&](int k) {
+      return Piece(args.warp_partial, first + (begun ? 2 * (chain - 1 + k) + (k == 0) : 2 * k), slot_rows, D);
+    };
+    float top = -INFINITY, sum = 0.0f;
+    for (int k = 0; k < pieces; ++k) top = fmaxf(top, at(k).m[r]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float2 o[S::DP / 64] = {};
+    for (int k = 0; k < pieces; ++k) {
+      const Piece p = at(k);
+      const float f = exp2_fast(__fadd_rn(p.m[r], -base));
+      sum = __fmaf_rn(p.l[r], f, sum);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = total == 0.0f ? 0.0f : __fmul_rn(sum[j], by);
-        st_stream<16>((T*)a.out.p + g.b * a.out.token + (int64_t)(h0 + r) * a.out.head + c, Vec<T, 16>::narrow(sum));
-        if (a.lse && c == 0) a.lse[(int64_t)g.b * a.Hq + h0 + r] = lse_of(most, total);
+      for (int i = 0; i < S::DP / 64; ++i) {
+        const int c = 64 * i + 2 * lane;
+        if (c >= D) continue;
+        const float2 v = *(const float2*)(p.o + r * D + c);
+        o[i] = make_float2(__fmaf_rn(v.x, f, o[i].x), __fmaf_rn(v.y, f, o[i].y));
       }
     }
-    __syncthreads();
+    if (done) {
+      const float by = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+#pragma unroll
+      for (int i = 0; i < S::DP / 64; ++i) {
+        const int c = 64 * i + 2 * lane;
+        if (c < D)
+          *(uint32_t*)((T*)a.out.p + b * a.out.token + h * a.out.head + c) =
+              Pair<T>::narrow(f2(__fmul_rn(o[i].x, by), __fmul_rn(o[i].y, by)));
+      }
+      if (lane == 0 && a.lse) a.lse[(int64_t)b * a.Hq + h] = lse_of(top, sum);
+    } else {
+      const Piece p(a.partial, 2 * blockIdx.x + begun, slot_rows, D);
+#pragma unroll
+      for (int i = 0; i < S::DP / 64; ++i) {
+        const int c = 64 * i + 2 * lane;
+        if (c < D) *(float2*)(p.o + r * D + c) = o[i];
+      }
+      if (lane == 0) {
+        p.m[r] = top;
+        p.l[r] = sum;
+        a.owner[2 * blockIdx.x + begun] = id;
+      }
+    }
   }
-  cp_async_wait<0>();  // no copy may outlive the CTA's shared memory
 }
 
-template <class T, bool FP8, int DP, bool HALF>
+Divisor divisor(uint32_t d) {
+  Divisor v{d, 0, 0};
+  while ((uint64_t(1) << v.s) < d) ++v.s;
+  v.m = (uint32_t)(((uint64_t(1) << (31 + v.s)) + d - 1) / d);
+  return v;
+}
+
+template <class T, bool FP8, int DP, int NB>
 cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cudaStream_t s) {
-  using S = Shape<T, FP8, DP, HALF>;
+  using S = Shape<T, FP8, DP, NB>;
   const auto kern = attend_mma_kernel<T, S>;
   static std::atomic<int> opted[kOptinDevices];
-  cudaError_t e = allow_shared((const void*)kern, dev, opted);
+  const cudaError_t e = allow_shared((const void*)kern, dev, opted);
   if (e != cudaSuccess) return e;
-  *ctas = std::min(kAttendMaxCtas, (int64_t)dev.sm_count);
-  kern<<<(unsigned)*ctas, S::THREADS, S::SMEM, s>>>(a);
+  *ctas = std::min(kAttendMmaCtas, (int64_t)dev.sm_count);
+  MmaArgs m;
+  m.a = a;
+  m.page = divisor((uint32_t)a.c.page_size);
+  m.page_rows = (int)(a.c.page_stride / a.c.D);
+  m.warp_partial = a.partial + *ctas * 2 * std::min(a.group, kAttendRows) * (a.c.D + 2);
+  kern<<<(unsigned)*ctas, S::THREADS, S::SMEM, s>>>(m);
   return cudaGetLastError();
 }
 
 template <class T, bool FP8, int DP>
 cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cudaStream_t s) {
-  return a.group <= 8 ? launch<T, FP8, DP, true>(dev, a, ctas, s)
-                      : launch<T, FP8, DP, false>(dev, a, ctas, s);
+  return a.group <= 8 ? launch<T, FP8, DP, 1>(dev, a, ctas, s) : launch<T, FP8, DP, 2>(dev, a, ctas, s);
 }
 template <class T, bool FP8>
 cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cudaStream_t s) {
@@ -532,9 +590,14 @@ cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cu
 
 }  // namespace
 
-cudaError_t launch_attend_mma(const DeviceInfo& dev, bool half, const AttendArgs& a, int64_t* ctas,
+bool attend_mma_takes(int dtype, bool granules, const AttendArgs& a) {
+  return dtype != 2 && granules && a.c.D <= 256 && a.capacity > 0 && a.c.page_stride % a.c.D == 0 &&
+         a.c.pages * (a.c.page_stride / a.c.D) <= 0x7FFFFFFF;
+}
+
+cudaError_t launch_attend_mma(const DeviceInfo& dev, int dtype, const AttendArgs& a, int64_t* ctas,
                               cudaStream_t s) {
-  return half ? launch<__half>(dev, a, ctas, s) : launch<__nv_bfloat16>(dev, a, ctas, s);
+  return dtype == 1 ? launch<__half>(dev, a, ctas, s) : launch<__nv_bfloat16>(dev, a, ctas, s);
 }
 
 }  // namespace dit

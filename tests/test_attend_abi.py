@@ -191,8 +191,8 @@ def attend(lib, o=QO, lse=LSE, q=Q, c=None, pages=PG, ps=4, width=4, lengths=IDS
 
 def test_attention(lib):
     wb = lib.dit_paged_attention_workspace_bytes
-    assert wb(4, 2, 64) == 9728 + 608 * 2 * 2 * 66 * 4
-    assert wb(64, 1, 64) == 9728 + 608 * 2 * 16 * 66 * 4
+    assert wb(4, 2, 64) == 9728 + 160 * 17 * 2 * 2 * 66 * 4
+    assert wb(64, 1, 64) == 9728 + 160 * 17 * 2 * 16 * 66 * 4
     assert wb(4, 3, 64) == wb(0, 1, 64) == wb(4, 0, 64) == wb(4, 2, 0) == wb(4, 2, 513) == -1
     assert attend(lib) == NODEV and attend(lib, lse=None) == NODEV and attend(lib, it=1) == NODEV
     assert attend(lib, c=cache(format=E4M3)) == NODEV and attend(lib, c=cache(format=E4M3), dt=FP32) == NODEV
