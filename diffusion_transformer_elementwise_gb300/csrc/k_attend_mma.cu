@@ -15,10 +15,9 @@
 // The contraction index of a product may be permuted if both operands agree, and so may
 // the rows of O.  So every lane's operands are 16 contiguous bytes of a row: of keys,
 // lane (g, c) = (lane / 4, lane % 4) has bytes 16 c of each 64 of tokens g and g + 8; of
-// values, bytes 16 g of each 128 of the tokens 2c, 2c + 1, 2c + 8, 2c + 9.  Each lane
-// copies the bytes that it will read itself to its own places in shared memory
-// (cp.async), some stages ahead: no bank conflicts, no barriers, no transposition
-// but of P (two movmatrix).
+// values, bytes 16 g of each 128 of the tokens 2c, 2c + 1, 2c + 8, 2c + 9 (or others in
+// their place).  They come through the warp's own stages in shared memory (cp.async): no bank
+// conflicts, no barriers but the warp's, no transposition but of P (two movmatrix).
 //
 // Every warp has a part of the line of tiles (dit_attend.cuh) and finishes its
 // segments alone; what it shares with others it leaves in the workspace, where the CTA's warps
@@ -28,9 +27,6 @@
 namespace dit {
 namespace {
 
-__device__ __forceinline__ void cp_async8_part(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void cp_async4_part(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -81,6 +77,27 @@ __device__ __forceinline__ float column_max(float v) {
   return v;
 }
 
+// Where chunk c (16 bytes) of row t is in a tile of keys or values: the rows lie one after the other, and each
+// 128 bytes of them have their chunks exchanged so that the eight lanes of a quarter of a warp
+// find theirs in eight different places, as the copies that write them do.  (Copies that spread a
+// line over the tile instead, to the order of the reading lanes, left the memory at 4.0 of 7.0 TB/s.)
+// Keys are read as chunks 0 to 3 or 4 to 7 of two rows by such eight lanes, values as two
+// chunks of four rows; with rows 0 5 2 7 4 1 6 3 in the place of 0 to 7 (chunk numbers change by the row's),
+// both do.  Rows of 64 bytes: two of them share 128.
+template <int ROW, bool VALUE>
+__device__ __forceinline__ uint32_t chunk_xor(int t) {
+  return (ROW >= 128 ? t & 7 : VALUE ? t / 2 * 2 & 7 : t / 2 & 3) * 16;
+}
+template <int ROW, bool VALUE>
+__device__ __forceinline__ uint32_t chunk_at(int t, int c) {
+  return (t * ROW + c * 16) ^ chunk_xor<ROW, VALUE>(t);
+}
+// chunk 4 p + c of the row whose chunk c is at `key`
+template <int ROW>
+__device__ __forceinline__ uint32_t key_at(uint32_t key, int p) {
+  return (key ^ (p & 1) * 64) + p / 2 * 128;
+}
+
 // T: the queries' type; FP8: an E4M3 cache; DP: columns, D rounded up (the rest is zero); NB: blocks of
 // eight heads.
 template <class T, bool FP8_, int DP_, int NB_>
@@ -98,8 +115,8 @@ struct Shape {
   static constexpr int STEPS = DP / 16;               // products of 16 columns
   static constexpr int STAGE = 32 * ROW;              // bytes of a warp's stage: 16 keys and values
   // behind them: the scales of 16 keys and values (E4M3), and which tokens count
-  static constexpr int EXTRA = FP8 ? 144 : 16;
-  static constexpr int WARPS = ROW <= 128 ? 16 : ROW <= 256 ? 8 : 4;
+  static constexpr int EXTRA = FP8 ? 256 : 128;
+  static constexpr int WARPS = ROW <= 128 && NB == 1 ? 16 : ROW <= 256 ? 8 : 4;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int FIT = (226 * 1024) / (WARPS * (STAGE + EXTRA));
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
@@ -124,6 +141,7 @@ struct MmaArgs {
   AttendArgs a;
   Divisor page;         // page_size
   int page_rows;        // rows of D from page to page
+  bool whole;           // no page ends within a tile
   float* warp_partial;  // [ctas][warps][2][rows][D + 2]: the parts of segments that warps share
 };
 
@@ -142,7 +160,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
   __shared__ int64_t numbers[S::WARPS + 2];
   __shared__ int64_t owner[S::WARPS][2];  // the warps' shared segments, or -1
   __shared__ bool open[S::WARPS];         // whether the first goes on in the next warp's part
-  extern __shared__ __align__(128) unsigned char space[];
+  extern __shared__ __align__(1024) unsigned char space[];
   const AttendArgs& a = args.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gl = lane >> 2, cl = lane & 3;
@@ -152,6 +170,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
   const int slot_rows = min(a.group, kAttendRows);
   unsigned char* stages = space + warp * S::STAGES * (S::STAGE + S::EXTRA);
   const uint32_t stages_at = smem_addr(stages);
+  // Rows of a product of tokens are not tokens g but tg, and g + 8 but tg + 8: see chunk_at.
+  const int tg = gl ^ ((gl & 1) << 2);
 
   const int64_t total = line.total<S::THREADS>(a, numbers);
   const int64_t warps = (int64_t)gridDim.x * S::WARPS;
@@ -190,39 +210,41 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
         }
       }
     };
+    // A copy takes 512 bytes as they lie in memory: lane l has chunk l % LPR of row l / LPR of RPC.
+    constexpr int LPR = S::ROW / 16, RPC = 32 / LPR, COPIES = kTile / RPC;
+    const int row_bytes = D * S::ES;
+    const int my_row = lane / LPR, my_chunk = lane % LPR;
+    const int my_bytes = my_chunk * 16 < row_bytes ? 16 : 0;
+    const int my_at = my_row * row_bytes + (my_bytes ? my_chunk * 16 : 0);
+    const uint32_t k_to = chunk_at<S::ROW, false>(my_row, my_chunk), v_to = chunk_at<S::ROW, true>(my_row, my_chunk);
     auto issue = [&](int stage) {
       if (more) {
         const uint32_t to = stages_at + stage * (S::STAGE + S::EXTRA);
+        asm volatile("" : "+r"(page));  // (not waited for before it is needed)
         const bool there = page >= 0 && page < a.c.pages;
         const int in_page = head * (int)args.page.d + place;
         // (of a token that does not count nothing is read, and zeros are written)
         const int row = there ? page * args.page_rows + in_page : -1;
         const uint32_t count = __ballot_sync(0xFFFFFFFFu, there);
+        auto copy = [&](int n, int64_t at, int bytes) {
+          // chunk_at of row n RPC + my_row: its part in n moves by constants
+          const uint32_t k = (to + k_to) ^ chunk_xor<S::ROW, false>(n * RPC), v = (to + v_to) ^ chunk_xor<S::ROW, true>(n * RPC);
+          cp_async16_part(k + n * 512, (const char*)a.c.k + at, bytes);
+          cp_async16_part(v + S::STAGE / 2 + n * 512, (const char*)a.c.v + at, bytes);
+        };
+        if (count == 0xFFFFFFFFu && args.whole) {  // 16 rows that lie side by side
+          int64_t at = (int64_t)__shfl_sync(0xFFFFFFFFu, row, 0) * row_bytes + my_at;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int r = __shfl_sync(0xFFFFFFFFu, row, gl + 8 * b);
-          const char* src = (const char*)a.c.k + (int64_t)max(r, 0) * (D * S::ES) + cl * 16;
-          const int bytes = r < 0 ? 0 : D * S::ES - cl * 16;
-#pragma unroll
-          for (int p = 0; p < S::KP; ++p) {
-            const bool any = bytes > p * 64;
-            cp_async16_part(to + ((b * S::KP + p) * 32 + lane) * 16, any ? src + p * 64 : src, any ? 16 : 0);
+          for (int n = 0; n < COPIES; ++n) {
+            copy(n, at, my_bytes);
+            at += RPC * row_bytes;
           }
-        }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = __shfl_sync(0xFFFFFFFFu, row, 2 * cl + (i & 1) + 8 * (i >> 1));
-          const char* src = (const char*)a.c.v + (int64_t)max(r, 0) * (D * S::ES) + gl * S::VB;
-          const int bytes = r < 0 ? 0 : D * S::ES - gl * S::VB;
-#pragma unroll
-          for (int p = 0; p < S::VP; ++p) {
-            const bool any = bytes > p * 8 * S::VB;
-            const uint32_t dst = to + S::STAGE / 2 + ((i * S::VP + p) * 32 + lane) * S::VB;
-            const char* from = any ? src + p * 8 * S::VB : (const char*)a.c.v;
-            if constexpr (S::VB == 16)
-              cp_async16_part(dst, from, any ? 16 : 0);
-            else
-              cp_async8_part(dst, from, any ? 8 : 0);
+          for (int n = 0; n < COPIES; ++n) {
+            const int r = __shfl_sync(0xFFFFFFFFu, row, n * RPC + my_row);
+            const int bytes = r < 0 ? 0 : my_bytes;
+            copy(n, bytes ? (int64_t)r * row_bytes + my_chunk * 16 : 0, bytes);
           }
         }
         if constexpr (FP8) {
@@ -242,6 +264,14 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
     for (int s = 0; s < S::STAGES - 1; ++s) issue(s);
 
     // ----- products -----
+    // where the lane's first key is, and its values of tokens 2c and 2c + 1 (as rows of a product)
+    const uint32_t key = chunk_at<S::ROW, false>(tg, cl);
+    uint32_t value[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = (2 * cl + i) ^ (i << 2);
+      value[i] = S::VB == 16 ? chunk_at<S::ROW, true>(t, gl) : chunk_at<S::ROW, true>(t, gl >> 1) + (gl & 1) * 8;
+    }
     int stage = 0;
     Walk walk(a, line, begin, end, mine);
     Segment g;
@@ -316,28 +346,61 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
       for (int n = g.last - g.first; n > 0; --n) {
         cp_async_wait<S::STAGES - 2>();
         __syncwarp();
-        issue(stage == 0 ? S::STAGES - 1 : stage - 1);
         const uint32_t from = stages_at + stage * (S::STAGE + S::EXTRA);
         const unsigned char* extra = stages + stage * (S::STAGE + S::EXTRA) + S::STAGE;
-        const uint32_t count = *(const uint32_t*)(extra + S::EXTRA - 16) >> gl;  // bits 0 and 8: tokens g and g + 8
+        const uint32_t count = *(const uint32_t*)(extra + S::EXTRA - 16) >> tg;  // bits 0 and 8: the lane's tokens
         const float* scales = (const float*)extra;
 
-        float s[NB][4] = {};
+        // pieces of keys, KG at a time, in registers before the products that wait for each other
+        constexpr int KG = S::KP < 4 ? S::KP : 4;
+        float s[NB][4] = {}, s2[NB][4] = {};
 #pragma unroll
-        for (int p = 0; p < S::KP; ++p) {
-          const Raw<16> x = lds16(from + (p * 32 + lane) * 16), y = lds16(from + ((S::KP + p) * 32 + lane) * 16);
-          constexpr int N = FP8 ? 4 : 2;  // products of a piece
+        for (int p0 = 0; p0 < S::KP; p0 += KG) {
+          Raw<16> x[KG], y[KG];
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const uint32_t a0 = FP8 ? e4m3x2_to_half2(x.w[i]) : x.w[2 * i];
-            const uint32_t a1 = FP8 ? e4m3x2_to_half2(y.w[i]) : y.w[2 * i];
-            const uint32_t a2 = FP8 ? e4m3x2_to_half2(x.w[i] >> 16) : x.w[2 * i + 1];
-            const uint32_t a3 = FP8 ? e4m3x2_to_half2(y.w[i] >> 16) : y.w[2 * i + 1];
+          for (int p = 0; p < KG; ++p) {
+            const uint32_t at = from + key_at<S::ROW>(key, p0 + p);
+            x[p] = lds16(at);
+            y[p] = lds16(at + 8 * S::ROW);
+          }
+          if (p0 == 0) issue(stage == 0 ? S::STAGES - 1 : stage - 1);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma<M>(s[nb], a0, a1, a2, a3, q[nb][p * N + i][0], q[nb][p * N + i][1]);
+          for (int p = 0; p < KG; ++p) {
+            constexpr int N = FP8 ? 4 : 2;  // products of a piece
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const uint32_t a0 = FP8 ? e4m3x2_to_half2(x[p].w[i]) : x[p].w[2 * i];
+              const uint32_t a1 = FP8 ? e4m3x2_to_half2(y[p].w[i]) : y[p].w[2 * i];
+              const uint32_t a2 = FP8 ? e4m3x2_to_half2(x[p].w[i] >> 16) : x[p].w[2 * i + 1];
+              const uint32_t a3 = FP8 ? e4m3x2_to_half2(y[p].w[i] >> 16) : y[p].w[2 * i + 1];
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                const uint32_t(&w)[2] = q[nb][(p0 + p) * N + i];
+                mma<M>(i & 1 ? s2[nb] : s[nb], a0, a1, a2, a3, w[0], w[1]);
+              }
+            }
           }
         }
-        const float k0 = FP8 ? scales[gl] : 1.0f, k1 = FP8 ? scales[gl + 8] : 1.0f;
+        // the first pieces of the values, on their way meanwhile
+        const uint32_t values = from + S::STAGE / 2;
+        auto load = [&](int i, int p) {
+          const uint32_t at = values + value[i & 1] + (i >> 1) * 8 * S::ROW + p * 128;
+          if constexpr (S::VB == 16)
+            return lds16(at);
+          else
+            return lds8(at);
+        };
+        constexpr int VG = S::VP < 2 ? S::VP : 2;
+        Raw<S::VB> v[VG][4];
+#pragma unroll
+        for (int p = 0; p < VG; ++p)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[p][i] = load(i, p);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[nb][k] = __fadd_rn(s[nb][k], s2[nb][k]);
+        const float k0 = FP8 ? scales[tg] : 1.0f, k1 = FP8 ? scales[tg + 8] : 1.0f;
         float f[NB][2];
         bool moved = false;
 #pragma unroll
@@ -360,7 +423,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
         }
         if constexpr (FP8) {
           // weights times the values' scales, in units of a power of two above all of them so far, fit fp16
-          const float v0 = scales[16 + gl], v1 = scales[24 + gl];
+          const float v0 = scales[16 + tg], v1 = scales[24 + tg];
           const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(__float_as_uint(v0), __float_as_uint(v1)));
           if (most >= __float_as_uint(vref)) {
             const uint32_t e = min((most >> 23) + 1, 253u);
@@ -399,18 +462,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int k = 0; k < 2; ++k) w[nb][k] = transposed(Pair<M>::narrow(f2(s[nb][2 * k], s[nb][2 * k + 1])));
-        const uint32_t values = from + S::STAGE / 2;
 #pragma unroll
         for (int p = 0; p < S::VP; ++p) {
-          Raw<S::VB> v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t at = values + ((i * S::VP + p) * 32 + lane) * S::VB;
-            if constexpr (S::VB == 16)
-              v[i] = lds16(at);
-            else
-              v[i] = lds8(at);
-          }
+          Raw<S::VB>(&u)[4] = v[p % VG];
 #pragma unroll
           for (int k = 0; k < S::VB / 4; ++k) {
             if constexpr (FP8) {
@@ -418,20 +472,24 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const uint32_t sel = h ? 0x7362 : 0x5140;
-                const uint32_t x = __byte_perm(v[0].w[k], v[1].w[k], sel), y = __byte_perm(v[2].w[k], v[3].w[k], sel);
+                const uint32_t x = __byte_perm(u[0].w[k], u[1].w[k], sel), y = __byte_perm(u[2].w[k], u[3].w[k], sel);
                 const uint32_t a0 = e4m3x2_to_half2(x), a1 = e4m3x2_to_half2(x >> 16);
                 const uint32_t a2 = e4m3x2_to_half2(y), a3 = e4m3x2_to_half2(y >> 16);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][2 * k + h], a0, a1, a2, a3, w[nb][0], w[nb][1]);
               }
             } else {
-              const uint32_t a0 = __byte_perm(v[0].w[k], v[1].w[k], 0x5410);
-              const uint32_t a1 = __byte_perm(v[0].w[k], v[1].w[k], 0x7632);
-              const uint32_t a2 = __byte_perm(v[2].w[k], v[3].w[k], 0x5410);
-              const uint32_t a3 = __byte_perm(v[2].w[k], v[3].w[k], 0x7632);
+              const uint32_t a0 = __byte_perm(u[0].w[k], u[1].w[k], 0x5410);
+              const uint32_t a1 = __byte_perm(u[0].w[k], u[1].w[k], 0x7632);
+              const uint32_t a2 = __byte_perm(u[2].w[k], u[3].w[k], 0x5410);
+              const uint32_t a3 = __byte_perm(u[2].w[k], u[3].w[k], 0x7632);
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][k], a0, a1, a2, a3, w[nb][0], w[nb][1]);
             }
+          }
+          if (p + VG < S::VP) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = load(i, p + VG);
           }
         }
         stage = stage + 1 == S::STAGES ? 0 : stage + 1;
@@ -567,6 +625,7 @@ cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cu
   MmaArgs m;
   m.a = a;
   m.page = divisor((uint32_t)a.c.page_size);
+  m.whole = a.c.page_size % kTile == 0;
   m.page_rows = (int)(a.c.page_stride / a.c.D);
   m.warp_partial = a.partial + *ctas * 2 * std::min(a.group, kAttendRows) * (a.c.D + 2);
   kern<<<(unsigned)*ctas, S::THREADS, S::SMEM, s>>>(m);
