@@ -31,19 +31,28 @@ struct Sequence {
   }
 };
 
-// The sum of `v` over the CTA's threads.  shared: THREADS / 32 numbers.
+// Shared memory of a CTA that finds its place on the line.
 template <int THREADS>
-__device__ __forceinline__ int64_t cta_sum(int64_t v, int64_t* shared) {
+struct Plan {
+  int64_t start[THREADS];
+  int64_t sum[THREADS / 32];
+  // the sum of v over this thread and those before it
+  __device__ __forceinline__ int64_t upto(int64_t v) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t w = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += w;
+    }
+    if (lane == 31) sum[warp] = v;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) v += shared[w];
-  __syncthreads();
-  return v;
-}
+    for (int w = 0; w < THREADS / 32; ++w)
+      if (w < warp) v += sum[w];
+    __syncthreads();
+    return v;
+  }
+};
 
 // A place of the line: a sequence, and where on the line it starts.
 struct Mark {
@@ -58,42 +67,56 @@ struct Line {
   __device__ __forceinline__ int64_t length(const Sequence& q) const {
     return (int64_t)(q.tiles + extra) * segments;
   }
+  // The line's length, for the whole CTA; `plan` keeps where up to THREADS sequences start.
   template <int THREADS>
-  __device__ __forceinline__ int64_t total(const AttendArgs& a, int64_t* shared) const {
+  __device__ __forceinline__ int64_t total(const AttendArgs& a, Plan<THREADS>& plan) const {
     int64_t mine = 0;
+    if (a.B <= THREADS) {
+      if (threadIdx.x < a.B) mine = length(Sequence(a, threadIdx.x));
+      const int64_t upto = plan.upto(mine);
+      plan.start[threadIdx.x] = upto - mine;
+      if (threadIdx.x == THREADS - 1) plan.sum[0] = upto;
+      __syncthreads();
+      return plan.sum[0];
+    }
     for (int b = threadIdx.x; b < a.B; b += THREADS) mine += length(Sequence(a, b));
-    return cta_sum<THREADS>(mine, shared);
+    mine = plan.upto(mine);
+    if (threadIdx.x == THREADS - 1) plan.start[0] = mine;
+    __syncthreads();
+    mine = plan.start[0];
+    __syncthreads();
+    return mine;
   }
-  // the sequence that holds unit `at` of the line, for the whole CTA; shared: THREADS / 32 + 2 numbers
+  // the sequence that holds unit `at` of the line, for the whole CTA
   template <int THREADS>
-  __device__ __forceinline__ Mark find(const AttendArgs& a, int64_t at, int64_t* shared) const {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __device__ __forceinline__ Mark find(const AttendArgs& a, int64_t at, Plan<THREADS>& plan) const {
+    if (a.B <= THREADS) {
+      int lo = 0, hi = a.B;  // start[lo] <= at < start[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (plan.start[mid] <= at)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      return Mark{lo, plan.start[lo]};
+    }
     int64_t before = 0;
     for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-      const int b = b0 + tid;
+      const int b = b0 + threadIdx.x;
       const int64_t n = b < a.B ? length(Sequence(a, b)) : 0;
-      int64_t upto = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      if (lane == 31) shared[warp] = upto;
-      __syncthreads();
-      upto += before;
-#pragma unroll
-      for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) upto += shared[w];
-        before += shared[w];
-      }
+      const int64_t upto = before + plan.upto(n);
       if (at < upto && at >= upto - n) {
-        shared[THREADS / 32] = b;
-        shared[THREADS / 32 + 1] = upto - n;
+        plan.start[0] = b;
+        plan.start[1] = upto - n;
       }
+      if (threadIdx.x == THREADS - 1) plan.start[2] = upto;
       __syncthreads();
+      before = plan.start[2];
       if (at < before) break;
+      __syncthreads();
     }
-    const Mark m{(int)shared[THREADS / 32], shared[THREADS / 32 + 1]};
+    const Mark m{(int)plan.start[0], plan.start[1]};
     __syncthreads();
     return m;
   }

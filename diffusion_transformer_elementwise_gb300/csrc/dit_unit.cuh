@@ -391,10 +391,10 @@ __device__ __forceinline__ void let_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 template <class Args>
-cudaError_t launch_after(void (*kern)(Args), unsigned grid, dim3 block, size_t smem, cudaStream_t s,
+cudaError_t launch_after(void (*kern)(Args), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                          const Args& args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

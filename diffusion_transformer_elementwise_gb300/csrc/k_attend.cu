@@ -26,7 +26,7 @@ __device__ __forceinline__ float cached(const void* p, int64_t i) {
 template <class T, class K>
 __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant__ AttendArgs a) {
   constexpr bool FP8 = sizeof(K) == 1;
-  __shared__ int64_t numbers[kWarps + 2];
+  __shared__ Plan<kThreads> plan;
   __shared__ int64_t place[kTokens];
   __shared__ float kscale[kTokens], vscale[kTokens];
   __shared__ float weight[kAttendRows][kTokens];
@@ -38,14 +38,15 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int blocks = (a.group + kAttendRows - 1) / kAttendRows;
   const Line line{(int)a.c.heads * blocks, kExtra};
-  const int64_t total = line.total<kThreads>(a, numbers);
+  after_previous();
+  const int64_t total = line.total(a, plan);
   const int64_t per = max((int64_t)kLeast, (total + gridDim.x - 1) / gridDim.x);
   const int64_t begin = min(blockIdx.x * per, total), end = min(begin + per, total);
   if (tid < 2) a.owner[2 * blockIdx.x + tid] = -1;
   let_next();
   if (begin >= end) return;
   const int slot_rows = min(a.group, kAttendRows);
-  Walk walk(a, line, begin, end, line.find<kThreads>(a, begin, numbers));
+  Walk walk(a, line, begin, end, line.find(a, begin, plan));
   Segment g;
   while (walk.next(a, line, g)) {
     const int head = g.s / blocks, row0 = (g.s - head * blocks) * kAttendRows;
@@ -150,45 +151,76 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
   }
 }
 
-// The join of the segments that begin in CTA blockIdx.x and end in a later one.
+// The join of the segments that begin in CTA blockIdx.x and end in a later one: row blockIdx.y of it.  A warp has
+// every kJoinWarps-th of the parts, four columns a lane at a time.
+constexpr int kJoinWarps = 8;
 struct JoinArgs {
   AttendArgs a;
   int ctas;
 };
 template <class T>
-__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ JoinArgs j) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ JoinArgs j) {
+  __shared__ float most[kJoinWarps], sums[kJoinWarps], columns[kJoinWarps][kMaxD];
   const AttendArgs& a = j.a;
-  const int ctas = j.ctas;
-  const int D = (int)a.c.D, tid = threadIdx.x;
+  const int D = (int)a.c.D, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y, cta = blockIdx.x;
   after_previous();
-  const int64_t id = a.owner[2 * blockIdx.x + 1];
+  let_next();
+  const int64_t id = a.owner[2 * cta + 1];
   if (id < 0) return;
   const int blocks = (a.group + kAttendRows - 1) / kAttendRows;
   const int segments = (int)a.c.heads * blocks;
   const int b = (int)(id / segments), s = (int)(id - (int64_t)b * segments);
   const int head = s / blocks, row0 = (s - head * blocks) * kAttendRows;
-  const int rows = min(kAttendRows, a.group - row0), slot_rows = min(a.group, kAttendRows);
-  const int h0 = head * a.group + row0;
+  const int slot_rows = min(a.group, kAttendRows);
+  if (r >= min(kAttendRows, a.group - row0)) return;
+  int count = 1;  // parts: this CTA's, and the first ones of those after it
+  for (;; count += 32) {
+    const int k = cta + count + lane;
+    const uint32_t other = __ballot_sync(0xFFFFFFFFu, k >= j.ctas || a.owner[2 * min(k, j.ctas - 1)] != id);
+    if (other == 0) continue;
+    count += __ffs(other) - 1;
+    break;
+  }
   const int64_t size = (int64_t)slot_rows * (D + 2);
-  int end = blockIdx.x + 1;
-  while (end < ctas && a.owner[2 * end] == id) ++end;
-  auto place = [&](int cta) { return a.partial + (2 * (int64_t)cta + (cta == (int)blockIdx.x ? 1 : 0)) * size; };
-  for (int i = tid; i < rows * D; i += kThreads) {
-    const int r = i / D, c = i - r * D;
-    float m = -INFINITY;
-    for (int k = blockIdx.x; k < end; ++k) m = fmaxf(m, place(k)[r]);
-    const float base = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o = 0.0f;
-    for (int k = blockIdx.x; k < end; ++k) {
-      const float* p = place(k);
+  auto part = [&](int k) { return a.partial + (2 * (int64_t)(cta + k) + (k == 0)) * size; };
+  float m = -INFINITY;
+  for (int k = threadIdx.x; k < count; k += 32 * kJoinWarps) m = fmaxf(m, part(k)[r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if (lane == 0) most[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, most[w]);
+  const float base = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f;
+  for (int c0 = 0; c0 < D; c0 += 128) {
+    float o[4] = {};
+    l = 0.0f;
+#pragma unroll 4
+    for (int k = warp; k < count; k += kJoinWarps) {
+      const float* p = part(k);
       const float f = exp2f(__fadd_rn(p[r], -base));
       l = __fmaf_rn(p[slot_rows + r], f, l);
-      o = __fmaf_rn(p[2 * slot_rows + i], f, o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c0 + 32 * i + lane < D) o[i] = __fmaf_rn(p[2 * slot_rows + r * D + c0 + 32 * i + lane], f, o[i]);
     }
-    ((T*)a.out.p)[b * a.out.token + (h0 + r) * a.out.head + c] =
-        from_float<T>(l == 0.0f ? 0.0f : __fdiv_rn(o, l));
-    if (a.lse && c == 0) a.lse[(int64_t)b * a.Hq + h0 + r] = lse_of(m, l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) columns[warp][c0 + 32 * i + lane] = o[i];
   }
+  if (lane == 0) sums[warp] = l;
+  __syncthreads();
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) l = __fadd_rn(l, sums[w]);
+  const int h = head * a.group + row0 + r;
+  for (int c = threadIdx.x; c < D; c += 32 * kJoinWarps) {
+    float o = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) o = __fadd_rn(o, columns[w][c]);
+    ((T*)a.out.p)[b * a.out.token + h * a.out.head + c] = from_float<T>(l == 0.0f ? 0.0f : __fdiv_rn(o, l));
+  }
+  if (threadIdx.x == 0 && a.lse) a.lse[(int64_t)b * a.Hq + h] = lse_of(m, l);
 }
 
 template <class T, class K>
@@ -200,8 +232,7 @@ cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cu
   if (e != cudaSuccess) return e;
   *ctas = std::min(kAttendMaxCtas,
                    (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kThreads, smem));
-  kern<<<(unsigned)*ctas, kThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_after(kern, (unsigned)*ctas, kThreads, smem, s, a);
 }
 
 template <class T>
@@ -211,7 +242,9 @@ cudaError_t launch(const DeviceInfo& dev, bool mma, const AttendArgs& a, cudaStr
                         : a.c.format == DIT_E4M3 ? launch<T, uint8_t>(dev, a, &ctas, s)
                                                  : launch<T, T>(dev, a, &ctas, s);
   if (e != cudaSuccess) return e;
-  return launch_after(join_kernel<T>, (unsigned)ctas, kThreads, 0, s, JoinArgs{a, (int)ctas});
+  const JoinArgs j{a, (int)ctas};
+  return launch_after(join_kernel<T>, dim3((unsigned)ctas, (unsigned)std::min(a.group, kAttendRows)), 32 * kJoinWarps, 0,
+                      s, j);
 }
 
 }  // namespace

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
   using M = typename S::M;
   constexpr bool FP8 = S::FP8;
   constexpr int NB = S::NB, NCE = S::CE / 2;
-  __shared__ int64_t numbers[S::WARPS + 2];
+  __shared__ Plan<S::THREADS> plan;
   __shared__ int64_t owner[S::WARPS][2];  // the warps' shared segments, or -1
   __shared__ bool open[S::WARPS];         // whether the first goes on in the next warp's part
   extern __shared__ __align__(1024) unsigned char space[];
@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
   // Rows of a product of tokens are not tokens g but tg, and g + 8 but tg + 8: see chunk_at.
   const int tg = gl ^ ((gl & 1) << 2);
 
-  const int64_t total = line.total<S::THREADS>(a, numbers);
+  after_previous();
+  const int64_t total = line.total(a, plan);
   const int64_t warps = (int64_t)gridDim.x * S::WARPS;
   const int64_t per = max((int64_t)kLeast, (total + warps - 1) / warps);
   const int64_t begin = min((blockIdx.x * (int64_t)S::WARPS + warp) * per, total), end = min(begin + per, total);
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
   if (tid < 2) a.owner[2 * blockIdx.x + tid] = -1;
   let_next();
   if (cta_begin >= total) return;
-  const Mark mark = line.find<S::THREADS>(a, cta_begin, numbers);
+  const Mark mark = line.find(a, cta_begin, plan);
   const int64_t slot = (blockIdx.x * (int64_t)S::WARPS + warp) * 2;
   if (lane < 2) owner[warp][lane] = -1;
 
@@ -565,20 +566,24 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
     auto at = [&](int k) {
       return Piece(args.warp_partial, first + (begun ? 2 * (chain - 1 + k) + (k == 0) : 2 * k), slot_rows, D);
     };
-    float top = -INFINITY, sum = 0.0f;
-    for (int k = 0; k < pieces; ++k) top = fmaxf(top, at(k).m[r]);
-    const float base = top == -INFINITY ? 0.0f : top;
+    // lane k has piece k's maximum and sum
+    static_assert(S::WARPS < 32, "a piece a lane");
+    const float m = lane < pieces ? at(lane).m[r] : -INFINITY;
+    float top = m;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
+    const float f = exp2_fast(__fadd_rn(m, -(top == -INFINITY ? 0.0f : top)));
+    const float sum = lanes_sum<32>(lane < pieces ? __fmul_rn(at(lane).l[r], f) : 0.0f);
     float2 o[S::DP / 64] = {};
+#pragma unroll 4
     for (int k = 0; k < pieces; ++k) {
       const Piece p = at(k);
-      const float f = exp2_fast(__fadd_rn(p.m[r], -base));
-      sum = __fmaf_rn(p.l[r], f, sum);
+      const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
 #pragma unroll
       for (int i = 0; i < S::DP / 64; ++i) {
         const int c = 64 * i + 2 * lane;
-        if (c >= D) continue;
-        const float2 v = *(const float2*)(p.o + r * D + c);
-        o[i] = make_float2(__fmaf_rn(v.x, f, o[i].x), __fmaf_rn(v.y, f, o[i].y));
+        const float2 v = c < D ? *(const float2*)(p.o + r * D + c) : float2{};
+        o[i] = make_float2(__fmaf_rn(v.x, fk, o[i].x), __fmaf_rn(v.y, fk, o[i].y));
       }
     }
     if (done) {
@@ -628,8 +633,7 @@ cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cu
   m.whole = a.c.page_size % kTile == 0;
   m.page_rows = (int)(a.c.page_stride / a.c.D);
   m.warp_partial = a.partial + *ctas * 2 * std::min(a.group, kAttendRows) * (a.c.D + 2);
-  kern<<<(unsigned)*ctas, S::THREADS, S::SMEM, s>>>(m);
-  return cudaGetLastError();
+  return launch_after(kern, (unsigned)*ctas, S::THREADS, S::SMEM, s, m);
 }
 
 template <class T, bool FP8, int DP>
