@@ -35,10 +35,10 @@ struct RopeArgs {
   float eps, offset;
   bool interleaved, inverse;
   bool granules;          // every tensor lies on 16-byte boundaries, row by row
-  float* partial;         // gradient: [ctas][2][D] sums of the weights' gradients
+  float* partial;         // gradient: rows of D, the CTAs' sums of a weight's gradient
 };
 cudaError_t launch_rope(const DeviceInfo& dev, int dtype, const RopeArgs& a, cudaStream_t s);
-// the most rows of `partial`
+// half of the most rows of `partial`
 constexpr int64_t kRopeGradMaxCtas = 608;
 cudaError_t launch_rope_grad(const DeviceInfo& dev, int dtype, const RopeArgs& a, void* gwq,
                              void* gwk, cudaStream_t s);

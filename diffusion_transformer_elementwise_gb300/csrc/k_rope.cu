@@ -99,6 +99,8 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const __grid_constant
   const int heads = a.t[0].H + a.t[1].H;
   const int64_t rows = a.tokens * heads;
   const int64_t stride = (int64_t)gridDim.x * (kRowThreads / 32);
+  after_previous();
+  let_next();
   for (int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); i < rows; i += stride) {
     const HeadRow row(a, i, heads);
     const RopeTensor& t = a.t[row.tensor];
@@ -135,15 +137,117 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const __grid_constant
   }
 }
 
+// Heads in granules: AHEAD heads of a lane are loaded before the first is computed.
+constexpr int kAhead = 4;
+
+struct RopeHeads {
+  RopeArgs a;
+  HeadBlocks b;
+};
+template <class T, int TEAM, bool NORM, bool INTER, bool ALL>
+__global__ void __launch_bounds__(kRowThreads) rope_heads_kernel(const __grid_constant__ RopeHeads args) {
+  constexpr int P = HeadLane<T>::P, TEAMS = 32 / TEAM;
+  const RopeArgs& a = args.a;
+  const int lane = threadIdx.x & 31, team = lane / TEAM;
+  const int which = (int)blockIdx.y >= args.b.blocks[0];
+  const RopeTensor& t = a.t[which];
+  const int first = ((int)blockIdx.y - (which ? args.b.blocks[0] : 0)) * args.b.heads;
+  const int last = min(first + args.b.heads, t.H);
+  const HeadLane<T> h(a, lane % TEAM);
+  after_previous();
+  let_next();
+  F2 w[2][P];
+  if constexpr (NORM) head_weight<T>(w, h, t.w, a.offset);
+  const uint32_t stride = gridDim.x * (kRowThreads / 32);
+  for (uint32_t token = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); token < a.tokens; token += stride) {
+    const TokenAt at(a, token);
+    const int64_t from = at.batch * t.x.batch + at.place * t.x.token;
+    const int64_t to = at.batch * t.out.batch + at.place * t.out.token;
+    LaneAngles<T, INTER> angles;
+    if (a.R > 0) angles.load(a, h, at.table);
+    for (int head = first + team; head - team < last; head += kAhead * TEAMS) {
+      Raw<16> raw[kAhead][2];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        head_load<T>(raw[k], h, t.x.p, from + (int64_t)(head + k * TEAMS) * t.x.head, head + k * TEAMS < last);
+      float r[kAhead];
+      if constexpr (NORM) {
+        // the sums of all heads first; each lane then finds the r of one of them
+        float mine = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          F2 sum = f2(0.0f, 0.0f);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            F2 x[P];
+            Granule<T>::widen(raw[k][j], x);
+#pragma unroll
+            for (int i = 0; i < P; ++i) sum = f2_fma(x[i], x[i], sum);
+          }
+          const float total = lanes_sum<TEAM>(__fadd_rn(sum.x, sum.y));
+          if (TEAM < kAhead || lane % kAhead == k) mine = total;
+          if constexpr (TEAM < kAhead) r[k] = inverse_rms(mine, a.D, a.eps);
+        }
+        if constexpr (TEAM >= kAhead) {
+          mine = inverse_rms(mine, a.D, a.eps);
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) r[k] = __shfl_sync(0xFFFFFFFFu, mine, lane / kAhead * kAhead + k);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        F2 x[2][P];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          Granule<T>::widen(raw[k][j], x[j]);
+          if constexpr (NORM) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) x[j][i] = f2_mul(f2_mul(x[j][i], f2(r[k], r[k])), w[j][i]);
+          }
+        }
+        if (a.R > 0) angles.template turn<ALL>(x, h);
+        if (head + k * TEAMS < last) {
+          T* out = (T*)t.out.p + to + (int64_t)(head + k * TEAMS) * t.out.head;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (h.on[j]) st_stream<16>(out + h.column[j], Granule<T>::narrow(x[j]));
+        }
+      }
+    }
+  }
+}
+
+template <class T, int TEAM, bool NORM, bool INTER>
+cudaError_t launch_heads(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {
+  const auto kern = 2 * a.R == a.D ? rope_heads_kernel<T, TEAM, NORM, INTER, true>
+                                   : rope_heads_kernel<T, TEAM, NORM, INTER, false>;
+  const RopeHeads h{a, head_blocks(dev, a, 32 / TEAM, kAhead)};
+  const int64_t warps = kRowThreads / 32;
+  return launch_after(kern, dim3((unsigned)((a.tokens + warps - 1) / warps), h.b.blocks[0] + h.b.blocks[1]), kRowThreads,
+                      0, s, h);
+}
+template <class T, int TEAM>
+cudaError_t launch_heads(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {
+  const bool norm = a.t[0].w || a.t[1].w;
+  return a.interleaved ? (norm ? launch_heads<T, TEAM, true, true>(dev, a, s) : launch_heads<T, TEAM, false, true>(dev, a, s))
+                       : (norm ? launch_heads<T, TEAM, true, false>(dev, a, s) : launch_heads<T, TEAM, false, false>(dev, a, s));
+}
+
 template <class T>
 cudaError_t launch(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {
+  if (head_granules<T>(a)) {
+    const int units = head_units(a, HeadLane<T>::PER);
+    return units <= 4    ? launch_heads<T, 4>(dev, a, s)
+           : units <= 8  ? launch_heads<T, 8>(dev, a, s)
+           : units <= 16 ? launch_heads<T, 16>(dev, a, s)
+                         : launch_heads<T, 32>(dev, a, s);
+  }
   const int64_t rows = a.tokens * (a.t[0].H + a.t[1].H);
   const bool norm = a.t[0].w || a.t[1].w;
   const auto kern = norm ? rope_kernel<T, true> : rope_kernel<T, false>;
   const int64_t warps = kRowThreads / 32;
   const int64_t most = (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kRowThreads) * 8;
-  kern<<<(unsigned)std::min(most, (rows + warps - 1) / warps), kRowThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_after(kern, (unsigned)std::min(most, (rows + warps - 1) / warps), kRowThreads, 0, s, a);
 }
 
 }  // namespace

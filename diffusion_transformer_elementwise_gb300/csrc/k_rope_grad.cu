@@ -11,29 +11,32 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 
-// Any view: a warp has a head, an element per access.  Each warp adds up its
-// weights' gradients in shared memory (its own row of it), the CTA its warps'.
+// Any view: a warp has a head, an element per access; blockIdx.y tells queries from keys.  Each warp
+// adds up its weight's gradient in shared memory (its own row of it), the CTA its warps'.
 template <class T>
 __global__ void __launch_bounds__(kRowThreads) rope_grad_kernel(const __grid_constant__ RopeArgs a) {
-  extern __shared__ float sums[];  // [warps][2][D]
+  extern __shared__ float sums[];  // [warps][D]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* mine = sums + (size_t)warp * 2 * a.D;
+  float* mine = sums + (size_t)warp * a.D;
   if (a.partial) {
-    for (int c = lane; c < 2 * a.D; c += 32) mine[c] = 0.0f;
+    for (int c = lane; c < a.D; c += 32) mine[c] = 0.0f;
     __syncwarp();
   }
-  const int heads = a.t[0].H + a.t[1].H;
-  const int64_t rows = a.tokens * heads;
+  const RopeTensor& t = a.t[blockIdx.y > 0 || a.t[0].H == 0];
+  const int64_t rows = a.tokens * t.H;
   const int64_t stride = (int64_t)gridDim.x * kRowWarps;
+  after_previous();
+  let_next();
   for (int64_t i = (int64_t)blockIdx.x * kRowWarps + warp; i < rows; i += stride) {
-    const HeadRow row(a, i, heads);
-    const RopeTensor& t = a.t[row.tensor];
-    const T* x = (const T*)t.x.p + row.at(t.x);
-    const T* g = (const T*)t.g.p + row.at(t.g);
-    T* out = (T*)t.out.p + row.at(t.out);
+    const int64_t token = i / t.H, head = i - token * t.H;
+    const TokenAt place(a, (uint32_t)token);
+    auto at = [&](const dit_heads& v) { return place.batch * v.batch + place.place * v.token + head * v.head; };
+    const T* x = (const T*)t.x.p + at(t.x);
+    const T* g = (const T*)t.g.p + at(t.g);
+    T* out = (T*)t.out.p + at(t.out);
     const T* w = (const T*)t.w;
-    const float* cs = a.cos + row.table * a.R;
-    const float* sn = a.sin + row.table * a.R;
+    const float* cs = a.cos + place.table * a.R;
+    const float* sn = a.sin + place.table * a.R;
     // columns come in pairs (c, d); those that are not turned come alone
     auto columns = [&](auto&& body) {
       for (int j = lane; j < a.R; j += 32) {
@@ -61,7 +64,7 @@ __global__ void __launch_bounds__(kRowThreads) rope_grad_kernel(const __grid_con
       auto one = [&](int k, float grad) {
         const float n = __fmul_rn(to_float(x[k]), r);
         const float y = __fmul_rn(r, __fadd_rn(weighted(k, grad), -__fmul_rn(n, mean)));
-        if (a.partial) mine[row.tensor * a.D + k] = __fmaf_rn(grad, n, mine[row.tensor * a.D + k]);
+        if (a.partial) mine[k] = __fmaf_rn(grad, n, mine[k]);
         return from_float<T>(y);
       };
       const T first = one(c, u);
@@ -74,54 +77,189 @@ __global__ void __launch_bounds__(kRowThreads) rope_grad_kernel(const __grid_con
   }
   if (!a.partial) return;
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * a.D; c += kRowThreads) {
+  float* partial = a.partial + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * a.D;
+  for (int c = threadIdx.x; c < a.D; c += kRowThreads) {
     float v = 0.0f;
-    for (int k = 0; k < kRowWarps; ++k) v = __fadd_rn(v, sums[(size_t)k * 2 * a.D + c]);
-    a.partial[(int64_t)blockIdx.x * 2 * a.D + c] = v;
+    for (int k = 0; k < kRowWarps; ++k) v = __fadd_rn(v, sums[(size_t)k * a.D + c]);
+    partial[c] = v;
   }
 }
 
-// gw[k][c] = the sum over the CTAs' partial sums: 32 columns a CTA, its 32
-// warps the rows w, w + 32, ..., then their sums in order.
+// Heads in granules.  A CTA has heads of the queries or of the keys alone, and tokens with a stride, so that a
+// lane adds up its columns' part of one weight's gradient in registers.
+constexpr int kAhead = 2;
+
+struct GradHeads {
+  RopeArgs a;
+  HeadBlocks b;
+};
+template <class T, int TEAM, bool INTER, bool ALL>
+__global__ void __launch_bounds__(kRowThreads) rope_grad_heads_kernel(const __grid_constant__ GradHeads args) {
+  constexpr int P = HeadLane<T>::P, TEAMS = 32 / TEAM;
+  extern __shared__ float sums[];  // [warps][D]
+  const RopeArgs& a = args.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = lane / TEAM;
+  const int which = (int)blockIdx.y >= args.b.blocks[0];
+  const RopeTensor& t = a.t[which];
+  const int first = ((int)blockIdx.y - (which ? args.b.blocks[0] : 0)) * args.b.heads;
+  const int last = min(first + args.b.heads, t.H);
+  const HeadLane<T> h(a, lane % TEAM);
+  after_previous();
+  let_next();
+  F2 w[2][P], acc[2][P];
+  head_weight<T>(w, h, t.w, a.offset);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int i = 0; i < P; ++i) acc[j][i] = f2(0.0f, 0.0f);
+  const uint32_t stride = gridDim.x * kRowWarps;
+  for (uint32_t token = blockIdx.x * kRowWarps + warp; token < a.tokens; token += stride) {
+    const TokenAt at(a, token);
+    const int64_t from = at.batch * t.x.batch + at.place * t.x.token;
+    const int64_t grad = at.batch * t.g.batch + at.place * t.g.token;
+    const int64_t to = at.batch * t.out.batch + at.place * t.out.token;
+    LaneAngles<T, INTER> angles;
+    if (a.R > 0) angles.load(a, h, at.table);  // (a.inverse is set: the gradient is turned back)
+    for (int head = first + team; head - team < last; head += kAhead * TEAMS) {
+      Raw<16> rx[kAhead][2], rg[kAhead][2];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const bool on = head + k * TEAMS < last;
+        head_load<T>(rx[k], h, t.x.p, from + (int64_t)(head + k * TEAMS) * t.x.head, on);
+        head_load<T>(rg[k], h, t.g.p, grad + (int64_t)(head + k * TEAMS) * t.g.head, on);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        F2 x[2][P], u[2][P];
+        F2 square = f2(0.0f, 0.0f), dot = f2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          Granule<T>::widen(rx[k][j], x[j]);
+          Granule<T>::widen(rg[k][j], u[j]);
+        }
+        if (a.R > 0) angles.template turn<ALL>(u, h);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            square = f2_fma(x[j][i], x[j][i], square);
+            dot = f2_fma(f2_mul(u[j][i], w[j][i]), x[j][i], dot);
+          }
+        const float r = inverse_rms(lanes_sum<TEAM>(__fadd_rn(square.x, square.y)), a.D, a.eps);
+        const float mean = __fdiv_rn(__fmul_rn(lanes_sum<TEAM>(__fadd_rn(dot.x, dot.y)), r), (float)a.D);
+        const bool on = head + k * TEAMS < last;
+        T* out = (T*)t.out.p + to + (int64_t)(head + k * TEAMS) * t.out.head;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          F2 y[P];
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const F2 n = f2_mul(x[j][i], f2(r, r));
+            if (on) acc[j][i] = f2_fma(u[j][i], n, acc[j][i]);
+            y[i] = f2_mul(f2_fma(n, f2(-mean, -mean), f2_mul(u[j][i], w[j][i])), f2(r, r));
+          }
+          if (on && h.on[j]) st_stream<16>(out + h.column[j], Granule<T>::narrow(y));
+        }
+      }
+    }
+  }
+  if (!a.partial) return;
+  // the warp's teams, then the CTA's warps, in order
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+#pragma unroll
+      for (int o = TEAM; o < 32; o <<= 1) {
+        acc[j][i].x = __fadd_rn(acc[j][i].x, __shfl_xor_sync(0xFFFFFFFFu, acc[j][i].x, o));
+        acc[j][i].y = __fadd_rn(acc[j][i].y, __shfl_xor_sync(0xFFFFFFFFu, acc[j][i].y, o));
+      }
+      if (team == 0 && h.on[j]) *(float2*)(sums + warp * a.D + h.column[j] + 2 * i) = acc[j][i];
+    }
+  __syncthreads();
+  float* out = a.partial + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * a.D;
+  for (int c = threadIdx.x; c < a.D; c += kRowThreads) {
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kRowWarps; ++k) v = __fadd_rn(v, sums[k * a.D + c]);
+    out[c] = v;
+  }
+}
+
+// gw[which][c] = the sum over the partial rows [0, split) (queries) or [split, rows) (keys): 32 columns
+// a CTA, its 32 warps every 32nd row, then their sums in order.
 struct JoinArgs {
   const float* partial;
-  int ctas, D;
+  int split, rows, D;
   void* gw[2];
 };
 template <class T>
-__global__ void __launch_bounds__(1024) join_kernel(JoinArgs a) {
+__global__ void __launch_bounds__(1024) join_kernel(const __grid_constant__ JoinArgs a) {
   __shared__ float part[32][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float v = 0.0f;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y;
+  T* gw = (T*)a.gw[which];
   after_previous();
-  if (c < 2 * a.D)
-    for (int i = warp; i < a.ctas; i += 32) v = __fadd_rn(v, a.partial[(int64_t)i * 2 * a.D + c]);
+  let_next();
+  if (!gw) return;
+  const int c = blockIdx.x * 32 + lane;
+  const int end = which ? a.rows : a.split;
+  float v = 0.0f;
+  if (c < a.D) {
+#pragma unroll 8
+    for (int i = (which ? a.split : 0) + warp; i < end; i += 32) v = __fadd_rn(v, a.partial[(int64_t)i * a.D + c]);
+  }
   part[warp][lane] = v;
   __syncthreads();
   v = lanes_sum<32>(part[lane][warp]);
   const int k = blockIdx.x * 32 + warp;
-  if (lane == 0 && k < 2 * a.D) {
-    T* gw = (T*)a.gw[k >= a.D];
-    if (gw) gw[k >= a.D ? k - a.D : k] = from_float<T>(v);
+  if (lane == 0 && k < a.D) gw[k] = from_float<T>(v);
+}
+
+// split, rows: the partial rows written
+template <class T, int TEAM>
+cudaError_t launch_heads(const DeviceInfo& dev, const RopeArgs& a, int* split, int* rows, cudaStream_t s) {
+  const bool all = 2 * a.R == a.D;
+  const auto kern = a.interleaved ? (all ? rope_grad_heads_kernel<T, TEAM, true, true> : rope_grad_heads_kernel<T, TEAM, true, false>)
+                                  : (all ? rope_grad_heads_kernel<T, TEAM, false, true> : rope_grad_heads_kernel<T, TEAM, false, false>);
+  GradHeads g{a, head_blocks(dev, a, 32 / TEAM, kAhead)};
+  // (the workspace has room for so many partial rows)
+  const int64_t limit = 2 * kRopeGradMaxCtas;
+  while (g.b.blocks[0] + g.b.blocks[1] > limit) {
+    g.b.heads *= 2;
+    for (int i = 0; i < 2; ++i) g.b.blocks[i] = (a.t[i].H + g.b.heads - 1) / g.b.heads;
   }
+  const int blocks = g.b.blocks[0] + g.b.blocks[1];
+  const size_t smem = (size_t)kRowWarps * a.D * 4;
+  const int64_t resident = (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kRowThreads, smem);
+  const int64_t x = std::max<int64_t>(1, std::min({resident / blocks, limit / blocks, (a.tokens + kRowWarps - 1) / kRowWarps}));
+  *split = (int)x * g.b.blocks[0];
+  *rows = (int)x * blocks;
+  return launch_after(kern, dim3((unsigned)x, blocks), kRowThreads, smem, s, g);
 }
 
 template <class T>
 cudaError_t launch(const DeviceInfo& dev, const RopeArgs& a, void* gwq, void* gwk, cudaStream_t s) {
-  const int64_t rows = a.tokens * (a.t[0].H + a.t[1].H);
-  const auto kern = rope_grad_kernel<T>;
-  const size_t smem = a.partial ? (size_t)kRowWarps * 2 * a.D * 4 : 0;
-  static std::atomic<int> opted[kOptinDevices];
-  cudaError_t e = allow_shared((const void*)kern, dev, opted);
-  if (e != cudaSuccess) return e;
-  const int64_t most = std::min(kRopeGradMaxCtas, (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kRowThreads, smem));
-  const unsigned grid = (unsigned)std::min(most, (rows + kRowWarps - 1) / kRowWarps);
-  kern<<<grid, kRowThreads, smem, s>>>(a);
-  e = cudaGetLastError();
+  int split = 0, rows = 0;
+  cudaError_t e;
+  if (head_granules<T>(a)) {
+    const int units = head_units(a, HeadLane<T>::PER);
+    e = units <= 4    ? launch_heads<T, 4>(dev, a, &split, &rows, s)
+        : units <= 8  ? launch_heads<T, 8>(dev, a, &split, &rows, s)
+        : units <= 16 ? launch_heads<T, 16>(dev, a, &split, &rows, s)
+                      : launch_heads<T, 32>(dev, a, &split, &rows, s);
+  } else {
+    const auto kern = rope_grad_kernel<T>;
+    const size_t smem = a.partial ? (size_t)kRowWarps * a.D * 4 : 0;
+    const int64_t most = std::min(kRopeGradMaxCtas, (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kRowThreads, smem));
+    const int64_t heads = std::max(a.t[0].H, a.t[1].H);
+    const unsigned grid = (unsigned)std::min(most, (a.tokens * heads + kRowWarps - 1) / kRowWarps);
+    split = a.t[0].H ? (int)grid : 0;
+    rows = split + (a.t[1].H ? (int)grid : 0);
+    e = launch_after(kern, dim3(grid, (a.t[0].H > 0) + (a.t[1].H > 0)), kRowThreads, smem, s, a);
+  }
   if (e != cudaSuccess || !a.partial) return e;
-  return launch_after(join_kernel<T>, (unsigned)((2 * a.D + 31) / 32), 1024, 0, s,
-                      JoinArgs{a.partial, (int)grid, a.D, {gwq, gwk}});
+  return launch_after(join_kernel<T>, dim3((unsigned)((a.D + 31) / 32), 2), 1024, 0, s,
+                      JoinArgs{a.partial, split, rows, a.D, {gwq, gwk}});
 }
 
 }  // namespace
