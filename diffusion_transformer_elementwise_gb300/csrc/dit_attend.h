@@ -32,7 +32,7 @@ struct RopeArgs {
   int64_t tokens, L;      // B * L, L
   int64_t table_rows;     // of cos and sin
   int D, R;
-  float eps, offset;
+  float eps, offset, inv_d;  // inv_d: fl(1 / D)
   bool interleaved, inverse;
   bool granules;          // every tensor lies on 16-byte boundaries, row by row
   float* partial;         // gradient: rows of D, the CTAs' sums of a weight's gradient

@@ -193,6 +193,7 @@ dit_status rope_checks(const RopeCall& c, dit::RopeArgs* a, View (*views)[3], bo
   a->R = (int)c.R;
   a->eps = c.eps;
   a->offset = c.offset;
+  a->inv_d = c.D > 0 ? 1.0f / (float)c.D : 0.0f;
   a->interleaved = c.interleaved != 0;
   a->inverse = c.inverse != 0;
   *go = any;

@@ -36,9 +36,9 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
-// r of a head's norm from its sum of squares: each step correctly rounded.
-__device__ __forceinline__ float inverse_rms(float sum, int D, float eps) {
-  return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)D), eps)));
+// r of a head's norm from its sum of squares (inv_d: fl(1 / D)).
+__device__ __forceinline__ float inverse_rms(float sum, float inv_d, float eps) {
+  return rsqrtf(__fmaf_rn(sum, inv_d, eps));
 }
 
 // The pair (a, b) turned: one product rounded, the other one with the sum.

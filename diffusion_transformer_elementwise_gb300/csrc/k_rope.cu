@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const __grid_constant
         const float v = to_float(x[c]);
         sum = __fmaf_rn(v, v, sum);
       }
-      r = inverse_rms(lanes_sum<32>(sum), a.D, a.eps);
+      r = inverse_rms(lanes_sum<32>(sum), a.inv_d, a.eps);
     }
     auto value = [&](int c) {
       const float v = to_float(x[c]);
@@ -145,7 +145,7 @@ struct RopeHeads {
   HeadBlocks b;
 };
 template <class T, int TEAM, bool NORM, bool INTER, bool ALL>
-__global__ void __launch_bounds__(kRowThreads) rope_heads_kernel(const __grid_constant__ RopeHeads args) {
+__global__ void __launch_bounds__(kRowThreads, 2) rope_heads_kernel(const __grid_constant__ RopeHeads args) {
   constexpr int P = HeadLane<T>::P, TEAMS = 32 / TEAM;
   const RopeArgs& a = args.a;
   const int lane = threadIdx.x & 31, team = lane / TEAM;
@@ -186,10 +186,10 @@ __global__ void __launch_bounds__(kRowThreads) rope_heads_kernel(const __grid_co
           }
           const float total = lanes_sum<TEAM>(__fadd_rn(sum.x, sum.y));
           if (TEAM < kAhead || lane % kAhead == k) mine = total;
-          if constexpr (TEAM < kAhead) r[k] = inverse_rms(mine, a.D, a.eps);
+          if constexpr (TEAM < kAhead) r[k] = inverse_rms(mine, a.inv_d, a.eps);
         }
         if constexpr (TEAM >= kAhead) {
-          mine = inverse_rms(mine, a.D, a.eps);
+          mine = inverse_rms(mine, a.inv_d, a.eps);
 #pragma unroll
           for (int k = 0; k < kAhead; ++k) r[k] = __shfl_sync(0xFFFFFFFFu, mine, lane / kAhead * kAhead + k);
         }

@@ -57,9 +57,9 @@ __global__ void __launch_bounds__(kRowThreads) rope_grad_kernel(const __grid_con
       sum = __fmaf_rn(q, q, sum);
       dot = __fmaf_rn(weighted(d, v), q, dot);
     });
-    const float r = inverse_rms(lanes_sum<32>(sum), a.D, a.eps);
+    const float r = inverse_rms(lanes_sum<32>(sum), a.inv_d, a.eps);
     // mean(t n), n = x r
-    const float mean = __fdiv_rn(__fmul_rn(lanes_sum<32>(dot), r), (float)a.D);
+    const float mean = __fmul_rn(__fmul_rn(lanes_sum<32>(dot), r), a.inv_d);
     columns([&](int c, float u, int d, float v) {
       auto one = [&](int k, float grad) {
         const float n = __fmul_rn(to_float(x[k]), r);
@@ -87,14 +87,14 @@ __global__ void __launch_bounds__(kRowThreads) rope_grad_kernel(const __grid_con
 
 // Heads in granules.  A CTA has heads of the queries or of the keys alone, and tokens with a stride, so that a
 // lane adds up its columns' part of one weight's gradient in registers.
-constexpr int kAhead = 2;
+constexpr int kAhead = 1;
 
 struct GradHeads {
   RopeArgs a;
   HeadBlocks b;
 };
 template <class T, int TEAM, bool INTER, bool ALL>
-__global__ void __launch_bounds__(kRowThreads) rope_grad_heads_kernel(const __grid_constant__ GradHeads args) {
+__global__ void __launch_bounds__(kRowThreads, 2) rope_grad_heads_kernel(const __grid_constant__ GradHeads args) {
   constexpr int P = HeadLane<T>::P, TEAMS = 32 / TEAM;
   extern __shared__ float sums[];  // [warps][D]
   const RopeArgs& a = args.a;
@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(kRowThreads) rope_grad_heads_kernel(const __gr
             square = f2_fma(x[j][i], x[j][i], square);
             dot = f2_fma(f2_mul(u[j][i], w[j][i]), x[j][i], dot);
           }
-        const float r = inverse_rms(lanes_sum<TEAM>(__fadd_rn(square.x, square.y)), a.D, a.eps);
-        const float mean = __fdiv_rn(__fmul_rn(lanes_sum<TEAM>(__fadd_rn(dot.x, dot.y)), r), (float)a.D);
+        const float r = inverse_rms(lanes_sum<TEAM>(__fadd_rn(square.x, square.y)), a.inv_d, a.eps);
+        const float mean = __fmul_rn(__fmul_rn(lanes_sum<TEAM>(__fadd_rn(dot.x, dot.y)), r), a.inv_d);
         const bool on = head + k * TEAMS < last;
         T* out = (T*)t.out.p + to + (int64_t)(head + k * TEAMS) * t.out.head;
 #pragma unroll

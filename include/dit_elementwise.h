@@ -690,7 +690,7 @@ dit_status dit_rope(const dit_heads* q_out, const dit_heads* k_out, const dit_he
  * The same after a weighted RMSNorm of each head (its D columns), in one pass and
  * rounded once:  y = x * r * (weight_offset + weight),  r = 1 / sqrt(mean(x^2) + eps).
  * weight_q, weight_k: [D], shared by the heads.  The statistic is a
- * fp32 sum, a correctly rounded quotient, root and reciprocal.  R may be 0 (the norm alone; cos and
+ * fp32 sum; r is within three fp32 ulps of that sum's.  R may be 0 (the norm alone; cos and
  * sin may then be NULL).
  */
 dit_status dit_rmsnorm_rope(const dit_heads* q_out, const dit_heads* k_out, const dit_heads* q,

@@ -4,9 +4,8 @@ arithmetic.  CPU, numpy; shares no code with the library.
 
 Tolerances count roundings, u = 2^-24 each.  The statistic of a head's norm is a sum
 of at most 1024 squares in a tree (at most 32 chained additions in a lane and 5 across
-lanes), a quotient, a root and a reciprocal: r is within 22 u (the sum's error is halved by the
-root).  A normed value carries two products more and the weight's addition, a turned one a product,
-a sum and the table's roundings as given (the reference reads the same table): within 28 u of
+lanes; the root halves its error), a product and a reciprocal root of 2 ulp: r is within 25 u.  A normed value carries two products more and the weight's addition, a turned one a product,
+a sum and the table's roundings as given (the reference reads the same table): within 31 u of
 the two products' sizes.  REL = 2^-18 (64 u) leaves a factor of two for the second order.
 A result stored in a dtype is off by half a step more.
 """
