@@ -9,6 +9,15 @@
 
 namespace dit {
 
+__device__ __forceinline__ void cp_async8_part(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ Raw<8> lds8(uint32_t at) {
+  Raw<8> r;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(at));
+  return r;
+}
+
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_float(float v) { return v; }
@@ -20,6 +29,21 @@ template <>
 __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ float from_float(float v) { return v; }
+
+// q = t / d for 0 <= t < 2^31: t m / 2^(31 + s) with 2^(s - 1) < d <= 2^s, m = ceil(2^(31 + s) / d): m d exceeds
+// 2^(31 + s) by less than 2^s, which moves the quotient by less than 1 / d.
+struct Divisor {
+  uint32_t d, m, s;
+};
+__device__ __forceinline__ uint32_t quotient(uint32_t t, const Divisor& v) {
+  return (uint32_t)(((uint64_t)t * v.m) >> (31 + v.s));
+}
+inline Divisor divisor(uint32_t d) {
+  Divisor v{d, 0, 0};
+  while ((uint64_t(1) << v.s) < d) ++v.s;
+  v.m = (uint32_t)(((uint64_t(1) << (31 + v.s)) + d - 1) / d);
+  return v;
+}
 
 // The sum over the N lanes of an aligned group, in every one of them.
 template <int N>
@@ -72,7 +96,7 @@ struct HeadRow {
 // where the pairs are adjacent columns, or two that are not turned.  So the partners of every
 // rotation are in one lane, and a team's accesses are contiguous.  A warp takes a token, its
 // teams the token's heads one beside the other, so that the angles (and the weights) are
-// loaded once for all of a token's heads.
+// loaded once for several heads.
 // ---------------------------------------------------------------------------
 
 // units of a head: lanes that its granules take
@@ -115,77 +139,102 @@ struct HeadLane {
   }
 };
 
-// The angles of a lane's columns.  INTER: cosines twice, sines with their signs, for each granule; else cosines,
-// and sines with either sign, for both granules.
-template <class T, bool INTER>
+// The copies of one item of work, a token's next HEADS heads of each team: for each lane its granules of NT tensors
+// and the angles of its columns, each to a place of its own in shared memory that no other lane reads.
+template <class T, int TEAM, bool INTER, int NT>
+struct HeadStage {
+  using Lane = HeadLane<T>;
+  static constexpr int TEAMS = 32 / TEAM;
+  static constexpr int HEADS = NT == 1 ? 4 : 2;
+  static constexpr int GRANULES = HEADS * NT * 2;
+  // angles: cosines and sines of PER columns (both granules'), or of PER / 2 pairs for each granule
+  static constexpr int AB = INTER && sizeof(T) == 4 ? 8 : 16;  // bytes of a piece
+  static constexpr int AN = INTER ? 2 : Lane::PER * 4 / 16;    // pieces of cosines
+  static constexpr int BYTES = 32 * (GRANULES * 16 + 2 * AN * AB);
+
+  __device__ __forceinline__ static uint32_t granule(uint32_t stage, int lane, int tensor, int head, int j) {
+    return stage + (((tensor * HEADS + head) * 2 + j) * 32 + lane) * 16;
+  }
+  __device__ __forceinline__ static uint32_t angle(uint32_t stage, int lane, int i) {
+    return stage + GRANULES * 512 + (i * 32 + lane) * AB;
+  }
+  // tensor[at + head k stride]: heads [first, last)
+  __device__ __forceinline__ static void copy_heads(uint32_t stage, int lane, const Lane& h, int tensor, const void* p,
+                                                    int64_t at, int64_t stride, int first, int last) {
+    const T* src = (const T*)p + at + first * stride;
+#pragma unroll
+    for (int k = 0; k < HEADS; ++k) {
+      const bool on = first + k * TEAMS < last;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool any = on && h.on[j];
+        cp_async16_part(granule(stage, lane, tensor, k, j), any ? src + h.column[j] : (const T*)p, any ? 16 : 0);
+      }
+      src += TEAMS * stride;
+    }
+  }
+  __device__ __forceinline__ static void copy_angles(uint32_t stage, int lane, const Lane& h, const RopeArgs& a,
+                                                     int64_t row) {
+    if (a.R == 0) return;
+#pragma unroll
+    for (int i = 0; i < 2 * AN; ++i) {
+      const int k = INTER ? i % AN : 0;
+      const bool any = h.on[k] && h.turn[k];
+      const float* from = (i < AN ? a.cos : a.sin) + (any ? row * a.R + (INTER ? h.column[k] / 2 : h.column[0] + i % AN * 4) : 0);
+      if constexpr (AB == 16)
+        cp_async16_part(angle(stage, lane, i), from, any ? 16 : 0);
+      else
+        cp_async8_part(angle(stage, lane, i), from, any ? 8 : 0);
+    }
+  }
+};
+
+// The angles of a lane's columns: cosines and sines of PER columns, or of the pairs of both granules.
+template <class T, int TEAM, bool INTER, int NT>
 struct LaneAngles {
-  static constexpr int P = HeadLane<T>::P;
-  F2 c[INTER ? 2 : 1][P], s[2][P];
-  __device__ __forceinline__ void load(const RopeArgs& a, const HeadLane<T>& h, int64_t row) {
-    const float* cs = a.cos + row * a.R;
-    const float* sn = a.sin + row * a.R;
-    const float sign = a.inverse ? -1.0f : 1.0f;
-    if constexpr (INTER) {
+  using Stage = HeadStage<T, TEAM, INTER, NT>;
+  static constexpr int P = HeadLane<T>::P, N = 2 * P;
+  float c[N], s[N];
+  __device__ __forceinline__ void load(uint32_t stage, int lane, bool inverse) {
+    constexpr int F = Stage::AB / 4;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+    for (int i = 0; i < Stage::AN; ++i) {
+      if constexpr (F == 4) {
+        const Raw<16> x = lds16(Stage::angle(stage, lane, i)), y = lds16(Stage::angle(stage, lane, Stage::AN + i));
 #pragma unroll
-        for (int i = 0; i < P; ++i) c[k][i] = f2(1.0f, 1.0f), s[k][i] = f2(0.0f, 0.0f);
+        for (int k = 0; k < 4; ++k) c[4 * i + k] = __uint_as_float(x.w[k]), s[4 * i + k] = __uint_as_float(y.w[k]);
+      } else {
+        const Raw<8> x = lds8(Stage::angle(stage, lane, i)), y = lds8(Stage::angle(stage, lane, Stage::AN + i));
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (!h.on[k] || !h.turn[k]) continue;
-        const Raw<P * 4> x = ld_bcast<P * 4>(cs + h.column[k] / 2), y = ld_bcast<P * 4>(sn + h.column[k] / 2);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const float u = __uint_as_float(x.w[i]), v = __fmul_rn(sign, __uint_as_float(y.w[i]));
-          c[k][i] = f2(u, u);
-          s[k][i] = f2(-v, v);
-        }
+        for (int k = 0; k < 2; ++k) c[2 * i + k] = __uint_as_float(x.w[k]), s[2 * i + k] = __uint_as_float(y.w[k]);
       }
-    } else {
+    }
+    if (inverse) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) c[0][i] = f2(1.0f, 1.0f), s[0][i] = s[1][i] = f2(0.0f, 0.0f);
-      if (!h.on[0] || !h.turn[0]) return;
-#pragma unroll
-      for (int i = 0; i < P; i += 2) {
-        const Raw<16> x = ld_bcast<16>(cs + h.column[0] + 2 * i), y = ld_bcast<16>(sn + h.column[0] + 2 * i);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          c[0][i + k] = f2(__uint_as_float(x.w[2 * k]), __uint_as_float(x.w[2 * k + 1]));
-          const F2 v = f2(__uint_as_float(y.w[2 * k]), __uint_as_float(y.w[2 * k + 1]));
-          s[1][i + k] = f2_mul(v, f2(sign, sign));
-          s[0][i + k] = f2_mul(v, f2(-sign, -sign));
-        }
-      }
+      for (int i = 0; i < N; ++i) s[i] = -s[i];
     }
   }
   // ALL: every column of a head is turned
   template <bool ALL>
   __device__ __forceinline__ void turn(F2 (&x)[2][P], const HeadLane<T>& h) const {
+    if constexpr (INTER) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const F2 a = x[0][i], b = x[1][i];
-      F2 u, v;
-      if constexpr (INTER) {
-        u = f2_fma(a, c[0][i], f2_mul(f2(a.y, a.x), s[0][i]));
-        v = f2_fma(b, c[1][i], f2_mul(f2(b.y, b.x), s[1][i]));
-      } else {
-        u = f2_fma(a, c[0][i], f2_mul(b, s[0][i]));
-        v = f2_fma(b, c[0][i], f2_mul(a, s[1][i]));
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const F2 y = turned(x[j][i].x, x[j][i].y, c[j * P + i], s[j * P + i]);
+          if (ALL || h.turn[j]) x[j][i] = y;
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const F2 y = turned(x[0][i].x, x[1][i].x, c[2 * i], s[2 * i]), z = turned(x[0][i].y, x[1][i].y, c[2 * i + 1], s[2 * i + 1]);
+        if (ALL || h.turn[0]) x[0][i] = f2(y.x, z.x), x[1][i] = f2(y.y, z.y);
       }
-      x[0][i] = ALL || h.turn[0] ? u : a;
-      x[1][i] = ALL || h.turn[1] ? v : b;
     }
   }
 };
 
-template <class T>
-__device__ __forceinline__ void head_load(Raw<16> (&r)[2], const HeadLane<T>& h, const void* p, int64_t at, bool on) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    r[k] = Raw<16>{};
-    if (on && h.on[k]) r[k] = ld_stream<16>((const T*)p + at + h.column[k]);
-  }
-}
 template <class T>
 __device__ __forceinline__ void head_weight(F2 (&w)[2][HeadLane<T>::P], const HeadLane<T>& h, const void* p, float offset) {
 #pragma unroll
@@ -198,24 +247,44 @@ __device__ __forceinline__ void head_weight(F2 (&w)[2][HeadLane<T>::P], const He
   }
 }
 
-// How the heads of a call are given to warps: CTA (x, y) has tokens x WARPS + warp, and so on with a stride of
-// gridDim.x WARPS, and block y of the heads: blocks [0, blocks[0]) of `heads` queries, then the keys'.
-struct HeadBlocks {
-  int heads, blocks[2];
+// How the items of a call are given to warps: CTAs [0, ctas[0]) have the queries', the others the keys'; a
+// tensor's warps take its items in turn.  A token has per[i] items.
+struct HeadGrid {
+  int ctas[2], per[2];
 };
-// teams: heads that a warp has at once, `ahead` of them a lane
-inline HeadBlocks head_blocks(const DeviceInfo& dev, const RopeArgs& a, int teams, int ahead) {
-  // all heads of a token, unless that leaves less than 32 warps an SM
-  const int64_t most = std::max(a.t[0].H, a.t[1].H), want = (int64_t)dev.sm_count * 32;
-  const int64_t split = std::max<int64_t>(1, want / std::max<int64_t>(1, a.tokens));
-  int64_t heads = std::max<int64_t>(teams, (most + split - 1) / split);
-  heads = (heads + teams - 1) / teams * teams;
-  if (heads > (int64_t)teams * ahead) heads = (heads + teams * ahead - 1) / (teams * ahead) * (teams * ahead);
-  HeadBlocks b;
-  b.heads = (int)heads;
-  for (int i = 0; i < 2; ++i) b.blocks[i] = (int)((a.t[i].H + heads - 1) / heads);
-  return b;
+// together: heads of an item; most: CTAs
+inline HeadGrid head_grid(const RopeArgs& a, int together, int warps, int64_t most) {
+  HeadGrid g = {};
+  double items[2];
+  for (int i = 0; i < 2; ++i) {
+    g.per[i] = (a.t[i].H + together - 1) / together;
+    items[i] = (double)g.per[i] * (double)a.tokens;
+  }
+  for (int i = 0; i < 2; ++i) {
+    if (items[i] == 0) continue;
+    const double share = items[1 - i] == 0 ? (double)most : std::max(1.0, (double)(most - 1) * items[i] / (items[0] + items[1]));
+    g.ctas[i] = (int)std::min(share, (items[i] + warps - 1) / warps);
+  }
+  return g;
 }
+
+// A warp's walk over its items.
+struct HeadWalk {
+  int64_t token, step;
+  int part, per, rest;
+  __device__ __forceinline__ HeadWalk(const HeadGrid& g, int which, int64_t warp, int64_t warps)
+      : per(g.per[which]) {
+    token = warp / per;
+    part = (int)(warp - token * per);
+    step = warps / per;
+    rest = (int)(warps - step * per);
+  }
+  __device__ __forceinline__ void next() {
+    token += step;
+    part += rest;
+    if (part >= per) part -= per, ++token;
+  }
+};
 
 // A token's batch, place and row of angles (tokens < 2^31).
 struct TokenAt {

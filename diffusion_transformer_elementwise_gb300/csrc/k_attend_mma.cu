@@ -60,11 +60,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t codes) {  // the lo
   asm("{ .reg .b16 c, d; mov.b32 {c, d}, %1; cvt.rn.f16x2.e4m3x2 %0, c; }" : "=r"(h) : "r"(codes));
   return h;
 }
-__device__ __forceinline__ Raw<8> lds8(uint32_t at) {
-  Raw<8> r;
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(at));
-  return r;
-}
 // the sum or maximum over the lanes of one c
 __device__ __forceinline__ float column_sum(float v) {
 #pragma unroll
@@ -127,15 +122,6 @@ struct Shape {
 
 constexpr int kExtra = 2;  // units of a segment beside its tiles
 constexpr int kLeast = 2;  // the smallest part of a warp
-
-// q = t / d for 0 <= t < 2^31: t m / 2^(31 + s) with 2^(s - 1) < d <= 2^s, m = ceil(2^(31 + s) / d): m d exceeds
-// 2^(31 + s) by less than 2^s, which moves the quotient by less than 1 / d.
-struct Divisor {
-  uint32_t d, m, s;
-};
-__device__ __forceinline__ uint32_t quotient(uint32_t t, const Divisor& v) {
-  return (uint32_t)(((uint64_t)t * v.m) >> (31 + v.s));
-}
 
 struct MmaArgs {
   AttendArgs a;
@@ -610,13 +596,6 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
       }
     }
   }
-}
-
-Divisor divisor(uint32_t d) {
-  Divisor v{d, 0, 0};
-  while ((uint64_t(1) << v.s) < d) ++v.s;
-  v.m = (uint32_t)(((uint64_t(1) << (31 + v.s)) + d - 1) / d);
-  return v;
 }
 
 template <class T, bool FP8, int DP, int NB>

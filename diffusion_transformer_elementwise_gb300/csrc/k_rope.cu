@@ -137,94 +137,116 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const __grid_constant
   }
 }
 
-// Heads in granules: AHEAD heads of a lane are loaded before the first is computed.
-constexpr int kAhead = 4;
+// Heads in granules: a warp's items one after the other, the next kStages - 1 on their way.
+constexpr int kStages = 3;
 
 struct RopeHeads {
   RopeArgs a;
-  HeadBlocks b;
+  HeadGrid g;
 };
 template <class T, int TEAM, bool NORM, bool INTER, bool ALL>
 __global__ void __launch_bounds__(kRowThreads, 2) rope_heads_kernel(const __grid_constant__ RopeHeads args) {
-  constexpr int P = HeadLane<T>::P, TEAMS = 32 / TEAM;
+  using Stage = HeadStage<T, TEAM, INTER, 1>;
+  constexpr int P = HeadLane<T>::P, TEAMS = Stage::TEAMS, HEADS = Stage::HEADS, WARPS = kRowThreads / 32;
+  extern __shared__ __align__(16) unsigned char space[];
   const RopeArgs& a = args.a;
-  const int lane = threadIdx.x & 31, team = lane / TEAM;
-  const int which = (int)blockIdx.y >= args.b.blocks[0];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = lane / TEAM;
+  const int which = (int)blockIdx.x >= args.g.ctas[0], cta = which ? blockIdx.x - args.g.ctas[0] : blockIdx.x;
   const RopeTensor& t = a.t[which];
-  const int first = ((int)blockIdx.y - (which ? args.b.blocks[0] : 0)) * args.b.heads;
-  const int last = min(first + args.b.heads, t.H);
   const HeadLane<T> h(a, lane % TEAM);
+  const uint32_t stages = smem_addr(space) + warp * kStages * Stage::BYTES;
   after_previous();
   let_next();
+  const HeadWalk start(args.g, which, (int64_t)cta * WARPS + warp, (int64_t)args.g.ctas[which] * WARPS);
+  HeadWalk ahead = start;
+  auto issue = [&](int s) {
+    if (ahead.token < a.tokens) {
+      const TokenAt at(a, (uint32_t)ahead.token);
+      const uint32_t stage = stages + s * Stage::BYTES;
+      Stage::copy_heads(stage, lane, h, 0, t.x.p, at.batch * t.x.batch + at.place * t.x.token, t.x.head,
+                        ahead.part * HEADS * TEAMS + team, t.H);
+      Stage::copy_angles(stage, lane, h, a, at.table);
+      ahead.next();
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) issue(s);
   F2 w[2][P];
   if constexpr (NORM) head_weight<T>(w, h, t.w, a.offset);
-  const uint32_t stride = gridDim.x * (kRowThreads / 32);
-  for (uint32_t token = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); token < a.tokens; token += stride) {
-    const TokenAt at(a, token);
-    const int64_t from = at.batch * t.x.batch + at.place * t.x.token;
-    const int64_t to = at.batch * t.out.batch + at.place * t.out.token;
-    LaneAngles<T, INTER> angles;
-    if (a.R > 0) angles.load(a, h, at.table);
-    for (int head = first + team; head - team < last; head += kAhead * TEAMS) {
-      Raw<16> raw[kAhead][2];
+  int s = 0;
+  for (HeadWalk i = start; i.token < a.tokens; i.next()) {
+    issue(s == 0 ? kStages - 1 : s - 1);
+    cp_async_wait<kStages - 1>();
+    const uint32_t stage = stages + s * Stage::BYTES;
+    const TokenAt at(a, (uint32_t)i.token);
+    const int first = i.part * HEADS * TEAMS + team;
+    T* out = (T*)t.out.p + at.batch * t.out.batch + at.place * t.out.token + first * t.out.head;
+    Raw<16> raw[HEADS][2];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        head_load<T>(raw[k], h, t.x.p, from + (int64_t)(head + k * TEAMS) * t.x.head, head + k * TEAMS < last);
-      float r[kAhead];
-      if constexpr (NORM) {
-        // the sums of all heads first; each lane then finds the r of one of them
-        float mine = 0.0f;
+    for (int k = 0; k < HEADS; ++k)
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          F2 sum = f2(0.0f, 0.0f);
+      for (int j = 0; j < 2; ++j) raw[k][j] = lds16(Stage::granule(stage, lane, 0, k, j));
+    LaneAngles<T, TEAM, INTER, 1> angles;
+    if (a.R > 0) angles.load(stage, lane, a.inverse);
+    float r[HEADS];
+    if constexpr (NORM) {
+      // the sums of all heads first; each lane then finds the r of one of them
+      float mine = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            F2 x[P];
-            Granule<T>::widen(raw[k][j], x);
-#pragma unroll
-            for (int i = 0; i < P; ++i) sum = f2_fma(x[i], x[i], sum);
-          }
-          const float total = lanes_sum<TEAM>(__fadd_rn(sum.x, sum.y));
-          if (TEAM < kAhead || lane % kAhead == k) mine = total;
-          if constexpr (TEAM < kAhead) r[k] = inverse_rms(mine, a.inv_d, a.eps);
-        }
-        if constexpr (TEAM >= kAhead) {
-          mine = inverse_rms(mine, a.inv_d, a.eps);
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k) r[k] = __shfl_sync(0xFFFFFFFFu, mine, lane / kAhead * kAhead + k);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        F2 x[2][P];
+      for (int k = 0; k < HEADS; ++k) {
+        F2 sum = f2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          Granule<T>::widen(raw[k][j], x[j]);
-          if constexpr (NORM) {
+          F2 x[P];
+          Granule<T>::widen(raw[k][j], x);
 #pragma unroll
-            for (int i = 0; i < P; ++i) x[j][i] = f2_mul(f2_mul(x[j][i], f2(r[k], r[k])), w[j][i]);
-          }
+          for (int n = 0; n < P; ++n) sum = f2_fma(x[n], x[n], sum);
         }
-        if (a.R > 0) angles.template turn<ALL>(x, h);
-        if (head + k * TEAMS < last) {
-          T* out = (T*)t.out.p + to + (int64_t)(head + k * TEAMS) * t.out.head;
+        const float total = lanes_sum<TEAM>(__fadd_rn(sum.x, sum.y));
+        if (lane % HEADS == k) mine = total;
+      }
+      mine = inverse_rms(mine, a.inv_d, a.eps);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (h.on[j]) st_stream<16>(out + h.column[j], Granule<T>::narrow(x[j]));
+      for (int k = 0; k < HEADS; ++k) r[k] = __shfl_sync(0xFFFFFFFFu, mine, lane / HEADS * HEADS + k);
+    }
+#pragma unroll
+    for (int k = 0; k < HEADS; ++k) {
+      F2 x[2][P];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        Granule<T>::widen(raw[k][j], x[j]);
+        if constexpr (NORM) {
+#pragma unroll
+          for (int n = 0; n < P; ++n) x[j][n] = f2_mul(f2_mul(x[j][n], f2(r[k], r[k])), w[j][n]);
         }
       }
+      if (a.R > 0) angles.template turn<ALL>(x, h);
+      if (first + k * TEAMS < t.H) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (h.on[j]) st_stream<16>(out + h.column[j], Granule<T>::narrow(x[j]));
+      }
+      out += TEAMS * t.out.head;
     }
+    s = s + 1 == kStages ? 0 : s + 1;
   }
+  cp_async_wait<0>();  // no copy may outlive the CTA's shared memory
 }
 
 template <class T, int TEAM, bool NORM, bool INTER>
 cudaError_t launch_heads(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {
-  const auto kern = 2 * a.R == a.D ? rope_heads_kernel<T, TEAM, NORM, INTER, true>
-                                   : rope_heads_kernel<T, TEAM, NORM, INTER, false>;
-  const RopeHeads h{a, head_blocks(dev, a, 32 / TEAM, kAhead)};
-  const int64_t warps = kRowThreads / 32;
-  return launch_after(kern, dim3((unsigned)((a.tokens + warps - 1) / warps), h.b.blocks[0] + h.b.blocks[1]), kRowThreads,
-                      0, s, h);
+  using Stage = HeadStage<T, TEAM, INTER, 1>;
+  const bool all = 2 * a.R == a.D;
+  const auto kern = all ? rope_heads_kernel<T, TEAM, NORM, INTER, true> : rope_heads_kernel<T, TEAM, NORM, INTER, false>;
+  static std::atomic<int> opted[2][kOptinDevices];
+  const cudaError_t e = allow_shared((const void*)kern, dev, opted[all]);
+  if (e != cudaSuccess) return e;
+  constexpr int warps = kRowThreads / 32;
+  const size_t smem = (size_t)warps * kStages * Stage::BYTES;
+  const int64_t most = (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kRowThreads, smem);
+  const RopeHeads h{a, head_grid(a, Stage::HEADS * Stage::TEAMS, warps, most)};
+  return launch_after(kern, (unsigned)(h.g.ctas[0] + h.g.ctas[1]), kRowThreads, smem, s, h);
 }
 template <class T, int TEAM>
 cudaError_t launch_heads(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {

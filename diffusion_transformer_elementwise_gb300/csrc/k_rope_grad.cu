@@ -85,85 +85,99 @@ __global__ void __launch_bounds__(kRowThreads) rope_grad_kernel(const __grid_con
   }
 }
 
-// Heads in granules.  A CTA has heads of the queries or of the keys alone, and tokens with a stride, so that a
-// lane adds up its columns' part of one weight's gradient in registers.
-constexpr int kAhead = 1;
+// Heads in granules: a warp's items one after the other, the next kStages - 1 on their way.  A CTA has heads of the
+// queries or of the keys alone, so that a lane adds up its columns' part of one weight's gradient in registers.
+constexpr int kStages = 2;
 
 struct GradHeads {
   RopeArgs a;
-  HeadBlocks b;
+  HeadGrid g;
 };
 template <class T, int TEAM, bool INTER, bool ALL>
-__global__ void __launch_bounds__(kRowThreads, 2) rope_grad_heads_kernel(const __grid_constant__ GradHeads args) {
-  constexpr int P = HeadLane<T>::P, TEAMS = 32 / TEAM;
-  extern __shared__ float sums[];  // [warps][D]
+__global__ void __launch_bounds__(kRowThreads) rope_grad_heads_kernel(const __grid_constant__ GradHeads args) {
+  using Stage = HeadStage<T, TEAM, INTER, 2>;
+  constexpr int P = HeadLane<T>::P, TEAMS = Stage::TEAMS, HEADS = Stage::HEADS;
+  extern __shared__ __align__(16) unsigned char space[];
   const RopeArgs& a = args.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = lane / TEAM;
-  const int which = (int)blockIdx.y >= args.b.blocks[0];
+  const int which = (int)blockIdx.x >= args.g.ctas[0], cta = which ? blockIdx.x - args.g.ctas[0] : blockIdx.x;
   const RopeTensor& t = a.t[which];
-  const int first = ((int)blockIdx.y - (which ? args.b.blocks[0] : 0)) * args.b.heads;
-  const int last = min(first + args.b.heads, t.H);
   const HeadLane<T> h(a, lane % TEAM);
+  const uint32_t stages = smem_addr(space) + warp * kStages * Stage::BYTES;
   after_previous();
   let_next();
+  const HeadWalk start(args.g, which, (int64_t)cta * kRowWarps + warp, (int64_t)args.g.ctas[which] * kRowWarps);
+  HeadWalk ahead = start;
+  auto issue = [&](int s) {
+    if (ahead.token < a.tokens) {
+      const TokenAt at(a, (uint32_t)ahead.token);
+      const uint32_t stage = stages + s * Stage::BYTES;
+      const int first = ahead.part * HEADS * TEAMS + team;
+      Stage::copy_heads(stage, lane, h, 0, t.x.p, at.batch * t.x.batch + at.place * t.x.token, t.x.head, first, t.H);
+      Stage::copy_heads(stage, lane, h, 1, t.g.p, at.batch * t.g.batch + at.place * t.g.token, t.g.head, first, t.H);
+      Stage::copy_angles(stage, lane, h, a, at.table);
+      ahead.next();
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) issue(s);
   F2 w[2][P], acc[2][P];
   head_weight<T>(w, h, t.w, a.offset);
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int i = 0; i < P; ++i) acc[j][i] = f2(0.0f, 0.0f);
-  const uint32_t stride = gridDim.x * kRowWarps;
-  for (uint32_t token = blockIdx.x * kRowWarps + warp; token < a.tokens; token += stride) {
-    const TokenAt at(a, token);
-    const int64_t from = at.batch * t.x.batch + at.place * t.x.token;
-    const int64_t grad = at.batch * t.g.batch + at.place * t.g.token;
-    const int64_t to = at.batch * t.out.batch + at.place * t.out.token;
-    LaneAngles<T, INTER> angles;
-    if (a.R > 0) angles.load(a, h, at.table);  // (a.inverse is set: the gradient is turned back)
-    for (int head = first + team; head - team < last; head += kAhead * TEAMS) {
-      Raw<16> rx[kAhead][2], rg[kAhead][2];
+  int s = 0;
+  for (HeadWalk i = start; i.token < a.tokens; i.next()) {
+    issue(s == 0 ? kStages - 1 : s - 1);
+    cp_async_wait<kStages - 1>();
+    const uint32_t stage = stages + s * Stage::BYTES;
+    const TokenAt at(a, (uint32_t)i.token);
+    const int first = i.part * HEADS * TEAMS + team;
+    T* out = (T*)t.out.p + at.batch * t.out.batch + at.place * t.out.token + first * t.out.head;
+    LaneAngles<T, TEAM, INTER, 2> angles;
+    if (a.R > 0) angles.load(stage, lane, true);  // the gradient is turned back
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const bool on = head + k * TEAMS < last;
-        head_load<T>(rx[k], h, t.x.p, from + (int64_t)(head + k * TEAMS) * t.x.head, on);
-        head_load<T>(rg[k], h, t.g.p, grad + (int64_t)(head + k * TEAMS) * t.g.head, on);
+    for (int k = 0; k < HEADS; ++k) {
+      // (a head that is not there holds zeros, and adds none)
+      F2 x[2][P], u[2][P];
+      F2 square = f2(0.0f, 0.0f), dot = f2(0.0f, 0.0f);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        Granule<T>::widen(lds16(Stage::granule(stage, lane, 0, k, j)), x[j]);
+        Granule<T>::widen(lds16(Stage::granule(stage, lane, 1, k, j)), u[j]);
       }
+      if (a.R > 0) angles.template turn<ALL>(u, h);
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        F2 x[2][P], u[2][P];
-        F2 square = f2(0.0f, 0.0f), dot = f2(0.0f, 0.0f);
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          Granule<T>::widen(rx[k][j], x[j]);
-          Granule<T>::widen(rg[k][j], u[j]);
+        for (int n = 0; n < P; ++n) {
+          square = f2_fma(x[j][n], x[j][n], square);
+          dot = f2_fma(f2_mul(u[j][n], w[j][n]), x[j][n], dot);
         }
-        if (a.R > 0) angles.template turn<ALL>(u, h);
+      const float r = inverse_rms(lanes_sum<TEAM>(__fadd_rn(square.x, square.y)), a.inv_d, a.eps);
+      const float mean = __fmul_rn(__fmul_rn(lanes_sum<TEAM>(__fadd_rn(dot.x, dot.y)), r), a.inv_d);
+      const bool on = first + k * TEAMS < t.H;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j) {
+        F2 y[P];
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            square = f2_fma(x[j][i], x[j][i], square);
-            dot = f2_fma(f2_mul(u[j][i], w[j][i]), x[j][i], dot);
-          }
-        const float r = inverse_rms(lanes_sum<TEAM>(__fadd_rn(square.x, square.y)), a.inv_d, a.eps);
-        const float mean = __fmul_rn(__fmul_rn(lanes_sum<TEAM>(__fadd_rn(dot.x, dot.y)), r), a.inv_d);
-        const bool on = head + k * TEAMS < last;
-        T* out = (T*)t.out.p + to + (int64_t)(head + k * TEAMS) * t.out.head;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          F2 y[P];
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const F2 n = f2_mul(x[j][i], f2(r, r));
-            if (on) acc[j][i] = f2_fma(u[j][i], n, acc[j][i]);
-            y[i] = f2_mul(f2_fma(n, f2(-mean, -mean), f2_mul(u[j][i], w[j][i])), f2(r, r));
-          }
-          if (on && h.on[j]) st_stream<16>(out + h.column[j], Granule<T>::narrow(y));
+        for (int n = 0; n < P; ++n) {
+          const F2 v = f2_mul(x[j][n], f2(r, r));
+          if (on) acc[j][n] = f2_fma(u[j][n], v, acc[j][n]);
+          y[n] = f2_mul(f2_fma(v, f2(-mean, -mean), f2_mul(u[j][n], w[j][n])), f2(r, r));
         }
+        if (on && h.on[j]) st_stream<16>(out + h.column[j], Granule<T>::narrow(y));
       }
+      out += TEAMS * t.out.head;
     }
+    s = s + 1 == kStages ? 0 : s + 1;
   }
+  cp_async_wait<0>();
   if (!a.partial) return;
+  __syncthreads();  // the stages become the warps' sums, [warps][D]
+  float* sums = (float*)space;
   // the warp's teams, then the CTA's warps, in order
 #pragma unroll
   for (int j = 0; j < 2; ++j)
@@ -177,7 +191,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) rope_grad_heads_kernel(const _
       if (team == 0 && h.on[j]) *(float2*)(sums + warp * a.D + h.column[j] + 2 * i) = acc[j][i];
     }
   __syncthreads();
-  float* out = a.partial + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * a.D;
+  float* out = a.partial + (int64_t)blockIdx.x * a.D;
   for (int c = threadIdx.x; c < a.D; c += kRowThreads) {
     float v = 0.0f;
 #pragma unroll
@@ -216,25 +230,26 @@ __global__ void __launch_bounds__(1024) join_kernel(const __grid_constant__ Join
 }
 
 // split, rows: the partial rows written
+template <class T, int TEAM, bool INTER>
+cudaError_t launch_heads(const DeviceInfo& dev, const RopeArgs& a, int* split, int* rows, cudaStream_t s) {
+  using Stage = HeadStage<T, TEAM, INTER, 2>;
+  const bool all = 2 * a.R == a.D;
+  const auto kern = all ? rope_grad_heads_kernel<T, TEAM, INTER, true> : rope_grad_heads_kernel<T, TEAM, INTER, false>;
+  static std::atomic<int> opted[2][kOptinDevices];
+  const cudaError_t e = allow_shared((const void*)kern, dev, opted[all]);
+  if (e != cudaSuccess) return e;
+  static_assert(Stage::BYTES * kStages >= 32 / Stage::TEAMS * 2 * 16 / (int)sizeof(T) * 4, "room for a warp's sums");
+  const size_t smem = (size_t)kRowWarps * kStages * Stage::BYTES;
+  const int64_t most = std::min(2 * kRopeGradMaxCtas, (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kRowThreads, smem));
+  const GradHeads g{a, head_grid(a, Stage::HEADS * Stage::TEAMS, kRowWarps, most)};
+  *split = g.g.ctas[0];
+  *rows = g.g.ctas[0] + g.g.ctas[1];
+  return launch_after(kern, (unsigned)*rows, kRowThreads, smem, s, g);
+}
 template <class T, int TEAM>
 cudaError_t launch_heads(const DeviceInfo& dev, const RopeArgs& a, int* split, int* rows, cudaStream_t s) {
-  const bool all = 2 * a.R == a.D;
-  const auto kern = a.interleaved ? (all ? rope_grad_heads_kernel<T, TEAM, true, true> : rope_grad_heads_kernel<T, TEAM, true, false>)
-                                  : (all ? rope_grad_heads_kernel<T, TEAM, false, true> : rope_grad_heads_kernel<T, TEAM, false, false>);
-  GradHeads g{a, head_blocks(dev, a, 32 / TEAM, kAhead)};
-  // (the workspace has room for so many partial rows)
-  const int64_t limit = 2 * kRopeGradMaxCtas;
-  while (g.b.blocks[0] + g.b.blocks[1] > limit) {
-    g.b.heads *= 2;
-    for (int i = 0; i < 2; ++i) g.b.blocks[i] = (a.t[i].H + g.b.heads - 1) / g.b.heads;
-  }
-  const int blocks = g.b.blocks[0] + g.b.blocks[1];
-  const size_t smem = (size_t)kRowWarps * a.D * 4;
-  const int64_t resident = (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kRowThreads, smem);
-  const int64_t x = std::max<int64_t>(1, std::min({resident / blocks, limit / blocks, (a.tokens + kRowWarps - 1) / kRowWarps}));
-  *split = (int)x * g.b.blocks[0];
-  *rows = (int)x * blocks;
-  return launch_after(kern, dim3((unsigned)x, blocks), kRowThreads, smem, s, g);
+  return a.interleaved ? launch_heads<T, TEAM, true>(dev, a, split, rows, s)
+                       : launch_heads<T, TEAM, false>(dev, a, split, rows, s);
 }
 
 template <class T>
