@@ -139,24 +139,28 @@ struct HeadLane {
   }
 };
 
-// The copies of one item of work, a token's next HEADS heads of each team: for each lane its granules of NT tensors
-// and the angles of its columns, each to a place of its own in shared memory that no other lane reads.
+// The copies of one item of work, a token's next HEADS heads of each team: for each lane its granules of NT tensors,
+// each to a place of its own in shared memory that no other lane reads, and the angles, which the teams
+// copy a share of each.
 template <class T, int TEAM, bool INTER, int NT>
 struct HeadStage {
   using Lane = HeadLane<T>;
   static constexpr int TEAMS = 32 / TEAM;
-  static constexpr int HEADS = NT == 1 ? 4 : 2;
+  #ifndef HEADS1
+#define HEADS1 4
+#endif
+  static constexpr int HEADS = NT == 1 ? HEADS1 : 2;
   static constexpr int GRANULES = HEADS * NT * 2;
   // angles: cosines and sines of PER columns (both granules'), or of PER / 2 pairs for each granule
   static constexpr int AB = INTER && sizeof(T) == 4 ? 8 : 16;  // bytes of a piece
   static constexpr int AN = INTER ? 2 : Lane::PER * 4 / 16;    // pieces of cosines
-  static constexpr int BYTES = 32 * (GRANULES * 16 + 2 * AN * AB);
+  static constexpr int BYTES = 32 * GRANULES * 16 + TEAM * 2 * AN * AB;
 
   __device__ __forceinline__ static uint32_t granule(uint32_t stage, int lane, int tensor, int head, int j) {
     return stage + (((tensor * HEADS + head) * 2 + j) * 32 + lane) * 16;
   }
   __device__ __forceinline__ static uint32_t angle(uint32_t stage, int lane, int i) {
-    return stage + GRANULES * 512 + (i * 32 + lane) * AB;
+    return stage + GRANULES * 512 + (i * TEAM + lane % TEAM) * AB;
   }
   // tensor[at + head k stride]: heads [first, last)
   __device__ __forceinline__ static void copy_heads(uint32_t stage, int lane, const Lane& h, int tensor, const void* p,
@@ -177,10 +181,13 @@ struct HeadStage {
                                                      int64_t row) {
     if (a.R == 0) return;
 #pragma unroll
-    for (int i = 0; i < 2 * AN; ++i) {
+    for (int n = 0; n < 2 * AN; n += TEAMS) {
+      const int i = n + lane / TEAM;  // the team's piece
+      if (TEAMS > 2 * AN && i >= 2 * AN) break;
       const int k = INTER ? i % AN : 0;
-      const bool any = h.on[k] && h.turn[k];
-      const float* from = (i < AN ? a.cos : a.sin) + (any ? row * a.R + (INTER ? h.column[k] / 2 : h.column[0] + i % AN * 4) : 0);
+      const bool any = k ? h.on[1] && h.turn[1] : h.on[0] && h.turn[0];
+      const int column = k ? h.column[1] : h.column[0];
+      const float* from = (i < AN ? a.cos : a.sin) + (any ? row * a.R + (INTER ? column / 2 : column + i % AN * 4) : 0);
       if constexpr (AB == 16)
         cp_async16_part(angle(stage, lane, i), from, any ? 16 : 0);
       else
@@ -302,26 +309,33 @@ struct TokenAt {
   }
 };
 
-// scale and factors to codes of a row whose largest magnitude is m: codes of x are
-// e4m3(fl(x (mul + low))), 448 / m as two fp32 numbers.  Rows so small that
-// 448 / m would overflow are scaled up first (small).  m not finite: all NaN.
+// Scale and factors to codes of a row whose largest magnitude is m: scale = fl(m / 448), and codes of x are
+// e4m3(fl(x (mul + low))), 448 / m as two fp32 numbers: an approximate reciprocal and what it leaves of 448.  Rows
+// so small or large that such steps would leave fp32 are scaled first (by `by`).  m not finite: all NaN.
 struct RowQuant {
-  float mul, low, small, scale;
+  float mul, low, by, scale;
 };
 __device__ __forceinline__ RowQuant row_quant(float m) {
   constexpr float most = 448.0f;
   RowQuant q;
-  q.small = m < 0x1p-60f ? 0x1p64f : 1.0f;
-  const float v = __fmul_rn(m, q.small);
-  const bool zero = m == 0.0f;
-  q.mul = zero ? 0.0f : __fdiv_rn(most, v);
-  q.low = zero ? 0.0f : __fdiv_rn(__fmaf_rn(-q.mul, v, most), v);
-  q.scale = __fdiv_rn(m, most);
+  const bool usable = m >= 0x1p-100f && m <= 0x1p100f;
+  q.by = usable ? 1.0f : m < 1.0f ? 0x1p64f : 0x1p-64f;
+  const float v = __fmul_rn(m, q.by);
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(m == 0.0f ? 1.0f : v));
+  q.mul = m == 0.0f ? 0.0f : __fmul_rn(most, y);
+  q.low = m == 0.0f ? 0.0f : __fmul_rn(__fmaf_rn(-q.mul, v, most), y);
+  if (usable) {  // the quotient by a rounded reciprocal, corrected by its remainder
+    const float part = __fmul_rn(m, 1.0f / most);
+    q.scale = __fmaf_rn(__fmaf_rn(-part, most, m), 1.0f / most, part);
+  } else {
+    q.scale = __fdiv_rn(m, most);
+  }
   if (!isfinite(m)) q.mul = q.low = q.scale = __int_as_float(0x7FC00000);
   return q;
 }
 __device__ __forceinline__ float code_value(float x, const RowQuant& q) {
-  const float v = __fmul_rn(x, q.small);
+  const float v = __fmul_rn(x, q.by);
   return __fmaf_rn(v, q.mul, __fmul_rn(v, q.low));
 }
 

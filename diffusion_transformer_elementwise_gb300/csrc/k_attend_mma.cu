@@ -113,7 +113,7 @@ struct Shape {
   static constexpr int EXTRA = FP8 ? 256 : 128;
   static constexpr int WARPS = ROW <= 128 && NB == 1 ? 16 : ROW <= 256 ? 8 : 4;
   static constexpr int THREADS = 32 * WARPS;
-  static constexpr int FIT = (226 * 1024) / (WARPS * (STAGE + EXTRA));
+  static constexpr int FIT = (220 * 1024) / (WARPS * (STAGE + EXTRA));
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int SMEM = STAGES * WARPS * (STAGE + EXTRA);
   static_assert(STAGES >= 2, "a stage in flight and one in use");

@@ -93,157 +93,186 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
   }
 }
 
-// Rows in 16-byte granules: a team of TEAM lanes has a row, a lane granules l and l + TEAM of it; a warp
-// takes kAhead rows of each team at once, which are consecutive: a token's keys, its values, the next token's keys.
-constexpr int kAhead = 4;
-
+// Rows in 16-byte granules.  A team of TEAM lanes has a row, a lane granules l and l + TEAM of it.  `abreast` of a
+// warp's teams (a power of two, at most the heads) have the heads of one token, the others the next tokens'; so a
+// team finds its token's places once, and goes on from head to head, keys and values both (BOTH; else one of them,
+// for few tokens: twice the warps).
 struct CacheRows {
   CacheArgs a;
-  Divisor rows, page;  // 2 heads, page_size
-  int64_t items;
+  Divisor page;        // page_size
+  int abreast;
+  int64_t items;       // of 32 / TEAM / abreast tokens
 };
-// The row `local` rows behind row `part` of token `token`.
-struct RowAt {
-  int which, head;
-  int64_t token, page, place;
+// A team's token: its rows of keys [0] and values [1] and their places in the cache (ES bytes an element there).
+template <class T, int ES>
+struct CacheToken {
+  const char* row[2];
+  char* cached[2];
+  int64_t scale;
   bool on, inside;
-  __device__ __forceinline__ RowAt(const CacheRows& c, int64_t token0, int part, int local) {
-    const uint32_t r = part + local, q = quotient(r, c.rows);
-    token = token0 + q;
-    head = (int)(r - q * c.rows.d);
-    which = head >= (int)c.a.c.heads;
-    if (which) head -= (int)c.a.c.heads;
-    on = token < c.a.tokens;
-    const int64_t slot = on ? id_at(c.a.slots, token, c.a.ids64) : -1;
-    inside = slot >= 0 && slot < c.a.c.pages * c.a.c.page_size;
-    page = inside ? quotient((uint32_t)slot, c.page) : 0;
-    place = inside ? slot - page * c.page.d : 0;
-  }
-  // granule 0 of the row in the cache (ES bytes an element), its scale, and its granule 0 among the tokens'
-  template <int ES>
-  __device__ __forceinline__ char* cached(const dit_cache& c) const {
-    return (char*)(which ? c.v : c.k) + (page * c.page_stride + ((int64_t)head * c.page_size + place) * c.D) * ES;
-  }
-  __device__ __forceinline__ float* scale(const dit_cache& c) const {
-    return (which ? c.v_scales : c.k_scales) + page * c.scale_stride + (int64_t)head * c.page_size + place;
-  }
-  template <int ES>
-  __device__ __forceinline__ char* row(const CacheArgs& a) const {
-    const dit_heads& t = which ? a.v : a.k;
-    return (char*)t.p + (token * t.token + head * t.head) * ES;
+  __device__ __forceinline__ CacheToken(const CacheRows& c, int64_t token, int head) {
+    const CacheArgs& a = c.a;
+    on = token < a.tokens;
+    if (!on) token = 0;
+    const int64_t slot = on ? id_at(a.slots, token, a.ids64) : -1;
+    inside = slot >= 0 && slot < a.c.pages * a.c.page_size;
+    const uint32_t page = inside ? quotient((uint32_t)slot, c.page) : 0;
+    const uint32_t place = inside ? (uint32_t)slot - page * c.page.d : 0;
+    const int64_t in_page = (int64_t)head * a.c.page_size + place;
+    scale = page * a.c.scale_stride + in_page;
+    const int64_t at = (page * a.c.page_stride + in_page * a.c.D) * ES;
+    cached[0] = (char*)a.c.k + at;
+    cached[1] = (char*)a.c.v + at;
+    row[0] = (const char*)a.k.p + (token * a.k.token + head * a.k.head) * (int)sizeof(T);
+    row[1] = (const char*)a.v.p + (token * a.v.token + head * a.v.head) * (int)sizeof(T);
   }
 };
+constexpr int kHeads = 2;  // heads of a lane at once, beside keys and values
 
-template <class T, int TEAM, bool FP8>
+template <class T, int TEAM, bool FP8, bool BOTH>
 __global__ void __launch_bounds__(kThreads) write_rows_kernel(const __grid_constant__ CacheRows args) {
   constexpr int ES = (int)sizeof(T), PER = 16 / ES, P = PER / 2, TEAMS = 32 / TEAM;
+  constexpr int CES = FP8 ? 1 : ES, N = BOTH ? 2 : 1;
   const CacheArgs& a = args.a;
   const int lane = threadIdx.x & 31, team = lane / TEAM, l = lane % TEAM, n = (int)a.c.D / PER;
+  const int heads = (int)a.c.heads, abreast = args.abreast;
+  const int64_t head_bytes = a.c.page_size * a.c.D * CES * abreast;
+  const int64_t step[2] = {a.k.head * ES * abreast, a.v.head * ES * abreast};
   after_previous();
   let_next();
   const int64_t stride = (int64_t)gridDim.x * (kThreads / 32);
   for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < args.items; i += stride) {
-    const int64_t token0 = i * (kAhead * TEAMS) / args.rows.d;
-    const int part = (int)(i * (kAhead * TEAMS) - token0 * args.rows.d);
-    Raw<16> raw[kAhead][2];
+    const int64_t group = BOTH ? i : i >> 1;
+    const int only = BOTH ? 0 : (int)(i & 1);
+    int head = team & (abreast - 1);
+    CacheToken<T, CES> t(args, group * (TEAMS / abreast) + team / abreast, head);
+    for (int h0 = 0; h0 < heads; h0 += kHeads * abreast) {
+      Raw<16> raw[kHeads][N][2];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const RowAt row(args, token0, part, k * TEAMS + team);
-      const char* x = row.row<ES>(a);
+      for (int h = 0; h < kHeads; ++h)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        raw[k][j] = Raw<16>{};
-        if (row.inside && l + j * TEAM < n) raw[k][j] = ld_stream<16>(x + (l + j * TEAM) * 16);
-      }
-    }
+        for (int w = 0; w < N; ++w) {
+          const int which = BOTH ? w : only;
+          const char* x = (which ? t.row[1] : t.row[0]) + h * step[which];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const RowAt row(args, token0, part, k * TEAMS + team);
-      if constexpr (FP8) {
-        F2 x[2][P];
-        float m = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          Granule<T>::widen(raw[k][j], x[j]);
-#pragma unroll
-          for (int e = 0; e < P; ++e) m = max_abs3(m, x[j][e].x, x[j][e].y);
-        }
-        const RowQuant q = row_quant(lanes_max<TEAM>(m));
-        if (!row.inside) continue;
-        char* out = row.cached<1>(a.c);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          Raw<PER> codes;
-#pragma unroll
-          for (int e = 0; e < P / 2; ++e) {
-            F2 v[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const F2 y = f2_mul(x[j][2 * e + h], f2(q.small, q.small));
-              v[h] = f2_fma(y, f2(q.mul, q.mul), f2_mul(y, f2(q.low, q.low)));
-            }
-            codes.w[e] = e4m3x2(v[0]) | e4m3x2(v[1]) << 16;
+          for (int j = 0; j < 2; ++j) {
+            raw[h][w][j] = Raw<16>{};
+            if (t.inside && head + h * abreast < heads && l + j * TEAM < n) raw[h][w][j] = ld_stream<16>(x + (l + j * TEAM) * 16);
           }
-          if (l + j * TEAM < n) st_stream<PER>(out + (l + j * TEAM) * PER, codes);
         }
-        if (l == 0) *row.scale(a.c) = q.scale;
-      } else {
-        if (!row.inside) continue;
-        char* out = row.cached<ES>(a.c);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (l + j * TEAM < n) st_stream<16>(out + (l + j * TEAM) * 16, raw[k][j]);
-      }
+      for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+        for (int w = 0; w < N; ++w) {
+          const int which = BOTH ? w : only;
+          char* out = (which ? t.cached[1] : t.cached[0]) + h * head_bytes;
+          const bool on = t.inside && head + h * abreast < heads;
+          if constexpr (FP8) {
+            F2 x[2][P];
+            float m = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              Granule<T>::widen(raw[h][w][j], x[j]);
+#pragma unroll
+              for (int e = 0; e < P; ++e) m = max_abs3(m, x[j][e].x, x[j][e].y);
+            }
+            const RowQuant q = row_quant(lanes_max<TEAM>(m));
+            if (!on) continue;
+            const bool plain = q.by == 1.0f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              Raw<PER> codes;
+#pragma unroll
+              for (int e = 0; e < P / 2; ++e) {
+                F2 v[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  F2 y = x[j][2 * e + k];
+                  if (!plain) y = f2_mul(y, f2(q.by, q.by));
+                  v[k] = f2_fma(y, f2(q.mul, q.mul), f2_mul(y, f2(q.low, q.low)));
+                }
+                codes.w[e] = e4m3x2(v[0]) | e4m3x2(v[1]) << 16;
+              }
+              if (l + j * TEAM < n) st_stream<PER>(out + (l + j * TEAM) * PER, codes);
+            }
+            if (l == 0) (which ? a.c.v_scales : a.c.k_scales)[t.scale + (int64_t)h * a.c.page_size * abreast] = q.scale;
+          } else if (on) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (l + j * TEAM < n) st_stream<16>(out + (l + j * TEAM) * 16, raw[h][w][j]);
+          }
+        }
+      head += kHeads * abreast;
+      t.scale += kHeads * a.c.page_size * abreast;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) t.row[w] += kHeads * step[w], t.cached[w] += kHeads * head_bytes;
     }
   }
 }
 
-template <class T, int TEAM, bool FP8>
+template <class T, int TEAM, bool FP8, bool BOTH>
 __global__ void __launch_bounds__(kThreads) read_rows_kernel(const __grid_constant__ CacheRows args) {
   constexpr int ES = (int)sizeof(T), PER = 16 / ES, P = PER / 2, TEAMS = 32 / TEAM;
-  constexpr int CB = FP8 ? PER : 16;  // bytes of a granule's columns in the cache
+  constexpr int CES = FP8 ? 1 : ES, CB = FP8 ? PER : 16, N = BOTH ? 2 : 1;  // CB: bytes of a granule's columns in the cache
   const CacheArgs& a = args.a;
   const int lane = threadIdx.x & 31, team = lane / TEAM, l = lane % TEAM, n = (int)a.c.D / PER;
+  const int heads = (int)a.c.heads, abreast = args.abreast;
+  const int64_t head_bytes = a.c.page_size * a.c.D * CES * abreast;
+  const int64_t step[2] = {a.k.head * ES * abreast, a.v.head * ES * abreast};
   after_previous();
   let_next();
   const int64_t stride = (int64_t)gridDim.x * (kThreads / 32);
   for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < args.items; i += stride) {
-    const int64_t token0 = i * (kAhead * TEAMS) / args.rows.d;
-    const int part = (int)(i * (kAhead * TEAMS) - token0 * args.rows.d);
-    Raw<CB> raw[kAhead][2];
-    float scale[kAhead];
+    const int64_t group = BOTH ? i : i >> 1;
+    const int only = BOTH ? 0 : (int)(i & 1);
+    int head = team & (abreast - 1);
+    CacheToken<T, CES> t(args, group * (TEAMS / abreast) + team / abreast, head);
+    for (int h0 = 0; h0 < heads; h0 += kHeads * abreast) {
+      Raw<CB> raw[kHeads][N][2];
+      float scale[kHeads][N];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const RowAt row(args, token0, part, k * TEAMS + team);
-      const char* x = row.cached<FP8 ? 1 : ES>(a.c);
+      for (int h = 0; h < kHeads; ++h)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        raw[k][j] = Raw<CB>{};
-        if (row.inside && l + j * TEAM < n) raw[k][j] = ld_stream<CB>(x + (l + j * TEAM) * CB);
-      }
-      if constexpr (FP8) scale[k] = row.inside ? *row.scale(a.c) : 0.0f;
-    }
+        for (int w = 0; w < N; ++w) {
+          const int which = BOTH ? w : only;
+          const char* x = (which ? t.cached[1] : t.cached[0]) + h * head_bytes;
+          const bool on = t.inside && head + h * abreast < heads;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const RowAt row(args, token0, part, k * TEAMS + team);
-      if (!row.on) continue;
-      char* out = row.row<ES>(a);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        Raw<16> y;
-        if constexpr (FP8) {
-          F2 x[P];
-#pragma unroll
-          for (int e = 0; e < P; ++e) {
-            const float2 v = from_e4m3x2((uint16_t)(raw[k][j].w[e / 2] >> (16 * (e & 1))));
-            x[e] = f2_mul(v, f2(scale[k], scale[k]));
+          for (int j = 0; j < 2; ++j) {
+            raw[h][w][j] = Raw<CB>{};
+            if (on && l + j * TEAM < n) raw[h][w][j] = ld_stream<CB>(x + (l + j * TEAM) * CB);
           }
-          y = Granule<T>::narrow(x);
-        } else {
-          y = raw[k][j];
+          if constexpr (FP8)
+            scale[h][w] = on ? (which ? a.c.v_scales : a.c.k_scales)[t.scale + (int64_t)h * a.c.page_size * abreast] : 0.0f;
         }
-        if (l + j * TEAM < n) st_stream<16>(out + (l + j * TEAM) * 16, y);
-      }
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+        for (int w = 0; w < N; ++w) {
+          const int which = BOTH ? w : only;
+          if (!t.on || head + h * abreast >= heads) continue;
+          char* out = (char*)(which ? t.row[1] : t.row[0]) + h * step[which];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            Raw<16> y;
+            if constexpr (FP8) {
+              F2 x[P];
+#pragma unroll
+              for (int e = 0; e < P; ++e) {
+                const float2 v = from_e4m3x2((uint16_t)(raw[h][w][j].w[e / 2] >> (16 * (e & 1))));
+                x[e] = f2_mul(v, f2(scale[h][w], scale[h][w]));
+              }
+              y = Granule<T>::narrow(x);
+            } else {
+              y = raw[h][w][j];
+            }
+            if (l + j * TEAM < n) st_stream<16>(out + (l + j * TEAM) * 16, y);
+          }
+        }
+      head += kHeads * abreast;
+      t.scale += kHeads * a.c.page_size * abreast;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) t.row[w] += kHeads * step[w], t.cached[w] += kHeads * head_bytes;
     }
   }
 }
@@ -258,11 +287,17 @@ template <class T, bool FP8>
 cudaError_t launch(const DeviceInfo& dev, bool write, const CacheArgs& a, cudaStream_t s) {
   const int64_t rows = a.tokens * 2 * a.c.heads, half = (a.c.D * (int)sizeof(T) / 16 + 1) / 2;
   if (!a.granules || half > 32) return launch(dev, write ? write_kernel<T, FP8> : read_kernel<T, FP8>, rows, a, s);
-  CacheRows c{a, divisor((uint32_t)(2 * a.c.heads)), divisor((uint32_t)a.c.page_size), 0};
+  CacheRows c{a, divisor((uint32_t)a.c.page_size), 1, 0};
   auto team = [&](auto lanes) {
-    constexpr int TEAM = decltype(lanes)::value;
-    c.items = (rows + kAhead * 32 / TEAM - 1) / (kAhead * 32 / TEAM);
-    return launch(dev, write ? write_rows_kernel<T, TEAM, FP8> : read_rows_kernel<T, TEAM, FP8>, c.items, c, s);
+    constexpr int TEAM = decltype(lanes)::value, TEAMS = 32 / TEAM;
+    while (c.abreast * 2 <= std::min<int64_t>(TEAMS, a.c.heads)) c.abreast *= 2;
+    const int64_t tokens = TEAMS / c.abreast;
+    c.items = (a.tokens + tokens - 1) / tokens;
+    const bool both = c.items >= (int64_t)dev.sm_count * 16;
+    if (!both) c.items *= 2;
+    const auto kern = write ? (both ? write_rows_kernel<T, TEAM, FP8, true> : write_rows_kernel<T, TEAM, FP8, false>)
+                            : (both ? read_rows_kernel<T, TEAM, FP8, true> : read_rows_kernel<T, TEAM, FP8, false>);
+    return launch(dev, kern, c.items, c, s);
   };
   return half <= 4    ? team(std::integral_constant<int, 4>{})
          : half <= 8  ? team(std::integral_constant<int, 8>{})

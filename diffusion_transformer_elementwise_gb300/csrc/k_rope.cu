@@ -138,14 +138,18 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const __grid_constant
 }
 
 // Heads in granules: a warp's items one after the other, the next kStages - 1 on their way.
-constexpr int kStages = 3;
+#ifndef STAGES
+#define STAGES 2
+#define MINB 2
+#endif
+constexpr int kStages = STAGES;
 
 struct RopeHeads {
   RopeArgs a;
   HeadGrid g;
 };
 template <class T, int TEAM, bool NORM, bool INTER, bool ALL>
-__global__ void __launch_bounds__(kRowThreads, 2) rope_heads_kernel(const __grid_constant__ RopeHeads args) {
+__global__ void __launch_bounds__(kRowThreads, MINB) rope_heads_kernel(const __grid_constant__ RopeHeads args) {
   using Stage = HeadStage<T, TEAM, INTER, 1>;
   constexpr int P = HeadLane<T>::P, TEAMS = Stage::TEAMS, HEADS = Stage::HEADS, WARPS = kRowThreads / 32;
   extern __shared__ __align__(16) unsigned char space[];
@@ -176,8 +180,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) rope_heads_kernel(const __grid
   if constexpr (NORM) head_weight<T>(w, h, t.w, a.offset);
   int s = 0;
   for (HeadWalk i = start; i.token < a.tokens; i.next()) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();  // every lane's copies are there, and every lane is done with the stage before
     issue(s == 0 ? kStages - 1 : s - 1);
-    cp_async_wait<kStages - 1>();
     const uint32_t stage = stages + s * Stage::BYTES;
     const TokenAt at(a, (uint32_t)i.token);
     const int first = i.part * HEADS * TEAMS + team;

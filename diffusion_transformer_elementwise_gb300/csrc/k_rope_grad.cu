@@ -94,7 +94,7 @@ struct GradHeads {
   HeadGrid g;
 };
 template <class T, int TEAM, bool INTER, bool ALL>
-__global__ void __launch_bounds__(kRowThreads) rope_grad_heads_kernel(const __grid_constant__ GradHeads args) {
+__global__ void __launch_bounds__(kRowThreads, 2) rope_grad_heads_kernel(const __grid_constant__ GradHeads args) {
   using Stage = HeadStage<T, TEAM, INTER, 2>;
   constexpr int P = HeadLane<T>::P, TEAMS = Stage::TEAMS, HEADS = Stage::HEADS;
   extern __shared__ __align__(16) unsigned char space[];
@@ -130,8 +130,9 @@ __global__ void __launch_bounds__(kRowThreads) rope_grad_heads_kernel(const __gr
     for (int i = 0; i < P; ++i) acc[j][i] = f2(0.0f, 0.0f);
   int s = 0;
   for (HeadWalk i = start; i.token < a.tokens; i.next()) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();  // every lane's copies are there, and every lane is done with the stage before
     issue(s == 0 ? kStages - 1 : s - 1);
-    cp_async_wait<kStages - 1>();
     const uint32_t stage = stages + s * Stage::BYTES;
     const TokenAt at(a, (uint32_t)i.token);
     const int first = i.part * HEADS * TEAMS + team;
