@@ -57,42 +57,51 @@ def declare(lib) -> None:
 # ---------------------------------------------------------------------------
 
 _SIZE = 32  # bytes of a dit_heads
-_HEADS = [ctypes.c_int64 * (4 * n) for n in range(7)]
+_WORDS = [ctypes.c_int64 * (4 * n) for n in range(7)]
+_addressof = ctypes.addressof
 
 
-def _heads(views):
-    """The dit_heads of [..., tokens, heads, D] tensors of 3 or 4 dimensions:
-    the array that holds them, and its address."""
+def _heads(dims, like, *views):
+    """The dit_heads of views ([..., tokens, heads, D], of `dims` dimensions, 3 or 4): (device index,
+    dtype code, their array, its address), after a check that they are CUDA tensors of one dtype
+    and device, with contiguous rows, and each of the shape of its entry in `like`.  The usual
+    case takes one pass; what is wrong is found out in a second (_refuse)."""
     words = []
-    for t in views:
-        s = t.stride()
-        words += (t.data_ptr(), s[0] if len(s) == 4 else 0, s[-3], s[-2])
-    array = _HEADS[len(views)](*words)
-    return array, ctypes.addressof(array)
+    try:
+        first = views[0]
+        dtype, dev = first.dtype, first.get_device()
+        ok = dev >= 0
+        for t, shape in zip(views, like):
+            stride = t.stride()
+            if (t.dtype is not dtype or t.get_device() != dev or t.shape != shape
+                    or len(stride) != dims or (stride[-1] != 1 and shape[-1] > 1)):
+                ok = False
+                break
+            words += (t.data_ptr(), stride[0] if dims == 4 else 0, stride[-3], stride[-2])
+        code = DTYPE_CODES[dtype] if ok else 0
+    except (AttributeError, KeyError, IndexError):
+        ok = False
+    if not ok:
+        return None
+    array = _WORDS[len(views)](*words)
+    return dev, code, array, _addressof(array)
 
 
-def _same_heads(ref, named, dims):
-    """Checks that the tensors of `named` (name, tensor, ...) are of ref's dtype and device, of one of
-    the numbers of dimensions `dims`, with contiguous rows.  Returns (device index, dtype code)."""
-    dtype, dev, n = ref.dtype, ref.get_device(), ref.dim()
-    ok = dev >= 0 and dtype in DTYPE_CODES and n in dims
-    if ok:
-        for t in named[1::2]:
-            ok = (ok and t.dtype is dtype and t.get_device() == dev and t.dim() == n
-                  and (t.stride(-1) == 1 or t.shape[-1] <= 1))
-    if ok:
-        return dev, DTYPE_CODES[dtype]
-    for name, t in zip(named[::2], named[1::2]):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
+def _refuse(dims, like, names, views):
+    """Raises what is wrong with the views of a _heads that returned None."""
+    for name, t in zip(names, views):
+        _tensor(t, name)
+    dev = views[0].get_device()
+    for name, t, shape in zip(names, views, like):
         if t.get_device() != dev:
             raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{dev}")
-        if t.dim() != n or n not in dims:
-            raise ValueError(f"{name} must have {' or '.join(map(str, dims))} dimensions, as the "
-                             f"others; got {t.dim()}")
+        _match(name, t, shape)
+        if t.dim() != dims:
+            raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
         if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError(f"the rows of {name} (its last dimension) must be contiguous")
-    return dev, _dtype(ref, *zip(named[::2], named[1::2]))
+    _dtype(views[0], *zip(names, views))
+    raise ValueError("tensors that do not go together")
 
 
 def _tensor(x, name):
@@ -106,54 +115,65 @@ def _match(name, t, shape):
 
 
 def _angles(cos, sin, B, L, dev):
-    """(R, rows) of a rotary table for B batches of L tokens."""
+    """(R, rows, addresses) of a rotary table for B batches of L tokens."""
     if cos is None and sin is None:
         return 0, B * L, None, None
-    _cuda(("cos", cos), ("sin", sin))
-    if cos.dtype is not torch.float32 or sin.dtype is not torch.float32:
-        raise TypeError("cos and sin must be float32")
-    if cos.shape != sin.shape or cos.dim() < 2:
-        raise ValueError("cos and sin must be [rows, R], of one shape")
-    if cos.get_device() != dev:
+    try:
+        shape = cos.shape
+        ok = (cos.dtype is torch.float32 and sin.dtype is torch.float32 and sin.shape == shape
+              and cos.get_device() == dev and sin.get_device() == dev and cos.is_contiguous()
+              and sin.is_contiguous() and len(shape) >= 2)
+    except AttributeError:
+        ok = False
+    if not ok:
+        _cuda(("cos", cos), ("sin", sin))
+        if cos.dtype is not torch.float32 or sin.dtype is not torch.float32:
+            raise TypeError("cos and sin must be float32")
+        if cos.shape != sin.shape or cos.dim() < 2:
+            raise ValueError("cos and sin must be [rows, R], of one shape")
         raise ValueError(f"cos is on cuda:{cos.get_device()}, expected cuda:{dev}")
-    R = cos.shape[-1]
-    rows = cos.numel() // R if R else B * L
+    R = shape[-1]
+    rows = (shape[0] if len(shape) == 2 else cos.numel() // R) if R else B * L
     if rows != L and rows != B * L:
         raise ValueError(f"cos and sin have {rows} rows, for {B} x {L} tokens")
     return R, rows, cos.data_ptr(), sin.data_ptr()
 
 
 def _shapes(q, k):
-    """(B, L, Hq, Hk, D) of queries and keys ([B, L, H, D], or [L, H, D])."""
-    _tensor(q, "q")
-    if q.dim() not in (3, 4):
+    """(B, L, Hq, Hk, D, dimensions, q's shape, k's shape) of queries and keys ([B, L, H, D], or
+    [L, H, D])."""
+    if not isinstance(q, torch.Tensor) or (k is not None and not isinstance(k, torch.Tensor)):
+        _tensor(q, "q")
+        _tensor(k, "k")
+    sq = q.shape
+    n = len(sq)
+    if n == 3:
+        B = 1
+        L, Hq, D = sq
+    elif n == 4:
+        B, L, Hq, D = sq
+    else:
+        _tensor(q, "q")
         raise ValueError("q must be [tokens, heads, D] or [B, L, heads, D]")
-    B, L, Hq, D = q.shape if q.dim() == 4 else (1, *q.shape)
     if k is None:
-        return B, L, Hq, 0, D
-    _tensor(k, "k")
-    if k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != D:
-        raise ValueError(f"k must be of q's shape but for its heads, got {tuple(k.shape)} for "
-                         f"{tuple(q.shape)}")
-    return B, L, Hq, k.shape[-2], D
+        return B, L, Hq, 0, D, n, sq, None
+    sk = k.shape
+    if len(sk) != n or sk[-1] != D or sk[:-2] != sq[:-2]:
+        _tensor(k, "k")
+        raise ValueError(f"k must be of q's shape but for its heads, got {tuple(sk)} for {tuple(sq)}")
+    return B, L, Hq, sk[-2], D, n, sq, sk
 
 
-def _out(given, name, like, stream):
-    if given is None:
-        return _empty(like.shape, like.dtype, like.device, stream)
-    _tensor(given, name)
-    _match(name, given, like.shape)
-    return given
-
-
-def _weight(w, name, D, ref):
-    if (not isinstance(w, torch.Tensor) or w.dtype is not ref.dtype
-            or w.get_device() != ref.get_device() or w.dim() != 1 or w.numel() != D
-            or not w.is_contiguous()):
-        _tensor(w, name)
-        raise ValueError(f"{name} must be a contiguous [{D}] {ref.dtype} tensor on {ref.device}, "
-                         f"got {tuple(w.shape)} {w.dtype} on {w.device}")
-    return w.data_ptr()
+def _weight(w, name, D, ref, dev):
+    try:
+        if (w.dtype is ref.dtype and w.get_device() == dev and w.shape == (D,)
+                and w.is_contiguous()):
+            return w.data_ptr()
+    except AttributeError:
+        pass
+    _tensor(w, name)
+    raise ValueError(f"{name} must be a contiguous [{D}] {ref.dtype} tensor on {ref.device}, got "
+                     f"{tuple(w.shape)} {w.dtype} on {w.device}")
 
 
 # ---------------------------------------------------------------------------
@@ -217,20 +237,24 @@ def rope(q, k, cos, sin, interleaved=False, inverse=False, out_q=None, out_k=Non
     interleaved, by row t of cos and sin ([B * L, R], or [L, R] for all batches);
     columns from 2R on are copied.  inverse=True turns back, which is the gradient.
     out_q may be q, out_k may be k.  Returns (out_q, out_k)."""
-    B, L, Hq, Hk, D = _shapes(q, k)
-    out_q = _out(out_q, "out_q", q, stream)
+    B, L, Hq, Hk, D, n, sq, sk = _shapes(q, k)
+    if out_q is None:
+        out_q = _empty(sq, q.dtype, q.device, stream)
     if k is None:
         if out_k is not None:
             raise ValueError("out_k without k")
-        views, named = (out_q, q), ("q", q, "out_q", out_q)
+        like, views = (sq, sq), (q, out_q)
     else:
-        out_k = _out(out_k, "out_k", k, stream)
-        views, named = (out_q, q, out_k, k), ("q", q, "out_q", out_q, "k", k, "out_k", out_k)
-    dev, dt = _same_heads(q, named, (3, 4))
+        if out_k is None:
+            out_k = _empty(sk, k.dtype, k.device, stream)
+        like, views = (sq, sq, sk, sk), (q, out_q, k, out_k)
+    found = _heads(n, like, *views)
+    if found is None:
+        _refuse(n, like, ("q", "out_q", "k", "out_k"), views)
+    dev, dt, _keep, at = found
     R, rows, pc, ps = _angles(cos, sin, B, L, dev)
-    _keep, at = _heads(views)
-    ko, ki = (at + 2 * _SIZE, at + 3 * _SIZE) if k is not None else (None, None)
-    _call(dev, library().dit_rope, "dit_rope", at, ko, at + _SIZE, ki, pc, ps, B, L, Hq, Hk, D, R,
+    kp, ko = (at + 2 * _SIZE, at + 3 * _SIZE) if k is not None else (None, None)
+    _call(dev, library().dit_rope, "dit_rope", at + _SIZE, ko, at, kp, pc, ps, B, L, Hq, Hk, D, R,
           rows, int(interleaved), int(inverse), dt, _stream(dev, stream))
     return out_q, out_k
 
@@ -240,22 +264,27 @@ def rmsnorm_rope(q, k, weight_q, weight_k, cos, sin, eps=1e-6, weight_offset=0.0
     """rope of the weighted RMSNorm of each head (over its D columns) in one pass: weight_q
     and weight_k are [D], weight_offset 1 for weights stored as their difference from one.
     cos=sin=None: the norm alone.  out_q may be q, out_k may be k.  Returns (out_q, out_k)."""
-    B, L, Hq, Hk, D = _shapes(q, k)
-    out_q = _out(out_q, "out_q", q, stream)
+    B, L, Hq, Hk, D, n, sq, sk = _shapes(q, k)
+    if out_q is None:
+        out_q = _empty(sq, q.dtype, q.device, stream)
     if k is None:
         if out_k is not None or weight_k is not None:
             raise ValueError("out_k or weight_k without k")
-        views, named = (out_q, q), ("q", q, "out_q", out_q)
+        like, views = (sq, sq), (q, out_q)
     else:
-        out_k = _out(out_k, "out_k", k, stream)
-        views, named = (out_q, q, out_k, k), ("q", q, "out_q", out_q, "k", k, "out_k", out_k)
-    dev, dt = _same_heads(q, named, (3, 4))
-    wq = _weight(weight_q, "weight_q", D, q)
-    wk = _weight(weight_k, "weight_k", D, q) if k is not None else None
+        if out_k is None:
+            out_k = _empty(sk, k.dtype, k.device, stream)
+        like, views = (sq, sq, sk, sk), (q, out_q, k, out_k)
+    found = _heads(n, like, *views)
+    if found is None:
+        _refuse(n, like, ("q", "out_q", "k", "out_k"), views)
+    dev, dt, _keep, at = found
+    wq = _weight(weight_q, "weight_q", D, q, dev)
+    wk, kp, ko = None, None, None
+    if k is not None:
+        wk, kp, ko = _weight(weight_k, "weight_k", D, q, dev), at + 2 * _SIZE, at + 3 * _SIZE
     R, rows, pc, ps = _angles(cos, sin, B, L, dev)
-    _keep, at = _heads(views)
-    ko, ki = (at + 2 * _SIZE, at + 3 * _SIZE) if k is not None else (None, None)
-    _call(dev, library().dit_rmsnorm_rope, "dit_rmsnorm_rope", at, ko, at + _SIZE, ki, wq, wk, pc,
+    _call(dev, library().dit_rmsnorm_rope, "dit_rmsnorm_rope", at + _SIZE, ko, at, kp, wq, wk, pc,
           ps, B, L, Hq, Hk, D, R, rows, eps, weight_offset, int(interleaved), dt,
           _stream(dev, stream))
     return out_q, out_k
@@ -270,43 +299,42 @@ def rmsnorm_rope_backward(grad_out_q, grad_out_k, q, k, weight_q, weight_k, cos,
     grad_q may be grad_out_q, grad_k may be grad_out_k.  workspace: a uint8
     CUDA tensor of at least dit_rmsnorm_rope_backward_workspace_bytes(D) bytes
     (allocated if None)."""
-    B, L, Hq, Hk, D = _shapes(q, k)
-    _tensor(grad_out_q, "grad_out_q")
-    _match("grad_out_q", grad_out_q, q.shape)
-    grad_q = _out(grad_q, "grad_q", q, stream)
-    views = (grad_q, grad_out_q, q)
-    named = ("q", q, "grad_out_q", grad_out_q, "grad_q", grad_q)
+    B, L, Hq, Hk, D, n, sq, sk = _shapes(q, k)
+    if grad_q is None:
+        grad_q = _empty(sq, q.dtype, q.device, stream)
+    like, views = (sq, sq, sq), (q, grad_out_q, grad_q)
     if k is None:
-        if any(t is not None for t in (grad_out_k, grad_k, weight_k, grad_weight_k)):
+        if (grad_out_k is not None or grad_k is not None or weight_k is not None
+                or grad_weight_k is not None):
             raise ValueError("a key's tensor without k")
     else:
-        _tensor(grad_out_k, "grad_out_k")
-        _match("grad_out_k", grad_out_k, k.shape)
-        grad_k = _out(grad_k, "grad_k", k, stream)
-        views += (grad_k, grad_out_k, k)
-        named += ("k", k, "grad_out_k", grad_out_k, "grad_k", grad_k)
-    dev, dt = _same_heads(q, named, (3, 4))
-    wq = _weight(weight_q, "weight_q", D, q)
-    wk = _weight(weight_k, "weight_k", D, q) if k is not None else None
+        if grad_k is None:
+            grad_k = _empty(sk, k.dtype, k.device, stream)
+        like, views = like + (sk, sk, sk), views + (k, grad_out_k, grad_k)
+    found = _heads(n, like, *views)
+    if found is None:
+        _refuse(n, like, ("q", "grad_out_q", "grad_q", "k", "grad_out_k", "grad_k"), views)
+    dev, dt, _keep, at = found
     lib = library()
+    wq = _weight(weight_q, "weight_q", D, q, dev)
+    wk, k_at = None, (None,) * 3
+    if k is not None:
+        wk, k_at = _weight(weight_k, "weight_k", D, q, dev), (at + 3 * _SIZE, at + 4 * _SIZE, at + 5 * _SIZE)
     ws, wp, wn, gq, gk = None, None, 0, None, None
     if not need_weight:
         grad_weight_q = grad_weight_k = None
     else:
         if grad_weight_q is None:
             grad_weight_q = _empty((D,), q.dtype, q.device, stream)
-        gq = _weight(grad_weight_q, "grad_weight_q", D, q)
+        gq = _weight(grad_weight_q, "grad_weight_q", D, q, dev)
         if k is not None:
             if grad_weight_k is None:
                 grad_weight_k = _empty((D,), q.dtype, q.device, stream)
-            gk = _weight(grad_weight_k, "grad_weight_k", D, q)
+            gk = _weight(grad_weight_k, "grad_weight_k", D, q, dev)
         ws, wp, wn = _workspace(workspace, lib.dit_rmsnorm_rope_backward_workspace_bytes(D), q, stream)
     R, rows, pc, ps = _angles(cos, sin, B, L, dev)
-    _keep, at = _heads(views)
-    q_at = (at, at + _SIZE, at + 2 * _SIZE)
-    k_at = tuple(p + 3 * _SIZE for p in q_at) if k is not None else (None,) * 3
-    _call(dev, lib.dit_rmsnorm_rope_backward, "dit_rmsnorm_rope_backward", q_at[0], k_at[0], gq, gk,
-          q_at[1], k_at[1], q_at[2], k_at[2], wq, wk, pc, ps, B, L, Hq, Hk, D, R, rows, eps,
+    _call(dev, lib.dit_rmsnorm_rope_backward, "dit_rmsnorm_rope_backward", at + 2 * _SIZE, k_at[2],
+          gq, gk, at + _SIZE, k_at[1], at, k_at[0], wq, wk, pc, ps, B, L, Hq, Hk, D, R, rows, eps,
           weight_offset, int(interleaved), dt, wp, wn, _stream(dev, stream))
     return grad_q, grad_k, grad_weight_q, grad_weight_k
 
@@ -379,21 +407,20 @@ def _slots(cache, k, v, slots):
         raise TypeError("cache must be a KVCache")
     if not isinstance(slots, torch.Tensor) or slots.dtype not in ID_CODES:
         raise TypeError("slots must be an int32 or int64 CUDA tensor")
-    _tensor(k, "k")
-    _tensor(v, "v")
     if slots.dim() != 1:
         raise ValueError("slots must be [tokens]")
-    shape = (slots.shape[0], cache.heads, cache.D)
-    _match("k", k, shape)
-    _match("v", v, shape)
-    dev, dt = _same_heads(k, ("k", k, "v", v), (3,))
+    like = ((slots.shape[0], cache.heads, cache.D),) * 2
+    found = _heads(3, like, k, v)
+    if found is None:
+        _refuse(3, like, ("k", "v"), (k, v))
+    dev, dt, keep, at = found
     if dev != cache.device_index:
         raise ValueError(f"k is on cuda:{dev}, expected {cache.device}")
     if slots.get_device() != dev or not slots.is_contiguous():
-        _cuda(("k", k[:0].contiguous()), ("slots", slots))
+        _tensor(slots, "slots")
+        raise ValueError(f"slots must be contiguous, on cuda:{dev}")
     if cache.format != E4M3 and cache.format != dt:
         raise TypeError(f"k is {k.dtype}, the cache {cache.dtype}")
-    keep, at = _heads((k, v))
     return dev, dt, ID_CODES[slots.dtype], keep, at
 
 
@@ -445,14 +472,21 @@ def paged_attention(q, cache, pages, lengths, scale=None, window=0, out=None, ls
     None).  Returns (out, lse)."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
-    _tensor(q, "q")
-    if q.dim() != 3 or q.shape[2] != cache.D:
-        raise ValueError(f"q must be [B, heads, {cache.D}], got {tuple(q.shape)}")
-    B, Hq, D = q.shape
+    if not isinstance(q, torch.Tensor):
+        _tensor(q, "q")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.D:
+        _tensor(q, "q")
+        raise ValueError(f"q must be [B, heads, {cache.D}], got {tuple(shape)}")
+    B, Hq, D = shape
     if cache.heads == 0 or Hq == 0 or Hq % cache.heads:
         raise ValueError(f"q has {Hq} heads, the cache {cache.heads}")
-    out = _out(out, "out", q, stream)
-    dev, dt = _same_heads(q, ("q", q, "out", out), (3,))
+    if out is None:
+        out = _empty(shape, q.dtype, q.device, stream)
+    found = _heads(3, (shape, shape), q, out)
+    if found is None:
+        _refuse(3, (shape, shape), ("q", "out"), (q, out))
+    dev, dt, _keep, at = found
     if dev != cache.device_index:
         raise ValueError(f"q is on cuda:{dev}, expected {cache.device}")
     if cache.format != E4M3 and cache.format != dt:
@@ -479,9 +513,8 @@ def paged_attention(q, cache, pages, lengths, scale=None, window=0, out=None, ls
     ws, wp, wn = _workspace(workspace, lib.dit_paged_attention_workspace_bytes(Hq, cache.heads, D),
                             q, stream)
     width = pages.shape[1]
-    _keep, at = _heads((out, q))
-    _call(dev, lib.dit_paged_attention, "dit_paged_attention", at,
-          None if lse is None else lse.data_ptr(), at + _SIZE, cache.address, pages.data_ptr(),
+    _call(dev, lib.dit_paged_attention, "dit_paged_attention", at + _SIZE,
+          None if lse is None else lse.data_ptr(), at, cache.address, pages.data_ptr(),
           pages.stride(0) if B > 1 else width, width, lengths.data_ptr(), B, Hq,
           D ** -0.5 if scale is None else scale, int(window), ID_CODES[lengths.dtype], dt, wp, wn,
           _stream(dev, stream))

@@ -146,10 +146,7 @@ template <class T, int TEAM, bool INTER, int NT>
 struct HeadStage {
   using Lane = HeadLane<T>;
   static constexpr int TEAMS = 32 / TEAM;
-  #ifndef HEADS1
-#define HEADS1 4
-#endif
-  static constexpr int HEADS = NT == 1 ? HEADS1 : 2;
+  static constexpr int HEADS = 2;
   static constexpr int GRANULES = HEADS * NT * 2;
   // angles: cosines and sines of PER columns (both granules'), or of PER / 2 pairs for each granule
   static constexpr int AB = INTER && sizeof(T) == 4 ? 8 : 16;  // bytes of a piece

@@ -16,35 +16,46 @@ namespace {
 // the table
 // ---------------------------------------------------------------------------
 
-constexpr int kTableThreads = 256;
+constexpr int kTableThreads = 512, kTablePairs = 512;
 
-// A frequency in turns per unit: for integer positions |f| modulo one turn as a
-// 64-bit fraction (a position times it, modulo 2^64, is the angle whatever the position),
-// for fp32 ones as the sum of three fp32 numbers.
-struct Turns {
+// The frequencies in turns per unit: for integer positions |f| modulo one turn as a 64-bit fraction (a position
+// times it, modulo 2^64, is the angle whatever the position), for fp32 ones as the sum of three fp32 numbers.
+// Made once a CTA: fp64 comes at two operations a clock and SM.
+template <class P>
+struct Turns;
+template <>
+struct Turns<int64_t> {
   uint64_t fraction;
-  float part[3];
-  bool negative, usable;
+  uint32_t flags;  // 1: negative, 2: not finite
+  __device__ __forceinline__ explicit Turns(double freq) {
+    const double f = freq * 0.15915494309189535, m = fabs(f);  // 1 / (2 pi)
+    fraction = isfinite(freq) ? __double2ull_rn((m - floor(m)) * 18446744073709551616.0) : 0;
+    flags = (f < 0.0 ? 1 : 0) | (isfinite(freq) ? 0 : 2);
+  }
+  Turns() = default;
 };
-__device__ __forceinline__ Turns turns_of(double freq) {
-  Turns t;
-  const double f = freq * 0.15915494309189535;  // 1 / (2 pi)
-  t.usable = isfinite(freq);
-  t.negative = f < 0.0;
-  const double m = fabs(f);
-  t.fraction = t.usable ? __double2ull_rn((m - floor(m)) * 18446744073709551616.0) : 0;
-  t.part[0] = (float)f;
-  t.part[1] = (float)(f - (double)t.part[0]);
-  t.part[2] = (float)(f - (double)t.part[0] - (double)t.part[1]);
-  return t;
-}
+template <>
+struct Turns<float> {
+  float part[3];
+  uint32_t flags;
+  __device__ __forceinline__ explicit Turns(double freq) {
+    double f = freq * 0.15915494309189535;
+    flags = isfinite(freq) ? 0 : 2;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      part[i] = (float)f;
+      f -= (double)part[i];
+    }
+  }
+  Turns() = default;
+};
 // a part of a turn in [-1/2, 1/2] or a little beyond
-__device__ __forceinline__ float turn_part(const Turns& f, int64_t position) {
+__device__ __forceinline__ float turn_part(const Turns<int64_t>& f, int64_t position) {
   int64_t x = (int64_t)((uint64_t)position * f.fraction);
-  if (f.negative) x = (int64_t)(0 - (uint64_t)x);
+  if (f.flags & 1) x = (int64_t)(0 - (uint64_t)x);
   return (float)x * 0x1p-64f;
 }
-__device__ __forceinline__ float turn_part(const Turns& f, float p) {
+__device__ __forceinline__ float turn_part(const Turns<float>& f, float p) {
   // p f as high parts and their errors, each without its whole turns
   float sum = __fmul_rn(p, f.part[2]);
   sum = __fadd_rn(sum, -rintf(sum));
@@ -58,31 +69,35 @@ __device__ __forceinline__ float turn_part(const Turns& f, float p) {
   return __fadd_rn(sum, -rintf(sum));
 }
 
-// A thread has a column and every gridDim.y-th token.
+// A thread has a column (or every 512th) and every so many tokens.
 template <class P>
 __global__ void __launch_bounds__(kTableThreads) table_kernel(const __grid_constant__ TableArgs a) {
-  const int columns = min(a.R, kTableThreads);
-  const int rows = kTableThreads / columns;
-  const int row = threadIdx.x / columns;
+  using F = Turns<typename std::conditional<std::is_same<P, float>::value, float, int64_t>::type>;
+  __shared__ F turns[kTablePairs];
+  after_previous();
+  let_next();
+  if ((int)threadIdx.x < a.R) turns[threadIdx.x] = F(a.freqs[threadIdx.x]);
+  __syncthreads();
+  const int rows = kTableThreads / a.R, row = threadIdx.x / a.R, j = threadIdx.x - row * a.R;
   if (row >= rows) return;
-  for (int j = threadIdx.x % columns; j < a.R; j += columns) {
-    const Turns f = turns_of(a.freqs[j]);
-    int axis = 0;
-    while (axis < a.axes - 1 && j >= a.end[axis]) ++axis;
-    const P* positions = (const P*)a.positions + (int64_t)axis * a.tokens;
-    for (int64_t t = (int64_t)blockIdx.x * rows + row; t < a.tokens; t += (int64_t)gridDim.x * rows) {
-      float s, c;
-      if constexpr (sizeof(P) == 4 && P(0.5) != P(0)) {
-        const float p = positions[t];
-        sincospif(2.0f * turn_part(f, p), &s, &c);
-        if (!isfinite(p)) s = c = CUDART_NAN_F;
-      } else {
-        sincospif(2.0f * turn_part(f, (int64_t)positions[t]), &s, &c);
-      }
-      if (!f.usable) s = c = CUDART_NAN_F;
-      a.cos[t * a.R + j] = c;
-      a.sin[t * a.R + j] = s;
+  const F f = turns[j];
+  int axis = 0;
+  while (axis < a.axes - 1 && j >= a.end[axis]) ++axis;
+  const P* positions = (const P*)a.positions + (int64_t)axis * a.tokens;
+  const int64_t step = (int64_t)gridDim.x * rows;
+#pragma unroll 4
+  for (int64_t t = (int64_t)blockIdx.x * rows + row; t < a.tokens; t += step) {
+    const P p = positions[t];
+    float s, c;
+    bool finite = !(f.flags & 2);
+    if constexpr (std::is_same<P, float>::value) {
+      sincospif(2.0f * turn_part(f, p), &s, &c);
+      finite = finite && isfinite(p);
+    } else {
+      sincospif(2.0f * turn_part(f, (int64_t)p), &s, &c);
     }
+    a.cos[t * a.R + j] = finite ? c : CUDART_NAN_F;
+    a.sin[t * a.R + j] = finite ? s : CUDART_NAN_F;
   }
 }
 
@@ -138,18 +153,14 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const __grid_constant
 }
 
 // Heads in granules: a warp's items one after the other, the next kStages - 1 on their way.
-#ifndef STAGES
-#define STAGES 2
-#define MINB 2
-#endif
-constexpr int kStages = STAGES;
+constexpr int kStages = 2;
 
 struct RopeHeads {
   RopeArgs a;
   HeadGrid g;
 };
 template <class T, int TEAM, bool NORM, bool INTER, bool ALL>
-__global__ void __launch_bounds__(kRowThreads, MINB) rope_heads_kernel(const __grid_constant__ RopeHeads args) {
+__global__ void __launch_bounds__(kRowThreads, 2) rope_heads_kernel(const __grid_constant__ RopeHeads args) {
   using Stage = HeadStage<T, TEAM, INTER, 1>;
   constexpr int P = HeadLane<T>::P, TEAMS = Stage::TEAMS, HEADS = Stage::HEADS, WARPS = kRowThreads / 32;
   extern __shared__ __align__(16) unsigned char space[];
@@ -281,16 +292,13 @@ cudaError_t launch(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {
 
 cudaError_t launch_table(const DeviceInfo& dev, int position_type, const TableArgs& a,
                          cudaStream_t s) {
-  const int64_t rows = kTableThreads / std::min(a.R, kTableThreads);
-  const int64_t most = (int64_t)dev.sm_count * 8;
-  const unsigned grid = (unsigned)std::min(most, (a.tokens + rows - 1) / rows);
-  if (position_type == DIT_POS_INT32)
-    table_kernel<int32_t><<<grid, kTableThreads, 0, s>>>(a);
-  else if (position_type == DIT_POS_INT64)
-    table_kernel<int64_t><<<grid, kTableThreads, 0, s>>>(a);
-  else
-    table_kernel<float><<<grid, kTableThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  static_assert(kTablePairs <= kTableThreads, "a frequency a thread");
+  const int64_t rows = kTableThreads / a.R;
+  // (no more CTAs than are resident at once: each makes the frequencies anew)
+  const unsigned grid = (unsigned)std::min((int64_t)dev.sm_count * 3, (a.tokens + rows - 1) / rows);
+  return position_type == DIT_POS_INT32   ? launch_after(table_kernel<int32_t>, grid, kTableThreads, 0, s, a)
+         : position_type == DIT_POS_INT64 ? launch_after(table_kernel<int64_t>, grid, kTableThreads, 0, s, a)
+                                          : launch_after(table_kernel<float>, grid, kTableThreads, 0, s, a);
 }
 
 cudaError_t launch_rope(const DeviceInfo& dev, int dtype, const RopeArgs& a, cudaStream_t s) {
