@@ -40,7 +40,8 @@ struct Turns<float> {
   uint32_t flags;
   __device__ __forceinline__ explicit Turns(double freq) {
     double f = freq * 0.15915494309189535;
-    flags = isfinite(freq) ? 0 : 2;
+    flags = 0;
+    if (!isfinite(freq)) f = CUDART_NAN;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       part[i] = (float)f;
@@ -49,24 +50,49 @@ struct Turns<float> {
   }
   Turns() = default;
 };
-// a part of a turn in [-1/2, 1/2] or a little beyond
-__device__ __forceinline__ float turn_part(const Turns<int64_t>& f, int64_t position) {
-  int64_t x = (int64_t)((uint64_t)position * f.fraction);
-  if (f.flags & 1) x = (int64_t)(0 - (uint64_t)x);
-  return (float)x * 0x1p-64f;
+// An angle as a quarter of a turn, modulo four, and the turns from it, at most 1/8.
+struct Angle {
+  int quarter;  // its last two bits
+  float rest;
+};
+__device__ __forceinline__ Angle angle_of(const Turns<int64_t>& f, int64_t position) {
+  const uint64_t x = (uint64_t)position * f.fraction;
+  const uint64_t quarter = (x + (uint64_t(1) << 61)) >> 62;
+  const int64_t rest = (int64_t)(x - (quarter << 62));
+  // (both halves to fp32: small angles keep their digits)
+  return Angle{(int)quarter, __fmaf_rn((float)(uint32_t)rest, 0x1p-64f, __fmul_rn((float)(int32_t)(rest >> 32), 0x1p-32f))};
 }
-__device__ __forceinline__ float turn_part(const Turns<float>& f, float p) {
-  // p f as high parts and their errors, each without its whole turns
-  float sum = __fmul_rn(p, f.part[2]);
-  sum = __fadd_rn(sum, -rintf(sum));
-#pragma unroll
-  for (int i = 1; i >= 0; --i) {
-    const float high = __fmul_rn(p, f.part[i]);
-    const float low = __fmaf_rn(p, f.part[i], -high);
-    sum = __fadd_rn(sum, __fadd_rn(low, -rintf(low)));
-    sum = __fadd_rn(sum, __fadd_rn(high, -rintf(high)));
+__device__ __forceinline__ Angle angle_of(const Turns<float>& f, float p) {
+  // the products' high parts and errors
+  const float h0 = __fmul_rn(p, f.part[0]), l0 = __fmaf_rn(p, f.part[0], -h0);
+  const float h1 = __fmul_rn(p, f.part[1]), l1 = __fmaf_rn(p, f.part[1], -h1);
+  const float rest = __fmaf_rn(p, f.part[2], l1);
+  constexpr float shift = 12582912.0f;  // 1.5 2^23: a sum with it ends in whole numbers
+  float sum;
+  if (fabsf(h0) < 0x1p22f) {  // then the other parts are below 1/2, and shift rounds
+    sum = __fadd_rn(__fadd_rn(h0, -__fadd_rn(__fadd_rn(h0, shift), -shift)), __fadd_rn(l0, __fadd_rn(h1, rest)));
+  } else {  // each without its whole turns; NaN where h0 is not finite
+    auto fraction = [](float v) { return __fadd_rn(v, -rintf(v)); };
+    sum = __fadd_rn(fraction(h0), __fadd_rn(fraction(l0), __fadd_rn(fraction(h1), fraction(rest))));
   }
-  return __fadd_rn(sum, -rintf(sum));
+  const float quarter = __fmaf_rn(sum, 4.0f, shift);
+  return Angle{__float_as_int(quarter), __fmaf_rn(__fadd_rn(quarter, -shift), -0.25f, sum)};
+}
+// Its cosine and sine: Taylor's series of the rest, which is at most pi / 4 (the first terms left out: x^10 / 10! and
+// x^11 / 11!, below 2^-25), and a quarter turn's exchange and signs.
+__device__ __forceinline__ float2 cos_sin(const Angle& a) {
+  constexpr float high = 6.2831855f, low = -1.7484556e-7f;  // 2 pi in two parts
+  const float x = __fmaf_rn(a.rest, high, __fmul_rn(a.rest, low)), y = __fmul_rn(x, x);
+  float s = __fmaf_rn(y, 1.0f / 362880, -1.0f / 5040), c = __fmaf_rn(y, 1.0f / 40320, -1.0f / 720);
+  s = __fmaf_rn(s, y, 1.0f / 120);
+  c = __fmaf_rn(c, y, 1.0f / 24);
+  s = __fmaf_rn(s, y, -1.0f / 6);
+  c = __fmaf_rn(c, y, -0.5f);
+  s = __fmaf_rn(__fmul_rn(s, y), x, x);
+  c = __fmaf_rn(c, y, 1.0f);
+  const bool odd = a.quarter & 1;
+  const float u = odd ? s : c, v = odd ? c : s;
+  return make_float2((a.quarter + 1) & 2 ? -u : u, a.quarter & 2 ? -v : v);
 }
 
 // A thread has a column (or every 512th) and every so many tokens.
@@ -76,28 +102,48 @@ __global__ void __launch_bounds__(kTableThreads) table_kernel(const __grid_const
   __shared__ F turns[kTablePairs];
   after_previous();
   let_next();
-  if ((int)threadIdx.x < a.R) turns[threadIdx.x] = F(a.freqs[threadIdx.x]);
-  __syncthreads();
   const int rows = kTableThreads / a.R, row = threadIdx.x / a.R, j = threadIdx.x - row * a.R;
-  if (row >= rows) return;
-  const F f = turns[j];
   int axis = 0;
   while (axis < a.axes - 1 && j >= a.end[axis]) ++axis;
   const P* positions = (const P*)a.positions + (int64_t)axis * a.tokens;
-  const int64_t step = (int64_t)gridDim.x * rows;
-#pragma unroll 4
-  for (int64_t t = (int64_t)blockIdx.x * rows + row; t < a.tokens; t += step) {
-    const P p = positions[t];
-    float s, c;
-    bool finite = !(f.flags & 2);
-    if constexpr (std::is_same<P, float>::value) {
-      sincospif(2.0f * turn_part(f, p), &s, &c);
-      finite = finite && isfinite(p);
-    } else {
-      sincospif(2.0f * turn_part(f, (int64_t)p), &s, &c);
+  const uint32_t step = gridDim.x * rows, first = blockIdx.x * rows + row;
+  // tokens of this thread; the next AHEAD positions are on their way, the first ones while the frequencies are made
+  const int count = row < rows && first < a.tokens ? (int)(((uint32_t)a.tokens - first + step - 1) / step) : 0;
+  constexpr int AHEAD = 4;
+  P p[AHEAD];
+  positions += first;
+  auto load = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (i + k < count) p[k] = positions[(int64_t)k * step];
+    positions += (int64_t)AHEAD * step;
+  };
+  load(0);
+  if ((int)threadIdx.x < a.R) turns[threadIdx.x] = F(a.freqs[threadIdx.x]);
+  __syncthreads();
+  if (count == 0) return;
+  const F f = turns[j];
+  const bool finite = !(f.flags & 2), negative = f.flags & 1;
+  int64_t at = (int64_t)first * a.R + j;
+  const int64_t skip = (int64_t)step * a.R;
+  for (int i = 0; i < count; i += AHEAD) {
+    P now[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) now[k] = p[k];
+    load(i + AHEAD);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      float2 y = cos_sin(angle_of(f, now[k]));
+      if constexpr (!std::is_same<P, float>::value) {  // (of fp32 positions the products tell)
+        if (!finite) y = make_float2(CUDART_NAN_F, CUDART_NAN_F);
+        if (negative) y.y = -y.y;
+      }
+      if (i + k < count) {
+        a.cos[at] = y.x;
+        a.sin[at] = y.y;
+      }
+      at += skip;
     }
-    a.cos[t * a.R + j] = finite ? c : CUDART_NAN_F;
-    a.sin[t * a.R + j] = finite ? s : CUDART_NAN_F;
   }
 }
 
@@ -295,7 +341,7 @@ cudaError_t launch_table(const DeviceInfo& dev, int position_type, const TableAr
   static_assert(kTablePairs <= kTableThreads, "a frequency a thread");
   const int64_t rows = kTableThreads / a.R;
   // (no more CTAs than are resident at once: each makes the frequencies anew)
-  const unsigned grid = (unsigned)std::min((int64_t)dev.sm_count * 3, (a.tokens + rows - 1) / rows);
+  const unsigned grid = (unsigned)std::min((int64_t)dev.sm_count * 2, (a.tokens + rows - 1) / rows);
   return position_type == DIT_POS_INT32   ? launch_after(table_kernel<int32_t>, grid, kTableThreads, 0, s, a)
          : position_type == DIT_POS_INT64 ? launch_after(table_kernel<int64_t>, grid, kTableThreads, 0, s, a)
                                           : launch_after(table_kernel<float>, grid, kTableThreads, 0, s, a);
