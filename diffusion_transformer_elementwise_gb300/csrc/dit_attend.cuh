@@ -2,7 +2,7 @@
 // over the GPU (sm_103a).
 //
 // A segment is one sequence's tokens for up to kAttendRows query heads of one
-// key head; its tokens come in tiles of 16.  The tiles of all segments form one
+// key head; its tokens come in tiles of 32.  The tiles of all segments form one
 // line, which the CTAs cut into equal parts, so that sequences of any lengths
 // keep every SM equally busy: a CTA's part may hold many short segments or a piece of a
 // long one.  A segment within one CTA is finished there; of one that several
@@ -16,7 +16,7 @@
 
 namespace dit {
 
-constexpr int kTile = 16;
+constexpr int kTile = 32;
 
 // A sequence's tokens: [lo, hi), in tiles [first, last).
 struct Sequence {

@@ -5,7 +5,7 @@
 // in one pass over the tokens, with s in powers of two (scale times log2 e).
 //
 // What bounds it is memory: each key and value is read once for all query heads
-// of its key head.  A warp takes tiles of 16 tokens, each a product of 16 x 8 x 16
+// of its key head.  A warp takes tiles of 32 tokens, each two products of 16 x 8 x 16
 // steps (mma.sync): S (tokens x heads) = K Q^T, then O (columns x heads) += V^T P,
 // so that up to eight heads of a key head fill a product, and sixteen two.  The
 // 5th generation's instructions want 64 or 128 rows and their operands in shared
@@ -108,10 +108,14 @@ struct Shape {
   static constexpr int CE = VB / ES;                  // columns of such a piece
   static constexpr int PER = 16 / ES;                 // columns of a key's piece
   static constexpr int STEPS = DP / 16;               // products of 16 columns
-  static constexpr int STAGE = 32 * ROW;              // bytes of a warp's stage: 16 keys and values
-  // behind them: the scales of 16 keys and values (E4M3), and which tokens count
-  static constexpr int EXTRA = FP8 ? 256 : 128;
-  static constexpr int WARPS = ROW <= 128 && NB == 1 ? 16 : ROW <= 256 ? 8 : 4;
+  static constexpr int STAGE = 2 * kTile * ROW;       // bytes of a warp's stage: a tile of keys and values
+  // behind them: their scales (E4M3), and which tokens count
+  static constexpr int EXTRA = FP8 ? 8 * kTile + 128 : 128;
+#ifndef W128
+#define W128 12
+#define W256 6
+#endif
+  static constexpr int WARPS = ROW <= 64 && NB == 1 ? 16 : ROW <= 128 ? (NB == 1 ? W128 : 8) : ROW <= 256 ? W256 : 3;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int FIT = (220 * 1024) / (WARPS * (STAGE + EXTRA));
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
@@ -120,14 +124,17 @@ struct Shape {
   static_assert(WARPS <= kAttendWarps, "the workspace has room for their parts");
 };
 
-constexpr int kExtra = 2;  // units of a segment beside its tiles
-constexpr int kLeast = 2;  // the smallest part of a warp
+#ifndef KEXTRA
+#define KEXTRA 4
+#endif
+constexpr int kExtra = KEXTRA;  // units of a segment beside its tiles
+constexpr int kLeast = 1;  // the smallest part of a warp
 
 struct MmaArgs {
   AttendArgs a;
   Divisor page;         // page_size
   int page_rows;        // rows of D from page to page
-  bool whole;           // no page ends within a tile
+  bool whole;           // no page ends within half a tile
   float* warp_partial;  // [ctas][warps][2][rows][D + 2]: the parts of segments that warps share
 };
 
@@ -142,7 +149,7 @@ template <class T, class S>
 __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_constant__ MmaArgs args) {
   using M = typename S::M;
   constexpr bool FP8 = S::FP8;
-  constexpr int NB = S::NB, NCE = S::CE / 2;
+  constexpr int NB = S::NB, NCE = S::CE / 2, MB = kTile / 16;
   __shared__ Plan<S::THREADS> plan;
   __shared__ int64_t owner[S::WARPS][2];  // the warps' shared segments, or -1
   __shared__ bool open[S::WARPS];         // whether the first goes on in the next warp's part
@@ -180,7 +187,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
     Segment ag = {};
     bool more = ahead.next(a, line, ag);
     int tile = ag.first, head = more ? ag.s / blocks : 0;
-    int page = -1, place = 0;  // of token lane % 16 of that tile
+    int page = -1, place = 0;  // of token `lane` of that tile
     auto look = [&]() {
       if (more && tile >= ag.last) {
         more = ahead.next(a, line, ag);
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
       }
       page = -1;
       if (more) {
-        const int t = tile * kTile + (lane & 15);
+        const int t = tile * kTile + lane;
         if (t >= ag.lo && t < ag.hi) {
           const int n = (int)quotient(t, args.page);
           place = t - n * (int)args.page.d;
@@ -219,12 +226,15 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
           cp_async16_part(k + n * 512, (const char*)a.c.k + at, bytes);
           cp_async16_part(v + S::STAGE / 2 + n * 512, (const char*)a.c.v + at, bytes);
         };
-        if (count == 0xFFFFFFFFu && args.whole) {  // 16 rows that lie side by side
-          int64_t at = (int64_t)__shfl_sync(0xFFFFFFFFu, row, 0) * row_bytes + my_at;
+        if (count == 0xFFFFFFFFu && args.whole) {  // twice 16 rows that lie side by side
 #pragma unroll
-          for (int n = 0; n < COPIES; ++n) {
-            copy(n, at, my_bytes);
-            at += RPC * row_bytes;
+          for (int h = 0; h < 2; ++h) {
+            int64_t at = (int64_t)__shfl_sync(0xFFFFFFFFu, row, 16 * h) * row_bytes + my_at;
+#pragma unroll
+            for (int n = 0; n < COPIES / 2; ++n) {
+              copy(h * (COPIES / 2) + n, at, my_bytes);
+              at += RPC * row_bytes;
+            }
           }
         } else {
 #pragma unroll
@@ -235,12 +245,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
           }
         }
         if constexpr (FP8) {
-          const float* scales = lane < 16 ? a.c.k_scales : a.c.v_scales;
-          cp_async4_part(to + S::STAGE + lane * 4, scales + (there ? page * a.c.scale_stride + in_page : 0),
-                         there ? 4 : 0);
+          const int64_t at = there ? page * a.c.scale_stride + in_page : 0;
+          cp_async4_part(to + S::STAGE + lane * 4, a.c.k_scales + at, there ? 4 : 0);
+          cp_async4_part(to + S::STAGE + 4 * kTile + lane * 4, a.c.v_scales + at, there ? 4 : 0);
         }
         if (lane == 0)
-          *(uint32_t*)(stages + stage * (S::STAGE + S::EXTRA) + S::STAGE + S::EXTRA - 16) = count & 0xFFFFu;
+          *(uint32_t*)(stages + stage * (S::STAGE + S::EXTRA) + S::STAGE + S::EXTRA - 16) = count;
         ++tile;
         look();
       }
@@ -335,83 +345,101 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
         __syncwarp();
         const uint32_t from = stages_at + stage * (S::STAGE + S::EXTRA);
         const unsigned char* extra = stages + stage * (S::STAGE + S::EXTRA) + S::STAGE;
-        const uint32_t count = *(const uint32_t*)(extra + S::EXTRA - 16) >> tg;  // bits 0 and 8: the lane's tokens
+        // bits 0, 8, 16 and 24: the lane's tokens tg, tg + 8 of both halves of the tile
+        const uint32_t count = *(const uint32_t*)(extra + S::EXTRA - 16) >> tg;
         const float* scales = (const float*)extra;
 
         // pieces of keys, KG at a time, in registers before the products that wait for each other
         constexpr int KG = S::KP < 4 ? S::KP : 4;
-        float s[NB][4] = {}, s2[NB][4] = {};
+        float s[NB][MB][4] = {};
 #pragma unroll
         for (int p0 = 0; p0 < S::KP; p0 += KG) {
-          Raw<16> x[KG], y[KG];
+          Raw<16> x[MB][KG], y[MB][KG];
 #pragma unroll
-          for (int p = 0; p < KG; ++p) {
-            const uint32_t at = from + key_at<S::ROW>(key, p0 + p);
-            x[p] = lds16(at);
-            y[p] = lds16(at + 8 * S::ROW);
-          }
+          for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int p = 0; p < KG; ++p) {
+              const uint32_t at = from + key_at<S::ROW>(key, p0 + p) + 16 * b * S::ROW;
+              x[b][p] = lds16(at);
+              y[b][p] = lds16(at + 8 * S::ROW);
+            }
           if (p0 == 0) issue(stage == 0 ? S::STAGES - 1 : stage - 1);
 #pragma unroll
           for (int p = 0; p < KG; ++p) {
             constexpr int N = FP8 ? 4 : 2;  // products of a piece
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const uint32_t a0 = FP8 ? e4m3x2_to_half2(x[p].w[i]) : x[p].w[2 * i];
-              const uint32_t a1 = FP8 ? e4m3x2_to_half2(y[p].w[i]) : y[p].w[2 * i];
-              const uint32_t a2 = FP8 ? e4m3x2_to_half2(x[p].w[i] >> 16) : x[p].w[2 * i + 1];
-              const uint32_t a3 = FP8 ? e4m3x2_to_half2(y[p].w[i] >> 16) : y[p].w[2 * i + 1];
+            for (int i = 0; i < N; ++i)
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                const uint32_t(&w)[2] = q[nb][(p0 + p) * N + i];
-                mma<M>(i & 1 ? s2[nb] : s[nb], a0, a1, a2, a3, w[0], w[1]);
+              for (int b = 0; b < MB; ++b) {
+                const Raw<16>&u = x[b][p], &v = y[b][p];
+                const uint32_t a0 = FP8 ? e4m3x2_to_half2(u.w[i]) : u.w[2 * i];
+                const uint32_t a1 = FP8 ? e4m3x2_to_half2(v.w[i]) : v.w[2 * i];
+                const uint32_t a2 = FP8 ? e4m3x2_to_half2(u.w[i] >> 16) : u.w[2 * i + 1];
+                const uint32_t a3 = FP8 ? e4m3x2_to_half2(v.w[i] >> 16) : v.w[2 * i + 1];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                  const uint32_t(&w)[2] = q[nb][(p0 + p) * N + i];
+                  mma<M>(s[nb][b], a0, a1, a2, a3, w[0], w[1]);
+                }
               }
-            }
           }
         }
         // the first pieces of the values, on their way meanwhile
         const uint32_t values = from + S::STAGE / 2;
-        auto load = [&](int i, int p) {
-          const uint32_t at = values + value[i & 1] + (i >> 1) * 8 * S::ROW + p * 128;
+        auto load = [&](int b, int i, int p) {
+          const uint32_t at = values + value[i & 1] + (16 * b + (i >> 1) * 8) * S::ROW + p * 128;
           if constexpr (S::VB == 16)
             return lds16(at);
           else
             return lds8(at);
         };
-        constexpr int VG = S::VP < 2 ? S::VP : 2;
+        // (pieces in the order p, b)
+        constexpr int VN = S::VP * MB, VG = VN < 2 ? VN : 2;
         Raw<S::VB> v[VG][4];
 #pragma unroll
-        for (int p = 0; p < VG; ++p)
+        for (int n = 0; n < VG; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[p][i] = load(i, p);
+          for (int i = 0; i < 4; ++i) v[n][i] = load(n % MB, i, n / MB);
+        float ks[2 * MB], vs[2 * MB];  // scales of the lane's tokens
+        if constexpr (FP8) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[nb][k] = __fadd_rn(s[nb][k], s2[nb][k]);
-        const float k0 = FP8 ? scales[tg] : 1.0f, k1 = FP8 ? scales[tg + 8] : 1.0f;
+          for (int t = 0; t < 2 * MB; ++t) ks[t] = scales[tg + 8 * t], vs[t] = scales[kTile + tg + 8 * t];
+        }
         float f[NB][2];
         bool moved = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float x = s[nb][j], y = s[nb][2 + j];
-            if constexpr (FP8) x = __fmul_rn(x, k0), y = __fmul_rn(y, k1);
-            x = count & 1 ? __fmul_rn(x, factor[nb][j]) : -INFINITY;
-            y = count & 256 ? __fmul_rn(y, factor[nb][j]) : -INFINITY;
-            const float most = column_max(fmaxf(m[nb][j], fmaxf(x, y)));
+            float most = m[nb][j];
+#pragma unroll
+            for (int t = 0; t < 2 * MB; ++t) {
+              float& x = s[nb][t / 2][2 * (t & 1) + j];
+              if constexpr (FP8) x = __fmul_rn(x, ks[t]);
+              x = count >> (8 * t) & 1 ? __fmul_rn(x, factor[nb][j]) : -INFINITY;
+              most = fmaxf(most, x);
+            }
+            most = column_max(most);
             const float base = most == -INFINITY ? 0.0f : most;
             f[nb][j] = exp2_fast(__fadd_rn(m[nb][j], -base));
             moved = moved || most != m[nb][j];
             m[nb][j] = most;
-            s[nb][j] = exp2_fast(__fadd_rn(x, -base));
-            s[nb][2 + j] = exp2_fast(__fadd_rn(y, -base));
-            l[nb][j] = __fmaf_rn(l[nb][j], f[nb][j], __fadd_rn(s[nb][j], s[nb][2 + j]));
+            float sum = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 2 * MB; ++t) {
+              float& x = s[nb][t / 2][2 * (t & 1) + j];
+              x = exp2_fast(__fadd_rn(x, -base));
+              sum = __fadd_rn(sum, x);
+            }
+            l[nb][j] = __fmaf_rn(l[nb][j], f[nb][j], sum);
           }
         }
         if constexpr (FP8) {
           // weights times the values' scales, in units of a power of two above all of them so far, fit fp16
-          const float v0 = scales[16 + tg], v1 = scales[24 + tg];
-          const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(__float_as_uint(v0), __float_as_uint(v1)));
+          uint32_t most = 0;
+#pragma unroll
+          for (int t = 0; t < 2 * MB; ++t) most = max(most, __float_as_uint(vs[t]));
+          most = __reduce_max_sync(0xFFFFFFFFu, most);
           if (most >= __float_as_uint(vref)) {
             const uint32_t e = min((most >> 23) + 1, 253u);
             const float now = most > 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(e << 23);
@@ -425,14 +453,14 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
           }
           // (1 / vref: its exponent reflected; NaN stays NaN)
           const float unit = vref != vref ? vref : __uint_as_float(0x7F000000u - __float_as_uint(vref));
-          const float w0 = __fmul_rn(v0, unit), w1 = __fmul_rn(v1, unit);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+          for (int t = 0; t < 2 * MB; ++t) {
+            const float by = __fmul_rn(vs[t], unit);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              s[nb][j] = __fmul_rn(s[nb][j], w0);
-              s[nb][2 + j] = __fmul_rn(s[nb][2 + j], w1);
-            }
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) s[nb][t / 2][2 * (t & 1) + j] = __fmul_rn(s[nb][t / 2][2 * (t & 1) + j], by);
+          }
         }
         if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
@@ -444,14 +472,18 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[nb][p][i][k] = __fmul_rn(o[nb][p][i][k], f[nb][k & 1]);
         }
-        uint32_t w[NB][2];
+        uint32_t w[NB][MB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) w[nb][k] = transposed(Pair<M>::narrow(f2(s[nb][2 * k], s[nb][2 * k + 1])));
+          for (int b = 0; b < MB; ++b)
 #pragma unroll
-        for (int p = 0; p < S::VP; ++p) {
-          Raw<S::VB>(&u)[4] = v[p % VG];
+            for (int k = 0; k < 2; ++k)
+              w[nb][b][k] = transposed(Pair<M>::narrow(f2(s[nb][b][2 * k], s[nb][b][2 * k + 1])));
+#pragma unroll
+        for (int n = 0; n < VN; ++n) {
+          const int p = n / MB, b = n % MB;
+          Raw<S::VB>(&u)[4] = v[n % VG];
 #pragma unroll
           for (int k = 0; k < S::VB / 4; ++k) {
             if constexpr (FP8) {
@@ -463,7 +495,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
                 const uint32_t a0 = e4m3x2_to_half2(x), a1 = e4m3x2_to_half2(x >> 16);
                 const uint32_t a2 = e4m3x2_to_half2(y), a3 = e4m3x2_to_half2(y >> 16);
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][2 * k + h], a0, a1, a2, a3, w[nb][0], w[nb][1]);
+                for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][2 * k + h], a0, a1, a2, a3, w[nb][b][0], w[nb][b][1]);
               }
             } else {
               const uint32_t a0 = __byte_perm(u[0].w[k], u[1].w[k], 0x5410);
@@ -471,12 +503,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
               const uint32_t a2 = __byte_perm(u[2].w[k], u[3].w[k], 0x5410);
               const uint32_t a3 = __byte_perm(u[2].w[k], u[3].w[k], 0x7632);
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][k], a0, a1, a2, a3, w[nb][0], w[nb][1]);
+              for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][k], a0, a1, a2, a3, w[nb][b][0], w[nb][b][1]);
             }
           }
-          if (p + VG < S::VP) {
+          if (n + VG < VN) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] = load(i, p + VG);
+            for (int i = 0; i < 4; ++i) u[i] = load((n + VG) % MB, i, (n + VG) / MB);
           }
         }
         stage = stage + 1 == S::STAGES ? 0 : stage + 1;
@@ -609,7 +641,7 @@ cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cu
   MmaArgs m;
   m.a = a;
   m.page = divisor((uint32_t)a.c.page_size);
-  m.whole = a.c.page_size % kTile == 0;
+  m.whole = a.c.page_size % 16 == 0;
   m.page_rows = (int)(a.c.page_stride / a.c.D);
   m.warp_partial = a.partial + *ctas * 2 * std::min(a.group, kAttendRows) * (a.c.D + 2);
   return launch_after(kern, (unsigned)*ctas, S::THREADS, S::SMEM, s, m);
