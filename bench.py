@@ -161,7 +161,7 @@ def _code_only(text):
 OTHER_SOURCES = {"dit_token.h", "dit_token_api.cu", "dit_unit.cuh", "k_norm.cu", "k_norm_grad.cu",
                  "k_embedding.cu", "k_clip.cu", "dit_attend.h", "dit_attend_api.cu",
                  "dit_attend.cuh", "dit_heads.cuh", "k_rope.cu", "k_rope_grad.cu", "k_cache.cu",
-                 "k_attend.cu", "k_attend_mma.cu"}
+                 "k_attend.cu", "k_attend_mma.cu", "k_attend_mma_fp32.cu"}
 
 
 def kernel_source_hash():

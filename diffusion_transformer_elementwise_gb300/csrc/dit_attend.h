@@ -66,9 +66,10 @@ struct AttendArgs {
   const void* lengths;
   bool ids64;
   int B, Hq, group;     // group: query heads of a key head
+  int rows;             // of them in a segment: kAttendRows, or 8
   float scale;
   int64_t window;
-  float* partial;       // [ctas][2][kAttendRows][D + 2]: the parts of split segments
+  float* partial;       // [ctas][2][rows][D + 2]: the parts of split segments
   int64_t* owner;       // [ctas][2]: their segments, or -1
 };
 // query heads that share a pass over the keys, and the most CTAs
@@ -77,13 +78,13 @@ constexpr int64_t kAttendMaxCtas = 608;
 cudaError_t launch_attend(const DeviceInfo& dev, int dtype, bool granules, const AttendArgs& a,
                           cudaStream_t s);
 
-// The tensor cores' form of its first kernel (k_attend_mma.cu): for 16-bit queries of at most 256
-// columns in 16-byte granules.  Its CTAs and their warps have parts of their own behind
+// The tensor cores' form of its first kernel (k_attend_mma.cu): at most 256
+// columns in 16-byte granules.  Sets a.rows.  Its CTAs and their warps have parts of their own behind
 // `partial`: [ctas][warps][2][rows][D + 2].
 constexpr int64_t kAttendMmaCtas = 160;
 constexpr int kAttendWarps = 16;
-bool attend_mma_takes(int dtype, bool granules, const AttendArgs& a);
-cudaError_t launch_attend_mma(const DeviceInfo& dev, int dtype, const AttendArgs& a, int64_t* ctas,
-                              cudaStream_t s);
+bool attend_mma_takes(bool granules, const AttendArgs& a);
+cudaError_t launch_attend_mma(const DeviceInfo& dev, int dtype, AttendArgs& a, int64_t* ctas, cudaStream_t s);
+cudaError_t launch_attend_mma_fp32(const DeviceInfo& dev, AttendArgs& a, int64_t* ctas, cudaStream_t s);
 
 }  // namespace dit

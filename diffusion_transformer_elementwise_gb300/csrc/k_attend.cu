@@ -167,12 +167,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   let_next();
   const int64_t id = a.owner[2 * cta + 1];
   if (id < 0) return;
-  const int blocks = (a.group + kAttendRows - 1) / kAttendRows;
+  const int blocks = (a.group + a.rows - 1) / a.rows;
   const int segments = (int)a.c.heads * blocks;
   const int b = (int)(id / segments), s = (int)(id - (int64_t)b * segments);
-  const int head = s / blocks, row0 = (s - head * blocks) * kAttendRows;
-  const int slot_rows = min(a.group, kAttendRows);
-  if (r >= min(kAttendRows, a.group - row0)) return;
+  const int head = s / blocks, row0 = (s - head * blocks) * a.rows;
+  const int slot_rows = min(a.group, a.rows);
+  if (r >= min(a.rows, a.group - row0)) return;
   int count = 1;  // parts: this CTA's, and the first ones of those after it
   for (;; count += 32) {
     const int k = cta + count + lane;
@@ -236,25 +236,25 @@ cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cu
 }
 
 template <class T>
-cudaError_t launch(const DeviceInfo& dev, bool mma, const AttendArgs& a, cudaStream_t s) {
+cudaError_t launch(const DeviceInfo& dev, int dtype, bool mma, AttendArgs a, cudaStream_t s) {
   int64_t ctas = 0;
-  const cudaError_t e = mma                        ? launch_attend_mma(dev, std::is_same<T, __half>::value ? 1 : 0, a, &ctas, s)
+  a.rows = kAttendRows;
+  const cudaError_t e = mma                        ? launch_attend_mma(dev, dtype, a, &ctas, s)
                         : a.c.format == DIT_E4M3 ? launch<T, uint8_t>(dev, a, &ctas, s)
                                                  : launch<T, T>(dev, a, &ctas, s);
   if (e != cudaSuccess) return e;
   const JoinArgs j{a, (int)ctas};
-  return launch_after(join_kernel<T>, dim3((unsigned)ctas, (unsigned)std::min(a.group, kAttendRows)), 32 * kJoinWarps, 0,
-                      s, j);
+  return launch_after(join_kernel<T>, dim3((unsigned)ctas, (unsigned)std::min(a.group, a.rows)), 32 * kJoinWarps, 0, s, j);
 }
 
 }  // namespace
 
 cudaError_t launch_attend(const DeviceInfo& dev, int dtype, bool granules, const AttendArgs& a,
                           cudaStream_t s) {
-  const bool mma = attend_mma_takes(dtype, granules, a);
-  return dtype == 0   ? launch<__nv_bfloat16>(dev, mma, a, s)
-         : dtype == 1 ? launch<__half>(dev, mma, a, s)
-                      : launch<float>(dev, false, a, s);
+  const bool mma = attend_mma_takes(granules, a);
+  return dtype == 0   ? launch<__nv_bfloat16>(dev, dtype, mma, a, s)
+         : dtype == 1 ? launch<__half>(dev, dtype, mma, a, s)
+                      : launch<float>(dev, dtype, mma, a, s);
 }
 
 }  // namespace dit

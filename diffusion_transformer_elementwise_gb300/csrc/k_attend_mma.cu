@@ -36,7 +36,9 @@ __device__ __forceinline__ float exp2_fast(float x) {  // within 2^-22
   return y;
 }
 
-// d += a b: a 16 x 16, b 16 x 8, of M.
+struct Tf32 {};
+
+// d += a b: a 16 x 16, b 16 x 8, of M (Tf32: 16 x 8 and 8 x 8).
 template <class M>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -44,11 +46,23 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else if constexpr (std::is_same<M, Tf32>::value)
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// fp32 as the nearest tf32 and the rest, of which the tensor cores read the first 11 bits
+struct Split {
+  uint32_t high, low;
+  __device__ __forceinline__ explicit Split(uint32_t x) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(high) : "f"(__uint_as_float(x)));
+    low = __float_as_uint(__fadd_rn(__uint_as_float(x), -__uint_as_float(high)));
+  }
+};
 // an 8 x 8 matrix of 16-bit numbers, a row's pairs over four lanes, transposed
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
@@ -94,28 +108,35 @@ __device__ __forceinline__ uint32_t key_at(uint32_t key, int p) {
 }
 
 // T: the queries' type; FP8: an E4M3 cache; DP: columns, D rounded up (the rest is zero); NB: blocks of
-// eight heads.
+// eight heads.  With fp32 queries every product is one of two parts each (SPLIT): keys and values of fp32 as two
+// tf32 numbers, queries and weights too, or, over an E4M3 cache, as two fp16 numbers; what is left out is 2^-22 of
+// a product.
 template <class T, bool FP8_, int DP_, int NB_>
 struct Shape {
-  static constexpr bool FP8 = FP8_;
+  static constexpr bool FP8 = FP8_, SPLIT = sizeof(T) == 4, TF32 = SPLIT && !FP8;
   static constexpr int DP = DP_, NB = NB_;
-  using M = typename std::conditional<FP8, __half, T>::type;  // of the products
-  static constexpr int ES = FP8 ? 1 : 2;
+  using M = typename std::conditional<FP8, __half, typename std::conditional<TF32, Tf32, T>::type>::type;  // of the products
+  static constexpr int ES = FP8 ? 1 : (int)sizeof(T);
   static constexpr int ROW = DP * ES;                 // bytes
   static constexpr int KP = ROW / 64;                 // 16-byte pieces of a key that a lane has
   static constexpr int VB = ROW / 8 < 16 ? ROW / 8 : 16;  // bytes of a piece of a value
   static constexpr int VP = ROW / 8 / VB;             // pieces of a value that a lane has
   static constexpr int CE = VB / ES;                  // columns of such a piece
   static constexpr int PER = 16 / ES;                 // columns of a key's piece
-  static constexpr int STEPS = DP / 16;               // products of 16 columns
-  static constexpr int STAGE = 2 * kTile * ROW;       // bytes of a warp's stage: a tile of keys and values
+  static constexpr int KN = FP8 ? 4 : 2;              // products of a key's piece
+  static constexpr int LOAD = 16 / (int)sizeof(T);    // queries' columns of 16 bytes
+  static constexpr int MB = ROW >= 512 || (NB == 2 && ROW >= 256) ? 1 : 2;  // blocks of 16 tokens of a stage
+  static constexpr int TOKENS = 16 * MB, PARTS = kTile / TOKENS;  // stages of a tile
+  static constexpr int STAGE = 2 * TOKENS * ROW;      // bytes of a warp's stage: keys and values
   // behind them: their scales (E4M3), and which tokens count
-  static constexpr int EXTRA = FP8 ? 8 * kTile + 128 : 128;
-#ifndef W128
-#define W128 12
-#define W256 6
-#endif
-  static constexpr int WARPS = ROW <= 64 && NB == 1 ? 16 : ROW <= 128 ? (NB == 1 ? W128 : 8) : ROW <= 256 ? W256 : 3;
+  static constexpr int EXTRA = FP8 ? 8 * TOKENS + 128 : 128;
+  // As many warps as registers and two stages of each in 220 KB let in.  Long sequences are as fast with fewer and more
+  // stages (bf16, D = 128: six warps of two, four of three), E4M3 wants the warps (12: 96.7 us for 553 MB, 8: 100.9).
+  static constexpr int WARPS = ROW <= 64 && NB == 1 && !SPLIT ? 16
+                               : ROW <= 128                   ? (NB == 1 && !SPLIT ? 12 : 8)
+                               : ROW <= 256                   ? (NB == 1 ? 6 : 8)
+                               : ROW <= 512                   ? 6
+                                                              : 3;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int FIT = (220 * 1024) / (WARPS * (STAGE + EXTRA));
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
@@ -124,11 +145,10 @@ struct Shape {
   static_assert(WARPS <= kAttendWarps, "the workspace has room for their parts");
 };
 
-#ifndef KEXTRA
-#define KEXTRA 4
-#endif
-constexpr int kExtra = KEXTRA;  // units of a segment beside its tiles
-constexpr int kLeast = 1;  // the smallest part of a warp
+// Units of a segment beside its tiles (128 sequences of 8 to 8192 tokens, E4M3: 1 80.0 us, 2 78.8, 4 78.1), and the
+// smallest part of a warp.
+constexpr int kExtra = 4;
+constexpr int kLeast = 1;
 
 struct MmaArgs {
   AttendArgs a;
@@ -149,7 +169,8 @@ template <class T, class S>
 __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_constant__ MmaArgs args) {
   using M = typename S::M;
   constexpr bool FP8 = S::FP8;
-  constexpr int NB = S::NB, NCE = S::CE / 2, MB = kTile / 16;
+  constexpr int NB = S::NB, NCE = S::CE / 2, MB = S::MB, TOKENS = S::TOKENS;
+  constexpr bool SPLIT = S::SPLIT, TF32 = S::TF32;
   __shared__ Plan<S::THREADS> plan;
   __shared__ int64_t owner[S::WARPS][2];  // the warps' shared segments, or -1
   __shared__ bool open[S::WARPS];         // whether the first goes on in the next warp's part
@@ -160,7 +181,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
   const int D = (int)a.c.D;
   const int blocks = (a.group + 8 * NB - 1) / (8 * NB);
   const Line line{(int)a.c.heads * blocks, kExtra};
-  const int slot_rows = min(a.group, kAttendRows);
+  const int slot_rows = min(a.group, 8 * NB);
   unsigned char* stages = space + warp * S::STAGES * (S::STAGE + S::EXTRA);
   const uint32_t stages_at = smem_addr(stages);
   // Rows of a product of tokens are not tokens g but tg, and g + 8 but tg + 8: see chunk_at.
@@ -186,17 +207,17 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
     Walk ahead(a, line, begin, end, mine);
     Segment ag = {};
     bool more = ahead.next(a, line, ag);
-    int tile = ag.first, head = more ? ag.s / blocks : 0;
-    int page = -1, place = 0;  // of token `lane` of that tile
+    int tile = ag.first * S::PARTS, head = more ? ag.s / blocks : 0;  // (tile: of TOKENS)
+    int page = -1, place = 0;  // of token lane % TOKENS of that tile
     auto look = [&]() {
-      if (more && tile >= ag.last) {
+      if (more && tile >= ag.last * S::PARTS) {
         more = ahead.next(a, line, ag);
-        tile = ag.first;
+        tile = ag.first * S::PARTS;
         head = ag.s / blocks;
       }
       page = -1;
       if (more) {
-        const int t = tile * kTile + lane;
+        const int t = tile * TOKENS + lane % TOKENS;
         if (t >= ag.lo && t < ag.hi) {
           const int n = (int)quotient(t, args.page);
           place = t - n * (int)args.page.d;
@@ -204,12 +225,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
         }
       }
     };
-    // A copy takes 512 bytes as they lie in memory: lane l has chunk l % LPR of row l / LPR of RPC.
-    constexpr int LPR = S::ROW / 16, RPC = 32 / LPR, COPIES = kTile / RPC;
+    // A copy takes 512 bytes as they lie in memory: lane l has chunk l % LPR of row l / LPR of RPC, or of
+    // rows of more than 512 bytes chunk l of one of CPR parts.
+    constexpr int LPR = S::ROW < 512 ? S::ROW / 16 : 32, RPC = 32 / LPR, CPR = S::ROW > 512 ? S::ROW / 512 : 1;
+    constexpr int COPIES = TOKENS / RPC * CPR;
     const int row_bytes = D * S::ES;
     const int my_row = lane / LPR, my_chunk = lane % LPR;
-    const int my_bytes = my_chunk * 16 < row_bytes ? 16 : 0;
-    const int my_at = my_row * row_bytes + (my_bytes ? my_chunk * 16 : 0);
     const uint32_t k_to = chunk_at<S::ROW, false>(my_row, my_chunk), v_to = chunk_at<S::ROW, true>(my_row, my_chunk);
     auto issue = [&](int stage) {
       if (more) {
@@ -220,34 +241,39 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
         // (of a token that does not count nothing is read, and zeros are written)
         const int row = there ? page * args.page_rows + in_page : -1;
         const uint32_t count = __ballot_sync(0xFFFFFFFFu, there);
-        auto copy = [&](int n, int64_t at, int bytes) {
-          // chunk_at of row n RPC + my_row: its part in n moves by constants
-          const uint32_t k = (to + k_to) ^ chunk_xor<S::ROW, false>(n * RPC), v = (to + v_to) ^ chunk_xor<S::ROW, true>(n * RPC);
-          cp_async16_part(k + n * 512, (const char*)a.c.k + at, bytes);
-          cp_async16_part(v + S::STAGE / 2 + n * 512, (const char*)a.c.v + at, bytes);
+        // copy n: of the row that starts at element offset `at` in bytes, or of none
+        auto copy = [&](int n, int64_t at, bool on) {
+          const int chunk = (n % CPR * 32 + my_chunk) * 16;
+          const bool any = on && chunk < row_bytes;
+          at = any ? at + chunk : 0;
+          // chunk_at of the copy's row: its part in n moves by constants
+          const int t = n / CPR * RPC;
+          const uint32_t k = (to + k_to) ^ chunk_xor<S::ROW, false>(t), v = (to + v_to) ^ chunk_xor<S::ROW, true>(t);
+          cp_async16_part(k + n * 512, (const char*)a.c.k + at, any ? 16 : 0);
+          cp_async16_part(v + S::STAGE / 2 + n * 512, (const char*)a.c.v + at, any ? 16 : 0);
         };
-        if (count == 0xFFFFFFFFu && args.whole) {  // twice 16 rows that lie side by side
+        if (count == 0xFFFFFFFFu && args.whole) {  // 16 rows each that lie side by side
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            int64_t at = (int64_t)__shfl_sync(0xFFFFFFFFu, row, 16 * h) * row_bytes + my_at;
+          for (int h = 0; h < MB; ++h) {
+            int64_t at = (int64_t)(__shfl_sync(0xFFFFFFFFu, row, 16 * h) + my_row) * row_bytes;
 #pragma unroll
-            for (int n = 0; n < COPIES / 2; ++n) {
-              copy(h * (COPIES / 2) + n, at, my_bytes);
-              at += RPC * row_bytes;
+            for (int n = 0; n < COPIES / MB; ++n) {
+              copy(h * (COPIES / MB) + n, at, true);
+              if (n % CPR == CPR - 1) at += RPC * row_bytes;
             }
           }
         } else {
 #pragma unroll
           for (int n = 0; n < COPIES; ++n) {
-            const int r = __shfl_sync(0xFFFFFFFFu, row, n * RPC + my_row);
-            const int bytes = r < 0 ? 0 : my_bytes;
-            copy(n, bytes ? (int64_t)r * row_bytes + my_chunk * 16 : 0, bytes);
+            const int r = __shfl_sync(0xFFFFFFFFu, row, n / CPR * RPC + my_row);
+            copy(n, (int64_t)r * row_bytes, r >= 0);
           }
         }
         if constexpr (FP8) {
           const int64_t at = there ? page * a.c.scale_stride + in_page : 0;
-          cp_async4_part(to + S::STAGE + lane * 4, a.c.k_scales + at, there ? 4 : 0);
-          cp_async4_part(to + S::STAGE + 4 * kTile + lane * 4, a.c.v_scales + at, there ? 4 : 0);
+          const uint32_t dst = to + S::STAGE + lane * 4;  // MB = 1: the upper lanes have the same tokens' values
+          cp_async4_part(dst, (MB == 1 && lane >= 16 ? a.c.v_scales : a.c.k_scales) + at, there ? 4 : 0);
+          if constexpr (MB == 2) cp_async4_part(dst + 4 * TOKENS, a.c.v_scales + at, there ? 4 : 0);
         }
         if (lane == 0)
           *(uint32_t*)(stages + stage * (S::STAGE + S::EXTRA) + S::STAGE + S::EXTRA - 16) = count;
@@ -266,7 +292,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
     uint32_t value[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int t = (2 * cl + i) ^ (i << 2);
+      // (TF32: of tokens c and c + 4)
+      const int t = TF32 ? cl ^ (cl & 1) << 2 ^ i << 2 : (2 * cl + i) ^ (i << 2);
       value[i] = S::VB == 16 ? chunk_at<S::ROW, true>(t, gl) : chunk_at<S::ROW, true>(t, gl >> 1) + (gl & 1) * 8;
     }
     int stage = 0;
@@ -279,54 +306,61 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
 
       // queries of head 8 nb + g, in the order of the keys' bytes, and what the products of heads 8 nb + 2c and
       // the next are multiplied by
-      uint32_t q[NB][S::STEPS][2];
+      // (over an E4M3 cache as fp16, by a power of two that brings the head's largest below 2^14; SPLIT: the rest too)
+      constexpr int LOADS = S::KP * S::PER / S::LOAD, SUB = S::PER / S::LOAD, QN = SPLIT && FP8 ? 2 : 1;
+      uint32_t q[QN][NB][S::KP * S::KN][2];
       float factor[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        constexpr int N = S::KP * S::PER / 8;
         const bool real = gl + 8 * nb < rows;
         const T* from = (const T*)a.q.p + g.b * a.q.token + (int64_t)(h0 + gl + 8 * nb) * a.q.head;
         float by = __fmul_rn(a.scale, 1.4426950408889634f);
-        Raw<16> raw[N];
+        Raw<16> raw[LOADS];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int c = (i / (S::PER / 8) * 4 + cl) * S::PER + (i % (S::PER / 8)) * 8;
+        for (int i = 0; i < LOADS; ++i) {
+          const int c = (i / SUB * 4 + cl) * S::PER + i % SUB * S::LOAD;
           raw[i] = Raw<16>{};
           if (real && c < D) raw[i] = ld_bcast<16>(from + c);
         }
-        if constexpr (FP8 && std::is_same<T, __nv_bfloat16>::value) {
-          // to fp16, by a power of two that brings the head's largest below 2^14
+        float up = 1.0f;
+        if constexpr (FP8 && !std::is_same<T, __half>::value) {
           float most = 0.0f;
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            float f[8];
+          for (int i = 0; i < LOADS; ++i) {
+            float f[S::LOAD];
             Vec<T, 16>::widen(raw[i], f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) most = max_nan(most, fabsf(f[k]));
+            for (int k = 0; k < S::LOAD; ++k) most = max_nan(most, fabsf(f[k]));
           }
           most = max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
           most = max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
           int e = (int)(__float_as_uint(most) >> 23) - 127;
           e = most == 0.0f || !isfinite(most) ? 13 : max(e, -100);
-          const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+          up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
           by = __fmul_rn(by, __uint_as_float((uint32_t)(e - 13 + 127) << 23));
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            float f[8];
-            Vec<T, 16>::widen(raw[i], f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(f[k], up);
-            raw[i] = Vec<__half, 16>::narrow(f);
-          }
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) factor[nb][j] = __shfl_sync(0xFFFFFFFFu, by, 4 * (2 * cl + j));
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < LOADS; ++i) {
+          if constexpr (FP8) {
+            float f[S::LOAD];
+            Vec<T, 16>::widen(raw[i], f);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            q[nb][2 * i + k][0] = raw[i].w[2 * k];
-            q[nb][2 * i + k][1] = raw[i].w[2 * k + 1];
+            for (int k = 0; k < S::LOAD / 2; ++k) {
+              const float x = __fmul_rn(f[2 * k], up), y = __fmul_rn(f[2 * k + 1], up);
+              const __half2 h = __floats2half2_rn(x, y);
+              uint32_t(&to)[2] = q[0][nb][(i * S::LOAD + 2 * k) / 4];
+              to[k & 1] = *(const uint32_t*)&h;
+              if constexpr (SPLIT) {
+                const float2 back = __half22float2(h);
+                q[QN - 1][nb][(i * S::LOAD + 2 * k) / 4][k & 1] =
+                    Pair<__half>::narrow(f2(__fadd_rn(x, -back.x), __fadd_rn(y, -back.y)));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) q[0][nb][2 * i + k / 2][k & 1] = raw[i].w[k];
           }
         }
       }
@@ -338,9 +372,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int j = 0; j < 2; ++j) m[nb][j] = -INFINITY, l[nb][j] = 0.0f;
-      float vref = 0x1p-126f;  // E4M3: o is in units of this power of two
+      float vref = SPLIT ? 0x1p-110f : 0x1p-126f;  // E4M3: o is in units of this power of two
 
-      for (int n = g.last - g.first; n > 0; --n) {
+      for (int n = (g.last - g.first) * S::PARTS; n > 0; --n) {
         cp_async_wait<S::STAGES - 2>();
         __syncwarp();
         const uint32_t from = stages_at + stage * (S::STAGE + S::EXTRA);
@@ -366,20 +400,31 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
           if (p0 == 0) issue(stage == 0 ? S::STAGES - 1 : stage - 1);
 #pragma unroll
           for (int p = 0; p < KG; ++p) {
-            constexpr int N = FP8 ? 4 : 2;  // products of a piece
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < S::KN; ++i)
 #pragma unroll
               for (int b = 0; b < MB; ++b) {
                 const Raw<16>&u = x[b][p], &v = y[b][p];
-                const uint32_t a0 = FP8 ? e4m3x2_to_half2(u.w[i]) : u.w[2 * i];
-                const uint32_t a1 = FP8 ? e4m3x2_to_half2(v.w[i]) : v.w[2 * i];
-                const uint32_t a2 = FP8 ? e4m3x2_to_half2(u.w[i] >> 16) : u.w[2 * i + 1];
-                const uint32_t a3 = FP8 ? e4m3x2_to_half2(v.w[i] >> 16) : v.w[2 * i + 1];
+                const int step = (p0 + p) * S::KN + i;
+                if constexpr (TF32) {
+                  const Split a0(u.w[2 * i]), a1(v.w[2 * i]), a2(u.w[2 * i + 1]), a3(v.w[2 * i + 1]);
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                  const uint32_t(&w)[2] = q[nb][(p0 + p) * N + i];
-                  mma<M>(s[nb][b], a0, a1, a2, a3, w[0], w[1]);
+                  for (int nb = 0; nb < NB; ++nb) {
+                    const Split b0(q[0][nb][step][0]), b1(q[0][nb][step][1]);
+                    mma<M>(s[nb][b], a0.low, a1.low, a2.low, a3.low, b0.high, b1.high);
+                    mma<M>(s[nb][b], a0.high, a1.high, a2.high, a3.high, b0.low, b1.low);
+                    mma<M>(s[nb][b], a0.high, a1.high, a2.high, a3.high, b0.high, b1.high);
+                  }
+                } else {
+                  const uint32_t a0 = FP8 ? e4m3x2_to_half2(u.w[i]) : u.w[2 * i];
+                  const uint32_t a1 = FP8 ? e4m3x2_to_half2(v.w[i]) : v.w[2 * i];
+                  const uint32_t a2 = FP8 ? e4m3x2_to_half2(u.w[i] >> 16) : u.w[2 * i + 1];
+                  const uint32_t a3 = FP8 ? e4m3x2_to_half2(v.w[i] >> 16) : v.w[2 * i + 1];
+#pragma unroll
+                  for (int k = 0; k < QN; ++k)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                      mma<M>(s[nb][b], a0, a1, a2, a3, q[k][nb][step][0], q[k][nb][step][1]);
                 }
               }
           }
@@ -403,7 +448,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
         float ks[2 * MB], vs[2 * MB];  // scales of the lane's tokens
         if constexpr (FP8) {
 #pragma unroll
-          for (int t = 0; t < 2 * MB; ++t) ks[t] = scales[tg + 8 * t], vs[t] = scales[kTile + tg + 8 * t];
+          for (int t = 0; t < 2 * MB; ++t) ks[t] = scales[tg + 8 * t], vs[t] = scales[TOKENS + tg + 8 * t];
         }
         float f[NB][2];
         bool moved = false;
@@ -452,7 +497,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
               for (int j = 0; j < 2; ++j) f[nb][j] = __fmul_rn(f[nb][j], down);
           }
           // (1 / vref: its exponent reflected; NaN stays NaN)
-          const float unit = vref != vref ? vref : __uint_as_float(0x7F000000u - __float_as_uint(vref));
+          // (SPLIT: 2^14 of them, so that the low parts stay above fp16's smallest)
+          float unit = vref != vref ? vref : __uint_as_float(0x7F000000u - __float_as_uint(vref));
+          if constexpr (SPLIT) unit = __fmul_rn(unit, 0x1p14f);
 #pragma unroll
           for (int t = 0; t < 2 * MB; ++t) {
             const float by = __fmul_rn(vs[t], unit);
@@ -472,38 +519,75 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[nb][p][i][k] = __fmul_rn(o[nb][p][i][k], f[nb][k & 1]);
         }
-        uint32_t w[NB][MB][2];
+        // weights of head g: of tokens 2c, 2c + 1 and 8 more (TF32: c, c + 4, and 8 more)
+        uint32_t w[QN][NB][MB][TF32 ? 4 : 2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int b = 0; b < MB; ++b)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              w[nb][b][k] = transposed(Pair<M>::narrow(f2(s[nb][b][2 * k], s[nb][b][2 * k + 1])));
+            for (int k = 0; k < 2; ++k) {
+              const float x = s[nb][b][2 * k], y = s[nb][b][2 * k + 1];
+              if constexpr (TF32) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int src = (cl + 4 * i) * 4 + gl / 2;
+                  const float u = __shfl_sync(0xFFFFFFFFu, x, src), v = __shfl_sync(0xFFFFFFFFu, y, src);
+                  w[0][nb][b][(2 * k + i) % (TF32 ? 4 : 2)] = __float_as_uint(gl & 1 ? v : u);
+                }
+              } else {
+                const uint32_t h = Pair<typename std::conditional<TF32, __half, M>::type>::narrow(f2(x, y));
+                w[0][nb][b][k] = transposed(h);
+                if constexpr (SPLIT) {
+                  const F2 back = Pair<__half>::widen(h);
+                  w[QN - 1][nb][b][k] = transposed(Pair<__half>::narrow(f2(__fadd_rn(x, -back.x), __fadd_rn(y, -back.y))));
+                }
+              }
+            }
 #pragma unroll
         for (int n = 0; n < VN; ++n) {
           const int p = n / MB, b = n % MB;
           Raw<S::VB>(&u)[4] = v[n % VG];
+          if constexpr (TF32) {
 #pragma unroll
-          for (int k = 0; k < S::VB / 4; ++k) {
-            if constexpr (FP8) {
-              // the codes of two tokens side by side, column by column
+            for (int k = 0; k < 2; ++k)  // eight tokens
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t sel = h ? 0x7362 : 0x5140;
-                const uint32_t x = __byte_perm(u[0].w[k], u[1].w[k], sel), y = __byte_perm(u[2].w[k], u[3].w[k], sel);
-                const uint32_t a0 = e4m3x2_to_half2(x), a1 = e4m3x2_to_half2(x >> 16);
-                const uint32_t a2 = e4m3x2_to_half2(y), a3 = e4m3x2_to_half2(y >> 16);
+              for (int e = 0; e < 2; ++e) {  // two columns
+                const Split a0(u[2 * k].w[2 * e]), a1(u[2 * k].w[2 * e + 1]), a2(u[2 * k + 1].w[2 * e]), a3(u[2 * k + 1].w[2 * e + 1]);
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][2 * k + h], a0, a1, a2, a3, w[nb][b][0], w[nb][b][1]);
+                for (int nb = 0; nb < NB; ++nb) {
+                  const Split b0(w[0][nb][b][(2 * k) % (TF32 ? 4 : 2)]), b1(w[0][nb][b][(2 * k + 1) % (TF32 ? 4 : 2)]);
+                  float(&d)[4] = o[nb][p][e];
+                  mma<M>(d, a0.low, a1.low, a2.low, a3.low, b0.high, b1.high);
+                  mma<M>(d, a0.high, a1.high, a2.high, a3.high, b0.low, b1.low);
+                  mma<M>(d, a0.high, a1.high, a2.high, a3.high, b0.high, b1.high);
+                }
               }
-            } else {
-              const uint32_t a0 = __byte_perm(u[0].w[k], u[1].w[k], 0x5410);
-              const uint32_t a1 = __byte_perm(u[0].w[k], u[1].w[k], 0x7632);
-              const uint32_t a2 = __byte_perm(u[2].w[k], u[3].w[k], 0x5410);
-              const uint32_t a3 = __byte_perm(u[2].w[k], u[3].w[k], 0x7632);
+          } else {
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][k], a0, a1, a2, a3, w[nb][b][0], w[nb][b][1]);
+            for (int k = 0; k < S::VB / 4; ++k) {
+              if constexpr (FP8) {
+                // the codes of two tokens side by side, column by column
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t sel = h ? 0x7362 : 0x5140;
+                  const uint32_t x = __byte_perm(u[0].w[k], u[1].w[k], sel), y = __byte_perm(u[2].w[k], u[3].w[k], sel);
+                  const uint32_t a0 = e4m3x2_to_half2(x), a1 = e4m3x2_to_half2(x >> 16);
+                  const uint32_t a2 = e4m3x2_to_half2(y), a3 = e4m3x2_to_half2(y >> 16);
+#pragma unroll
+                  for (int i = 0; i < QN; ++i)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                      mma<M>(o[nb][p][2 * k + h], a0, a1, a2, a3, w[i][nb][b][0], w[i][nb][b][1]);
+                }
+              } else {
+                const uint32_t a0 = __byte_perm(u[0].w[k], u[1].w[k], 0x5410);
+                const uint32_t a1 = __byte_perm(u[0].w[k], u[1].w[k], 0x7632);
+                const uint32_t a2 = __byte_perm(u[2].w[k], u[3].w[k], 0x5410);
+                const uint32_t a3 = __byte_perm(u[2].w[k], u[3].w[k], 0x7632);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][k], a0, a1, a2, a3, w[0][nb][b][0], w[0][nb][b][1]);
+              }
             }
           }
           if (n + VG < VN) {
@@ -529,7 +613,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
           const int r = 8 * nb + 2 * cl + j;
           if (r >= rows) continue;
           float by = piece ? 1.0f : sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-          if constexpr (FP8) by = __fmul_rn(by, vref);
+          if constexpr (FP8) by = __fmul_rn(by, SPLIT ? __fmul_rn(vref, 0x1p-14f) : vref);
 #pragma unroll
           for (int p = 0; p < S::VP; ++p) {
             float out[S::CE];
@@ -540,13 +624,13 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
             }
             const int c = (8 * p + gl) * S::CE;
 #pragma unroll
-            for (int i = 0; i < S::CE; i += 8) {
+            for (int i = 0; i < S::CE; i += S::LOAD) {
               if (c + i >= D) continue;
-              const float(&x)[8] = *(const float(*)[8])(out + i);
+              const float(&x)[S::LOAD] = *(const float(*)[S::LOAD])(out + i);
               if (piece) {
                 float2* dst = (float2*)(to.o + r * D + c + i);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) dst[k] = make_float2(x[2 * k], x[2 * k + 1]);
+                for (int k = 0; k < S::LOAD / 2; ++k) dst[k] = make_float2(x[2 * k], x[2 * k + 1]);
               } else {
                 st_stream<16>((T*)a.out.p + g.b * a.out.token + (int64_t)(h0 + r) * a.out.head + c + i,
                               Vec<T, 16>::narrow(x));
@@ -609,9 +693,13 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < S::DP / 64; ++i) {
         const int c = 64 * i + 2 * lane;
-        if (c < D)
-          *(uint32_t*)((T*)a.out.p + b * a.out.token + h * a.out.head + c) =
-              Pair<T>::narrow(f2(__fmul_rn(o[i].x, by), __fmul_rn(o[i].y, by)));
+        T* out = (T*)a.out.p + b * a.out.token + h * a.out.head + c;
+        const float2 y = make_float2(__fmul_rn(o[i].x, by), __fmul_rn(o[i].y, by));
+        if (c >= D) continue;
+        if constexpr (sizeof(T) == 4)
+          *(float2*)out = y;
+        else
+          *(uint32_t*)out = Pair<T>::narrow(y);
       }
       if (lane == 0 && a.lse) a.lse[(int64_t)b * a.Hq + h] = lse_of(top, sum);
     } else {
@@ -631,47 +719,56 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
 }
 
 template <class T, bool FP8, int DP, int NB>
-cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cudaStream_t s) {
+cudaError_t launch(const DeviceInfo& dev, AttendArgs& a, int64_t* ctas, cudaStream_t s) {
   using S = Shape<T, FP8, DP, NB>;
   const auto kern = attend_mma_kernel<T, S>;
   static std::atomic<int> opted[kOptinDevices];
   const cudaError_t e = allow_shared((const void*)kern, dev, opted);
   if (e != cudaSuccess) return e;
   *ctas = std::min(kAttendMmaCtas, (int64_t)dev.sm_count);
+  a.rows = 8 * NB;
   MmaArgs m;
   m.a = a;
   m.page = divisor((uint32_t)a.c.page_size);
   m.whole = a.c.page_size % 16 == 0;
   m.page_rows = (int)(a.c.page_stride / a.c.D);
-  m.warp_partial = a.partial + *ctas * 2 * std::min(a.group, kAttendRows) * (a.c.D + 2);
+  m.warp_partial = a.partial + *ctas * 2 * std::min(a.group, a.rows) * (a.c.D + 2);
   return launch_after(kern, (unsigned)*ctas, S::THREADS, S::SMEM, s, m);
 }
 
+// (fp32 queries: eight heads at a time, for registers)
 template <class T, bool FP8, int DP>
-cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cudaStream_t s) {
-  return a.group <= 8 ? launch<T, FP8, DP, 1>(dev, a, ctas, s) : launch<T, FP8, DP, 2>(dev, a, ctas, s);
+cudaError_t launch(const DeviceInfo& dev, AttendArgs& a, int64_t* ctas, cudaStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (a.group > 8) return launch<T, FP8, DP, 2>(dev, a, ctas, s);
+  }
+  return launch<T, FP8, DP, 1>(dev, a, ctas, s);
 }
 template <class T, bool FP8>
-cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cudaStream_t s) {
+cudaError_t launch(const DeviceInfo& dev, AttendArgs& a, int64_t* ctas, cudaStream_t s) {
   return a.c.D <= 64    ? launch<T, FP8, 64>(dev, a, ctas, s)
          : a.c.D <= 128 ? launch<T, FP8, 128>(dev, a, ctas, s)
                         : launch<T, FP8, 256>(dev, a, ctas, s);
 }
-template <class T>
-cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cudaStream_t s) {
-  return a.c.format == DIT_E4M3 ? launch<T, true>(dev, a, ctas, s) : launch<T, false>(dev, a, ctas, s);
-}
 
 }  // namespace
 
-bool attend_mma_takes(int dtype, bool granules, const AttendArgs& a) {
-  return dtype != 2 && granules && a.c.D <= 256 && a.capacity > 0 && a.c.page_stride % a.c.D == 0 &&
+// (two compilations: 16-bit types in one, fp32 in the other)
+#ifdef DIT_ATTEND_FP32
+cudaError_t launch_attend_mma_fp32(const DeviceInfo& dev, AttendArgs& a, int64_t* ctas, cudaStream_t s) {
+  return a.c.format == DIT_E4M3 ? launch<float, true>(dev, a, ctas, s) : launch<float, false>(dev, a, ctas, s);
+}
+#else
+bool attend_mma_takes(bool granules, const AttendArgs& a) {
+  return granules && a.c.D <= 256 && a.capacity > 0 && a.c.page_stride % a.c.D == 0 &&
          a.c.pages * (a.c.page_stride / a.c.D) <= 0x7FFFFFFF;
 }
-
-cudaError_t launch_attend_mma(const DeviceInfo& dev, int dtype, const AttendArgs& a, int64_t* ctas,
-                              cudaStream_t s) {
-  return dtype == 1 ? launch<__half>(dev, a, ctas, s) : launch<__nv_bfloat16>(dev, a, ctas, s);
+cudaError_t launch_attend_mma(const DeviceInfo& dev, int dtype, AttendArgs& a, int64_t* ctas, cudaStream_t s) {
+  const bool fp8 = a.c.format == DIT_E4M3;
+  return dtype == 2   ? launch_attend_mma_fp32(dev, a, ctas, s)
+         : dtype == 1 ? (fp8 ? launch<__half, true>(dev, a, ctas, s) : launch<__half, false>(dev, a, ctas, s))
+                      : (fp8 ? launch<__nv_bfloat16, true>(dev, a, ctas, s) : launch<__nv_bfloat16, false>(dev, a, ctas, s));
 }
+#endif
 
 }  // namespace dit
