@@ -359,8 +359,11 @@ class KVCache:
             _tensor(t, name)
             if t.get_device() != k.get_device():
                 raise ValueError(f"{name} is on {t.device}, expected {k.device}")
-            if not t[:1].is_contiguous():
-                raise ValueError(f"the pages of {name} must be contiguous")
+            step = 1  # (sizes of one have any stride)
+            for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
+                if size > 1 and stride != step:
+                    raise ValueError(f"the pages of {name} must be contiguous")
+                step *= size
         if k.dim() != 4 or v.shape != k.shape or v.dtype is not k.dtype:
             raise ValueError("k and v must be [pages, heads, page_size, D], of one shape and dtype")
         if fp8:

@@ -55,6 +55,10 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void add(float (&d)[4], const float (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = __fadd_rn(d[i], x[i]);
+}
 // fp32 as the nearest tf32 and the rest, of which the tensor cores read the first 11 bits
 struct Split {
   uint32_t high, low;
@@ -110,7 +114,8 @@ __device__ __forceinline__ uint32_t key_at(uint32_t key, int p) {
 // T: the queries' type; FP8: an E4M3 cache; DP: columns, D rounded up (the rest is zero); NB: blocks of
 // eight heads.  With fp32 queries every product is one of two parts each (SPLIT): keys and values of fp32 as two
 // tf32 numbers, queries and weights too, or, over an E4M3 cache, as two fp16 numbers; what is left out is 2^-22 of
-// a product.
+// a product.  The tensor cores cut their sums off where fp32 rounds them: such sums are kept short (a product of the
+// high parts, or a tile) and added up outside (lse over 128 columns is 8e-8 off so, in long sums 6.5e-7).
 template <class T, bool FP8_, int DP_, int NB_>
 struct Shape {
   static constexpr bool FP8 = FP8_, SPLIT = sizeof(T) == 4, TF32 = SPLIT && !FP8;
@@ -385,7 +390,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
 
         // pieces of keys, KG at a time, in registers before the products that wait for each other
         constexpr int KG = S::KP < 4 ? S::KP : 4;
-        float s[NB][MB][4] = {};
+        float s[NB][MB][4] = {}, rest[TF32 ? NB : 1][TF32 ? MB : 1][4] = {};
 #pragma unroll
         for (int p0 = 0; p0 < S::KP; p0 += KG) {
           Raw<16> x[MB][KG], y[MB][KG];
@@ -411,9 +416,11 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
 #pragma unroll
                   for (int nb = 0; nb < NB; ++nb) {
                     const Split b0(q[0][nb][step][0]), b1(q[0][nb][step][1]);
-                    mma<M>(s[nb][b], a0.low, a1.low, a2.low, a3.low, b0.high, b1.high);
-                    mma<M>(s[nb][b], a0.high, a1.high, a2.high, a3.high, b0.low, b1.low);
-                    mma<M>(s[nb][b], a0.high, a1.high, a2.high, a3.high, b0.high, b1.high);
+                    mma<M>(rest[nb][b], a0.low, a1.low, a2.low, a3.low, b0.high, b1.high);
+                    mma<M>(rest[nb][b], a0.high, a1.high, a2.high, a3.high, b0.low, b1.low);
+                    float sum[4] = {};
+                    mma<M>(sum, a0.high, a1.high, a2.high, a3.high, b0.high, b1.high);
+                    add(s[nb][b], sum);
                   }
                 } else {
                   const uint32_t a0 = FP8 ? e4m3x2_to_half2(u.w[i]) : u.w[2 * i];
@@ -421,13 +428,25 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
                   const uint32_t a2 = FP8 ? e4m3x2_to_half2(u.w[i] >> 16) : u.w[2 * i + 1];
                   const uint32_t a3 = FP8 ? e4m3x2_to_half2(v.w[i] >> 16) : v.w[2 * i + 1];
 #pragma unroll
-                  for (int k = 0; k < QN; ++k)
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-                      mma<M>(s[nb][b], a0, a1, a2, a3, q[k][nb][step][0], q[k][nb][step][1]);
+                  for (int nb = 0; nb < NB; ++nb) {
+                    if constexpr (SPLIT) {
+                      float sum[4] = {};
+                      mma<M>(sum, a0, a1, a2, a3, q[QN - 1][nb][step][0], q[QN - 1][nb][step][1]);
+                      mma<M>(sum, a0, a1, a2, a3, q[0][nb][step][0], q[0][nb][step][1]);
+                      add(s[nb][b], sum);
+                    } else {
+                      mma<M>(s[nb][b], a0, a1, a2, a3, q[0][nb][step][0], q[0][nb][step][1]);
+                    }
+                  }
                 }
               }
           }
+        }
+        if constexpr (TF32) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int b = 0; b < MB; ++b) add(s[nb][b], rest[nb][b]);
         }
         // the first pieces of the values, on their way meanwhile
         const uint32_t values = from + S::STAGE / 2;
@@ -550,19 +569,23 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
           Raw<S::VB>(&u)[4] = v[n % VG];
           if constexpr (TF32) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k)  // eight tokens
+            for (int e = 0; e < 2; ++e) {  // two columns
+              float sum[NB][4] = {};
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {  // two columns
+              for (int k = 0; k < 2; ++k) {  // eight tokens
                 const Split a0(u[2 * k].w[2 * e]), a1(u[2 * k].w[2 * e + 1]), a2(u[2 * k + 1].w[2 * e]), a3(u[2 * k + 1].w[2 * e + 1]);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                   const Split b0(w[0][nb][b][(2 * k) % (TF32 ? 4 : 2)]), b1(w[0][nb][b][(2 * k + 1) % (TF32 ? 4 : 2)]);
-                  float(&d)[4] = o[nb][p][e];
+                  float(&d)[4] = sum[nb];
                   mma<M>(d, a0.low, a1.low, a2.low, a3.low, b0.high, b1.high);
                   mma<M>(d, a0.high, a1.high, a2.high, a3.high, b0.low, b1.low);
                   mma<M>(d, a0.high, a1.high, a2.high, a3.high, b0.high, b1.high);
                 }
               }
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) add(o[nb][p][e], sum[nb]);
+            }
           } else {
 #pragma unroll
             for (int k = 0; k < S::VB / 4; ++k) {
@@ -575,10 +598,16 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
                   const uint32_t a0 = e4m3x2_to_half2(x), a1 = e4m3x2_to_half2(x >> 16);
                   const uint32_t a2 = e4m3x2_to_half2(y), a3 = e4m3x2_to_half2(y >> 16);
 #pragma unroll
-                  for (int i = 0; i < QN; ++i)
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-                      mma<M>(o[nb][p][2 * k + h], a0, a1, a2, a3, w[i][nb][b][0], w[i][nb][b][1]);
+                  for (int nb = 0; nb < NB; ++nb) {
+                    if constexpr (SPLIT) {
+                      float sum[4] = {};
+                      mma<M>(sum, a0, a1, a2, a3, w[QN - 1][nb][b][0], w[QN - 1][nb][b][1]);
+                      mma<M>(sum, a0, a1, a2, a3, w[0][nb][b][0], w[0][nb][b][1]);
+                      add(o[nb][p][2 * k + h], sum);
+                    } else {
+                      mma<M>(o[nb][p][2 * k + h], a0, a1, a2, a3, w[0][nb][b][0], w[0][nb][b][1]);
+                    }
+                  }
                 }
               } else {
                 const uint32_t a0 = __byte_perm(u[0].w[k], u[1].w[k], 0x5410);
