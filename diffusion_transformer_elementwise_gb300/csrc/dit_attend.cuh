@@ -54,6 +54,13 @@ struct Plan {
   }
 };
 
+// a / b of positive numbers, in 32 bits where they fit
+__device__ __forceinline__ int64_t divided(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// A segment's name.
+__device__ __forceinline__ int64_t segment_id(int b, int s) { return (int64_t)b << 32 | (uint32_t)s; }
+
 // A place of the line: a sequence, and where on the line it starts.
 struct Mark {
   int b;
@@ -162,7 +169,7 @@ struct Walk {
       : at(at), end(end), start(mark.start), b(mark.b), s(0), q(a, mark.b) {
     if (at >= end) return;
     const int64_t n = q.tiles + line.extra;
-    s = (int)((at - start) / n);
+    s = (int)divided(at - start, n);
     start += s * n;
   }
   __device__ __forceinline__ bool next(const AttendArgs& a, const Line& line, Segment& g) {

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
     if (g.head || g.tail) {
       const int slot = g.head ? 0 : 1;
       float* out = a.partial + ((int64_t)blockIdx.x * 2 + slot) * slot_rows * (D + 2);
-      if (tid == 0) a.owner[2 * blockIdx.x + slot] = (int64_t)g.b * line.segments + g.s;
+      if (tid == 0) a.owner[2 * blockIdx.x + slot] = segment_id(g.b, g.s);
       for (int i = tid; i < rows * D; i += kThreads) out[2 * slot_rows + i] = o[i];
       if (tid < rows) {
         out[tid] = m[tid];
@@ -152,75 +152,68 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
 }
 
 // The join of the segments that begin in CTA blockIdx.x and end in a later one: row blockIdx.y of it.  A warp has
-// every kJoinWarps-th of the parts, four columns a lane at a time.
+// every kJoinWarps-th of the parts, columns lane, lane + 32, ..., each part scaled to the largest maximum so far.  What
+// a part holds is loaded beside its owner's name, before that is known to be this segment's.
 constexpr int kJoinWarps = 8;
 struct JoinArgs {
   AttendArgs a;
   int ctas;
 };
-template <class T>
+template <class T, int DP>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ JoinArgs j) {
-  __shared__ float most[kJoinWarps], sums[kJoinWarps], columns[kJoinWarps][kMaxD];
+  constexpr int N = DP / 32;
+  __shared__ float most[kJoinWarps], sums[kJoinWarps], columns[kJoinWarps][DP];
   const AttendArgs& a = j.a;
   const int D = (int)a.c.D, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y, cta = blockIdx.x;
+  const int slot_rows = min(a.group, a.rows);
+  const int64_t size = (int64_t)slot_rows * (D + 2);
   after_previous();
   let_next();
   const int64_t id = a.owner[2 * cta + 1];
   if (id < 0) return;
   const int blocks = (a.group + a.rows - 1) / a.rows;
-  const int segments = (int)a.c.heads * blocks;
-  const int b = (int)(id / segments), s = (int)(id - (int64_t)b * segments);
+  const int b = (int)(id >> 32), s = (int)(uint32_t)id;
   const int head = s / blocks, row0 = (s - head * blocks) * a.rows;
-  const int slot_rows = min(a.group, a.rows);
   if (r >= min(a.rows, a.group - row0)) return;
-  int count = 1;  // parts: this CTA's, and the first ones of those after it
-  for (;; count += 32) {
-    const int k = cta + count + lane;
-    const uint32_t other = __ballot_sync(0xFFFFFFFFu, k >= j.ctas || a.owner[2 * min(k, j.ctas - 1)] != id);
-    if (other == 0) continue;
-    count += __ffs(other) - 1;
-    break;
+  float m = -INFINITY, l = 0.0f, o[N] = {};
+  // (the parts of a segment are those of CTAs one after the other: the first is the second part of its CTA)
+#pragma unroll 2
+  for (int k = warp;; k += kJoinWarps) {
+    const int at = min(cta + k, j.ctas - 1);
+    const float* p = a.partial + (2 * (int64_t)at + (k == 0)) * size;
+    const int64_t owner = a.owner[2 * at + (k == 0)];
+    const float pm = p[r], pl = p[slot_rows + r];
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 32 * i + lane < D ? p[2 * slot_rows + r * D + 32 * i + lane] : 0.0f;
+    if (cta + k >= j.ctas || owner != id) break;
+    const float now = fmaxf(m, pm), base = now == -INFINITY ? 0.0f : now;
+    const float f = exp2f(__fadd_rn(m, -base)), g = exp2f(__fadd_rn(pm, -base));
+    m = now;
+    l = __fmaf_rn(l, f, __fmul_rn(pl, g));
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = __fmaf_rn(o[i], f, __fmul_rn(v[i], g));
   }
-  const int64_t size = (int64_t)slot_rows * (D + 2);
-  auto part = [&](int k) { return a.partial + (2 * (int64_t)(cta + k) + (k == 0)) * size; };
-  float m = -INFINITY;
-  for (int k = threadIdx.x; k < count; k += 32 * kJoinWarps) m = fmaxf(m, part(k)[r]);
+  if (lane == 0) most[warp] = m, sums[warp] = l;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  if (lane == 0) most[warp] = m;
+  for (int i = 0; i < N; ++i) columns[warp][32 * i + lane] = o[i];
   __syncthreads();
+  float top = -INFINITY, by[kJoinWarps], total = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, most[w]);
-  const float base = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f;
-  for (int c0 = 0; c0 < D; c0 += 128) {
-    float o[4] = {};
-    l = 0.0f;
-#pragma unroll 4
-    for (int k = warp; k < count; k += kJoinWarps) {
-      const float* p = part(k);
-      const float f = exp2f(__fadd_rn(p[r], -base));
-      l = __fmaf_rn(p[slot_rows + r], f, l);
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, most[w]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c0 + 32 * i + lane < D) o[i] = __fmaf_rn(p[2 * slot_rows + r * D + c0 + 32 * i + lane], f, o[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) columns[warp][c0 + 32 * i + lane] = o[i];
+  for (int w = 0; w < kJoinWarps; ++w) {
+    by[w] = exp2f(__fadd_rn(most[w], -(top == -INFINITY ? 0.0f : top)));
+    total = __fmaf_rn(sums[w], by[w], total);
   }
-  if (lane == 0) sums[warp] = l;
-  __syncthreads();
-  l = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) l = __fadd_rn(l, sums[w]);
   const int h = head * a.group + row0 + r;
   for (int c = threadIdx.x; c < D; c += 32 * kJoinWarps) {
-    float o = 0.0f;
+    float y = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) o = __fadd_rn(o, columns[w][c]);
-    ((T*)a.out.p)[b * a.out.token + h * a.out.head + c] = from_float<T>(l == 0.0f ? 0.0f : __fdiv_rn(o, l));
+    for (int w = 0; w < kJoinWarps; ++w) y = __fmaf_rn(columns[w][c], by[w], y);
+    ((T*)a.out.p)[b * a.out.token + h * a.out.head + c] = from_float<T>(total == 0.0f ? 0.0f : __fdiv_rn(y, total));
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[(int64_t)b * a.Hq + h] = lse_of(m, l);
+  if (threadIdx.x == 0 && a.lse) a.lse[(int64_t)b * a.Hq + h] = lse_of(top, total);
 }
 
 template <class T, class K>
@@ -244,7 +237,8 @@ cudaError_t launch(const DeviceInfo& dev, int dtype, bool mma, AttendArgs a, cud
                                                  : launch<T, T>(dev, a, &ctas, s);
   if (e != cudaSuccess) return e;
   const JoinArgs j{a, (int)ctas};
-  return launch_after(join_kernel<T>, dim3((unsigned)ctas, (unsigned)std::min(a.group, a.rows)), 32 * kJoinWarps, 0, s, j);
+  const auto join = a.c.D <= 128 ? join_kernel<T, 128> : a.c.D <= 256 ? join_kernel<T, 256> : join_kernel<T, kMaxD>;
+  return launch_after(join, dim3((unsigned)ctas, (unsigned)std::min(a.group, a.rows)), 32 * kJoinWarps, 0, s, j);
 }
 
 }  // namespace

@@ -55,9 +55,10 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void add(float (&d)[4], const float (&x)[4]) {
+template <int N>
+__device__ __forceinline__ void add(float (&d)[N], const float (&x)[N]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) d[i] = __fadd_rn(d[i], x[i]);
+  for (int i = 0; i < N; ++i) d[i] = __fadd_rn(d[i], x[i]);
 }
 // fp32 as the nearest tf32 and the rest, of which the tensor cores read the first 11 bits
 struct Split {
@@ -160,7 +161,7 @@ struct MmaArgs {
   Divisor page;         // page_size
   int page_rows;        // rows of D from page to page
   bool whole;           // no page ends within half a tile
-  float* warp_partial;  // [ctas][warps][2][rows][D + 2]: the parts of segments that warps share
+  float* warp_partial;  // [ctas][warps][2][rows][D]: the unscaled outputs of segments that warps share
 };
 
 // a part of a segment in the workspace: maxima, sums, and the unscaled output
@@ -177,8 +178,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
   constexpr int NB = S::NB, NCE = S::CE / 2, MB = S::MB, TOKENS = S::TOKENS;
   constexpr bool SPLIT = S::SPLIT, TF32 = S::TF32;
   __shared__ Plan<S::THREADS> plan;
-  __shared__ int64_t owner[S::WARPS][2];  // the warps' shared segments, or -1
-  __shared__ bool open[S::WARPS];         // whether the first goes on in the next warp's part
+  // the segments that warps share: which (or -1), their maxima and sums, and whether the first goes on in
+  // the next warp's part
+  __shared__ int64_t owner[S::WARPS][2];
+  __shared__ float piece_m[S::WARPS][2][8 * NB], piece_l[S::WARPS][2][8 * NB];
+  __shared__ bool open[S::WARPS];
+  __shared__ float factors[S::WARPS][S::WARPS + 1];  // of the pieces that a warp joins
   extern __shared__ __align__(1024) unsigned char space[];
   const AttendArgs& a = args.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -195,18 +200,18 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
   after_previous();
   const int64_t total = line.total(a, plan);
   const int64_t warps = (int64_t)gridDim.x * S::WARPS;
-  const int64_t per = max((int64_t)kLeast, (total + warps - 1) / warps);
+  const int64_t per = max((int64_t)kLeast, divided(total + warps - 1, warps));
   const int64_t begin = min((blockIdx.x * (int64_t)S::WARPS + warp) * per, total), end = min(begin + per, total);
   const int64_t cta_begin = min(blockIdx.x * (int64_t)S::WARPS * per, total);
   if (tid < 2) a.owner[2 * blockIdx.x + tid] = -1;
   let_next();
   if (cta_begin >= total) return;
-  const Mark mark = line.find(a, cta_begin, plan);
+  const Mark mark = a.B <= S::THREADS ? Mark{0, 0} : line.find(a, cta_begin, plan);
   const int64_t slot = (blockIdx.x * (int64_t)S::WARPS + warp) * 2;
   if (lane < 2) owner[warp][lane] = -1;
 
   if (begin < end) {
-    const Mark mine = line.find_from(a, begin, mark);
+    const Mark mine = a.B <= S::THREADS ? line.find(a, begin, plan) : line.find_from(a, begin, mark);
 
     // ----- copies, some tiles ahead -----
     Walk ahead(a, line, begin, end, mine);
@@ -629,9 +634,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
 
       // ----- the segment's result, or its piece -----
       const bool piece = g.head || g.tail;
-      const Piece to(args.warp_partial, slot + (g.head ? 0 : 1), slot_rows, D);
+      float* to = args.warp_partial + (slot + (g.head ? 0 : 1)) * slot_rows * D;
       if (piece && lane == 0) {
-        owner[warp][g.head ? 0 : 1] = (int64_t)g.b * line.segments + g.s;
+        owner[warp][g.head ? 0 : 1] = segment_id(g.b, g.s);
         if (g.head) open[warp] = g.open;
       }
 #pragma unroll
@@ -657,7 +662,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
               if (c + i >= D) continue;
               const float(&x)[S::LOAD] = *(const float(*)[S::LOAD])(out + i);
               if (piece) {
-                float2* dst = (float2*)(to.o + r * D + c + i);
+                float2* dst = (float2*)(to + r * D + c + i);
 #pragma unroll
                 for (int k = 0; k < S::LOAD / 2; ++k) dst[k] = make_float2(x[2 * k], x[2 * k + 1]);
               } else {
@@ -668,8 +673,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
           }
           if (gl != 0) continue;
           if (piece) {
-            to.m[r] = m[nb][j];
-            to.l[r] = sum;
+            piece_m[warp][g.head ? 0 : 1][r] = m[nb][j];
+            piece_l[warp][g.head ? 0 : 1][r] = sum;
           } else if (a.lse) {
             a.lse[(int64_t)g.b * a.Hq + h0 + r] = lse_of(m[nb][j], sum);
           }
@@ -679,70 +684,64 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
   }
 
   // ----- pieces of the same segment in this CTA, together: a warp takes a head of one -----
+  // (short code: what runs once is bound by fetching its instructions)
   __syncthreads();
-  const int64_t first = blockIdx.x * (int64_t)S::WARPS * 2;
+  static_assert(S::WARPS < 32, "a piece a lane");
+#pragma unroll 1
   for (int task = warp; task < (S::WARPS + 1) * slot_rows; task += S::WARPS) {
     // chain 0 begins before this CTA, chain i + 1 with the second piece of warp i
     const int chain = task / slot_rows, r = task - chain * slot_rows;
-    const int64_t id = chain == 0 ? owner[0][0] : owner[chain - 1][1];
+    const bool begun = chain > 0;
+    const int64_t id = begun ? owner[chain - 1][1] : owner[0][0];
     if (id < 0) continue;
-    const int b = (int)(id / line.segments), s = (int)(id - (int64_t)b * line.segments);
+    const int b = (int)(id >> 32), s = (int)(uint32_t)id;
     const int key_head = s / blocks, row0 = (s - key_head * blocks) * 8 * NB;
     if (r >= min(8 * NB, a.group - row0)) continue;
-    const int h = key_head * a.group + row0 + r;
-    int last = chain;  // the warps [chain, last) go on with it
-    while (last < S::WARPS && owner[last][0] == id) ++last;
-    const bool begun = chain > 0, done = begun && last > chain && !open[last - 1];
+    // the warps [chain, last) go on with it
+    const int last = __ffs(~__ballot_sync(0xFFFFFFFFu, lane >= chain && lane < S::WARPS && owner[min(lane, S::WARPS - 1)][0] == id) >> chain) - 1 + chain;
+    const bool done = begun && last > chain && !open[last - 1];
     const int pieces = last - chain + begun;
-    auto at = [&](int k) {
-      return Piece(args.warp_partial, first + (begun ? 2 * (chain - 1 + k) + (k == 0) : 2 * k), slot_rows, D);
-    };
     // lane k has piece k's maximum and sum
-    static_assert(S::WARPS < 32, "a piece a lane");
-    const float m = lane < pieces ? at(lane).m[r] : -INFINITY;
+    auto from = [&](int k) { return begun ? 2 * (chain - 1 + k) + (k == 0) : 2 * k; };
+    const bool on = lane < pieces;
+    const float m = on ? (&piece_m[0][0][0])[from(lane) * 8 * NB + r] : -INFINITY;
     float top = m;
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
     const float f = exp2_fast(__fadd_rn(m, -(top == -INFINITY ? 0.0f : top)));
-    const float sum = lanes_sum<32>(lane < pieces ? __fmul_rn(at(lane).l[r], f) : 0.0f);
-    float2 o[S::DP / 64] = {};
+    const float sum = lanes_sum<32>(on ? __fmul_rn((&piece_l[0][0][0])[from(lane) * 8 * NB + r], f) : 0.0f);
+    if (on) factors[warp][lane] = f;
+    __syncwarp();
+    const float* base = args.warp_partial + (blockIdx.x * (int64_t)S::WARPS * 2 * slot_rows + r) * D;
+    const float by = !done ? 1.0f : sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+    const int h = key_head * a.group + row0 + r;
+    const Piece p(a.partial, 2 * blockIdx.x + begun, slot_rows, D);
+#pragma unroll 1
+    for (int c = 2 * lane; c < D; c += 64) {
+      float2 o = {};
 #pragma unroll 4
-    for (int k = 0; k < pieces; ++k) {
-      const Piece p = at(k);
-      const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-#pragma unroll
-      for (int i = 0; i < S::DP / 64; ++i) {
-        const int c = 64 * i + 2 * lane;
-        const float2 v = c < D ? *(const float2*)(p.o + r * D + c) : float2{};
-        o[i] = make_float2(__fmaf_rn(v.x, fk, o[i].x), __fmaf_rn(v.y, fk, o[i].y));
+      for (int k = 0; k < pieces; ++k) {
+        const float2 v = *(const float2*)(base + from(k) * slot_rows * D + c);
+        const float fk = factors[warp][k];
+        o = make_float2(__fmaf_rn(v.x, fk, o.x), __fmaf_rn(v.y, fk, o.y));
       }
+      o = make_float2(__fmul_rn(o.x, by), __fmul_rn(o.y, by));
+      T* out = (T*)a.out.p + b * a.out.token + h * a.out.head + c;
+      if (!done)
+        *(float2*)(p.o + r * D + c) = o;
+      else if constexpr (sizeof(T) == 4)
+        *(float2*)out = o;
+      else
+        *(uint32_t*)out = Pair<T>::narrow(o);
     }
-    if (done) {
-      const float by = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-#pragma unroll
-      for (int i = 0; i < S::DP / 64; ++i) {
-        const int c = 64 * i + 2 * lane;
-        T* out = (T*)a.out.p + b * a.out.token + h * a.out.head + c;
-        const float2 y = make_float2(__fmul_rn(o[i].x, by), __fmul_rn(o[i].y, by));
-        if (c >= D) continue;
-        if constexpr (sizeof(T) == 4)
-          *(float2*)out = y;
-        else
-          *(uint32_t*)out = Pair<T>::narrow(y);
-      }
-      if (lane == 0 && a.lse) a.lse[(int64_t)b * a.Hq + h] = lse_of(top, sum);
-    } else {
-      const Piece p(a.partial, 2 * blockIdx.x + begun, slot_rows, D);
-#pragma unroll
-      for (int i = 0; i < S::DP / 64; ++i) {
-        const int c = 64 * i + 2 * lane;
-        if (c < D) *(float2*)(p.o + r * D + c) = o[i];
-      }
-      if (lane == 0) {
-        p.m[r] = top;
-        p.l[r] = sum;
-        a.owner[2 * blockIdx.x + begun] = id;
-      }
+    __syncwarp();
+    if (lane != 0) continue;
+    if (!done) {
+      p.m[r] = top;
+      p.l[r] = sum;
+      a.owner[2 * blockIdx.x + begun] = id;
+    } else if (a.lse) {
+      a.lse[(int64_t)b * a.Hq + h] = lse_of(top, sum);
     }
   }
 }
