@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
         if (t >= ag.lo && t < ag.hi) {
           const int n = (int)quotient(t, args.page);
           place = t - n * (int)args.page.d;
-          page = __ldg(a.pages + ag.b * a.pages_stride + n);
+          page = a.pages[ag.b * a.pages_stride + n];
         }
       }
     };
@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
         for (int i = 0; i < LOADS; ++i) {
           const int c = (i / SUB * 4 + cl) * S::PER + i % SUB * S::LOAD;
           raw[i] = Raw<16>{};
-          if (real && c < D) raw[i] = ld_bcast<16>(from + c);
+          // (not by the read-only path: the kernel before, which wrote them, may have run beside this one)
+          if (real && c < D) raw[i] = ld_stream<16>(from + c);
         }
         float up = 1.0f;
         if constexpr (FP8 && !std::is_same<T, __half>::value) {

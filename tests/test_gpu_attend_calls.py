@@ -215,3 +215,86 @@ def test_a_graph_with_other_lengths_and_pages():
     graph.replay()
     n = [700, 31]
     check_attention(out, lse, q, lambda b, h: kd[1 - b, :n[b], h // 4], lambda b, h: vd[1 - b, :n[b], h // 4], n, 128 ** -0.5)
+
+
+def test_no_pages():
+    """A page table without columns, and a cache without pages: no token anywhere."""
+    for t in (torch.bfloat16, torch.float32):
+        q = torch.ones(3, 4, 64, dtype=t, device="cuda")
+        lengths = torch.tensor([5, 0, 9], device="cuda")
+        for cache, width in ((dit.KVCache.empty(4, 2, 16, 64, t), 0), (dit.KVCache.empty(0, 2, 16, 64, t), 3)):
+            out, lse = dit.paged_attention(q, cache, torch.zeros(3, width, dtype=torch.int32, device="cuda"), lengths,
+                                           need_lse=True)
+            assert (out == 0).all() and (lse == -float("inf")).all()
+    dit.cache_write(cache, q[:, :2], q[:, :2], torch.tensor([0, 1, 2], device="cuda"))
+    k, v = dit.cache_read(cache, torch.tensor([0, 1, 2], device="cuda"))
+    assert (k == 0).all() and (v == 0).all()
+
+
+def test_graphs_of_other_nodes():
+    """Captured behind a fill, a copy and the ends of two forked streams, which are no kernels of this library."""
+    s = inputs(dit, torch, torch.bfloat16, 64, 200, True)
+    want = work(dit, s)
+    torch.cuda.synchronize()
+    source = {n: s[n].clone() for n in ("qkv", "positions", "slots", "lengths", "pages")}
+    side = [torch.cuda.Stream() for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        for n, st in (("qkv", side[0]), ("positions", side[1])):
+            st.wait_stream(main)
+            with torch.cuda.stream(st):
+                s[n].zero_()
+                s[n].copy_(source[n])
+        s["cache"].k.view(torch.uint8).zero_()
+        s["cache"].v.view(torch.uint8).zero_()
+        s["cache"].k_scales.zero_()
+        s["cache"].v_scales.zero_()
+        for st in side:
+            main.wait_stream(st)
+        cos, sin = dit.rotary_table(s["positions"], s["freqs"])
+        s["slots"].zero_()
+        s["slots"].copy_(source["slots"])
+        got = work(dit, s)
+    for _ in range(3):
+        for n in ("qkv", "positions", "slots"):
+            s[n].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(got, want, strict=True))
+        assert same(cos, want[0])
+
+
+def test_rows_written_in_place_by_the_call_before():
+    """A chain of calls that read what the one before has just written in place, in views of any kind."""
+    for t, D in ((torch.bfloat16, 34), (torch.float32, 35), (torch.bfloat16, 128)):
+        L = 700
+        qkv = act(L, 4, D, tag="chain").to(t)
+        w = act(D, tag="w").to(t)
+        cos, sin = dit.rotary_table(torch.arange(L, device="cuda"), dit.rotary_frequencies(D // 2))
+        cache = dit.KVCache.empty(L // 4, 1, 4, D, t)
+        slots = torch.arange(L, device="cuda")
+        pages = torch.arange(L // 4, device="cuda").int()[None].expand(L, -1).contiguous()
+        lengths = slots + 1
+        outs = []
+        for _ in range(6):
+            x = qkv.clone()
+            q, k, v = x[:, :2], x[:, 2:3], x[:, 3:]
+            dit.rmsnorm_rope(q, k, w, w, cos, sin, out_q=q, out_k=k)
+            dit.rope(q, k, cos, sin, inverse=True, out_q=q, out_k=k)
+            dit.rope(q, k, cos, sin, out_q=q, out_k=k)
+            dit.cache_write(cache, k, v, slots)
+            out, _ = dit.paged_attention(q, cache, pages, lengths)
+            outs.append((x, out))
+        torch.cuda.synchronize()
+        x = qkv.clone()
+        steps = [lambda: dit.rmsnorm_rope(x[:, :2], x[:, 2:3], w, w, cos, sin, out_q=x[:, :2], out_k=x[:, 2:3]),
+                 lambda: dit.rope(x[:, :2], x[:, 2:3], cos, sin, inverse=True, out_q=x[:, :2], out_k=x[:, 2:3]),
+                 lambda: dit.rope(x[:, :2], x[:, 2:3], cos, sin, out_q=x[:, :2], out_k=x[:, 2:3]),
+                 lambda: dit.cache_write(cache, x[:, 2:3], x[:, 3:], slots)]
+        for step in steps:
+            step()
+            torch.cuda.synchronize()
+        out, _ = dit.paged_attention(x[:, :2], cache, pages, lengths)
+        for a, b in outs:
+            assert torch.equal(a, x) and torch.equal(b, out)
