@@ -392,6 +392,7 @@ class KVCache:
                            (k_scales.stride(0) if self.pages > 1 else rows) if fp8 else 0,
                            self.format)
         self.address = ctypes.addressof(self.array)
+        self.needs = {}  # the attention's workspace by the number of query heads
         self.device_index = k.get_device()
 
     @classmethod
@@ -508,13 +509,15 @@ def paged_attention(q, cache, pages, lengths, scale=None, window=0, out=None, ls
     if lse is None:
         if need_lse:
             lse = _empty((B, Hq), torch.float32, q.device, stream)
-    else:
-        _cuda(("lse", lse))
-        if lse.dtype is not torch.float32 or lse.shape != (B, Hq) or lse.get_device() != dev:
-            raise ValueError(f"lse must be float32 [{B}, {Hq}] on cuda:{dev}")
+    elif (not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32
+          or lse.shape != (B, Hq) or lse.get_device() != dev or not lse.is_contiguous()):
+        _tensor(lse, "lse")
+        raise ValueError(f"lse must be a contiguous float32 [{B}, {Hq}] tensor on cuda:{dev}")
     lib = library()
-    ws, wp, wn = _workspace(workspace, lib.dit_paged_attention_workspace_bytes(Hq, cache.heads, D),
-                            q, stream)
+    need = cache.needs.get(Hq)
+    if need is None:
+        need = cache.needs[Hq] = lib.dit_paged_attention_workspace_bytes(Hq, cache.heads, D)
+    ws, wp, wn = _workspace(workspace, need, q, stream)
     width = pages.shape[1]
     _call(dev, lib.dit_paged_attention, "dit_paged_attention", at + _SIZE,
           None if lse is None else lse.data_ptr(), at, cache.address, pages.data_ptr(),

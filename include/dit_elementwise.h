@@ -690,8 +690,8 @@ dit_status dit_rope(const dit_heads* q_out, const dit_heads* k_out, const dit_he
  * The same after a weighted RMSNorm of each head (its D columns), in one pass and
  * rounded once:  y = x * r * (weight_offset + weight),  r = 1 / sqrt(mean(x^2) + eps).
  * weight_q, weight_k: [D], shared by the heads.  The statistic is a
- * fp32 sum; r is within three fp32 ulps of that sum's.  R may be 0 (the norm alone; cos and
- * sin may then be NULL).
+ * fp32 sum; r is within three fp32 ulps of that sum's (with eps = 0 a head of zeros gives NaN).  R may be
+ * 0 (the norm alone; cos and sin may then be NULL).
  */
 dit_status dit_rmsnorm_rope(const dit_heads* q_out, const dit_heads* k_out, const dit_heads* q,
                             const dit_heads* k, const void* weight_q, const void* weight_k,
@@ -774,7 +774,8 @@ dit_status dit_cache_read(const dit_cache* cache, const dit_heads* k, const dit_
  *   lse: fp32 [B, Hq], or NULL.
  * Keys, values and weights of 16-bit types are multiplied on the tensor cores: the weights
  * are rounded to that type there (E4M3: to fp16, after the value's scale is
- * taken in), products and sums are fp32.  For fp32 queries everything is fp32.
+ * taken in), products and sums are fp32.  For fp32 queries every number is taken in two parts,
+ * 22 bits and more of it (where an infinity among keys or values gives NaN).
  * The length is split over the GPU and the parts joined by a second kernel, in one order for
  * given lengths.
  */
