@@ -290,6 +290,39 @@ struct HeadWalk {
   }
 };
 
+// ---------------------------------------------------------------------------
+// heads of any alignment
+//
+// A warp has a head, a lane its columns lane + 32 i.  What a column is turned with lies in another lane: the
+// warp passes the head's columns through its row in shared memory.
+// ---------------------------------------------------------------------------
+template <int NC>
+struct LaneColumns {
+  int partner[NC], angle[NC];  // the column turned with this one, and the angle's number (-1: not turned)
+  bool second[NC];             // the pair's second column
+  __device__ __forceinline__ LaneColumns(const RopeArgs& a, int lane) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = lane + 32 * i;
+      const bool turn = c < 2 * a.R;
+      second[i] = a.interleaved ? c & 1 : c >= a.R;
+      partner[i] = !turn ? c : a.interleaved ? c ^ 1 : second[i] ? c - a.R : c + a.R;
+      angle[i] = !turn ? -1 : a.interleaved ? c >> 1 : second[i] ? c - a.R : c;
+    }
+  }
+  // cosines, and sines with the partner's sign
+  __device__ __forceinline__ void load(const RopeArgs& a, int64_t row, bool inverse, float (&c)[NC], float (&s)[NC]) const {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      c[i] = 1.0f, s[i] = 0.0f;
+      if (angle[i] < 0) continue;
+      c[i] = a.cos[row * a.R + angle[i]];
+      s[i] = a.sin[row * a.R + angle[i]];
+      if (second[i] == inverse) s[i] = -s[i];
+    }
+  }
+};
+
 // A token's batch, place and row of angles (tokens < 2^31).
 struct TokenAt {
   int64_t batch, place, table;

@@ -4,7 +4,7 @@
 //   m = max|x|,  scale = m / 448,  code = e4m3(x 448 / m)
 // with the quotient in two fp32 numbers, so that a code is the nearest to the exact
 // quotient but where that lies within 2^-24 of itself from the middle of two codes.
-// Both ways are bound by memory, the way in also by instructions (about 500 a warp for four rows each of keys and
+// Both ways are bound by memory, the way in also by instructions (760 of a warp for four rows each of keys and
 // values).  32640 tokens x 8 heads of 128, 1/20 of them padding, bf16: into E4M3 39 us, 4.9 TB/s, 72 % of a
 // copy's rate; back 32 us, 6.2 TB/s, 92 %.  By rows of any kind one after the other, each with its own places, they took 48
 // and 34 us; an element per access 168 and 112.
@@ -16,21 +16,23 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Any view: a warp has rows of a token one after the other, keys and then values of each head, an element per access;
+// AHEAD rows of up to 32 NC columns are loaded before the first is computed (NC = 0: any row, read as often as it
+// takes).  32640 tokens x 8 heads of 99, bf16, into E4M3 80 us, where a copy's rate gives
+// 22, back 59; one row after the other 168 and 112 (of 128 columns).
+constexpr int kColumnAhead = 4;
+
 struct CacheRow {
   int which, head;  // 0: keys, 1: values
-  int64_t token, page, place;
+  int64_t page, place;
   bool inside;
-  __device__ __forceinline__ CacheRow(const CacheArgs& a, int64_t i) {
-    const int rows = 2 * (int)a.c.heads;
-    token = i / rows;
-    head = (int)(i - token * rows);
-    which = head >= (int)a.c.heads;
-    if (which) head -= (int)a.c.heads;
+  __device__ __forceinline__ void find(const CacheArgs& a, int64_t token) {
     const int64_t slot = id_at(a.slots, token, a.ids64);
     inside = slot >= 0 && slot < a.c.pages * a.c.page_size;
-    page = inside ? slot / a.c.page_size : 0;
+    page = inside ? (int64_t)((uint32_t)slot / (uint32_t)a.c.page_size) : 0;
     place = inside ? slot - page * a.c.page_size : 0;
   }
+  __device__ __forceinline__ void row(int n) { which = n & 1, head = n >> 1; }
   // element and scale number in the cache
   __device__ __forceinline__ int64_t at(const dit_cache& c) const {
     return page * c.page_stride + ((int64_t)head * c.page_size + place) * c.D;
@@ -38,61 +40,109 @@ struct CacheRow {
   __device__ __forceinline__ int64_t scale_at(const dit_cache& c) const {
     return page * c.scale_stride + (int64_t)head * c.page_size + place;
   }
-  __device__ __forceinline__ int64_t at(const dit_heads& t) const {
-    return token * t.token + head * t.head;
-  }
 };
 
-// Any view: a warp has a row, an element per access.
-template <class T, bool FP8>
-__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ CacheArgs a) {
+template <class T, int NC, bool FP8, bool WRITE>
+__global__ void __launch_bounds__(kThreads) columns_kernel(const __grid_constant__ CacheArgs a) {
+  using K = typename std::conditional<FP8, uint8_t, T>::type;
   const int lane = threadIdx.x & 31;
-  const int64_t rows = a.tokens * 2 * a.c.heads;
   const int64_t stride = (int64_t)gridDim.x * (kThreads / 32);
-  const int D = (int)a.c.D;
+  const int D = (int)a.c.D, rows = 2 * (int)a.c.heads;
+  // a token's rows in parts: as many warps as it takes to have kColumnAhead rows each
+  const int parts = (rows + kColumnAhead - 1) / kColumnAhead;
+  const int64_t items = a.tokens * parts;
   after_previous();
   let_next();
-  for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < rows; i += stride) {
-    const CacheRow row(a, i);
-    if (!row.inside) continue;
-    const dit_heads& from = row.which ? a.v : a.k;
-    const T* x = (const T*)from.p + row.at(from);
-    if constexpr (FP8) {
-      float m = 0.0f;
-      for (int c = lane; c < D; c += 32) m = max_nan(m, fabsf(to_float(x[c])));
-      const RowQuant q = row_quant(lanes_max<32>(m));
-      uint8_t* out = (uint8_t*)(row.which ? a.c.v : a.c.k) + row.at(a.c);
-      for (int c = lane; c < D; c += 32)
-        out[c] = (uint8_t)e4m3x2(f2(code_value(to_float(x[c]), q), 0.0f));
-      if (lane == 0) (row.which ? a.c.v_scales : a.c.k_scales)[row.scale_at(a.c)] = q.scale;
+  for (int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); item < items; item += stride) {
+    const int64_t token = items >> 32 ? item / parts : (uint32_t)item / (uint32_t)parts;
+    const int first = (int)(item - token * parts) * kColumnAhead;
+    CacheRow row;
+    row.find(a, token);
+    if (WRITE && !row.inside) continue;
+    auto tokens = [&]() {
+      const dit_heads& v = row.which ? a.v : a.k;
+      return (T*)v.p + token * v.token + row.head * v.head;
+    };
+    auto cached = [&]() { return (K*)(row.which ? a.c.v : a.c.k) + row.at(a.c); };
+    auto value = [&](K x) {
+      if constexpr (FP8)
+        return from_e4m3(x);
+      else
+        return to_float(x);
+    };
+    if constexpr (NC > 0) {
+      using From = typename std::conditional<WRITE, T, K>::type;
+      From raw[kColumnAhead][NC];
+      float scale[kColumnAhead];
+#pragma unroll
+      for (int k = 0; k < kColumnAhead; ++k) {
+        row.row(first + k);
+        const From* x;
+        if constexpr (WRITE)
+          x = tokens();
+        else
+          x = cached();
+        const bool on = first + k < rows && row.inside;
+        if constexpr (FP8 && !WRITE) scale[k] = on ? (row.which ? a.c.v_scales : a.c.k_scales)[row.scale_at(a.c)] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          raw[k][i] = From();
+          if (on && lane + 32 * i < D) raw[k][i] = x[lane + 32 * i];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kColumnAhead; ++k) {
+        row.row(first + k);
+        if (first + k >= rows) break;
+        if constexpr (WRITE) {
+          K* out = cached();
+          RowQuant q;
+          if constexpr (FP8) {
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) m = max_nan(m, fabsf(to_float(raw[k][i])));
+            q = row_quant(lanes_max<32>(m));
+            if (lane == 0) (row.which ? a.c.v_scales : a.c.k_scales)[row.scale_at(a.c)] = q.scale;
+          }
+#pragma unroll
+          for (int i = 0; i < NC; ++i) {
+            if (lane + 32 * i >= D) continue;
+            if constexpr (FP8)
+              out[lane + 32 * i] = (uint8_t)e4m3x2(f2(code_value(to_float(raw[k][i]), q), 0.0f));
+            else
+              out[lane + 32 * i] = raw[k][i];
+          }
+        } else {
+          T* out = tokens();
+#pragma unroll
+          for (int i = 0; i < NC; ++i) {
+            if (lane + 32 * i >= D) continue;
+            if constexpr (FP8)
+              out[lane + 32 * i] = from_float<T>(__fmul_rn(value(raw[k][i]), scale[k]));
+            else
+              out[lane + 32 * i] = row.inside ? raw[k][i] : from_float<T>(0.0f);
+          }
+        }
+      }
     } else {
-      T* out = (T*)(row.which ? a.c.v : a.c.k) + row.at(a.c);
-      for (int c = lane; c < D; c += 32) out[c] = x[c];
-    }
-  }
-}
-
-template <class T, bool FP8>
-__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ CacheArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = a.tokens * 2 * a.c.heads;
-  const int64_t stride = (int64_t)gridDim.x * (kThreads / 32);
-  const int D = (int)a.c.D;
-  after_previous();
-  let_next();
-  for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < rows; i += stride) {
-    const CacheRow row(a, i);
-    const dit_heads& to = row.which ? a.v : a.k;
-    T* out = (T*)to.p + row.at(to);
-    if (!row.inside) {
-      for (int c = lane; c < D; c += 32) out[c] = from_float<T>(0.0f);
-    } else if constexpr (FP8) {
-      const uint8_t* x = (const uint8_t*)(row.which ? a.c.v : a.c.k) + row.at(a.c);
-      const float scale = (row.which ? a.c.v_scales : a.c.k_scales)[row.scale_at(a.c)];
-      for (int c = lane; c < D; c += 32) out[c] = from_float<T>(__fmul_rn(from_e4m3(x[c]), scale));
-    } else {
-      const T* x = (const T*)(row.which ? a.c.v : a.c.k) + row.at(a.c);
-      for (int c = lane; c < D; c += 32) out[c] = x[c];
+      for (int k = 0; k < kColumnAhead && first + k < rows; ++k) {
+        row.row(first + k);
+        T* x = tokens();
+        K* kept = cached();
+        if constexpr (WRITE && FP8) {
+          float m = 0.0f;
+          for (int c = lane; c < D; c += 32) m = max_nan(m, fabsf(to_float(x[c])));
+          const RowQuant q = row_quant(lanes_max<32>(m));
+          for (int c = lane; c < D; c += 32) kept[c] = (uint8_t)e4m3x2(f2(code_value(to_float(x[c]), q), 0.0f));
+          if (lane == 0) (row.which ? a.c.v_scales : a.c.k_scales)[row.scale_at(a.c)] = q.scale;
+        } else if constexpr (WRITE) {
+          for (int c = lane; c < D; c += 32) kept[c] = x[c];
+        } else {
+          const float scale = FP8 && row.inside ? (row.which ? a.c.v_scales : a.c.k_scales)[row.scale_at(a.c)] : 1.0f;
+          for (int c = lane; c < D; c += 32)
+            x[c] = row.inside ? from_float<T>(FP8 ? __fmul_rn(value(kept[c]), scale) : value(kept[c])) : from_float<T>(0.0f);
+        }
+      }
     }
   }
 }
@@ -289,8 +339,14 @@ cudaError_t launch(const DeviceInfo& dev, void (*kern)(Args), int64_t warps, con
 
 template <class T, bool FP8>
 cudaError_t launch(const DeviceInfo& dev, bool write, const CacheArgs& a, cudaStream_t s) {
-  const int64_t rows = a.tokens * 2 * a.c.heads, half = (a.c.D * (int)sizeof(T) / 16 + 1) / 2;
-  if (!a.granules || half > 32) return launch(dev, write ? write_kernel<T, FP8> : read_kernel<T, FP8>, rows, a, s);
+  const int64_t half = (a.c.D * (int)sizeof(T) / 16 + 1) / 2;  // granules of a lane's pair
+  if (!a.granules || half > 32) {
+    const auto columns = a.c.D <= 64    ? (write ? columns_kernel<T, 2, FP8, true> : columns_kernel<T, 2, FP8, false>)
+                         : a.c.D <= 128 ? (write ? columns_kernel<T, 4, FP8, true> : columns_kernel<T, 4, FP8, false>)
+                         : a.c.D <= 256 ? (write ? columns_kernel<T, 8, FP8, true> : columns_kernel<T, 8, FP8, false>)
+                                        : (write ? columns_kernel<T, 0, FP8, true> : columns_kernel<T, 0, FP8, false>);
+    return launch(dev, columns, a.tokens * ((2 * a.c.heads + kColumnAhead - 1) / kColumnAhead), a, s);
+  }
   CacheRows c{a, divisor((uint32_t)a.c.page_size), 1, 0};
   auto team = [&](auto lanes) {
     constexpr int TEAM = decltype(lanes)::value, TEAMS = 32 / TEAM;

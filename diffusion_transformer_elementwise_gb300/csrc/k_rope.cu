@@ -159,8 +159,7 @@ __global__ void __launch_bounds__(kTableThreads) table_kernel(const __grid_const
 
 constexpr int kRowThreads = 256;
 
-// Any view: a warp has a head, an element per access (32640 tokens x 64 heads of 128, bf16: 1015 us, so only where
-// granules cannot be used).
+// Any view, and any head: a warp has a head, an element per access.
 template <class T, bool NORM>
 __global__ void __launch_bounds__(kRowThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   const int lane = threadIdx.x & 31;
@@ -307,6 +306,77 @@ __global__ void __launch_bounds__(kRowThreads, 2) rope_heads_kernel(const __grid
   cp_async_wait<0>();  // no copy may outlive the CTA's shared memory
 }
 
+// Any view of up to 32 NC columns: a warp has a token's heads, kColumnHeads of them an item, kColumnAhead loaded before
+// the first is computed.  For rows that granules do not fit, 64 or 128 bytes an access (8160 tokens x 64 heads of 80
+// with 10 pairs, bf16: 87 us, where a copy's rate gives 25; with a head after the other, by its number: 215).
+constexpr int kColumnHeads = 8, kColumnAhead = 4;
+
+template <class T, int NC, bool NORM>
+__global__ void __launch_bounds__(kRowThreads) rope_columns_kernel(const __grid_constant__ RopeHeads args) {
+  constexpr int WARPS = kRowThreads / 32;
+  __shared__ float rows[WARPS][kColumnAhead][32 * NC];
+  const RopeArgs& a = args.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int which = (int)blockIdx.x >= args.g.ctas[0], cta = which ? blockIdx.x - args.g.ctas[0] : blockIdx.x;
+  const RopeTensor& t = a.t[which];
+  const LaneColumns<NC> columns(a, lane);
+  after_previous();
+  let_next();
+  float w[NC];
+  if constexpr (NORM) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      w[i] = lane + 32 * i < a.D ? __fadd_rn(a.offset, to_float(((const T*)t.w)[lane + 32 * i])) : 0.0f;
+  }
+  HeadWalk walk(args.g, which, (int64_t)cta * WARPS + warp, (int64_t)args.g.ctas[which] * WARPS);
+  for (; walk.token < a.tokens; walk.next()) {
+    const TokenAt at(a, (uint32_t)walk.token);
+    float cs[NC], sn[NC];
+    if (a.R > 0) columns.load(a, at.table, a.inverse, cs, sn);
+    const int first = walk.part * kColumnHeads, last = min(first + kColumnHeads, t.H);
+    const T* x = (const T*)t.x.p + at.batch * t.x.batch + at.place * t.x.token + first * t.x.head + lane;
+    T* out = (T*)t.out.p + at.batch * t.out.batch + at.place * t.out.token + first * t.out.head + lane;
+    for (int head = first; head < last; head += kColumnAhead) {
+      T raw[kColumnAhead][NC];
+#pragma unroll
+      for (int k = 0; k < kColumnAhead; ++k)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          raw[k][i] = from_float<T>(0.0f);
+          if (head + k < last && lane + 32 * i < a.D) raw[k][i] = x[k * t.x.head + 32 * i];
+        }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kColumnAhead; ++k) {
+        float y[NC], r = 1.0f;
+        if constexpr (NORM) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NC; ++i) sum = __fmaf_rn(to_float(raw[k][i]), to_float(raw[k][i]), sum);
+          r = inverse_rms(lanes_sum<32>(sum), a.inv_d, a.eps);
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          y[i] = to_float(raw[k][i]);
+          if constexpr (NORM) y[i] = __fmul_rn(__fmul_rn(y[i], r), w[i]);
+          rows[warp][k][lane + 32 * i] = y[i];
+        }
+        __syncwarp();
+        if (head + k < last) {
+#pragma unroll
+          for (int i = 0; i < NC; ++i) {
+            if (lane + 32 * i >= a.D) continue;
+            if (columns.angle[i] >= 0) y[i] = __fmaf_rn(y[i], cs[i], __fmul_rn(rows[warp][k][columns.partner[i]], sn[i]));
+            out[k * t.out.head + 32 * i] = NORM || columns.angle[i] >= 0 ? from_float<T>(y[i]) : raw[k][i];
+          }
+        }
+      }
+      x += kColumnAhead * t.x.head;
+      out += kColumnAhead * t.out.head;
+    }
+  }
+}
+
 template <class T, int TEAM, bool NORM, bool INTER>
 cudaError_t launch_heads(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {
   using Stage = HeadStage<T, TEAM, INTER, 1>;
@@ -337,8 +407,16 @@ cudaError_t launch(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {
            : units <= 16 ? launch_heads<T, 16>(dev, a, s)
                          : launch_heads<T, 32>(dev, a, s);
   }
-  const int64_t rows = a.tokens * (a.t[0].H + a.t[1].H);
   const bool norm = a.t[0].w || a.t[1].w;
+  if (a.D <= 256) {
+    const auto columns = a.D <= 64    ? (norm ? rope_columns_kernel<T, 2, true> : rope_columns_kernel<T, 2, false>)
+                         : a.D <= 128 ? (norm ? rope_columns_kernel<T, 4, true> : rope_columns_kernel<T, 4, false>)
+                                      : (norm ? rope_columns_kernel<T, 8, true> : rope_columns_kernel<T, 8, false>);
+    const int64_t most = (int64_t)dev.sm_count * resident_ctas(dev, (const void*)columns, kRowThreads);
+    const RopeHeads h{a, head_grid(a, kColumnHeads, kRowThreads / 32, most)};
+    return launch_after(columns, (unsigned)(h.g.ctas[0] + h.g.ctas[1]), kRowThreads, 0, s, h);
+  }
+  const int64_t rows = a.tokens * (a.t[0].H + a.t[1].H);
   const auto kern = norm ? rope_kernel<T, true> : rope_kernel<T, false>;
   const int64_t warps = kRowThreads / 32;
   const int64_t most = (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kRowThreads) * 8;

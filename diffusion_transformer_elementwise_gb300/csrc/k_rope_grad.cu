@@ -11,7 +11,7 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 
-// Any view (8160 tokens x 40 heads of 128, bf16: 230 us): a warp has a head, an element per access; blockIdx.y tells queries from keys.  Each warp
+// Any view, and any head: a warp has a head, an element per access; blockIdx.y tells queries from keys.  Each warp
 // adds up its weight's gradient in shared memory (its own row of it), the CTA its warps'.
 template <class T>
 __global__ void __launch_bounds__(kRowThreads) rope_grad_kernel(const __grid_constant__ RopeArgs a) {
@@ -204,6 +204,95 @@ __global__ void __launch_bounds__(kRowThreads, 2) rope_grad_heads_kernel(const _
   }
 }
 
+// Any view of up to 32 NC columns: a warp has a token's heads, kColumnHeads of them an item, two loaded before the first
+// is computed; a lane adds up its columns' part of one weight's gradient (8160 tokens x 40 heads of 99, bf16: 114
+// us, where a copy's rate gives 29; with a head after the other, by its number: 283).
+constexpr int kColumnHeads = 8, kColumnAhead = 2;
+
+template <class T, int NC>
+__global__ void __launch_bounds__(kRowThreads) rope_grad_columns_kernel(const __grid_constant__ GradHeads args) {
+  __shared__ float rows[kRowWarps][kColumnAhead][32 * NC];
+  const RopeArgs& a = args.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int which = (int)blockIdx.x >= args.g.ctas[0], cta = which ? blockIdx.x - args.g.ctas[0] : blockIdx.x;
+  const RopeTensor& t = a.t[which];
+  const LaneColumns<NC> columns(a, lane);
+  after_previous();
+  let_next();
+  float w[NC], acc[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    w[i] = lane + 32 * i < a.D ? __fadd_rn(a.offset, to_float(((const T*)t.w)[lane + 32 * i])) : 0.0f;
+    acc[i] = 0.0f;
+  }
+  HeadWalk walk(args.g, which, (int64_t)cta * kRowWarps + warp, (int64_t)args.g.ctas[which] * kRowWarps);
+  for (; walk.token < a.tokens; walk.next()) {
+    const TokenAt at(a, (uint32_t)walk.token);
+    float cs[NC], sn[NC];
+    if (a.R > 0) columns.load(a, at.table, true, cs, sn);  // the gradient is turned back
+    const int first = walk.part * kColumnHeads, last = min(first + kColumnHeads, t.H);
+    const T* x = (const T*)t.x.p + at.batch * t.x.batch + at.place * t.x.token + first * t.x.head + lane;
+    const T* g = (const T*)t.g.p + at.batch * t.g.batch + at.place * t.g.token + first * t.g.head + lane;
+    T* out = (T*)t.out.p + at.batch * t.out.batch + at.place * t.out.token + first * t.out.head + lane;
+    for (int head = first; head < last; head += kColumnAhead) {
+      T rx[kColumnAhead][NC], rg[kColumnAhead][NC];
+#pragma unroll
+      for (int k = 0; k < kColumnAhead; ++k)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          rx[k][i] = rg[k][i] = from_float<T>(0.0f);
+          if (head + k >= last || lane + 32 * i >= a.D) continue;
+          rx[k][i] = x[k * t.x.head + 32 * i];
+          rg[k][i] = g[k * t.g.head + 32 * i];
+        }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kColumnAhead; ++k)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) rows[warp][k][lane + 32 * i] = to_float(rg[k][i]);
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kColumnAhead; ++k) {
+        float u[NC], square = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          u[i] = to_float(rg[k][i]);
+          if (columns.angle[i] >= 0) u[i] = __fmaf_rn(u[i], cs[i], __fmul_rn(rows[warp][k][columns.partner[i]], sn[i]));
+          const float v = to_float(rx[k][i]);
+          square = __fmaf_rn(v, v, square);
+          dot = __fmaf_rn(__fmul_rn(u[i], w[i]), v, dot);
+        }
+        const float r = inverse_rms(lanes_sum<32>(square), a.inv_d, a.eps);
+        const float mean = __fmul_rn(__fmul_rn(lanes_sum<32>(dot), r), a.inv_d);
+        if (head + k >= last) continue;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          if (lane + 32 * i >= a.D) continue;
+          const float n = __fmul_rn(to_float(rx[k][i]), r);
+          acc[i] = __fmaf_rn(u[i], n, acc[i]);
+          out[k * t.out.head + 32 * i] = from_float<T>(__fmul_rn(r, __fmaf_rn(n, -mean, __fmul_rn(u[i], w[i]))));
+        }
+      }
+      x += kColumnAhead * t.x.head;
+      g += kColumnAhead * t.g.head;
+      out += kColumnAhead * t.out.head;
+    }
+  }
+  if (!a.partial) return;
+  __syncthreads();
+  float* sums = &rows[0][0][0];  // [warps][32 NC]
+#pragma unroll
+  for (int i = 0; i < NC; ++i) sums[warp * 32 * NC + lane + 32 * i] = acc[i];
+  __syncthreads();
+  float* partial = a.partial + (int64_t)blockIdx.x * a.D;
+  for (int c = threadIdx.x; c < a.D; c += kRowThreads) {
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kRowWarps; ++k) v = __fadd_rn(v, sums[k * 32 * NC + c]);
+    partial[c] = v;
+  }
+}
+
 // gw[which][c] = the sum over the partial rows [0, split) (queries) or [split, rows) (keys): 32 columns
 // a CTA, its 32 warps every 32nd row, then their sums in order.
 struct JoinArgs {
@@ -266,6 +355,13 @@ cudaError_t launch(const DeviceInfo& dev, const RopeArgs& a, void* gwq, void* gw
         : units <= 8  ? launch_heads<T, 8>(dev, a, &split, &rows, s)
         : units <= 16 ? launch_heads<T, 16>(dev, a, &split, &rows, s)
                       : launch_heads<T, 32>(dev, a, &split, &rows, s);
+  } else if (a.D <= 256) {
+    const auto columns = a.D <= 64 ? rope_grad_columns_kernel<T, 2> : a.D <= 128 ? rope_grad_columns_kernel<T, 4> : rope_grad_columns_kernel<T, 8>;
+    const int64_t most = std::min(2 * kRopeGradMaxCtas, (int64_t)dev.sm_count * resident_ctas(dev, (const void*)columns, kRowThreads));
+    const GradHeads g{a, head_grid(a, kColumnHeads, kRowWarps, most)};
+    split = g.g.ctas[0];
+    rows = g.g.ctas[0] + g.g.ctas[1];
+    e = launch_after(columns, (unsigned)rows, kRowThreads, 0, s, g);
   } else {
     const auto kern = rope_grad_kernel<T>;
     const size_t smem = a.partial ? (size_t)kRowWarps * a.D * 4 : 0;
