@@ -4,7 +4,7 @@
 //   m = max|x|,  scale = m / 448,  code = e4m3(x 448 / m)
 // with the quotient in two fp32 numbers, so that a code is the nearest to the exact
 // quotient but where that lies within 2^-24 of itself from the middle of two codes.
-// Both ways are bound by memory, the way in also by instructions (760 of a warp for four rows each of keys and
+// Both ways are bound by memory, the way in also by instructions (800 of a warp for four rows each of keys and
 // values).  32640 tokens x 8 heads of 128, 1/20 of them padding, bf16: into E4M3 39 us, 4.9 TB/s, 72 % of a
 // copy's rate; back 32 us, 6.2 TB/s, 92 %.  By rows of any kind one after the other, each with its own places, they took 48
 // and 34 us; an element per access 168 and 112.

@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kRowThreads) rope_columns_kernel(const __grid_
     const TokenAt at(a, (uint32_t)walk.token);
     float cs[NC], sn[NC];
     if (a.R > 0) columns.load(a, at.table, a.inverse, cs, sn);
-    const int first = walk.part * kColumnHeads, last = min(first + kColumnHeads, t.H);
+    const int first = walk.part * args.g.together, last = min(first + args.g.together, t.H);
     const T* x = (const T*)t.x.p + at.batch * t.x.batch + at.place * t.x.token + first * t.x.head + lane;
     T* out = (T*)t.out.p + at.batch * t.out.batch + at.place * t.out.token + first * t.out.head + lane;
     for (int head = first; head < last; head += kColumnAhead) {
@@ -413,7 +413,8 @@ cudaError_t launch(const DeviceInfo& dev, const RopeArgs& a, cudaStream_t s) {
                          : a.D <= 128 ? (norm ? rope_columns_kernel<T, 4, true> : rope_columns_kernel<T, 4, false>)
                                       : (norm ? rope_columns_kernel<T, 8, true> : rope_columns_kernel<T, 8, false>);
     const int64_t most = (int64_t)dev.sm_count * resident_ctas(dev, (const void*)columns, kRowThreads);
-    const RopeHeads h{a, head_grid(a, kColumnHeads, kRowThreads / 32, most)};
+    const int together = column_heads(dev, a, kColumnHeads, kColumnAhead);
+    const RopeHeads h{a, head_grid(a, together, kRowThreads / 32, most)};
     return launch_after(columns, (unsigned)(h.g.ctas[0] + h.g.ctas[1]), kRowThreads, 0, s, h);
   }
   const int64_t rows = a.tokens * (a.t[0].H + a.t[1].H);

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kRowThreads) rope_grad_columns_kernel(const __
     const TokenAt at(a, (uint32_t)walk.token);
     float cs[NC], sn[NC];
     if (a.R > 0) columns.load(a, at.table, true, cs, sn);  // the gradient is turned back
-    const int first = walk.part * kColumnHeads, last = min(first + kColumnHeads, t.H);
+    const int first = walk.part * args.g.together, last = min(first + args.g.together, t.H);
     const T* x = (const T*)t.x.p + at.batch * t.x.batch + at.place * t.x.token + first * t.x.head + lane;
     const T* g = (const T*)t.g.p + at.batch * t.g.batch + at.place * t.g.token + first * t.g.head + lane;
     T* out = (T*)t.out.p + at.batch * t.out.batch + at.place * t.out.token + first * t.out.head + lane;
@@ -358,7 +358,8 @@ cudaError_t launch(const DeviceInfo& dev, const RopeArgs& a, void* gwq, void* gw
   } else if (a.D <= 256) {
     const auto columns = a.D <= 64 ? rope_grad_columns_kernel<T, 2> : a.D <= 128 ? rope_grad_columns_kernel<T, 4> : rope_grad_columns_kernel<T, 8>;
     const int64_t most = std::min(2 * kRopeGradMaxCtas, (int64_t)dev.sm_count * resident_ctas(dev, (const void*)columns, kRowThreads));
-    const GradHeads g{a, head_grid(a, kColumnHeads, kRowWarps, most)};
+    const int together = column_heads(dev, a, kColumnHeads, kColumnAhead);
+    const GradHeads g{a, head_grid(a, together, kRowWarps, most)};
     split = g.g.ctas[0];
     rows = g.g.ctas[0] + g.g.ctas[1];
     e = launch_after(columns, (unsigned)rows, kRowThreads, 0, s, g);
