@@ -3,8 +3,11 @@
 //
 //   s = scale q.k,  m = max s,  l = sum 2^(s - m),  o = sum 2^(s - m) v
 // in one pass over the tokens, with s in powers of two (scale times log2 e).  For rows
-// that are not made of 16-byte granules, or of more than 256 columns: bound by the shuffles
-// of its dot products (one sequence of 131072 tokens x 8 heads of 128, bf16: 3.1 ms).
+// that are not made of 16-byte granules, or of more than 256 columns.  A CTA has 64 tokens at a time: a warp its
+// keys, columns over the lanes; then a thread a column of the values and a share of the tokens.  Bound by
+// instructions (some 300 of a warp a token, two bytes a load) and the latency of one stage after the other:
+// 131072 tokens x 8 heads, bf16, heads of 99 316 us, of 320 1.07 ms, five times their bytes at the copy rate.  A load is
+// converted only when all of its batch are under way: one that waits for its own takes 607 us, and 3.35 ms.
 #include "dit_attend.cuh"
 
 namespace dit {
@@ -14,30 +17,40 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = 64;  // at a time
 constexpr int kMaxD = 512;
-constexpr int kExtra = 4, kLeast = 8;  // units of a segment beside its tiles; the smallest part
+constexpr int kExtra = 4, kLeast = 2;  // units of a segment beside its tiles; the smallest part
+
+// Threads of a column of values, each with its share of the tokens and its own sum.
+__host__ __device__ inline int column_threads(int D) {
+  const int threads = kThreads / ((D + 31) / 32 * 32);
+  return threads > 1 ? threads : 1;
+}
 
 template <class K>
-__device__ __forceinline__ float cached(const void* p, int64_t i) {
+__device__ __forceinline__ float cached(K x) {
   if constexpr (sizeof(K) == 1)
-    return from_e4m3(((const uint8_t*)p)[i]);
+    return from_e4m3(x);
   else
-    return to_float(((const K*)p)[i]);
+    return to_float(x);
 }
 
 // K: the cache's type (uint8_t: E4M3), T: the queries'.
-template <class T, class K>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant__ AttendArgs a) {
+// N: columns of a lane, at most; R: rows (query heads) at most.
+template <class T, class K, int N, int R>
+__global__ void __launch_bounds__(kThreads, N == 4 && R == 4 ? 4 : 2) attend_kernel(const __grid_constant__ AttendArgs a) {
   constexpr bool FP8 = sizeof(K) == 1;
+  constexpr int kAhead = N == 4 ? 4 : 2, kValues = 8;  // keys of a warp, and values of a thread, in flight
   __shared__ Plan<kThreads> plan;
   __shared__ int64_t place[kTokens];
   __shared__ float kscale[kTokens], vscale[kTokens];
-  __shared__ float weight[kAttendRows][kTokens];
-  __shared__ float m[kAttendRows], l[kAttendRows], factor[kAttendRows];
+  __shared__ __align__(16) float weight[kTokens][R + 4];  // (4: banks, and 16-byte reads)
+  __shared__ float m[R], l[R], factor[R];
   extern __shared__ float space[];
   const int D = (int)a.c.D;
   float* q = space;                    // [rows][D]
-  float* o = space + kAttendRows * D;  // [rows][D]
+  float* o = space + R * D;            // [threads of a column][rows][D]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int shares = column_threads(D), share = shares > 1 ? tid / ((D + 31) / 32 * 32) : 0;
+  const int column = share < shares ? tid - share * ((D + 31) / 32 * 32) : D;
   const int blocks = (a.group + kAttendRows - 1) / kAttendRows;
   const Line line{(int)a.c.heads * blocks, kExtra};
   after_previous();
@@ -59,9 +72,10 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
       const int r = i / D, c = i - r * D;
       q[i] = __fmul_rn(to_float(((const T*)a.q.p)[g.b * a.q.token + (h0 + r) * a.q.head + c]),
                        a.scale);
-      o[i] = 0.0f;
     }
-    if (tid < kAttendRows) m[tid] = -INFINITY, l[tid] = 0.0f;
+    for (int i = tid; i < shares * rows * D; i += kThreads) o[i] = 0.0f;
+    for (int i = tid; i < kTokens * (R + 4); i += kThreads) weight[0][i] = 0.0f;  // (rows beyond the last)
+    if (tid < R) m[tid] = -INFINITY, l[tid] = 0.0f;
     for (int t0 = g.first * kTile; t0 < g.last * kTile; t0 += kTokens) {
       const int n = min(kTokens, g.last * kTile - t0);
       __syncthreads();
@@ -74,28 +88,45 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
         }
       }
       __syncthreads();
-      for (int t = warp; t < kTokens; t += kWarps) {
-        if (place[t] < 0) {
-          if (lane < rows) weight[lane][t] = -INFINITY;
-          continue;
+      for (int t0 = warp * kAhead; t0 < kTokens; t0 += kWarps * kAhead) {
+        // (all loads before the first conversion, which would wait for its own)
+        K raw[kAhead][N] = {};
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const K* row = (const K*)a.c.k + place[t0 + j] + lane;
+          const int size = place[t0 + j] >= 0 ? D - lane : 0;
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (32 * i < size) raw[j][i] = row[32 * i];
         }
-        float k[kMaxD / 32];
+        float k[kAhead][N];
 #pragma unroll
-        for (int i = 0; i < kMaxD / 32; ++i)
-          if (lane + 32 * i < D) k[i] = cached<K>(a.c.k, place[t] + lane + 32 * i);
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+          for (int i = 0; i < N; ++i) k[j][i] = cached(raw[j][i]);
         for (int r = 0; r < rows; ++r) {
-          float s = 0.0f;
+          float s[kAhead] = {};
 #pragma unroll
-          for (int i = 0; i < kMaxD / 32; ++i)
-            if (lane + 32 * i < D) s = __fmaf_rn(q[r * D + lane + 32 * i], k[i], s);
-          s = lanes_sum<32>(s);
-          if constexpr (FP8) s = __fmul_rn(s, kscale[t]);
-          if (lane == 0) weight[r][t] = __fmul_rn(s, 1.4426950408889634f);
+          for (int i = 0; i < N; ++i)
+            if (lane + 32 * i < D) {
+              const float x = q[r * D + lane + 32 * i];
+#pragma unroll
+              for (int j = 0; j < kAhead; ++j) s[j] = __fmaf_rn(x, k[j][i], s[j]);
+            }
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) s[j] = lanes_sum<32>(s[j]);
+          float mine = s[0];
+#pragma unroll
+          for (int j = 1; j < kAhead; ++j) mine = lane == j ? s[j] : mine;
+          if (lane < kAhead) {
+            if constexpr (FP8) mine = __fmul_rn(mine, kscale[t0 + lane]);
+            weight[t0 + lane][r] = place[t0 + lane] >= 0 ? __fmul_rn(mine, 1.4426950408889634f) : -INFINITY;
+          }
         }
       }
       __syncthreads();
       for (int r = warp; r < rows; r += kWarps) {
-        const float s0 = weight[r][lane], s1 = weight[r][lane + 32];
+        const float s0 = weight[lane][r], s1 = weight[lane + 32][r];
         float most = fmaxf(s0, s1);
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, k));
@@ -104,8 +135,8 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
         const float p0 = exp2f(__fadd_rn(s0, -base)), p1 = exp2f(__fadd_rn(s1, -base));
         const float f = exp2f(__fadd_rn(was, -base));
         const float sum = lanes_sum<32>(__fadd_rn(p0, p1));
-        weight[r][lane] = p0;
-        weight[r][lane + 32] = p1;
+        weight[lane][r] = p0;
+        weight[lane + 32][r] = p1;
         __syncwarp();
         if (lane == 0) {
           m[r] = now;
@@ -114,29 +145,46 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
         }
       }
       __syncthreads();
-      for (int c = tid; c < D; c += kThreads) {
-        float acc[kAttendRows];
+      for (int c = column; c < D; c += kThreads) {
+        float* sum = o + share * rows * D + c;
+        float acc[R];
 #pragma unroll
-        for (int r = 0; r < kAttendRows; ++r) acc[r] = r < rows ? __fmul_rn(o[r * D + c], factor[r]) : 0.0f;
-        for (int t = 0; t < n; ++t) {
-          if (place[t] < 0) continue;
-          float v = cached<K>(a.c.v, place[t] + c);
-          if constexpr (FP8) v = __fmul_rn(v, vscale[t]);
+        for (int r = 0; r < R; ++r) acc[r] = r < rows ? __fmul_rn(sum[r * D], factor[r]) : 0.0f;
+        for (int t = share * kValues; t < n; t += shares * kValues) {
+          K raw[kValues] = {};
 #pragma unroll
-          for (int r = 0; r < kAttendRows; ++r)
-            if (r < rows) acc[r] = __fmaf_rn(weight[r][t], v, acc[r]);
+          for (int j = 0; j < kValues; ++j)
+            if (place[t + j] >= 0) raw[j] = ((const K*)a.c.v)[place[t + j] + c];
+#pragma unroll
+          for (int j = 0; j < kValues; ++j) {
+            float v = cached(raw[j]);
+            if constexpr (FP8) v = __fmul_rn(v, vscale[t + j]);
+#pragma unroll
+            for (int r = 0; r < R; r += 4) {
+              const float4 p = *(const float4*)&weight[t + j][r];
+              acc[r] = __fmaf_rn(p.x, v, acc[r]);
+              acc[r + 1] = __fmaf_rn(p.y, v, acc[r + 1]);
+              acc[r + 2] = __fmaf_rn(p.z, v, acc[r + 2]);
+              acc[r + 3] = __fmaf_rn(p.w, v, acc[r + 3]);
+            }
+          }
         }
 #pragma unroll
-        for (int r = 0; r < kAttendRows; ++r)
-          if (r < rows) o[r * D + c] = acc[r];
+        for (int r = 0; r < R; ++r)
+          if (r < rows) sum[r * D] = acc[r];
       }
     }
     __syncthreads();
+    const auto value = [&](int i) {
+      float y = o[i];
+      for (int k = 1; k < shares; ++k) y = __fadd_rn(y, o[k * rows * D + i]);
+      return y;
+    };
     if (g.head || g.tail) {
       const int slot = g.head ? 0 : 1;
       float* out = a.partial + ((int64_t)blockIdx.x * 2 + slot) * slot_rows * (D + 2);
       if (tid == 0) a.owner[2 * blockIdx.x + slot] = segment_id(g.b, g.s);
-      for (int i = tid; i < rows * D; i += kThreads) out[2 * slot_rows + i] = o[i];
+      for (int i = tid; i < rows * D; i += kThreads) out[2 * slot_rows + i] = value(i);
       if (tid < rows) {
         out[tid] = m[tid];
         out[slot_rows + tid] = l[tid];
@@ -146,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
         const int r = i / D, c = i - r * D;
         const float total = l[r];
         ((T*)a.out.p)[g.b * a.out.token + (h0 + r) * a.out.head + c] =
-            from_float<T>(total == 0.0f ? 0.0f : __fdiv_rn(o[i], total));
+            from_float<T>(total == 0.0f ? 0.0f : __fdiv_rn(value(i), total));
       }
       if (a.lse && tid < rows) a.lse[(int64_t)g.b * a.Hq + h0 + tid] = lse_of(m[tid], l[tid]);
     }
@@ -218,16 +266,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   if (threadIdx.x == 0 && a.lse) a.lse[(int64_t)b * a.Hq + h] = lse_of(top, total);
 }
 
-template <class T, class K>
+template <class T, class K, int N, int R>
 cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cudaStream_t s) {
-  const auto kern = attend_kernel<T, K>;
-  const size_t smem = (size_t)2 * kAttendRows * a.c.D * 4;
+  const auto kern = attend_kernel<T, K, N, R>;
+  const size_t smem = (size_t)(1 + column_threads((int)a.c.D)) * R * a.c.D * 4;
   static std::atomic<int> opted[kOptinDevices];
   const cudaError_t e = allow_shared((const void*)kern, dev, opted);
   if (e != cudaSuccess) return e;
   *ctas = std::min(kAttendMaxCtas,
                    (int64_t)dev.sm_count * resident_ctas(dev, (const void*)kern, kThreads, smem));
   return launch_after(kern, (unsigned)*ctas, kThreads, smem, s, a);
+}
+template <class T, class K>
+cudaError_t launch(const DeviceInfo& dev, const AttendArgs& a, int64_t* ctas, cudaStream_t s) {
+  return a.c.D <= 128 ? (a.group <= 4 ? launch<T, K, 4, 4>(dev, a, ctas, s) : launch<T, K, 4, kAttendRows>(dev, a, ctas, s))
+                      : (a.group <= 4 ? launch<T, K, kMaxD / 32, 4>(dev, a, ctas, s)
+                                      : launch<T, K, kMaxD / 32, kAttendRows>(dev, a, ctas, s));
 }
 
 template <class T>
