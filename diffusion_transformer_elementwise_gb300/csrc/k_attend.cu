@@ -5,7 +5,8 @@
 // in one pass over the tokens, with s in powers of two (scale times log2 e).  For rows
 // that are not made of 16-byte granules, or of more than 256 columns.  A CTA has 64 tokens at a time: a warp its
 // keys, columns over the lanes; then a thread a column of the values and a share of the tokens.  Bound by
-// instructions (some 300 of a warp a token, two bytes a load) and the latency of one stage after the other:
+// instructions (264 of a warp a token and key head of 99, two bytes a load; 68 % of the issue slots) and, for
+// longer heads, the latency of one stage after the other:
 // 131072 tokens x 8 heads, bf16, heads of 99 316 us, of 320 1.07 ms, five times their bytes at the copy rate.  A load is
 // converted only when all of its batch are under way: one that waits for its own takes 607 us, and 3.35 ms.
 #include "dit_attend.cuh"
