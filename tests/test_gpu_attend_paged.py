@@ -250,3 +250,65 @@ def test_far_pages(fp8):
     out, lse = dit.paged_attention(q, cache, table, torch.tensor([45], dtype=torch.int32, device="cuda"),
                                    need_lse=True)
     check_attention(out, lse, q, lambda b, h: rk[:45, 0], lambda b, h: rv[:45, 0], [45], D ** -0.5, fp8)
+
+
+# Caches that the kernel for any alignment takes: odd heads, heads of more than 256 columns, views off 16 bytes.
+ANY = [(5, 6, 1), (33, 5, 1), (99, 4, 2), (99, 8, 1), (99, 17, 1), (70, 40, 2), (129, 3, 3), (264, 9, 1), (320, 4, 1),
+       (511, 40, 2)]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dtype", T)
+@pytest.mark.parametrize("D,Hq,Hk", ANY)
+def test_any_alignment(D, Hq, Hk, dtype, fp8):
+    """Groups in one block and in several, sequences of several parts, windows, empty rows."""
+    s = Setup([3000, 9, 0, 130, 64], Hq, Hk, D, 13, dtype, fp8)
+    out, lse = s.run()
+    s.check(out, lse)
+    assert (out[2] == 0).all() and (lse[2] == -math.inf).all()
+    again, l2 = s.run()
+    assert torch.equal(out, again) and torch.equal(lse, l2)
+    for s.window in (1, 65, 2990):
+        s.check(*s.run(), what=s.window)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,Hq,Hk", [(99, 4, 2), (99, 8, 1), (320, 2, 1)])
+def test_any_alignment_missing_pages_and_sharp_logits(D, Hq, Hk, fp8):
+    s = Setup([200, 40, 33, 8], Hq, Hk, D, 8, "bf16", fp8)
+    for scale in (0.0, 20.0, -3.0, 1e-30):
+        s.check(*s.run(scale=scale), scale=scale)
+    s.pages[0, 2] = s.pages[0, 3] = -1
+    s.pages[0, 20] = s.cache.pages
+    s.pages[1, :] = -7
+    gone = {0: (2, 3, 20), 1: range(5)}
+
+    def seen(b, n):
+        keep = torch.ones(n, dtype=torch.bool)
+        for page in gone.get(b, ()):
+            keep[8 * page:8 * page + 8] = False
+        return keep.numpy()
+
+    s.seen = seen
+    out, lse = s.run()
+    s.check(out, lse)
+    assert (out[1] == 0).all() and (lse[1] == -math.inf).all()
+
+
+@pytest.mark.parametrize("D", [99, 320])
+def test_any_alignment_nan_reaches_its_sequence_alone(D):
+    s = Setup([40, 100, 40], 4, 2, D, 16)
+    clean, _ = s.run()
+    s.cache.k[int(s.pages[1, 1]), 0, 3, 7] = math.nan
+    s.cache.v[int(s.pages[2, 0]), 1, 3, 9] = math.inf
+    out, lse = s.run()
+    assert torch.equal(out[0], clean[0]) and torch.isnan(out[1, :2]).all() and torch.equal(out[1, 2:], clean[1, 2:])
+    assert torch.isnan(lse[1, :2]).all() and torch.isfinite(lse[2]).all()
+    assert torch.isinf(out[2, 2:, 9]).all() and torch.isfinite(out[2, :2]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,Hq,Hk", [(99, 8, 2), (320, 4, 1)])
+def test_any_alignment_long(D, Hq, Hk, fp8):
+    s = Setup([20000, 1, 9999, 0, 20], Hq, Hk, D, 64, "bf16", fp8)
+    s.check(*s.run())
