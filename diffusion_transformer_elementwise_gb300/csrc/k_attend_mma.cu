@@ -509,10 +509,11 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
           }
         }
         if constexpr (FP8) {
-          // weights times the values' scales, in units of a power of two above all of them so far, fit fp16
+          // weights times the values' scales, in units of a power of two above all of their magnitudes so far, fit fp16
+          // (magnitudes order as their bits without the sign; NaN lies above infinity)
           uint32_t most = 0;
 #pragma unroll
-          for (int t = 0; t < 2 * MB; ++t) most = max(most, __float_as_uint(vs[t]));
+          for (int t = 0; t < 2 * MB; ++t) most = max(most, __float_as_uint(vs[t]) & 0x7FFFFFFFu);
           most = __reduce_max_sync(0xFFFFFFFFu, most);
           if (most >= __float_as_uint(vref)) {
             const uint32_t e = min((most >> 23) + 1, 253u);
