@@ -78,6 +78,12 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+// the larger of both upper and of both lower halves
+__device__ __forceinline__ uint32_t max_halves(uint32_t x, uint32_t y) {
+  uint32_t z;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+  return z;
+}
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t codes) {  // the low two codes
   uint32_t h;
   asm("{ .reg .b16 c, d; mov.b32 {c, d}, %1; cvt.rn.f16x2.e4m3x2 %0, c; }" : "=r"(h) : "r"(codes));
@@ -126,6 +132,7 @@ struct Shape {
   static constexpr bool FP8 = FP8_, SPLIT = sizeof(T) == 4, TF32 = SPLIT && !FP8;
   static constexpr int DP = DP_, NB = NB_;
   using M = typename std::conditional<FP8, __half, typename std::conditional<TF32, Tf32, T>::type>::type;  // of the products
+  static constexpr bool HALF = FP8;  // weights in units (Unit)
   static constexpr int ES = FP8 ? 1 : (int)sizeof(T);
   static constexpr int ROW = DP * ES;                 // bytes
   static constexpr int KP = ROW / 64;                 // 16-byte pieces of a key that a lane has
@@ -155,6 +162,37 @@ struct Shape {
   static_assert(WARPS <= kAttendWarps, "the workspace has room for their parts");
 };
 
+// The units of fp16 weights.  fp16 holds eleven digits down to 2^-14 and fewer below, so weights are brought near its
+// top.  Over an E4M3 cache a weight is a token's share times its
+// value's scale, and what counts is the largest of those: a large scale with next to no share must not push the others
+// down, so each head has a bound of its own on them, which falls as the maximum of the logits rises and its older tokens'
+// shares fall.  It is held as the upper half of an fp32 number (rounded up), two heads a word; the unit is 2^-14 of the
+// power of two above it.  (With one bound on the scales alone, a row of values 2^40 times the others' left nothing of
+// them, whatever its own share, and a first token of e^16 times the others' share and 2^-10 of their values left
+// the output 4 % off.)  64 x 4096 tokens in E4M3: 97.6 us as with the one bound; sixteen query heads a key head 55.7
+// where that took 55.0, fp32 queries 105.5 where 102.4.
+struct Unit {
+  static constexpr uint32_t kLeast = 0x0700, kMost = 0x7EFF;  // so that what follows are normal numbers
+  // 2^14 over the power of two above bound j of a word, and its reciprocal
+  __device__ __forceinline__ static float factor(uint32_t bounds, int j) {
+    return __uint_as_float(0x85800000u - ((j ? bounds : bounds << 16) & 0x7F800000u));
+  }
+  __device__ __forceinline__ static float value(uint32_t bounds, int j) {
+    return __uint_as_float(((j ? bounds : bounds << 16) & 0x7F800000u) - 0x06800000u);
+  }
+  // Bound j of the next word, from a word, the factor that the logits' maximum leaves of older shares, and the largest
+  // of this tile's; f becomes the factor from old units to new ones.
+  __device__ __forceinline__ static uint32_t moved(uint32_t bounds, uint32_t most, int j, float& f) {
+    const uint32_t was = j ? bounds >> 16 : bounds & 0xFFFFu, tile = j ? most >> 16 : most & 0xFFFFu;
+    uint32_t now = (__float_as_uint(__fmul_rn(__uint_as_float(was << 16), f)) + 0xFFFFu) >> 16;
+    if (tile > now) now = tile | 0x7Fu;  // (all below the next power of two: seldom raised)
+    now = max(min(now, kMost), kLeast);
+    const int up = (int)(was >> 7) - (int)(now >> 7) + 127;
+    f = __fmul_rn(f, __uint_as_float((uint32_t)max(min(up, 253), 1) << 23));
+    return now << (16 * j);
+  }
+};
+
 // Units of a segment beside its tiles (128 sequences of 8 to 8192 tokens, E4M3: 1 80.0 us, 2 78.8, 4 78.1), and the
 // smallest part of a warp.
 constexpr int kExtra = 4;
@@ -180,7 +218,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
   using M = typename S::M;
   constexpr bool FP8 = S::FP8;
   constexpr int NB = S::NB, NCE = S::CE / 2, MB = S::MB, TOKENS = S::TOKENS;
-  constexpr bool SPLIT = S::SPLIT, TF32 = S::TF32;
+  constexpr bool SPLIT = S::SPLIT, TF32 = S::TF32, HALF = S::HALF;
   __shared__ Plan<S::THREADS> plan;
   // the segments that warps share: which (or -1), their maxima and sums, and whether the first goes on in
   // the next warp's part
@@ -387,7 +425,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int j = 0; j < 2; ++j) m[nb][j] = -INFINITY, l[nb][j] = 0.0f;
-      float vref = SPLIT ? 0x1p-110f : 0x1p-126f;  // E4M3: o is in units of this power of two
+      uint32_t bound[NB];  // E4M3: see Unit; o is in these units
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) bound[nb] = Unit::kLeast * 0x10001u;
 
       for (int n = (g.last - g.first) * S::PARTS; n > 0; --n) {
         cp_async_wait<S::STAGES - 2>();
@@ -508,38 +548,29 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
             l[nb][j] = __fmaf_rn(l[nb][j], f[nb][j], sum);
           }
         }
+        uint32_t top[NB];  // E4M3: the upper halves of the largest magnitudes
         if constexpr (FP8) {
-          // weights times the values' scales, in units of a power of two above all of their magnitudes so far, fit fp16
-          // (magnitudes order as their bits without the sign; NaN lies above infinity)
-          uint32_t most = 0;
 #pragma unroll
-          for (int t = 0; t < 2 * MB; ++t) most = max(most, __float_as_uint(vs[t]) & 0x7FFFFFFFu);
-          most = __reduce_max_sync(0xFFFFFFFFu, most);
-          if (most >= __float_as_uint(vref)) {
-            const uint32_t e = min((most >> 23) + 1, 253u);
-            const float now = most > 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(e << 23);
-            const float down = __fdiv_rn(vref, now);
-            vref = now;
-            moved = true;
+          for (int nb = 0; nb < NB; ++nb) {
+            top[nb] = 0;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int t = 0; t < 2 * MB; ++t) {
+              float &x = s[nb][t / 2][2 * (t & 1)], &y = s[nb][t / 2][2 * (t & 1) + 1];
+              x = __fmul_rn(x, vs[t]);
+              y = __fmul_rn(y, vs[t]);
+              top[nb] = max_halves(top[nb], __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632) & 0x7FFF7FFFu);
+            }
 #pragma unroll
-              for (int j = 0; j < 2; ++j) f[nb][j] = __fmul_rn(f[nb][j], down);
-          }
-          // (1 / vref: its exponent reflected; NaN stays NaN)
-          // (SPLIT: 2^14 of them, so that the low parts stay above fp16's smallest)
-          float unit = vref != vref ? vref : __uint_as_float(0x7F000000u - __float_as_uint(vref));
-          if constexpr (SPLIT) unit = __fmul_rn(unit, 0x1p14f);
-#pragma unroll
-          for (int t = 0; t < 2 * MB; ++t) {
-            const float by = __fmul_rn(vs[t], unit);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) s[nb][t / 2][2 * (t & 1) + j] = __fmul_rn(s[nb][t / 2][2 * (t & 1) + j], by);
+            for (int i = 4; i < 32; i <<= 1) top[nb] = max_halves(top[nb], __shfl_xor_sync(0xFFFFFFFFu, top[nb], i));
+            moved = moved || max_halves(top[nb], bound[nb]) != bound[nb];
           }
         }
         if (__any_sync(0xFFFFFFFFu, moved)) {
+          if constexpr (FP8) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              bound[nb] = Unit::moved(bound[nb], top[nb], 0, f[nb][0]) | Unit::moved(bound[nb], top[nb], 1, f[nb][1]);
+          }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -548,6 +579,16 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
               for (int i = 0; i < NCE; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[nb][p][i][k] = __fmul_rn(o[nb][p][i][k], f[nb][k & 1]);
+        }
+        if constexpr (HALF) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float by = Unit::factor(bound[nb], j);
+#pragma unroll
+              for (int t = 0; t < 2 * MB; ++t) s[nb][t / 2][2 * (t & 1) + j] = __fmul_rn(s[nb][t / 2][2 * (t & 1) + j], by);
+            }
         }
         // weights of head g: of tokens 2c, 2c + 1 and 8 more (TF32: c, c + 4, and 8 more)
         uint32_t w[QN][NB][MB][TF32 ? 4 : 2];
@@ -652,8 +693,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
           const float sum = column_sum(l[nb][j]);
           const int r = 8 * nb + 2 * cl + j;
           if (r >= rows) continue;
-          float by = piece ? 1.0f : sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-          if constexpr (FP8) by = __fmul_rn(by, SPLIT ? __fmul_rn(vref, 0x1p-14f) : vref);
+          const float by = piece ? 1.0f : sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+          const float unit = FP8 ? Unit::value(bound[nb], j) : 1.0f;
 #pragma unroll
           for (int p = 0; p < S::VP; ++p) {
             float out[S::CE];
@@ -661,6 +702,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
             for (int i = 0; i < NCE; ++i) {
               out[2 * i] = __fmul_rn(o[nb][p][i][j], by);
               out[2 * i + 1] = __fmul_rn(o[nb][p][i][2 + j], by);
+              if constexpr (HALF) out[2 * i] = __fmul_rn(out[2 * i], unit), out[2 * i + 1] = __fmul_rn(out[2 * i + 1], unit);
             }
             const int c = (8 * p + gl) * S::CE;
 #pragma unroll
