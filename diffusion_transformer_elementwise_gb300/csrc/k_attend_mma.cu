@@ -132,7 +132,7 @@ struct Shape {
   static constexpr bool FP8 = FP8_, SPLIT = sizeof(T) == 4, TF32 = SPLIT && !FP8;
   static constexpr int DP = DP_, NB = NB_;
   using M = typename std::conditional<FP8, __half, typename std::conditional<TF32, Tf32, T>::type>::type;  // of the products
-  static constexpr bool HALF = FP8;  // weights in units (Unit)
+  static constexpr bool HALF = std::is_same<M, __half>::value;  // weights in fp16
   static constexpr int ES = FP8 ? 1 : (int)sizeof(T);
   static constexpr int ROW = DP * ES;                 // bytes
   static constexpr int KP = ROW / 64;                 // 16-byte pieces of a key that a lane has
@@ -163,7 +163,7 @@ struct Shape {
 };
 
 // The units of fp16 weights.  fp16 holds eleven digits down to 2^-14 and fewer below, so weights are brought near its
-// top.  Over an E4M3 cache a weight is a token's share times its
+// top: of an fp16 cache 2^14 of them (the largest is one).  Over an E4M3 cache a weight is a token's share times its
 // value's scale, and what counts is the largest of those: a large scale with next to no share must not push the others
 // down, so each head has a bound of its own on them, which falls as the maximum of the logits rises and its older tokens'
 // shares fall.  It is held as the upper half of an fp32 number (rounded up), two heads a word; the unit is 2^-14 of the
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float by = Unit::factor(bound[nb], j);
+              const float by = FP8 ? Unit::factor(bound[nb], j) : 0x1p14f;
 #pragma unroll
               for (int t = 0; t < 2 * MB; ++t) s[nb][t / 2][2 * (t & 1) + j] = __fmul_rn(s[nb][t / 2][2 * (t & 1) + j], by);
             }
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
           const int r = 8 * nb + 2 * cl + j;
           if (r >= rows) continue;
           const float by = piece ? 1.0f : sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-          const float unit = FP8 ? Unit::value(bound[nb], j) : 1.0f;
+          const float unit = FP8 ? Unit::value(bound[nb], j) : 0x1p-14f;
 #pragma unroll
           for (int p = 0; p < S::VP; ++p) {
             float out[S::CE];

@@ -152,7 +152,7 @@ def test_long_parts(kind, dtype):
 
 
 @pytest.mark.parametrize("D,Hq", [(64, 2), (128, 6), (256, 2), (128, 16), (33, 2)])
-@pytest.mark.parametrize("fp8", [True])
+@pytest.mark.parametrize("fp8", [False, True])
 def test_fp16_weights(D, Hq, fp8):
     """Tokens of 2^-25 of the largest weight and more, whose values are a hundred times its own."""
     n = 20000
