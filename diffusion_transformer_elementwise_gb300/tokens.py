@@ -144,10 +144,15 @@ def project(y, site, heads):
 
 
 def places(pages, positions, page_size):
-    """The cache's places of each sequence's token at positions[b] (negative where there is no page)."""
-    at = positions.long()
-    page = pages.gather(1, (at // page_size).clamp_(0, pages.shape[1] - 1)[:, None])[:, 0]
-    return page.long() * page_size + at % page_size
+    """The cache's places of each sequence's token at positions[b], -1 where it has none: before the start (an empty
+    sequence's last token), behind the page table, or where there is no page."""
+    import torch
+    at, width = positions.long(), pages.shape[1]
+    if width == 0:
+        return torch.full_like(at, -1)
+    page = pages.gather(1, (at // page_size).clamp_(0, width - 1)[:, None])[:, 0].long()
+    there = (at >= 0) & (at < width * page_size) & (page >= 0)
+    return torch.where(there, page * page_size + at % page_size, -1)
 
 
 def prompt(y, site, heads, cache, cos, sin, slots, eps=1e-6):
@@ -170,7 +175,8 @@ def attend(y, site, heads, cache, cos, sin, slots, pages, lengths, eps=1e-6):
 
 def decode_attending(ids, table, weights, stand_ins, sites, heads, caches, pages, lengths, freqs,
                      scale=1.0, eps=1e-6, group=128):
-    """One decoding step of B sequences: ids [B] are their new tokens, lengths [B] count them in.  sites
+    """One decoding step of B sequences: ids [B] are their new tokens, lengths [B] count them in (0: an idle row of a padded
+    batch; a token without a place is not written, and attention takes the tokens that the page table holds).  sites
     and caches: one for each block (make_attention, KVCache); the second site of a
     block has its stand-in, stand_ins[1::2].  Hq * head_dim is the width D.
     Returns (x, codes, scales), the last norm in E4M3."""
