@@ -355,7 +355,9 @@ dit_status cache_checks(const dit_cache* c, CacheViews* o) {
   if (!fp8 && (c->format < 0 || c->format > 2)) return DIT_ERR_BAD_FORMAT;
   const int es = fp8 ? 1 : elem_size((dit_dtype)c->format);
   int64_t slots, rows, n;
-  if (c->pages < 0 || c->heads < 0 || c->heads > kMaxHeads || c->page_size < 1 || c->D < 0 ||
+  // (page_size has a bound of its own: of no pages too, a launch divides by its low 32 bits)
+  if (c->pages < 0 || c->heads < 0 || c->heads > kMaxHeads || c->page_size < 1 ||
+      c->page_size > kMaxCount || c->D < 0 ||
       c->D > kMaxHeadDim || __builtin_mul_overflow(c->pages, c->page_size, &slots) ||
       slots > kMaxCount || __builtin_mul_overflow(c->heads, c->page_size, &rows) ||
       __builtin_mul_overflow(rows, c->D, &n) || n > kMaxStride || c->page_stride < n ||

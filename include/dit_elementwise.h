@@ -727,7 +727,7 @@ dit_status dit_rmsnorm_rope_backward(const dit_heads* q_grad, const dit_heads* k
  * both may be halves of one allocation) and the rest contiguous.  format: a dit_dtype value, or
  * DIT_E4M3: codes with one scale per row of D, scales [pages, heads,
  * page_size] fp32, page p at p * scale_stride.  The value is code * scale, whatever the scale's sign.
- * pages * page_size is at most 2^31 - 1, D at most 1024, page_stride at most 2^40.
+ * page_size and pages * page_size are at most 2^31 - 1, D at most 1024, page_stride at most 2^40.
  * A place ("slot") is page * page_size + the token's place in the page.
  */
 #define DIT_E4M3 3
