@@ -244,7 +244,8 @@ __device__ __forceinline__ void head_weight(F2 (&w)[2][HeadLane<T>::P], const He
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     Raw<16> r = {};
-    if (h.on[k]) r = ld_bcast<16>((const T*)p + h.column[k]);
+    // (not by the read-only path: the call before, which may have written them, can have run beside this kernel)
+    if (h.on[k]) r = ld_stream<16>((const T*)p + h.column[k]);
     Granule<T>::widen(r, w[k]);
 #pragma unroll
     for (int i = 0; i < HeadLane<T>::P; ++i) w[k][i] = f2_add(f2(offset, offset), w[k][i]);
