@@ -468,7 +468,7 @@ def paged_attention(q, cache, pages, lengths, scale=None, window=0, out=None, ls
     b (the last `window` of them, if that is not 0), token t at place t % page_size of
     page pages[b, t // page_size] of the cache (KVCache).  Hq is a multiple
     of the cache's heads; query head h reads key head h // (Hq / heads).
-    pages: int32 [B, width], rows contiguous; a page outside the cache leaves its tokens out.
+    pages: int32 [B, width], rows contiguous (one row for all sequences may be expanded); a page outside the cache leaves its tokens out.
     lengths: int32 or int64 [B].  scale: of the logits (D^-0.5 if None).  A sequence without a token has
     out 0 and lse -inf.  lse (float32 [B, Hq], where given or needed): the
     logarithm of the sum of the exponentials.  workspace: a uint8 CUDA tensor of

@@ -476,7 +476,8 @@ dit_status dit_paged_attention(const dit_heads* out, float* lse, const dit_heads
   if (st != DIT_OK) return st;
   if (cache->format != DIT_E4M3 && cache->format != (int64_t)dtype) return DIT_ERR_BAD_DTYPE;
   int64_t capacity, segments;
-  if (B < 0 || B > kMaxCount || width < 0 || pages_stride < (B > 1 ? width : 0) ||
+  // (the page table is only read: a stride of 0 repeats its row, as of the views)
+  if (B < 0 || B > kMaxCount || width < 0 || pages_stride < (B > 1 && pages_stride != 0 ? width : 0) ||
       pages_stride > kMaxStride || __builtin_mul_overflow(width, cache->page_size, &capacity) ||
       capacity > kMaxTokens || window < 0 || __builtin_mul_overflow(B, Hq, &segments) ||
       segments > kMaxCount)

@@ -767,7 +767,7 @@ dit_status dit_cache_read(const dit_cache* cache, const dit_heads* k, const dit_
  * Token t is at place t % page_size of page pages[b, t / page_size].  The new token's own
  * key and value are in the cache (write them first).
  *   q, out: [B, Hq, D] (dit_heads without `batch`); Hq a multiple of the cache's heads; D <= 512.
- *   pages: int32 [B, width], row b at b * pages_stride.  lengths: [B], int32 or
+ *   pages: int32 [B, width], row b at b * pages_stride (0: one row for all).  lengths: [B], int32 or
  *   int64.  A length is cut to [0, width * page_size] (at most 2^31 - 4096).  A token whose page
  *   is outside the cache is left out.  A sequence with no token has out 0
  *   and lse -infinity.  What lies in the cache's pages behind a sequence does not matter, NaN included.

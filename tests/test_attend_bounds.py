@@ -46,3 +46,16 @@ def test_page_size(lib, format):
                                        0, 0, BF16, 10 * A, need, None) == SHAPE, size
     for size in (1, (1 << 31) - 1):
         assert lib.dit_cache_read(ctypes.addressof(cache(0, size, format=format)), *rows) == NODEV
+
+
+def test_page_table_strides(lib):
+    """A page table is read alone: rows apart, or one row for all sequences."""
+    q, out, c = heads(5 * A), heads(6 * A), cache(3, 16)
+    need = lib.dit_paged_attention_workspace_bytes(1, 1, 16)
+    call = lambda B, stride, width: lib.dit_paged_attention(
+        ctypes.addressof(out), None, ctypes.addressof(q), ctypes.addressof(c), 8 * A, stride, width, 9 * A, B, 1, 1.0, 0,
+        0, BF16, 10 * A, need, None)
+    for B, stride, width in ((5, 0, 4), (5, 4, 4), (5, 7, 4), (1, 0, 4), (5, 0, 0)):
+        assert call(B, stride, width) == NODEV, (B, stride, width)
+    for B, stride, width in ((5, 1, 4), (5, 3, 4), (5, -4, 4), (1, -1, 4), (5, -1, 0)):
+        assert call(B, stride, width) == SHAPE, (B, stride, width)
