@@ -50,3 +50,43 @@ def test_weights_written_by_the_call_before(D):
     for n, (a, b) in enumerate(zip(got, want)):
         assert torch.equal(a, b), n
     assert not torch.equal(want[0], want[2]) and not torch.equal(want[0], want[8])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("D", [128, 34])
+def test_e4m3_rows_written_by_the_call_before(D, dtype):
+    """The same places get rows of other sizes each time, so that codes and scales differ from step to step: in place from
+    the packed projection into an E4M3 cache, back, and attention over it."""
+    L, size = 500, 8
+    w = act(D, tag="w", dtype=dtype)
+    qkv = act(L, 6, D, tag="qkv", dtype=dtype)
+    slots = torch.arange(L, device="cuda")
+    pages = torch.arange(-(-L // size), device="cuda").int()[None].expand(L, -1)
+    lengths = slots + 1
+
+    def chain(wait):
+        cache = dit.KVCache.empty(-(-L // size), 1, size, D, torch.float8_e4m3fn)
+        for t in (cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scales, cache.v_scales):
+            t.zero_()
+        outs = []
+        for i in range(10):
+            x = qkv * float(2.0 ** (i % 4) * (1 + 0.25 * i))
+            q, k, v = x[:, :4], x[:, 4:5], x[:, 5:]
+            cos, sin = dit.rotary_table(slots + 17 * i, freqs)
+            wait()
+            dit.rmsnorm_rope(q, k, w, w, cos, sin, weight_offset=float(i), out_q=q, out_k=k)
+            wait()
+            dit.cache_write(cache, k, v, slots)
+            wait()
+            outs += dit.paged_attention(q, cache, pages, lengths, need_lse=True)
+            wait()
+            outs += dit.cache_read(cache, slots, dtype=x.dtype)
+            wait()
+        return outs
+
+    freqs = dit.rotary_frequencies(D // 2)
+    got = chain(lambda: None)
+    want = chain(torch.cuda.synchronize)
+    for n, (a, b) in enumerate(zip(got, want, strict=True)):
+        assert torch.equal(a, b), n
+    assert not torch.equal(want[3], want[7])  # (the scales do differ)
