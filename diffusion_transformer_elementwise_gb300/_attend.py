@@ -522,6 +522,8 @@ def paged_attention(q, cache, pages, lengths, scale=None, window=0, out=None, ls
     _call(dev, lib.dit_paged_attention, "dit_paged_attention", at + _SIZE,
           None if lse is None else lse.data_ptr(), at, cache.address, pages.data_ptr(),
           pages.stride(0) if B > 1 else width, width, lengths.data_ptr(), B, Hq,
-          D ** -0.5 if scale is None else scale, int(window), ID_CODES[lengths.dtype], dt, wp, wn,
+          D ** -0.5 if scale is None else scale,
+          # (of 64 bits there; no sequence is as long)
+          max(-1, min(int(window), 1 << 62)), ID_CODES[lengths.dtype], dt, wp, wn,
           _stream(dev, stream))
     return out, lse
