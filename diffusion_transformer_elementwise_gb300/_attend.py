@@ -361,7 +361,7 @@ class KVCache:
                 raise ValueError(f"{name} is on {t.device}, expected {k.device}")
             step = 1  # (sizes of one have any stride)
             for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
-                if size > 1 and stride != step:
+                if size > 1 and stride != step and t.numel() > 0:
                     raise ValueError(f"the pages of {name} must be contiguous")
                 step *= size
         if k.dim() != 4 or v.shape != k.shape or v.dtype is not k.dtype:

@@ -28,3 +28,21 @@ def test_windows_past_64_bits():
     for window in (-1, -2 ** 63, -2 ** 64 + 3, -2 ** 200):
         with pytest.raises(dit.DitError):
             dit.paged_attention(*args, window=window)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("shape", [(3, 2, 16, 0), (3, 0, 16, 64), (0, 2, 16, 64), (3, 2, 1, 1), (1, 1, 1, 1)])
+def test_caches_of_nothing(shape, fp8):
+    """A cache without pages, heads or columns takes rows of that size, as the C entry points do."""
+    t = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    cache = dit.KVCache.empty(*shape, dtype=t)
+    pages, heads, size, D = shape
+    x = torch.ones(2, heads, D, dtype=torch.bfloat16, device="cuda")
+    slots = torch.tensor([0, pages * size], device="cuda")
+    dit.cache_write(cache, x, x, slots)
+    k, v = dit.cache_read(cache, slots, dtype=torch.bfloat16)
+    want = x.clone()
+    want[1] = 0
+    if pages == 0:
+        want[0] = 0
+    assert torch.equal(k, want) and torch.equal(v, want)
