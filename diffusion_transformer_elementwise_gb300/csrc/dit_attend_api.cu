@@ -335,7 +335,6 @@ dit_status dit_rmsnorm_rope_backward(const dit_heads* q_grad, const dit_heads* k
   }
   if (!go) return DIT_OK;
   a.partial = gw[0] || gw[1] ? (float*)workspace : nullptr;
-  a.inverse = true;  // the gradient is turned back
   return launch_status(dit::launch_rope_grad(dev, dtype, a, gw[0], gw[1], s));
 }
 
