@@ -219,6 +219,10 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
   constexpr bool FP8 = S::FP8;
   constexpr int NB = S::NB, NCE = S::CE / 2, MB = S::MB, TOKENS = S::TOKENS;
   constexpr bool SPLIT = S::SPLIT, TF32 = S::TF32, HALF = S::HALF;
+  // Parts of a weight.  One fp16 number leaves an output that is rounded to fp16 by no more than the weight itself 1.4 times
+  // as far off as it need be (over E4M3; 3.1e-4 of 2.1e-4), so fp16 queries have two as well as fp32 ones: 64 x 2048 tokens
+  // of fp16 95.4 us where one takes 95.1.  bf16's own rounding hides both fp16's (by 1 %) and bf16's of its caches (1 to 7 %).
+  constexpr int WN = HALF && !std::is_same<T, __nv_bfloat16>::value ? 2 : 1;
   __shared__ Plan<S::THREADS> plan;
   // the segments that warps share: which (or -1), their maxima and sums, and whether the first goes on in
   // the next warp's part
@@ -591,7 +595,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
             }
         }
         // weights of head g: of tokens 2c, 2c + 1 and 8 more (TF32: c, c + 4, and 8 more)
-        uint32_t w[QN][NB][MB][TF32 ? 4 : 2];
+        uint32_t w[WN][NB][MB][TF32 ? 4 : 2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -609,9 +613,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
               } else {
                 const uint32_t h = Pair<typename std::conditional<TF32, __half, M>::type>::narrow(f2(x, y));
                 w[0][nb][b][k] = transposed(h);
-                if constexpr (SPLIT) {
+                if constexpr (WN == 2) {
                   const F2 back = Pair<__half>::widen(h);
-                  w[QN - 1][nb][b][k] = transposed(Pair<__half>::narrow(f2(__fadd_rn(x, -back.x), __fadd_rn(y, -back.y))));
+                  w[1][nb][b][k] = transposed(Pair<__half>::narrow(f2(__fadd_rn(x, -back.x), __fadd_rn(y, -back.y))));
                 }
               }
             }
@@ -653,10 +657,11 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
                   for (int nb = 0; nb < NB; ++nb) {
                     if constexpr (SPLIT) {
                       float sum[4] = {};
-                      mma<M>(sum, a0, a1, a2, a3, w[QN - 1][nb][b][0], w[QN - 1][nb][b][1]);
+                      mma<M>(sum, a0, a1, a2, a3, w[WN - 1][nb][b][0], w[WN - 1][nb][b][1]);
                       mma<M>(sum, a0, a1, a2, a3, w[0][nb][b][0], w[0][nb][b][1]);
                       add(o[nb][p][2 * k + h], sum);
                     } else {
+                      if constexpr (WN == 2) mma<M>(o[nb][p][2 * k + h], a0, a1, a2, a3, w[WN - 1][nb][b][0], w[WN - 1][nb][b][1]);
                       mma<M>(o[nb][p][2 * k + h], a0, a1, a2, a3, w[0][nb][b][0], w[0][nb][b][1]);
                     }
                   }
@@ -667,7 +672,10 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
                 const uint32_t a2 = __byte_perm(u[2].w[k], u[3].w[k], 0x5410);
                 const uint32_t a3 = __byte_perm(u[2].w[k], u[3].w[k], 0x7632);
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][k], a0, a1, a2, a3, w[0][nb][b][0], w[0][nb][b][1]);
+                for (int nb = 0; nb < NB; ++nb) {
+                  if constexpr (WN == 2) mma<M>(o[nb][p][k], a0, a1, a2, a3, w[WN - 1][nb][b][0], w[WN - 1][nb][b][1]);
+                  mma<M>(o[nb][p][k], a0, a1, a2, a3, w[0][nb][b][0], w[0][nb][b][1]);
+                }
               }
             }
           }
