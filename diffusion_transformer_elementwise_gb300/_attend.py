@@ -194,8 +194,9 @@ def rotary_frequencies(sections, theta=10000.0, shared=False, device="cuda"):
 def rotary_table(positions, freqs, sections=None, cos=None, sin=None, stream=None):
     """cos and sin of positions[axis(j), t] * freqs[j], float32 [tokens, R].  positions: int32, int64
     or float32, [tokens] for one axis or [axes, tokens]; freqs: float64 [R]; sections: the
-    number of columns of each axis, in order (None: one axis).  The angle is reduced
-    exactly, however far the position.  Returns (cos, sin)."""
+    number of columns of each axis, in order (None: one axis).  The frequency is held in
+    turns, to 2^-52 of it; beyond that the angle is reduced without loss, however far the
+    position.  Returns (cos, sin)."""
     _tensor(positions, "positions")
     if positions.dtype not in POSITION_CODES:
         raise TypeError("positions must be int32, int64 or float32")

@@ -60,7 +60,9 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
-// r of a head's norm from its sum of squares (inv_d: fl(1 / D)).
+// r of a head's norm from its sum of squares (inv_d: fl(1 / D)).  The root halves the two roundings before it (2 u, u =
+// 2^-24), and rsqrtf's own error was at most 2.1 u over all numbers of two binades: 3.1 u together.  A Newton step
+// would leave 2.5 u; it costs the kernels for any alignment 3 to 4 % (8160 x 64 heads of 99: 95.6 us with the root alone, 99.6).
 __device__ __forceinline__ float inverse_rms(float sum, float inv_d, float eps) {
   return rsqrtf(__fmaf_rn(sum, inv_d, eps));
 }

@@ -3,7 +3,8 @@
 //
 //   s = scale q.k,  m = max s,  l = sum 2^(s - m),  o = sum 2^(s - m) v
 // in one pass over the tokens, with s in powers of two (scale times log2 e).  For rows
-// that are not made of 16-byte granules, or of more than 256 columns.  A CTA has 64 tokens at a time: a warp its
+// that are not made of 16-byte granules (E4M3: of columns by sixteens), or of more than 256 columns, or whose pages are
+// no whole number of rows apart (attend_mma_takes).  A CTA has 64 tokens at a time: a warp its
 // keys, columns over the lanes; then a thread a column of the values and a share of the tokens.  Bound by
 // instructions (264 of a warp a token and key head of 99, two bytes a load; 68 % of the issue slots) and, for
 // longer heads, the latency of one stage after the other:

@@ -13,8 +13,8 @@
 // so that what they could do beyond does not count.
 // Measured (GPU time with the join): one sequence of 131072 tokens x 8 heads of 128, bf16, 88.6 us for 537 MB, 6.1
 // TB/s or 89 % of a copy's rate: 6.9 TB/s while it lasts and some 9 us for lengths, pages, first rows and joins one
-// after the other.  128 sequences of 8 to 8192 tokens in E4M3 79 us for 422 MB (5.3 TB/s; with the conversion of codes
-// some 700 instructions a tile and head, 43 % of the issue slots).  64 x 2048 tokens fp32 188 us, 5.7 TB/s.
+// after the other.  128 sequences of 8 to 8192 tokens in E4M3 80 us for 422 MB (5.3 TB/s; with the conversion of codes
+// some 730 instructions a tile and head, 45 % of the issue slots).  64 x 2048 tokens fp32 189 us, 5.7 TB/s.
 //
 // The contraction index of a product may be permuted if both operands agree, and so may
 // the rows of O.  So every lane's operands are 16 contiguous bytes of a row: of keys,

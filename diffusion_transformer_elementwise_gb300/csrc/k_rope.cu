@@ -100,7 +100,7 @@ __device__ __forceinline__ float2 cos_sin(const Angle& a) {
 }
 
 // A thread has a column and every so many tokens.  32640 tokens of three axes and 64 columns: 6.8 us for 17 MB
-// written, of which 2 are the launch; bound by instructions (some 60 an angle) and the latency of positions and
+// written, of which 2 are the launch; bound by instructions (87 an angle) and the latency of positions and
 // frequencies.  With CUDA's sincospif, 64-bit counters and every CTA's fp64 behind the loads it was 10.3.
 template <class P>
 __global__ void __launch_bounds__(kTableThreads) table_kernel(const __grid_constant__ TableArgs a) {
