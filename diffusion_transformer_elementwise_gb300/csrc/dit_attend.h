@@ -82,7 +82,8 @@ cudaError_t launch_attend(const DeviceInfo& dev, int dtype, bool granules, const
 // columns in 16-byte granules.  Sets a.rows.  Its CTAs and their warps have parts of their own behind
 // `partial`: [ctas][warps][2][rows][D + 2].
 constexpr int64_t kAttendMmaCtas = 160;
-constexpr int kAttendWarps = 16;
+// the most warps of a CTA, of any type, for heads of D columns (0: it does not take them)
+constexpr int attend_warps(int64_t D) { return D <= 64 ? 16 : D <= 128 ? 12 : D <= 256 ? 8 : 0; }
 bool attend_mma_takes(bool granules, const AttendArgs& a);
 cudaError_t launch_attend_mma(const DeviceInfo& dev, int dtype, AttendArgs& a, int64_t* ctas, cudaStream_t s);
 cudaError_t launch_attend_mma_fp32(const DeviceInfo& dev, AttendArgs& a, int64_t* ctas, cudaStream_t s);

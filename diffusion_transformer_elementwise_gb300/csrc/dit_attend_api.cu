@@ -459,7 +459,7 @@ int64_t dit_paged_attention_workspace_bytes(int64_t Hq, int64_t heads, int64_t D
       D > kMaxAttendDim)
     return -1;
   const int64_t rows = std::min<int64_t>(Hq / heads, dit::kAttendRows);
-  const int64_t parts = std::max(dit::kAttendMaxCtas, dit::kAttendMmaCtas * (1 + dit::kAttendWarps));
+  const int64_t parts = std::max(dit::kAttendMaxCtas, dit::kAttendMmaCtas * (1 + dit::attend_warps(D)));
   return round_up(dit::kAttendMaxCtas * 2 * 8) + round_up(parts * 2 * rows * (D + 2) * 4);
 }
 

@@ -159,7 +159,7 @@ struct Shape {
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int SMEM = STAGES * WARPS * (STAGE + EXTRA);
   static_assert(STAGES >= 2, "a stage in flight and one in use");
-  static_assert(WARPS <= kAttendWarps, "the workspace has room for their parts");
+  static_assert(WARPS <= attend_warps(DP), "the workspace has room for their parts");
 };
 
 // The units of fp16 weights.  fp16 holds eleven digits down to 2^-14 and fewer below, so weights are brought near its

@@ -59,3 +59,14 @@ def test_page_table_strides(lib):
         assert call(B, stride, width) == NODEV, (B, stride, width)
     for B, stride, width in ((5, 1, 4), (5, 3, 4), (5, -4, 4), (1, -1, 4), (5, -1, 0)):
         assert call(B, stride, width) == SHAPE, (B, stride, width)
+
+
+def test_attention_workspace(lib):
+    """Room for the parts that the kernels for heads of D columns have, and no more: 160 CTAs and the warps of each, at most
+    16, 12 or 8 of them, or 608 CTAs; two parts each, of up to 16 rows of D + 2 numbers."""
+    need = lib.dit_paged_attention_workspace_bytes
+    up = lambda n: -(-n // 256) * 256
+    for D, parts in ((1, 160 * 17), (64, 160 * 17), (65, 160 * 13), (128, 160 * 13), (129, 160 * 9), (256, 160 * 9),
+                     (257, 608), (512, 608)):
+        for Hq, Hk, rows in ((1, 1, 1), (8, 2, 4), (16, 1, 16), (80, 2, 16)):
+            assert need(Hq, Hk, D) == up(608 * 2 * 8) + up(parts * 2 * rows * (D + 2) * 4), (D, Hq, Hk)
