@@ -219,10 +219,11 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
   constexpr bool FP8 = S::FP8;
   constexpr int NB = S::NB, NCE = S::CE / 2, MB = S::MB, TOKENS = S::TOKENS;
   constexpr bool SPLIT = S::SPLIT, TF32 = S::TF32, HALF = S::HALF;
-  // Parts of a weight.  One fp16 number leaves an output that is rounded to fp16 by no more than the weight itself 1.4 times
-  // as far off as it need be (over E4M3; 3.1e-4 of 2.1e-4), so fp16 queries have two as well as fp32 ones: 64 x 2048 tokens
-  // of fp16 95.4 us where one takes 95.1.  bf16's own rounding hides both fp16's (by 1 %) and bf16's of its caches (1 to 7 %).
-  constexpr int WN = HALF && !std::is_same<T, __nv_bfloat16>::value ? 2 : 1;
+  // Parts of a weight.  Over E4M3 one fp16 number leaves an output that is itself rounded to fp16 1.4 times
+  // as far off as it need be (3.1e-4 of 2.1e-4), so fp16 queries have two there as well as fp32 ones: 64 x 4096 tokens
+  // 98.6 us where one takes 97.6.  bf16's own rounding hides it (1 %), as the types' own do over their caches (1 to 7 %), where
+  // a second part would also make NaN of an infinite value, as infinity times 0 or less.
+  constexpr int WN = FP8 && !std::is_same<T, __nv_bfloat16>::value ? 2 : 1;
   __shared__ Plan<S::THREADS> plan;
   // the segments that warps share: which (or -1), their maxima and sums, and whether the first goes on in
   // the next warp's part
@@ -614,8 +615,10 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
                 const uint32_t h = Pair<typename std::conditional<TF32, __half, M>::type>::narrow(f2(x, y));
                 w[0][nb][b][k] = transposed(h);
                 if constexpr (WN == 2) {
+                  // (what is left is at most 16; -64 in the place of infinity less infinity changes no infinite product)
                   const F2 back = Pair<__half>::widen(h);
-                  w[1][nb][b][k] = transposed(Pair<__half>::narrow(f2(__fadd_rn(x, -back.x), __fadd_rn(y, -back.y))));
+                  const float u = fmaxf(__fadd_rn(x, -back.x), -64.0f), v = fmaxf(__fadd_rn(y, -back.y), -64.0f);
+                  w[1][nb][b][k] = transposed(Pair<__half>::narrow(f2(u, v)));
                 }
               }
             }
@@ -672,10 +675,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attend_mma_kernel(const __grid_
                 const uint32_t a2 = __byte_perm(u[2].w[k], u[3].w[k], 0x5410);
                 const uint32_t a3 = __byte_perm(u[2].w[k], u[3].w[k], 0x7632);
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                  if constexpr (WN == 2) mma<M>(o[nb][p][k], a0, a1, a2, a3, w[WN - 1][nb][b][0], w[WN - 1][nb][b][1]);
-                  mma<M>(o[nb][p][k], a0, a1, a2, a3, w[0][nb][b][0], w[0][nb][b][1]);
-                }
+                for (int nb = 0; nb < NB; ++nb) mma<M>(o[nb][p][k], a0, a1, a2, a3, w[0][nb][b][0], w[0][nb][b][1]);
               }
             }
           }

@@ -772,10 +772,10 @@ dit_status dit_cache_read(const dit_cache* cache, const dit_heads* k, const dit_
  *   is outside the cache is left out.  A sequence with no token has out 0
  *   and lse -infinity.  What lies in the cache's pages behind a sequence does not matter, NaN included.
  *   lse: fp32 [B, Hq], or NULL.
- * Keys, values and weights of 16-bit types are multiplied on the tensor cores, with products and sums in fp32.  For
- * bf16 queries the weights are rounded there: to bf16, or over E4M3 to fp16, after the value's scale
- * is taken in.  For fp16 queries they are taken in two parts, 22 bits of them.  For fp32 queries every number
- * is, 22 bits and more of it (where an infinity among keys or values gives NaN).
+ * Keys, values and weights of 16-bit types are multiplied on the tensor cores, with products and sums in fp32.  The
+ * weights of bf16 and fp16 caches are rounded there to their type.  Over E4M3 they are rounded to fp16, after the value's
+ * scale is taken in, or for fp16 queries taken in two parts, 22 bits of them.  For fp32 queries every number is
+ * taken so, 22 bits and more of it (where an infinity among keys or values gives NaN).
  * The length is split over the GPU and the parts joined by a second kernel, in one order for
  * given lengths.
  */

@@ -73,14 +73,17 @@ class Rows:
     def check(self, window=0):
         """A logit of magnitude S is off by 8 u S and a weight by its exponential's 2^-21 more; the output by that
         share of sum p |v| twice (its own and the sum's), by its weights' rounding to fp16 (half a step, 2^-11 of
-        each, over E4M3 with bf16 queries; bf16 2^-8; two parts of fp16 or tf32, as fp16 and fp32 queries have, 2^-19), and, where the weights are fp16, by what they cannot hold:
+        each: fp16 caches, and bf16 queries over E4M3; bf16 caches 2^-8; two parts of fp16 or tf32 2^-19: fp32 queries, and
+        fp16 ones over E4M3), and, where the weights are fp16, by what they cannot hold:
         they are kept in units that put the largest weight times its row's scale at 2^12 and more, so a token loses
         2^-25 / 2^12 of that, times its codes (at most 1), at most."""
         out, lse = dit.paged_attention(self.q, self.cache, self.pages, self.lengths, scale=1.0, window=window,
                                        need_lse=True)
         fp8 = self.cache.k_scales is not None
         dtype = self.q.dtype
-        share = 2.0 ** -8 if dtype is torch.bfloat16 and not fp8 else 2.0 ** -11 if dtype is torch.bfloat16 else 2.0 ** -19
+        share = 2.0 ** -19
+        if dtype is not torch.float32 and not (fp8 and dtype is torch.float16):
+            share = 2.0 ** -8 if dtype is torch.bfloat16 and not fp8 else 2.0 ** -11
         lo = len(self.logit) - window if window else 0
         v, size = self.v[lo:], self.size[lo:]
         for h in range(self.q.shape[1]):
