@@ -5,9 +5,9 @@
 // with the quotient in two fp32 numbers, so that a code is the nearest to the exact
 // quotient but where that lies within 2^-24 of itself from the middle of two codes.
 // Both ways are bound by memory; the way in is held up by its instructions too (760 of a warp for a token's 16 rows,
-// 53 % of the issue slots).  32640 tokens x 8 heads of 128, 1/20 of them padding, bf16: into E4M3 39 us, 4.9 TB/s, 72 % of a
-// copy's rate; back 32 us, 6.2 TB/s, 92 %; in bf16 40 us in and 41 back, 6.3 and 6.4 TB/s.  By rows of any kind one after the other, each with its own places, they took 48
-// and 34 us; an element per access 168 and 112.
+// 53 % of the issue slots).  32640 tokens x 8 heads of 128, 1/20 of them padding, bf16: into E4M3 39 us, 4.9 TB/s, 72 %
+// of a copy's rate; back 32 us, 6.2 TB/s, 92 %; in bf16 40 us in and 41 back, 6.3 and 6.4 TB/s.  By rows of any kind one
+// after the other, each with its own places, E4M3 took 48 and 34 us; an element per access 168 and 112.
 #include "dit_attend.h"
 #include "dit_heads.cuh"
 
